@@ -66,6 +66,9 @@ typedef int32_t mm_status;
 #define MM_ERR_NOT_FOUND 8          /* key not in the table / unknown name */
 
 typedef enum { MM_BF16 = 0, MM_F16 = 1, MM_F32 = 2 } mm_dtype;
+/* 8-bit floating point (4 exponent, 3 mantissa bits, largest value 448, no
+ * infinities), taken only by the operators that name it. */
+#define MM_E4M3 3
 
 /* Element types of A, B and C (mm_dtype values). */
 typedef struct {
@@ -350,6 +353,105 @@ mm_status mm_splitk_gemm_noalloc(const void *lhs, const void *rhs, void *out, in
  * calls may be wrong).  Errors: MM_ERR_CUDA.
  */
 mm_status mm_splitk_gemm_noalloc_status(void *stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around a quantised linear layer.  They share the conventions
+ * above (row-major operands with a leading dimension in ELEMENTS, pointers
+ * aligned to their element size, asynchronous on `stream`, nothing retained)
+ * and take no part in tuning: no key, no table, no candidate.  Each call
+ * launches on `stream` only; calls on one stream are ordered, and calls on
+ * different streams may overlap (scratch is private to a stream).  Scratch a
+ * call needs is allocated on the first call of its size on a stream; while
+ * the stream is being captured into a graph such a call returns
+ * MM_ERR_UNSUPPORTED, so make one call of that size before the capture.
+ * Sums and statistics are held in fp32.  Errors of every one of them:
+ * MM_ERR_INVALID_ARG (negative size, leading dimension smaller than a row,
+ * null or misaligned pointer, type out of place), MM_ERR_UNSUPPORTED (not an
+ * sm_10x device, or a size beyond the limits given), MM_ERR_CUDA.
+ * --------------------------------------------------------------------- */
+
+/*
+ * mm_rmsnorm -- root-mean-square norm with the residual's addition.  For each
+ * of `rows` rows of `cols` values:
+ *   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * weight
+ * computed in fp32 from the unrounded h, each output rounded once.
+ *   residual  NULL: h = x.
+ *   h         receives h rounded to x's type (the residual stream to carry
+ *             on); NULL: not written.
+ *   y         the output, of type dt.c: bf16, f16, f32 or MM_E4M3.
+ *   scale     one fp32 a row, required for an MM_E4M3 output and NULL
+ *             otherwise: scale = max|y| / 448 (1 for a row of zeros, at least
+ *             2^-126 for any other), and the 8-bit values are e4m3(y / scale),
+ *             nearest even, so that y ~ scale * value.  A row that holds a
+ *             NaN gets a NaN scale.
+ *   rstd      one fp32 a row (what mm_rmsnorm_backward takes); NULL: not
+ *             written.
+ *   dt        a: type of x, residual and h; b: of weight; c: of y
+ *   eps       >= 0 and finite.
+ * h and y may each be x or residual in place (the same address, leading
+ * dimension and element size); other overlaps are not allowed.  rows or cols
+ * of 0 is a no-op.  cols < 2^31.
+ */
+mm_status mm_rmsnorm(const void *x, const void *residual, const void *weight, void *h, void *y,
+                     float *scale, float *rstd, int64_t rows, int64_t cols, int64_t ldx,
+                     int64_t ldr, int64_t ldh, int64_t ldy, mm_dtypes dt, float eps, void *stream);
+
+/*
+ * mm_rmsnorm_backward -- the gradients of mm_rmsnorm.  With g = dy * weight:
+ *   dx = dh + rstd * (g - h * rstd^2 * mean(g * h))     (of x and of residual)
+ *   dweight = sum over rows of dy * h * rstd
+ *   dy        gradient of y, type dt.c (bf16, f16 or f32).
+ *   dh        gradient that reaches h past the norm, type dt.a; NULL: none.
+ *   h         as the forward pass wrote it (x where there was no residual).
+ *   rstd      as the forward pass wrote it; NULL: computed from h with eps.
+ *   dx        type dt.a; may be dy or dh in place (same address, leading
+ *             dimension and element size).
+ *   dweight   `cols` values of type dt.b, overwritten; NULL: not computed.
+ *             The sum's order depends on the sizes and the device only, so
+ *             equal calls give equal bits.
+ * rows = 0 writes zeros to dweight; cols = 0 is a no-op.  cols < 2^31.
+ */
+mm_status mm_rmsnorm_backward(const void *dy, const void *dh, const void *h, const void *weight,
+                              const float *rstd, void *dx, void *dweight, int64_t rows,
+                              int64_t cols, int64_t lddy, int64_t lddh, int64_t ldh, int64_t lddx,
+                              mm_dtypes dt, float eps, void *stream);
+
+/*
+ * mm_gemm_w4 -- out = A . W^T with W held in 4 bits with group scales:
+ *   out[m, n] = sum_k A[m, k] * scales[n, k / group] *
+ *               (code[n, k] - zeros[n, k / group])
+ *   A         M x K, type dt.a: bf16 or f16.
+ *   codes     N rows of K unsigned 4-bit codes, two to a byte along k, the
+ *             even k in the low half; ldw, the distance between rows, is in
+ *             codes and even.  Codes past K are never used.
+ *   scales    N rows of ceil(K / group) scales, type dt.b: bf16, f16 or f32,
+ *             lds apart.
+ *   zeros     zero points 0..15, one byte each (the low 4 bits are used), laid
+ *             out as scales (lds apart too); NULL: 8 everywhere.
+ *   out       M x N, type dt.c: bf16, f16 or f32.
+ *   group     32, 64 or 128 codes; the last group of a row may be short.
+ * For M <= 16 the differences code - zero enter the product as they are and
+ * the scales are applied to fp32 sums of a group; for larger M each weight is
+ * rounded once to A's type.
+ * M or N of 0 is a no-op; K = 0 writes zeros.  M, N, K < 2^30.
+ */
+mm_status mm_gemm_w4(const void *A, const void *codes, const void *scales, const void *zeros,
+                     void *out, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw,
+                     int64_t lds, int64_t ldc, int32_t group, mm_dtypes dt, void *stream);
+
+/*
+ * mm_gemm_q8 -- out = (scale_a . A) . (scale_b . B)^T, A and B in 8 bits:
+ *   out[m, n] = scale_a[m] * scale_b[n] * sum_k A[m, k] * B[n, k]
+ *   A         M x K MM_E4M3 (mm_rmsnorm's 8-bit output); scale_a: M fp32 (its
+ *             scales) or NULL for 1.
+ *   B         N x K MM_E4M3, the weights, a row for each output column;
+ *             scale_b: N fp32 or NULL for 1.
+ *   out       M x N, type dt.c: bf16, f16 or f32; dt.a = dt.b = MM_E4M3.
+ * M or N of 0 is a no-op; K = 0 writes zeros.  M, N, K < 2^30.
+ */
+mm_status mm_gemm_q8(const void *A, const void *B, const float *scale_a, const float *scale_b,
+                     void *out, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                     int64_t ldc, mm_dtypes dt, void *stream);
 
 /* Free every library-owned device buffer and the tables; saves the table of
  * each device to MM_CACHE_FILE first when that option is set and tuning

@@ -29,6 +29,7 @@ MM_ERR_TIMEOUT = 7
 MM_ERR_NOT_FOUND = 8
 
 MM_BF16, MM_F16, MM_F32 = 0, 1, 2
+MM_E4M3 = 3  # only where an operator names it
 MM_NN, MM_NT, MM_TN, MM_TT = 0, 1, 2, 3
 LAYOUTS = {"NN": MM_NN, "NT": MM_NT, "TN": MM_TN, "TT": MM_TT}
 
@@ -103,6 +104,10 @@ _sig = {
     "mm_splitk_gemm_noalloc": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64,
                                       mm_dtypes, ctypes.c_int, _vp]),
     "mm_splitk_gemm_noalloc_status": (_i32, [_vp]),
+    "mm_rmsnorm": (_i32, [_vp] * 7 + [_i64] * 6 + [mm_dtypes, ctypes.c_float, _vp]),
+    "mm_rmsnorm_backward": (_i32, [_vp] * 7 + [_i64] * 6 + [mm_dtypes, ctypes.c_float, _vp]),
+    "mm_gemm_w4": (_i32, [_vp] * 5 + [_i64] * 7 + [_i32, mm_dtypes, _vp]),
+    "mm_gemm_q8": (_i32, [_vp] * 5 + [_i64] * 6 + [mm_dtypes, _vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -315,6 +320,35 @@ def mm_splitk_gemm_noalloc_status(stream=None):
     """Synchronise `stream` and report (and clear) a bounded wait that gave up
     in a no-allocation call since the previous query."""
     return _lib.mm_splitk_gemm_noalloc_status(_stream(stream))
+
+
+def mm_rmsnorm(x, residual, weight, h, y, scale, rstd, rows, cols, ldx, ldr, ldh, ldy, dtypes, eps,
+               stream=None):
+    """h = x + residual, y = h / rms(h) * weight; y in 8 bits takes `scale`."""
+    return _lib.mm_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y), _ptr(scale),
+                           _ptr(rstd), rows, cols, ldx, ldr, ldh, ldy, _dt(dtypes), eps,
+                           _stream(stream))
+
+
+def mm_rmsnorm_backward(dy, dh, h, weight, rstd, dx, dweight, rows, cols, lddy, lddh, ldh, lddx,
+                        dtypes, eps, stream=None):
+    """The gradients of mm_rmsnorm to its input and its weight."""
+    return _lib.mm_rmsnorm_backward(_ptr(dy), _ptr(dh), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dx),
+                                    _ptr(dweight), rows, cols, lddy, lddh, ldh, lddx, _dt(dtypes),
+                                    eps, _stream(stream))
+
+
+def mm_gemm_w4(A, codes, scales, zeros, out, M, N, K, lda, ldw, lds, ldc, group, dtypes,
+               stream=None):
+    """out = A . W^T, W in 4-bit codes with group scales and zero points."""
+    return _lib.mm_gemm_w4(_ptr(A), _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(out), M, N, K,
+                           lda, ldw, lds, ldc, group, _dt(dtypes), _stream(stream))
+
+
+def mm_gemm_q8(A, B, scale_a, scale_b, out, M, N, K, lda, ldb, ldc, dtypes, stream=None):
+    """out = A . B^T of e4m3 operands with row scales of A and of B."""
+    return _lib.mm_gemm_q8(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), _ptr(out), M, N, K, lda,
+                           ldb, ldc, _dt(dtypes), _stream(stream))
 
 
 def library_handle():

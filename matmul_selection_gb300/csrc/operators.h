@@ -1,0 +1,59 @@
+// Internal declarations of the operators around a quantised linear layer:
+// what operators.cpp has checked and the kernels take.
+#pragma once
+
+#include "common.h"
+
+namespace mm {
+
+struct NormArgs {
+  const void *x, *residual, *weight;
+  void *h, *y;
+  float *scale, *rstd;
+  int64_t rows;
+  int cols;
+  int64_t ldx, ldr, ldh, ldy;  // elements
+  int tx, tw, ty;              // mm_dtype, ty also MM_E4M3
+  float eps;
+};
+mm_status launch_rmsnorm(const NormArgs &a, LaunchCtx &ctx);
+
+struct NormBwdArgs {
+  const void *dy, *dh, *h, *weight;
+  const float *rstd;
+  void *dx, *dweight;
+  int64_t rows;
+  int cols;
+  int64_t lddy, lddh, ldh, lddx;  // elements
+  int tx, tw, ty;                 // h, dh, dx; weight, dweight; dy
+  float eps;
+};
+mm_status launch_rmsnorm_backward(const NormBwdArgs &a, LaunchCtx &ctx);
+
+struct W4Args {
+  const void *A;
+  const uint8_t *codes;
+  const void *scales;
+  const uint8_t *zeros;  // null: 8
+  void *out;
+  int M, N, K;
+  int64_t lda, ldw, lds, ldc;  // elements (codes for ldw)
+  int group;
+  int ta, ts, tc;
+};
+mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx);
+
+struct Q8Args {
+  const uint8_t *A, *B;
+  const float *scale_a, *scale_b;  // null: 1
+  void *out;
+  int M, N, K;
+  int64_t lda, ldb, ldc;
+  int tc;
+};
+mm_status launch_gemm_q8(const Q8Args &a, LaunchCtx &ctx);
+
+// A kernel launch of the library outside the candidates, for the counters.
+inline void count_operator_launch() { stats().launches.fetch_add(1, std::memory_order_relaxed); }
+
+}  // namespace mm
