@@ -453,6 +453,15 @@ mm_status mm_gemm_q8(const void *A, const void *B, const float *scale_a, const f
                      void *out, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
                      int64_t ldc, mm_dtypes dt, void *stream);
 
+/*
+ * mm_operator_status -- synchronises `stream` and reports whether a kernel of
+ * the operators above gave up a bounded wait since the previous query on the
+ * current device (their calls are asynchronous and have returned by then):
+ * MM_OK, or MM_ERR_TIMEOUT (the results of those calls may be wrong), which
+ * also clears the record.  Errors: MM_ERR_CUDA.
+ */
+mm_status mm_operator_status(void *stream);
+
 /* Free every library-owned device buffer and the tables; saves the table of
  * each device to MM_CACHE_FILE first when that option is set and tuning
  * produced new entries.  The library may be used again afterwards. */

@@ -108,6 +108,7 @@ _sig = {
     "mm_rmsnorm_backward": (_i32, [_vp] * 7 + [_i64] * 6 + [mm_dtypes, ctypes.c_float, _vp]),
     "mm_gemm_w4": (_i32, [_vp] * 5 + [_i64] * 7 + [_i32, mm_dtypes, _vp]),
     "mm_gemm_q8": (_i32, [_vp] * 5 + [_i64] * 6 + [mm_dtypes, _vp]),
+    "mm_operator_status": (_i32, [_vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -349,6 +350,12 @@ def mm_gemm_q8(A, B, scale_a, scale_b, out, M, N, K, lda, ldb, ldc, dtypes, stre
     """out = A . B^T of e4m3 operands with row scales of A and of B."""
     return _lib.mm_gemm_q8(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), _ptr(out), M, N, K, lda,
                            ldb, ldc, _dt(dtypes), _stream(stream))
+
+
+def mm_operator_status(stream=None):
+    """Synchronise `stream`; report (and clear) a bounded wait that gave up in
+    an operator's kernel since the previous query."""
+    return _lib.mm_operator_status(_stream(stream))
 
 
 def library_handle():

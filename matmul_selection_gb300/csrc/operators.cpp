@@ -187,4 +187,19 @@ mm_status mm_gemm_q8(const void *A, const void *B, const float *scale_a, const f
   });
 }
 
+mm_status mm_operator_status(void *stream) {
+  return guarded([&]() -> mm_status {
+    LaunchCtx ctx;
+    MM_TRY(operator_context(stream, &ctx));
+    MM_CUDA_TRY(cudaStreamSynchronize(ctx.stream));
+    int code = 0, *word = ctx.dev->d_err + kOperatorErrorWord;
+    MM_CUDA_TRY(cudaMemcpy(&code, word, sizeof code, cudaMemcpyDeviceToHost));
+    if (code == 0) return MM_OK;
+    MM_CUDA_TRY(cudaMemset(word, 0, sizeof code));
+    return set_error(MM_ERR_TIMEOUT,
+                     "an operator kernel's bounded wait gave up (code 0x%x); results of the calls "
+                     "since the previous status query may be wrong", code);
+  });
+}
+
 }  // extern "C"

@@ -53,6 +53,11 @@ struct Q8Args {
 };
 mm_status launch_gemm_q8(const Q8Args &a, LaunchCtx &ctx);
 
+// The operators' error word among the 16 of DeviceState::d_err (the first is
+// the GEMM candidates').  A kernel whose bounded wait gives up leaves a code
+// there; mm_operator_status reports and clears it.
+constexpr int kOperatorErrorWord = 8;
+
 // A kernel launch of the library outside the candidates, for the counters.
 inline void count_operator_launch() { stats().launches.fetch_add(1, std::memory_order_relaxed); }
 

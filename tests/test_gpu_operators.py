@@ -17,6 +17,12 @@ import matmul_selection_gb300 as mm
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True)
+def no_wait_gave_up():
+    yield
+    assert mm.mm_operator_status() == mm.MM_OK, mm.mm_last_error()
+
 BF, H, F, Q = mm.MM_BF16, mm.MM_F16, mm.MM_F32, mm.MM_E4M3
 U = {BF: 2.0 ** -8, H: 2.0 ** -11, F: 2.0 ** -24}
 LEAST = {BF: 2.0 ** -133, H: 2.0 ** -24, F: 2.0 ** -149}  # least positive values
