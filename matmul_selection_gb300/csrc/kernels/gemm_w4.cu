@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(kThreads) w4_simple_kernel(const W4Args a) {
 }  // namespace
 
 mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
+  if (a.M > 16 && a.K > 0) return launch_gemm_w4_tiles(a, ctx);
   const int64_t gx = ((int64_t)a.N + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t gy = std::min<int64_t>(((int64_t)a.M + kRows - 1) / kRows, 1024);
   cudaError_t e = launch_pdl(w4_simple_kernel, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), 0,

@@ -56,6 +56,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Acquire at cluster scope, for arrivals that the other CTA of a pair releases.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ uint64_t global_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -65,13 +77,15 @@ __device__ __forceinline__ uint64_t global_ns() {
 // Wait for the phase of `parity`, by a whole warp.  Gives up (false, in every
 // lane) when the CTA's abort flag is up, or after the limit: then it raises
 // the flag and records `code` in the error word.
+template <bool CLUSTER>
 __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                             int *err, int code) {
   const uint64_t t0 = global_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
+        return true;
     int stop = 0;
     if ((threadIdx.x & 31) == 0) {
       if (*abort_flag) {
@@ -85,10 +99,12 @@ __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volat
     if (__shfl_sync(0xffffffffu, stop, 0)) return false;
   }
 }
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                           int *err, int code) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return warp_wait_slow(bar, parity, abort_flag, err, code);
+  if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
+    return true;
+  return warp_wait_slow<CLUSTER>(bar, parity, abort_flag, err, code);
 }
 // A bounded wait that ignores the abort flag, for copies and MMAs in flight.
 __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, int *err, int code) {
@@ -98,6 +114,12 @@ __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, int *err,
       atomicCAS(err, 0, code);
       return;
     }
+}
+
+// Generic-proxy writes of this thread to shared memory, made visible to the
+// async proxy (the MMA's operand reads).
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- clusters
@@ -194,22 +216,28 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                  : "memory");
 }
-// D += A B^T of e4m3 operands in shared memory, 32 of K.  Warp-collective.
-template <int CG>
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                       uint32_t idesc, uint32_t accumulate) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+// D += A B^T of operands in shared memory, 32 bytes of K: F8 e4m3
+// (kind::f8f6f4), else bf16 or f16 (kind::f16, both operands the same type).
+// CG: CTAs of the group.  Warp-collective.
+#define MM_MMA_ASM(CGS, KIND)                                                                     \
+  asm volatile(                                                                                   \
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"          \
+      "@e tcgen05.mma.cta_group::" CGS ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), \
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)                                         \
+      : "memory")
+template <int CG, bool F8>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                    uint32_t accumulate) {
+  if constexpr (CG == 1 && F8) MM_MMA_ASM("1", "f8f6f4");
+  if constexpr (CG == 2 && F8) MM_MMA_ASM("2", "f8f6f4");
+  if constexpr (CG == 1 && !F8) MM_MMA_ASM("1", "f16");
+  if constexpr (CG == 2 && !F8) MM_MMA_ASM("2", "f16");
+}
+#undef MM_MMA_ASM
+// Instruction descriptor: D fp32, A and B of one type (kind::f8f6f4: 0 e4m3;
+// kind::f16: 0 f16, 1 bf16), both K-major, m x n.
+__host__ __device__ constexpr uint32_t instr_desc(uint32_t type, uint32_t m, uint32_t n) {
+  return (1u << 4) | (type << 7) | (type << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 // Arrive on `bar` (this CTA's) when the MMAs issued so far are complete.
 // Warp-collective.

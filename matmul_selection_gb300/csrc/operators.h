@@ -42,6 +42,7 @@ struct W4Args {
   int ta, ts, tc;
 };
 mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx);
+mm_status launch_gemm_w4_tiles(const W4Args &a, LaunchCtx &ctx);  // on tcgen05
 
 struct Q8Args {
   const uint8_t *A, *B;
@@ -52,6 +53,11 @@ struct Q8Args {
   int tc;
 };
 mm_status launch_gemm_q8(const Q8Args &a, LaunchCtx &ctx);
+
+// Rows of `bytes` bytes, ld apart, copied to rows ld16 (a multiple of 16)
+// apart, zeros after the last byte.
+mm_status launch_pack_rows(const void *src, int64_t ld, int64_t rows, int64_t bytes, void *dst,
+                           int64_t ld16, LaunchCtx &ctx);
 
 // The operators' error word among the 16 of DeviceState::d_err (the first is
 // the GEMM candidates').  A kernel whose bounded wait gives up leaves a code
