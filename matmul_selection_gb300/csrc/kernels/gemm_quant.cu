@@ -41,17 +41,20 @@ enum Format { FMT_E4M3, FMT_W4_BF16, FMT_W4_F16 };
 __host__ __device__ constexpr bool is_w4(int f) { return f != FMT_E4M3; }
 
 // Warp 0 copies operands, warp 1 issues MMAs, warps 2-5 store; for 4-bit
-// weights warps 6-13 make them and warp 14 copies codes.
-constexpr int kDequantWarps = 8;
+// weights warps 6-21 make them and warp 22 copies codes.  The weight-making
+// warps work in four groups of four, each on every fourth stage of the ring: a
+// stage's chain (a wait, the codes, the arithmetic, the fence to
+// the async proxy, the arrival) is then four stages long before it holds the
+// MMA up.
+constexpr int kGroups = 4, kGroupWarps = 4, kDequantWarps = kGroups * kGroupWarps;
 __host__ __device__ constexpr int threads_of(int f) { return is_w4(f) ? 32 * (6 + kDequantWarps + 1) : 192; }
 constexpr uint32_t kRowB = 128;  // bytes of K a stage
 constexpr int kErrCopy = 0x801, kErrMma = 0x802, kErrStore = 0x803, kErrDrain = 0x804, kErrCodes = 0x805,
               kErrDequant = 0x806;
 // A stage of codes: 128 bytes (256 codes, four stages of the operand ring) of
 // 128 rows.
-constexpr int kCodeStages = 3;
 constexpr uint32_t kCodeStageB = 128 * 128;
-__host__ __device__ constexpr uint32_t code_ring(int f) { return is_w4(f) ? kCodeStages * kCodeStageB : 0; }
+__host__ __device__ constexpr uint32_t code_ring(int f, int stages) { return is_w4(f) ? stages * kCodeStageB : 0; }
 
 struct QuantParams {
   void *out;
@@ -162,70 +165,81 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, const GroupScale<F> &g, bo
 
 // The weight-making warps' side of the two rings.
 struct DequantRing {
-  uint8_t *codes;             // kCodeStages stages of codes
-  uint32_t cfull0, cempty0;   // their barriers
-  uint32_t empty0;            // the operand ring's
-  int cs = 0, stage = 0;
-  uint32_t cphase = 0, phase = 0;
+  uint8_t *codes;
+  uint32_t cfull0, cempty0;  // the code stages' barriers
+  uint32_t empty0;           // the operand ring's
+  int cs = 0;
+  uint32_t cphase = 0;
+  uint32_t fill = 0;  // stages of the operand ring filled before this tile
 };
 
 // 128 rows (from row n0 of the weights; `rows` of them are needed) of the
-// blocks [kb0, kb0 + nk) into the operand ring: thread t makes the 32 weights
-// of half t / 128 of row t % 128 of every block.  `slot(stage)` is the
-// address of the stage's 128-byte rows, `arrive(stage)` reports one warp.
-template <int F, int STAGES, typename Slot, typename Arrive>
+// blocks [kb0, kb0 + nk) into the operand ring: each thread a row of its
+// group's blocks, those whose place in the ring is the group's modulo 4.
+// `slot(stage)` is the address of the stage's 128-byte rows, `arrive(stage)`
+// reports one warp.
+// A parity wait tells only adjacent phases apart: when a group waits for the
+// consumption of fill f - STAGES, its previous fill f - 4 needed that of
+// f - 4 - STAGES, which covers f - 2 STAGES only when STAGES >= 4.
+template <int F, int STAGES, int CSTAGES, typename Slot, typename Arrive>
 __device__ __forceinline__ bool dequant_blocks(const QuantParams &p, DequantRing &r, int n0, int rows,
                                                int kb0, int nk, volatile int *abort_flag, Slot &&slot,
                                                Arrive &&arrive) {
-  const int t = (int)threadIdx.x - 32 * 6, row = t & 127, half = t >> 7, lane = t & 31;
+  static_assert(STAGES >= kGroups, "the groups may not run more than a ring ahead");
+  const int t = (int)threadIdx.x - 32 * 6, row = t & 127, lane = t & 31;
+  const int j = (int)(((uint32_t)(t >> 7) - r.fill) % kGroups);  // the group's block of a stage of codes
   const int n = n0 + row;
-  RawScale next[4];
+  RawScale next[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) next[j] = load_raw_scale(p, n, (kb0 + j) * 64 + 32 * half);
-  for (int i = 0; i < nk; i += 4) {
-    RawScale cur[4];
+  for (int h = 0; h < 2; ++h) next[h] = load_raw_scale(p, n, (kb0 + j) * 64 + 32 * h);
+  for (int i = j; i < nk + j; i += kGroups) {  // a stage of codes, of which this group takes block j
+    RawScale cur[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      cur[j] = next[j];
-      next[j] = load_raw_scale(p, n, (kb0 + i + 4 + j) * 64 + 32 * half);
+    for (int h = 0; h < 2; ++h) {
+      cur[h] = next[h];
+      next[h] = load_raw_scale(p, n, (kb0 + i + kGroups) * 64 + 32 * h);
     }
     if (!warp_wait(r.cfull0 + 8 * r.cs, r.cphase, abort_flag, p.err, kErrDequant)) return false;
     const uint8_t *crow = r.codes + r.cs * kCodeStageB + row * 128;
+    uint4 c[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (i + j < nk) {
-        const uint4 c = *reinterpret_cast<const uint4 *>(crow + (((2 * j + half) ^ (row & 7)) << 4));
-        if (!warp_wait(r.empty0 + 8 * r.stage, r.phase ^ 1, abort_flag, p.err, kErrDequant)) return false;
-        if (row < rows) {
-          const GroupScale<F> g = group_scale<F>(p, cur[j]);
-          uint8_t *dst = slot(r.stage) + row * 128;
-          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-          if (p.split_scale) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4 *>(dst + (((4 * half + q) ^ (row & 7)) << 4)) = dequant8<F>(w[q], g, true);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4 *>(dst + (((4 * half + q) ^ (row & 7)) << 4)) = dequant8<F>(w[q], g, false);
-          }
-        }
-        fence_proxy_async_smem();  // the MMA reads through the async proxy
-        __syncwarp();
-        if (lane == 0) arrive(r.stage);
-        if (++r.stage == STAGES) {
-          r.stage = 0;
-          r.phase ^= 1;
-        }
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(r.cempty0 + 8 * r.cs);
-    if (++r.cs == kCodeStages) {
+    for (int h = 0; h < 2; ++h) c[h] = *reinterpret_cast<const uint4 *>(crow + (((2 * j + h) ^ (row & 7)) << 4));
+    const uint32_t cempty = r.cempty0 + 8 * r.cs;
+    if (++r.cs == CSTAGES) {
       r.cs = 0;
       r.cphase ^= 1;
     }
+    if (i >= nk) {  // the last stage of codes ends before this group's block
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cempty);
+      break;
+    }
+    const uint32_t f = r.fill + (uint32_t)i;
+    const int stage = (int)(f % STAGES);
+    if (!warp_wait(r.empty0 + 8 * stage, ((f / STAGES) & 1u) ^ 1u, abort_flag, p.err, kErrDequant)) return false;
+    if (row < rows) {
+      uint8_t *dst = slot(stage) + row * 128;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const GroupScale<F> g = group_scale<F>(p, cur[h]);
+        const uint32_t w[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4 *>(dst + (((4 * h + q) ^ (row & 7)) << 4)) =
+              p.split_scale ? dequant8<F>(w[q], g, true) : dequant8<F>(w[q], g, false);
+      }
+    }
+    fence_proxy_async_smem();  // the MMA reads through the async proxy
+    __syncwarp();
+    // The codes are given back only here, after their use: given back right
+    // behind the loads, the next copy overwrote some before they were read
+    // (wrong rows at K >= 2048).
+    if (lane == 0) {
+      arrive(stage);
+      mbar_arrive(cempty);
+    }
   }
+  r.fill += (uint32_t)nk;
   return true;
 }
 
@@ -234,6 +248,7 @@ struct CodeRing {
   int cs = 0;
   uint32_t phase = 0;
 };
+template <int CSTAGES>
 __device__ __forceinline__ bool copy_codes(const QuantParams &p, CodeRing &r, const CUtensorMap *map,
                                            uint8_t *codes, uint32_t cfull0, uint32_t cempty0, int n0, int kb0,
                                            int nk, volatile int *abort_flag) {
@@ -241,16 +256,17 @@ __device__ __forceinline__ bool copy_codes(const QuantParams &p, CodeRing &r, co
     if (!warp_wait(cempty0 + 8 * r.cs, r.phase ^ 1, abort_flag, p.err, kErrCodes)) return false;
     mbar_expect_tx(cfull0 + 8 * r.cs, kCodeStageB);
     tma_load_2d(smem_u32(codes + r.cs * kCodeStageB), map, cfull0 + 8 * r.cs, (kb0 + i) * 32, n0);
-    if (++r.cs == kCodeStages) {
+    if (++r.cs == CSTAGES) {
       r.cs = 0;
       r.phase ^= 1;
     }
   }
   return true;
 }
+template <int CSTAGES>
 __device__ __forceinline__ void drain_codes(const QuantParams &p, const CodeRing &r, uint32_t cfull0) {
-  for (int s = 0; s < kCodeStages; ++s) {
-    const int st = (r.cs + s) % kCodeStages;
+  for (int s = 0; s < CSTAGES; ++s) {
+    const int st = (r.cs + s) % CSTAGES;
     wait_drain(cfull0 + 8 * st, st < r.cs ? r.phase : r.phase ^ 1, p.err, kErrCodes);
   }
 }
@@ -266,8 +282,9 @@ __device__ __forceinline__ uint32_t pack2(int tc, float lo, float hi) {
 
 // ---------------------------------------------------------------- pair
 constexpr uint32_t kPairStageB = 2 * 128 * kRowB;
+constexpr int kPairCodeStages = 3;
 __host__ __device__ constexpr int pair_stages(int f) { return is_w4(f) ? 5 : 6; }
-__host__ __device__ constexpr size_t pair_smem(int f) { return pair_stages(f) * kPairStageB + code_ring(f) + 1024 + 256; }
+__host__ __device__ constexpr size_t pair_smem(int f) { return pair_stages(f) * kPairStageB + code_ring(f, kPairCodeStages) + 1024 + 512; }
 constexpr int kGroupRows = 8;  // row tiles walked together, so their A and B stay in L2
 
 // Tile of a unit: row tile, first column, width (256, or 128 for the halves
@@ -290,18 +307,18 @@ template <int F>
 __global__ void __launch_bounds__(threads_of(F), 1)
     quant_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmBh, const QuantParams p) {
-  constexpr int STAGES = pair_stages(F);
+  constexpr int STAGES = pair_stages(F), CSTAGES = kPairCodeStages;
   constexpr bool W4 = is_w4(F);
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *codes = smem + STAGES * kPairStageB;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(codes + code_ring(F));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(codes + code_ring(F, CSTAGES));
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
   const uint32_t tfull0 = empty0 + 8 * STAGES, tempty0 = tfull0 + 16, drain = tempty0 + 16;
-  const uint32_t cfull0 = drain + 8, cempty0 = cfull0 + 8 * kCodeStages;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 5 + 2 * kCodeStages);
+  const uint32_t cfull0 = drain + 8, cempty0 = cfull0 + 8 * CSTAGES;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 5 + 2 * CSTAGES);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t pos = cluster_ctarank();
@@ -310,7 +327,7 @@ __global__ void __launch_bounds__(threads_of(F), 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full0 + 8 * s, W4 ? 1 + 2 * kDequantWarps : 1);  // the arming; both CTAs' weights
+      mbar_init(full0 + 8 * s, W4 ? 1 + 2 * kGroupWarps : 1);  // the arming; both CTAs' weights
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -318,7 +335,7 @@ __global__ void __launch_bounds__(threads_of(F), 1)
       mbar_init(tempty0 + 8 * a, 8);  // four storing warps of both CTAs
     }
     mbar_init(drain, 1);
-    for (int s = 0; s < kCodeStages; ++s) {
+    for (int s = 0; s < CSTAGES; ++s) {
       mbar_init(cfull0 + 8 * s, 1);
       mbar_init(cempty0 + 8 * s, kDequantWarps);
     }
@@ -337,7 +354,7 @@ __global__ void __launch_bounds__(threads_of(F), 1)
         if (!W4) tma_prefetch_2d(&tmB, kb * 128, n0 + (int)pos * (w / 2));
       }
       if (W4)
-        for (int c = 0; c < min((p.num_kb + 3) / 4, kCodeStages); ++c)
+        for (int c = 0; c < min((p.num_kb + 3) / 4, CSTAGES); ++c)
           tma_prefetch_2d(&tmB, c * 128, n0 + (int)pos * (w / 2));
     }
   }
@@ -428,17 +445,17 @@ __global__ void __launch_bounds__(threads_of(F), 1)
         for (int u = cid; u < p.total_units; u += ncl) {
           int tm, n0, w;
           pair_unit(p, u, tm, n0, w);
-          if (!copy_codes(p, r, &tmB, codes, cfull0, cempty0, n0 + (int)pos * (w / 2), 0, p.num_kb, abort_flag))
+          if (!copy_codes<CSTAGES>(p, r, &tmB, codes, cfull0, cempty0, n0 + (int)pos * (w / 2), 0, p.num_kb, abort_flag))
             break;
         }
-        drain_codes(p, r, cfull0);
+        drain_codes<CSTAGES>(p, r, cfull0);
         __syncwarp();
       } else {
         DequantRing r{codes, cfull0, cempty0, empty0};
         for (int u = cid; u < p.total_units; u += ncl) {
           int tm, n0, w;
           pair_unit(p, u, tm, n0, w);
-          if (!dequant_blocks<F, STAGES>(
+          if (!dequant_blocks<F, STAGES, CSTAGES>(
                   p, r, n0 + (int)pos * (w / 2), w / 2, 0, p.num_kb, abort_flag,
                   [&](int st) { return smem + st * kPairStageB + 128 * kRowB; },
                   [&](int st) { mbar_arrive_cluster(leader_full0 + 8 * st); }))
@@ -514,10 +531,11 @@ __global__ void __launch_bounds__(threads_of(F), 1)
 template <int F, int BN>
 struct Swap {
   static constexpr uint32_t kStageB = (128 + BN) * kRowB;
-  static constexpr int kStages = is_w4(F) ? (BN <= 64 ? 6 : BN == 128 ? 5 : 3)
+  static constexpr int kCodeStages = BN == 256 ? 2 : 3;
+  static constexpr int kStages = is_w4(F) ? (BN <= 64 ? 6 : BN == 128 ? 5 : 4)
                                           : (BN == 32 ? 10 : BN == 64 ? 8 : BN == 128 ? 6 : 4);
   static constexpr size_t kTileB = (size_t)BN * 128 * 4;  // the fp32 tile, over the ring
-  static constexpr size_t kSmem = kStages * kStageB + code_ring(F) + 1024 + 256;
+  static constexpr size_t kSmem = kStages * kStageB + code_ring(F, kCodeStages) + 1024 + 512;
   static constexpr uint32_t kCols = BN;  // TMEM columns, a power of two of at least 32
   static_assert(kTileB <= kStages * kStageB, "the fp32 tile fits the ring");
 };
@@ -533,11 +551,11 @@ __global__ void __launch_bounds__(threads_of(F), 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *codes = smem + S::kStages * S::kStageB;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(codes + code_ring(F));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(codes + code_ring(F, S::kCodeStages));
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages;
   const uint32_t done = empty0 + 8 * S::kStages;
-  const uint32_t cfull0 = done + 8, cempty0 = cfull0 + 8 * kCodeStages;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S::kStages + 1 + 2 * kCodeStages);
+  const uint32_t cfull0 = done + 8, cempty0 = cfull0 + 8 * S::kCodeStages;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S::kStages + 1 + 2 * S::kCodeStages);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster along x splits K
@@ -546,11 +564,11 @@ __global__ void __launch_bounds__(threads_of(F), 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full0 + 8 * s, W4 ? 1 + kDequantWarps : 1);
+      mbar_init(full0 + 8 * s, W4 ? 1 + kGroupWarps : 1);
       mbar_init(empty0 + 8 * s, 1);
     }
     mbar_init(done, 1);
-    for (int s = 0; s < kCodeStages; ++s) {
+    for (int s = 0; s < S::kCodeStages; ++s) {
       mbar_init(cfull0 + 8 * s, 1);
       mbar_init(cempty0 + 8 * s, kDequantWarps);
     }
@@ -603,12 +621,12 @@ __global__ void __launch_bounds__(threads_of(F), 1)
     if constexpr (W4) {
       if (warp == 6 + kDequantWarps) {
         CodeRing r;
-        copy_codes(p, r, &tmB, codes, cfull0, cempty0, n0, kb0, nk, abort_flag);
-        drain_codes(p, r, cfull0);
+        copy_codes<S::kCodeStages>(p, r, &tmB, codes, cfull0, cempty0, n0, kb0, nk, abort_flag);
+        drain_codes<S::kCodeStages>(p, r, cfull0);
         __syncwarp();
       } else {
         DequantRing r{codes, cfull0, cempty0, empty0};
-        dequant_blocks<F, S::kStages>(
+        dequant_blocks<F, S::kStages, S::kCodeStages>(
             p, r, n0, 128, kb0, nk, abort_flag, [&](int st) { return smem + st * S::kStageB; },
             [&](int st) { mbar_arrive(full0 + 8 * st); });
       }

@@ -404,6 +404,20 @@ def test_w4_sizes(M, N, K, group):
         check_w4(a, w, t, run_w4(a, codes, ldw, s, z, N, K, group, t, 3 if zeros else 0))
 
 
+@pytest.mark.parametrize("M", [1, 16, 100, 250, 300])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_long_k(M, group):
+    """The rings of the main loops wrap many times; equal calls, equal bits."""
+    g = generator(M + group)
+    N, K, t = 512, 12288, (BF, BF, BF)
+    a = rows_of(g, M, K, BF)
+    codes, ldw, s, z, w = w4_weights(g, N, K, group, BF, True)
+    first = run_w4(a, codes, ldw, s, z, N, K, group, t)
+    check_w4(a, w, t, first)
+    for _ in range(8):
+        assert T().equal(run_w4(a, codes, ldw, s, z, N, K, group, t), first)
+
+
 @pytest.mark.parametrize("M", [1, 5, 16, 40])
 @pytest.mark.parametrize("K", [1, 2, 15, 31, 32, 33, 63, 64, 127, 129, 255, 257])
 def test_w4_short_k(M, K):
