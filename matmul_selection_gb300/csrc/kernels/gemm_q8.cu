@@ -1,0 +1,538 @@
+// Product of e4m3 operands with row scales, on tcgen05 (kind::f8f6f4):
+//   out[m, n] = scale_a[m] scale_b[n] sum_k A[m, k] B[n, k]
+// The scales are factors of a whole row or column of the output, so they stay
+// out of the sum: the tensor core adds e4m3 products in fp32 and the epilogue
+// multiplies once.  Both operands are K-major; a stage of the ring holds 128
+// bytes of K (four MMAs of 32), laid out by TMA with the 128-byte swizzle.
+//
+//   pair   many rows: 256 x 256 output tiles on pairs of SMs
+//          (cta_group::2), each SM loading 128 rows of A and 128 of B a stage;
+//          persistent, two accumulators in TMEM, so that a tile's epilogue
+//          runs under the next tile's main loop.
+//   swap   few rows: out^T = B A^T, 128 rows of B (the weights) on the MMA's
+//          128-lane side and BN rows of A on the other, so that a short A is
+//          not padded to 128 rows.  K is split over the CTAs of a cluster;
+//          their fp32 tiles are added through distributed shared memory in
+//          rank order, which is one launch, no workspace and the same bits
+//          every time.
+// Every mbarrier wait is bounded (see tcgen05.cuh); a wait that gives up
+// records a code in the operators' error word.
+#include <algorithm>
+#include <mutex>
+
+#include "../operators.h"
+#include "tcgen05.cuh"
+#include "values.cuh"
+
+namespace mm {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 192;  // warp 0 copies, warp 1 issues MMAs, warps 2-5 store
+constexpr uint32_t kRowB = 128;  // bytes of K a stage
+constexpr int kErrCopy = 0x801, kErrMma = 0x802, kErrStore = 0x803, kErrDrain = 0x804;
+
+struct Q8Params {
+  void *out;
+  int64_t ldc;
+  const float *sa, *sb;
+  int tc;
+  int M, N;
+  int num_kb;       // 128-byte blocks of K
+  int tiles_m, tiles_n;
+  int full_units;   // pair: units of whole tiles; those after are half tiles
+  int total_units;
+  int kb_per_rank;  // swap
+  int vec;          // out's rows are 16-byte aligned
+  int *err;
+};
+
+__device__ __forceinline__ uint32_t pack2(int tc, float lo, float hi) {
+  if (tc == MM_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// ---------------------------------------------------------------- pair
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairStageB = 2 * 128 * kRowB;
+constexpr size_t kPairSmem = kPairStages * kPairStageB + 1024 + 256;
+constexpr int kGroupRows = 8;  // row tiles walked together, so their A and B stay in L2
+
+// Tile of a unit: row tile, first column, width (256, or 128 for the halves
+// that the last, partly filled wave's tiles are cut into).
+__device__ __forceinline__ void pair_unit(const Q8Params &p, int u, int &tm, int &n0, int &w) {
+  int t = u, half = -1;
+  if (u >= p.full_units) {
+    t = p.full_units + ((u - p.full_units) >> 1);
+    half = (u - p.full_units) & 1;
+  }
+  const int per = kGroupRows * p.tiles_n;
+  const int g = t / per, rows = min(kGroupRows, p.tiles_m - g * kGroupRows);
+  const int r = t - g * per;
+  tm = g * kGroupRows + r % rows;
+  n0 = (r / rows) * 256 + (half > 0 ? 128 : 0);
+  w = half < 0 ? 256 : 128;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    q8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmBh, const Q8Params p) {
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kPairStages * kPairStageB);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kPairStages;
+  const uint32_t tfull0 = empty0 + 8 * kPairStages, tempty0 = tfull0 + 16, drain = tempty0 + 16;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kPairStages + 5);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t pos = cluster_ctarank();
+  const bool leader = pos == 0;
+  const int cid = (int)cluster_id_x(), ncl = (int)nclusters_x();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, 8);  // four storing warps of both CTAs
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmBh);
+    if (cid < p.total_units) {  // the first blocks of this CTA's operands into L2
+      int tm, n0, w;
+      pair_unit(p, cid, tm, n0, w);
+      for (int kb = 0; kb < min(p.num_kb, kPairStages); ++kb) {
+        tma_prefetch_2d(&tmA, kb * (int)kRowB, tm * 256 + (int)pos * 128);
+        tma_prefetch_2d(&tmB, kb * (int)kRowB, n0 + (int)pos * (w / 2));
+      }
+    }
+  }
+  if (warp == 1) tmem_alloc<2>(smem_u32(tmem_slot), 512);
+  fence_before();
+  cluster_sync_all();
+  fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t leader_full0 = map_to_rank(full0, 0), leader_tempty0 = map_to_rank(tempty0, 0);
+  pdl_wait();
+
+  if (warp == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = cid; u < p.total_units && ok; u += ncl) {
+      int tm, n0, w;
+      pair_unit(p, u, tm, n0, w);
+      const int nh = w / 2, m0 = tm * 256 + (int)pos * 128;
+      const uint32_t bytes = 2 * (128 + nh) * kRowB;  // of both CTAs
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.err, kErrCopy)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = smem_u32(smem + stage * kPairStageB), sb = sa + 128 * kRowB;
+        const uint32_t lfb = leader_full0 + 8 * stage;
+        if (leader) mbar_expect_tx(full0 + 8 * stage, bytes);
+        tma_load_2d_pair(sa, &tmA, lfb, kb * (int)kRowB, m0);
+        tma_load_2d_pair(sb, w == 256 ? &tmB : &tmBh, lfb, kb * (int)kRowB, n0 + (int)pos * nh);
+        if (++stage == kPairStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (leader)  // both CTAs' copies have landed
+      for (int s = 0; s < kPairStages; ++s) {
+        const int st = (stage + s) % kPairStages;
+        wait_drain(full0 + 8 * st, st < stage ? phase : phase ^ 1, p.err, kErrCopy);
+      }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (leader) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int u = cid; u < p.total_units && ok; u += ncl) {
+        int tm, n0, w;
+        pair_unit(p, u, tm, n0, w);
+        const uint32_t idesc = instr_desc(0, 256, (uint32_t)w);
+        if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.err, kErrMma)) break;
+        fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * 256);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.err, kErrMma)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint32_t sa = smem_u32(smem + stage * kPairStageB);
+          const uint64_t ad = desc_at(sa), bd = desc_at(sa + 128 * kRowB);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8<2>(d, ad + 2 * kk, bd + 2 * kk, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_pair(empty0 + 8 * stage);
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(tfull0 + 8 * acc);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      mma_commit<2>(drain);
+      wait_drain(drain, 0, p.err, kErrDrain);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;  // the TMEM lanes this warp may read
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int u = cid; u < p.total_units; u += ncl) {
+      int tm, n0, w;
+      pair_unit(p, u, tm, n0, w);
+      if (!warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.err, kErrStore)) break;
+      fence_after();
+      const int row = tm * 256 + (int)pos * 128 + q * 32 + lane;
+      const float sa = p.sa && row < p.M ? p.sa[row] : 1.f;
+      const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
+#pragma unroll 1
+      for (int c = 0; c < w && n0 + c < p.N; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32cols(tbase + (uint32_t)c, r);
+        tmem_ld_wait();
+        if (row >= p.M) continue;
+        const int col = n0 + c;
+        const int64_t at = (int64_t)row * p.ldc + col;
+        if (p.vec && col + 32 <= p.N) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = __uint_as_float(r[i]) * sa * (p.sb ? __ldg(p.sb + col + i) : 1.f);
+          if (p.tc == MM_F32) {
+            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack2(p.tc, v[8 * i], v[8 * i + 1]), pack2(p.tc, v[8 * i + 2], v[8 * i + 3]),
+                                  pack2(p.tc, v[8 * i + 4], v[8 * i + 5]), pack2(p.tc, v[8 * i + 6], v[8 * i + 7]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (col + i < p.N)
+              store_value(p.out, p.tc, at + i, __uint_as_float(r[i]) * sa * (p.sb ? __ldg(p.sb + col + i) : 1.f));
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8 * acc);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (*abort_flag) {  // the other CTA's copies into this one may still be landing
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 100000ull) __nanosleep(1000);
+  }
+  cluster_sync_all();  // the leader's MMAs read both CTAs' memory
+  fence_after();
+  if (warp == 1) tmem_dealloc<2>(tmem_base, 512);
+}
+
+// ---------------------------------------------------------------- swap
+template <int BN>
+struct Swap {
+  static constexpr uint32_t kStageB = (128 + BN) * kRowB;
+  static constexpr int kStages = BN == 32 ? 10 : BN == 64 ? 8 : BN == 128 ? 6 : 4;
+  static constexpr size_t kTileB = (size_t)BN * 128 * 4;  // the fp32 tile, over the ring
+  static constexpr size_t kSmem = kStages * kStageB + 1024 + 256;
+  static constexpr uint32_t kCols = BN;  // TMEM columns, a power of two of at least 32
+  static_assert(kTileB <= kStages * kStageB, "the fp32 tile fits the ring");
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    q8_swap_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA,
+                   const Q8Params p) {
+  using S = Swap<BN>;
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kStages * S::kStageB);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages;
+  const uint32_t done = empty0 + 8 * S::kStages;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S::kStages + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ranks = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster along x splits K
+  const int n0 = (int)blockIdx.y * 128, m0 = (int)blockIdx.z * BN;
+  const int kb0 = rank * p.kb_per_rank, nk = max(0, min(p.kb_per_rank, p.num_kb - kb0));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    for (int i = 0; i < min(nk, 16); ++i) tma_prefetch_2d(&tmB, (kb0 + i) * (int)kRowB, n0);
+  }
+  if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), S::kCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+
+  if (warp == 0) {
+    int i = 0;
+    for (; i < nk; ++i) {
+      const int st = i % S::kStages;
+      if (!warp_wait(empty0 + 8 * st, ((uint32_t)(i / S::kStages) & 1u) ^ 1u, abort_flag, p.err, kErrCopy)) break;
+      const uint32_t sb = smem_u32(smem + st * S::kStageB);
+      mbar_expect_tx(full0 + 8 * st, S::kStageB);
+      tma_load_2d(sb, &tmB, full0 + 8 * st, (kb0 + i) * (int)kRowB, n0);
+      tma_load_2d(sb + 128 * kRowB, &tmA, full0 + 8 * st, (kb0 + i) * (int)kRowB, m0);
+    }
+    for (int f = max(0, i - S::kStages); f < i; ++f)
+      wait_drain(full0 + 8 * (f % S::kStages), (uint32_t)(f / S::kStages) & 1u, p.err, kErrCopy);
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = instr_desc(0, 128, BN);
+    for (int i = 0; i < nk; ++i) {
+      const int st = i % S::kStages;
+      if (!warp_wait(full0 + 8 * st, (uint32_t)(i / S::kStages) & 1u, abort_flag, p.err, kErrMma)) break;
+      fence_after();
+      const uint32_t sb = smem_u32(smem + st * S::kStageB);
+      const uint64_t bd = desc_at(sb), ad = desc_at(sb + 128 * kRowB);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_f8<1>(tmem_base, bd + 2 * kk, ad + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+      mma_commit<1>(empty0 + 8 * st);
+    }
+    mma_commit<1>(done);
+    wait_drain(done, 0, p.err, kErrDrain);
+    __syncwarp();
+  }
+  // A wait at the end of a short main loop, by every thread that stores: the
+  // MMAs are complete (the ring is idle) and the accumulator can be read.
+  const int q = warp & 3;
+  bool ok = true;
+  if (warp >= 2) {
+    ok = warp_wait(done, 0, abort_flag, p.err, kErrStore);
+    fence_after();
+  }
+  const int cols = min(BN, p.M - m0);  // rows of A in the tile
+  const int n = n0 + q * 32 + lane;
+  const float sb = p.sb && n < p.N ? p.sb[n] : 1.f;
+  const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16);
+  if (ranks == 1) {
+    if (warp >= 2 && ok) {
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32cols(tbase + (uint32_t)c, r);
+        tmem_ld_wait();
+        if (n < p.N) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < cols) {
+              const int m = m0 + c + i;
+              store_value(p.out, p.tc, (int64_t)m * p.ldc + n,
+                          __uint_as_float(r[i]) * (p.sa ? __ldg(p.sa + m) : 1.f) * sb);
+            }
+        }
+      }
+    }
+  } else {
+    float *tile = reinterpret_cast<float *>(smem);  // [BN][128]
+    if (warp >= 2) {
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32cols(tbase + (uint32_t)c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) tile[(c + i) * 128 + q * 32 + lane] = nk > 0 ? __uint_as_float(r[i]) : 0.f;
+      }
+    }
+    cluster_sync_all();
+    // rank r adds the rows r, r + ranks, ... of the tile, over the ranks in order
+    if (warp >= 2 && n < p.N) {
+      const uint32_t mine = smem_u32(tile + q * 32 + lane);
+      for (int m = rank; m < cols; m += ranks) {
+        float part[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < ranks) part[k] = ld_cluster_f32(map_to_rank(mine + (uint32_t)m * 512u, (uint32_t)k));
+        float v = part[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+          if (k < ranks) v += part[k];
+        store_value(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n, v * (p.sa ? __ldg(p.sa + m0 + m) : 1.f) * sb);
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its tile
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) tmem_dealloc<1>(tmem_base, S::kCols);
+}
+
+// ---------------------------------------------------------------- host side
+// A K-major map in boxes of 128 bytes of K x box_rows.
+mm_status rows_map(CUtensorMap *map, const uint8_t *p, int rows, int K, int64_t ld, int box_rows) {
+  if (rows == 1) ld = ((int64_t)K + 15) / 16 * 16;
+  return encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, (uint64_t)K, (uint64_t)rows, (uint64_t)ld,
+                       kRowB, (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+mm_status pair_capacity(int *clusters) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  static int n = 0;
+  std::call_once(once, [] {
+    err = cudaFuncSetAttribute(q8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+    if (err != cudaSuccess) return;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(2);
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = kPairSmem;
+    lc.attrs = &at;
+    lc.numAttrs = 1;
+    err = cudaOccupancyMaxActiveClusters(&n, q8_pair_kernel, &lc);
+  });
+  if (err != cudaSuccess) return cuda_error(err, "gemm_q8 set-up");
+  if (n < 1) return set_error(MM_ERR_UNSUPPORTED, "no pair of CTAs fits on this device");
+  *clusters = n;
+  return MM_OK;
+}
+
+mm_status run_pair(const Q8Args &a, Q8Params p, int clusters, LaunchCtx &ctx) {
+  CUtensorMap ma, mb, mbh;
+  mm_status st;
+  if ((st = rows_map(&ma, a.A, a.M, a.K, a.lda, 128)) != MM_OK) return st;
+  if ((st = rows_map(&mb, a.B, a.N, a.K, a.ldb, 128)) != MM_OK) return st;
+  if ((st = rows_map(&mbh, a.B, a.N, a.K, a.ldb, 64)) != MM_OK) return st;
+  p.tiles_m = (a.M + 255) / 256;
+  p.tiles_n = (a.N + 255) / 256;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  if (tiles >= (1LL << 30)) return set_error(MM_ERR_UNSUPPORTED, "too many tiles");
+  // a last wave that fills at most half the pairs is cut into half tiles
+  const int64_t rem = tiles % clusters;
+  const bool halve = tiles > clusters && rem > 0 && 2 * rem <= clusters;
+  p.full_units = (int)(halve ? tiles - rem : tiles);
+  p.total_units = (int)(halve ? tiles + rem : tiles);
+  const int grid = 2 * (int)std::min<int64_t>(p.total_units, clusters);
+  cudaError_t e = launch_pdl(q8_pair_kernel, dim3((unsigned)grid), dim3(kThreads), kPairSmem, ctx.stream,
+                             dim3(2), ma, mb, mbh, p);
+  return e == cudaSuccess ? MM_OK : cuda_error(e, "gemm_q8 launch (pair)");
+}
+
+template <int BN>
+mm_status run_swap(const Q8Args &a, Q8Params p, int ranks, LaunchCtx &ctx) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    err = cudaFuncSetAttribute(q8_swap_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)Swap<BN>::kSmem);
+  });
+  if (err != cudaSuccess) return cuda_error(err, "gemm_q8 set-up");
+  CUtensorMap ma, mb;
+  mm_status st;
+  if ((st = rows_map(&mb, a.B, a.N, a.K, a.ldb, 128)) != MM_OK) return st;
+  if ((st = rows_map(&ma, a.A, a.M, a.K, a.lda, BN)) != MM_OK) return st;
+  p.kb_per_rank = (p.num_kb + ranks - 1) / ranks;
+  const int gy = (a.N + 127) / 128, gz = (a.M + BN - 1) / BN;
+  if (gy > 65535 || gz > 65535) return set_error(MM_ERR_UNSUPPORTED, "too many tiles");
+  cudaError_t e = launch_pdl(q8_swap_kernel<BN>, dim3((unsigned)ranks, (unsigned)gy, (unsigned)gz),
+                             dim3(kThreads), Swap<BN>::kSmem, ctx.stream, dim3((unsigned)ranks), mb, ma, p);
+  return e == cudaSuccess ? MM_OK : cuda_error(e, "gemm_q8 launch (swap)");
+}
+
+}  // namespace
+
+mm_status launch_gemm_q8(const Q8Args &in, LaunchCtx &ctx) {
+  Q8Args a = in;
+  mm_status st;
+  if (a.K == 0) {
+    const size_t es = (size_t)dtype_bytes(a.tc);
+    MM_CUDA_TRY(cudaMemset2DAsync(a.out, (size_t)a.ldc * es, 0, (size_t)a.N * es, (size_t)a.M, ctx.stream));
+    return MM_OK;
+  }
+  TmaRows ra{a.A, a.lda, a.M, a.K}, rb{a.B, a.ldb, a.N, a.K};
+  if ((st = align_rows(ra, rb, ctx)) != MM_OK) return st;
+  a.A = static_cast<const uint8_t *>(ra.p);
+  a.lda = ra.ld;
+  a.B = static_cast<const uint8_t *>(rb.p);
+  a.ldb = rb.ld;
+  Q8Params p;
+  std::memset(&p, 0, sizeof p);
+  p.out = a.out;
+  p.ldc = a.ldc;
+  p.sa = a.scale_a;
+  p.sb = a.scale_b;
+  p.tc = a.tc;
+  p.M = a.M;
+  p.N = a.N;
+  p.num_kb = (int)(((int64_t)a.K + kRowB - 1) / kRowB);
+  p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0;
+  p.err = ctx.dev->d_err + kOperatorErrorWord;
+  int clusters = 0;
+  if ((st = pair_capacity(&clusters)) != MM_OK) return st;
+  if (a.M > 256) {
+    st = run_pair(a, p, clusters, ctx);
+  } else {
+    const int bn = a.M <= 32 ? 32 : a.M <= 64 ? 64 : a.M <= 128 ? 128 : 256;
+    const int64_t tiles = ((int64_t)a.N + 127) / 128 * ((a.M + bn - 1) / bn);
+    int ranks = 1;
+    while (ranks < 8 && tiles * ranks * 2 <= ctx.dev->info.sms && p.num_kb >= 4 * ranks) ranks *= 2;
+    st = bn == 32    ? run_swap<32>(a, p, ranks, ctx)
+         : bn == 64  ? run_swap<64>(a, p, ranks, ctx)
+         : bn == 128 ? run_swap<128>(a, p, ranks, ctx)
+                     : run_swap<256>(a, p, ranks, ctx);
+  }
+  if (st != MM_OK) return st;
+  count_operator_launch();
+  return MM_OK;
+}
+
+}  // namespace mm

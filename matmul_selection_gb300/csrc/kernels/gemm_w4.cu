@@ -1,15 +1,488 @@
 // Product with weights held in 4 bits and group scales:
 //   out[m, n] = sum_k A[m, k] s[n, k / group] (q[n, k] - z[n, k / group])
 //
-// Simple form: a warp an output row of W and kRows rows of A; each lane sums
-// its k's in fp32.
+// M > 16, on tcgen05 (kind::f16), as out^T = W A^T: 128 rows of the weights are
+// the MMA's A side, BN rows of A its other side.  The scales change along K, so
+// the weights are made on the way in: sixteen warps turn codes into 16-bit
+// weights (q - z is exact, its product with the scale is rounded once to A's
+// type) and write them into TMEM, from where the MMA takes its A operand.
+// Through shared memory the writes would have to be fenced to the async proxy
+// stage by stage, which took longer than the MMA of the stage.  Codes and
+// rows of A come by TMA through a ring each; a stage holds 64 of K.  CTAs are
+// persistent; where there are few tiles K is split over the CTAs of a cluster,
+// whose fp32 tiles are added through distributed shared memory in rank order.
+//
+// M <= 16: a warp an output column and kRows rows of A; each lane sums its k's
+// in fp32.
+#include <algorithm>
+#include <mutex>
+
 #include "../operators.h"
+#include "tcgen05.cuh"
 #include "values.cuh"
 
 namespace mm {
 
 namespace {
 
+using namespace tc;
+
+// ---------------------------------------------------------------- tiles
+constexpr int kErrCopy = 0x901, kErrMma = 0x902, kErrStore = 0x903, kErrDrain = 0x904, kErrCodes = 0x905,
+              kErrDequant = 0x906;
+
+// Warp 0 copies A, warp 1 issues MMAs, warp 2 copies codes, warps 4-11 store
+// (two for each quarter of the 128 lanes), warps 12-27 make weights: four
+// groups of four, each on every fourth stage, so that a stage's chain (two
+// waits, the codes, the arithmetic, the write to TMEM) may take four stages'
+// time.
+constexpr int kStoreWarp = 4, kStoreWarps = 8, kDequantWarp = 12;
+constexpr int kGroups = 4, kGroupWarps = 4, kDequantWarps = kGroups * kGroupWarps;
+constexpr int kTileThreads = 32 * (kDequantWarp + kDequantWarps);
+constexpr uint32_t kCodeStageB = 128 * 128;  // 256 codes (four stages) of 128 rows
+
+template <int BN>
+struct Tile {
+  static constexpr uint32_t kStageB = BN * 128;
+  static constexpr int kStages = BN == 256 ? 5 : BN == 128 ? 6 : 7;
+  static constexpr int kCodeStages = BN == 256 ? 3 : 5;
+  static constexpr size_t kSmem = kStages * kStageB + kCodeStages * kCodeStageB + 1024 + 512;
+  // TMEM: the accumulator, then the stages' weights, 32 columns each
+  static constexpr uint32_t kUsed = BN + 32 * kStages, kCols = kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512 && kStages >= kGroups, "TMEM; see dequant_blocks");
+  static_assert((size_t)BN * 512 <= kStages * kStageB + kCodeStages * kCodeStageB, "the fp32 tile fits the rings");
+};
+
+struct TileParams {
+  void *out;
+  int64_t ldc;
+  int tc;
+  int M, N;
+  int num_kb;       // blocks of 64 of K
+  int kb_per_rank;  // a multiple of 4 where K is split
+  int tiles_n, tiles;
+  int *err;
+  const void *scales;
+  const uint8_t *zeros;
+  int64_t lds;
+  int ts, group_shift, groups;
+  int split_scale;  // the scales' type is not A's
+};
+
+template <int TA>
+struct Pair16 {
+  using T = __nv_bfloat162;
+  static __device__ __forceinline__ T both(float v) { return __float2bfloat162_rn(v); }
+};
+template <>
+struct Pair16<MM_F16> {
+  using T = __half2;
+  static __device__ __forceinline__ T both(float v) { return __float2half2_rn(v); }
+};
+template <typename T>
+__device__ __forceinline__ T bits_as(uint32_t v) {
+  return *reinterpret_cast<const T *>(&v);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t as_bits(const T &v) {
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// A row's scales and zero points: where they start, and how many there are (0
+// past the last row).
+struct ScaleRow {
+  const char *s;
+  const uint8_t *z;
+  int groups;
+};
+__device__ __forceinline__ ScaleRow scale_row(const TileParams &p, int n) {
+  const bool in = n < p.N;
+  const int64_t at = in ? (int64_t)n * p.lds : 0;
+  return ScaleRow{static_cast<const char *>(p.scales) + at * (p.ts == MM_F32 ? 4 : 2),
+                  p.zeros ? p.zeros + at : nullptr, in ? p.groups : 0};
+}
+// A scale and a zero point as they lie in memory, loaded a stage of codes ahead.
+struct RawScale {
+  uint32_t s, z;
+};
+__device__ __forceinline__ RawScale load_raw_scale(const TileParams &p, const ScaleRow &row, int k) {
+  RawScale r{0u, 8u};
+  const int g = k >> p.group_shift;
+  if (g < row.groups) {
+    r.s = p.ts == MM_F32 ? __ldg(reinterpret_cast<const uint32_t *>(row.s) + g)
+                         : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row.s) + g);
+    if (row.z) r.z = __ldg(row.z + g);
+  }
+  return r;
+}
+
+// The scale and zero point of 32 codes of a row.  A scale of another type than
+// A's is taken as a sum of two of A's type, hi + lo, so that a weight is still
+// rounded once (to within 2^-8 of a rounding).
+template <int TA>
+struct GroupScale {
+  typename Pair16<TA>::T hi, lo, zero;
+};
+template <int TA>
+__device__ __forceinline__ GroupScale<TA> group_scale(const TileParams &p, const RawScale &r) {
+  using T = typename Pair16<TA>::T;
+  const float s = p.ts == MM_F32    ? __uint_as_float(r.s)
+                  : p.ts == MM_BF16 ? __uint_as_float(r.s << 16)
+                                    : __half2float(__ushort_as_half((unsigned short)r.s));
+  GroupScale<TA> g;
+  g.hi = Pair16<TA>::both(s);
+  g.lo = Pair16<TA>::both(p.split_scale ? s - __low2float(g.hi) : 0.f);
+  // the bias that the codes are read with, and the zero point
+  g.zero = bits_as<T>((TA == MM_BF16 ? 0x43004300u : 0x64006400u) + (r.z & 15u) * 0x00010001u);
+  return g;
+}
+
+// Eight codes of a word into eight weights in k order.  A code in the low
+// mantissa bits of 128 (bf16) or 1024 (f16) is the number 128 + q or 1024 + q;
+// the difference with 128 + z or 1024 + z is exact.
+template <int TA>
+__device__ __forceinline__ void dequant8(uint32_t w, const GroupScale<TA> &g, bool split, uint32_t *out) {
+  using T = typename Pair16<TA>::T;
+  constexpr uint32_t kBias = TA == MM_BF16 ? 0x43004300u : 0x64006400u;
+  uint32_t v[4];  // (0, 4), (1, 5), (2, 6), (3, 7)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const T d = __hsub2(bits_as<T>(((w >> (4 * i)) & 0x000f000fu) | kBias), g.zero);
+    v[i] = as_bits(split ? __hfma2(d, g.hi, __hmul2(d, g.lo)) : __hmul2(d, g.hi));
+  }
+  out[0] = __byte_perm(v[0], v[1], 0x5410);
+  out[1] = __byte_perm(v[2], v[3], 0x5410);
+  out[2] = __byte_perm(v[0], v[1], 0x7632);
+  out[3] = __byte_perm(v[2], v[3], 0x7632);
+}
+
+// The weight-making warps' side of the rings.
+struct DequantRing {
+  const uint8_t *codes;
+  uint32_t cfull0, cempty0;  // the code stages' barriers
+  uint32_t empty0, wfull0;   // a stage is free; its weights are written
+  uint32_t weights;          // TMEM address of stage 0's weights
+  int cs = 0;
+  uint32_t cphase = 0;
+  uint32_t fill = 0;  // stages filled before this tile
+};
+
+// The weights of 128 rows from row n0, blocks [kb0, kb0 + nk), into TMEM: each
+// thread a row (its lane) of its group's blocks, those whose place in the ring
+// is the group's modulo 4.
+// A parity wait tells only adjacent phases apart: when a group waits for the
+// consumption of fill f - STAGES, its previous fill f - 4 needed that of
+// f - 4 - STAGES, which covers f - 2 STAGES only when STAGES >= 4.
+template <int TA, int STAGES, int CSTAGES>
+__device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing &r, int n0, int kb0, int nk,
+                                               volatile int *abort_flag) {
+  const int warp = (int)threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = (warp & 3) * 32 + lane;  // the TMEM lanes this warp may write
+  const int j = (int)(((uint32_t)((warp - kDequantWarp) / kGroupWarps) - r.fill) % kGroups);
+  const uint32_t dst0 = r.weights + ((uint32_t)((warp & 3) * 32) << 16);
+  const ScaleRow srow = scale_row(p, n0 + row);
+  RawScale next[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) next[h] = load_raw_scale(p, srow, (kb0 + j) * 64 + 32 * h);
+  for (int i = j; i < nk + j; i += kGroups) {  // a stage of codes, of which this group takes block j
+    RawScale cur[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      cur[h] = next[h];
+      next[h] = load_raw_scale(p, srow, (kb0 + i + kGroups) * 64 + 32 * h);
+    }
+    if (!warp_wait(r.cfull0 + 8 * r.cs, r.cphase, abort_flag, p.err, kErrDequant)) return false;
+    const uint8_t *crow = r.codes + r.cs * kCodeStageB + row * 128;
+    uint4 c[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) c[h] = *reinterpret_cast<const uint4 *>(crow + (((2 * j + h) ^ (row & 7)) << 4));
+    const uint32_t cempty = r.cempty0 + 8 * r.cs;
+    if (++r.cs == CSTAGES) {
+      r.cs = 0;
+      r.cphase ^= 1;
+    }
+    if (i >= nk) {  // the last stage of codes ends before this group's block
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cempty);
+      break;
+    }
+    const uint32_t f = r.fill + (uint32_t)i;
+    const int stage = (int)(f % STAGES);
+    if (!warp_wait(r.empty0 + 8 * stage, ((f / STAGES) & 1u) ^ 1u, abort_flag, p.err, kErrDequant)) return false;
+    fence_after();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const GroupScale<TA> g = group_scale<TA>(p, cur[h]);
+      uint32_t v[16];
+      if (p.split_scale) {
+        dequant8<TA>(c[h].x, g, true, v);
+        dequant8<TA>(c[h].y, g, true, v + 4);
+        dequant8<TA>(c[h].z, g, true, v + 8);
+        dequant8<TA>(c[h].w, g, true, v + 12);
+      } else {
+        dequant8<TA>(c[h].x, g, false, v);
+        dequant8<TA>(c[h].y, g, false, v + 4);
+        dequant8<TA>(c[h].z, g, false, v + 8);
+        dequant8<TA>(c[h].w, g, false, v + 12);
+      }
+      tmem_st_16cols(dst0 + (uint32_t)(stage * 32 + h * 16), v);
+    }
+    tmem_st_wait();
+    fence_before();
+    __syncwarp();
+    // The codes are given back only here, after their use: given back right
+    // behind the loads, the next copy overwrote some before they were read
+    // (wrong rows at K >= 2048).
+    if (lane == 0) {
+      mbar_arrive(r.wfull0 + 8 * stage);
+      mbar_arrive(cempty);
+    }
+  }
+  r.fill += (uint32_t)nk;
+  return true;
+}
+
+template <int TA, int BN>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    w4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+                   const TileParams p) {
+  using S = Tile<BN>;
+  constexpr int STAGES = S::kStages, CSTAGES = S::kCodeStages;
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *codes = smem + STAGES * S::kStageB;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(codes + CSTAGES * kCodeStageB);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, wfull0 = empty0 + 8 * STAGES;
+  const uint32_t cfull0 = wfull0 + 8 * STAGES, cempty0 = cfull0 + 8 * CSTAGES;
+  const uint32_t tfull = cempty0 + 8 * CSTAGES, tempty = tfull + 8, drain = tempty + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 3 * STAGES + 2 * CSTAGES + 3);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ranks = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster along x splits K
+  const int kb0 = rank * p.kb_per_rank, nk = max(0, min(p.kb_per_rank, p.num_kb - kb0));
+  const int first = (int)blockIdx.y, step = (int)gridDim.y;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+      mbar_init(wfull0 + 8 * s, kGroupWarps);
+    }
+    for (int s = 0; s < CSTAGES; ++s) {
+      mbar_init(cfull0 + 8 * s, 1);
+      mbar_init(cempty0 + 8 * s, kDequantWarps);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, kStoreWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 2 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmW);
+    for (int i = 0; i < min((nk + 3) / 4, 16); ++i)  // the first tile's codes into L2
+      tma_prefetch_2d(&tmW, kb0 * 32 + i * 128, (first % p.tiles_n) * 128);
+  }
+  if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), S::kCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  if (warp == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = first; u < p.tiles && ok; u += step)
+      for (int i = 0; i < nk; ++i) {
+        if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.err, kErrCopy)) {
+          ok = false;
+          break;
+        }
+        mbar_expect_tx(full0 + 8 * stage, S::kStageB);
+        tma_load_2d(smem_u32(smem + stage * S::kStageB), &tmA, full0 + 8 * stage, (kb0 + i) * 64,
+                    u / p.tiles_n * BN);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    for (int s = 0; s < STAGES; ++s) {
+      const int st = (stage + s) % STAGES;
+      wait_drain(full0 + 8 * st, st < stage ? phase : phase ^ 1, p.err, kErrCopy);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = instr_desc(TA == MM_BF16 ? 1 : 0, 128, BN);
+    int stage = 0;
+    uint32_t phase = 0, tphase = 0;
+    bool ok = true;
+    for (int u = first; u < p.tiles && ok; u += step) {
+      if (!warp_wait(tempty, tphase ^ 1, abort_flag, p.err, kErrMma)) break;
+      for (int i = 0; i < nk; ++i) {
+        if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.err, kErrMma) ||
+            !warp_wait(wfull0 + 8 * stage, phase, abort_flag, p.err, kErrMma)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint64_t bd = desc_at(smem_u32(smem + stage * S::kStageB));
+        const uint32_t w = tmem + BN + (uint32_t)(stage * 32);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts(tmem, w + 8 * kk, bd + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+        mma_commit<1>(empty0 + 8 * stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      mma_commit<1>(tfull);
+      tphase ^= 1;
+    }
+    mma_commit<1>(drain);
+    wait_drain(drain, 0, p.err, kErrDrain);
+    __syncwarp();
+  } else if (warp == 2) {
+    int cs = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = first; u < p.tiles && ok; u += step)
+      for (int i = 0; i < nk; i += 4) {
+        if (!warp_wait(cempty0 + 8 * cs, phase ^ 1, abort_flag, p.err, kErrCodes)) {
+          ok = false;
+          break;
+        }
+        mbar_expect_tx(cfull0 + 8 * cs, kCodeStageB);
+        tma_load_2d(smem_u32(codes + cs * kCodeStageB), &tmW, cfull0 + 8 * cs, (kb0 + i) * 32,
+                    u % p.tiles_n * 128);
+        if (++cs == CSTAGES) {
+          cs = 0;
+          phase ^= 1;
+        }
+      }
+    for (int s = 0; s < CSTAGES; ++s) {
+      const int st = (cs + s) % CSTAGES;
+      wait_drain(cfull0 + 8 * st, st < cs ? phase : phase ^ 1, p.err, kErrCodes);
+    }
+    __syncwarp();
+  } else if (warp >= kDequantWarp) {
+    DequantRing r{codes, cfull0, cempty0, empty0, wfull0, tmem + BN};
+    for (int u = first; u < p.tiles; u += step)
+      if (!dequant_blocks<TA, STAGES, CSTAGES>(p, r, u % p.tiles_n * 128, kb0, nk, abort_flag)) break;
+  }
+  const int q = warp & 3, half = (warp - kStoreWarp) >> 2;
+  const bool stores = warp >= kStoreWarp && warp < kStoreWarp + kStoreWarps;
+  const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
+  if (ranks == 1) {
+    if (stores) {
+      uint32_t tphase = 0;
+      for (int u = first; u < p.tiles; u += step) {
+        if (!warp_wait(tfull, tphase, abort_flag, p.err, kErrStore)) break;
+        tphase ^= 1;
+        fence_after();
+        const int m0 = u / p.tiles_n * BN, n = u % p.tiles_n * 128 + q * 32 + lane;
+#pragma unroll 1
+        for (int c = half * 32; c < BN && m0 + c < p.M; c += 64) {
+          uint32_t r[32];
+          tmem_ld_32cols(tbase + (uint32_t)c, r);
+          tmem_ld_wait();
+          if (n < p.N) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (m0 + c + i < p.M)
+                store_value(p.out, p.tc, (int64_t)(m0 + c + i) * p.ldc + n, __uint_as_float(r[i]));
+          }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty);
+      }
+    }
+  } else {  // one tile a cluster
+    const int u = first, m0 = u / p.tiles_n * BN, n = u % p.tiles_n * 128 + q * 32 + lane;
+    const int cols = min(BN, p.M - m0);
+    float *tile = reinterpret_cast<float *>(smem);  // [BN][128], over the rings
+    if (stores) {
+      warp_wait(tfull, 0, abort_flag, p.err, kErrStore);
+      fence_after();
+#pragma unroll 1
+      for (int c = half * 32; c < cols; c += 64) {
+        uint32_t r[32];
+        tmem_ld_32cols(tbase + (uint32_t)c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) tile[(c + i) * 128 + q * 32 + lane] = nk > 0 ? __uint_as_float(r[i]) : 0.f;
+      }
+    }
+    cluster_sync_all();
+    // rank r adds the rows r, r + ranks, ... of the tile, over the ranks in order
+    if (stores && n < p.N) {
+      const uint32_t mine = smem_u32(tile + q * 32 + lane);
+      for (int m = rank + half * ranks; m < cols; m += 2 * ranks) {
+        float part[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < ranks) part[k] = ld_cluster_f32(map_to_rank(mine + (uint32_t)m * 512u, (uint32_t)k));
+        float v = part[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+          if (k < ranks) v += part[k];
+        store_value(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n, v);
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its tile
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) tmem_dealloc<1>(tmem, S::kCols);
+}
+
+template <int TA, int BN>
+mm_status run_tiles(const W4Args &a, const TmaRows &ra, const TmaRows &rw, TileParams p, LaunchCtx &ctx) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  auto kern = w4_tile_kernel<TA, BN>;
+  std::call_once(once, [&] {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile<BN>::kSmem);
+  });
+  if (err != cudaSuccess) return cuda_error(err, "gemm_w4 set-up");
+  CUtensorMap mw, ma;
+  mm_status st = encode_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, rw.p, (uint64_t)rw.bytes, (uint64_t)rw.rows,
+                               (uint64_t)rw.ld, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != MM_OK) return st;
+  st = encode_map_2d(&ma, TA == MM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ra.p,
+                     (uint64_t)a.K, (uint64_t)ra.rows, (uint64_t)ra.ld, 64, BN, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != MM_OK) return st;
+  p.tiles_n = (a.N + 127) / 128;
+  const int64_t tiles = (int64_t)p.tiles_n * ((a.M + BN - 1) / BN);
+  if (tiles >= (1LL << 31)) return set_error(MM_ERR_UNSUPPORTED, "too many tiles");
+  p.tiles = (int)tiles;
+  int ranks = 1;
+  while (ranks < 8 && tiles * ranks * 2 <= ctx.dev->info.sms && p.num_kb >= 8 * ranks) ranks *= 2;
+  p.kb_per_rank = (p.num_kb + ranks - 1) / ranks;
+  if (ranks > 1) p.kb_per_rank = (p.kb_per_rank + 3) / 4 * 4;  // whole stages of codes
+  const int grid = ranks > 1 ? p.tiles : std::min(p.tiles, ctx.dev->info.sms);
+  cudaError_t e = launch_pdl(kern, dim3((unsigned)ranks, (unsigned)grid), dim3(kTileThreads), Tile<BN>::kSmem,
+                             ctx.stream, dim3((unsigned)ranks), mw, ma, p);
+  return e == cudaSuccess ? MM_OK : cuda_error(e, "gemm_w4 launch (tiles)");
+}
+
+template <int TA>
+mm_status launch_tiles(const W4Args &a, const TmaRows &ra, const TmaRows &rw, const TileParams &p, LaunchCtx &ctx) {
+  return a.M <= 32    ? run_tiles<TA, 32>(a, ra, rw, p, ctx)
+         : a.M <= 64  ? run_tiles<TA, 64>(a, ra, rw, p, ctx)
+         : a.M <= 128 ? run_tiles<TA, 128>(a, ra, rw, p, ctx)
+                      : run_tiles<TA, 256>(a, ra, rw, p, ctx);
+}
+
+// ---------------------------------------------------------------- few rows
 constexpr int kThreads = 256;
 constexpr int kRows = 8;
 
@@ -44,7 +517,30 @@ __global__ void __launch_bounds__(kThreads) w4_simple_kernel(const W4Args a) {
 }  // namespace
 
 mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
-  if (a.M > 16 && a.K > 0) return launch_gemm_w4_tiles(a, ctx);
+  mm_status st;
+  if (a.M > 16 && a.K > 0) {
+    TmaRows ra{a.A, a.lda * 2, a.M, (int64_t)a.K * 2}, rw{a.codes, a.ldw / 2, a.N, ((int64_t)a.K + 1) / 2};
+    if ((st = align_rows(ra, rw, ctx)) != MM_OK) return st;
+    TileParams p;
+    std::memset(&p, 0, sizeof p);
+    p.out = a.out;
+    p.ldc = a.ldc;
+    p.tc = a.tc;
+    p.M = a.M;
+    p.N = a.N;
+    p.num_kb = (int)(((int64_t)a.K + 63) / 64);
+    p.err = ctx.dev->d_err + kOperatorErrorWord;
+    p.scales = a.scales;
+    p.zeros = a.zeros;
+    p.lds = a.lds;
+    p.ts = a.ts;
+    p.group_shift = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
+    p.groups = (a.K + a.group - 1) / a.group;
+    p.split_scale = a.ts != a.ta;
+    st = a.ta == MM_BF16 ? launch_tiles<MM_BF16>(a, ra, rw, p, ctx) : launch_tiles<MM_F16>(a, ra, rw, p, ctx);
+    if (st == MM_OK) count_operator_launch();
+    return st;
+  }
   const int64_t gx = ((int64_t)a.N + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t gy = std::min<int64_t>(((int64_t)a.M + kRows - 1) / kRows, 1024);
   cudaError_t e = launch_pdl(w4_simple_kernel, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), 0,

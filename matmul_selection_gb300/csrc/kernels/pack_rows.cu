@@ -30,15 +30,41 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const uint8_t *src, int6
   }
 }
 
-}  // namespace
-
-mm_status launch_pack_rows(const void *src, int64_t ld, int64_t rows, int64_t bytes, void *dst, int64_t ld16,
-                           LaunchCtx &ctx) {
-  const int64_t blocks = std::min<int64_t>((ld16 / 16 * rows + 255) / 256, 16 * ctx.dev->info.sms);
+mm_status pack(TmaRows &r, uint8_t *dst, int64_t ld16, LaunchCtx &ctx) {
+  const int64_t blocks = std::min<int64_t>((ld16 / 16 * r.rows + 255) / 256, 16 * ctx.dev->info.sms);
   cudaError_t e = launch_pdl(pack_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, ctx.stream, dim3(1),
-                             static_cast<const uint8_t *>(src), ld, rows, bytes, static_cast<uint8_t *>(dst), ld16);
+                             static_cast<const uint8_t *>(r.p), r.ld, r.rows, r.bytes, dst, ld16);
   if (e != cudaSuccess) return cuda_error(e, "row copy launch");
   count_operator_launch();
+  r.p = dst;
+  r.ld = ld16;
+  return MM_OK;
+}
+
+bool addressable(const TmaRows &r) {
+  return (uintptr_t)r.p % 16 == 0 && (r.rows == 1 || (r.ld % 16 == 0 && r.ld < (1LL << 40)));
+}
+
+}  // namespace
+
+mm_status align_rows(TmaRows &a, TmaRows &b, LaunchCtx &ctx) {
+  TmaRows *op[2] = {&a, &b};
+  int64_t ld16[2];
+  size_t need = 0, at[2];
+  for (int i = 0; i < 2; ++i) {
+    ld16[i] = (op[i]->bytes + 15) / 16 * 16;
+    at[i] = need;
+    if (!addressable(*op[i])) need += (size_t)ld16[i] * op[i]->rows;
+    else if (op[i]->rows == 1) op[i]->ld = ld16[i];  // a distance that is never used, as maps want it
+  }
+  if (!need) return MM_OK;
+  void *w = nullptr;
+  mm_status st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_REPACK, need, &w);
+  if (st != MM_OK) return st;
+  for (int i = 0; i < 2; ++i)
+    if (!addressable(*op[i]) &&
+        (st = pack(*op[i], static_cast<uint8_t *>(w) + at[i], ld16[i], ctx)) != MM_OK)
+      return st;
   return MM_OK;
 }
 

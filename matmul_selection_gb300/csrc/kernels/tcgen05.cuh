@@ -56,18 +56,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Acquire at cluster scope, for arrivals that the other CTA of a pair releases.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ uint64_t global_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -77,15 +65,13 @@ __device__ __forceinline__ uint64_t global_ns() {
 // Wait for the phase of `parity`, by a whole warp.  Gives up (false, in every
 // lane) when the CTA's abort flag is up, or after the limit: then it raises
 // the flag and records `code` in the error word.
-template <bool CLUSTER>
-__device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+static __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                             int *err, int code) {
   const uint64_t t0 = global_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
-      if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
-        return true;
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     int stop = 0;
     if ((threadIdx.x & 31) == 0) {
       if (*abort_flag) {
@@ -99,27 +85,19 @@ __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volat
     if (__shfl_sync(0xffffffffu, stop, 0)) return false;
   }
 }
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                           int *err, int code) {
-  if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
-    return true;
-  return warp_wait_slow<CLUSTER>(bar, parity, abort_flag, err, code);
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_slow(bar, parity, abort_flag, err, code);
 }
 // A bounded wait that ignores the abort flag, for copies and MMAs in flight.
-__device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, int *err, int code) {
+static __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, int *err, int code) {
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
     if (global_ns() - t0 > kDrainLimitNs) {
       atomicCAS(err, 0, code);
       return;
     }
-}
-
-// Generic-proxy writes of this thread to shared memory, made visible to the
-// async proxy (the MMA's operand reads).
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- clusters
@@ -216,24 +194,32 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                  : "memory");
 }
-// D += A B^T of operands in shared memory, 32 bytes of K: F8 e4m3
-// (kind::f8f6f4), else bf16 or f16 (kind::f16, both operands the same type).
-// CG: CTAs of the group.  Warp-collective.
+// D += A B^T of e4m3 operands in shared memory (kind::f8f6f4), 32 of K.  CG:
+// CTAs of the group.  Warp-collective.
 #define MM_MMA_ASM(CGS, KIND)                                                                     \
   asm volatile(                                                                                   \
       "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"          \
       "@e tcgen05.mma.cta_group::" CGS ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), \
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)                                         \
       : "memory")
-template <int CG, bool F8>
-__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                    uint32_t accumulate) {
-  if constexpr (CG == 1 && F8) MM_MMA_ASM("1", "f8f6f4");
-  if constexpr (CG == 2 && F8) MM_MMA_ASM("2", "f8f6f4");
-  if constexpr (CG == 1 && !F8) MM_MMA_ASM("1", "f16");
-  if constexpr (CG == 2 && !F8) MM_MMA_ASM("2", "f16");
+template <int CG>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (CG == 1)
+    MM_MMA_ASM("1", "f8f6f4");
+  else
+    MM_MMA_ASM("2", "f8f6f4");
 }
 #undef MM_MMA_ASM
+// The same with A in TMEM (16-bit types, two of K a column), one CTA.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Instruction descriptor: D fp32, A and B of one type (kind::f8f6f4: 0 e4m3;
 // kind::f16: 0 f16, 1 bf16), both K-major, m x n.
 __host__ __device__ constexpr uint32_t instr_desc(uint32_t type, uint32_t m, uint32_t n) {
@@ -279,6 +265,19 @@ __device__ __forceinline__ void tmem_ld_32cols(uint32_t taddr, uint32_t (&r)[32]
 }
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// 16 consecutive columns of 32 lanes: thread i writes lane i's.
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- host side

@@ -42,7 +42,6 @@ struct W4Args {
   int ta, ts, tc;
 };
 mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx);
-mm_status launch_gemm_w4_tiles(const W4Args &a, LaunchCtx &ctx);  // on tcgen05
 
 struct Q8Args {
   const uint8_t *A, *B;
@@ -54,10 +53,14 @@ struct Q8Args {
 };
 mm_status launch_gemm_q8(const Q8Args &a, LaunchCtx &ctx);
 
-// Rows of `bytes` bytes, ld apart, copied to rows ld16 (a multiple of 16)
-// apart, zeros after the last byte.
-mm_status launch_pack_rows(const void *src, int64_t ld, int64_t rows, int64_t bytes, void *dst,
-                           int64_t ld16, LaunchCtx &ctx);
+// Rows that TMA is to read: `rows` rows of `bytes` bytes, ld bytes apart.
+struct TmaRows {
+  const void *p;
+  int64_t ld, rows, bytes;
+};
+// Operands whose base or distance between rows is not a multiple of 16 bytes
+// are copied into the stream's scratch and pointed there.
+mm_status align_rows(TmaRows &a, TmaRows &b, LaunchCtx &ctx);
 
 // The operators' error word among the 16 of DeviceState::d_err (the first is
 // the GEMM candidates').  A kernel whose bounded wait gives up leaves a code
