@@ -49,7 +49,7 @@ struct Tile {
   static constexpr size_t kSmem = kStages * kStageB + kCodeStages * kCodeStageB + 1024 + 512;
   // TMEM: the accumulator, then the stages' weights, 32 columns each
   static constexpr uint32_t kUsed = BN + 32 * kStages, kCols = kUsed <= 256 ? 256 : 512;
-  static_assert(kUsed <= 512 && kStages >= kGroups, "TMEM; see dequant_blocks");
+  static_assert(kUsed <= 512 && kStages >= kGroups && kStages < 2 * kGroups, "TMEM; see dequant_blocks");
   static_assert((size_t)BN * 512 <= kStages * kStageB + kCodeStages * kCodeStageB, "the fp32 tile fits the rings");
 };
 
@@ -126,12 +126,16 @@ struct GroupScale {
 template <int TA>
 __device__ __forceinline__ GroupScale<TA> group_scale(const TileParams &p, const RawScale &r) {
   using T = typename Pair16<TA>::T;
-  const float s = p.ts == MM_F32    ? __uint_as_float(r.s)
-                  : p.ts == MM_BF16 ? __uint_as_float(r.s << 16)
-                                    : __half2float(__ushort_as_half((unsigned short)r.s));
   GroupScale<TA> g;
-  g.hi = Pair16<TA>::both(s);
-  g.lo = Pair16<TA>::both(p.split_scale ? s - __low2float(g.hi) : 0.f);
+  if (!p.split_scale) {
+    g.hi = g.lo = bits_as<T>(r.s * 0x00010001u);
+  } else {
+    const float s = p.ts == MM_F32    ? __uint_as_float(r.s)
+                    : p.ts == MM_BF16 ? __uint_as_float(r.s << 16)
+                                      : __half2float(__ushort_as_half((unsigned short)r.s));
+    g.hi = Pair16<TA>::both(s);
+    g.lo = Pair16<TA>::both(s - __low2float(g.hi));
+  }
   // the bias that the codes are read with, and the zero point
   g.zero = bits_as<T>((TA == MM_BF16 ? 0x43004300u : 0x64006400u) + (r.z & 15u) * 0x00010001u);
   return g;
@@ -139,21 +143,20 @@ __device__ __forceinline__ GroupScale<TA> group_scale(const TileParams &p, const
 
 // Eight codes of a word into eight weights in k order.  A code in the low
 // mantissa bits of 128 (bf16) or 1024 (f16) is the number 128 + q or 1024 + q;
-// the difference with 128 + z or 1024 + z is exact.
+// the difference with 128 + z or 1024 + z is exact.  A byte of the word holds
+// two neighbours: one permute of the word and the word shifted by a nibble
+// puts both into the low nibbles of two halves.
 template <int TA>
 __device__ __forceinline__ void dequant8(uint32_t w, const GroupScale<TA> &g, bool split, uint32_t *out) {
   using T = typename Pair16<TA>::T;
   constexpr uint32_t kBias = TA == MM_BF16 ? 0x43004300u : 0x64006400u;
-  uint32_t v[4];  // (0, 4), (1, 5), (2, 6), (3, 7)
+  const uint32_t w4 = w >> 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const T d = __hsub2(bits_as<T>(((w >> (4 * i)) & 0x000f000fu) | kBias), g.zero);
-    v[i] = as_bits(split ? __hfma2(d, g.hi, __hmul2(d, g.lo)) : __hmul2(d, g.hi));
+    const uint32_t pair = __byte_perm(w, w4, 0x0400 + 0x0101 * i);  // bytes i of w, of w4 (from 16 bits up)
+    const T d = __hsub2(bits_as<T>((pair & 0x000f000fu) | kBias), g.zero);
+    out[i] = as_bits(split ? __hfma2(d, g.hi, __hmul2(d, g.lo)) : __hmul2(d, g.hi));
   }
-  out[0] = __byte_perm(v[0], v[1], 0x5410);
-  out[1] = __byte_perm(v[2], v[3], 0x5410);
-  out[2] = __byte_perm(v[0], v[1], 0x7632);
-  out[3] = __byte_perm(v[2], v[3], 0x7632);
 }
 
 // The weight-making warps' side of the rings.
@@ -164,7 +167,10 @@ struct DequantRing {
   uint32_t weights;          // TMEM address of stage 0's weights
   int cs = 0;
   uint32_t cphase = 0;
-  uint32_t fill = 0;  // stages filled before this tile
+  int group;        // of this warp
+  int turn = 0;     // stages filled before this tile, modulo the groups
+  int stage;        // of the group's next fill
+  uint32_t phase = 0;
 };
 
 // The weights of 128 rows from row n0, blocks [kb0, kb0 + nk), into TMEM: each
@@ -178,24 +184,23 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
                                                volatile int *abort_flag) {
   const int warp = (int)threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = (warp & 3) * 32 + lane;  // the TMEM lanes this warp may write
-  const int j = (int)(((uint32_t)((warp - kDequantWarp) / kGroupWarps) - r.fill) % kGroups);
+  const int j = (r.group - r.turn) & (kGroups - 1);
   const uint32_t dst0 = r.weights + ((uint32_t)((warp & 3) * 32) << 16);
   const ScaleRow srow = scale_row(p, n0 + row);
+  const bool two = p.group_shift == 5;  // a block of 64 spans two groups
+  const uint8_t *crow = r.codes + row * 128;
+  const uint32_t at[2] = {(uint32_t)((2 * j) ^ (row & 7)) << 4, (uint32_t)((2 * j + 1) ^ (row & 7)) << 4};
   RawScale next[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) next[h] = load_raw_scale(p, srow, (kb0 + j) * 64 + 32 * h);
+  next[0] = load_raw_scale(p, srow, (kb0 + j) * 64);
+  next[1] = two ? load_raw_scale(p, srow, (kb0 + j) * 64 + 32) : next[0];
   for (int i = j; i < nk + j; i += kGroups) {  // a stage of codes, of which this group takes block j
-    RawScale cur[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      cur[h] = next[h];
-      next[h] = load_raw_scale(p, srow, (kb0 + i + kGroups) * 64 + 32 * h);
-    }
+    const RawScale cur[2] = {next[0], next[1]};
+    next[0] = load_raw_scale(p, srow, (kb0 + i + kGroups) * 64);
+    next[1] = two ? load_raw_scale(p, srow, (kb0 + i + kGroups) * 64 + 32) : next[0];
     if (!warp_wait(r.cfull0 + 8 * r.cs, r.cphase, abort_flag, p.err, kErrDequant)) return false;
-    const uint8_t *crow = r.codes + r.cs * kCodeStageB + row * 128;
     uint4 c[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) c[h] = *reinterpret_cast<const uint4 *>(crow + (((2 * j + h) ^ (row & 7)) << 4));
+    for (int h = 0; h < 2; ++h) c[h] = *reinterpret_cast<const uint4 *>(crow + r.cs * kCodeStageB + at[h]);
     const uint32_t cempty = r.cempty0 + 8 * r.cs;
     if (++r.cs == CSTAGES) {
       r.cs = 0;
@@ -206,13 +211,17 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
       if (lane == 0) mbar_arrive(cempty);
       break;
     }
-    const uint32_t f = r.fill + (uint32_t)i;
-    const int stage = (int)(f % STAGES);
-    if (!warp_wait(r.empty0 + 8 * stage, ((f / STAGES) & 1u) ^ 1u, abort_flag, p.err, kErrDequant)) return false;
+    const int stage = r.stage;
+    if (!warp_wait(r.empty0 + 8 * stage, r.phase ^ 1, abort_flag, p.err, kErrDequant)) return false;
+    if ((r.stage += kGroups) >= STAGES) {
+      r.stage -= STAGES;
+      r.phase ^= 1;
+    }
     fence_after();
+    GroupScale<TA> g = group_scale<TA>(p, cur[0]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const GroupScale<TA> g = group_scale<TA>(p, cur[h]);
+      if (h && two) g = group_scale<TA>(p, cur[1]);
       uint32_t v[16];
       if (p.split_scale) {
         dequant8<TA>(c[h].x, g, true, v);
@@ -238,7 +247,7 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
       mbar_arrive(cempty);
     }
   }
-  r.fill += (uint32_t)nk;
+  r.turn = (r.turn + nk) & (kGroups - 1);
   return true;
 }
 
@@ -373,6 +382,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncwarp();
   } else if (warp >= kDequantWarp) {
     DequantRing r{codes, cfull0, cempty0, empty0, wfull0, tmem + BN};
+    r.group = r.stage = (warp - kDequantWarp) / kGroupWarps;
     for (int u = first; u < p.tiles; u += step)
       if (!dequant_blocks<TA, STAGES, CSTAGES>(p, r, u % p.tiles_n * 128, kb0, nk, abort_flag)) break;
   }

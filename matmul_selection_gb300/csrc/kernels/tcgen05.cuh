@@ -56,6 +56,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// The same, suspended for up to `ns` before it answers no: a waiting warp then
+// takes few issue slots from the working ones.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ uint64_t global_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -70,8 +83,8 @@ static __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity
   const uint64_t t0 = global_ns();
   while (true) {
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    for (int i = 0; i < 4; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, 20000u))) return true;
     int stop = 0;
     if ((threadIdx.x & 31) == 0) {
       if (*abort_flag) {
