@@ -390,21 +390,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     cluster_sync_all();
-    // rank r adds the rows r, r + ranks, ... of the tile, over the ranks in order
-    if (warp >= 2 && n < p.N) {
-      const uint32_t mine = smem_u32(tile + q * 32 + lane);
-      for (int m = rank; m < cols; m += ranks) {
-        float part[8];
+    add_cluster_tiles(smem_u32(tile), cols, rank, ranks, warp, kThreads / 32, [&](int m, int c, float4 v) {
+      const float sa = p.sa ? __ldg(p.sa + m0 + m) : 1.f;
+      const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < ranks) part[k] = ld_cluster_f32(map_to_rank(mine + (uint32_t)m * 512u, (uint32_t)k));
-        float v = part[0];
-#pragma unroll
-        for (int k = 1; k < 8; ++k)
-          if (k < ranks) v += part[k];
-        store_value(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n, v * (p.sa ? __ldg(p.sa + m0 + m) : 1.f) * sb);
+      for (int i = 0; i < 4; ++i) {
+        const int col = n0 + c + i;
+        if (col < p.N)
+          store_value(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + col, x[i] * sa * (p.sb ? __ldg(p.sb + col) : 1.f));
       }
-    }
+    });
     cluster_sync_all();  // no CTA leaves while another reads its tile
   }
   fence_before();

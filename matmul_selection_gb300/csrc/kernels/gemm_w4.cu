@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
   } else {  // one tile a cluster
-    const int u = first, m0 = u / p.tiles_n * BN, n = u % p.tiles_n * 128 + q * 32 + lane;
+    const int u = first, m0 = u / p.tiles_n * BN;
     const int cols = min(BN, p.M - m0);
     float *tile = reinterpret_cast<float *>(smem);  // [BN][128], over the rings
     if (stores) {
@@ -431,21 +431,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
     cluster_sync_all();
-    // rank r adds the rows r, r + ranks, ... of the tile, over the ranks in order
-    if (stores && n < p.N) {
-      const uint32_t mine = smem_u32(tile + q * 32 + lane);
-      for (int m = rank + half * ranks; m < cols; m += 2 * ranks) {
-        float part[8];
+    const int n0 = u % p.tiles_n * 128;
+    add_cluster_tiles(smem_u32(tile), cols, rank, ranks, warp, kTileThreads / 32, [&](int m, int c, float4 v) {
+      const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < ranks) part[k] = ld_cluster_f32(map_to_rank(mine + (uint32_t)m * 512u, (uint32_t)k));
-        float v = part[0];
-#pragma unroll
-        for (int k = 1; k < 8; ++k)
-          if (k < ranks) v += part[k];
-        store_value(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n, v);
-      }
-    }
+      for (int i = 0; i < 4; ++i)
+        if (n0 + c + i < p.N) store_value(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n0 + c + i, x[i]);
+    });
     cluster_sync_all();  // no CTA leaves while another reads its tile
   }
   fence_before();
