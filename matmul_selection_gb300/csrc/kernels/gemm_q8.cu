@@ -12,8 +12,8 @@
 //   swap   few rows: out^T = B A^T, 128 rows of B (the weights) on the MMA's
 //          128-lane side and BN rows of A on the other, so that a short A is
 //          not padded to 128 rows.  K is split over the CTAs of a cluster;
-//          their fp32 tiles are added through distributed shared memory in
-//          rank order, which is one launch, no workspace and the same bits
+//          their fp32 tiles meet in distributed shared memory and are added
+//          in rank order, which is one launch, no workspace and the same bits
 //          every time.
 // Every mbarrier wait is bounded (see tcgen05.cuh); a wait that gives up
 // records a code in the operators' error word.
@@ -267,18 +267,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- swap
+// Warps 0 and 3 copy B and A, warp 1 issues MMAs, warps 4-11 take the tile out
+// of TMEM (two for each quarter of the lanes); all of them store it.
+constexpr int kSwapThreads = 384, kSwapStore = 4;
+
 template <int BN>
 struct Swap {
   static constexpr uint32_t kStageB = (128 + BN) * kRowB;
-  static constexpr int kStages = BN == 32 ? 10 : BN == 64 ? 8 : BN == 128 ? 6 : 4;
-  static constexpr size_t kTileB = (size_t)BN * 128 * 4;  // the fp32 tile, over the ring
-  static constexpr size_t kSmem = kStages * kStageB + 1024 + 256;
+  static constexpr int kStages = BN == 32 ? 9 : BN == 64 ? 7 : 5;
+  static constexpr uint32_t kTileB = BN * 128 * 4;  // the fp32 tile, beside the ring: others write it early
+  static constexpr size_t kSmem = kStages * kStageB + kTileB + 1024 + 256;
   static constexpr uint32_t kCols = BN;  // TMEM columns, a power of two of at least 32
-  static_assert(kTileB <= kStages * kStageB, "the fp32 tile fits the ring");
 };
 
 template <int BN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kSwapThreads, 1)
     q8_swap_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA,
                    const Q8Params p) {
   using S = Swap<BN>;
@@ -286,7 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kStages * S::kStageB);
+  float *tile = reinterpret_cast<float *>(smem + S::kStages * S::kStageB);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kStages * S::kStageB + S::kTileB);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages;
   const uint32_t done = empty0 + 8 * S::kStages;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S::kStages + 1);
@@ -298,34 +302,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, 2);  // both copying warps arm their bytes
       mbar_init(empty0 + 8 * s, 1);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
+  if (warp == 3 && lane == 0) prefetch_tmap(&tmA);
   if (warp == 0 && lane == 0) {
-    prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
     for (int i = 0; i < min(nk, 16); ++i) tma_prefetch_2d(&tmB, (kb0 + i) * (int)kRowB, n0);
   }
   if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), S::kCols);
   fence_before();
-  __syncthreads();
+  if (ranks > 1) cluster_sync_all();  // the others run: their memory may be written
+  else __syncthreads();
   fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
+    const CUtensorMap *map = warp == 0 ? &tmB : &tmA;
+    const uint32_t offset = warp == 0 ? 0u : 128 * kRowB, bytes = (warp == 0 ? 128 : BN) * kRowB;
+    const int y = warp == 0 ? n0 : m0;
     int i = 0;
     for (; i < nk; ++i) {
       const int st = i % S::kStages;
       if (!warp_wait(empty0 + 8 * st, ((uint32_t)(i / S::kStages) & 1u) ^ 1u, abort_flag, p.err, kErrCopy)) break;
-      const uint32_t sb = smem_u32(smem + st * S::kStageB);
-      mbar_expect_tx(full0 + 8 * st, S::kStageB);
-      tma_load_2d(sb, &tmB, full0 + 8 * st, (kb0 + i) * (int)kRowB, n0);
-      tma_load_2d(sb + 128 * kRowB, &tmA, full0 + 8 * st, (kb0 + i) * (int)kRowB, m0);
+      mbar_expect_tx(full0 + 8 * st, bytes);
+      tma_load_2d(smem_u32(smem + st * S::kStageB + offset), map, full0 + 8 * st, (kb0 + i) * (int)kRowB, y);
     }
     for (int f = max(0, i - S::kStages); f < i; ++f)
       wait_drain(full0 + 8 * (f % S::kStages), (uint32_t)(f / S::kStages) & 1u, p.err, kErrCopy);
@@ -340,72 +346,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t bd = desc_at(sb), ad = desc_at(sb + 128 * kRowB);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_f8<1>(tmem_base, bd + 2 * kk, ad + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+        mma_f8<1>(tmem, bd + 2 * kk, ad + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
       mma_commit<1>(empty0 + 8 * st);
     }
     mma_commit<1>(done);
     wait_drain(done, 0, p.err, kErrDrain);
     __syncwarp();
   }
-  // A wait at the end of a short main loop, by every thread that stores: the
-  // MMAs are complete (the ring is idle) and the accumulator can be read.
-  const int q = warp & 3;
-  bool ok = true;
-  if (warp >= 2) {
-    ok = warp_wait(done, 0, abort_flag, p.err, kErrStore);
+  const int rows = min(BN, p.M - m0), per = BN / ranks;
+  if (warp >= kSwapStore) {
+    warp_wait(done, 0, abort_flag, p.err, kErrStore);
     fence_after();
+    const int q = warp & 3;
+    push_tile(tmem + ((uint32_t)(q * 32) << 16), smem_u32(tile), rank, ranks, per, rows,
+              ((warp - kSwapStore) >> 2) * 32, 64, q * 32 + lane, nk == 0);
+    fence_before();
   }
-  const int cols = min(BN, p.M - m0);  // rows of A in the tile
-  const int n = n0 + q * 32 + lane;
-  const float sb = p.sb && n < p.N ? p.sb[n] : 1.f;
-  const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16);
-  if (ranks == 1) {
-    if (warp >= 2 && ok) {
-#pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32cols(tbase + (uint32_t)c, r);
-        tmem_ld_wait();
-        if (n < p.N) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < cols) {
-              const int m = m0 + c + i;
-              store_value(p.out, p.tc, (int64_t)m * p.ldc + n,
-                          __uint_as_float(r[i]) * (p.sa ? __ldg(p.sa + m) : 1.f) * sb);
-            }
-        }
-      }
-    }
-  } else {
-    float *tile = reinterpret_cast<float *>(smem);  // [BN][128]
-    if (warp >= 2) {
-#pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32cols(tbase + (uint32_t)c, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) tile[(c + i) * 128 + q * 32 + lane] = nk > 0 ? __uint_as_float(r[i]) : 0.f;
-      }
-    }
-    cluster_sync_all();
-    add_cluster_tiles(smem_u32(tile), cols, rank, ranks, warp, kThreads / 32, [&](int m, int c, float4 v) {
-      const float sa = p.sa ? __ldg(p.sa + m0 + m) : 1.f;
-      const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = n0 + c + i;
-        if (col < p.N)
-          store_value(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + col, x[i] * sa * (p.sb ? __ldg(p.sb + col) : 1.f));
-      }
-    });
-    cluster_sync_all();  // no CTA leaves while another reads its tile
-  }
-  fence_before();
-  __syncthreads();
+  if (ranks > 1) cluster_sync_all();
+  else __syncthreads();
   fence_after();
-  if (warp == 1) tmem_dealloc<1>(tmem_base, S::kCols);
+  if (warp == 1) tmem_dealloc<1>(tmem, S::kCols);
+  auto store = [&](auto step) {
+    constexpr int STEP = decltype(step)::value;
+    const int n = n0 + (STEP == 1 ? 4 * lane : lane), left = p.N - n;
+    float sb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sb[i] = p.sb && i * STEP < left ? __ldg(p.sb + n + i * STEP) : 1.f;
+    sum_tile<STEP == 1>(tile, rank, ranks, per, rows, warp, kSwapThreads / 32, [&](int m, float4 v) {
+      const float sa = p.sa ? __ldg(p.sa + m0 + m) : 1.f;
+      store_four<STEP>(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n,
+                       make_float4(v.x * sa * sb[0], v.y * sa * sb[1], v.z * sa * sb[2], v.w * sa * sb[3]), left);
+    });
+  };
+  if (p.vec) store(std::integral_constant<int, 1>());
+  else store(std::integral_constant<int, 32>());
 }
 
 // ---------------------------------------------------------------- host side
@@ -479,7 +453,7 @@ mm_status run_swap(const Q8Args &a, Q8Params p, int ranks, LaunchCtx &ctx) {
   const int gy = (a.N + 127) / 128, gz = (a.M + BN - 1) / BN;
   if (gy > 65535 || gz > 65535) return set_error(MM_ERR_UNSUPPORTED, "too many tiles");
   cudaError_t e = launch_pdl(q8_swap_kernel<BN>, dim3((unsigned)ranks, (unsigned)gy, (unsigned)gz),
-                             dim3(kThreads), Swap<BN>::kSmem, ctx.stream, dim3((unsigned)ranks), mb, ma, p);
+                             dim3(kSwapThreads), Swap<BN>::kSmem, ctx.stream, dim3((unsigned)ranks), mb, ma, p);
   return e == cudaSuccess ? MM_OK : cuda_error(e, "gemm_q8 launch (swap)");
 }
 
@@ -516,14 +490,13 @@ mm_status launch_gemm_q8(const Q8Args &in, LaunchCtx &ctx) {
   if (a.M > 256) {
     st = run_pair(a, p, clusters, ctx);
   } else {
-    const int bn = a.M <= 32 ? 32 : a.M <= 64 ? 64 : a.M <= 128 ? 128 : 256;
+    // a tile of as few rows as hold A, and K over as many CTAs as fill the SMs
+    const int bn = a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
     const int64_t tiles = ((int64_t)a.N + 127) / 128 * ((a.M + bn - 1) / bn);
     int ranks = 1;
     while (ranks < 8 && tiles * ranks * 2 <= ctx.dev->info.sms && p.num_kb >= 4 * ranks) ranks *= 2;
-    st = bn == 32    ? run_swap<32>(a, p, ranks, ctx)
-         : bn == 64  ? run_swap<64>(a, p, ranks, ctx)
-         : bn == 128 ? run_swap<128>(a, p, ranks, ctx)
-                     : run_swap<256>(a, p, ranks, ctx);
+    st = bn == 32 ? run_swap<32>(a, p, ranks, ctx) : bn == 64 ? run_swap<64>(a, p, ranks, ctx)
+                                                              : run_swap<128>(a, p, ranks, ctx);
   }
   if (st != MM_OK) return st;
   count_operator_launch();

@@ -10,7 +10,8 @@
 // stage by stage, which took longer than the MMA of the stage.  Codes and
 // rows of A come by TMA through a ring each; a stage holds 64 of K.  CTAs are
 // persistent; where there are few tiles K is split over the CTAs of a cluster,
-// whose fp32 tiles are added through distributed shared memory in rank order.
+// whose fp32 tiles meet in distributed shared memory and are added in rank
+// order.
 //
 // M <= 16: a warp an output column and kRows rows of A; each lane sums its k's
 // in fp32.
@@ -45,12 +46,15 @@ template <int BN>
 struct Tile {
   static constexpr uint32_t kStageB = BN * 128;
   static constexpr int kStages = BN == 256 ? 5 : BN == 128 ? 6 : 7;
-  static constexpr int kCodeStages = BN == 256 ? 3 : 5;
-  static constexpr size_t kSmem = kStages * kStageB + kCodeStages * kCodeStageB + 1024 + 512;
+  static constexpr int kCodeStages = BN == 256 ? 3 : 4;
+  // the fp32 tile where K is split: beside the rings, or, for 256 rows, over them
+  static constexpr bool kOver = BN == 256;
+  static constexpr uint32_t kTileB = kOver ? 0 : BN * 512;
+  static constexpr size_t kSmem = kStages * kStageB + kCodeStages * kCodeStageB + kTileB + 1024 + 512;
   // TMEM: the accumulator, then the stages' weights, 32 columns each
   static constexpr uint32_t kUsed = BN + 32 * kStages, kCols = kUsed <= 256 ? 256 : 512;
   static_assert(kUsed <= 512 && kStages >= kGroups && kStages < 2 * kGroups, "TMEM; see dequant_blocks");
-  static_assert((size_t)BN * 512 <= kStages * kStageB + kCodeStages * kCodeStageB, "the fp32 tile fits the rings");
+  static_assert(!kOver || (size_t)BN * 512 <= kStages * kStageB, "the fp32 tile fits the ring");
 };
 
 struct TileParams {
@@ -67,6 +71,7 @@ struct TileParams {
   int64_t lds;
   int ts, group_shift, groups;
   int split_scale;  // the scales' type is not A's
+  bool vec;         // out's rows are 16-byte aligned
 };
 
 template <int TA>
@@ -262,7 +267,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *codes = smem + STAGES * S::kStageB;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(codes + CSTAGES * kCodeStageB);
+  float *tile = reinterpret_cast<float *>(S::kOver ? smem : codes + CSTAGES * kCodeStageB);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(codes + CSTAGES * kCodeStageB + S::kTileB);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, wfull0 = empty0 + 8 * STAGES;
   const uint32_t cfull0 = wfull0 + 8 * STAGES, cempty0 = cfull0 + 8 * CSTAGES;
   const uint32_t tfull = cempty0 + 8 * CSTAGES, tempty = tfull + 8, drain = tempty + 8;
@@ -297,7 +303,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), S::kCols);
   fence_before();
-  __syncthreads();
+  if (ranks > 1) cluster_sync_all();  // the others run: their memory may be written
+  else __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
@@ -415,30 +422,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
   } else {  // one tile a cluster
-    const int u = first, m0 = u / p.tiles_n * BN;
-    const int cols = min(BN, p.M - m0);
-    float *tile = reinterpret_cast<float *>(smem);  // [BN][128], over the rings
+    const int m0 = first / p.tiles_n * BN, rows = min(BN, p.M - m0), per = BN / ranks;
     if (stores) {
       warp_wait(tfull, 0, abort_flag, p.err, kErrStore);
       fence_after();
-#pragma unroll 1
-      for (int c = half * 32; c < cols; c += 64) {
-        uint32_t r[32];
-        tmem_ld_32cols(tbase + (uint32_t)c, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) tile[(c + i) * 128 + q * 32 + lane] = nk > 0 ? __uint_as_float(r[i]) : 0.f;
-      }
     }
+    if (S::kOver) cluster_sync_all();  // every CTA's rings are idle
+    if (stores)
+      push_tile(tbase, smem_u32(tile), rank, ranks, per, rows, half * 32, 64, q * 32 + lane, nk == 0);
     cluster_sync_all();
-    const int n0 = u % p.tiles_n * 128;
-    add_cluster_tiles(smem_u32(tile), cols, rank, ranks, warp, kTileThreads / 32, [&](int m, int c, float4 v) {
-      const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n0 + c + i < p.N) store_value(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n0 + c + i, x[i]);
-    });
-    cluster_sync_all();  // no CTA leaves while another reads its tile
+    auto store = [&](auto step) {
+      constexpr int STEP = decltype(step)::value;
+      const int n = first % p.tiles_n * 128 + (STEP == 1 ? 4 * lane : lane);
+      sum_tile<STEP == 1>(tile, rank, ranks, per, rows, warp, kTileThreads / 32, [&](int m, float4 v) {
+        store_four<STEP>(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n, v, p.N - n);
+      });
+    };
+    if (p.vec) store(std::integral_constant<int, 1>());
+    else store(std::integral_constant<int, 32>());
   }
   fence_before();
   __syncthreads();
@@ -539,6 +540,7 @@ mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
     p.group_shift = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
     p.groups = (a.K + a.group - 1) / a.group;
     p.split_scale = a.ts != a.ta;
+    p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0;
     st = a.ta == MM_BF16 ? launch_tiles<MM_BF16>(a, ra, rw, p, ctx) : launch_tiles<MM_F16>(a, ra, rw, p, ctx);
     if (st == MM_OK) count_operator_launch();
     return st;

@@ -137,42 +137,8 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr)
-               : "memory");
-  return v;
-}
-// Add the fp32 tiles [rows][128] that the CTAs of a cluster (at most 8) hold
-// at the same shared-memory address, over the ranks in order: CTA `rank`
-// takes the rows rank, rank + ranks, ..., a warp a row, four columns a lane,
-// and hands them to out(row, column, sum).  Two rows of loads are in flight
-// a warp (one at a time took 4 us more for 128 rows over 4 CTAs).
-template <typename Out>
-__device__ __forceinline__ void add_cluster_tiles(uint32_t tile, int rows, int rank, int ranks, int warp,
-                                                  int warps, Out &&out) {
-  const int lane = threadIdx.x & 31;
-  for (int m = rank + warp * ranks; m < rows; m += 2 * warps * ranks) {
-    const int m2 = m + warps * ranks;
-    float4 a[8], b[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < ranks) {
-        const uint32_t at = map_to_rank(tile + (uint32_t)lane * 16u, (uint32_t)k);
-        a[k] = ld_cluster_f32x4(at + (uint32_t)m * 512u);
-        if (m2 < rows) b[k] = ld_cluster_f32x4(at + (uint32_t)m2 * 512u);
-      }
-#pragma unroll
-    for (int k = 1; k < 8; ++k)
-      if (k < ranks) {
-        a[0].x += a[k].x, a[0].y += a[k].y, a[0].z += a[k].z, a[0].w += a[k].w;
-        b[0].x += b[k].x, b[0].y += b[k].y, b[0].z += b[k].z, b[0].w += b[k].w;
-      }
-    out(m, lane * 4, a[0]);
-    if (m2 < rows) out(m2, lane * 4, b[0]);
-  }
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
 // ---------------------------------------------------------------- TMA
@@ -310,6 +276,68 @@ __device__ __forceinline__ void tmem_ld_32cols(uint32_t taddr, uint32_t (&r)[32]
 }
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- tiles out of TMEM
+// A swapped product's fp32 tile (lane = column n of the output, TMEM column =
+// row m) on its way out, where K may be split over the RANKS CTAs of a
+// cluster.  Row m belongs to CTA m % RANKS: each storing warp writes its 32
+// lanes' values of a row to the owner's shared memory, [rank][m / RANKS][128]
+// floats, which costs the sender no wait; after a barrier each owner adds its
+// rows' parts in rank order from its own memory, a warp a row, four columns a
+// lane, so the stores to global memory are whole rows of 128.  (The owners
+// reading the other CTAs' tiles instead, a column at a time, cost 13 us at
+// 128 rows; 9 us read 16 bytes a lane.)
+// Columns [c0, c0 + step, ...) of 32 of `rows`, by one warp; `tile` is the
+// address in this CTA, `lane_col` the lane's column n.
+template <int RANKS>
+__device__ __forceinline__ void push_tile(uint32_t tmem_addr, uint32_t tile, int rank, int per, int rows,
+                                          int c0, int step, int lane_col, bool empty) {
+  uint32_t owner[RANKS];
+#pragma unroll
+  for (int k = 0; k < RANKS; ++k)
+    owner[k] = map_to_rank(tile + (uint32_t)(rank * per * 128 + lane_col) * 4u, (uint32_t)k);
+#pragma unroll 1
+  for (int c = c0; c < rows; c += step) {
+    uint32_t r[32];
+    tmem_ld_32cols(tmem_addr + (uint32_t)c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i < rows)
+        st_cluster_f32(owner[i % RANKS] + (uint32_t)((c + i) / RANKS) * 512u, empty ? 0.f : __uint_as_float(r[i]));
+  }
+}
+__device__ __forceinline__ void push_tile(uint32_t tmem_addr, uint32_t tile, int rank, int ranks, int per,
+                                          int rows, int c0, int step, int lane_col, bool empty) {
+  switch (ranks) {
+  case 1: return push_tile<1>(tmem_addr, tile, rank, per, rows, c0, step, lane_col, empty);
+  case 2: return push_tile<2>(tmem_addr, tile, rank, per, rows, c0, step, lane_col, empty);
+  case 4: return push_tile<4>(tmem_addr, tile, rank, per, rows, c0, step, lane_col, empty);
+  default: return push_tile<8>(tmem_addr, tile, rank, per, rows, c0, step, lane_col, empty);
+  }
+}
+// The owner's side: its rows to out(m, v), a warp a row.  A lane has the
+// columns 4 lane .. 4 lane + 3 (VEC, for rows that take 16-byte aligned
+// stores), else lane, lane + 32, lane + 64 and lane + 96.
+template <bool VEC, typename Out>
+__device__ __forceinline__ void sum_tile(const float *tile, int rank, int ranks, int per, int rows, int warp,
+                                         int warps, Out &&out) {
+  const int lane = threadIdx.x & 31;
+  for (int s = warp; s * ranks + rank < rows; s += warps) {
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < ranks) {
+        const float *part = tile + (k * per + s) * 128;
+        v[k] = VEC ? reinterpret_cast<const float4 *>(part)[lane]
+                   : make_float4(part[lane], part[lane + 32], part[lane + 64], part[lane + 96]);
+      }
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+      if (k < ranks) v[0].x += v[k].x, v[0].y += v[k].y, v[0].z += v[k].z, v[0].w += v[k].w;
+    out(s * ranks + rank, v[0]);
+  }
 }
 
 // 16 consecutive columns of 32 lanes: thread i writes lane i's.

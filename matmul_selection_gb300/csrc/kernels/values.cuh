@@ -34,4 +34,28 @@ __device__ __forceinline__ void store_value(void *p, int t, int64_t i, float v) 
     static_cast<uint8_t *>(p)[i] = to_e4m3(v);
 }
 
+// Four values of a row from element i on, `step` apart, those below `left`
+// elements from i: one store where step is 1 (a 16-byte aligned row).
+template <int STEP>
+__device__ __forceinline__ void store_four(void *p, int t, int64_t i, float4 v, int left) {
+  if (STEP == 1 && left >= 4) {
+    if (t == MM_F32) {
+      *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = v;
+    } else if (t == MM_BF16) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+      *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + i) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
+      const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+      *reinterpret_cast<uint2 *>(static_cast<__half *>(p) + i) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+    return;
+  }
+  const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k * STEP < left) store_value(p, t, i + k * STEP, x[k]);
+}
+
 }  // namespace mm
