@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S::kStages + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ranks = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster along x splits K
-  const int n0 = (int)blockIdx.y * 128, m0 = (int)blockIdx.z * BN;
+  const int ranks = (int)gridDim.y, rank = (int)blockIdx.y;  // a cluster along y splits K
+  const int n0 = (int)blockIdx.x * 128, m0 = (int)blockIdx.z * BN;
   const int kb0 = rank * p.kb_per_rank, nk = max(0, min(p.kb_per_rank, p.num_kb - kb0));
 
   if (threadIdx.x == 0) {
@@ -450,10 +450,9 @@ mm_status run_swap(const Q8Args &a, Q8Params p, int ranks, LaunchCtx &ctx) {
   if ((st = rows_map(&mb, a.B, a.N, a.K, a.ldb, 128)) != MM_OK) return st;
   if ((st = rows_map(&ma, a.A, a.M, a.K, a.lda, BN)) != MM_OK) return st;
   p.kb_per_rank = (p.num_kb + ranks - 1) / ranks;
-  const int gy = (a.N + 127) / 128, gz = (a.M + BN - 1) / BN;
-  if (gy > 65535 || gz > 65535) return set_error(MM_ERR_UNSUPPORTED, "too many tiles");
-  cudaError_t e = launch_pdl(q8_swap_kernel<BN>, dim3((unsigned)ranks, (unsigned)gy, (unsigned)gz),
-                             dim3(kSwapThreads), Swap<BN>::kSmem, ctx.stream, dim3((unsigned)ranks), mb, ma, p);
+  const int gx = (a.N + 127) / 128, gz = (a.M + BN - 1) / BN;
+  cudaError_t e = launch_pdl(q8_swap_kernel<BN>, dim3((unsigned)gx, (unsigned)ranks, (unsigned)gz),
+                             dim3(kSwapThreads), Swap<BN>::kSmem, ctx.stream, dim3(1, (unsigned)ranks), mb, ma, p);
   return e == cudaSuccess ? MM_OK : cuda_error(e, "gemm_q8 launch (swap)");
 }
 
@@ -462,11 +461,8 @@ mm_status run_swap(const Q8Args &a, Q8Params p, int ranks, LaunchCtx &ctx) {
 mm_status launch_gemm_q8(const Q8Args &in, LaunchCtx &ctx) {
   Q8Args a = in;
   mm_status st;
-  if (a.K == 0) {
-    const size_t es = (size_t)dtype_bytes(a.tc);
-    MM_CUDA_TRY(cudaMemset2DAsync(a.out, (size_t)a.ldc * es, 0, (size_t)a.N * es, (size_t)a.M, ctx.stream));
-    return MM_OK;
-  }
+  if (a.K == 0) return write_zeros(a.out, a.ldc, a.M, a.N, a.tc, ctx);
+  if (a.M <= 16) return launch_gemv_q8(a, ctx);
   TmaRows ra{a.A, a.lda, a.M, a.K}, rb{a.B, a.ldb, a.N, a.K};
   if ((st = align_rows(ra, rb, ctx)) != MM_OK) return st;
   a.A = static_cast<const uint8_t *>(ra.p);

@@ -1,7 +1,8 @@
 // Product with weights held in 4 bits and group scales:
 //   out[m, n] = sum_k A[m, k] s[n, k / group] (q[n, k] - z[n, k / group])
 //
-// M > 16, on tcgen05 (kind::f16), as out^T = W A^T: 128 rows of the weights are
+// For more than 16 rows of A (fewer: gemv_quant.cu), on tcgen05 (kind::f16), as
+// out^T = W A^T: 128 rows of the weights are
 // the MMA's A side, BN rows of A its other side.  The scales change along K, so
 // the weights are made on the way in: sixteen warps turn codes into 16-bit
 // weights (q - z is exact, its product with the scale is rounded once to A's
@@ -12,15 +13,13 @@
 // persistent; where there are few tiles K is split over the CTAs of a cluster,
 // whose fp32 tiles meet in distributed shared memory and are added in rank
 // order.
-//
-// M <= 16: a warp an output column and kRows rows of A; each lane sums its k's
-// in fp32.
 #include <algorithm>
 #include <mutex>
 
 #include "../operators.h"
 #include "tcgen05.cuh"
 #include "values.cuh"
+#include "w4.cuh"
 
 namespace mm {
 
@@ -66,60 +65,10 @@ struct TileParams {
   int kb_per_rank;  // a multiple of 4 where K is split
   int tiles_n, tiles;
   int *err;
-  const void *scales;
-  const uint8_t *zeros;
-  int64_t lds;
-  int ts, group_shift, groups;
+  W4Scales w;
   int split_scale;  // the scales' type is not A's
   bool vec;         // out's rows are 16-byte aligned
 };
-
-template <int TA>
-struct Pair16 {
-  using T = __nv_bfloat162;
-  static __device__ __forceinline__ T both(float v) { return __float2bfloat162_rn(v); }
-};
-template <>
-struct Pair16<MM_F16> {
-  using T = __half2;
-  static __device__ __forceinline__ T both(float v) { return __float2half2_rn(v); }
-};
-template <typename T>
-__device__ __forceinline__ T bits_as(uint32_t v) {
-  return *reinterpret_cast<const T *>(&v);
-}
-template <typename T>
-__device__ __forceinline__ uint32_t as_bits(const T &v) {
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-// A row's scales and zero points: where they start, and how many there are (0
-// past the last row).
-struct ScaleRow {
-  const char *s;
-  const uint8_t *z;
-  int groups;
-};
-__device__ __forceinline__ ScaleRow scale_row(const TileParams &p, int n) {
-  const bool in = n < p.N;
-  const int64_t at = in ? (int64_t)n * p.lds : 0;
-  return ScaleRow{static_cast<const char *>(p.scales) + at * (p.ts == MM_F32 ? 4 : 2),
-                  p.zeros ? p.zeros + at : nullptr, in ? p.groups : 0};
-}
-// A scale and a zero point as they lie in memory, loaded a stage of codes ahead.
-struct RawScale {
-  uint32_t s, z;
-};
-__device__ __forceinline__ RawScale load_raw_scale(const TileParams &p, const ScaleRow &row, int k) {
-  RawScale r{0u, 8u};
-  const int g = k >> p.group_shift;
-  if (g < row.groups) {
-    r.s = p.ts == MM_F32 ? __ldg(reinterpret_cast<const uint32_t *>(row.s) + g)
-                         : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row.s) + g);
-    if (row.z) r.z = __ldg(row.z + g);
-  }
-  return r;
-}
 
 // The scale and zero point of 32 codes of a row.  A scale of another type than
 // A's is taken as a sum of two of A's type, hi + lo, so that a weight is still
@@ -135,9 +84,7 @@ __device__ __forceinline__ GroupScale<TA> group_scale(const TileParams &p, const
   if (!p.split_scale) {
     g.hi = g.lo = bits_as<T>(r.s * 0x00010001u);
   } else {
-    const float s = p.ts == MM_F32    ? __uint_as_float(r.s)
-                    : p.ts == MM_BF16 ? __uint_as_float(r.s << 16)
-                                      : __half2float(__ushort_as_half((unsigned short)r.s));
+    const float s = raw_scale_value(p.w, r);
     g.hi = Pair16<TA>::both(s);
     g.lo = Pair16<TA>::both(s - __low2float(g.hi));
   }
@@ -191,17 +138,17 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
   const int row = (warp & 3) * 32 + lane;  // the TMEM lanes this warp may write
   const int j = (r.group - r.turn) & (kGroups - 1);
   const uint32_t dst0 = r.weights + ((uint32_t)((warp & 3) * 32) << 16);
-  const ScaleRow srow = scale_row(p, n0 + row);
-  const bool two = p.group_shift == 5;  // a block of 64 spans two groups
+  const ScaleRow srow = scale_row(p.w, n0 + row);
+  const bool two = p.w.group_shift == 5;  // a block of 64 spans two groups
   const uint8_t *crow = r.codes + row * 128;
   const uint32_t at[2] = {(uint32_t)((2 * j) ^ (row & 7)) << 4, (uint32_t)((2 * j + 1) ^ (row & 7)) << 4};
   RawScale next[2];
-  next[0] = load_raw_scale(p, srow, (kb0 + j) * 64);
-  next[1] = two ? load_raw_scale(p, srow, (kb0 + j) * 64 + 32) : next[0];
+  next[0] = load_raw_scale(p.w, srow, (kb0 + j) * 64);
+  next[1] = two ? load_raw_scale(p.w, srow, (kb0 + j) * 64 + 32) : next[0];
   for (int i = j; i < nk + j; i += kGroups) {  // a stage of codes, of which this group takes block j
     const RawScale cur[2] = {next[0], next[1]};
-    next[0] = load_raw_scale(p, srow, (kb0 + i + kGroups) * 64);
-    next[1] = two ? load_raw_scale(p, srow, (kb0 + i + kGroups) * 64 + 32) : next[0];
+    next[0] = load_raw_scale(p.w, srow, (kb0 + i + kGroups) * 64);
+    next[1] = two ? load_raw_scale(p.w, srow, (kb0 + i + kGroups) * 64 + 32) : next[0];
     if (!warp_wait(r.cfull0 + 8 * r.cs, r.cphase, abort_flag, p.err, kErrDequant)) return false;
     uint4 c[2];
 #pragma unroll
@@ -485,73 +432,29 @@ mm_status launch_tiles(const W4Args &a, const TmaRows &ra, const TmaRows &rw, co
                       : run_tiles<TA, 256>(a, ra, rw, p, ctx);
 }
 
-// ---------------------------------------------------------------- few rows
-constexpr int kThreads = 256;
-constexpr int kRows = 8;
-
-__global__ void __launch_bounds__(kThreads) w4_simple_kernel(const W4Args a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t n = (int64_t)blockIdx.x * (kThreads / 32) + warp;
-  if (n >= a.N) return;
-  for (int64_t m0 = (int64_t)blockIdx.y * kRows; m0 < a.M; m0 += (int64_t)gridDim.y * kRows) {
-    float acc[kRows] = {};
-    for (int k = lane; k < a.K; k += 32) {
-      const int g = k / a.group;
-      const uint8_t b = a.codes[(n * a.ldw + k) / 2];
-      const int q = k & 1 ? b >> 4 : b & 15;
-      const int z = a.zeros ? a.zeros[n * a.lds + g] & 15 : 8;
-      const float w = load_value(a.scales, a.ts, n * a.lds + g) * (float)(q - z);
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        if (m0 + i < a.M) acc[i] += w * load_value(a.A, a.ta, (m0 + i) * a.lda + k);
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      float v = acc[i];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0 && m0 + i < a.M) store_value(a.out, a.tc, (m0 + i) * a.ldc + n, v);
-    }
-  }
-}
-
 }  // namespace
 
 mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
+  if (a.K == 0) return write_zeros(a.out, a.ldc, a.M, a.N, a.tc, ctx);
+  if (a.M <= 16) return launch_gemv_w4(a, ctx);
   mm_status st;
-  if (a.M > 16 && a.K > 0) {
-    TmaRows ra{a.A, a.lda * 2, a.M, (int64_t)a.K * 2}, rw{a.codes, a.ldw / 2, a.N, ((int64_t)a.K + 1) / 2};
-    if ((st = align_rows(ra, rw, ctx)) != MM_OK) return st;
-    TileParams p;
-    std::memset(&p, 0, sizeof p);
-    p.out = a.out;
-    p.ldc = a.ldc;
-    p.tc = a.tc;
-    p.M = a.M;
-    p.N = a.N;
-    p.num_kb = (int)(((int64_t)a.K + 63) / 64);
-    p.err = ctx.dev->d_err + kOperatorErrorWord;
-    p.scales = a.scales;
-    p.zeros = a.zeros;
-    p.lds = a.lds;
-    p.ts = a.ts;
-    p.group_shift = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
-    p.groups = (a.K + a.group - 1) / a.group;
-    p.split_scale = a.ts != a.ta;
-    p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0;
-    st = a.ta == MM_BF16 ? launch_tiles<MM_BF16>(a, ra, rw, p, ctx) : launch_tiles<MM_F16>(a, ra, rw, p, ctx);
-    if (st == MM_OK) count_operator_launch();
-    return st;
-  }
-  const int64_t gx = ((int64_t)a.N + kThreads / 32 - 1) / (kThreads / 32);
-  const int64_t gy = std::min<int64_t>(((int64_t)a.M + kRows - 1) / kRows, 1024);
-  cudaError_t e = launch_pdl(w4_simple_kernel, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), 0,
-                             ctx.stream, dim3(1), a);
-  if (e != cudaSuccess) return cuda_error(e, "gemm_w4 launch");
-  count_operator_launch();
-  return MM_OK;
+  TmaRows ra{a.A, a.lda * 2, a.M, (int64_t)a.K * 2}, rw{a.codes, a.ldw / 2, a.N, ((int64_t)a.K + 1) / 2};
+  if ((st = align_rows(ra, rw, ctx)) != MM_OK) return st;
+  TileParams p;
+  std::memset(&p, 0, sizeof p);
+  p.out = a.out;
+  p.ldc = a.ldc;
+  p.tc = a.tc;
+  p.M = a.M;
+  p.N = a.N;
+  p.num_kb = (int)(((int64_t)a.K + 63) / 64);
+  p.err = ctx.dev->d_err + kOperatorErrorWord;
+  p.w = w4_scales(a);
+  p.split_scale = a.ts != a.ta;
+  p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0;
+  st = a.ta == MM_BF16 ? launch_tiles<MM_BF16>(a, ra, rw, p, ctx) : launch_tiles<MM_F16>(a, ra, rw, p, ctx);
+  if (st == MM_OK) count_operator_launch();
+  return st;
 }
 
 }  // namespace mm

@@ -1,0 +1,374 @@
+// Products of at most 16 rows with quantised weights, both held [N][K]:
+//   4-bit  out[m, n] = sum_k A[m, k] s[n, k / group] (q[n, k] - z[n, k / group])
+//   e4m3   out[m, n] = scale_a[m] scale_b[n] sum_k A[m, k] B[n, k]
+// One pass over the weights, which is what bounds them.  A CTA of eight
+// computing warps owns R = 16 WR rows of the weights; WR warps side by side
+// take 16 rows each, and WK = 8 / WR of them take turns along K, a panel (128
+// bytes of each row) at a time.  The fewer rows A has, the fewer rows of the
+// weights share its panels: R = 8 M keeps A's traffic from L2 below the
+// weights'.  Panels of weights and of A come by TMA through a ring; the MMA is
+// the warp-level one with the weights as its 16-row operand:
+//   4-bit  ldmatrix hands each lane 8 neighbouring codes of a row and its
+//          lane's 16 bytes of A hold the same 8 k; q - z is exact in 16 bits,
+//          and the scale multiplies the fp32 sum of its group.
+//   e4m3   m16n8k32 on the bytes as they are.
+// The warps' parts (and those of a cluster's CTAs, which split K where there
+// are few rows of weights) meet in the owner's shared memory and are added in
+// order: one launch, the same bits every time.
+#include <algorithm>
+#include <mutex>
+
+#include "../operators.h"
+#include "tcgen05.cuh"
+#include "values.cuh"
+#include "w4.cuh"
+
+namespace mm {
+
+namespace {
+
+using namespace tc;
+
+enum Format { FMT_W4_BF16 = MM_BF16, FMT_W4_F16 = MM_F16, FMT_E4M3 = MM_E4M3 };
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * (kWarps + 2);  // and two copying warps
+constexpr int kStages = 4;
+constexpr uint32_t kWeightsB = 16384, kRowsB = 8192;  // a stage's weights and rows of A
+constexpr uint32_t kStageB = kWeightsB + kRowsB;
+constexpr uint32_t kPartsB = 8192, kSlackB = 4096;  // (rows of A past M are read, not used)
+constexpr size_t kSmem = kStages * kStageB + kSlackB + kPartsB + 1024 + 128;
+constexpr int kErrCopy = 0xa01, kErrMma = 0xa02;
+
+struct GemvParams {
+  void *out;
+  int64_t ldc;
+  int tc;
+  int M, N;
+  int panels, panels_per_rank;
+  const float *sa, *sb;
+  W4Scales w;
+  int *err;
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds_16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+// D (16 x 8, fp32) += A (16 rows of weights) . B (8 rows of A).
+template <int F>
+__device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+#define MM_MMA_SYNC(SHAPE_TYPES)                                                                        \
+  asm volatile("mma.sync.aligned." SHAPE_TYPES " {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};" \
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                         \
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+  if constexpr (F == FMT_W4_BF16) MM_MMA_SYNC("m16n8k16.row.col.f32.bf16.bf16.f32");
+  if constexpr (F == FMT_W4_F16) MM_MMA_SYNC("m16n8k16.row.col.f32.f16.f16.f32");
+  if constexpr (F == FMT_E4M3) MM_MMA_SYNC("m16n8k32.row.col.f32.e4m3.e4m3.f32");
+#undef MM_MMA_SYNC
+}
+
+// Scales (fp32) and biased zero points (16-bit pairs) of two rows, for 64 codes
+// of a panel each lane: lane t of four holds those of the panel's codes from
+// 64 t on, entry h those from 64 t + 32 h.
+struct PanelScales {
+  RawScale raw[2][2];  // [row][h]
+};
+template <int F>
+__device__ __forceinline__ void load_panel_scales(const W4Scales &w, const ScaleRow (&rows)[2], int k0, int t,
+                                                  PanelScales &s) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    s.raw[r][0] = load_raw_scale(w, rows[r], k0 + 64 * t);
+    s.raw[r][1] = w.group_shift == 5 ? load_raw_scale(w, rows[r], k0 + 64 * t + 32) : s.raw[r][0];
+  }
+}
+
+// A panel of 16 rows of 4-bit weights (256 codes) times 8 MT rows of A.
+template <int F, int MT>
+__device__ __forceinline__ void panel_w4(const GemvParams &p, uint32_t wrow, uint32_t xrow, const PanelScales &ps,
+                                         float (&acc)[MT][4]) {
+  using T = typename Pair16<F>::T;
+  constexpr uint32_t kBias = F == FMT_W4_BF16 ? 0x43004300u : 0x64006400u;
+  const int lane = threadIdx.x & 31;
+  float scale[2][2];
+  uint32_t zero[2][2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      scale[r][h] = raw_scale_value(p.w, ps.raw[r][h]);
+      zero[r][h] = kBias + (ps.raw[r][h].z & 15u) * 0x00010001u;
+    }
+  const int last = (1 << (p.w.group_shift - 5)) - 1;  // the chunk of 32 that ends a group: (c & last) == last
+  float part[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[m][i] = 0.f;
+#pragma unroll
+  for (int c2 = 0; c2 < 4; ++c2) {  // two chunks of 32 codes
+    uint32_t w[4];  // rows r, r + 8 of the first; of the second
+    const uint32_t rr = lane & 7, mat = lane >> 3;
+    ldmatrix_x4(wrow + (((2 * c2 + (mat >> 1)) ^ rr) << 4), w);
+    const int src = (lane & 28) | c2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      T z[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        z[r] = bits_as<T>(p.w.z ? __shfl_sync(0xffffffffu, zero[r][h], src) : kBias + 0x00080008u);
+      uint32_t a[2][4];  // row, pairs (0, 1), (2, 3), (4, 5), (6, 7)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t lo = w[2 * h + r], hi = lo >> 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          a[r][i] = as_bits(__hsub2(
+              bits_as<T>((__byte_perm(lo, hi, 0x0400 + 0x0101 * i) & 0x000f000fu) | kBias), z[r]));
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint4 x = lds_16(xrow + (uint32_t)(m * 8 * 512 + (2 * c2 + h) * 64));
+        mma_16x8<F>(part[m], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+        mma_16x8<F>(part[m], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+      }
+      if (((2 * c2 + h) & last) == last) {
+        const float s0 = __shfl_sync(0xffffffffu, scale[0][h], src), s1 = __shfl_sync(0xffffffffu, scale[1][h], src);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          acc[m][0] += s0 * part[m][0], acc[m][1] += s0 * part[m][1];
+          acc[m][2] += s1 * part[m][2], acc[m][3] += s1 * part[m][3];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) part[m][i] = 0.f;
+        }
+      }
+    }
+  }
+}
+
+// A panel of 16 rows of e4m3 weights (128 bytes) times 8 MT rows of A.
+template <int MT>
+__device__ __forceinline__ void panel_e4m3(uint32_t wrow, uint32_t xpanel, float (&acc)[MT][4]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t rr = lane & 7, mat = lane >> 3;
+#pragma unroll
+  for (int s = 0; s < 4; s += 2) {
+    uint32_t x[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)  // chunks 2 s .. 2 s + 3 of 8 rows of A
+      ldmatrix_x4(xpanel + (uint32_t)(m * 1024) + rr * 128 + (((2 * s + mat) ^ rr) << 4), x[m]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[4];
+      ldmatrix_x4(wrow + (((2 * (s + h) + (mat >> 1)) ^ rr) << 4), w);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        mma_16x8<FMT_E4M3>(acc[m], w[0], w[1], w[2], w[3], x[m][2 * h], x[m][2 * h + 1]);
+    }
+  }
+}
+
+template <int F, int WR>
+__global__ void __launch_bounds__(kThreads, 2)
+    gemv_quant_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                      const GemvParams p) {
+  constexpr int WK = kWarps / WR, R = 16 * WR, MT = WR == 8 ? 2 : 1;
+  constexpr bool W4 = F != FMT_E4M3;
+  constexpr uint32_t XPANEL = kRowsB / WK;  // 2 WR rows of 512 bytes, or 8 MT and more of 128
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  float *parts = reinterpret_cast<float *>(smem + kStages * kStageB + kSlackB);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kStageB + kSlackB + kPartsB);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 2 * kStages);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ranks = (int)gridDim.y, rank = (int)blockIdx.y;  // a cluster along y splits K
+  const int n0 = (int)blockIdx.x * R;
+  const int p0 = rank * p.panels_per_rank, np = max(0, min(p.panels_per_rank, p.panels - p0));
+  const int steps = (np + WK - 1) / WK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 2);  // both copying warps arm their bytes
+      mbar_init(empty0 + 8 * s, kWarps);
+    }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == kWarps) {
+    if (lane == 0) prefetch_tmap(&tmW);
+    for (int i = lane; i < min(np, 64); i += 32) tma_prefetch_2d(&tmW, (p0 + i) * 128, n0);
+  }
+  if (warp == kWarps + 1 && lane == 0) prefetch_tmap(&tmX);
+  if (ranks > 1) cluster_sync_all();  // the others run: their memory may be written
+  else __syncthreads();
+  pdl_wait();
+
+  if (warp >= kWarps) {
+    const bool weights = warp == kWarps;
+    const uint32_t bytes = weights ? R * 128 : (uint32_t)p.M * (W4 ? 512u : 128u);
+    const uint32_t offset = weights ? 0u : kWeightsB, pitch = weights ? R * 128 : XPANEL;
+    const int kx = weights ? 128 : W4 ? 256 : 128;  // a panel in the map's elements
+    int i = 0;
+    for (; i < steps; ++i) {
+      const int st = i % kStages;
+      if (!warp_wait(empty0 + 8 * st, ((uint32_t)(i / kStages) & 1u) ^ 1u, abort_flag, p.err, kErrCopy)) break;
+      const int nv = min(WK, np - i * WK);
+      mbar_expect_tx(full0 + 8 * st, (uint32_t)nv * bytes);
+      __syncwarp();
+      if (lane < nv)
+        tma_load_2d_lane(smem_u32(smem + st * kStageB + offset) + (uint32_t)lane * pitch, weights ? &tmW : &tmX,
+                         full0 + 8 * st, (p0 + i * WK + lane) * kx, weights ? n0 : 0);
+    }
+    __syncwarp();
+    for (int f = max(0, i - kStages); f < i; ++f)
+      wait_drain(full0 + 8 * (f % kStages), (uint32_t)(f / kStages) & 1u, p.err, kErrCopy);
+    __syncwarp();
+  } else {
+    const int wr = warp % WR, wk = warp / WR, t = lane & 3;
+    float acc[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+    const uint32_t stage0 = smem_u32(smem);
+    const uint32_t wrow = stage0 + (uint32_t)(wk * R * 128) + (uint32_t)(wr * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
+    const uint32_t xpan = stage0 + kWeightsB + (uint32_t)wk * XPANEL;
+    ScaleRow rows[2] = {};
+    PanelScales next = {};
+    if constexpr (W4) {
+      rows[0] = scale_row(p.w, n0 + wr * 16 + (lane >> 2));
+      rows[1] = scale_row(p.w, n0 + wr * 16 + (lane >> 2) + 8);
+      load_panel_scales<F>(p.w, rows, (p0 + wk) * 256, t, next);
+    }
+    for (int i = 0; i < steps; ++i) {
+      const int st = i % kStages;
+      PanelScales cur = next;
+      if constexpr (W4) load_panel_scales<F>(p.w, rows, (p0 + (i + 1) * WK + wk) * 256, t, next);
+      if (!warp_wait(full0 + 8 * st, (uint32_t)(i / kStages) & 1u, abort_flag, p.err, kErrMma)) break;
+      if (i * WK + wk < np) {
+        const uint32_t off = (uint32_t)st * kStageB;
+        if constexpr (W4)
+          panel_w4<F, MT>(p, wrow + off, xpan + off + (uint32_t)((lane >> 2) * 512 + t * 16), cur, acc);
+        else
+          panel_e4m3<MT>(wrow + off, xpan + off, acc);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8 * st);  // after the MMAs that used the stage
+    }
+    // to the owners: CTA r has the columns [r CS, (r + 1) CS) of the R, [part][m][CS]
+    const int cs = R / ranks, part = rank * WK + wk;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = wr * 16 + (lane >> 2) + (i >> 1) * 8, row = m * 8 + 2 * t + (i & 1);
+        if (row < p.M) {
+          const uint32_t at = smem_u32(parts + (part * p.M + row) * cs + col % cs);
+          st_cluster_f32(map_to_rank(at, (uint32_t)(col / cs)), acc[m][i]);
+        }
+      }
+  }
+  if (ranks > 1) cluster_sync_all();
+  else __syncthreads();
+  const int cs = R / ranks, nparts = ranks * WK;
+  for (int o = threadIdx.x; o < p.M * cs; o += kThreads) {
+    const int m = o / cs, n = n0 + rank * cs + o % cs;
+    if (n >= p.N) continue;
+    float v = 0.f;
+    for (int q = 0; q < nparts; ++q) v += parts[q * p.M * cs + o];
+    if constexpr (!W4) v = v * (p.sa ? __ldg(p.sa + m) : 1.f) * (p.sb ? __ldg(p.sb + n) : 1.f);
+    store_value(p.out, p.tc, (int64_t)m * p.ldc + n, v);
+  }
+}
+
+template <int F, int WR>
+mm_status run(const TmaRows &rx, const TmaRows &rw, int K, GemvParams p, LaunchCtx &ctx) {
+  constexpr int WK = kWarps / WR, R = 16 * WR;
+  auto kern = gemv_quant_kernel<F, WR>;
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [&] {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  });
+  if (err != cudaSuccess) return cuda_error(err, "quantised GEMV set-up");
+  CUtensorMap mw, mx;
+  mm_status st = encode_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, rw.p, (uint64_t)rw.bytes, (uint64_t)rw.rows,
+                               (uint64_t)rw.ld, 128, R, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != MM_OK) return st;
+  st = F == FMT_E4M3
+           ? encode_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, rx.p, (uint64_t)K, (uint64_t)rx.rows,
+                           (uint64_t)rx.ld, 128, (uint32_t)p.M, CU_TENSOR_MAP_SWIZZLE_128B)
+           : encode_map_2d(&mx, F == FMT_W4_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                           rx.p, (uint64_t)K, (uint64_t)rx.rows, (uint64_t)rx.ld, 256, (uint32_t)p.M,
+                           CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (st != MM_OK) return st;
+  p.panels = (int)((rw.bytes + 127) / 128);
+  const int tiles = (p.N + R - 1) / R;
+  // two CTAs an SM; each rank at least two steps of the ring
+  int ranks = 1;
+  while (ranks < 8 && (int64_t)tiles * ranks * 2 <= 2 * ctx.dev->info.sms && p.panels >= 2 * ranks * WK) ranks *= 2;
+  p.panels_per_rank = ((p.panels + ranks - 1) / ranks + WK - 1) / WK * WK;
+  cudaError_t e = launch_pdl(kern, dim3((unsigned)tiles, (unsigned)ranks), dim3(kThreads), kSmem, ctx.stream,
+                             dim3(1, (unsigned)ranks), mw, mx, p);
+  if (e != cudaSuccess) return cuda_error(e, "quantised GEMV launch");
+  count_operator_launch();
+  return MM_OK;
+}
+
+template <int F>
+mm_status run_rows(const TmaRows &rx, const TmaRows &rw, int K, const GemvParams &p, LaunchCtx &ctx) {
+  return p.M <= 2   ? run<F, 1>(rx, rw, K, p, ctx)
+         : p.M <= 4 ? run<F, 2>(rx, rw, K, p, ctx)
+         : p.M <= 8 ? run<F, 4>(rx, rw, K, p, ctx)
+                    : run<F, 8>(rx, rw, K, p, ctx);
+}
+
+GemvParams gemv_params(void *out, int64_t ldc, int tc, int M, int N, LaunchCtx &ctx) {
+  GemvParams p;
+  std::memset(&p, 0, sizeof p);
+  p.out = out;
+  p.ldc = ldc;
+  p.tc = tc;
+  p.M = M;
+  p.N = N;
+  p.err = ctx.dev->d_err + kOperatorErrorWord;
+  return p;
+}
+
+}  // namespace
+
+mm_status launch_gemv_w4(const W4Args &a, LaunchCtx &ctx) {
+  TmaRows rx{a.A, a.lda * 2, a.M, (int64_t)a.K * 2}, rw{a.codes, a.ldw / 2, a.N, ((int64_t)a.K + 1) / 2};
+  mm_status st = align_rows(rx, rw, ctx);
+  if (st != MM_OK) return st;
+  GemvParams p = gemv_params(a.out, a.ldc, a.tc, a.M, a.N, ctx);
+  p.w = w4_scales(a);
+  return a.ta == MM_BF16 ? run_rows<FMT_W4_BF16>(rx, rw, a.K, p, ctx) : run_rows<FMT_W4_F16>(rx, rw, a.K, p, ctx);
+}
+
+mm_status launch_gemv_q8(const Q8Args &a, LaunchCtx &ctx) {
+  TmaRows rx{a.A, a.lda, a.M, a.K}, rw{a.B, a.ldb, a.N, a.K};
+  mm_status st = align_rows(rx, rw, ctx);
+  if (st != MM_OK) return st;
+  GemvParams p = gemv_params(a.out, a.ldc, a.tc, a.M, a.N, ctx);
+  p.sa = a.scale_a;
+  p.sb = a.scale_b;
+  return run_rows<FMT_E4M3>(rx, rw, a.K, p, ctx);
+}
+
+}  // namespace mm

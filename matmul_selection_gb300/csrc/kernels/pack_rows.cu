@@ -68,4 +68,10 @@ mm_status align_rows(TmaRows &a, TmaRows &b, LaunchCtx &ctx) {
   return MM_OK;
 }
 
+mm_status write_zeros(void *out, int64_t ldc, int M, int N, int tc, LaunchCtx &ctx) {
+  const size_t es = (size_t)dtype_bytes(tc);
+  MM_CUDA_TRY(cudaMemset2DAsync(out, (size_t)ldc * es, 0, (size_t)N * es, (size_t)M, ctx.stream));
+  return MM_OK;
+}
+
 }  // namespace mm

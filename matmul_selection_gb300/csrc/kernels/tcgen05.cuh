@@ -163,7 +163,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
-// The same for a CTA pair: the bytes complete on the leader's barrier
+// The same by every active lane on its own.
+__device__ __forceinline__ void tma_load_2d_lane(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x,
+                                                 int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+// For a CTA pair: the bytes complete on the leader's barrier
 // (a shared::cluster address).  Warp-collective.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map,
                                                  uint32_t leader_bar, int x, int y) {

@@ -53,6 +53,13 @@ struct Q8Args {
 };
 mm_status launch_gemm_q8(const Q8Args &a, LaunchCtx &ctx);
 
+// Their forms for at most 16 rows of A (K > 0).
+mm_status launch_gemv_w4(const W4Args &a, LaunchCtx &ctx);
+mm_status launch_gemv_q8(const Q8Args &a, LaunchCtx &ctx);
+
+// The product over no k.
+mm_status write_zeros(void *out, int64_t ldc, int M, int N, int tc, LaunchCtx &ctx);
+
 // Rows that TMA is to read: `rows` rows of `bytes` bytes, ld bytes apart.
 struct TmaRows {
   const void *p;
