@@ -51,66 +51,120 @@ struct GemvParams {
   int *err;
 };
 
+// The loads and MMAs of a panel are left for the compiler to order (they are
+// not volatile): what keeps them between the wait for the stage and its
+// release is data, an address that is defined after the wait and sums that are
+// complete before the release (see after_wait, before_release).
 __device__ __forceinline__ void ldmatrix_x4(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
+  asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(a));
 }
 __device__ __forceinline__ uint4 lds_16(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
+  asm("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
+}
+__device__ __forceinline__ uint32_t after_wait(uint32_t a) {
+  asm volatile("" : "+r"(a)::"memory");
+  return a;
+}
+template <int MT>
+__device__ __forceinline__ void before_release(float (&acc)[MT][4]) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    asm volatile("" : "+f"(acc[m][0]), "+f"(acc[m][1]), "+f"(acc[m][2]), "+f"(acc[m][3])::"memory");
 }
 // D (16 x 8, fp32) += A (16 rows of weights) . B (8 rows of A).
 template <int F>
 __device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
 #define MM_MMA_SYNC(SHAPE_TYPES)                                                                        \
-  asm volatile("mma.sync.aligned." SHAPE_TYPES " {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};" \
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                         \
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+  asm("mma.sync.aligned." SHAPE_TYPES " {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};" \
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                         \
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
   if constexpr (F == FMT_W4_BF16) MM_MMA_SYNC("m16n8k16.row.col.f32.bf16.bf16.f32");
   if constexpr (F == FMT_W4_F16) MM_MMA_SYNC("m16n8k16.row.col.f32.f16.f16.f32");
   if constexpr (F == FMT_E4M3) MM_MMA_SYNC("m16n8k32.row.col.f32.e4m3.e4m3.f32");
 #undef MM_MMA_SYNC
 }
 
-// Scales (fp32) and biased zero points (16-bit pairs) of two rows, for 64 codes
-// of a panel each lane: lane t of four holds those of the panel's codes from
-// 64 t on, entry h those from 64 t + 32 h.
-struct PanelScales {
-  RawScale raw[2][2];  // [row][h]
+// Where a lane's scales and zero points are: of its two rows, for the 64 codes
+// of a panel from 64 t on (lane t of four), entry h those from 64 t + 32 h
+// (TWO: groups of 32; else both entries are one).  A row past N stands for the
+// last, and a group past the last one for that: their results are not used or
+// multiply zeros.
+struct ScaleCursor {
+  const char *s[2];
+  const uint8_t *z[2];
+  int g, step, last;
 };
-template <int F>
-__device__ __forceinline__ void load_panel_scales(const W4Scales &w, const ScaleRow (&rows)[2], int k0, int t,
-                                                  PanelScales &s) {
+struct PanelScales {
+  uint32_t s[2][2];  // [row][h], as in memory
+  uint32_t z[2][2];
+};
+__device__ __forceinline__ ScaleCursor scale_cursor(const W4Scales &w, int n, int k0, int k_step) {
+  ScaleCursor c;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    s.raw[r][0] = load_raw_scale(w, rows[r], k0 + 64 * t);
-    s.raw[r][1] = w.group_shift == 5 ? load_raw_scale(w, rows[r], k0 + 64 * t + 32) : s.raw[r][0];
+    const int64_t at = (int64_t)min(n + 8 * r, w.N - 1) * w.lds;
+    c.s[r] = static_cast<const char *>(w.s) + at * (w.ts == MM_F32 ? 4 : 2);
+    c.z[r] = w.z + at;  // (not read without zero points)
   }
+  c.g = k0 >> w.group_shift;
+  c.step = k_step >> w.group_shift;
+  c.last = w.groups - 1;
+  return c;
+}
+template <bool TWO>
+__device__ __forceinline__ void load_panel_scales(const W4Scales &w, ScaleCursor &c, PanelScales &s) {
+#pragma unroll
+  for (int h = 0; h < (TWO ? 2 : 1); ++h) {
+    const int g = min(c.g + h, c.last);
+    if (w.ts == MM_F32) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) s.s[r][h] = __ldg(reinterpret_cast<const uint32_t *>(c.s[r]) + g);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) s.s[r][h] = __ldg(reinterpret_cast<const uint16_t *>(c.s[r]) + g);
+    }
+    if (w.z) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) s.z[r][h] = __ldg(c.z[r] + g);
+    }
+  }
+  c.g += c.step;
+}
+// (a & b) | c
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 
 // A panel of 16 rows of 4-bit weights (256 codes) times 8 MT rows of A.
-template <int F, int MT>
+template <int F, int MT, bool TWO>
 __device__ __forceinline__ void panel_w4(const GemvParams &p, uint32_t wrow, uint32_t xrow, const PanelScales &ps,
                                          float (&acc)[MT][4]) {
   using T = typename Pair16<F>::T;
   constexpr uint32_t kBias = F == FMT_W4_BF16 ? 0x43004300u : 0x64006400u;
+  constexpr int E = TWO ? 2 : 1;
   const int lane = threadIdx.x & 31;
-  float scale[2][2];
-  uint32_t zero[2][2];
+  const bool zeros = p.w.z != nullptr;
+  float scale[2][E];
+  uint32_t zero[2][E];
+  if (p.w.ts == MM_F16) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+    for (int i = 0; i < 2 * E; ++i)
+      scale[i / E][i % E] = __half2float(__ushort_as_half((unsigned short)ps.s[i / E][i % E]));
+  } else {
+    const int shift = p.w.ts == MM_BF16 ? 16 : 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      scale[r][h] = raw_scale_value(p.w, ps.raw[r][h]);
-      zero[r][h] = kBias + (ps.raw[r][h].z & 15u) * 0x00010001u;
-    }
+    for (int i = 0; i < 2 * E; ++i) scale[i / E][i % E] = __uint_as_float(ps.s[i / E][i % E] << shift);
+  }
+  if (zeros)
+#pragma unroll
+    for (int i = 0; i < 2 * E; ++i) zero[i / E][i % E] = kBias + (ps.z[i / E][i % E] & 15u) * 0x00010001u;
   const int last = (1 << (p.w.group_shift - 5)) - 1;  // the chunk of 32 that ends a group: (c & last) == last
   float part[MT][4];
 #pragma unroll
@@ -128,7 +182,7 @@ __device__ __forceinline__ void panel_w4(const GemvParams &p, uint32_t wrow, uin
       T z[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        z[r] = bits_as<T>(p.w.z ? __shfl_sync(0xffffffffu, zero[r][h], src) : kBias + 0x00080008u);
+        z[r] = bits_as<T>(zeros ? __shfl_sync(0xffffffffu, zero[r][h % E], src) : kBias + 0x00080008u);
       uint32_t a[2][4];  // row, pairs (0, 1), (2, 3), (4, 5), (6, 7)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -136,7 +190,7 @@ __device__ __forceinline__ void panel_w4(const GemvParams &p, uint32_t wrow, uin
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           a[r][i] = as_bits(__hsub2(
-              bits_as<T>((__byte_perm(lo, hi, 0x0400 + 0x0101 * i) & 0x000f000fu) | kBias), z[r]));
+              bits_as<T>(and_or(__byte_perm(lo, hi, 0x0400 + 0x0101 * i), 0x000f000fu, kBias)), z[r]));
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -144,8 +198,9 @@ __device__ __forceinline__ void panel_w4(const GemvParams &p, uint32_t wrow, uin
         mma_16x8<F>(part[m], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
         mma_16x8<F>(part[m], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
       }
-      if (((2 * c2 + h) & last) == last) {
-        const float s0 = __shfl_sync(0xffffffffu, scale[0][h], src), s1 = __shfl_sync(0xffffffffu, scale[1][h], src);
+      if (TWO || ((2 * c2 + h) & last) == last) {
+        const float s0 = __shfl_sync(0xffffffffu, scale[0][h % E], src);
+        const float s1 = __shfl_sync(0xffffffffu, scale[1][h % E], src);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           acc[m][0] += s0 * part[m][0], acc[m][1] += s0 * part[m][1];
@@ -180,7 +235,7 @@ __device__ __forceinline__ void panel_e4m3(uint32_t wrow, uint32_t xpanel, float
   }
 }
 
-template <int F, int WR>
+template <int F, int WR, bool TWO>
 __global__ void __launch_bounds__(kThreads, 2)
     gemv_quant_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                       const GemvParams p) {
@@ -248,27 +303,27 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t stage0 = smem_u32(smem);
     const uint32_t wrow = stage0 + (uint32_t)(wk * R * 128) + (uint32_t)(wr * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
     const uint32_t xpan = stage0 + kWeightsB + (uint32_t)wk * XPANEL;
-    ScaleRow rows[2] = {};
+    ScaleCursor cursor = {};
     PanelScales next = {};
     if constexpr (W4) {
-      rows[0] = scale_row(p.w, n0 + wr * 16 + (lane >> 2));
-      rows[1] = scale_row(p.w, n0 + wr * 16 + (lane >> 2) + 8);
-      load_panel_scales<F>(p.w, rows, (p0 + wk) * 256, t, next);
+      cursor = scale_cursor(p.w, n0 + wr * 16 + (lane >> 2), (p0 + wk) * 256 + 64 * t, WK * 256);
+      load_panel_scales<TWO>(p.w, cursor, next);
     }
     for (int i = 0; i < steps; ++i) {
       const int st = i % kStages;
-      PanelScales cur = next;
-      if constexpr (W4) load_panel_scales<F>(p.w, rows, (p0 + (i + 1) * WK + wk) * 256, t, next);
+      const PanelScales cur = next;
+      if constexpr (W4) load_panel_scales<TWO>(p.w, cursor, next);
       if (!warp_wait(full0 + 8 * st, (uint32_t)(i / kStages) & 1u, abort_flag, p.err, kErrMma)) break;
       if (i * WK + wk < np) {
-        const uint32_t off = (uint32_t)st * kStageB;
+        const uint32_t off = after_wait((uint32_t)st * kStageB);
         if constexpr (W4)
-          panel_w4<F, MT>(p, wrow + off, xpan + off + (uint32_t)((lane >> 2) * 512 + t * 16), cur, acc);
+          panel_w4<F, MT, TWO>(p, wrow + off, xpan + off + (uint32_t)((lane >> 2) * 512 + t * 16), cur, acc);
         else
           panel_e4m3<MT>(wrow + off, xpan + off, acc);
+        before_release(acc);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty0 + 8 * st);  // after the MMAs that used the stage
+      if (lane == 0) mbar_arrive(empty0 + 8 * st);
     }
     // to the owners: CTA r has the columns [r CS, (r + 1) CS) of the R, [part][m][CS]
     const int cs = R / ranks, part = rank * WK + wk;
@@ -296,10 +351,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <int F, int WR>
+template <int F, int WR, bool TWO>
 mm_status run(const TmaRows &rx, const TmaRows &rw, int K, GemvParams p, LaunchCtx &ctx) {
   constexpr int WK = kWarps / WR, R = 16 * WR;
-  auto kern = gemv_quant_kernel<F, WR>;
+  auto kern = gemv_quant_kernel<F, WR, TWO>;
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [&] {
@@ -330,12 +385,12 @@ mm_status run(const TmaRows &rx, const TmaRows &rw, int K, GemvParams p, LaunchC
   return MM_OK;
 }
 
-template <int F>
+template <int F, bool TWO>
 mm_status run_rows(const TmaRows &rx, const TmaRows &rw, int K, const GemvParams &p, LaunchCtx &ctx) {
-  return p.M <= 2   ? run<F, 1>(rx, rw, K, p, ctx)
-         : p.M <= 4 ? run<F, 2>(rx, rw, K, p, ctx)
-         : p.M <= 8 ? run<F, 4>(rx, rw, K, p, ctx)
-                    : run<F, 8>(rx, rw, K, p, ctx);
+  return p.M <= 2   ? run<F, 1, TWO>(rx, rw, K, p, ctx)
+         : p.M <= 4 ? run<F, 2, TWO>(rx, rw, K, p, ctx)
+         : p.M <= 8 ? run<F, 4, TWO>(rx, rw, K, p, ctx)
+                    : run<F, 8, TWO>(rx, rw, K, p, ctx);
 }
 
 GemvParams gemv_params(void *out, int64_t ldc, int tc, int M, int N, LaunchCtx &ctx) {
@@ -358,7 +413,10 @@ mm_status launch_gemv_w4(const W4Args &a, LaunchCtx &ctx) {
   if (st != MM_OK) return st;
   GemvParams p = gemv_params(a.out, a.ldc, a.tc, a.M, a.N, ctx);
   p.w = w4_scales(a);
-  return a.ta == MM_BF16 ? run_rows<FMT_W4_BF16>(rx, rw, a.K, p, ctx) : run_rows<FMT_W4_F16>(rx, rw, a.K, p, ctx);
+  const bool two = a.group == 32;
+  if (a.ta == MM_BF16)
+    return two ? run_rows<FMT_W4_BF16, true>(rx, rw, a.K, p, ctx) : run_rows<FMT_W4_BF16, false>(rx, rw, a.K, p, ctx);
+  return two ? run_rows<FMT_W4_F16, true>(rx, rw, a.K, p, ctx) : run_rows<FMT_W4_F16, false>(rx, rw, a.K, p, ctx);
 }
 
 mm_status launch_gemv_q8(const Q8Args &a, LaunchCtx &ctx) {
@@ -368,7 +426,7 @@ mm_status launch_gemv_q8(const Q8Args &a, LaunchCtx &ctx) {
   GemvParams p = gemv_params(a.out, a.ldc, a.tc, a.M, a.N, ctx);
   p.sa = a.scale_a;
   p.sb = a.scale_b;
-  return run_rows<FMT_E4M3>(rx, rw, a.K, p, ctx);
+  return run_rows<FMT_E4M3, false>(rx, rw, a.K, p, ctx);
 }
 
 }  // namespace mm
