@@ -11,9 +11,10 @@
 // Statistics are fp32 sums.  Rows longer than the registers hold, and rows that
 // do not start on 16 bytes, have forms of their own below.
 #include <algorithm>
-#include <type_traits>
+#include <mutex>
 
 #include "../operators.h"
+#include "tcgen05.cuh"
 #include "values.cuh"
 
 namespace mm {
@@ -23,42 +24,85 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 
 // ---------------------------------------------------------------- elements
-template <int TX>
-struct Elem {  // bf16
-  using T = __nv_bfloat16;
-  static __device__ __forceinline__ float get(T v) { return __bfloat162float(v); }
-  static __device__ __forceinline__ T put(float v) { return __float2bfloat16_rn(v); }
-};
-template <>
-struct Elem<MM_F16> {
-  using T = __half;
-  static __device__ __forceinline__ float get(T v) { return __half2float(v); }
-  static __device__ __forceinline__ T put(float v) { return __float2half_rn(v); }
-};
-template <>
-struct Elem<MM_F32> {
-  using T = float;
-  static __device__ __forceinline__ float get(T v) { return v; }
-  static __device__ __forceinline__ T put(float v) { return v; }
-};
+constexpr __host__ __device__ int bytes_of(int t) { return t == MM_F32 ? 4 : 2; }
 
-// E neighbours of type TX as one access.
+// E neighbours of type TX as they lie in memory, in registers: one access of
+// 2 to 16 bytes (two of 16 for eight fp32).
 template <int TX, int E>
-struct alignas(E * sizeof(typename Elem<TX>::T)) Piece {
-  typename Elem<TX>::T v[E];
+struct Piece {
+  static constexpr int kBytes = E * bytes_of(TX);
+  uint32_t w[(kBytes + 3) / 4];
+  static __device__ __forceinline__ Piece load(const void *p) {
+    Piece x;
+    if constexpr (kBytes == 2) {
+      x.w[0] = *static_cast<const uint16_t *>(p);
+    } else if constexpr (kBytes == 4) {
+      x.w[0] = *static_cast<const uint32_t *>(p);
+    } else if constexpr (kBytes == 8) {
+      const uint2 v = *static_cast<const uint2 *>(p);
+      x.w[0] = v.x, x.w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 v = static_cast<const uint4 *>(p)[i];
+        x.w[4 * i] = v.x, x.w[4 * i + 1] = v.y, x.w[4 * i + 2] = v.z, x.w[4 * i + 3] = v.w;
+      }
+    }
+    return x;
+  }
+  __device__ __forceinline__ void store(void *p) const {
+    if constexpr (kBytes == 2) {
+      *static_cast<uint16_t *>(p) = (uint16_t)w[0];
+    } else if constexpr (kBytes == 4) {
+      *static_cast<uint32_t *>(p) = w[0];
+    } else if constexpr (kBytes == 8) {
+      *static_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        static_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (TX == MM_F32) return __uint_as_float(w[e]);
+    if constexpr (TX == MM_BF16) return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    const __half2 v = *reinterpret_cast<const __half2 *>(&w[e / 2]);
+    return e & 1 ? __high2float(v) : __low2float(v);
+  }
+  static __device__ __forceinline__ Piece of(const float (&v)[E]) {
+    Piece x;
+    if constexpr (TX == MM_F32) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x.w[e] = __float_as_uint(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float hi = e + 1 < E ? v[(e + 1) % E] : 0.f;
+        if constexpr (TX == MM_BF16) {
+          const __nv_bfloat162 y = __floats2bfloat162_rn(v[e], hi);
+          x.w[e / 2] = *reinterpret_cast<const uint32_t *>(&y);
+        } else {
+          const __half2 y = __floats2half2_rn(v[e], hi);
+          x.w[e / 2] = *reinterpret_cast<const uint32_t *>(&y);
+        }
+      }
+    }
+    return x;
+  }
 };
+template <int TX>
+__device__ __forceinline__ const void *at(const void *p, int64_t i) {
+  return static_cast<const char *>(p) + i * bytes_of(TX);
+}
 template <int TX, int E>
 __device__ __forceinline__ void load_piece(const void *p, int64_t i, float (&out)[E]) {
-  const Piece<TX, E> x = *reinterpret_cast<const Piece<TX, E> *>(static_cast<const typename Elem<TX>::T *>(p) + i);
+  const Piece<TX, E> x = Piece<TX, E>::load(at<TX>(p, i));
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = Elem<TX>::get(x.v[e]);
+  for (int e = 0; e < E; ++e) out[e] = x.get(e);
 }
 template <int TX, int E>
 __device__ __forceinline__ void store_piece(void *p, int64_t i, const float (&v)[E]) {
-  Piece<TX, E> x;
-#pragma unroll
-  for (int e = 0; e < E; ++e) x.v[e] = Elem<TX>::put(v[e]);
-  *reinterpret_cast<Piece<TX, E> *>(static_cast<typename Elem<TX>::T *>(p) + i) = x;
+  Piece<TX, E>::of(v).store(static_cast<char *>(p) + i * bytes_of(TX));
 }
 // The same for a type that is known only at run time (the same for every
 // thread).
@@ -353,9 +397,8 @@ mm_status forward_form(const NormArgs &a, LaunchCtx &ctx) {
   } else {
     if (pieces <= 1024) return rows_form<TX, E, 256, 4>(a, ctx);
     if (pieces <= 2048) return rows_form<TX, E, 512, 4>(a, ctx);
-    if (pieces <= 4096) return rows_form<TX, E, 1024, 4>(a, ctx);
-    if (pieces <= 6144) return rows_form<TX, E, 1024, 6>(a, ctx);
-    if (pieces <= 8192) return rows_form<TX, E, 1024, 8>(a, ctx);
+    if (pieces <= 5120) return rows_form<TX, E, 512, 10>(a, ctx);
+    if (pieces <= 8192) return rows_form<TX, E, 512, 16>(a, ctx);
     if (pieces <= 16384) return rows_form<TX, E, 1024, 16>(a, ctx);
   }
   return launch(rmsnorm_long_kernel<TX, E>, std::min<int64_t>(a.rows, 2 * ctx.dev->info.sms), 1024, ctx,
@@ -371,82 +414,250 @@ mm_status forward_type(const NormArgs &a, LaunchCtx &ctx) {
   al.operand(a.weight, 0, 1, type_size(a.tw));
   al.operand(a.h, a.ldh, a.rows, type_size(a.tx));
   al.operand(a.y, a.ldy, a.rows, type_size(a.ty));
-  constexpr int most = 16 / sizeof(typename Elem<TX>::T);
+  constexpr int most = 16 / bytes_of(TX);
   return al.elements(most) == most ? forward_form<TX, most>(a, ctx) : forward_form<TX, 1>(a, ctx);
 }
 
 // ---------------------------------------------------------------- backward
-// A block of T threads walks rows blockIdx.x, blockIdx.x + gridDim.x, ...; a
-// thread holds the same V pieces of E columns of each (as they lie in memory,
-// dy of x's type) and its own sums of dy h rstd.  The weight comes from L1 each
-// time.  The blocks' sums go to a workspace and a second kernel adds them in
-// block order.
-template <int TX, int E, int T, int V>
-__global__ void __launch_bounds__(T) rmsnorm_bwd_kernel(const NormBwdArgs a, float *partial) {
+// Three forms, by the length of a row and its alignment.  Each block walks the
+// rows blockIdx.x, blockIdx.x + gridDim.x, ... (or its warps do) and keeps its
+// sums of dy h rstd in registers; the blocks' sums go to a workspace and a
+// second kernel adds them in block order.
+//
+// What a thread does with a piece of a row: its share of sum(dy w h) and
+// sum(h^2), then, when the sums are there, its dx and its part of dw.
+template <int TX, int E>
+struct BwdPiece {
   using P = Piece<TX, E>;
-  using X = typename Elem<TX>::T;
+  static __device__ __forceinline__ void sums(const P &dy, const P &h, const float (&w)[E], float &dot, float &ss) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float x = h.get(e);
+      dot += dy.get(e) * w[e] * x;
+      ss += x * x;
+    }
+  }
+  static __device__ __forceinline__ void outputs(const P &dy, const P &h, const P *dh, const float (&w)[E], float rs,
+                                                 float c, float (&dx)[E], float (&dw)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float g = dy.get(e), x = h.get(e);
+      dx[e] = rs * (g * w[e] - x * c);
+      if (dh) dx[e] += dh->get(e);
+      dw[e] += g * x * rs;
+    }
+  }
+};
+__device__ __forceinline__ int64_t partial_ld(int cols) { return (int64_t)(cols + 3) / 4 * 4; }
+
+// Short rows: a warp a row, eight warps a block, no barrier until the end,
+// where the warps' sums are added in order.
+template <int TX, int E, int V>
+__global__ void __launch_bounds__(256) rmsnorm_bwd_warps_kernel(const NormBwdArgs a, float *partial) {
+  using P = Piece<TX, E>;
   pdl_launch_dependents();
   pdl_wait();
+  __shared__ float sums[8][32 * V * E];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float w[V][E], dw[V][E];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int j = (v * 32 + lane) * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[v][e] = dw[v][e] = 0.f;
+    if (j < a.cols) load_piece(a.weight, a.tw, j, w[v]);
+  }
+  const float per_col = 1.f / (float)a.cols;
+  for (int64_t r = (int64_t)blockIdx.x * 8 + warp; r < a.rows; r += (int64_t)gridDim.x * 8) {
+    P dy[V], h[V], dh[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int j = (v * 32 + lane) * E;
+      if (j < a.cols) {
+        dy[v] = P::load(at<TX>(a.dy, r * a.lddy + j));
+        h[v] = P::load(at<TX>(a.h, r * a.ldh + j));
+        if (a.dh) dh[v] = P::load(at<TX>(a.dh, r * a.lddh + j));
+      }
+    }
+    float rs = a.rstd ? a.rstd[r] : 0.f;
+    float dot = 0.f, ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if ((v * 32 + lane) * E < a.cols) BwdPiece<TX, E>::sums(dy[v], h[v], w[v], dot, ss);
+    dot = row_sum<32>(dot, nullptr);
+    if (!a.rstd) rs = 1.f / sqrtf(row_sum<32>(ss, nullptr) / (float)a.cols + a.eps);
+    const float c = dot * per_col * rs * rs;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int j = (v * 32 + lane) * E;
+      if (j < a.cols) {
+        float dx[E];
+        BwdPiece<TX, E>::outputs(dy[v], h[v], a.dh ? &dh[v] : nullptr, w[v], rs, c, dx, dw[v]);
+        store_piece<TX>(a.dx, r * a.lddx + j, dx);
+      }
+    }
+  }
+  if (!partial) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[warp][(v * 32 + lane) * E + e] = dw[v][e];
+  __syncthreads();
+  for (int j = threadIdx.x; j < a.cols; j += 256) {
+    float s = sums[0][j];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += sums[k][j];
+    partial[blockIdx.x * partial_ld(a.cols) + j] = s;
+  }
+}
+
+// Rows of whole 16-byte pieces: a block a row at a time, its dy, h and dh
+// brought by bulk copies into a ring of rows in shared memory, so that what is
+// in flight (up to 200 KB an SM) does not depend on registers.  (Rows held in
+// registers, the next one's loads issued ahead: 85 us at 8192 x 4096 bf16, 47 %
+// of HBM's rate.)  Both passes read the row from shared memory.  A stage is
+// refilled after the next row's barrier, which every thread reaches only when
+// it is done with the row before.
+constexpr int kMaxRing = 8, kErrRing = 0xb01;
+template <int TX, int T, int V>
+__global__ void __launch_bounds__(T) rmsnorm_bwd_ring_kernel(const NormBwdArgs a, float *partial, int stages,
+                                                              int *err) {
+  constexpr int E = 16 / bytes_of(TX);
+  using P = Piece<TX, E>;
+  pdl_launch_dependents();
+  extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float sh[2][2 * (T / 32)];
+  __shared__ __align__(8) uint64_t full[kMaxRing];
   const int t = threadIdx.x;
+  const uint32_t row = (uint32_t)a.cols * bytes_of(TX), parts = a.dh ? 3 : 2, stage_bytes = parts * row;
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) tc::mbar_init(tc::smem_u32(full + s), 1);
+    tc::mbar_init_fence();
+  }
+  __syncthreads();
+  pdl_wait();
+  auto fill = [&](int64_t r, int s) {  // one thread
+    const uint32_t bar = tc::smem_u32(full + s), dst = tc::smem_u32(ring) + (uint32_t)s * stage_bytes;
+    tc::mbar_expect_tx_one(bar, stage_bytes);
+    tc::bulk_load(dst, at<TX>(a.dy, r * a.lddy), row, bar);
+    tc::bulk_load(dst + row, at<TX>(a.h, r * a.ldh), row, bar);
+    if (a.dh) tc::bulk_load(dst + 2 * row, at<TX>(a.dh, r * a.lddh), row, bar);
+  };
+  if (t == 0)
+    for (int s = 0; s < stages; ++s)
+      if (blockIdx.x + (int64_t)s * gridDim.x < a.rows) fill(blockIdx.x + (int64_t)s * gridDim.x, s);
   float dw[V][E];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[v][e] = 0.f;
-  P dy[V], h[V], dh[V];
-  auto load = [&](int64_t r) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = (v * T + t) * E;
-      if (j < a.cols) {
-        dy[v] = *reinterpret_cast<const P *>(static_cast<const X *>(a.dy) + r * a.lddy + j);
-        h[v] = *reinterpret_cast<const P *>(static_cast<const X *>(a.h) + r * a.ldh + j);
-        if (a.dh) dh[v] = *reinterpret_cast<const P *>(static_cast<const X *>(a.dh) + r * a.lddh + j);
-      }
-    }
-  };
-  int side = 0;
+  const float per_col = 1.f / (float)a.cols;
+  int s = 0, side = 0;
+  uint32_t phase = 0;
+  bool gave_up = false;  // (a wait ran into its limit: no further one is waited for)
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    load(r);
     const float given = a.rstd ? a.rstd[r] : 0.f;
+    const uint8_t *dy = ring + (size_t)s * stage_bytes, *h = dy + row, *dh = h + row;
     float dot = 0.f, ss = 0.f;
+    if (!gave_up && !tc::thread_wait(tc::smem_u32(full + s), phase, err, kErrRing)) gave_up = true;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int j = (v * T + t) * E;
-      if (j < a.cols) {
+      const int i = v * T + t;
+      if (i * E < a.cols) {
         float w[E];
-        load_piece(a.weight, a.tw, j, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float x = Elem<TX>::get(h[v].v[e]);
-          dot += Elem<TX>::get(dy[v].v[e]) * w[e] * x;
-          ss += x * x;
-        }
+        load_piece(a.weight, a.tw, i * E, w);
+        BwdPiece<TX, E>::sums(P::load(dy + i * 16), P::load(h + i * 16), w, dot, ss);
       }
     }
     // two sets of shared sums in turn: one barrier a row
     dot = row_sum<T>(dot, sh[side]);
     float rs = given;
-    if (!a.rstd) {
-      ss = row_sum<T>(ss, sh[side] + T / 32);
-      rs = 1.f / sqrtf(ss / (float)a.cols + a.eps);
-    }
+    if (!a.rstd) rs = 1.f / sqrtf(row_sum<T>(ss, sh[side] + T / 32) / (float)a.cols + a.eps);
     side ^= 1;
-    const float c = dot / (float)a.cols * rs * rs;
+    // every thread is done with the row before: its stage takes the row `stages` after it
+    const int64_t r_next = r + (int64_t)(stages - 1) * gridDim.x;
+    if (t == 0 && r != blockIdx.x && r_next < a.rows) fill(r_next, s == 0 ? stages - 1 : s - 1);
+    const float c = dot * per_col * rs * rs;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = v * T + t;
+      if (i * E < a.cols) {
+        float w[E], dx[E];
+        load_piece(a.weight, a.tw, i * E, w);
+        P d;
+        if (a.dh) d = P::load(dh + i * 16);
+        BwdPiece<TX, E>::outputs(P::load(dy + i * 16), P::load(h + i * 16), a.dh ? &d : nullptr, w, rs, c, dx, dw[v]);
+        store_piece<TX>(a.dx, r * a.lddx + i * E, dx);
+      }
+    }
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+  if (partial)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int j = (v * T + t) * E;
-      if (j < a.cols) {
-        float w[E], dx[E];
-        load_piece(a.weight, a.tw, j, w);
+      if (j < a.cols) store_piece<MM_F32>(partial, blockIdx.x * partial_ld(a.cols) + j, dw[v]);
+    }
+}
+
+// Rows that start anywhere: element by element, the row in registers, the next
+// row's loads issued before this row's sums are waited for.
+template <int TX, int T, int V>
+__global__ void __launch_bounds__(T) rmsnorm_bwd_elements_kernel(const NormBwdArgs a, float *partial) {
+  using P = Piece<TX, 1>;
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ float sh[2][2 * (T / 32)];
+  const int t = threadIdx.x;
+  float dw[V][1];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float g = Elem<TX>::get(dy[v].v[e]), x = Elem<TX>::get(h[v].v[e]);
-          dx[e] = rs * (g * w[e] - x * c);
-          if (a.dh) dx[e] += Elem<TX>::get(dh[v].v[e]);
-          dw[v][e] += g * x * rs;
-        }
+  for (int v = 0; v < V; ++v) dw[v][0] = 0.f;
+  struct Row {
+    P dy[V], h[V], dh[V];
+  };
+  auto load = [&](int64_t r, Row &x) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int j = v * T + t;
+      if (j < a.cols) {
+        x.dy[v] = P::load(at<TX>(a.dy, r * a.lddy + j));
+        x.h[v] = P::load(at<TX>(a.h, r * a.ldh + j));
+        if (a.dh) x.dh[v] = P::load(at<TX>(a.dh, r * a.lddh + j));
+      }
+    }
+  };
+  const float per_col = 1.f / (float)a.cols;
+  Row next;
+  if (blockIdx.x < a.rows) load(blockIdx.x, next);
+  int side = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const Row cur = next;
+    if (r + gridDim.x < a.rows) load(r + gridDim.x, next);
+    const float given = a.rstd ? a.rstd[r] : 0.f;
+    float dot = 0.f, ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int j = v * T + t;
+      if (j < a.cols) {
+        const float w[1] = {load_value(a.weight, a.tw, j)};
+        BwdPiece<TX, 1>::sums(cur.dy[v], cur.h[v], w, dot, ss);
+      }
+    }
+    dot = row_sum<T>(dot, sh[side]);
+    float rs = given;
+    if (!a.rstd) rs = 1.f / sqrtf(row_sum<T>(ss, sh[side] + T / 32) / (float)a.cols + a.eps);
+    side ^= 1;
+    const float c = dot * per_col * rs * rs;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int j = v * T + t;
+      if (j < a.cols) {
+        const float w[1] = {load_value(a.weight, a.tw, j)};
+        float dx[1];
+        BwdPiece<TX, 1>::outputs(cur.dy[v], cur.h[v], a.dh ? &cur.dh[v] : nullptr, w, rs, c, dx, dw[v]);
         store_piece<TX>(a.dx, r * a.lddx + j, dx);
       }
     }
@@ -454,12 +665,12 @@ __global__ void __launch_bounds__(T) rmsnorm_bwd_kernel(const NormBwdArgs a, flo
   if (partial)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int j = (v * T + t) * E;
-      if (j < a.cols) store_piece<MM_F32>(partial, (int64_t)blockIdx.x * ((a.cols + 3) / 4 * 4) + j, dw[v]);
+      const int j = v * T + t;
+      if (j < a.cols) partial[blockIdx.x * partial_ld(a.cols) + j] = dw[v][0];
     }
 }
 
-// Rows too long for the registers: 1 / rms and the mean of g h of each row (two
+// Longer rows, and dy of another type than h: 1 / rms and the mean of g h of each row (two
 // floats a row), then columns in slices, each thread walking down the rows.
 template <int TX, int E>
 __global__ void __launch_bounds__(1024) rmsnorm_bwd_stats_kernel(const NormBwdArgs a, float2 *stats) {
@@ -468,16 +679,27 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_stats_kernel(const NormBwdAr
   __shared__ float sh[64];
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     float dot = 0.f, ss = 0.f;
-    for (int j = threadIdx.x * E; j < a.cols; j += 1024 * E) {
-      float dy[E], h[E], w[E];
-      load_piece(a.dy, a.ty, r * a.lddy + j, dy);
-      load_piece<TX>(a.h, r * a.ldh + j, h);
-      load_piece(a.weight, a.tw, j, w);
+    constexpr int U = E == 1 ? 4 : 2;  // pieces in flight
+    for (int j0 = threadIdx.x * E; j0 < a.cols; j0 += U * 1024 * E) {
+      float dy[U][E], h[U][E], w[U][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        dot += dy[e] * w[e] * h[e];
-        ss += h[e] * h[e];
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * 1024 * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) dy[u][e] = h[u][e] = w[u][e] = 0.f;
+        if (j < a.cols) {
+          load_piece(a.dy, a.ty, r * a.lddy + j, dy[u]);
+          load_piece<TX>(a.h, r * a.ldh + j, h[u]);
+          load_piece(a.weight, a.tw, j, w[u]);
+        }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          dot += dy[u][e] * w[u][e] * h[u][e];
+          ss += h[u][e] * h[u][e];
+        }
     }
     __syncthreads();
     dot = row_sum<1024>(dot, sh);
@@ -497,23 +719,33 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_cols_kernel(const NormBwdArgs
   if (j >= a.cols) return;
   float w[E], dw[E] = {};
   load_piece(a.weight, a.tw, j, w);
-  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    float dy[E], h[E], dx[E];
-    load_piece(a.dy, a.ty, r * a.lddy + j, dy);
-    load_piece<TX>(a.h, r * a.ldh + j, h);
-    const float2 s = stats[r];
+  constexpr int U = E == 1 ? 4 : 2;  // rows in flight
+  for (int64_t r0 = blockIdx.y; r0 < a.rows; r0 += (int64_t)U * gridDim.y) {
+    float dy[U][E], h[U][E], dh[U][E] = {};
+    float2 s[U];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      dx[e] = s.x * (dy[e] * w[e] - h[e] * s.y);
-      dw[e] += dy[e] * h[e] * s.x;
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = r0 + (int64_t)u * gridDim.y;
+      if (r < a.rows) {
+        load_piece(a.dy, a.ty, r * a.lddy + j, dy[u]);
+        load_piece<TX>(a.h, r * a.ldh + j, h[u]);
+        if (a.dh) load_piece<TX>(a.dh, r * a.lddh + j, dh[u]);
+        s[u] = stats[r];
+      }
     }
-    if (a.dh) {
-      float dh[E];
-      load_piece<TX>(a.dh, r * a.lddh + j, dh);
 #pragma unroll
-      for (int e = 0; e < E; ++e) dx[e] += dh[e];
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = r0 + (int64_t)u * gridDim.y;
+      if (r < a.rows) {
+        float dx[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          dx[e] = dh[u][e] + s[u].x * (dy[u][e] * w[e] - h[u][e] * s[u].y);
+          dw[e] += dy[u][e] * h[u][e] * s[u].x;
+        }
+        store_piece<TX>(a.dx, r * a.lddx + j, dx);
+      }
     }
-    store_piece<TX>(a.dx, r * a.lddx + j, dx);
   }
   if (partial) store_piece<MM_F32>(partial, (int64_t)blockIdx.y * ((a.cols + 3) / 4 * 4) + j, dw);
 }
@@ -561,15 +793,47 @@ mm_status add_parts(const NormBwdArgs &a, const float *partial, int parts, Launc
                 parts, a.cols, a.dweight, a.tw);
 }
 
-template <int TX, int E, int T, int V>
-mm_status bwd_rows_form(const NormBwdArgs &a, int per_sm, LaunchCtx &ctx) {
-  const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)per_sm * ctx.dev->info.sms);
+// `blocks` blocks of a kernel that leaves a part of dweight a block.
+template <typename K, typename... Args>
+mm_status bwd_blocks(const NormBwdArgs &a, K kern, int64_t blocks, int threads, size_t smem, LaunchCtx &ctx,
+                     Args... args) {
   float *partial = nullptr;
   mm_status st;
   if (a.dweight && (st = partial_space(a, blocks, 0, ctx, &partial)) != MM_OK) return st;
-  st = launch(rmsnorm_bwd_kernel<TX, E, T, V>, blocks, T, ctx, "rmsnorm_backward launch", a, partial);
-  if (st != MM_OK || !a.dweight) return st;
-  return add_parts(a, partial, (int)blocks, ctx);
+  cudaError_t e = launch_pdl(kern, dim3((unsigned)blocks), dim3((unsigned)threads), smem, ctx.stream, dim3(1), a,
+                             partial, args...);
+  if (e != cudaSuccess) return cuda_error(e, "rmsnorm_backward launch");
+  count_operator_launch();
+  return a.dweight ? add_parts(a, partial, (int)blocks, ctx) : MM_OK;
+}
+
+template <int TX, int E, int V>
+mm_status bwd_warps_form(const NormBwdArgs &a, LaunchCtx &ctx) {
+  const int64_t blocks = std::min<int64_t>((a.rows + 7) / 8, 3 * ctx.dev->info.sms);
+  return bwd_blocks(a, rmsnorm_bwd_warps_kernel<TX, E, V>, blocks, 256, 0, ctx);
+}
+
+constexpr size_t kRingBytes = 208 << 10;  // of an SM's shared memory
+
+template <int TX, int T, int V>
+mm_status bwd_ring_form(const NormBwdArgs &a, int per_sm, LaunchCtx &ctx) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  auto kern = rmsnorm_bwd_ring_kernel<TX, T, V>;
+  std::call_once(once, [&] {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+  });
+  if (err != cudaSuccess) return cuda_error(err, "rmsnorm_backward set-up");
+  const size_t stage = (size_t)(a.dh ? 3 : 2) * a.cols * bytes_of(TX);
+  const int stages = (int)std::min<size_t>(kMaxRing, kRingBytes / per_sm / stage);
+  const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)per_sm * ctx.dev->info.sms);
+  return bwd_blocks(a, kern, blocks, T, stages * stage, ctx, stages, ctx.dev->d_err + kOperatorErrorWord);
+}
+
+template <int TX, int T, int V>
+mm_status bwd_elements_form(const NormBwdArgs &a, int per_sm, LaunchCtx &ctx) {
+  return bwd_blocks(a, rmsnorm_bwd_elements_kernel<TX, T, V>,
+                    std::min<int64_t>(a.rows, (int64_t)per_sm * ctx.dev->info.sms), T, 0, ctx);
 }
 
 template <int TX, int E>
@@ -594,13 +858,20 @@ template <int TX, int E>
 mm_status bwd_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   const int pieces = (a.cols + E - 1) / E;
   if (a.ty == TX) {
-    if (pieces <= 128) return bwd_rows_form<TX, E, 128, 1>(a, 8, ctx);
-    if (pieces <= 256) return bwd_rows_form<TX, E, 256, 1>(a, 4, ctx);
-    if (pieces <= 512) return bwd_rows_form<TX, E, 256, 2>(a, 3, ctx);
-    if (pieces <= 1024) return bwd_rows_form<TX, E, 512, 2>(a, 2, ctx);
-    if (pieces <= 2048) return bwd_rows_form<TX, E, 1024, 2>(a, 1, ctx);
-    if constexpr (E == 1)
-      if (pieces <= 8192) return bwd_rows_form<TX, E, 1024, 8>(a, 1, ctx);
+    if (pieces <= 32) return bwd_warps_form<TX, E, 1>(a, ctx);
+    if (pieces <= 64) return bwd_warps_form<TX, E, 2>(a, ctx);
+    if (pieces <= 128) return bwd_warps_form<TX, E, 4>(a, ctx);
+    if constexpr (E > 1) {
+      if (pieces <= 256) return bwd_ring_form<TX, 256, 1>(a, 4, ctx);
+      if (pieces <= 512) return bwd_ring_form<TX, 256, 2>(a, 3, ctx);
+      if (pieces <= 1024) return bwd_ring_form<TX, 512, 2>(a, 2, ctx);
+      if (pieces <= 2048) return bwd_ring_form<TX, 512, 4>(a, 1, ctx);
+    } else {
+      if (pieces <= 1024) return bwd_elements_form<TX, 256, 4>(a, 4, ctx);
+      if (pieces <= 2048) return bwd_elements_form<TX, 256, 8>(a, 3, ctx);
+      if (pieces <= 4096) return bwd_elements_form<TX, 512, 8>(a, 2, ctx);
+      if (pieces <= 8192) return bwd_elements_form<TX, 512, 16>(a, 1, ctx);
+    }
   }
   return bwd_long_form<TX, E>(a, ctx);
 }
@@ -614,7 +885,7 @@ mm_status bwd_type(const NormBwdArgs &a, LaunchCtx &ctx) {
   al.operand(a.h, a.ldh, a.rows, type_size(a.tx));
   al.operand(a.weight, 0, 1, type_size(a.tw));
   al.operand(a.dx, a.lddx, a.rows, type_size(a.tx));
-  constexpr int most = 16 / sizeof(typename Elem<TX>::T);
+  constexpr int most = 16 / bytes_of(TX);
   return al.elements(most) == most ? bwd_form<TX, most>(a, ctx) : bwd_form<TX, 1>(a, ctx);
 }
 
