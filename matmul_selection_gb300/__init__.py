@@ -121,10 +121,12 @@ EXPORTED = tuple(_sig)
 def _ptr(x):
     if x is None:
         return None
+    try:  # torch tensors first: the common case, and the one that is called most
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if hasattr(x, "ctypes"):  # numpy array (host entry point)
         return x.ctypes.data
     raise TypeError(f"cannot take the address of {type(x)}")
@@ -138,11 +140,18 @@ def _stream(s):
     return s.cuda_stream  # torch.cuda.Stream
 
 
+_dtypes_of = {}  # (a, b, c) -> the struct, passed by value
+
+
 def _dt(dt):
     if isinstance(dt, mm_dtypes):
         return dt
-    a, b, c = dt
-    return mm_dtypes(a, b, c)
+    dt = tuple(dt)
+    got = _dtypes_of.get(dt)
+    if got is None:
+        a, b, c = dt
+        got = _dtypes_of[dt] = mm_dtypes(a, b, c)
+    return got
 
 
 def _layout(layout):

@@ -750,33 +750,35 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_cols_kernel(const NormBwdArgs
   if (partial) store_piece<MM_F32>(partial, (int64_t)blockIdx.y * ((a.cols + 3) / 4 * 4) + j, dw);
 }
 
-// dweight: the parts of each column added in their order, by runs: thread y of
-// eight adds every eighth part, then the eight sums are added.
-__global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float *partial, int parts, int cols, void *dweight,
-                                                              int tw) {
+// dweight: the parts of each column added in a fixed order: thread y of 32 adds
+// every 32nd part, eight loads in flight, then the 32 sums are added in order.
+__global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float *partial, int parts, int cols,
+                                                               void *dweight, int tw) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float sh[8][33];
+  __shared__ float sh[32][33];
   const int c = threadIdx.x & 31, y = threadIdx.x >> 5, j = (int)blockIdx.x * 32 + c;
-  const int64_t ld = (cols + 3) / 4 * 4;
+  const int64_t ld = partial_ld(cols);
   float s = 0.f;
-  if (j < cols) {
-    int q = y;
-    for (; q + 24 < parts; q += 32) {
-      float v[4];
+  if (j < cols)
+    for (int q = y; q < parts; q += 8 * 32) {
+      float v[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = partial[(int64_t)(q + 8 * k) * ld + j];
+      for (int k = 0; k < 8; ++k) v[k] = q + 32 * k < parts ? partial[(int64_t)(q + 32 * k) * ld + j] : 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s += v[k];
+      for (int k = 0; k < 8; ++k) s += v[k];
     }
-    for (; q < parts; q += 8) s += partial[(int64_t)q * ld + j];
-  }
   sh[y][c] = s;
   __syncthreads();
-  if (y == 0 && j < cols) {
+  if (y < 4) {  // four warps, eight columns each: lane (column, quarter of the sums)
+    const int col = y * 8 + (c & 7), part = c >> 3;
+    float v = 0.f;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += sh[k][c];
-    store_value(dweight, tw, j, s);
+    for (int k = 0; k < 8; ++k) v += sh[part * 8 + k][col];
+    v += __shfl_down_sync(0xffffffffu, v, 16);
+    v += __shfl_down_sync(0xffffffffu, v, 8);
+    const int jj = (int)blockIdx.x * 32 + col;
+    if (c < 8 && jj < cols) store_value(dweight, tw, jj, v);
   }
 }
 
@@ -789,7 +791,7 @@ mm_status partial_space(const NormBwdArgs &a, int64_t parts, size_t more, Launch
 }
 
 mm_status add_parts(const NormBwdArgs &a, const float *partial, int parts, LaunchCtx &ctx) {
-  return launch(rmsnorm_dweight_kernel, (a.cols + 31) / 32, 256, ctx, "rmsnorm_backward launch (dweight)", partial,
+  return launch(rmsnorm_dweight_kernel, (a.cols + 31) / 32, 1024, ctx, "rmsnorm_backward launch (dweight)", partial,
                 parts, a.cols, a.dweight, a.tw);
 }
 
