@@ -112,6 +112,32 @@ __device__ __forceinline__ void load_piece(const void *p, int t, int64_t i, floa
   else if (t == MM_F16) load_piece<MM_F16>(p, i, out);
   else load_piece<MM_F32>(p, i, out);
 }
+// N pieces `step` elements apart, those below `n`, the others zeros.  The type is
+// looked at once, outside the loop: looked at a piece, with its conversion in the
+// branch, each load was waited for before the next was issued.
+template <int TX, int E, int N>
+__device__ __forceinline__ void load_pieces(const void *p, int64_t i, int64_t step, int n, float (&out)[N][E]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (k < n) {
+      load_piece<TX>(p, i + k * step, out[k]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) out[k][e] = 0.f;
+    }
+  }
+}
+template <int E, int N>
+__device__ __forceinline__ void load_pieces(const void *p, int t, int64_t i, int64_t step, int n,
+                                            float (&out)[N][E]) {
+  if (t == MM_BF16) load_pieces<MM_BF16>(p, i, step, n, out);
+  else if (t == MM_F16) load_pieces<MM_F16>(p, i, step, n, out);
+  else load_pieces<MM_F32>(p, i, step, n, out);
+}
+// How many of the pieces i, i + step, ... start below `end`.
+__device__ __forceinline__ int pieces_below(int64_t i, int64_t step, int64_t end) {
+  return i < end ? (int)((end - i + step - 1) / step) : 0;
+}
 template <int E>
 __device__ __forceinline__ void store_piece(void *p, int t, int64_t i, const float (&v)[E]) {
   if (t == MM_BF16) {
@@ -197,40 +223,18 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_rows_kernel(const N
   const int t = threadIdx.x % T;
   const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / T;
   if (T < 256 && r >= a.rows) return;  // (T = 32: no barrier below)
-  float h[V][E];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int j = (v * T + t) * E;
-    if (j < a.cols) {
-      load_piece<TX>(a.x, r * a.ldx + j, h[v]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) h[v][e] = 0.f;
-    }
-  }
+  const int n = max(0, (a.cols - t * E + T * E - 1) / (T * E));  // this thread's pieces
+  float h[V][E], w[V][E];
+  load_pieces<TX>(a.x, r * a.ldx + t * E, T * E, n, h);
   if (a.residual) {
     float res[V][E];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = (v * T + t) * E;
-      if (j < a.cols) {
-        load_piece<TX>(a.residual, r * a.ldr + j, res[v]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) res[v][e] = 0.f;
-      }
-    }
+    load_pieces<TX>(a.residual, r * a.ldr + t * E, T * E, n, res);
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int e = 0; e < E; ++e) h[v][e] += res[v][e];
   }
-  float w[V][E];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int j = (v * T + t) * E;
-    if (j < a.cols) load_piece(a.weight, a.tw, j, w[v]);
-  }
+  load_pieces(a.weight, a.tw, t * E, T * E, n, w);
   float ss = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -295,25 +299,23 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
   pdl_wait();
   __shared__ float sh[64];
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    constexpr int U = E == 1 ? 4 : 2;  // pieces in flight
     float ss = 0.f;
     uint32_t big = 0;
-    for (int j = threadIdx.x * E; j < a.cols; j += 1024 * E) {
-      float h[E];
-      load_piece<TX>(a.x, r * a.ldx + j, h);
-      if (a.residual) {
-        float s[E];
-        load_piece<TX>(a.residual, r * a.ldr + j, s);
+    for (int j0 = threadIdx.x * E; j0 < a.cols; j0 += U * 1024 * E) {
+      const int n = pieces_below(j0, 1024 * E, a.cols);
+      float h[U][E], s[U][E] = {}, w[U][E];
+      load_pieces<TX>(a.x, r * a.ldx + j0, 1024 * E, n, h);
+      if (a.residual) load_pieces<TX>(a.residual, r * a.ldr + j0, 1024 * E, n, s);
+      if (a.scale) load_pieces(a.weight, a.tw, j0, 1024 * E, n, w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] += s[e];
-      }
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < E; ++e) ss += h[e] * h[e];
-      if (a.scale) {
-        float w[E];
-        load_piece(a.weight, a.tw, j, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) big = max(big, __float_as_uint(fabsf(h[e] * w[e])));
-      }
+        for (int e = 0; e < E; ++e) {
+          const float x = h[u][e] + s[u][e];
+          ss += x * x;
+          if (a.scale) big = max(big, __float_as_uint(fabsf(x * w[u][e])));
+        }
     }
     __syncthreads();  // the previous row's sums have been read
     row_sum_max<1024>(ss, big, sh);
@@ -325,23 +327,26 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
       if (threadIdx.x == 0) a.scale[r] = scale;
     }
     if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
-    for (int j = threadIdx.x * E; j < a.cols; j += 1024 * E) {
-      float h[E], w[E];
-      load_piece<TX>(a.x, r * a.ldx + j, h);
-      if (a.residual) {
-        float s[E];
-        load_piece<TX>(a.residual, r * a.ldr + j, s);
+    for (int j0 = threadIdx.x * E; j0 < a.cols; j0 += U * 1024 * E) {
+      const int n = pieces_below(j0, 1024 * E, a.cols);
+      float h[U][E], s[U][E] = {}, w[U][E];
+      load_pieces<TX>(a.x, r * a.ldx + j0, 1024 * E, n, h);
+      if (a.residual) load_pieces<TX>(a.residual, r * a.ldr + j0, 1024 * E, n, s);
+      load_pieces(a.weight, a.tw, j0, 1024 * E, n, w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] += s[e];
-      }
-      load_piece(a.weight, a.tw, j, w);
-      if (a.h) store_piece<TX>(a.h, r * a.ldh + j, h);
+      for (int u = 0; u < U; ++u)
+        if (u < n) {
+          const int j = j0 + u * 1024 * E;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        h[e] = h[e] * rstd * w[e];
-        if (a.scale) h[e] *= inv;
-      }
-      store_piece(a.y, a.ty, r * a.ldy + j, h);
+          for (int e = 0; e < E; ++e) h[u][e] += s[u][e];
+          if (a.h) store_piece<TX>(a.h, r * a.ldh + j, h[u]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            h[u][e] = h[u][e] * rstd * w[u][e];
+            if (a.scale) h[u][e] *= inv;
+          }
+          store_piece(a.y, a.ty, r * a.ldy + j, h[u]);
+        }
     }
   }
 }
@@ -459,14 +464,8 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_warps_kernel(const NormBwdArg
   pdl_wait();
   __shared__ float sums[8][32 * V * E];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float w[V][E], dw[V][E];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int j = (v * 32 + lane) * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) w[v][e] = dw[v][e] = 0.f;
-    if (j < a.cols) load_piece(a.weight, a.tw, j, w[v]);
-  }
+  float w[V][E], dw[V][E] = {};
+  load_pieces(a.weight, a.tw, lane * E, 32 * E, max(0, (a.cols - lane * E + 32 * E - 1) / (32 * E)), w);
   const float per_col = 1.f / (float)a.cols;
   for (int64_t r = (int64_t)blockIdx.x * 8 + warp; r < a.rows; r += (int64_t)gridDim.x * 8) {
     P dy[V], h[V], dh[V];
@@ -546,11 +545,8 @@ __global__ void __launch_bounds__(T) rmsnorm_bwd_ring_kernel(const NormBwdArgs a
   if (t == 0)
     for (int s = 0; s < stages; ++s)
       if (blockIdx.x + (int64_t)s * gridDim.x < a.rows) fill(blockIdx.x + (int64_t)s * gridDim.x, s);
-  float dw[V][E];
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int e = 0; e < E; ++e) dw[v][e] = 0.f;
+  float w[V][E], dw[V][E] = {};
+  load_pieces(a.weight, a.tw, t * E, T * E, max(0, (a.cols - t * E + T * E - 1) / (T * E)), w);
   const float per_col = 1.f / (float)a.cols;
   int s = 0, side = 0;
   uint32_t phase = 0;
@@ -563,11 +559,7 @@ __global__ void __launch_bounds__(T) rmsnorm_bwd_ring_kernel(const NormBwdArgs a
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = v * T + t;
-      if (i * E < a.cols) {
-        float w[E];
-        load_piece(a.weight, a.tw, i * E, w);
-        BwdPiece<TX, E>::sums(P::load(dy + i * 16), P::load(h + i * 16), w, dot, ss);
-      }
+      if (i * E < a.cols) BwdPiece<TX, E>::sums(P::load(dy + i * 16), P::load(h + i * 16), w[v], dot, ss);
     }
     // two sets of shared sums in turn: one barrier a row
     dot = row_sum<T>(dot, sh[side]);
@@ -582,11 +574,10 @@ __global__ void __launch_bounds__(T) rmsnorm_bwd_ring_kernel(const NormBwdArgs a
     for (int v = 0; v < V; ++v) {
       const int i = v * T + t;
       if (i * E < a.cols) {
-        float w[E], dx[E];
-        load_piece(a.weight, a.tw, i * E, w);
+        float dx[E];
         P d;
         if (a.dh) d = P::load(dh + i * 16);
-        BwdPiece<TX, E>::outputs(P::load(dy + i * 16), P::load(h + i * 16), a.dh ? &d : nullptr, w, rs, c, dx, dw[v]);
+        BwdPiece<TX, E>::outputs(P::load(dy + i * 16), P::load(h + i * 16), a.dh ? &d : nullptr, w[v], rs, c, dx, dw[v]);
         store_piece<TX>(a.dx, r * a.lddx + i * E, dx);
       }
     }
@@ -603,71 +594,54 @@ __global__ void __launch_bounds__(T) rmsnorm_bwd_ring_kernel(const NormBwdArgs a
     }
 }
 
-// Rows that start anywhere: element by element, the row in registers, the next
-// row's loads issued before this row's sums are waited for.
+// Rows that start anywhere: element by element, the row and the weight in
+// registers, two blocks an SM.
 template <int TX, int T, int V>
-__global__ void __launch_bounds__(T) rmsnorm_bwd_elements_kernel(const NormBwdArgs a, float *partial) {
+__global__ void __launch_bounds__(T, 1024 / T) rmsnorm_bwd_elements_kernel(const NormBwdArgs a, float *partial) {
   using P = Piece<TX, 1>;
   pdl_launch_dependents();
   pdl_wait();
   __shared__ float sh[2][2 * (T / 32)];
   const int t = threadIdx.x;
-  float dw[V][1];
-#pragma unroll
-  for (int v = 0; v < V; ++v) dw[v][0] = 0.f;
-  struct Row {
-    P dy[V], h[V], dh[V];
-  };
-  auto load = [&](int64_t r, Row &x) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = v * T + t;
-      if (j < a.cols) {
-        x.dy[v] = P::load(at<TX>(a.dy, r * a.lddy + j));
-        x.h[v] = P::load(at<TX>(a.h, r * a.ldh + j));
-        if (a.dh) x.dh[v] = P::load(at<TX>(a.dh, r * a.lddh + j));
-      }
-    }
-  };
+  const int n = max(0, (a.cols - t + T - 1) / T);  // this thread's elements
+  float w[V][1], dw[V][1] = {};
+  load_pieces(a.weight, a.tw, t, T, n, w);
   const float per_col = 1.f / (float)a.cols;
-  Row next;
-  if (blockIdx.x < a.rows) load(blockIdx.x, next);
   int side = 0;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const Row cur = next;
-    if (r + gridDim.x < a.rows) load(r + gridDim.x, next);
-    const float given = a.rstd ? a.rstd[r] : 0.f;
+    P dy[V], h[V], dh[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v < n) {
+        dy[v] = P::load(at<TX>(a.dy, r * a.lddy + v * T + t));
+        h[v] = P::load(at<TX>(a.h, r * a.ldh + v * T + t));
+      }
+    if (a.dh)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v < n) dh[v] = P::load(at<TX>(a.dh, r * a.lddh + v * T + t));
+    float rs = a.rstd ? a.rstd[r] : 0.f;
     float dot = 0.f, ss = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = v * T + t;
-      if (j < a.cols) {
-        const float w[1] = {load_value(a.weight, a.tw, j)};
-        BwdPiece<TX, 1>::sums(cur.dy[v], cur.h[v], w, dot, ss);
-      }
-    }
+    for (int v = 0; v < V; ++v)
+      if (v < n) BwdPiece<TX, 1>::sums(dy[v], h[v], w[v], dot, ss);
+    // two sets of shared sums in turn: one barrier a row
     dot = row_sum<T>(dot, sh[side]);
-    float rs = given;
     if (!a.rstd) rs = 1.f / sqrtf(row_sum<T>(ss, sh[side] + T / 32) / (float)a.cols + a.eps);
     side ^= 1;
     const float c = dot * per_col * rs * rs;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = v * T + t;
-      if (j < a.cols) {
-        const float w[1] = {load_value(a.weight, a.tw, j)};
+    for (int v = 0; v < V; ++v)
+      if (v < n) {
         float dx[1];
-        BwdPiece<TX, 1>::outputs(cur.dy[v], cur.h[v], a.dh ? &cur.dh[v] : nullptr, w, rs, c, dx, dw[v]);
-        store_piece<TX>(a.dx, r * a.lddx + j, dx);
+        BwdPiece<TX, 1>::outputs(dy[v], h[v], a.dh ? &dh[v] : nullptr, w[v], rs, c, dx, dw[v]);
+        store_piece<TX>(a.dx, r * a.lddx + v * T + t, dx);
       }
-    }
   }
   if (partial)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = v * T + t;
-      if (j < a.cols) partial[blockIdx.x * partial_ld(a.cols) + j] = dw[v][0];
-    }
+    for (int v = 0; v < V; ++v)
+      if (v < n) partial[blockIdx.x * partial_ld(a.cols) + v * T + t] = dw[v][0];
 }
 
 // Longer rows, and dy of another type than h: 1 / rms and the mean of g h of each row (two
@@ -682,17 +656,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_stats_kernel(const NormBwdAr
     constexpr int U = E == 1 ? 4 : 2;  // pieces in flight
     for (int j0 = threadIdx.x * E; j0 < a.cols; j0 += U * 1024 * E) {
       float dy[U][E], h[U][E], w[U][E];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * 1024 * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) dy[u][e] = h[u][e] = w[u][e] = 0.f;
-        if (j < a.cols) {
-          load_piece(a.dy, a.ty, r * a.lddy + j, dy[u]);
-          load_piece<TX>(a.h, r * a.ldh + j, h[u]);
-          load_piece(a.weight, a.tw, j, w[u]);
-        }
-      }
+      const int n = pieces_below(j0, 1024 * E, a.cols);
+      load_pieces(a.dy, a.ty, r * a.lddy + j0, 1024 * E, n, dy);
+      load_pieces<TX>(a.h, r * a.ldh + j0, 1024 * E, n, h);
+      load_pieces(a.weight, a.tw, j0, 1024 * E, n, w);
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -723,16 +690,13 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_cols_kernel(const NormBwdArgs
   for (int64_t r0 = blockIdx.y; r0 < a.rows; r0 += (int64_t)U * gridDim.y) {
     float dy[U][E], h[U][E], dh[U][E] = {};
     float2 s[U];
+    const int n = pieces_below(r0, gridDim.y, a.rows);
+    load_pieces(a.dy, a.ty, r0 * a.lddy + j, gridDim.y * a.lddy, n, dy);
+    load_pieces<TX>(a.h, r0 * a.ldh + j, gridDim.y * a.ldh, n, h);
+    if (a.dh) load_pieces<TX>(a.dh, r0 * a.lddh + j, gridDim.y * a.lddh, n, dh);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + (int64_t)u * gridDim.y;
-      if (r < a.rows) {
-        load_piece(a.dy, a.ty, r * a.lddy + j, dy[u]);
-        load_piece<TX>(a.h, r * a.ldh + j, h[u]);
-        if (a.dh) load_piece<TX>(a.dh, r * a.lddh + j, dh[u]);
-        s[u] = stats[r];
-      }
-    }
+    for (int u = 0; u < U; ++u)
+      if (u < n) s[u] = stats[r0 + (int64_t)u * gridDim.y];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = r0 + (int64_t)u * gridDim.y;
@@ -811,8 +775,16 @@ mm_status bwd_blocks(const NormBwdArgs &a, K kern, int64_t blocks, int threads, 
 
 template <int TX, int E, int V>
 mm_status bwd_warps_form(const NormBwdArgs &a, LaunchCtx &ctx) {
-  const int64_t blocks = std::min<int64_t>((a.rows + 7) / 8, 3 * ctx.dev->info.sms);
-  return bwd_blocks(a, rmsnorm_bwd_warps_kernel<TX, E, V>, blocks, 256, 0, ctx);
+  // as many blocks as are resident at once: one more would be a second, nearly
+  // empty round over its share of the rows (65536 x 512 bf16: 2 an SM 50 us, 3 60)
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  static int per_sm = 0;
+  auto kern = rmsnorm_bwd_warps_kernel<TX, E, V>;
+  std::call_once(once, [&] { err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 256, 0); });
+  if (err != cudaSuccess) return cuda_error(err, "rmsnorm_backward set-up");
+  const int64_t blocks = std::min<int64_t>((a.rows + 7) / 8, (int64_t)std::max(1, per_sm) * ctx.dev->info.sms);
+  return bwd_blocks(a, kern, blocks, 256, 0, ctx);
 }
 
 constexpr size_t kRingBytes = 208 << 10;  // of an SM's shared memory
@@ -828,6 +800,7 @@ mm_status bwd_ring_form(const NormBwdArgs &a, int per_sm, LaunchCtx &ctx) {
   if (err != cudaSuccess) return cuda_error(err, "rmsnorm_backward set-up");
   const size_t stage = (size_t)(a.dh ? 3 : 2) * a.cols * bytes_of(TX);
   const int stages = (int)std::min<size_t>(kMaxRing, kRingBytes / per_sm / stage);
+  if (stages < 2) return set_error(MM_ERR_UNSUPPORTED, "rmsnorm_backward: no two rows fit the ring");
   const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)per_sm * ctx.dev->info.sms);
   return bwd_blocks(a, kern, blocks, T, stages * stage, ctx, stages, ctx.dev->d_err + kOperatorErrorWord);
 }
@@ -864,15 +837,20 @@ mm_status bwd_form(const NormBwdArgs &a, LaunchCtx &ctx) {
     if (pieces <= 64) return bwd_warps_form<TX, E, 2>(a, ctx);
     if (pieces <= 128) return bwd_warps_form<TX, E, 4>(a, ctx);
     if constexpr (E > 1) {
-      if (pieces <= 256) return bwd_ring_form<TX, 256, 1>(a, 4, ctx);
-      if (pieces <= 512) return bwd_ring_form<TX, 256, 2>(a, 3, ctx);
+      // Threads and blocks an SM, measured (bf16, us for 33.5 M values in rows of
+      // 2048 / 4096 / 8192): 256 x 5 52.6 (x 4 66, x 3 76) / 512 x 2 50.6 (256 x
+      // 3 56; 512 x 3, of which two fit, 72) / 512 x 2 53 (1024 x 1 55)
+      if (pieces <= 256) return bwd_ring_form<TX, 256, 1>(a, 5, ctx);
+      if (pieces <= 512) return bwd_ring_form<TX, 512, 1>(a, 2, ctx);
       if (pieces <= 1024) return bwd_ring_form<TX, 512, 2>(a, 2, ctx);
-      if (pieces <= 2048) return bwd_ring_form<TX, 512, 4>(a, 1, ctx);
+      if (pieces <= 2048) return bwd_ring_form<TX, 1024, 2>(a, 1, ctx);
     } else {
+      if (pieces <= 512) return bwd_elements_form<TX, 128, 4>(a, 8, ctx);
       if (pieces <= 1024) return bwd_elements_form<TX, 256, 4>(a, 4, ctx);
-      if (pieces <= 2048) return bwd_elements_form<TX, 256, 8>(a, 3, ctx);
+      if (pieces <= 2048) return bwd_elements_form<TX, 256, 8>(a, 4, ctx);
       if (pieces <= 4096) return bwd_elements_form<TX, 512, 8>(a, 2, ctx);
-      if (pieces <= 8192) return bwd_elements_form<TX, 512, 16>(a, 1, ctx);
+      if (pieces <= 5120) return bwd_elements_form<TX, 512, 10>(a, 2, ctx);
+      if (pieces <= 8192) return bwd_elements_form<TX, 1024, 8>(a, 1, ctx);
     }
   }
   return bwd_long_form<TX, E>(a, ctx);
