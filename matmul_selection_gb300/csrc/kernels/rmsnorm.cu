@@ -518,8 +518,8 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_warps_kernel(const NormBwdArg
 // refilled after the next row's barrier, which every thread reaches only when
 // it is done with the row before.
 constexpr int kMaxRing = 8, kErrRing = 0xb01;
-template <int TX, int T, int V>
-__global__ void __launch_bounds__(T) rmsnorm_bwd_ring_kernel(const NormBwdArgs a, float *partial, int stages,
+template <int TX, int T, int V, int PER_SM>
+__global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormBwdArgs a, float *partial, int stages,
                                                               int *err) {
   constexpr int E = 16 / bytes_of(TX);
   using P = Piece<TX, E>;
@@ -789,19 +789,19 @@ mm_status bwd_warps_form(const NormBwdArgs &a, LaunchCtx &ctx) {
 
 constexpr size_t kRingBytes = 208 << 10;  // of an SM's shared memory
 
-template <int TX, int T, int V>
-mm_status bwd_ring_form(const NormBwdArgs &a, int per_sm, LaunchCtx &ctx) {
+template <int TX, int T, int V, int PER_SM>
+mm_status bwd_ring_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
-  auto kern = rmsnorm_bwd_ring_kernel<TX, T, V>;
+  auto kern = rmsnorm_bwd_ring_kernel<TX, T, V, PER_SM>;
   std::call_once(once, [&] {
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
   });
   if (err != cudaSuccess) return cuda_error(err, "rmsnorm_backward set-up");
   const size_t stage = (size_t)(a.dh ? 3 : 2) * a.cols * bytes_of(TX);
-  const int stages = (int)std::min<size_t>(kMaxRing, kRingBytes / per_sm / stage);
+  const int stages = (int)std::min<size_t>(kMaxRing, kRingBytes / PER_SM / stage);
   if (stages < 2) return set_error(MM_ERR_UNSUPPORTED, "rmsnorm_backward: no two rows fit the ring");
-  const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)per_sm * ctx.dev->info.sms);
+  const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)PER_SM * ctx.dev->info.sms);
   return bwd_blocks(a, kern, blocks, T, stages * stage, ctx, stages, ctx.dev->d_err + kOperatorErrorWord);
 }
 
@@ -840,10 +840,10 @@ mm_status bwd_form(const NormBwdArgs &a, LaunchCtx &ctx) {
       // Threads and blocks an SM, measured (bf16, us for 33.5 M values in rows of
       // 2048 / 4096 / 8192): 256 x 5 52.6 (x 4 66, x 3 76) / 512 x 2 50.6 (256 x
       // 3 56; 512 x 3, of which two fit, 72) / 512 x 2 53 (1024 x 1 55)
-      if (pieces <= 256) return bwd_ring_form<TX, 256, 1>(a, 5, ctx);
-      if (pieces <= 512) return bwd_ring_form<TX, 512, 1>(a, 2, ctx);
-      if (pieces <= 1024) return bwd_ring_form<TX, 512, 2>(a, 2, ctx);
-      if (pieces <= 2048) return bwd_ring_form<TX, 1024, 2>(a, 1, ctx);
+      if (pieces <= 256) return bwd_ring_form<TX, 256, 1, 5>(a, ctx);
+      if (pieces <= 512) return bwd_ring_form<TX, 512, 1, 2>(a, ctx);
+      if (pieces <= 1024) return bwd_ring_form<TX, 512, 2, 2>(a, ctx);
+      if (pieces <= 2048) return bwd_ring_form<TX, 1024, 2, 1>(a, ctx);
     } else {
       if (pieces <= 512) return bwd_elements_form<TX, 128, 4>(a, 8, ctx);
       if (pieces <= 1024) return bwd_elements_form<TX, 256, 4>(a, 4, ctx);
