@@ -7,11 +7,16 @@ objects with ``data_ptr()`` (torch tensors); ``stream`` accepts an int
 handle, a ``torch.cuda.Stream`` or None (legacy default stream).
 
 Importing the package loads the library and fails loudly when it has not
-been built (``python matmul_selection_gb300/build.py``).
+been built (``python matmul_selection_gb300/build.py``).  The operators that a
+model calls once a layer and token go through a small extension module instead
+of ctypes (``csrc/binding/fastcall.cpp``): the same C functions, the arguments
+converted in C.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -64,6 +69,18 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
                       "`python matmul_selection_gb300/build.py` (needs nvcc)")
 _lib = ctypes.CDLL(LIB_PATH)
+
+
+def _load_fastcall():
+    path = os.path.join(_HERE, "_build", "mm_fastcall.so")
+    loader = importlib.machinery.ExtensionFileLoader("mm_fastcall", path)
+    module = importlib.util.module_from_spec(
+        importlib.util.spec_from_file_location("mm_fastcall", path, loader=loader))
+    loader.exec_module(module)
+    return module
+
+
+_fast = _load_fastcall()
 
 _i64, _i32, _vp, _cp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_char_p
 _P32 = ctypes.POINTER(ctypes.c_int32)
@@ -332,33 +349,42 @@ def mm_splitk_gemm_noalloc_status(stream=None):
     return _lib.mm_splitk_gemm_noalloc_status(_stream(stream))
 
 
+def _types(dt):
+    return (dt.a, dt.b, dt.c) if isinstance(dt, mm_dtypes) else tuple(dt)
+
+
 def mm_rmsnorm(x, residual, weight, h, y, scale, rstd, rows, cols, ldx, ldr, ldh, ldy, dtypes, eps,
                stream=None):
     """h = x + residual, y = h / rms(h) * weight; y in 8 bits takes `scale`."""
-    return _lib.mm_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y), _ptr(scale),
-                           _ptr(rstd), rows, cols, ldx, ldr, ldh, ldy, _dt(dtypes), eps,
-                           _stream(stream))
+    if type(dtypes) is not tuple:
+        dtypes = _types(dtypes)
+    return _fast.rmsnorm(x, residual, weight, h, y, scale, rstd, rows, cols, ldx, ldr, ldh, ldy,
+                         dtypes, eps, stream)
 
 
 def mm_rmsnorm_backward(dy, dh, h, weight, rstd, dx, dweight, rows, cols, lddy, lddh, ldh, lddx,
                         dtypes, eps, stream=None):
     """The gradients of mm_rmsnorm to its input and its weight."""
-    return _lib.mm_rmsnorm_backward(_ptr(dy), _ptr(dh), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dx),
-                                    _ptr(dweight), rows, cols, lddy, lddh, ldh, lddx, _dt(dtypes),
-                                    eps, _stream(stream))
+    if type(dtypes) is not tuple:
+        dtypes = _types(dtypes)
+    return _fast.rmsnorm_backward(dy, dh, h, weight, rstd, dx, dweight, rows, cols, lddy, lddh, ldh,
+                                  lddx, dtypes, eps, stream)
 
 
 def mm_gemm_w4(A, codes, scales, zeros, out, M, N, K, lda, ldw, lds, ldc, group, dtypes,
                stream=None):
     """out = A . W^T, W in 4-bit codes with group scales and zero points."""
-    return _lib.mm_gemm_w4(_ptr(A), _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(out), M, N, K,
-                           lda, ldw, lds, ldc, group, _dt(dtypes), _stream(stream))
+    if type(dtypes) is not tuple:
+        dtypes = _types(dtypes)
+    return _fast.gemm_w4(A, codes, scales, zeros, out, M, N, K, lda, ldw, lds, ldc, group, dtypes,
+                         stream)
 
 
 def mm_gemm_q8(A, B, scale_a, scale_b, out, M, N, K, lda, ldb, ldc, dtypes, stream=None):
     """out = A . B^T of e4m3 operands with row scales of A and of B."""
-    return _lib.mm_gemm_q8(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), _ptr(out), M, N, K, lda,
-                           ldb, ldc, _dt(dtypes), _stream(stream))
+    if type(dtypes) is not tuple:
+        dtypes = _types(dtypes)
+    return _fast.gemm_q8(A, B, scale_a, scale_b, out, M, N, K, lda, ldb, ldc, dtypes, stream)
 
 
 def mm_operator_status(stream=None):

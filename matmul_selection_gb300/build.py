@@ -1,7 +1,8 @@
 """Build the library in-tree: nvcc for sm_103a, objects compiled in parallel.
 
-Produces ``matmul_selection_gb300/_build/libmm_gb300.so``.  Usable as
-``python matmul_selection_gb300/build.py``.
+Produces ``matmul_selection_gb300/_build/libmm_gb300.so`` and, linked to it,
+the Python module of the operators' calls, ``_build/mm_fastcall.so``.  Usable
+as ``python matmul_selection_gb300/build.py``.
 """
 from __future__ import annotations
 
@@ -11,12 +12,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmm_gb300.so")
+FASTCALL = os.path.join(BUILD, "mm_fastcall.so")
+FASTCALL_SRC = os.path.join(CSRC, "binding", "fastcall.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,7 +49,7 @@ def headers():
 
 def build_id() -> str:
     h = hashlib.sha1()
-    for p in sources() + headers():
+    for p in sources() + headers() + [FASTCALL_SRC]:
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode())
             h.update(f.read())
@@ -67,11 +71,22 @@ def _compile(src: str, obj: str, bid: str, verbose: bool) -> None:
         print(r.stderr, file=sys.stderr)
 
 
+def _compile_fastcall() -> None:
+    tmp = FASTCALL + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared",
+           "-I", sysconfig.get_paths()["include"], FASTCALL_SRC, "-o", tmp,
+           "-L", BUILD, "-l:libmm_gb300.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {FASTCALL_SRC}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FASTCALL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     bid = build_id()
     stamp = os.path.join(BUILD, "build_id")
-    if not force and os.path.exists(LIB) and os.path.exists(stamp):
+    if not force and os.path.exists(LIB) and os.path.exists(FASTCALL) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == bid:
                 return LIB
@@ -88,6 +103,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _compile_fastcall()
     with open(stamp, "w") as f:
         f.write(bid)
     return LIB

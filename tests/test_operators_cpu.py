@@ -98,3 +98,28 @@ def test_empty_calls_launch_nothing(call, args):
     before = mm.mm_get_stats()["launches"]
     assert call(**args) == mm.MM_OK
     assert mm.mm_get_stats()["launches"] == before
+
+
+def test_argument_forms():
+    """Types as a tuple, a list or the struct; addresses as numbers, None or
+    objects with data_ptr(); streams as numbers or objects with cuda_stream;
+    anything else is a TypeError, before any call."""
+    class Tensor:
+        def data_ptr(self):
+            return 0x1001
+
+    class Stream:
+        cuda_stream = 0
+
+    for dt in ((BF, BF, BF), [BF, BF, BF], mm.mm_dtypes(BF, BF, BF)):
+        assert norm(dt=dt, rows=0) == mm.MM_OK
+        assert norm(dt=dt, x=Tensor()) == BAD and "x not aligned" in mm.mm_last_error()
+    assert mm.mm_gemm_q8(None, None, None, None, None, 0, 1, 1, 1, 1, 1, (Q, Q, F), Stream()) == mm.MM_OK
+    assert mm.mm_gemm_q8(None, None, None, None, None, 0, 1, 1, 1, 1, 1, (Q, Q, F), stream=0) == mm.MM_OK
+    for bad in (lambda: norm(x="x"), lambda: norm(x=1.5), lambda: norm(rows="4"), lambda: norm(dt=(0, 0)),
+                lambda: norm(dt=("a", 0, 0)), lambda: norm(eps="x"), lambda: w4(group=1.5),
+                lambda: mm.mm_gemm_q8(None, None, None, None, None, 0, 1, 1, 1, 1, 1, (Q, Q, F), "stream")):
+        with pytest.raises((TypeError, AttributeError)):
+            bad()
+    with pytest.raises(OverflowError):
+        norm(rows=1 << 70)
