@@ -462,7 +462,12 @@ mm_status launch_gemm_q8(const Q8Args &in, LaunchCtx &ctx) {
   Q8Args a = in;
   mm_status st;
   if (a.K == 0) return write_zeros(a.out, a.ldc, a.M, a.N, a.tc, ctx);
-  if (a.M <= 16) return launch_gemv_q8(a, ctx);
+  // At most 8 rows of A and too few rows of weights to fill the SMs with tiles
+  // of 128: the GEMV form, whose tiles are of 16 to 64.  us, GEMV / swap: 1 x
+  // 4096 x 4096 5.4 / 6.5, 1 x 2048 x 16384 9.2 / 13.9, 4 x 6144 x 6144 10.6 /
+  // 10.4, 1 x 8192 x 8192 16.1 / 14.2, 1 x 16384 x 8192 29.0 / 23.5; 16 rows:
+  // 16 x 4096 x 4096 7.6 / 6.7.
+  if (a.M <= 8 && a.N <= 6144) return launch_gemv_q8(a, ctx);
   TmaRows ra{a.A, a.lda, a.M, a.K}, rb{a.B, a.ldb, a.N, a.K};
   if ((st = align_rows(ra, rb, ctx)) != MM_OK) return st;
   a.A = static_cast<const uint8_t *>(ra.p);

@@ -1,6 +1,6 @@
-// Products of at most 16 rows with quantised weights, both held [N][K]:
-//   4-bit  out[m, n] = sum_k A[m, k] s[n, k / group] (q[n, k] - z[n, k / group])
-//   e4m3   out[m, n] = scale_a[m] scale_b[n] sum_k A[m, k] B[n, k]
+// Products of few rows with quantised weights, held [N][K]:
+//   4-bit  (at most 16 rows) out[m, n] = sum_k A[m, k] s[n, k / group] (q[n, k] - z[n, k / group])
+//   e4m3   (at most 8) out[m, n] = scale_a[m] scale_b[n] sum_k A[m, k] B[n, k]
 // One pass over the weights, which is what bounds them.  A CTA of eight
 // computing warps owns R = 16 WR rows of the weights; WR warps side by side
 // take 16 rows each, and WK = 8 / WR of them take turns along K, a panel (128
@@ -177,12 +177,13 @@ __device__ __forceinline__ void panel_w4(const GemvParams &p, uint32_t wrow, uin
     const uint32_t rr = lane & 7, mat = lane >> 3;
     ldmatrix_x4(wrow + (((2 * c2 + (mat >> 1)) ^ rr) << 4), w);
     const int src = (lane & 28) | c2;
+    T z[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      T z[2];
+      if (TWO || h == 0)
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        z[r] = bits_as<T>(zeros ? __shfl_sync(0xffffffffu, zero[r][h % E], src) : kBias + 0x00080008u);
+        for (int r = 0; r < 2; ++r)
+          z[r] = bits_as<T>(zeros ? __shfl_sync(0xffffffffu, zero[r][h % E], src) : kBias + 0x00080008u);
       uint32_t a[2][4];  // row, pairs (0, 1), (2, 3), (4, 5), (6, 7)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -303,6 +304,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t stage0 = smem_u32(smem);
     const uint32_t wrow = stage0 + (uint32_t)(wk * R * 128) + (uint32_t)(wr * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
     const uint32_t xpan = stage0 + kWeightsB + (uint32_t)wk * XPANEL;
+    // a lane's row of A; past the last, the last once more (its columns of the
+    // product are not used, and lanes that read one address share the read)
+    const uint32_t xrow = xpan + (uint32_t)(min(lane >> 2, p.M - 1) * 512 + t * 16);
     ScaleCursor cursor = {};
     PanelScales next = {};
     if constexpr (W4) {
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (i * WK + wk < np) {
         const uint32_t off = after_wait((uint32_t)st * kStageB);
         if constexpr (W4)
-          panel_w4<F, MT, TWO>(p, wrow + off, xpan + off + (uint32_t)((lane >> 2) * 512 + t * 16), cur, acc);
+          panel_w4<F, MT, TWO>(p, wrow + off, xrow + off, cur, acc);
         else
           panel_e4m3<MT>(wrow + off, xpan + off, acc);
         before_release(acc);
@@ -387,10 +391,11 @@ mm_status run(const TmaRows &rx, const TmaRows &rw, int K, GemvParams p, LaunchC
 
 template <int F, bool TWO>
 mm_status run_rows(const TmaRows &rx, const TmaRows &rw, int K, const GemvParams &p, LaunchCtx &ctx) {
-  return p.M <= 2   ? run<F, 1, TWO>(rx, rw, K, p, ctx)
-         : p.M <= 4 ? run<F, 2, TWO>(rx, rw, K, p, ctx)
-         : p.M <= 8 ? run<F, 4, TWO>(rx, rw, K, p, ctx)
-                    : run<F, 8, TWO>(rx, rw, K, p, ctx);
+  if (p.M <= 2) return run<F, 1, TWO>(rx, rw, K, p, ctx);
+  if (p.M <= 4) return run<F, 2, TWO>(rx, rw, K, p, ctx);
+  if constexpr (F != FMT_E4M3)
+    if (p.M > 8) return run<F, 8, TWO>(rx, rw, K, p, ctx);
+  return run<F, 4, TWO>(rx, rw, K, p, ctx);
 }
 
 GemvParams gemv_params(void *out, int64_t ldc, int tc, int M, int N, LaunchCtx &ctx) {

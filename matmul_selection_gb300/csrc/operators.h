@@ -53,7 +53,7 @@ struct Q8Args {
 };
 mm_status launch_gemm_q8(const Q8Args &a, LaunchCtx &ctx);
 
-// Their forms for at most 16 rows of A (K > 0).
+// Their forms for at most 16 and at most 8 rows of A (K > 0).
 mm_status launch_gemv_w4(const W4Args &a, LaunchCtx &ctx);
 mm_status launch_gemv_q8(const Q8Args &a, LaunchCtx &ctx);
 
