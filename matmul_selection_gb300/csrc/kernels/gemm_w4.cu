@@ -39,20 +39,24 @@ constexpr int kErrCopy = 0x901, kErrMma = 0x902, kErrStore = 0x903, kErrDrain = 
 constexpr int kStoreWarp = 4, kStoreWarps = 8, kDequantWarp = 12;
 constexpr int kGroups = 4, kGroupWarps = 4, kDequantWarps = kGroups * kGroupWarps;
 constexpr int kTileThreads = 32 * (kDequantWarp + kDequantWarps);
-constexpr uint32_t kCodeStageB = 128 * 128;  // 256 codes (four stages) of 128 rows
+constexpr uint32_t kCodeStageB = 128 * 128;  // 256 codes (four blocks of 64) of 128 rows
 
 template <int BN>
 struct Tile {
-  static constexpr uint32_t kStageB = BN * 128;
-  static constexpr int kStages = BN == 256 ? 5 : BN == 128 ? 6 : 7;
-  static constexpr int kCodeStages = BN == 256 ? 3 : 4;
-  // the fp32 tile where K is split: beside the rings, or, for 256 rows, over them
-  static constexpr bool kOver = BN == 256;
+  // Blocks of 64 of K a stage: two, which halves what a stage costs the warps
+  // that hand it on, but for 256 rows, where the MMA of one takes longer.
+  static constexpr int kBlocks = BN == 256 ? 1 : 2;
+  static constexpr uint32_t kPanelB = BN * 128, kStageB = kBlocks * kPanelB;
+  static constexpr int kStages = BN >= 128 ? 5 : 6;
+  static constexpr int kCodeStages = BN >= 128 ? 3 : 4;
+  // the fp32 tile where K is split: beside the rings, or over them
+  static constexpr bool kOver = BN >= 128;
   static constexpr uint32_t kTileB = kOver ? 0 : BN * 512;
   static constexpr size_t kSmem = kStages * kStageB + kCodeStages * kCodeStageB + kTileB + 1024 + 512;
-  // TMEM: the accumulator, then the stages' weights, 32 columns each
-  static constexpr uint32_t kUsed = BN + 32 * kStages, kCols = kUsed <= 256 ? 256 : 512;
-  static_assert(kUsed <= 512 && kStages >= kGroups && kStages < 2 * kGroups, "TMEM; see dequant_blocks");
+  // TMEM: the accumulator, then the stages' weights, 32 columns a block
+  static constexpr uint32_t kUsed = BN + 32 * kBlocks * kStages, kCols = kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512, "TMEM");
+  static_assert(kStages >= kGroups && kStages <= 4 / kBlocks * (kCodeStages - 1) + 1, "see dequant_blocks");
   static_assert(!kOver || (size_t)BN * 512 <= kStages * kStageB, "the fp32 tile fits the ring");
 };
 
@@ -61,8 +65,7 @@ struct TileParams {
   int64_t ldc;
   int tc;
   int M, N;
-  int num_kb;       // blocks of 64 of K
-  int kb_per_rank;  // a multiple of 4 where K is split
+  int num_kb, kb_per_rank;  // blocks of 64 of K, multiples of 4
   int tiles_n, tiles;
   int *err;
   W4Scales w;
@@ -117,76 +120,83 @@ struct DequantRing {
   uint32_t cfull0, cempty0;  // the code stages' barriers
   uint32_t empty0, wfull0;   // a stage is free; its weights are written
   uint32_t weights;          // TMEM address of stage 0's weights
-  int cs = 0;
-  uint32_t cphase = 0;
-  int group;        // of this warp
-  int turn = 0;     // stages filled before this tile, modulo the groups
-  int stage;        // of the group's next fill
+  int group;                 // of this warp
+  int stage;                 // of the group's next fill
   uint32_t phase = 0;
+  uint32_t fills = 0;        // stages filled before this tile
 };
 
-// The weights of 128 rows from row n0, blocks [kb0, kb0 + nk), into TMEM: each
-// thread a row (its lane) of its group's blocks, those whose place in the ring
-// is the group's modulo 4.
-// A parity wait tells only adjacent phases apart: when a group waits for the
-// consumption of fill f - STAGES, its previous fill f - 4 needed that of
-// f - 4 - STAGES, which covers f - 2 STAGES only when STAGES >= 4.
-template <int TA, int STAGES, int CSTAGES>
+// The weights of 128 rows from row n0, blocks [kb0, kb0 + nk) (whole stages of
+// codes), into TMEM: each thread a row (its lane) of the stages whose place in
+// the ring is its group's modulo 4.
+// A parity wait tells only adjacent phases apart.  Operand ring: when a group
+// waits for the consumption of fill f - STAGES, its previous fill f - 4 needed
+// that of f - 4 - STAGES, which covers f - 2 STAGES as STAGES >= 4.  Codes: the
+// wait for a stage of codes follows that consumption, and the fill STAGES back
+// used the codes CSTAGES back, or later ones: those had landed.
+template <int TA, typename S>
 __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing &r, int n0, int kb0, int nk,
                                                volatile int *abort_flag) {
+  constexpr int B = S::kBlocks, PER = 4 / B;  // stages a stage of codes makes
   const int warp = (int)threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = (warp & 3) * 32 + lane;  // the TMEM lanes this warp may write
-  const int j = (r.group - r.turn) & (kGroups - 1);
+  const int j = (int)(((uint32_t)r.group - r.fills) % kGroups), part = j % PER;
   const uint32_t dst0 = r.weights + ((uint32_t)((warp & 3) * 32) << 16);
   const ScaleRow srow = scale_row(p.w, n0 + row);
   const bool two = p.w.group_shift == 5;  // a block of 64 spans two groups
   const uint8_t *crow = r.codes + row * 128;
-  const uint32_t at[2] = {(uint32_t)((2 * j) ^ (row & 7)) << 4, (uint32_t)((2 * j + 1) ^ (row & 7)) << 4};
-  RawScale next[2];
-  next[0] = load_raw_scale(p.w, srow, (kb0 + j) * 64);
-  next[1] = two ? load_raw_scale(p.w, srow, (kb0 + j) * 64 + 32) : next[0];
-  for (int i = j; i < nk + j; i += kGroups) {  // a stage of codes, of which this group takes block j
-    const RawScale cur[2] = {next[0], next[1]};
-    next[0] = load_raw_scale(p.w, srow, (kb0 + i + kGroups) * 64);
-    next[1] = two ? load_raw_scale(p.w, srow, (kb0 + i + kGroups) * 64 + 32) : next[0];
-    if (!warp_wait(r.cfull0 + 8 * r.cs, r.cphase, abort_flag, p.err, kErrDequant)) return false;
-    uint4 c[2];
+  const int ns = nk / B;
+  RawScale next[B][2];
+  auto load_scales = [&](int i) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) c[h] = *reinterpret_cast<const uint4 *>(crow + r.cs * kCodeStageB + at[h]);
-    const uint32_t cempty = r.cempty0 + 8 * r.cs;
-    if (++r.cs == CSTAGES) {
-      r.cs = 0;
-      r.cphase ^= 1;
+    for (int b = 0; b < B; ++b) {
+      const int k = (kb0 + i * B + b) * 64;
+      next[b][0] = load_raw_scale(p.w, srow, k);
+      next[b][1] = two ? load_raw_scale(p.w, srow, k + 32) : next[b][0];
     }
-    if (i >= nk) {  // the last stage of codes ends before this group's block
-      __syncwarp();
-      if (lane == 0) mbar_arrive(cempty);
-      break;
-    }
+  };
+  load_scales(j);
+  uint32_t c = (r.fills + (uint32_t)j) / PER;  // the stage of codes, over all tiles
+  for (int i = j; i < ns; i += kGroups, c += kGroups / PER) {
+    RawScale cur[B][2];
+#pragma unroll
+    for (int b = 0; b < B; ++b) cur[b][0] = next[b][0], cur[b][1] = next[b][1];
+    load_scales(i + kGroups);
     const int stage = r.stage;
     if (!warp_wait(r.empty0 + 8 * stage, r.phase ^ 1, abort_flag, p.err, kErrDequant)) return false;
-    if ((r.stage += kGroups) >= STAGES) {
-      r.stage -= STAGES;
+    if ((r.stage += kGroups) >= S::kStages) {
+      r.stage -= S::kStages;
       r.phase ^= 1;
     }
-    fence_after();
-    GroupScale<TA> g = group_scale<TA>(p, cur[0]);
+    const uint32_t cs = c % S::kCodeStages;
+    if (!warp_wait(r.cfull0 + 8 * cs, (c / S::kCodeStages) & 1u, abort_flag, p.err, kErrDequant)) return false;
+    uint4 q[2 * B];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h && two) g = group_scale<TA>(p, cur[1]);
-      uint32_t v[16];
-      if (p.split_scale) {
-        dequant8<TA>(c[h].x, g, true, v);
-        dequant8<TA>(c[h].y, g, true, v + 4);
-        dequant8<TA>(c[h].z, g, true, v + 8);
-        dequant8<TA>(c[h].w, g, true, v + 12);
-      } else {
-        dequant8<TA>(c[h].x, g, false, v);
-        dequant8<TA>(c[h].y, g, false, v + 4);
-        dequant8<TA>(c[h].z, g, false, v + 8);
-        dequant8<TA>(c[h].w, g, false, v + 12);
+    for (int h = 0; h < 2 * B; ++h)
+      q[h] = *reinterpret_cast<const uint4 *>(crow + cs * kCodeStageB +
+                                              ((uint32_t)((part * 2 * B + h) ^ (row & 7)) << 4));
+    fence_after();
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      GroupScale<TA> g = group_scale<TA>(p, cur[b][0]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h && two) g = group_scale<TA>(p, cur[b][1]);
+        const uint4 w = q[2 * b + h];
+        uint32_t v[16];
+        if (p.split_scale) {
+          dequant8<TA>(w.x, g, true, v);
+          dequant8<TA>(w.y, g, true, v + 4);
+          dequant8<TA>(w.z, g, true, v + 8);
+          dequant8<TA>(w.w, g, true, v + 12);
+        } else {
+          dequant8<TA>(w.x, g, false, v);
+          dequant8<TA>(w.y, g, false, v + 4);
+          dequant8<TA>(w.z, g, false, v + 8);
+          dequant8<TA>(w.w, g, false, v + 12);
+        }
+        tmem_st_16cols(dst0 + (uint32_t)((stage * B + b) * 32 + h * 16), v);
       }
-      tmem_st_16cols(dst0 + (uint32_t)(stage * 32 + h * 16), v);
     }
     tmem_st_wait();
     fence_before();
@@ -196,10 +206,10 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
     // (wrong rows at K >= 2048).
     if (lane == 0) {
       mbar_arrive(r.wfull0 + 8 * stage);
-      mbar_arrive(cempty);
+      mbar_arrive(r.cempty0 + 8 * cs);
     }
   }
-  r.turn = (r.turn + nk) & (kGroups - 1);
+  r.fills += (uint32_t)ns;
   return true;
 }
 
@@ -223,7 +233,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster along x splits K
-  const int kb0 = rank * p.kb_per_rank, nk = max(0, min(p.kb_per_rank, p.num_kb - kb0));
+  const int kb0 = rank * p.kb_per_rank, nk = max(0, min(p.kb_per_rank, p.num_kb - kb0));  // multiples of 4
+  constexpr int B = S::kBlocks;
   const int first = (int)blockIdx.y, step = (int)gridDim.y;
 
   if (threadIdx.x == 0) {
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int s = 0; s < CSTAGES; ++s) {
       mbar_init(cfull0 + 8 * s, 1);
-      mbar_init(cempty0 + 8 * s, kDequantWarps);
+      mbar_init(cempty0 + 8 * s, 4 / B * kGroupWarps);
     }
     mbar_init(tfull, 1);
     mbar_init(tempty, kStoreWarps);
@@ -261,14 +272,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int u = first; u < p.tiles && ok; u += step)
-      for (int i = 0; i < nk; ++i) {
+      for (int i = 0; i < nk; i += B) {
         if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.err, kErrCopy)) {
           ok = false;
           break;
         }
         mbar_expect_tx(full0 + 8 * stage, S::kStageB);
-        tma_load_2d(smem_u32(smem + stage * S::kStageB), &tmA, full0 + 8 * stage, (kb0 + i) * 64,
-                    u / p.tiles_n * BN);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+          tma_load_2d(smem_u32(smem + stage * S::kStageB + b * S::kPanelB), &tmA, full0 + 8 * stage,
+                      (kb0 + i + b) * 64, u / p.tiles_n * BN);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
@@ -286,18 +299,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     for (int u = first; u < p.tiles && ok; u += step) {
       if (!warp_wait(tempty, tphase ^ 1, abort_flag, p.err, kErrMma)) break;
-      for (int i = 0; i < nk; ++i) {
+      for (int i = 0; i < nk; i += B) {
         if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.err, kErrMma) ||
             !warp_wait(wfull0 + 8 * stage, phase, abort_flag, p.err, kErrMma)) {
           ok = false;
           break;
         }
         fence_after();
-        const uint64_t bd = desc_at(smem_u32(smem + stage * S::kStageB));
-        const uint32_t w = tmem + BN + (uint32_t)(stage * 32);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ts(tmem, w + 8 * kk, bd + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+        for (int b = 0; b < B; ++b) {
+          const uint64_t bd = desc_at(smem_u32(smem + stage * S::kStageB + b * S::kPanelB));
+          const uint32_t w = tmem + BN + (uint32_t)((stage * B + b) * 32);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tmem, w + 8 * kk, bd + 2 * kk, idesc, (i > 0 || b > 0 || kk > 0) ? 1u : 0u);
+        }
         mma_commit<1>(empty0 + 8 * stage);
         if (++stage == STAGES) {
           stage = 0;
@@ -338,7 +354,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     DequantRing r{codes, cfull0, cempty0, empty0, wfull0, tmem + BN};
     r.group = r.stage = (warp - kDequantWarp) / kGroupWarps;
     for (int u = first; u < p.tiles; u += step)
-      if (!dequant_blocks<TA, STAGES, CSTAGES>(p, r, u % p.tiles_n * 128, kb0, nk, abort_flag)) break;
+      if (!dequant_blocks<TA, S>(p, r, u % p.tiles_n * 128, kb0, nk, abort_flag)) break;
   }
   const int q = warp & 3, half = (warp - kStoreWarp) >> 2;
   const bool stores = warp >= kStoreWarp && warp < kStoreWarp + kStoreWarps;
@@ -416,8 +432,7 @@ mm_status run_tiles(const W4Args &a, const TmaRows &ra, const TmaRows &rw, TileP
   p.tiles = (int)tiles;
   int ranks = 1;
   while (ranks < 8 && tiles * ranks * 2 <= ctx.dev->info.sms && p.num_kb >= 8 * ranks) ranks *= 2;
-  p.kb_per_rank = (p.num_kb + ranks - 1) / ranks;
-  if (ranks > 1) p.kb_per_rank = (p.kb_per_rank + 3) / 4 * 4;  // whole stages of codes
+  p.kb_per_rank = (p.num_kb / 4 + ranks - 1) / ranks * 4;
   const int grid = ranks > 1 ? p.tiles : std::min(p.tiles, ctx.dev->info.sms);
   cudaError_t e = launch_pdl(kern, dim3((unsigned)ranks, (unsigned)grid), dim3(kTileThreads), Tile<BN>::kSmem,
                              ctx.stream, dim3((unsigned)ranks), mw, ma, p);
@@ -447,7 +462,8 @@ mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
   p.tc = a.tc;
   p.M = a.M;
   p.N = a.N;
-  p.num_kb = (int)(((int64_t)a.K + 63) / 64);
+  // blocks of 64 of K, up to whole stages of codes (what is past K multiplies zeros)
+  p.num_kb = (int)(((int64_t)a.K + 255) / 256 * 4);
   p.err = ctx.dev->d_err + kOperatorErrorWord;
   p.w = w4_scales(a);
   p.split_scale = a.ts != a.ta;
