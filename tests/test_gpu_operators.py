@@ -728,3 +728,23 @@ def test_kernels_are_the_librarys_own():
         mm.check(call(None))
         assert mm.mm_get_stats()["launches"] > before
     T().cuda.synchronize()
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("tokens", [1, 16, 200])
+def test_example_runs_the_operators_together(tokens):
+    """examples/quantised_layer.py against its plain form.  The serving step
+    rounds its activations to e4m3 (2^-4 at most a value, about 2.6e-2 in the
+    mean square) and three times to bf16; the training step rounds twice to
+    bf16 before each gradient (2^-8 a value at most, each)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "quantised_layer.py")
+    spec = importlib.util.spec_from_file_location("quantised_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for name, rel in example.run(tokens, 1024, 2048).items():
+        bound = 2.0 ** -8 if name == "residual stream" else 2.0 ** -4 if "quantised" in name else 3 * 2.0 ** -8
+        assert rel <= bound, (name, rel)
