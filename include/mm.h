@@ -390,7 +390,7 @@ mm_status mm_splitk_gemm_noalloc_status(void *stream);
  *   eps       >= 0 and finite.
  * h and y may each be x or residual in place (the same address, leading
  * dimension and element size); other overlaps are not allowed.  rows or cols
- * of 0 is a no-op.  cols < 2^31.
+ * of 0 is a no-op.  cols < 2^30.
  */
 mm_status mm_rmsnorm(const void *x, const void *residual, const void *weight, void *h, void *y,
                      float *scale, float *rstd, int64_t rows, int64_t cols, int64_t ldx,
@@ -407,9 +407,9 @@ mm_status mm_rmsnorm(const void *x, const void *residual, const void *weight, vo
  *   dx        type dt.a; may be dy or dh in place (same address, leading
  *             dimension and element size).
  *   dweight   `cols` values of type dt.b, overwritten; NULL: not computed.
- *             The sum's order depends on the sizes and the device only, so
- *             equal calls give equal bits.
- * rows = 0 writes zeros to dweight; cols = 0 is a no-op.  cols < 2^31.
+ *             The sum's order depends on the sizes, the alignment and the
+ *             device only, so equal calls give equal bits.
+ * rows = 0 writes zeros to dweight; cols = 0 is a no-op.  cols < 2^30.
  */
 mm_status mm_rmsnorm_backward(const void *dy, const void *dh, const void *h, const void *weight,
                               const float *rstd, void *dx, void *dweight, int64_t rows,

@@ -134,9 +134,13 @@ __device__ __forceinline__ void load_pieces(const void *p, int t, int64_t i, int
   else if (t == MM_F16) load_pieces<MM_F16>(p, i, step, n, out);
   else load_pieces<MM_F32>(p, i, step, n, out);
 }
-// How many of the pieces i, i + step, ... start below `end`.
+// How many of the N pieces i, i + step, ... start below `end`.
+template <int N>
 __device__ __forceinline__ int pieces_below(int64_t i, int64_t step, int64_t end) {
-  return i < end ? (int)((end - i + step - 1) / step) : 0;
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) n += i + k * step < end;
+  return n;
 }
 template <int E>
 __device__ __forceinline__ void store_piece(void *p, int t, int64_t i, const float (&v)[E]) {
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
     float ss = 0.f;
     uint32_t big = 0;
     for (int j0 = threadIdx.x * E; j0 < a.cols; j0 += U * 1024 * E) {
-      const int n = pieces_below(j0, 1024 * E, a.cols);
+      const int n = pieces_below<U>(j0, 1024 * E, a.cols);
       float h[U][E], s[U][E] = {}, w[U][E];
       load_pieces<TX>(a.x, r * a.ldx + j0, 1024 * E, n, h);
       if (a.residual) load_pieces<TX>(a.residual, r * a.ldr + j0, 1024 * E, n, s);
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
     }
     if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
     for (int j0 = threadIdx.x * E; j0 < a.cols; j0 += U * 1024 * E) {
-      const int n = pieces_below(j0, 1024 * E, a.cols);
+      const int n = pieces_below<U>(j0, 1024 * E, a.cols);
       float h[U][E], s[U][E] = {}, w[U][E];
       load_pieces<TX>(a.x, r * a.ldx + j0, 1024 * E, n, h);
       if (a.residual) load_pieces<TX>(a.residual, r * a.ldr + j0, 1024 * E, n, s);
@@ -656,7 +660,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_stats_kernel(const NormBwdAr
     constexpr int U = E == 1 ? 4 : 2;  // pieces in flight
     for (int j0 = threadIdx.x * E; j0 < a.cols; j0 += U * 1024 * E) {
       float dy[U][E], h[U][E], w[U][E];
-      const int n = pieces_below(j0, 1024 * E, a.cols);
+      const int n = pieces_below<U>(j0, 1024 * E, a.cols);
       load_pieces(a.dy, a.ty, r * a.lddy + j0, 1024 * E, n, dy);
       load_pieces<TX>(a.h, r * a.ldh + j0, 1024 * E, n, h);
       load_pieces(a.weight, a.tw, j0, 1024 * E, n, w);
@@ -690,7 +694,7 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_cols_kernel(const NormBwdArgs
   for (int64_t r0 = blockIdx.y; r0 < a.rows; r0 += (int64_t)U * gridDim.y) {
     float dy[U][E], h[U][E], dh[U][E] = {};
     float2 s[U];
-    const int n = pieces_below(r0, gridDim.y, a.rows);
+    const int n = pieces_below<U>(r0, gridDim.y, a.rows);
     load_pieces(a.dy, a.ty, r0 * a.lddy + j, gridDim.y * a.lddy, n, dy);
     load_pieces<TX>(a.h, r0 * a.ldh + j, gridDim.y * a.ldh, n, h);
     if (a.dh) load_pieces<TX>(a.dh, r0 * a.lddh + j, gridDim.y * a.lddh, n, dh);

@@ -86,7 +86,7 @@ mm_status mm_rmsnorm(const void *x, const void *residual, const void *weight, vo
     if ((dt.c == MM_E4M3) != (scale != nullptr) && rows > 0 && cols > 0)
       return set_error(MM_ERR_INVALID_ARG, "scale goes with an e4m3 output, and only with it");
     if (rows == 0 || cols == 0) return MM_OK;
-    if (cols >= (1LL << 31)) return set_error(MM_ERR_UNSUPPORTED, "cols too large");
+    if (cols >= kMaxDim) return set_error(MM_ERR_UNSUPPORTED, "cols too large");
     MM_TRY(check_rows("x", x, rows, cols, ldx, dt.a));
     if (residual) MM_TRY(check_rows("residual", residual, rows, cols, ldr, dt.a));
     MM_TRY(check_vector("weight", weight, dt.b));
@@ -113,7 +113,7 @@ mm_status mm_rmsnorm_backward(const void *dy, const void *dh, const void *h, con
       return set_error(MM_ERR_INVALID_ARG, "types (%d, %d, %d): bf16, f16 or f32", dt.a, dt.b, dt.c);
     MM_TRY(check_eps(eps));
     if (cols == 0) return MM_OK;
-    if (cols >= (1LL << 31)) return set_error(MM_ERR_UNSUPPORTED, "cols too large");
+    if (cols >= kMaxDim) return set_error(MM_ERR_UNSUPPORTED, "cols too large");
     if (dweight) MM_TRY(check_vector("dweight", dweight, dt.b));
     if (rows > 0) {
       MM_TRY(check_rows("dy", dy, rows, cols, lddy, dt.c));

@@ -80,7 +80,8 @@ def test_refused_before_any_launch(call, args, says):
 
 @pytest.mark.parametrize("call,args", [
     (norm, dict(cols=1 << 31, ldx=1 << 31, ldr=1 << 31, ldh=1 << 31, ldy=1 << 31)),
-    (bwd, dict(cols=1 << 31)),
+    (norm, dict(cols=1 << 30, ldx=1 << 31, ldr=1 << 31, ldh=1 << 31, ldy=1 << 31)),
+    (bwd, dict(cols=1 << 31)), (bwd, dict(cols=1 << 30)),
     (w4, dict(M=1 << 30)), (w4, dict(N=1 << 30)), (w4, dict(K=1 << 30)),
     (q8, dict(M=1 << 30)), (q8, dict(N=1 << 30)), (q8, dict(K=1 << 30)),
 ])
