@@ -215,18 +215,18 @@ __device__ __forceinline__ float row_scale(float amax) {
 }
 
 // ---------------------------------------------------------------- forward
-// T threads a row (256 threads a block, or T), V pieces of E elements a thread:
+// T threads a row (a warp, eight of them a block, or a block), V pieces of E elements a thread:
 // the row of T V E elements or fewer stays in registers.  Pieces past cols are
 // not accessed (cols is a multiple of E).
 template <int TX, int E, int T, int V>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_rows_kernel(const NormArgs a) {
-  constexpr int ROWS = T < 256 ? 256 / T : 1;
+__global__ void __launch_bounds__(T == 32 ? 256 : T) rmsnorm_rows_kernel(const NormArgs a) {
+  constexpr int ROWS = T == 32 ? 8 : 1;
   pdl_launch_dependents();
   pdl_wait();
   __shared__ float sh[2 * (T / 32)];
   const int t = threadIdx.x % T;
   const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / T;
-  if (T < 256 && r >= a.rows) return;  // (T = 32: no barrier below)
+  if (T == 32 && r >= a.rows) return;  // (no barrier below)
   const int n = max(0, (a.cols - t * E + T * E - 1) / (T * E));  // this thread's pieces
   float h[V][E], w[V][E];
   load_pieces<TX>(a.x, r * a.ldx + t * E, T * E, n, h);
@@ -386,10 +386,10 @@ int type_size(int t) { return t == MM_E4M3 ? 1 : dtype_bytes(t); }
 
 template <int TX, int E, int T, int V>
 mm_status rows_form(const NormArgs &a, LaunchCtx &ctx) {
-  constexpr int ROWS = T < 256 ? 256 / T : 1;
+  constexpr int ROWS = T == 32 ? 8 : 1;
   const int64_t blocks = (a.rows + ROWS - 1) / ROWS;
   if (blocks >= (1LL << 31)) return set_error(MM_ERR_UNSUPPORTED, "too many rows");
-  return launch(rmsnorm_rows_kernel<TX, E, T, V>, blocks, T < 256 ? 256 : T, ctx, "rmsnorm launch", a);
+  return launch(rmsnorm_rows_kernel<TX, E, T, V>, blocks, T == 32 ? 256 : T, ctx, "rmsnorm launch", a);
 }
 
 // A warp a row up to 128 pieces, then a block of 256 to 1024.
@@ -404,8 +404,10 @@ mm_status forward_form(const NormArgs &a, LaunchCtx &ctx) {
     if (pieces <= 1024) return rows_form<TX, E, 512, 2>(a, ctx);
     if (pieces <= 2048) return rows_form<TX, E, 1024, 2>(a, ctx);
   } else {
-    if (pieces <= 1024) return rows_form<TX, E, 256, 4>(a, ctx);
-    if (pieces <= 2048) return rows_form<TX, E, 512, 4>(a, ctx);
+    // single elements: many a thread, so that enough bytes are in flight
+    if (pieces <= 1024) return rows_form<TX, E, 128, 8>(a, ctx);
+    if (pieces <= 2048) return rows_form<TX, E, 128, 16>(a, ctx);
+    if (pieces <= 4096) return rows_form<TX, E, 256, 16>(a, ctx);
     if (pieces <= 5120) return rows_form<TX, E, 512, 10>(a, ctx);
     if (pieces <= 8192) return rows_form<TX, E, 512, 16>(a, ctx);
     if (pieces <= 16384) return rows_form<TX, E, 1024, 16>(a, ctx);
@@ -599,9 +601,9 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
 }
 
 // Rows that start anywhere: element by element, the row and the weight in
-// registers, two blocks an SM.
-template <int TX, int T, int V>
-__global__ void __launch_bounds__(T, 1024 / T) rmsnorm_bwd_elements_kernel(const NormBwdArgs a, float *partial) {
+// registers, many elements a thread, so that enough bytes are in flight.
+template <int TX, int T, int V, int PER_SM>
+__global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_elements_kernel(const NormBwdArgs a, float *partial) {
   using P = Piece<TX, 1>;
   pdl_launch_dependents();
   pdl_wait();
@@ -809,10 +811,10 @@ mm_status bwd_ring_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   return bwd_blocks(a, kern, blocks, T, stages * stage, ctx, stages, ctx.dev->d_err + kOperatorErrorWord);
 }
 
-template <int TX, int T, int V>
-mm_status bwd_elements_form(const NormBwdArgs &a, int per_sm, LaunchCtx &ctx) {
-  return bwd_blocks(a, rmsnorm_bwd_elements_kernel<TX, T, V>,
-                    std::min<int64_t>(a.rows, (int64_t)per_sm * ctx.dev->info.sms), T, 0, ctx);
+template <int TX, int T, int V, int PER_SM>
+mm_status bwd_elements_form(const NormBwdArgs &a, LaunchCtx &ctx) {
+  return bwd_blocks(a, rmsnorm_bwd_elements_kernel<TX, T, V, PER_SM>,
+                    std::min<int64_t>(a.rows, (int64_t)PER_SM * ctx.dev->info.sms), T, 0, ctx);
 }
 
 template <int TX, int E>
@@ -849,12 +851,12 @@ mm_status bwd_form(const NormBwdArgs &a, LaunchCtx &ctx) {
       if (pieces <= 1024) return bwd_ring_form<TX, 512, 2, 2>(a, ctx);
       if (pieces <= 2048) return bwd_ring_form<TX, 1024, 2, 1>(a, ctx);
     } else {
-      if (pieces <= 512) return bwd_elements_form<TX, 128, 4>(a, 8, ctx);
-      if (pieces <= 1024) return bwd_elements_form<TX, 256, 4>(a, 4, ctx);
-      if (pieces <= 2048) return bwd_elements_form<TX, 256, 8>(a, 4, ctx);
-      if (pieces <= 4096) return bwd_elements_form<TX, 512, 8>(a, 2, ctx);
-      if (pieces <= 5120) return bwd_elements_form<TX, 512, 10>(a, 2, ctx);
-      if (pieces <= 8192) return bwd_elements_form<TX, 1024, 8>(a, 1, ctx);
+      if (pieces <= 512) return bwd_elements_form<TX, 64, 8, 16>(a, ctx);
+      if (pieces <= 1024) return bwd_elements_form<TX, 128, 8, 8>(a, ctx);
+      if (pieces <= 2048) return bwd_elements_form<TX, 128, 16, 5>(a, ctx);
+      if (pieces <= 4096) return bwd_elements_form<TX, 256, 16, 2>(a, ctx);
+      if (pieces <= 5120) return bwd_elements_form<TX, 256, 20, 2>(a, ctx);
+      if (pieces <= 8192) return bwd_elements_form<TX, 512, 16, 1>(a, ctx);
     }
   }
   return bwd_long_form<TX, E>(a, ctx);
