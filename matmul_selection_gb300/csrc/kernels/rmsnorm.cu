@@ -404,10 +404,10 @@ mm_status forward_form(const NormArgs &a, LaunchCtx &ctx) {
     if (pieces <= 1024) return rows_form<TX, E, 512, 2>(a, ctx);
     if (pieces <= 2048) return rows_form<TX, E, 1024, 2>(a, ctx);
   } else {
-    // single elements: many a thread, so that enough bytes are in flight
+    // single elements: eight to sixteen a thread, so that enough of them are in flight
     if (pieces <= 1024) return rows_form<TX, E, 128, 8>(a, ctx);
-    if (pieces <= 2048) return rows_form<TX, E, 128, 16>(a, ctx);
-    if (pieces <= 4096) return rows_form<TX, E, 256, 16>(a, ctx);
+    if (pieces <= 2048) return rows_form<TX, E, 256, 8>(a, ctx);
+    if (pieces <= 4096) return rows_form<TX, E, 512, 8>(a, ctx);
     if (pieces <= 5120) return rows_form<TX, E, 512, 10>(a, ctx);
     if (pieces <= 8192) return rows_form<TX, E, 512, 16>(a, ctx);
     if (pieces <= 16384) return rows_form<TX, E, 1024, 16>(a, ctx);
