@@ -58,10 +58,24 @@ __device__ __forceinline__ uint32_t pack2(int tc, float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Whether `ok` holds in all of the 128 threads of the storing warps (barrier 1).
+__device__ __forceinline__ bool all_of_128(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
 // ---------------------------------------------------------------- pair
 constexpr int kPairStages = 6;
 constexpr uint32_t kPairStageB = 2 * 128 * kRowB;
-constexpr size_t kPairSmem = kPairStages * kPairStageB + 1024 + 256;
+constexpr uint32_t kBoxB = 32 * 128;                 // an output box: 32 rows of 128 bytes
+constexpr uint32_t kPairBoxesB = 4 * 2 * kBoxB;      // two for each storing warp
+constexpr size_t kPairSmem = kPairStages * kPairStageB + kPairBoxesB + 1024 /* column scales */ + 1024 + 256;
 constexpr int kGroupRows = 8;  // row tiles walked together, so their A and B stay in L2
 
 // Tile of a unit: row tile, first column, width (256, or 128 for the halves
@@ -82,12 +96,15 @@ __device__ __forceinline__ void pair_unit(const Q8Params &p, int u, int &tm, int
 
 __global__ void __launch_bounds__(kThreads, 1)
     q8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmBh, const Q8Params p) {
+                   const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmC,
+                   const Q8Params p) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kPairStages * kPairStageB);
+  uint8_t *boxes = smem + kPairStages * kPairStageB;
+  float *col_scale = reinterpret_cast<float *>(boxes + kPairBoxesB);  // of the tile being stored
+  uint64_t *bars = reinterpret_cast<uint64_t *>(boxes + kPairBoxesB + 1024);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kPairStages;
   const uint32_t tfull0 = empty0 + 8 * kPairStages, tempty0 = tfull0 + 16, drain = tempty0 + 16;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kPairStages + 5);
@@ -114,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
     prefetch_tmap(&tmBh);
+    if (p.vec) prefetch_tmap(&tmC);
     if (cid < p.total_units) {  // the first blocks of this CTA's operands into L2
       int tm, n0, w;
       pair_unit(p, cid, tm, n0, w);
@@ -204,46 +222,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     const int q = warp & 3;  // the TMEM lanes this warp may read
-    int acc = 0;
+    uint8_t *mine = boxes + (warp - 2) * 2 * kBoxB;
+    const bool f32 = p.tc == MM_F32;
+    const int step = f32 ? 32 : 64;  // columns a box
+    int acc = 0, side = 0;
     uint32_t acc_phase = 0;
     for (int u = cid; u < p.total_units; u += ncl) {
       int tm, n0, w;
       pair_unit(p, u, tm, n0, w);
-      if (!warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.err, kErrStore)) break;
+      // the four warps go on or give up together (and are all done with the last
+      // tile's column scales)
+      if (!all_of_128(warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.err, kErrStore))) break;
       fence_after();
-      const int row = tm * 256 + (int)pos * 128 + q * 32 + lane;
+      const int row0 = tm * 256 + (int)pos * 128 + q * 32, row = row0 + lane;
       const float sa = p.sa && row < p.M ? p.sa[row] : 1.f;
       const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
+      if (p.vec) {
+        // Rows through a swizzled box in shared memory and TMA, which clips what
+        // is past M and N.  (Stored by the lanes, 64 bytes of a row each, a
+        // product with K = 64 took 19.0 us at 1865 x 5056.)
+        for (int i = (int)threadIdx.x - 64; i < 256; i += 128)
+          col_scale[i] = p.sb && n0 + i < p.N ? __ldg(p.sb + n0 + i) : 1.f;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll 1
-      for (int c = 0; c < w && n0 + c < p.N; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32cols(tbase + (uint32_t)c, r);
-        tmem_ld_wait();
-        if (row >= p.M) continue;
-        const int col = n0 + c;
-        const int64_t at = (int64_t)row * p.ldc + col;
-        if (p.vec && col + 32 <= p.N) {
-          float v[32];
+        for (int c = 0; c < w && n0 + c < p.N && row0 < p.M; c += step) {
+          uint32_t r0[32], r1[32];
+          tmem_ld_32cols(tbase + (uint32_t)c, r0);
+          if (!f32) tmem_ld_32cols(tbase + (uint32_t)(c + 32), r1);
+          tmem_ld_wait();
+          if (lane == 0) tma_store_wait_read<1>();  // this box's previous store has read it
+          __syncwarp();
+          uint8_t *box = mine + side * kBoxB;
+          const float4 *s4 = reinterpret_cast<const float4 *>(col_scale + c);
+          auto put = [&](int j, uint32_t a, uint32_t b, uint32_t c2, uint32_t d) {  // 16-byte chunk j of the row
+            *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(a, b, c2, d);
+          };
+          if (f32) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            v[i] = __uint_as_float(r[i]) * sa * (p.sb ? __ldg(p.sb + col + i) : 1.f);
-          if (p.tc == MM_F32) {
-            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int j = 0; j < 8; ++j) {
+              const float4 s = s4[j];
+              put(j, __float_as_uint(__uint_as_float(r0[4 * j]) * sa * s.x),
+                  __float_as_uint(__uint_as_float(r0[4 * j + 1]) * sa * s.y),
+                  __float_as_uint(__uint_as_float(r0[4 * j + 2]) * sa * s.z),
+                  __float_as_uint(__uint_as_float(r0[4 * j + 3]) * sa * s.w));
+            }
           } else {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack2(p.tc, v[8 * i], v[8 * i + 1]), pack2(p.tc, v[8 * i + 2], v[8 * i + 3]),
-                                  pack2(p.tc, v[8 * i + 4], v[8 * i + 5]), pack2(p.tc, v[8 * i + 6], v[8 * i + 7]));
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t *r = j < 4 ? r0 + 8 * j : r1 + 8 * (j - 4);
+              const float4 s = s4[2 * j], q4 = s4[2 * j + 1];
+              put(j, pack2(p.tc, __uint_as_float(r[0]) * sa * s.x, __uint_as_float(r[1]) * sa * s.y),
+                  pack2(p.tc, __uint_as_float(r[2]) * sa * s.z, __uint_as_float(r[3]) * sa * s.w),
+                  pack2(p.tc, __uint_as_float(r[4]) * sa * q4.x, __uint_as_float(r[5]) * sa * q4.y),
+                  pack2(p.tc, __uint_as_float(r[6]) * sa * q4.z, __uint_as_float(r[7]) * sa * q4.w));
+            }
           }
-        } else {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&tmC, smem_u32(box), n0 + c, row0);
+          side ^= 1;
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < w && n0 + c < p.N; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32cols(tbase + (uint32_t)c, r);
+          tmem_ld_wait();
+          const int col = n0 + c;
+          if (row < p.M)
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (col + i < p.N)
-              store_value(p.out, p.tc, at + i, __uint_as_float(r[i]) * sa * (p.sb ? __ldg(p.sb + col + i) : 1.f));
+            for (int i = 0; i < 32; ++i)
+              if (col + i < p.N)
+                store_value(p.out, p.tc, (int64_t)row * p.ldc + col + i,
+                            __uint_as_float(r[i]) * sa * (p.sb ? __ldg(p.sb + col + i) : 1.f));
         }
       }
       fence_before();
@@ -254,6 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc_phase ^= 1;
       }
     }
+    if (lane == 0) tma_store_wait_all();
+    __syncwarp();
   }
   fence_before();
   __syncthreads();
@@ -416,11 +469,22 @@ mm_status pair_capacity(int *clusters) {
 }
 
 mm_status run_pair(const Q8Args &a, Q8Params p, int clusters, LaunchCtx &ctx) {
-  CUtensorMap ma, mb, mbh;
+  CUtensorMap ma, mb, mbh, mc;
   mm_status st;
   if ((st = rows_map(&ma, a.A, a.M, a.K, a.lda, 128)) != MM_OK) return st;
   if ((st = rows_map(&mb, a.B, a.N, a.K, a.ldb, 128)) != MM_OK) return st;
   if ((st = rows_map(&mbh, a.B, a.N, a.K, a.ldb, 64)) != MM_OK) return st;
+  mc = ma;
+  if (p.vec) {
+    const int es = dtype_bytes(p.tc);
+    st = encode_map_2d(&mc,
+                       p.tc == MM_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                       : p.tc == MM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                       p.out, (uint64_t)p.N, (uint64_t)p.M, (uint64_t)p.ldc * es, 128 / es, 32,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != MM_OK) return st;
+  }
   p.tiles_m = (a.M + 255) / 256;
   p.tiles_n = (a.N + 255) / 256;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
@@ -432,7 +496,7 @@ mm_status run_pair(const Q8Args &a, Q8Params p, int clusters, LaunchCtx &ctx) {
   p.total_units = (int)(halve ? tiles + rem : tiles);
   const int grid = 2 * (int)std::min<int64_t>(p.total_units, clusters);
   cudaError_t e = launch_pdl(q8_pair_kernel, dim3((unsigned)grid), dim3(kThreads), kPairSmem, ctx.stream,
-                             dim3(2), ma, mb, mbh, p);
+                             dim3(2), ma, mb, mbh, mc, p);
   return e == cudaSuccess ? MM_OK : cuda_error(e, "gemm_q8 launch (pair)");
 }
 
@@ -451,6 +515,7 @@ mm_status run_swap(const Q8Args &a, Q8Params p, int ranks, LaunchCtx &ctx) {
   if ((st = rows_map(&ma, a.A, a.M, a.K, a.lda, BN)) != MM_OK) return st;
   p.kb_per_rank = (p.num_kb + ranks - 1) / ranks;
   const int gx = (a.N + 127) / 128, gz = (a.M + BN - 1) / BN;
+  if (gz > 65535) return set_error(MM_ERR_UNSUPPORTED, "too many rows of A");
   cudaError_t e = launch_pdl(q8_swap_kernel<BN>, dim3((unsigned)gx, (unsigned)ranks, (unsigned)gz),
                              dim3(kSwapThreads), Swap<BN>::kSmem, ctx.stream, dim3(1, (unsigned)ranks), mb, ma, p);
   return e == cudaSuccess ? MM_OK : cuda_error(e, "gemm_q8 launch (swap)");
@@ -484,21 +549,27 @@ mm_status launch_gemm_q8(const Q8Args &in, LaunchCtx &ctx) {
   p.M = a.M;
   p.N = a.N;
   p.num_kb = (int)(((int64_t)a.K + kRowB - 1) / kRowB);
-  p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0;
+  p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0 && a.ldc < (1LL << 37);
   p.err = ctx.dev->d_err + kOperatorErrorWord;
   int clusters = 0;
   if ((st = pair_capacity(&clusters)) != MM_OK) return st;
-  if (a.M > 256) {
-    st = run_pair(a, p, clusters, ctx);
-  } else {
-    // a tile of as few rows as hold A, and K over as many CTAs as fill the SMs
-    const int bn = a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
-    const int64_t tiles = ((int64_t)a.N + 127) / 128 * ((a.M + bn - 1) / bn);
-    int ranks = 1;
-    while (ranks < 8 && tiles * ranks * 2 <= ctx.dev->info.sms && p.num_kb >= 4 * ranks) ranks *= 2;
-    st = bn == 32 ? run_swap<32>(a, p, ranks, ctx) : bn == 64 ? run_swap<64>(a, p, ranks, ctx)
-                                                              : run_swap<128>(a, p, ranks, ctx);
-  }
+  // swap: a tile of as few rows as hold A, and K over as many CTAs as fill the SMs
+  const int sms = ctx.dev->info.sms, bn = a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+  const int64_t tiles = ((int64_t)a.N + 127) / 128 * ((a.M + bn - 1) / bn);
+  int ranks = 1;
+  while (ranks < 8 && tiles * ranks * 2 <= sms && p.num_kb >= 4 * ranks) ranks *= 2;
+  // Above 128 rows of A, pair or swap, whichever its waves say takes less: a
+  // wave costs its stages (0.29 us of a pair's, 0.18 of a swap's, the measured
+  // slopes) and what surrounds them.  us, pair / swap: 300 x 4096 x 4096 17.5 /
+  // 13.4, 512 x 4096 x 4096 18.4 / 14.3.
+  const int64_t pairs = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + 255) / 256);
+  const double pair_us = (double)((pairs + clusters - 1) / clusters) * p.num_kb * 0.29 + 8.0;
+  const double swap_us =
+      (double)((tiles * ranks + sms - 1) / sms) * (((p.num_kb + ranks - 1) / ranks) * 0.183 + 2.5) + 5.0;
+  st = a.M > 128 && pair_us < swap_us ? run_pair(a, p, clusters, ctx)
+       : bn == 32                     ? run_swap<32>(a, p, ranks, ctx)
+       : bn == 64                     ? run_swap<64>(a, p, ranks, ctx)
+                                      : run_swap<128>(a, p, ranks, ctx);
   if (st != MM_OK) return st;
   count_operator_launch();
   return MM_OK;
