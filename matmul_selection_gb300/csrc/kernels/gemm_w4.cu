@@ -118,7 +118,7 @@ __device__ __forceinline__ void dequant8(uint32_t w, const GroupScale<TA> &g, bo
 struct DequantRing {
   const uint8_t *codes;
   uint32_t cfull0, cempty0;  // the code stages' barriers
-  uint32_t empty0, wfull0;   // a stage is free; its weights are written
+  uint32_t empty0, full0;    // a stage is free; its weights (and A's rows) are there
   uint32_t weights;          // TMEM address of stage 0's weights
   int group;                 // of this warp
   int stage;                 // of the group's next fill
@@ -205,7 +205,7 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
     // behind the loads, the next copy overwrote some before they were read
     // (wrong rows at K >= 2048).
     if (lane == 0) {
-      mbar_arrive(r.wfull0 + 8 * stage);
+      mbar_arrive(r.full0 + 8 * stage);
       mbar_arrive(r.cempty0 + 8 * cs);
     }
   }
@@ -226,10 +226,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t *codes = smem + STAGES * S::kStageB;
   float *tile = reinterpret_cast<float *>(S::kOver ? smem : codes + CSTAGES * kCodeStageB);
   uint64_t *bars = reinterpret_cast<uint64_t *>(codes + CSTAGES * kCodeStageB + S::kTileB);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, wfull0 = empty0 + 8 * STAGES;
-  const uint32_t cfull0 = wfull0 + 8 * STAGES, cempty0 = cfull0 + 8 * CSTAGES;
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
+  const uint32_t cfull0 = empty0 + 8 * STAGES, cempty0 = cfull0 + 8 * CSTAGES;
   const uint32_t tfull = cempty0 + 8 * CSTAGES, tempty = tfull + 8, drain = tempty + 8;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 3 * STAGES + 2 * CSTAGES + 3);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 2 * CSTAGES + 3);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster along x splits K
@@ -239,9 +239,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, 1 + kGroupWarps);  // A's arming; the weights' four warps
       mbar_init(empty0 + 8 * s, 1);
-      mbar_init(wfull0 + 8 * s, kGroupWarps);
     }
     for (int s = 0; s < CSTAGES; ++s) {
       mbar_init(cfull0 + 8 * s, 1);
@@ -300,8 +299,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int u = first; u < p.tiles && ok; u += step) {
       if (!warp_wait(tempty, tphase ^ 1, abort_flag, p.err, kErrMma)) break;
       for (int i = 0; i < nk; i += B) {
-        if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.err, kErrMma) ||
-            !warp_wait(wfull0 + 8 * stage, phase, abort_flag, p.err, kErrMma)) {
+        if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.err, kErrMma)) {
           ok = false;
           break;
         }
@@ -351,7 +349,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     __syncwarp();
   } else if (warp >= kDequantWarp) {
-    DequantRing r{codes, cfull0, cempty0, empty0, wfull0, tmem + BN};
+    DequantRing r{codes, cfull0, cempty0, empty0, full0, tmem + BN};
     r.group = r.stage = (warp - kDequantWarp) / kGroupWarps;
     for (int u = first; u < p.tiles; u += step)
       if (!dequant_blocks<TA, S>(p, r, u % p.tiles_n * 128, kb0, nk, abort_flag)) break;
