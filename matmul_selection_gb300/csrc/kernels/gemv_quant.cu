@@ -236,6 +236,22 @@ __device__ __forceinline__ void panel_e4m3(uint32_t wrow, uint32_t xpanel, float
   }
 }
 
+__device__ __forceinline__ void computing_warps_sync() {
+  asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+// Element o of a tile of M x cols from its parts (PARTS of them, or `parts`), in order.
+template <bool W4, int PARTS>
+__device__ __forceinline__ void store_sum(const GemvParams &p, const float *buf, int cols, int n0, int o,
+                                          int parts = PARTS) {
+  const int m = o / cols, n = n0 + o % cols;
+  if (n >= p.N) return;
+  float v = 0.f;
+#pragma unroll
+  for (int q = 0; q < (PARTS ? PARTS : parts); ++q) v += buf[q * p.M * cols + o];
+  if constexpr (!W4) v = v * (p.sa ? __ldg(p.sa + m) : 1.f) * (p.sb ? __ldg(p.sb + n) : 1.f);
+  store_value(p.out, p.tc, (int64_t)m * p.ldc + n, v);
+}
+
 template <int F, int WR, bool TWO>
 __global__ void __launch_bounds__(kThreads, 2)
     gemv_quant_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 2 * kStages);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = (int)gridDim.y, rank = (int)blockIdx.y;  // a cluster along y splits K
-  const int n0 = (int)blockIdx.x * R;
+  const int tile0 = (int)blockIdx.x, tiles = (p.N + R - 1) / R, hop = (int)gridDim.x;
   const int p0 = rank * p.panels_per_rank, np = max(0, min(p.panels_per_rank, p.panels - p0));
   const int steps = (np + WK - 1) / WK;
 
@@ -267,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (warp == kWarps) {
     if (lane == 0) prefetch_tmap(&tmW);
-    for (int i = lane; i < min(np, 64); i += 32) tma_prefetch_2d(&tmW, (p0 + i) * 128, n0);
+    for (int i = lane; i < min(np, 64); i += 32) tma_prefetch_2d(&tmW, (p0 + i) * 128, tile0 * R);
   }
   if (warp == kWarps + 1 && lane == 0) prefetch_tmap(&tmX);
   if (ranks > 1) cluster_sync_all();  // the others run: their memory may be written
@@ -279,79 +295,97 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t bytes = weights ? R * 128 : (uint32_t)p.M * (W4 ? 512u : 128u);
     const uint32_t offset = weights ? 0u : kWeightsB, pitch = weights ? R * 128 : XPANEL;
     const int kx = weights ? 128 : W4 ? 256 : 128;  // a panel in the map's elements
-    int i = 0;
-    for (; i < steps; ++i) {
-      const int st = i % kStages;
-      if (!warp_wait(empty0 + 8 * st, ((uint32_t)(i / kStages) & 1u) ^ 1u, abort_flag, p.err, kErrCopy)) break;
-      const int nv = min(WK, np - i * WK);
-      mbar_expect_tx(full0 + 8 * st, (uint32_t)nv * bytes);
-      __syncwarp();
-      if (lane < nv)
-        tma_load_2d_lane(smem_u32(smem + st * kStageB + offset) + (uint32_t)lane * pitch, weights ? &tmW : &tmX,
-                         full0 + 8 * st, (p0 + i * WK + lane) * kx, weights ? n0 : 0);
-    }
+    int n = 0;  // stages filled
+    bool ok = true;
+    for (int tile = tile0; tile < tiles && ok; tile += hop)
+      for (int i = 0; i < steps; ++i, ++n) {
+        const int st = n % kStages;
+        ok = warp_wait(empty0 + 8 * st, ((uint32_t)(n / kStages) & 1u) ^ 1u, abort_flag, p.err, kErrCopy);
+        if (!ok) break;
+        const int nv = min(WK, np - i * WK);
+        mbar_expect_tx(full0 + 8 * st, (uint32_t)nv * bytes);
+        __syncwarp();
+        if (lane < nv)
+          tma_load_2d_lane(smem_u32(smem + st * kStageB + offset) + (uint32_t)lane * pitch, weights ? &tmW : &tmX,
+                           full0 + 8 * st, (p0 + i * WK + lane) * kx, weights ? tile * R : 0);
+      }
     __syncwarp();
-    for (int f = max(0, i - kStages); f < i; ++f)
+    for (int f = max(0, n - kStages); f < n; ++f)
       wait_drain(full0 + 8 * (f % kStages), (uint32_t)(f / kStages) & 1u, p.err, kErrCopy);
     __syncwarp();
   } else {
     const int wr = warp % WR, wk = warp / WR, t = lane & 3;
-    float acc[MT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
     const uint32_t stage0 = smem_u32(smem);
     const uint32_t wrow = stage0 + (uint32_t)(wk * R * 128) + (uint32_t)(wr * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
     const uint32_t xpan = stage0 + kWeightsB + (uint32_t)wk * XPANEL;
     // a lane's row of A; past the last, the last once more (its columns of the
     // product are not used, and lanes that read one address share the read)
     const uint32_t xrow = xpan + (uint32_t)(min(lane >> 2, p.M - 1) * 512 + t * 16);
+    const int row0 = wr * 16 + (lane >> 2), k0 = (p0 + wk) * 256 + 64 * t;
     ScaleCursor cursor = {};
     PanelScales next = {};
     if constexpr (W4) {
-      cursor = scale_cursor(p.w, n0 + wr * 16 + (lane >> 2), (p0 + wk) * 256 + 64 * t, WK * 256);
+      cursor = scale_cursor(p.w, tile0 * R + row0, k0, WK * 256);
       load_panel_scales<TWO>(p.w, cursor, next);
     }
-    for (int i = 0; i < steps; ++i) {
-      const int st = i % kStages;
-      const PanelScales cur = next;
-      if constexpr (W4) load_panel_scales<TWO>(p.w, cursor, next);
-      if (!warp_wait(full0 + 8 * st, (uint32_t)(i / kStages) & 1u, abort_flag, p.err, kErrMma)) break;
-      if (i * WK + wk < np) {
-        const uint32_t off = after_wait((uint32_t)st * kStageB);
-        if constexpr (W4)
-          panel_w4<F, MT, TWO>(p, wrow + off, xrow + off, cur, acc);
-        else
-          panel_e4m3<MT>(wrow + off, xpan + off, acc);
-        before_release(acc);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty0 + 8 * st);
-    }
-    // to the owners: CTA r has the columns [r CS, (r + 1) CS) of the R, [part][m][CS]
-    const int cs = R / ranks, part = rank * WK + wk;
+    int n = 0, buffer = 0;
+    bool ok = true;  // (after a wait that gave up the barriers below are still met)
+    for (int tile = tile0; tile < tiles; tile += hop, buffer ^= 1) {
+      float acc[MT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = wr * 16 + (lane >> 2) + (i >> 1) * 8, row = m * 8 + 2 * t + (i & 1);
-        if (row < p.M) {
-          const uint32_t at = smem_u32(parts + (part * p.M + row) * cs + col % cs);
-          st_cluster_f32(map_to_rank(at, (uint32_t)(col / cs)), acc[m][i]);
+        for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+      for (int i = 0; i < steps && ok; ++i, ++n) {
+        const int st = n % kStages;
+        const PanelScales cur = next;
+        if constexpr (W4) {
+          if (i + 1 == steps) cursor = scale_cursor(p.w, (tile + hop) * R + row0, k0, WK * 256);
+          load_panel_scales<TWO>(p.w, cursor, next);
         }
+        ok = warp_wait(full0 + 8 * st, (uint32_t)(n / kStages) & 1u, abort_flag, p.err, kErrMma);
+        if (!ok) break;
+        if (i * WK + wk < np) {
+          const uint32_t off = after_wait((uint32_t)st * kStageB);
+          if constexpr (W4)
+            panel_w4<F, MT, TWO>(p, wrow + off, xrow + off, cur, acc);
+          else
+            panel_e4m3<MT>(wrow + off, xpan + off, acc);
+          before_release(acc);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty0 + 8 * st);
       }
+      // to the owners: CTA r has the columns [r CS, (r + 1) CS) of the R, [part][m][CS]
+      const int cs = R / ranks, part = rank * WK + wk;
+      float *buf = parts + (ranks == 1 && WK > 1 ? buffer * (kPartsB / 8) : 0);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = wr * 16 + (lane >> 2) + (i >> 1) * 8, row = m * 8 + 2 * t + (i & 1);
+          if (row < p.M) {
+            const uint32_t at = smem_u32(buf + (part * p.M + row) * cs + col % cs);
+            st_cluster_f32(map_to_rank(at, (uint32_t)(col / cs)), acc[m][i]);
+          }
+        }
+      if (ranks > 1) break;
+      // Two buffers: one is written again only past the next tile's barrier,
+      // which a warp meets when it has read this one.
+      if constexpr (WK > 1) {
+        computing_warps_sync();
+        for (int o = threadIdx.x; o < p.M * R; o += 32 * kWarps) store_sum<W4, WK>(p, buf, R, tile * R, o);
+      } else {  // a warp's columns are its own
+        __syncwarp();
+        for (int o = lane; o < p.M * 16; o += 32) store_sum<W4, WK>(p, buf, R, tile * R, (o >> 4) * R + wr * 16 + (o & 15));
+        __syncwarp();
+      }
+    }
   }
-  if (ranks > 1) cluster_sync_all();
-  else __syncthreads();
-  const int cs = R / ranks, nparts = ranks * WK;
-  for (int o = threadIdx.x; o < p.M * cs; o += kThreads) {
-    const int m = o / cs, n = n0 + rank * cs + o % cs;
-    if (n >= p.N) continue;
-    float v = 0.f;
-    for (int q = 0; q < nparts; ++q) v += parts[q * p.M * cs + o];
-    if constexpr (!W4) v = v * (p.sa ? __ldg(p.sa + m) : 1.f) * (p.sb ? __ldg(p.sb + n) : 1.f);
-    store_value(p.out, p.tc, (int64_t)m * p.ldc + n, v);
+  if (ranks > 1) {
+    cluster_sync_all();
+    const int cs = R / ranks;
+    for (int o = threadIdx.x; o < p.M * cs; o += kThreads) store_sum<W4, 0>(p, parts, cs, tile0 * R + rank * cs, o, ranks * WK);
   }
 }
 
@@ -382,7 +416,8 @@ mm_status run(const TmaRows &rx, const TmaRows &rw, int K, GemvParams p, LaunchC
   int ranks = 1;
   while (ranks < 8 && (int64_t)tiles * ranks * 2 <= 2 * ctx.dev->info.sms && p.panels >= 2 * ranks * WK) ranks *= 2;
   p.panels_per_rank = ((p.panels + ranks - 1) / ranks + WK - 1) / WK * WK;
-  cudaError_t e = launch_pdl(kern, dim3((unsigned)tiles, (unsigned)ranks), dim3(kThreads), kSmem, ctx.stream,
+  const int columns = ranks > 1 ? tiles : std::min(tiles, 2 * ctx.dev->info.sms);
+  cudaError_t e = launch_pdl(kern, dim3((unsigned)columns, (unsigned)ranks), dim3(kThreads), kSmem, ctx.stream,
                              dim3(1, (unsigned)ranks), mw, mx, p);
   if (e != cudaSuccess) return cuda_error(e, "quantised GEMV launch");
   count_operator_launch();
