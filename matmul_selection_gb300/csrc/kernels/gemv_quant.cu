@@ -88,6 +88,18 @@ __device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1
   if constexpr (F == FMT_E4M3) MM_MMA_SYNC("m16n8k32.row.col.f32.e4m3.e4m3.f32");
 #undef MM_MMA_SYNC
 }
+// The same into fresh sums.
+template <int F>
+__device__ __forceinline__ void mma_16x8_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+#define MM_MMA_SYNC(SHAPE_TYPES)                                                                        \
+  asm("mma.sync.aligned." SHAPE_TYPES " {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};" \
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                         \
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f))
+  if constexpr (F == FMT_W4_BF16) MM_MMA_SYNC("m16n8k16.row.col.f32.bf16.bf16.f32");
+  else MM_MMA_SYNC("m16n8k16.row.col.f32.f16.f16.f32");
+#undef MM_MMA_SYNC
+}
 
 // Where a lane's scales and zero points are: of its two rows, for the 64 codes
 // of a panel from 64 t on (lane t of four), entry h those from 64 t + 32 h
@@ -135,22 +147,36 @@ __device__ __forceinline__ void load_panel_scales(const W4Scales &w, ScaleCursor
   }
   c.g += c.step;
 }
-// (a & b) | c
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
+// A byte b under a byte of zeros is b 2^-133 as a bf16 (and b 2^-24 as an f16):
+// the denormals and the first binade lie on one line.  So a pair of codes that
+// came in one byte needs two masks and one byte permutation, and one FMA, exact,
+// makes (q - z) 2^-6 (f16: 2^-9) of both: the high code's factor is 1/16 of the
+// low one's.  The results are scaled back when they are stored.
+template <int F>
+struct Unpack {
+  static constexpr bool B = F == FMT_W4_BF16;
+  static constexpr uint32_t kFactors = B ? 0x7d007f00u : 0x68007800u;  // 2^127 and 2^123; 2^15 and 2^11
+  static constexpr uint32_t kMinus = B ? 0xff00ff00u : 0xf800f800u;    // -2^127; -2^15
+  static constexpr float kBack = B ? 64.f : 512.f;
+  using T = typename Pair16<F>::T;
+  static __device__ __forceinline__ T minus_zero(uint32_t z) {  // -z 2^-6, twice
+    return __hmul2(bits_as<T>((z & 15u) * 0x00010001u), bits_as<T>(kMinus));
+  }
+  static __device__ __forceinline__ uint32_t pair(uint32_t lo, uint32_t hi, int i, T minus_z) {
+    uint32_t both;  // byte i of lo; zeros (lo's sign, which is 0); byte i of hi; zeros
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(both) : "r"(lo), "r"(hi), "r"(0x8480 + 0x1111 * i));
+    return as_bits(__hfma2(bits_as<T>(both), bits_as<T>(kFactors), minus_z));
+  }
+};
 
 // A panel of 16 rows of 4-bit weights (256 codes) times 8 MT rows of A.
-template <int F, int MT, bool TWO>
+template <int F, int MT, int XBLOCK, bool TWO, bool Z>
 __device__ __forceinline__ void panel_w4(const GemvParams &p, uint32_t wrow, uint32_t xrow, const PanelScales &ps,
                                          float (&acc)[MT][4]) {
-  using T = typename Pair16<F>::T;
-  constexpr uint32_t kBias = F == FMT_W4_BF16 ? 0x43004300u : 0x64006400u;
+  using U = Unpack<F>;
+  using T = typename U::T;
   constexpr int E = TWO ? 2 : 1;
   const int lane = threadIdx.x & 31;
-  const bool zeros = p.w.z != nullptr;
   float scale[2][E];
   uint32_t zero[2][E];
   if (p.w.ts == MM_F16) {
@@ -162,52 +188,48 @@ __device__ __forceinline__ void panel_w4(const GemvParams &p, uint32_t wrow, uin
 #pragma unroll
     for (int i = 0; i < 2 * E; ++i) scale[i / E][i % E] = __uint_as_float(ps.s[i / E][i % E] << shift);
   }
-  if (zeros)
+  if constexpr (Z)
 #pragma unroll
-    for (int i = 0; i < 2 * E; ++i) zero[i / E][i % E] = kBias + (ps.z[i / E][i % E] & 15u) * 0x00010001u;
-  const int last = (1 << (p.w.group_shift - 5)) - 1;  // the chunk of 32 that ends a group: (c & last) == last
-  float part[MT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) part[m][i] = 0.f;
-#pragma unroll
+    for (int i = 0; i < 2 * E; ++i) zero[i / E][i % E] = as_bits(U::minus_zero(ps.z[i / E][i % E]));
+  const uint32_t rr = lane & 7, mat = lane >> 3;
+  // A group of 64 or more is summed 64 codes at a time all the same: scaling
+  // costs less than asking whether a group ends, and no branch stands between
+  // one pair of chunks and the next.
+#pragma unroll (MT == 2 ? 2 : 4)  // (four spill with two blocks of A's rows)
   for (int c2 = 0; c2 < 4; ++c2) {  // two chunks of 32 codes
     uint32_t w[4];  // rows r, r + 8 of the first; of the second
-    const uint32_t rr = lane & 7, mat = lane >> 3;
     ldmatrix_x4(wrow + (((2 * c2 + (mat >> 1)) ^ rr) << 4), w);
     const int src = (lane & 28) | c2;
     T z[2];
+    float part[MT][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (TWO || h == 0)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          z[r] = bits_as<T>(zeros ? __shfl_sync(0xffffffffu, zero[r][h % E], src) : kBias + 0x00080008u);
+          z[r] = Z ? bits_as<T>(__shfl_sync(0xffffffffu, zero[r][h % E], src)) : U::minus_zero(8);
       uint32_t a[2][4];  // row, pairs (0, 1), (2, 3), (4, 5), (6, 7)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const uint32_t lo = w[2 * h + r], hi = lo >> 4;
+        const uint32_t lo = w[2 * h + r] & 0x0f0f0f0fu, hi = w[2 * h + r] & 0xf0f0f0f0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          a[r][i] = as_bits(__hsub2(
-              bits_as<T>(and_or(__byte_perm(lo, hi, 0x0400 + 0x0101 * i), 0x000f000fu, kBias)), z[r]));
+        for (int i = 0; i < 4; ++i) a[r][i] = U::pair(lo, hi, i, z[r]);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const uint4 x = lds_16(xrow + (uint32_t)(m * 8 * 512 + (2 * c2 + h) * 64));
-        mma_16x8<F>(part[m], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+        const uint4 x = lds_16(XBLOCK ? (xrow ^ (uint32_t)(h << 6)) + (uint32_t)(c2 * XBLOCK + m * 1024)
+                                      : xrow + (uint32_t)((2 * c2 + h) * 64));
+        if (TWO || h == 0) mma_16x8_first<F>(part[m], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+        else mma_16x8<F>(part[m], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
         mma_16x8<F>(part[m], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
       }
-      if (TWO || ((2 * c2 + h) & last) == last) {
+      if (TWO || h == 1) {
         const float s0 = __shfl_sync(0xffffffffu, scale[0][h % E], src);
         const float s1 = __shfl_sync(0xffffffffu, scale[1][h % E], src);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           acc[m][0] += s0 * part[m][0], acc[m][1] += s0 * part[m][1];
           acc[m][2] += s1 * part[m][2], acc[m][3] += s1 * part[m][3];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) part[m][i] = 0.f;
         }
       }
     }
@@ -239,8 +261,14 @@ __device__ __forceinline__ void panel_e4m3(uint32_t wrow, uint32_t xpanel, float
 __device__ __forceinline__ void computing_warps_sync() {
   asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * kWarps) : "memory");
 }
+// A panel of A is M rows of 512 bytes, which meet in the banks in pairs.  Where
+// a warp reads two blocks of rows of A that costs more than copying the panel in
+// four boxes of 128 bytes a row with TMA's swizzle (16 x 16384 x 8192: 37.8 us
+// against 32.2; 8 rows: 20.8 against 21.4); this many bytes apart.
+template <int F, int WR>
+constexpr int kXBlock = F != FMT_E4M3 && WR == 8 ? 2048 : 0;
 // Element o of a tile of M x cols from its parts (PARTS of them, or `parts`), in order.
-template <bool W4, int PARTS>
+template <int F, int PARTS>
 __device__ __forceinline__ void store_sum(const GemvParams &p, const float *buf, int cols, int n0, int o,
                                           int parts = PARTS) {
   const int m = o / cols, n = n0 + o % cols;
@@ -248,7 +276,8 @@ __device__ __forceinline__ void store_sum(const GemvParams &p, const float *buf,
   float v = 0.f;
 #pragma unroll
   for (int q = 0; q < (PARTS ? PARTS : parts); ++q) v += buf[q * p.M * cols + o];
-  if constexpr (!W4) v = v * (p.sa ? __ldg(p.sa + m) : 1.f) * (p.sb ? __ldg(p.sb + n) : 1.f);
+  if constexpr (F != FMT_E4M3) v *= Unpack<F>::kBack;
+  else v = v * (p.sa ? __ldg(p.sa + m) : 1.f) * (p.sb ? __ldg(p.sb + n) : 1.f);
   store_value(p.out, p.tc, (int64_t)m * p.ldc + n, v);
 }
 
@@ -259,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int WK = kWarps / WR, R = 16 * WR, MT = WR == 8 ? 2 : 1;
   constexpr bool W4 = F != FMT_E4M3;
   constexpr uint32_t XPANEL = kRowsB / WK;  // 2 WR rows of 512 bytes, or 8 MT and more of 128
+  constexpr int XBLOCK = kXBlock<F, WR>;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -295,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t bytes = weights ? R * 128 : (uint32_t)p.M * (W4 ? 512u : 128u);
     const uint32_t offset = weights ? 0u : kWeightsB, pitch = weights ? R * 128 : XPANEL;
     const int kx = weights ? 128 : W4 ? 256 : 128;  // a panel in the map's elements
+    const int boxes = weights || XBLOCK == 0 ? 1 : 4;
     int n = 0;  // stages filled
     bool ok = true;
     for (int tile = tile0; tile < tiles && ok; tile += hop)
@@ -305,9 +336,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int nv = min(WK, np - i * WK);
         mbar_expect_tx(full0 + 8 * st, (uint32_t)nv * bytes);
         __syncwarp();
-        if (lane < nv)
-          tma_load_2d_lane(smem_u32(smem + st * kStageB + offset) + (uint32_t)lane * pitch, weights ? &tmW : &tmX,
-                           full0 + 8 * st, (p0 + i * WK + lane) * kx, weights ? tile * R : 0);
+        const int panel = boxes == 4 ? lane >> 2 : lane, box = boxes == 4 ? lane & 3 : 0;
+        if (lane < nv * boxes)
+          tma_load_2d_lane(smem_u32(smem + st * kStageB + offset) + (uint32_t)panel * pitch + (uint32_t)(box * XBLOCK),
+                           weights ? &tmW : &tmX, full0 + 8 * st, (p0 + i * WK + panel) * kx + box * 64,
+                           weights ? tile * R : 0);
       }
     __syncwarp();
     for (int f = max(0, n - kStages); f < n; ++f)
@@ -320,7 +353,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t xpan = stage0 + kWeightsB + (uint32_t)wk * XPANEL;
     // a lane's row of A; past the last, the last once more (its columns of the
     // product are not used, and lanes that read one address share the read)
-    const uint32_t xrow = xpan + (uint32_t)(min(lane >> 2, p.M - 1) * 512 + t * 16);
+    // (swizzled, rows 0, 4, 1, 5, ... : two neighbours are in different banks)
+    const int xr = min(XBLOCK ? (lane >> 3) + 4 * ((lane >> 2) & 1) : lane >> 2, p.M - 1);
+    const uint32_t xrow = xpan + (uint32_t)(XBLOCK ? xr * 128 + (((t ^ xr) & 7) << 4) : xr * 512 + t * 16);
     const int row0 = wr * 16 + (lane >> 2), k0 = (p0 + wk) * 256 + 64 * t;
     ScaleCursor cursor = {};
     PanelScales next = {};
@@ -347,45 +382,47 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!ok) break;
         if (i * WK + wk < np) {
           const uint32_t off = after_wait((uint32_t)st * kStageB);
-          if constexpr (W4)
-            panel_w4<F, MT, TWO>(p, wrow + off, xrow + off, cur, acc);
-          else
+          if constexpr (W4) {
+            if (p.w.z) panel_w4<F, MT, XBLOCK, TWO, true>(p, wrow + off, xrow + off, cur, acc);
+            else panel_w4<F, MT, XBLOCK, TWO, false>(p, wrow + off, xrow + off, cur, acc);
+          } else {
             panel_e4m3<MT>(wrow + off, xpan + off, acc);
+          }
           before_release(acc);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + 8 * st);
       }
-      // to the owners: CTA r has the columns [r CS, (r + 1) CS) of the R, [part][m][CS]
       const int cs = R / ranks, part = rank * WK + wk;
+      // to the owners: CTA r has the columns [r CS, (r + 1) CS) of the R, [part][m][CS]
       float *buf = parts + (ranks == 1 && WK > 1 ? buffer * (kPartsB / 8) : 0);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int col = wr * 16 + (lane >> 2) + (i >> 1) * 8, row = m * 8 + 2 * t + (i & 1);
-          if (row < p.M) {
-            const uint32_t at = smem_u32(buf + (part * p.M + row) * cs + col % cs);
-            st_cluster_f32(map_to_rank(at, (uint32_t)(col / cs)), acc[m][i]);
+          const int col = wr * 16 + (lane >> 2) + (i >> 1) * 8, row = m * 8 + (XBLOCK ? t + 4 * (i & 1) : 2 * t + (i & 1));
+          if (row >= p.M) continue;
+          if (WK == 1 && ranks == 1) {  // nothing is left to be added
+            if (tile * R + col < p.N)
+              store_value(p.out, p.tc, (int64_t)row * p.ldc + tile * R + col, acc[m][i] * Unpack<F>::kBack);
+            continue;
           }
+          const uint32_t at = smem_u32(buf + (part * p.M + row) * cs + col % cs);
+          st_cluster_f32(map_to_rank(at, (uint32_t)(col / cs)), acc[m][i]);
         }
       if (ranks > 1) break;
       // Two buffers: one is written again only past the next tile's barrier,
       // which a warp meets when it has read this one.
       if constexpr (WK > 1) {
         computing_warps_sync();
-        for (int o = threadIdx.x; o < p.M * R; o += 32 * kWarps) store_sum<W4, WK>(p, buf, R, tile * R, o);
-      } else {  // a warp's columns are its own
-        __syncwarp();
-        for (int o = lane; o < p.M * 16; o += 32) store_sum<W4, WK>(p, buf, R, tile * R, (o >> 4) * R + wr * 16 + (o & 15));
-        __syncwarp();
+        for (int o = threadIdx.x; o < p.M * R; o += 32 * kWarps) store_sum<F, WK>(p, buf, R, tile * R, o);
       }
     }
   }
   if (ranks > 1) {
     cluster_sync_all();
     const int cs = R / ranks;
-    for (int o = threadIdx.x; o < p.M * cs; o += kThreads) store_sum<W4, 0>(p, parts, cs, tile0 * R + rank * cs, o, ranks * WK);
+    for (int o = threadIdx.x; o < p.M * cs; o += kThreads) store_sum<F, 0>(p, parts, cs, tile0 * R + rank * cs, o, ranks * WK);
   }
 }
 
@@ -407,8 +444,8 @@ mm_status run(const TmaRows &rx, const TmaRows &rw, int K, GemvParams p, LaunchC
            ? encode_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, rx.p, (uint64_t)K, (uint64_t)rx.rows,
                            (uint64_t)rx.ld, 128, (uint32_t)p.M, CU_TENSOR_MAP_SWIZZLE_128B)
            : encode_map_2d(&mx, F == FMT_W4_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                           rx.p, (uint64_t)K, (uint64_t)rx.rows, (uint64_t)rx.ld, 256, (uint32_t)p.M,
-                           CU_TENSOR_MAP_SWIZZLE_NONE);
+                           rx.p, (uint64_t)K, (uint64_t)rx.rows, (uint64_t)rx.ld, kXBlock<F, WR> ? 64 : 256,
+                           (uint32_t)p.M, kXBlock<F, WR> ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
   if (st != MM_OK) return st;
   p.panels = (int)((rw.bytes + 127) / 128);
   const int tiles = (p.N + R - 1) / R;

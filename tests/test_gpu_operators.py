@@ -418,6 +418,20 @@ def test_w4_long_k(M, group):
         assert T().equal(run_w4(a, codes, ldw, s, z, N, K, group, t), first)
 
 
+@pytest.mark.parametrize("M", [1, 3, 8, 13, 16])
+@pytest.mark.parametrize("N,K,group", [(40009, 300, 32), (40009, 1100, 64), (20011, 2500, 128)])
+def test_w4_many_rows_of_weights(M, N, K, group):
+    """More tiles than the device holds at a time: a block takes several in turn."""
+    g = generator(M + N + K)
+    t = (H, F, F) if group == 64 else (BF, BF, BF)
+    a = rows_of(g, M, K, t[0])
+    codes, ldw, s, z, w = w4_weights(g, N, K, group, t[1], group != 128)
+    first = run_w4(a, codes, ldw, s, z, N, K, group, t)
+    check_w4(a, w, t, first)
+    for _ in range(4):
+        assert T().equal(run_w4(a, codes, ldw, s, z, N, K, group, t), first)
+
+
 @pytest.mark.parametrize("M", [1, 5, 16, 40])
 @pytest.mark.parametrize("K", [1, 2, 15, 31, 32, 33, 63, 64, 127, 129, 255, 257])
 def test_w4_short_k(M, K):
@@ -556,6 +570,16 @@ def test_q8_sizes(M, N, K):
         a, b = q8_rows(g, M, K, -K % 16), q8_rows(g, N, K, -K % 16)
         sa, sb = q8_scales(g, M), q8_scales(g, N)
         check_q8(a, b, sa, sb, tc, run_q8(a, b, sa, sb, tc, pad))
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 8])
+@pytest.mark.parametrize("N,K", [(6100, 130), (6144, 2064), (5000, 900)])
+def test_q8_many_rows_of_weights(M, N, K):
+    """More tiles than the device holds at a time: a block takes several in turn."""
+    g = generator(M + N + K)
+    a, b = q8_rows(g, M, K), q8_rows(g, N, K)
+    sa, sb = q8_scales(g, M), q8_scales(g, N)
+    check_q8(a, b, sa, sb, F, run_q8(a, b, sa, sb, F))
 
 
 @pytest.mark.parametrize("M", [1, 12, 70, 300])
