@@ -134,6 +134,51 @@ __device__ __forceinline__ void load_pieces(const void *p, int t, int64_t i, int
   else if (t == MM_F16) load_pieces<MM_F16>(p, i, step, n, out);
   else load_pieces<MM_F32>(p, i, step, n, out);
 }
+// The same for pieces that start `shift` elements into a whole one (the same for
+// every thread): the two whole ones that hold a piece are loaded, the second of
+// them is the next thread's first, and shifted in registers.
+template <int TX, int E, int N>
+__device__ __forceinline__ void load_pieces_at(const void *p, int64_t i, int64_t step, int n, int shift,
+                                               float (&out)[N][E]) {
+  if (E == 1 || shift == 0) return load_pieces<TX>(p, i, step, n, out);
+  using P = Piece<TX, E>;
+  constexpr int W = (P::kBytes + 3) / 4;  // words
+  P first[N], second[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (k < n) {
+      first[k] = P::load(at<TX>(p, i + k * step - shift));
+      second[k] = P::load(at<TX>(p, i + k * step - shift + E));
+    }
+  const int words = shift * bytes_of(TX) / 4, bits = bytes_of(TX) == 2 ? (shift & 1) * 16 : 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    uint32_t w[2 * W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j] = first[k].w[j], w[W + j] = second[k].w[j];
+#pragma unroll
+    for (int b = W / 2; b > 0; b /= 2)
+#pragma unroll
+      for (int j = 0; j + b < 2 * W; ++j) w[j] = words & b ? w[j + b] : w[j];
+    P x;
+#pragma unroll
+    for (int j = 0; j < W; ++j) x.w[j] = bytes_of(TX) == 2 ? __funnelshift_r(w[j], w[j + 1], bits) : w[j];
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[k][e] = k < n ? x.get(e) : 0.f;
+  }
+}
+template <int E, int N>
+__device__ __forceinline__ void load_pieces_at(const void *p, int t, int64_t i, int64_t step, int n, int shift,
+                                               float (&out)[N][E]) {
+  if (t == MM_BF16) load_pieces_at<MM_BF16>(p, i, step, n, shift, out);
+  else if (t == MM_F16) load_pieces_at<MM_F16>(p, i, step, n, shift, out);
+  else load_pieces_at<MM_F32>(p, i, step, n, shift, out);
+}
+// How far into a whole piece of E elements element i lies.
+template <int E>
+__device__ __forceinline__ int piece_shift(const void *p, int element_bytes, int64_t i) {
+  return (int)(((uintptr_t)p / element_bytes + (uint64_t)i) % E);
+}
 // How many of the N pieces i, i + step, ... start below `end`.
 template <int N>
 __device__ __forceinline__ int pieces_below(int64_t i, int64_t step, int64_t end) {
@@ -215,10 +260,16 @@ __device__ __forceinline__ float row_scale(float amax) {
 }
 
 // ---------------------------------------------------------------- forward
-// T threads a row (a warp, eight of them a block, or a block), V pieces of E elements a thread:
-// the row of T V E elements or fewer stays in registers.  Pieces past cols are
-// not accessed (cols is a multiple of E).
-template <int TX, int E, int T, int V>
+// T threads a row (a warp, eight of them a block, or a block), V pieces of E
+// elements a thread: the row of T V E elements or fewer stays in registers.
+// Pieces past cols are not accessed (without EDGES cols is a multiple of E).
+// EDGES: rows that start anywhere.  The pieces are those that y stores whole; an
+// input that lies otherwise is read by whole pieces of its own, two for one (h
+// that lies otherwise is stored an element at a time).  Only pieces whose reads
+// stay inside the row are taken so; the elements before and behind, 29 at most,
+// go to the row's first threads, one each.  An element is read by other threads
+// than the one that writes it only where x or the residual is not an output.
+template <int TX, int E, int T, int V, bool EDGES>
 __global__ void __launch_bounds__(T == 32 ? 256 : T) rmsnorm_rows_kernel(const NormArgs a) {
   constexpr int ROWS = T == 32 ? 8 : 1;
   pdl_launch_dependents();
@@ -227,19 +278,42 @@ __global__ void __launch_bounds__(T == 32 ? 256 : T) rmsnorm_rows_kernel(const N
   const int t = threadIdx.x % T;
   const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / T;
   if (T == 32 && r >= a.rows) return;  // (no barrier below)
-  const int n = max(0, (a.cols - t * E + T * E - 1) / (T * E));  // this thread's pieces
+  int head = 0, end = a.cols, edge = -1;  // the pieces' [head, end), and this thread's element outside
+  int sx = 0, sr = 0, sw = 0;
+  bool whole_h = true;
+  if constexpr (EDGES) {
+    head = (E - piece_shift<E>(a.y, a.scale ? 1 : a.ty == MM_F32 ? 4 : 2, r * a.ldy)) % E;
+    sx = piece_shift<E>(a.x, bytes_of(TX), r * a.ldx + head);
+    if (a.residual) sr = piece_shift<E>(a.residual, bytes_of(TX), r * a.ldr + head);
+    sw = piece_shift<E>(a.weight, a.tw == MM_F32 ? 4 : 2, head);
+    whole_h = piece_shift<E>(a.h, bytes_of(TX), r * a.ldh + head) == 0;
+    if (sx | sr | sw) {  // [j - shift, j - shift + 2 E) of a piece at j lies inside
+      head += E;
+      end = a.cols - (E - 1);
+    }
+    end = head + max(0, end - head) / E * E;
+    if (end == head) head = end = min(head, a.cols);
+    if (t < head) edge = t;
+    else if (end + t - head < a.cols) edge = end + t - head;
+  }
+  const int j0 = head + t * E;
+  const int n = max(0, (end - j0 + T * E - 1) / (T * E));  // this thread's pieces
   float h[V][E], w[V][E];
-  load_pieces<TX>(a.x, r * a.ldx + t * E, T * E, n, h);
+  float eh = 0.f, ew = 0.f;
+  load_pieces_at<TX>(a.x, r * a.ldx + j0, T * E, n, EDGES ? sx : 0, h);
+  if (EDGES && edge >= 0) eh = load_value(a.x, TX, r * a.ldx + edge);
   if (a.residual) {
     float res[V][E];
-    load_pieces<TX>(a.residual, r * a.ldr + t * E, T * E, n, res);
+    load_pieces_at<TX>(a.residual, r * a.ldr + j0, T * E, n, EDGES ? sr : 0, res);
+    if (EDGES && edge >= 0) eh += load_value(a.residual, TX, r * a.ldr + edge);
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int e = 0; e < E; ++e) h[v][e] += res[v][e];
   }
-  load_pieces(a.weight, a.tw, t * E, T * E, n, w);
-  float ss = 0.f;
+  load_pieces_at(a.weight, a.tw, j0, T * E, n, EDGES ? sw : 0, w);
+  if (EDGES && edge >= 0) ew = load_value(a.weight, a.tw, edge);
+  float ss = eh * eh;
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -247,51 +321,63 @@ __global__ void __launch_bounds__(T == 32 ? 256 : T) rmsnorm_rows_kernel(const N
   if (a.h) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int j = (v * T + t) * E;
-      if (j < a.cols) store_piece<TX>(a.h, r * a.ldh + j, h[v]);
+      const int j = j0 + v * T * E;
+      if (j >= end) break;
+      if (!EDGES || whole_h) {
+        store_piece<TX>(a.h, r * a.ldh + j, h[v]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) store_value(a.h, TX, r * a.ldh + j + e, h[v][e]);
+      }
     }
+    if (EDGES && edge >= 0) store_value(a.h, TX, r * a.ldh + edge, eh);
   }
-  float inv = 1.f;
   if (a.scale) {
     uint32_t big = 0;  // of |h w|: y is this times rstd
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if ((v * T + t) * E < a.cols)
+      if (j0 + v * T * E < end)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           h[v][e] *= w[v][e];
           big = max(big, __float_as_uint(fabsf(h[v][e])));
         }
+    if (EDGES && edge >= 0) {
+      eh *= ew;
+      big = max(big, __float_as_uint(fabsf(eh)));
+    }
     row_sum_max<T>(ss, big, sh);
     const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
     const float scale = row_scale(__uint_as_float(big) * rstd);
-    inv = rstd * (1.f / scale);
+    const float inv = rstd * (1.f / scale);
     if (t == 0) {
       a.scale[r] = scale;
       if (a.rstd) a.rstd[r] = rstd;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int j = (v * T + t) * E;
-      if (j < a.cols) {
+      const int j = j0 + v * T * E;
+      if (j < end) {
 #pragma unroll
         for (int e = 0; e < E; ++e) h[v][e] *= inv;
         store_piece(a.y, MM_E4M3, r * a.ldy + j, h[v]);
       }
     }
+    if (EDGES && edge >= 0) static_cast<uint8_t *>(a.y)[r * a.ldy + edge] = to_e4m3(eh * inv);
   } else {
     ss = row_sum<T>(ss, sh);
     const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
     if (a.rstd && t == 0) a.rstd[r] = rstd;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int j = (v * T + t) * E;
-      if (j < a.cols) {
+      const int j = j0 + v * T * E;
+      if (j < end) {
 #pragma unroll
         for (int e = 0; e < E; ++e) h[v][e] = h[v][e] * rstd * w[v][e];
         store_piece(a.y, a.ty, r * a.ldy + j, h[v]);
       }
     }
+    if (EDGES && edge >= 0) store_value(a.y, a.ty, r * a.ldy + edge, eh * rstd * ew);
   }
 }
 
@@ -384,36 +470,43 @@ struct Alignment {
 
 int type_size(int t) { return t == MM_E4M3 ? 1 : dtype_bytes(t); }
 
-template <int TX, int E, int T, int V>
+template <int TX, int E, int T, int V, bool EDGES>
 mm_status rows_form(const NormArgs &a, LaunchCtx &ctx) {
   constexpr int ROWS = T == 32 ? 8 : 1;
   const int64_t blocks = (a.rows + ROWS - 1) / ROWS;
   if (blocks >= (1LL << 31)) return set_error(MM_ERR_UNSUPPORTED, "too many rows");
-  return launch(rmsnorm_rows_kernel<TX, E, T, V>, blocks, T == 32 ? 256 : T, ctx, "rmsnorm launch", a);
+  return launch(rmsnorm_rows_kernel<TX, E, T, V, EDGES>, blocks, T == 32 ? 256 : T, ctx, "rmsnorm launch", a);
 }
-
-// A warp a row up to 128 pieces, then a block of 256 to 1024.
 template <int TX, int E>
-mm_status forward_form(const NormArgs &a, LaunchCtx &ctx) {
-  const int pieces = (a.cols + E - 1) / E;
-  if (pieces <= 64) return rows_form<TX, E, 32, 2>(a, ctx);
-  if (pieces <= 128) return rows_form<TX, E, 32, 4>(a, ctx);
-  if (pieces <= 256) return rows_form<TX, E, 256, 1>(a, ctx);
-  if constexpr (E > 1) {
-    if (pieces <= 512) return rows_form<TX, E, 256, 2>(a, ctx);
-    if (pieces <= 1024) return rows_form<TX, E, 512, 2>(a, ctx);
-    if (pieces <= 2048) return rows_form<TX, E, 1024, 2>(a, ctx);
-  } else {
-    // single elements: eight to sixteen a thread, so that enough of them are in flight
-    if (pieces <= 1024) return rows_form<TX, E, 128, 8>(a, ctx);
-    if (pieces <= 2048) return rows_form<TX, E, 256, 8>(a, ctx);
-    if (pieces <= 4096) return rows_form<TX, E, 512, 8>(a, ctx);
-    if (pieces <= 5120) return rows_form<TX, E, 512, 10>(a, ctx);
-    if (pieces <= 8192) return rows_form<TX, E, 512, 16>(a, ctx);
-    if (pieces <= 16384) return rows_form<TX, E, 1024, 16>(a, ctx);
-  }
+mm_status long_form(const NormArgs &a, LaunchCtx &ctx) {
   return launch(rmsnorm_long_kernel<TX, E>, std::min<int64_t>(a.rows, 2 * ctx.dev->info.sms), 1024, ctx,
                 "rmsnorm launch (long rows)", a);
+}
+
+// A warp a row up to 128 pieces, then a block of 256 to 1024 (8192 x 4096 bf16:
+// 42 us, 6.4 TB/s; to e4m3 40 us).  Rows that start anywhere: up to 256 elements a
+// warp and an element an access (its pieces would leave most lanes idle: 100000 x
+// 101 f16 29 us against 63), above that in pieces and blocks half as large, since
+// the reads of two pieces for one need the registers (8192 x 4097 bf16 52 us, an
+// element an access 75; 33000 x 1001 50 and 62; with the aligned rows' blocks
+// 16384 x 1601 58 us, with these 47).
+template <int TX, bool EDGES>
+mm_status forward_form(const NormArgs &a, LaunchCtx &ctx) {
+  constexpr int E = 16 / bytes_of(TX);
+  const int pieces = a.cols / E;
+  if (EDGES && a.cols <= 128) return rows_form<TX, 1, 32, 4, false>(a, ctx);
+  if (EDGES && a.cols <= 256) return rows_form<TX, 1, 32, 8, false>(a, ctx);
+  if (pieces <= 64) return rows_form<TX, E, 32, 2, EDGES>(a, ctx);
+  if (EDGES && pieces <= 128) return rows_form<TX, E, 64, 2, EDGES>(a, ctx);
+  if (pieces <= 128) return rows_form<TX, E, 32, 4, EDGES>(a, ctx);
+  if (EDGES && pieces <= 256) return rows_form<TX, E, 128, 2, EDGES>(a, ctx);
+  if (pieces <= 256) return rows_form<TX, E, 256, 1, EDGES>(a, ctx);
+  if (pieces <= 512) return rows_form<TX, E, 256, 2, EDGES>(a, ctx);
+  if (pieces <= 1024) return rows_form<TX, E, 512, 2, EDGES>(a, ctx);
+  if (pieces <= 2048) return rows_form<TX, E, 1024, 2, EDGES>(a, ctx);
+  if constexpr (E == 4)
+    if (pieces <= 4096) return rows_form<TX, E, 1024, 4, EDGES>(a, ctx);
+  return long_form<TX, EDGES ? 1 : E>(a, ctx);
 }
 
 template <int TX>
@@ -426,7 +519,12 @@ mm_status forward_type(const NormArgs &a, LaunchCtx &ctx) {
   al.operand(a.h, a.ldh, a.rows, type_size(a.tx));
   al.operand(a.y, a.ldy, a.rows, type_size(a.ty));
   constexpr int most = 16 / bytes_of(TX);
-  return al.elements(most) == most ? forward_form<TX, most>(a, ctx) : forward_form<TX, 1>(a, ctx);
+  if (al.elements(most) == most) return forward_form<TX, false>(a, ctx);
+  // In place at another distance than y's: see the kernel's last sentence.
+  const uint64_t d = (uint64_t)(uintptr_t)a.h / bytes_of(TX) - (uint64_t)(uintptr_t)a.y / type_size(a.ty);
+  const bool alike = d % most == 0 && (a.rows == 1 || (uint64_t)(a.ldh - a.ldy) % most == 0);
+  if (a.h && (a.h == a.x || a.h == a.residual) && !alike) return long_form<TX, 1>(a, ctx);
+  return forward_form<TX, true>(a, ctx);
 }
 
 // ---------------------------------------------------------------- backward

@@ -170,6 +170,38 @@ def test_norm_bases_off_16_bytes(offset, t):
         check_norm(x, r, w, t, run_norm(x, r, w, t, pad=pad, offset=offset))
 
 
+@pytest.mark.parametrize("cols", [1, 9, 14, 15, 16, 23, 24, 30, 31, 37, 129, 257, 263, 300, 511, 520, 601, 1003,
+                                  1030, 2051, 4100, 8203, 16387])
+@pytest.mark.parametrize("t", [(BF, BF, BF), (BF, F, Q), (H, H, F), (F, F, F), (F, BF, Q)])
+def test_norm_rows_that_start_anywhere(cols, t):
+    """Every operand at its own offset and row distance."""
+    torch = T()
+    g = generator(cols)
+    rows = 9
+    for i, (px, pr, ph, py) in enumerate(((0, 0, 0, 0), (1, 1, 1, 1), (3, 0, 5, 0), (0, 1, 2, 3), (5, 7, 0, 1))):
+        x, r = rows_of(g, rows, cols, t[0], px, offset=i), rows_of(g, rows, cols, t[0], pr, 2.0, offset=3 * i)
+        w = rows_of(g, 1, cols, t[1], offset=i)[0]
+        h, h_ok = out_rows(rows, cols, t[0], ph, 2 * i)
+        y, y_ok = out_rows(rows, cols, t[2], py, i)
+        scale = torch.empty(rows, device="cuda") if t[2] == Q else None
+        rstd = torch.empty(rows, device="cuda")
+
+        def run(x, r, h):
+            mm.check(mm.mm_rmsnorm(x, r, w, h, y, scale, rstd, rows, cols, x.stride(0), r.stride(0), h.stride(0),
+                                   y.stride(0), t, EPS))
+            torch.cuda.synchronize()
+            y_ok()
+        run(x, r, h)
+        h_ok()
+        check_norm(x, r, w, t, (h, y, scale, rstd))
+        x0, r0 = x.clone(), r.clone()
+        run(x, r, x)  # h over x
+        check_norm(x0, r0, w, t, (x, y, scale, rstd))
+        x.copy_(x0)
+        run(x, r, r)  # h over the residual
+        check_norm(x0, r0, w, t, (r, y, scale, rstd))
+
+
 @pytest.mark.parametrize("cols", [64, 4096, 4099, 70001])
 def test_norm_in_place(cols):
     torch = T()
