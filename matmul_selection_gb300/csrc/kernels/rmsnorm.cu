@@ -134,15 +134,32 @@ __device__ __forceinline__ void load_pieces(const void *p, int t, int64_t i, int
   else if (t == MM_F16) load_pieces<MM_F16>(p, i, step, n, out);
   else load_pieces<MM_F32>(p, i, step, n, out);
 }
-// The same for pieces that start `shift` elements into a whole one (the same for
-// every thread): the two whole ones that hold a piece are loaded, the second of
-// them is the next thread's first, and shifted in registers.
+// The piece that starts `shift` elements (the same for every thread) into the
+// first of two that follow one another.
+template <int TX, int E>
+__device__ __forceinline__ Piece<TX, E> shifted(const Piece<TX, E> &first, const Piece<TX, E> &second, int shift) {
+  constexpr int W = (Piece<TX, E>::kBytes + 3) / 4;  // words
+  const int words = shift * bytes_of(TX) / 4, bits = bytes_of(TX) == 2 ? (shift & 1) * 16 : 0;
+  uint32_t w[2 * W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) w[j] = first.w[j], w[W + j] = second.w[j];
+#pragma unroll
+  for (int b = W / 2; b > 0; b /= 2)
+#pragma unroll
+    for (int j = 0; j + b < 2 * W; ++j) w[j] = words & b ? w[j + b] : w[j];
+  Piece<TX, E> x;
+#pragma unroll
+  for (int j = 0; j < W; ++j) x.w[j] = bytes_of(TX) == 2 ? __funnelshift_r(w[j], w[j + 1], bits) : w[j];
+  return x;
+}
+// The same as load_pieces for pieces that start `shift` elements into a whole
+// one: the two whole ones that hold a piece are loaded (the second of them is the
+// next thread's first) and shifted in registers.
 template <int TX, int E, int N>
 __device__ __forceinline__ void load_pieces_at(const void *p, int64_t i, int64_t step, int n, int shift,
                                                float (&out)[N][E]) {
-  if (E == 1 || shift == 0) return load_pieces<TX>(p, i, step, n, out);
+  if (shift == 0) return load_pieces<TX>(p, i, step, n, out);
   using P = Piece<TX, E>;
-  constexpr int W = (P::kBytes + 3) / 4;  // words
   P first[N], second[N];
 #pragma unroll
   for (int k = 0; k < N; ++k)
@@ -150,19 +167,9 @@ __device__ __forceinline__ void load_pieces_at(const void *p, int64_t i, int64_t
       first[k] = P::load(at<TX>(p, i + k * step - shift));
       second[k] = P::load(at<TX>(p, i + k * step - shift + E));
     }
-  const int words = shift * bytes_of(TX) / 4, bits = bytes_of(TX) == 2 ? (shift & 1) * 16 : 0;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    uint32_t w[2 * W];
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j] = first[k].w[j], w[W + j] = second[k].w[j];
-#pragma unroll
-    for (int b = W / 2; b > 0; b /= 2)
-#pragma unroll
-      for (int j = 0; j + b < 2 * W; ++j) w[j] = words & b ? w[j + b] : w[j];
-    P x;
-#pragma unroll
-    for (int j = 0; j < W; ++j) x.w[j] = bytes_of(TX) == 2 ? __funnelshift_r(w[j], w[j + 1], bits) : w[j];
+    const P x = shifted(first[k], second[k], shift);
 #pragma unroll
     for (int e = 0; e < E; ++e) out[k][e] = k < n ? x.get(e) : 0.f;
   }
@@ -528,7 +535,7 @@ mm_status forward_type(const NormArgs &a, LaunchCtx &ctx) {
 }
 
 // ---------------------------------------------------------------- backward
-// Three forms, by the length of a row and its alignment.  Each block walks the
+// Three forms, by the length of a row.  Each block walks the
 // rows blockIdx.x, blockIdx.x + gridDim.x, ... (or its warps do) and keeps its
 // sums of dy h rstd in registers; the blocks' sums go to a workspace and a
 // second kernel adds them in block order.
@@ -621,8 +628,18 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_warps_kernel(const NormBwdArg
 // of HBM's rate.)  Both passes read the row from shared memory.  A stage is
 // refilled after the next row's barrier, which every thread reaches only when
 // it is done with the row before.
+// EDGES: rows that start anywhere, as in the forward kernel: dx's pieces, inputs
+// that lie otherwise read two pieces for one, the elements before and behind one a
+// thread, straight from memory, a row ahead.  The grid is a multiple of E blocks,
+// so that a block's rows all lie alike and its sums keep their columns; bulk
+// copies take what of a row is whole pieces.
 constexpr int kMaxRing = 8, kErrRing = 0xb01;
-template <int TX, int T, int V, int PER_SM>
+// A row in the ring: what lies before it in its first 16 bytes comes with it.
+template <bool EDGES>
+constexpr __host__ __device__ uint32_t ring_row(uint32_t bytes) {
+  return EDGES ? (bytes + 30) / 16 * 16 : bytes;
+}
+template <int TX, int T, int V, int PER_SM, bool EDGES>
 __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormBwdArgs a, float *partial, int stages,
                                                               int *err) {
   constexpr int E = 16 / bytes_of(TX);
@@ -632,7 +649,8 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
   __shared__ float sh[2][2 * (T / 32)];
   __shared__ __align__(8) uint64_t full[kMaxRing];
   const int t = threadIdx.x;
-  const uint32_t row = (uint32_t)a.cols * bytes_of(TX), parts = a.dh ? 3 : 2, stage_bytes = parts * row;
+  const uint32_t bytes = (uint32_t)a.cols * bytes_of(TX), row = ring_row<EDGES>(bytes), parts = a.dh ? 3 : 2,
+                 stage_bytes = parts * row;
   if (t == 0) {
     for (int s = 0; s < stages; ++s) tc::mbar_init(tc::smem_u32(full + s), 1);
     tc::mbar_init_fence();
@@ -641,29 +659,87 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
   pdl_wait();
   auto fill = [&](int64_t r, int s) {  // one thread
     const uint32_t bar = tc::smem_u32(full + s), dst = tc::smem_u32(ring) + (uint32_t)s * stage_bytes;
-    tc::mbar_expect_tx_one(bar, stage_bytes);
-    tc::bulk_load(dst, at<TX>(a.dy, r * a.lddy), row, bar);
-    tc::bulk_load(dst + row, at<TX>(a.h, r * a.ldh), row, bar);
-    if (a.dh) tc::bulk_load(dst + 2 * row, at<TX>(a.dh, r * a.lddh), row, bar);
+    if constexpr (!EDGES) {
+      tc::mbar_expect_tx_one(bar, stage_bytes);
+      tc::bulk_load(dst, at<TX>(a.dy, r * a.lddy), row, bar);
+      tc::bulk_load(dst + row, at<TX>(a.h, r * a.ldh), row, bar);
+      if (a.dh) tc::bulk_load(dst + 2 * row, at<TX>(a.dh, r * a.lddh), row, bar);
+    } else {
+      const char *p[3] = {static_cast<const char *>(at<TX>(a.dy, r * a.lddy)),
+                          static_cast<const char *>(at<TX>(a.h, r * a.ldh)),
+                          static_cast<const char *>(at<TX>(a.dh, a.dh ? r * a.lddh : 0))};
+      uint32_t skip[3], size[3], all = 0;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t off = (uint32_t)(uintptr_t)p[k] & 15u;
+        skip[k] = (16u - off) & 15u;
+        size[k] = k < (int)parts && skip[k] < bytes ? (bytes - skip[k]) & ~15u : 0u;
+        all += size[k];
+      }
+      tc::mbar_expect_tx_one(bar, all);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (size[k]) tc::bulk_load(dst + k * row + (skip[k] ? 16u : 0u), p[k] + skip[k], size[k], bar);
+    }
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s)
       if (blockIdx.x + (int64_t)s * gridDim.x < a.rows) fill(blockIdx.x + (int64_t)s * gridDim.x, s);
+  // the pieces' [head, end), this thread's element outside; how far into whole
+  // pieces the inputs' are, and where a row's pieces start in the ring
+  int head = 0, end = a.cols, edge = -1, s_dy = 0, s_h = 0, s_dh = 0, s_w = 0;
+  uint32_t o_dy = 0, o_h = row, o_dh = 2 * row;
+  if constexpr (EDGES) {
+    const int64_t r = blockIdx.x;
+    head = (E - piece_shift<E>(a.dx, bytes_of(TX), r * a.lddx)) % E;
+    s_dy = piece_shift<E>(a.dy, bytes_of(TX), r * a.lddy + head);
+    s_h = piece_shift<E>(a.h, bytes_of(TX), r * a.ldh + head);
+    if (a.dh) s_dh = piece_shift<E>(a.dh, bytes_of(TX), r * a.lddh + head);
+    s_w = piece_shift<E>(a.weight, a.tw == MM_F32 ? 4 : 2, head);
+    if (s_dy | s_h | s_dh | s_w) {  // [j - shift, j - shift + 2 E) of a piece at j lies inside
+      head += E;
+      end = a.cols - (E - 1);
+    }
+    end = head + max(0, end - head) / E * E;
+    if (end == head) head = end = min(head, a.cols);
+    if (t < head) edge = t;
+    else if (end + t - head < a.cols) edge = end + t - head;
+    // whole pieces: a multiple of 16 bytes into the row's place
+    o_dy += (uint32_t)((piece_shift<E>(a.dy, bytes_of(TX), r * a.lddy) + head - s_dy) * bytes_of(TX));
+    o_h += (uint32_t)((piece_shift<E>(a.h, bytes_of(TX), r * a.ldh) + head - s_h) * bytes_of(TX));
+    if (a.dh) o_dh += (uint32_t)((piece_shift<E>(a.dh, bytes_of(TX), r * a.lddh) + head - s_dh) * bytes_of(TX));
+  }
+  const int n = max(0, (end - head - t * E + T * E - 1) / (T * E));  // this thread's pieces
+  auto piece = [&](const uint8_t *p, int i, int shift) {
+    const P x = P::load(p + i * 16);
+    return EDGES && shift ? shifted(x, P::load(p + i * 16 + 16), shift) : x;
+  };
   float w[V][E], dw[V][E] = {};
-  load_pieces(a.weight, a.tw, t * E, T * E, max(0, (a.cols - t * E + T * E - 1) / (T * E)), w);
+  load_pieces_at(a.weight, a.tw, head + t * E, T * E, n, EDGES ? s_w : 0, w);
+  float ew = 0.f, edw = 0.f, next_dy = 0.f, next_h = 0.f, next_dh = 0.f;
+  auto load_edge = [&](int64_t r) {
+    if (!EDGES || edge < 0 || r >= a.rows) return;
+    next_dy = load_value(a.dy, TX, r * a.lddy + edge);
+    next_h = load_value(a.h, TX, r * a.ldh + edge);
+    if (a.dh) next_dh = load_value(a.dh, TX, r * a.lddh + edge);
+  };
+  if (EDGES && edge >= 0) ew = load_value(a.weight, a.tw, edge);
+  load_edge(blockIdx.x);
   const float per_col = 1.f / (float)a.cols;
   int s = 0, side = 0;
   uint32_t phase = 0;
   bool gave_up = false;  // (a wait ran into its limit: no further one is waited for)
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const float given = a.rstd ? a.rstd[r] : 0.f;
-    const uint8_t *dy = ring + (size_t)s * stage_bytes, *h = dy + row, *dh = h + row;
-    float dot = 0.f, ss = 0.f;
+    const uint8_t *stage = ring + (size_t)s * stage_bytes, *dy = stage + o_dy, *h = stage + o_h, *dh = stage + o_dh;
+    const float edy = next_dy, eh = next_h, edh = next_dh;
+    load_edge(r + gridDim.x);
+    float dot = edy * ew * eh, ss = eh * eh;
     if (!gave_up && !tc::thread_wait(tc::smem_u32(full + s), phase, err, kErrRing)) gave_up = true;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = v * T + t;
-      if (i * E < a.cols) BwdPiece<TX, E>::sums(P::load(dy + i * 16), P::load(h + i * 16), w[v], dot, ss);
+      if (v < n) BwdPiece<TX, E>::sums(piece(dy, i, s_dy), piece(h, i, s_h), w[v], dot, ss);
     }
     // two sets of shared sums in turn: one barrier a row
     dot = row_sum<T>(dot, sh[side]);
@@ -677,75 +753,39 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = v * T + t;
-      if (i * E < a.cols) {
+      if (v < n) {
         float dx[E];
         P d;
-        if (a.dh) d = P::load(dh + i * 16);
-        BwdPiece<TX, E>::outputs(P::load(dy + i * 16), P::load(h + i * 16), a.dh ? &d : nullptr, w[v], rs, c, dx, dw[v]);
-        store_piece<TX>(a.dx, r * a.lddx + i * E, dx);
+        if (a.dh) d = piece(dh, i, s_dh);
+        BwdPiece<TX, E>::outputs(piece(dy, i, s_dy), piece(h, i, s_h), a.dh ? &d : nullptr, w[v], rs, c, dx, dw[v]);
+        store_piece<TX>(a.dx, r * a.lddx + head + i * E, dx);
       }
+    }
+    if (EDGES && edge >= 0) {
+      store_value(a.dx, TX, r * a.lddx + edge, rs * (edy * ew - eh * c) + edh);
+      edw += edy * eh * rs;
     }
     if (++s == stages) {
       s = 0;
       phase ^= 1;
     }
   }
-  if (partial)
+  if (partial) {
+    float *out = partial + blockIdx.x * partial_ld(a.cols);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int j = (v * T + t) * E;
-      if (j < a.cols) store_piece<MM_F32>(partial, blockIdx.x * partial_ld(a.cols) + j, dw[v]);
+      const int j = head + (v * T + t) * E;
+      if (v < n) {
+        if constexpr (!EDGES) {
+          store_piece<MM_F32>(out, j, dw[v]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) out[j + e] = dw[v][e];
+        }
+      }
     }
-}
-
-// Rows that start anywhere: element by element, the row and the weight in
-// registers, many elements a thread, so that enough bytes are in flight.
-template <int TX, int T, int V, int PER_SM>
-__global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_elements_kernel(const NormBwdArgs a, float *partial) {
-  using P = Piece<TX, 1>;
-  pdl_launch_dependents();
-  pdl_wait();
-  __shared__ float sh[2][2 * (T / 32)];
-  const int t = threadIdx.x;
-  const int n = max(0, (a.cols - t + T - 1) / T);  // this thread's elements
-  float w[V][1], dw[V][1] = {};
-  load_pieces(a.weight, a.tw, t, T, n, w);
-  const float per_col = 1.f / (float)a.cols;
-  int side = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    P dy[V], h[V], dh[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v < n) {
-        dy[v] = P::load(at<TX>(a.dy, r * a.lddy + v * T + t));
-        h[v] = P::load(at<TX>(a.h, r * a.ldh + v * T + t));
-      }
-    if (a.dh)
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v < n) dh[v] = P::load(at<TX>(a.dh, r * a.lddh + v * T + t));
-    float rs = a.rstd ? a.rstd[r] : 0.f;
-    float dot = 0.f, ss = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v < n) BwdPiece<TX, 1>::sums(dy[v], h[v], w[v], dot, ss);
-    // two sets of shared sums in turn: one barrier a row
-    dot = row_sum<T>(dot, sh[side]);
-    if (!a.rstd) rs = 1.f / sqrtf(row_sum<T>(ss, sh[side] + T / 32) / (float)a.cols + a.eps);
-    side ^= 1;
-    const float c = dot * per_col * rs * rs;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v < n) {
-        float dx[1];
-        BwdPiece<TX, 1>::outputs(dy[v], h[v], a.dh ? &dh[v] : nullptr, w[v], rs, c, dx, dw[v]);
-        store_piece<TX>(a.dx, r * a.lddx + v * T + t, dx);
-      }
+    if (EDGES && edge >= 0) out[edge] = edw;
   }
-  if (partial)
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v < n) partial[blockIdx.x * partial_ld(a.cols) + v * T + t] = dw[v][0];
 }
 
 // Longer rows, and dy of another type than h: 1 / rms and the mean of g h of each row (two
@@ -893,26 +933,22 @@ mm_status bwd_warps_form(const NormBwdArgs &a, LaunchCtx &ctx) {
 
 constexpr size_t kRingBytes = 208 << 10;  // of an SM's shared memory
 
-template <int TX, int T, int V, int PER_SM>
+template <int TX, int T, int V, int PER_SM, bool EDGES>
 mm_status bwd_ring_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
-  auto kern = rmsnorm_bwd_ring_kernel<TX, T, V, PER_SM>;
+  auto kern = rmsnorm_bwd_ring_kernel<TX, T, V, PER_SM, EDGES>;
   std::call_once(once, [&] {
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
   });
   if (err != cudaSuccess) return cuda_error(err, "rmsnorm_backward set-up");
-  const size_t stage = (size_t)(a.dh ? 3 : 2) * a.cols * bytes_of(TX);
+  const size_t stage = (size_t)(a.dh ? 3 : 2) * ring_row<EDGES>((uint32_t)a.cols * bytes_of(TX));
   const int stages = (int)std::min<size_t>(kMaxRing, kRingBytes / PER_SM / stage);
   if (stages < 2) return set_error(MM_ERR_UNSUPPORTED, "rmsnorm_backward: no two rows fit the ring");
-  const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)PER_SM * ctx.dev->info.sms);
+  constexpr int E = 16 / bytes_of(TX);
+  const int64_t most = (int64_t)PER_SM * ctx.dev->info.sms;
+  const int64_t blocks = std::min<int64_t>(a.rows, EDGES ? std::max<int64_t>(E, most / E * E) : most);
   return bwd_blocks(a, kern, blocks, T, stages * stage, ctx, stages, ctx.dev->d_err + kOperatorErrorWord);
-}
-
-template <int TX, int T, int V, int PER_SM>
-mm_status bwd_elements_form(const NormBwdArgs &a, LaunchCtx &ctx) {
-  return bwd_blocks(a, rmsnorm_bwd_elements_kernel<TX, T, V, PER_SM>,
-                    std::min<int64_t>(a.rows, (int64_t)PER_SM * ctx.dev->info.sms), T, 0, ctx);
 }
 
 template <int TX, int E>
@@ -933,31 +969,34 @@ mm_status bwd_long_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   return a.dweight ? add_parts(a, partial, (int)down, ctx) : MM_OK;
 }
 
-template <int TX, int E>
+template <int TX, bool EDGES>
 mm_status bwd_form(const NormBwdArgs &a, LaunchCtx &ctx) {
-  const int pieces = (a.cols + E - 1) / E;
+  constexpr int E = 16 / bytes_of(TX);
+  const int pieces = a.cols / E;
   if (a.ty == TX) {
-    if (pieces <= 32) return bwd_warps_form<TX, E, 1>(a, ctx);
-    if (pieces <= 64) return bwd_warps_form<TX, E, 2>(a, ctx);
-    if (pieces <= 128) return bwd_warps_form<TX, E, 4>(a, ctx);
-    if constexpr (E > 1) {
-      // Threads and blocks an SM, measured (bf16, us for 33.5 M values in rows of
-      // 2048 / 4096 / 8192): 256 x 5 52.6 (x 4 66, x 3 76) / 512 x 2 50.6 (256 x
-      // 3 56; 512 x 3, of which two fit, 72) / 512 x 2 53 (1024 x 1 55)
-      if (pieces <= 256) return bwd_ring_form<TX, 256, 1, 5>(a, ctx);
-      if (pieces <= 512) return bwd_ring_form<TX, 512, 1, 2>(a, ctx);
-      if (pieces <= 1024) return bwd_ring_form<TX, 512, 2, 2>(a, ctx);
-      if (pieces <= 2048) return bwd_ring_form<TX, 1024, 2, 1>(a, ctx);
+    if constexpr (!EDGES) {
+      if (pieces <= 32) return bwd_warps_form<TX, E, 1>(a, ctx);
+      if (pieces <= 64) return bwd_warps_form<TX, E, 2>(a, ctx);
+      if (pieces <= 128) return bwd_warps_form<TX, E, 4>(a, ctx);
     } else {
-      if (pieces <= 512) return bwd_elements_form<TX, 64, 8, 16>(a, ctx);
-      if (pieces <= 1024) return bwd_elements_form<TX, 128, 8, 8>(a, ctx);
-      if (pieces <= 2048) return bwd_elements_form<TX, 128, 16, 5>(a, ctx);
-      if (pieces <= 4096) return bwd_elements_form<TX, 256, 16, 2>(a, ctx);
-      if (pieces <= 5120) return bwd_elements_form<TX, 256, 20, 2>(a, ctx);
-      if (pieces <= 8192) return bwd_elements_form<TX, 512, 16, 1>(a, ctx);
+      // Rows that start anywhere: up to 512 elements a warp and an element an
+      // access (50000 x 333 bf16: 49 us; the ring with 64 threads 84), above that
+      // the ring (33000 x 1001 76 us, an element an access 91; 8192 x 4097 73 and
+      // 130; 2000 x 16383 82 and 201).
+      if (a.cols <= 128) return bwd_warps_form<TX, 1, 4>(a, ctx);
+      if (a.cols <= 256) return bwd_warps_form<TX, 1, 8>(a, ctx);
+      if (a.cols <= 512) return bwd_warps_form<TX, 1, 16>(a, ctx);
+      if (pieces <= 128) return bwd_ring_form<TX, 128, 1, 8, EDGES>(a, ctx);
     }
+    // Threads and blocks an SM, measured (bf16, us for 33.5 M values in rows of
+    // 2048 / 4096 / 8192): 256 x 5 52.6 (x 4 66, x 3 76) / 512 x 2 50.6 (256 x
+    // 3 56; 512 x 3, of which two fit, 72) / 512 x 2 53 (1024 x 1 55)
+    if (pieces <= 256) return bwd_ring_form<TX, 256, 1, 5, EDGES>(a, ctx);
+    if (pieces <= 512) return bwd_ring_form<TX, 512, 1, 2, EDGES>(a, ctx);
+    if (pieces <= 1024) return bwd_ring_form<TX, 512, 2, 2, EDGES>(a, ctx);
+    if (pieces <= 2048) return bwd_ring_form<TX, 1024, 2, 1, EDGES>(a, ctx);
   }
-  return bwd_long_form<TX, E>(a, ctx);
+  return bwd_long_form<TX, EDGES ? 1 : E>(a, ctx);
 }
 
 template <int TX>
@@ -970,7 +1009,7 @@ mm_status bwd_type(const NormBwdArgs &a, LaunchCtx &ctx) {
   al.operand(a.weight, 0, 1, type_size(a.tw));
   al.operand(a.dx, a.lddx, a.rows, type_size(a.tx));
   constexpr int most = 16 / bytes_of(TX);
-  return al.elements(most) == most ? bwd_form<TX, most>(a, ctx) : bwd_form<TX, 1>(a, ctx);
+  return al.elements(most) == most ? bwd_form<TX, false>(a, ctx) : bwd_form<TX, true>(a, ctx);
 }
 
 }  // namespace

@@ -332,6 +332,31 @@ def test_bwd_many_rows(rows, cols):
         assert none is None and T().equal(dx, got[0])
 
 
+@pytest.mark.parametrize("cols", [3, 29, 129, 200, 257, 335, 511, 513, 527, 601, 1003, 1039, 2050, 4103, 8199, 16391])
+@pytest.mark.parametrize("t", [(BF, BF, BF), (H, F, H), (F, F, F), (F, BF, F)])
+def test_bwd_rows_that_start_anywhere(cols, t):
+    """Every operand at its own offset and row distance; few rows, and more than
+    the grid has blocks."""
+    torch = T()
+    g = generator(cols)
+    for i, (py, pd, ph, px) in enumerate(((0, 0, 0, 0), (1, 1, 1, 1), (3, 3, 3, 0), (0, 5, 2, 7), (1, 0, 0, 3))):
+        rows = 3001 if i % 2 and cols < 4200 else 700 if i % 2 else 11
+        dy, dh = rows_of(g, rows, cols, t[0], py, offset=i), rows_of(g, rows, cols, t[0], pd, offset=5 * i)
+        h = rows_of(g, rows, cols, t[0], ph, 2.0, offset=3 * i)
+        w = rows_of(g, 1, cols, t[1], offset=i)[0]
+        rstd = (1 / (h.float().square().mean(1) + EPS).sqrt()).contiguous() if i > 1 else None
+        check_bwd(dy, dh, h, w, t, run_bwd(dy, dh, h, w, t, rstd=rstd, pad=px), rstd=rstd)
+        for over in (dy, dh):  # in place
+            kept = dy.clone(), dh.clone()
+            dw = torch.empty(cols, dtype=ttype(t[1]), device="cuda")
+            mm.check(mm.mm_rmsnorm_backward(dy, dh, h, w, rstd, over, dw, rows, cols, dy.stride(0), dh.stride(0),
+                                            h.stride(0), over.stride(0), t, EPS))
+            torch.cuda.synchronize()
+            check_bwd(*kept, h, w, t, (over, dw), rstd=rstd)
+            dy.copy_(kept[0])
+            dh.copy_(kept[1])
+
+
 def test_bwd_no_rows_writes_zeros():
     torch = T()
     dw = torch.full((100,), 3.0, device="cuda")
