@@ -639,6 +639,74 @@ template <bool EDGES>
 constexpr __host__ __device__ uint32_t ring_row(uint32_t bytes) {
   return EDGES ? (bytes + 30) / 16 * 16 : bytes;
 }
+// One thread starts the copies of a row.
+template <int TX, bool EDGES>
+__device__ __forceinline__ void ring_fill(const NormBwdArgs &a, int64_t r, uint32_t dst, uint32_t bar) {
+  const uint32_t bytes = (uint32_t)a.cols * bytes_of(TX), row = ring_row<EDGES>(bytes), parts = a.dh ? 3 : 2;
+  if constexpr (!EDGES) {
+    tc::mbar_expect_tx_one(bar, parts * row);
+    tc::bulk_load(dst, at<TX>(a.dy, r * a.lddy), row, bar);
+    tc::bulk_load(dst + row, at<TX>(a.h, r * a.ldh), row, bar);
+    if (a.dh) tc::bulk_load(dst + 2 * row, at<TX>(a.dh, r * a.lddh), row, bar);
+  } else {
+    const char *p[3] = {static_cast<const char *>(at<TX>(a.dy, r * a.lddy)),
+                        static_cast<const char *>(at<TX>(a.h, r * a.ldh)),
+                        static_cast<const char *>(at<TX>(a.dh, a.dh ? r * a.lddh : 0))};
+    uint32_t skip[3], size[3], all = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t off = (uint32_t)(uintptr_t)p[k] & 15u;
+      skip[k] = (16u - off) & 15u;
+      size[k] = k < (int)parts && skip[k] < bytes ? (bytes - skip[k]) & ~15u : 0u;
+      all += size[k];
+    }
+    tc::mbar_expect_tx_one(bar, all);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (size[k]) tc::bulk_load(dst + k * row + (skip[k] ? 16u : 0u), p[k] + skip[k], size[k], bar);
+  }
+}
+// Where the columns of a block's rows lie: the pieces' [head, end); how far into
+// whole pieces the inputs' are; where the inputs' pieces start in the ring's row.
+struct RingPlace {
+  int head, end, s_dy, s_h, s_dh, s_w;
+  uint32_t o_dy, o_h, o_dh;
+  // the element outside the pieces that the t-th of a row's threads has, or -1
+  __device__ __forceinline__ int edge(int t, int cols) const {
+    return t < head ? t : end + t - head < cols ? end + t - head : -1;
+  }
+};
+template <int TX, bool EDGES>
+__device__ __forceinline__ RingPlace ring_place(const NormBwdArgs &a, int64_t r) {
+  constexpr int E = 16 / bytes_of(TX), es = bytes_of(TX);
+  const uint32_t row = ring_row<EDGES>((uint32_t)a.cols * es);
+  RingPlace p{0, a.cols, 0, 0, 0, 0, 0, row, 2 * row};
+  if constexpr (EDGES) {
+    p.head = (E - piece_shift<E>(a.dx, es, r * a.lddx)) % E;
+    p.s_dy = piece_shift<E>(a.dy, es, r * a.lddy + p.head);
+    p.s_h = piece_shift<E>(a.h, es, r * a.ldh + p.head);
+    if (a.dh) p.s_dh = piece_shift<E>(a.dh, es, r * a.lddh + p.head);
+    p.s_w = piece_shift<E>(a.weight, a.tw == MM_F32 ? 4 : 2, p.head);
+    if (p.s_dy | p.s_h | p.s_dh | p.s_w) {  // [j - shift, j - shift + 2 E) of a piece at j lies inside
+      p.head += E;
+      p.end = a.cols - (E - 1);
+    }
+    p.end = p.head + max(0, p.end - p.head) / E * E;
+    if (p.end == p.head) p.head = p.end = min(p.head, a.cols);
+    // whole pieces: a multiple of 16 bytes into the row's place
+    p.o_dy += (uint32_t)((piece_shift<E>(a.dy, es, r * a.lddy) + p.head - p.s_dy) * es);
+    p.o_h += (uint32_t)((piece_shift<E>(a.h, es, r * a.ldh) + p.head - p.s_h) * es);
+    if (a.dh) p.o_dh += (uint32_t)((piece_shift<E>(a.dh, es, r * a.lddh) + p.head - p.s_dh) * es);
+  }
+  return p;
+}
+template <int TX, bool EDGES>
+__device__ __forceinline__ Piece<TX, 16 / bytes_of(TX)> ring_piece(const uint8_t *p, int i, int shift) {
+  using P = Piece<TX, 16 / bytes_of(TX)>;
+  const P x = P::load(p + i * 16);
+  return EDGES && shift ? shifted(x, P::load(p + i * 16 + 16), shift) : x;
+}
+
 template <int TX, int T, int V, int PER_SM, bool EDGES>
 __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormBwdArgs a, float *partial, int stages,
                                                               int *err) {
@@ -649,73 +717,24 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
   __shared__ float sh[2][2 * (T / 32)];
   __shared__ __align__(8) uint64_t full[kMaxRing];
   const int t = threadIdx.x;
-  const uint32_t bytes = (uint32_t)a.cols * bytes_of(TX), row = ring_row<EDGES>(bytes), parts = a.dh ? 3 : 2,
-                 stage_bytes = parts * row;
+  const uint32_t stage_bytes = (a.dh ? 3 : 2) * ring_row<EDGES>((uint32_t)a.cols * bytes_of(TX));
   if (t == 0) {
     for (int s = 0; s < stages; ++s) tc::mbar_init(tc::smem_u32(full + s), 1);
     tc::mbar_init_fence();
   }
   __syncthreads();
   pdl_wait();
-  auto fill = [&](int64_t r, int s) {  // one thread
-    const uint32_t bar = tc::smem_u32(full + s), dst = tc::smem_u32(ring) + (uint32_t)s * stage_bytes;
-    if constexpr (!EDGES) {
-      tc::mbar_expect_tx_one(bar, stage_bytes);
-      tc::bulk_load(dst, at<TX>(a.dy, r * a.lddy), row, bar);
-      tc::bulk_load(dst + row, at<TX>(a.h, r * a.ldh), row, bar);
-      if (a.dh) tc::bulk_load(dst + 2 * row, at<TX>(a.dh, r * a.lddh), row, bar);
-    } else {
-      const char *p[3] = {static_cast<const char *>(at<TX>(a.dy, r * a.lddy)),
-                          static_cast<const char *>(at<TX>(a.h, r * a.ldh)),
-                          static_cast<const char *>(at<TX>(a.dh, a.dh ? r * a.lddh : 0))};
-      uint32_t skip[3], size[3], all = 0;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const uint32_t off = (uint32_t)(uintptr_t)p[k] & 15u;
-        skip[k] = (16u - off) & 15u;
-        size[k] = k < (int)parts && skip[k] < bytes ? (bytes - skip[k]) & ~15u : 0u;
-        all += size[k];
-      }
-      tc::mbar_expect_tx_one(bar, all);
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (size[k]) tc::bulk_load(dst + k * row + (skip[k] ? 16u : 0u), p[k] + skip[k], size[k], bar);
-    }
+  auto fill = [&](int64_t r, int s) {
+    ring_fill<TX, EDGES>(a, r, tc::smem_u32(ring) + (uint32_t)s * stage_bytes, tc::smem_u32(full + s));
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s)
       if (blockIdx.x + (int64_t)s * gridDim.x < a.rows) fill(blockIdx.x + (int64_t)s * gridDim.x, s);
-  // the pieces' [head, end), this thread's element outside; how far into whole
-  // pieces the inputs' are, and where a row's pieces start in the ring
-  int head = 0, end = a.cols, edge = -1, s_dy = 0, s_h = 0, s_dh = 0, s_w = 0;
-  uint32_t o_dy = 0, o_h = row, o_dh = 2 * row;
-  if constexpr (EDGES) {
-    const int64_t r = blockIdx.x;
-    head = (E - piece_shift<E>(a.dx, bytes_of(TX), r * a.lddx)) % E;
-    s_dy = piece_shift<E>(a.dy, bytes_of(TX), r * a.lddy + head);
-    s_h = piece_shift<E>(a.h, bytes_of(TX), r * a.ldh + head);
-    if (a.dh) s_dh = piece_shift<E>(a.dh, bytes_of(TX), r * a.lddh + head);
-    s_w = piece_shift<E>(a.weight, a.tw == MM_F32 ? 4 : 2, head);
-    if (s_dy | s_h | s_dh | s_w) {  // [j - shift, j - shift + 2 E) of a piece at j lies inside
-      head += E;
-      end = a.cols - (E - 1);
-    }
-    end = head + max(0, end - head) / E * E;
-    if (end == head) head = end = min(head, a.cols);
-    if (t < head) edge = t;
-    else if (end + t - head < a.cols) edge = end + t - head;
-    // whole pieces: a multiple of 16 bytes into the row's place
-    o_dy += (uint32_t)((piece_shift<E>(a.dy, bytes_of(TX), r * a.lddy) + head - s_dy) * bytes_of(TX));
-    o_h += (uint32_t)((piece_shift<E>(a.h, bytes_of(TX), r * a.ldh) + head - s_h) * bytes_of(TX));
-    if (a.dh) o_dh += (uint32_t)((piece_shift<E>(a.dh, bytes_of(TX), r * a.lddh) + head - s_dh) * bytes_of(TX));
-  }
-  const int n = max(0, (end - head - t * E + T * E - 1) / (T * E));  // this thread's pieces
-  auto piece = [&](const uint8_t *p, int i, int shift) {
-    const P x = P::load(p + i * 16);
-    return EDGES && shift ? shifted(x, P::load(p + i * 16 + 16), shift) : x;
-  };
+  const RingPlace at_row = ring_place<TX, EDGES>(a, blockIdx.x);
+  const int head = at_row.head, edge = EDGES ? at_row.edge(t, a.cols) : -1;
+  const int n = max(0, (at_row.end - head - t * E + T * E - 1) / (T * E));  // this thread's pieces
   float w[V][E], dw[V][E] = {};
-  load_pieces_at(a.weight, a.tw, head + t * E, T * E, n, EDGES ? s_w : 0, w);
+  load_pieces_at(a.weight, a.tw, head + t * E, T * E, n, EDGES ? at_row.s_w : 0, w);
   float ew = 0.f, edw = 0.f, next_dy = 0.f, next_h = 0.f, next_dh = 0.f;
   auto load_edge = [&](int64_t r) {
     if (!EDGES || edge < 0 || r >= a.rows) return;
@@ -731,7 +750,9 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
   bool gave_up = false;  // (a wait ran into its limit: no further one is waited for)
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const float given = a.rstd ? a.rstd[r] : 0.f;
-    const uint8_t *stage = ring + (size_t)s * stage_bytes, *dy = stage + o_dy, *h = stage + o_h, *dh = stage + o_dh;
+    const uint8_t *stage = ring + (size_t)s * stage_bytes;
+    auto dy = [&](int i) { return ring_piece<TX, EDGES>(stage + at_row.o_dy, i, at_row.s_dy); };
+    auto h = [&](int i) { return ring_piece<TX, EDGES>(stage + at_row.o_h, i, at_row.s_h); };
     const float edy = next_dy, eh = next_h, edh = next_dh;
     load_edge(r + gridDim.x);
     float dot = edy * ew * eh, ss = eh * eh;
@@ -739,7 +760,7 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = v * T + t;
-      if (v < n) BwdPiece<TX, E>::sums(piece(dy, i, s_dy), piece(h, i, s_h), w[v], dot, ss);
+      if (v < n) BwdPiece<TX, E>::sums(dy(i), h(i), w[v], dot, ss);
     }
     // two sets of shared sums in turn: one barrier a row
     dot = row_sum<T>(dot, sh[side]);
@@ -756,8 +777,8 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
       if (v < n) {
         float dx[E];
         P d;
-        if (a.dh) d = piece(dh, i, s_dh);
-        BwdPiece<TX, E>::outputs(piece(dy, i, s_dy), piece(h, i, s_h), a.dh ? &d : nullptr, w[v], rs, c, dx, dw[v]);
+        if (a.dh) d = ring_piece<TX, EDGES>(stage + at_row.o_dh, i, at_row.s_dh);
+        BwdPiece<TX, E>::outputs(dy(i), h(i), a.dh ? &d : nullptr, w[v], rs, c, dx, dw[v]);
         store_piece<TX>(a.dx, r * a.lddx + head + i * E, dx);
       }
     }
@@ -788,7 +809,151 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
   }
 }
 
-// Longer rows, and dy of another type than h: 1 / rms and the mean of g h of each row (two
+// Longer rows: a cluster a row, each CTA a quarter of the columns, as above in
+// rows that start anywhere.  The rows of a whole ring are summed before the
+// CTAs' sums are exchanged, so that the cluster meets once for up to eight rows.
+// 2048 x 16384 f32 108 us (5.0 TB/s; in two passes over memory 127), 127 x 16385
+// 16 (19), 1000 x 32768 bf16 72 (109).  Clusters of eight with a full ring an SM
+// find room for fewer than half as many rows at a time: 234, 25, 144.
+constexpr int kCluster = 4;
+template <int TX, int T, int V>
+__global__ void __launch_bounds__(T, 1) rmsnorm_bwd_cluster_kernel(const NormBwdArgs whole, float *partial,
+                                                                   int stages, int *err) {
+  constexpr int E = 16 / bytes_of(TX), WARPS = T / 32;
+  static_assert(WARPS >= kMaxRing, "a warp a row of the ring");
+  using P = Piece<TX, E>;
+  pdl_launch_dependents();
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float2 warp_sums[kMaxRing][WARPS];
+  __shared__ float2 sums[2][kMaxRing][kCluster];
+  __shared__ float edges[kMaxRing][3][32];  // dy, h, dh outside the pieces; [0][31]: the given rstd
+  __shared__ __align__(8) uint64_t full[kMaxRing];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int rank = (int)blockIdx.x % kCluster;
+  const int64_t first = blockIdx.x / kCluster, hop = gridDim.x / kCluster;
+  const int slice = (whole.cols + kCluster - 1) / kCluster, col0 = rank * slice;
+  NormBwdArgs a = whole;  // this CTA's columns
+  a.cols = min(slice, whole.cols - col0);
+  a.dy = at<TX>(whole.dy, col0);
+  a.h = at<TX>(whole.h, col0);
+  if (whole.dh) a.dh = at<TX>(whole.dh, col0);
+  a.dx = static_cast<char *>(whole.dx) + (int64_t)col0 * bytes_of(TX);
+  a.weight = static_cast<const char *>(whole.weight) + (int64_t)col0 * (whole.tw == MM_F32 ? 4 : 2);
+  // the slices differ by a column or so: the largest one's ring in every CTA
+  const uint32_t stage_bytes = (a.dh ? 3 : 2) * ring_row<true>((uint32_t)slice * bytes_of(TX));
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) tc::mbar_init(tc::smem_u32(full + s), 1);
+    tc::mbar_init_fence();
+  }
+  tc::cluster_sync_all();  // the others run: their memory may be written
+  pdl_wait();
+  const int64_t count = (a.rows - first + hop - 1) / hop;  // rows of this cluster
+  auto fill = [&](int64_t k, int s) {
+    ring_fill<TX, true>(a, first + k * hop, tc::smem_u32(ring) + (uint32_t)s * stage_bytes, tc::smem_u32(full + s));
+  };
+  if (t == 0)
+    for (int s = 0; s < stages && s < count; ++s) fill(s, s);
+  const RingPlace at_row = ring_place<TX, true>(a, first);
+  const int head = at_row.head, edge = at_row.edge(lane, a.cols);
+  const int n = max(0, (at_row.end - head - t * E + T * E - 1) / (T * E));  // this thread's pieces
+  float e_dy = 0.f, e_h = 0.f, e_dh = 0.f;
+  auto load_edges = [&](int64_t k) {  // a warp a row of the ring that starts with the k-th
+    k += warp;
+    if (warp >= stages || k >= count) return;
+    const int64_t r = first + k * hop;
+    if (edge >= 0) {
+      e_dy = load_value(a.dy, TX, r * a.lddy + edge);
+      e_h = load_value(a.h, TX, r * a.ldh + edge);
+      if (a.dh) e_dh = load_value(a.dh, TX, r * a.lddh + edge);
+    }
+    if (lane == 31 && a.rstd) e_dy = a.rstd[r];
+  };
+  load_edges(0);
+  float w[V][E], dw[V][E] = {};
+  load_pieces_at(a.weight, a.tw, head + t * E, T * E, n, at_row.s_w, w);
+  const float ew = edge >= 0 ? load_value(a.weight, a.tw, edge) : 0.f;
+  float edw = 0.f;
+  const float per_col = 1.f / (float)whole.cols;
+  int side = 0;
+  bool gave_up = false;  // (a wait ran into its limit: no further one is waited for)
+  for (int64_t k0 = 0; k0 < count; k0 += stages, side ^= 1) {
+    const int nb = (int)min((int64_t)stages, count - k0);
+    if (warp < stages) edges[warp][0][lane] = e_dy, edges[warp][1][lane] = e_h, edges[warp][2][lane] = e_dh;
+    __syncthreads();
+    for (int s = 0; s < nb; ++s) {
+      const uint8_t *stage = ring + (size_t)s * stage_bytes;
+      float dot = 0.f, ss = 0.f;
+      if (warp == 0 && edge >= 0) {
+        const float eh = edges[s][1][lane];
+        dot = edges[s][0][lane] * ew * eh;
+        ss = eh * eh;
+      }
+      if (!gave_up && !tc::thread_wait(tc::smem_u32(full + s), (uint32_t)side, err, kErrRing)) gave_up = true;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v < n)
+          BwdPiece<TX, E>::sums(ring_piece<TX, true>(stage + at_row.o_dy, v * T + t, at_row.s_dy),
+                                ring_piece<TX, true>(stage + at_row.o_h, v * T + t, at_row.s_h), w[v], dot, ss);
+      dot = row_sum<32>(dot, nullptr);
+      ss = row_sum<32>(ss, nullptr);
+      if (lane == 0) warp_sums[s][warp] = make_float2(dot, ss);
+    }
+    __syncthreads();
+    if (warp < nb) {
+      const float2 x = lane < WARPS ? warp_sums[warp][lane] : make_float2(0.f, 0.f);
+      const float dot = row_sum<32>(x.x, nullptr), ss = row_sum<32>(x.y, nullptr);
+      if (lane < kCluster) {
+        const uint32_t to = tc::map_to_rank(tc::smem_u32(&sums[side][warp][rank]), (uint32_t)lane);
+        tc::st_cluster_f32(to, dot);
+        tc::st_cluster_f32(to + 4, ss);
+      }
+    }
+    // `side`'s sums are written again after the next meeting, which no CTA comes to
+    // before it has read these.
+    tc::cluster_sync_all();
+    load_edges(k0 + stages);
+    for (int s = 0; s < nb; ++s) {
+      const uint8_t *stage = ring + (size_t)s * stage_bytes;
+      const int64_t r = first + (k0 + s) * hop;
+      float dot = 0.f, ss = 0.f;
+#pragma unroll
+      for (int q = 0; q < kCluster; ++q) dot += sums[side][s][q].x, ss += sums[side][s][q].y;
+      const float rs = a.rstd ? edges[s][0][31] : 1.f / sqrtf(ss / (float)whole.cols + a.eps);
+      const float c = dot * per_col * rs * rs;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int i = v * T + t;
+        if (v < n) {
+          float dx[E];
+          P d;
+          if (a.dh) d = ring_piece<TX, true>(stage + at_row.o_dh, i, at_row.s_dh);
+          BwdPiece<TX, E>::outputs(ring_piece<TX, true>(stage + at_row.o_dy, i, at_row.s_dy),
+                                   ring_piece<TX, true>(stage + at_row.o_h, i, at_row.s_h), a.dh ? &d : nullptr, w[v],
+                                   rs, c, dx, dw[v]);
+          store_piece<TX>(a.dx, r * a.lddx + head + i * E, dx);
+        }
+      }
+      if (warp == 0 && edge >= 0) {
+        const float g = edges[s][0][lane], x = edges[s][1][lane];
+        store_value(a.dx, TX, r * a.lddx + edge, rs * (g * ew - x * c) + edges[s][2][lane]);
+        edw += g * x * rs;
+      }
+      __syncthreads();  // the stage, and in the end the edges, have been read
+      if (t == 0 && k0 + stages + s < count) fill(k0 + stages + s, s);
+    }
+  }
+  if (partial) {
+    float *out = partial + first * partial_ld(whole.cols) + col0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v < n)
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[head + (v * T + t) * E + e] = dw[v][e];
+    if (warp == 0 && edge >= 0) out[edge] = edw;
+  }
+}
+
+// Longer rows still, and dy of another type than h: 1 / rms and the mean of g h of each row (two
 // floats a row), then columns in slices, each thread walking down the rows.
 template <int TX, int E>
 __global__ void __launch_bounds__(1024) rmsnorm_bwd_stats_kernel(const NormBwdArgs a, float2 *stats) {
@@ -951,6 +1116,45 @@ mm_status bwd_ring_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   return bwd_blocks(a, kern, blocks, T, stages * stage, ctx, stages, ctx.dev->d_err + kOperatorErrorWord);
 }
 
+template <int TX, int T, int V>
+mm_status bwd_cluster_form(const NormBwdArgs &a, LaunchCtx &ctx) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  static int resident = 0;  // clusters
+  auto kern = rmsnorm_bwd_cluster_kernel<TX, T, V>;
+  std::call_once(once, [&] {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+    if (err != cudaSuccess) return;
+    cudaLaunchAttribute cluster = {};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = kCluster;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(kCluster);
+    config.blockDim = dim3(T);
+    config.dynamicSmemBytes = kRingBytes;
+    config.attrs = &cluster;
+    config.numAttrs = 1;
+    err = cudaOccupancyMaxActiveClusters(&resident, kern, &config);
+  });
+  if (err != cudaSuccess) return cuda_error(err, "rmsnorm_backward set-up");
+  constexpr int E = 16 / bytes_of(TX);
+  const size_t stage = (size_t)(a.dh ? 3 : 2) * ring_row<true>((uint32_t)((a.cols + kCluster - 1) / kCluster) * bytes_of(TX));
+  const int stages = (int)std::min<size_t>(kMaxRing, kRingBytes / stage);
+  if (stages < 1) return set_error(MM_ERR_UNSUPPORTED, "rmsnorm_backward: no row fits the ring");
+  // a cluster's rows all lie alike: a multiple of E clusters, or one row each
+  const int64_t most = std::max<int64_t>(E, resident / E * E);
+  const int64_t clusters = std::min<int64_t>(a.rows, most);
+  float *partial = nullptr;
+  mm_status st;
+  if (a.dweight && (st = partial_space(a, clusters, 0, ctx, &partial)) != MM_OK) return st;
+  cudaError_t e = launch_pdl(kern, dim3((unsigned)(clusters * kCluster)), dim3(T), stages * stage, ctx.stream,
+                             dim3(kCluster), a, partial, stages, ctx.dev->d_err + kOperatorErrorWord);
+  if (e != cudaSuccess) return cuda_error(e, "rmsnorm_backward launch (clusters)");
+  count_operator_launch();
+  return a.dweight ? add_parts(a, partial, (int)clusters, ctx) : MM_OK;
+}
+
 template <int TX, int E>
 mm_status bwd_long_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   const int64_t slices = ((int64_t)a.cols + 256 * E - 1) / (256 * E);
@@ -995,6 +1199,10 @@ mm_status bwd_form(const NormBwdArgs &a, LaunchCtx &ctx) {
     if (pieces <= 512) return bwd_ring_form<TX, 512, 1, 2, EDGES>(a, ctx);
     if (pieces <= 1024) return bwd_ring_form<TX, 512, 2, 2, EDGES>(a, ctx);
     if (pieces <= 2048) return bwd_ring_form<TX, 1024, 2, 1, EDGES>(a, ctx);
+    const int in_slice = (a.cols + kCluster - 1) / kCluster / E;
+    if (in_slice <= 512) return bwd_cluster_form<TX, 512, 1>(a, ctx);
+    if (in_slice <= 1024) return bwd_cluster_form<TX, 512, 2>(a, ctx);
+    if (in_slice <= 2048) return bwd_cluster_form<TX, 1024, 2>(a, ctx);
   }
   return bwd_long_form<TX, EDGES ? 1 : E>(a, ctx);
 }

@@ -357,6 +357,24 @@ def test_bwd_rows_that_start_anywhere(cols, t):
             dh.copy_(kept[1])
 
 
+@pytest.mark.parametrize("cols", [8196, 16400, 30001, 65537, 70001, 131071, 131101])
+@pytest.mark.parametrize("rows", [1, 16, 130, 700])
+def test_bwd_long_rows(cols, rows):
+    """Rows held by several blocks, and longer ones."""
+    g = generator(cols + rows)
+    for t, pad in (((F, F, F), 0), ((BF, F, BF), 3), ((H, H, H), 8)):
+        dy, dh, h = (rows_of(g, rows, cols, t[0], pad) for _ in range(3))
+        w = rows_of(g, 1, cols, t[1], offset=1)[0]
+        rstd = (1 / (h.float().square().mean(1) + EPS).sqrt()).contiguous() if pad else None
+        got = run_bwd(dy, dh, h, w, t, rstd=rstd)
+        check_bwd(dy, dh, h, w, t, got, rstd=rstd)
+        again = run_bwd(dy, None if rows == 16 else dh, h, w, t, rstd=rstd)
+        if rows == 16:
+            check_bwd(dy, None, h, w, t, again, rstd=rstd)
+        else:
+            assert T().equal(got[0], again[0]) and T().equal(got[1], again[1])
+
+
 def test_bwd_no_rows_writes_zeros():
     torch = T()
     dw = torch.full((100,), 3.0, device="cuda")
