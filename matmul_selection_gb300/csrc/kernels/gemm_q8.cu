@@ -45,7 +45,7 @@ struct Q8Params {
   int full_units;   // pair: units of whole tiles; those after are half tiles
   int total_units;
   int kb_per_rank;  // swap
-  int vec;          // out's rows are 16-byte aligned
+  int vec;          // out's rows are 16-byte aligned (pair: and whole pieces of 16 bytes)
   int *err;
 };
 
@@ -92,6 +92,43 @@ __device__ __forceinline__ void pair_unit(const Q8Params &p, int u, int &tm, int
   tm = g * kGroupRows + r % rows;
   n0 = (r / rows) * 256 + (half > 0 ? 128 : 0);
   w = half < 0 ? 256 : 128;
+}
+
+// A box of rows of 128 swizzled bytes to a matrix of ES-byte elements, from
+// element i on, `left` columns: a row an access of up to 128 bytes, which for
+// 2-byte elements is two a lane; where the row starts between two, its first
+// element goes alone.
+template <int ES>
+__device__ __forceinline__ void store_box(const uint8_t *box, void *out, int64_t i, int64_t ldc, int rows, int left) {
+  const int lane = threadIdx.x & 31;
+  constexpr int U = 8;  // rows read before the first of them is stored
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += U) {
+    uint32_t v[U], next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const auto word = [&](int k) {
+        return *reinterpret_cast<const uint32_t *>(box + (r0 + u) * 128 + (((k >> 2) ^ u) << 4) + (k & 3) * 4);
+      };
+      v[u] = word(lane);
+      if (ES == 2) next[u] = word((lane + 1) & 31);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (r0 + u >= rows) break;
+      char *to = static_cast<char *>(out) + (i + (r0 + u) * ldc) * ES;
+      if constexpr (ES == 4) {
+        if (lane < left) reinterpret_cast<uint32_t *>(to)[lane] = v[u];
+      } else {
+        uint16_t *const row = reinterpret_cast<uint16_t *>(to);
+        const int odd = (int)((uintptr_t)to >> 1) & 1, j = 2 * lane + odd;
+        if (odd && lane == 0) row[0] = (uint16_t)v[u];
+        const uint32_t x = __funnelshift_r(v[u], next[u], odd * 16);
+        if (j + 1 < left) *reinterpret_cast<uint32_t *>(row + j) = x;
+        else if (j < left) row[j] = (uint16_t)x;
+      }
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -237,65 +274,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row0 = tm * 256 + (int)pos * 128 + q * 32, row = row0 + lane;
       const float sa = p.sa && row < p.M ? p.sa[row] : 1.f;
       const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
-      if (p.vec) {
-        // Rows through a swizzled box in shared memory and TMA, which clips what
-        // is past M and N.  (Stored by the lanes, 64 bytes of a row each, a
-        // product with K = 64 took 19.0 us at 1865 x 5056.)
-        for (int i = (int)threadIdx.x - 64; i < 256; i += 128)
-          col_scale[i] = p.sb && n0 + i < p.N ? __ldg(p.sb + n0 + i) : 1.f;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+      // Rows through a swizzled box in shared memory and TMA, which clips what
+      // is past M and N.  (Stored by the lanes, 64 bytes of a row each, a
+      // product with K = 64 took 19.0 us at 1865 x 5056.)  Rows that TMA cannot
+      // address are read back from the box and stored by the warp, a row at a
+      // time: 330 us at 8000 x 16001 x 64.  (Stored by the lanes, a row each, 1298 us.)
+      for (int i = (int)threadIdx.x - 64; i < 256; i += 128)
+        col_scale[i] = p.sb && n0 + i < p.N ? __ldg(p.sb + n0 + i) : 1.f;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll 1
-        for (int c = 0; c < w && n0 + c < p.N && row0 < p.M; c += step) {
-          uint32_t r0[32], r1[32];
-          tmem_ld_32cols(tbase + (uint32_t)c, r0);
-          if (!f32) tmem_ld_32cols(tbase + (uint32_t)(c + 32), r1);
-          tmem_ld_wait();
-          if (lane == 0) tma_store_wait_read<1>();  // this box's previous store has read it
-          __syncwarp();
-          uint8_t *box = mine + side * kBoxB;
-          const float4 *s4 = reinterpret_cast<const float4 *>(col_scale + c);
-          auto put = [&](int j, uint32_t a, uint32_t b, uint32_t c2, uint32_t d) {  // 16-byte chunk j of the row
-            *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(a, b, c2, d);
-          };
-          if (f32) {
+      for (int c = 0; c < w && n0 + c < p.N && row0 < p.M; c += step) {
+        uint32_t r0[32], r1[32];
+        tmem_ld_32cols(tbase + (uint32_t)c, r0);
+        if (!f32) tmem_ld_32cols(tbase + (uint32_t)(c + 32), r1);
+        tmem_ld_wait();
+        if (lane == 0) tma_store_wait_read<1>();  // this box's previous store has read it
+        __syncwarp();
+        uint8_t *box = mine + side * kBoxB;
+        const float4 *s4 = reinterpret_cast<const float4 *>(col_scale + c);
+        auto put = [&](int j, uint32_t a, uint32_t b, uint32_t c2, uint32_t d) {  // 16-byte chunk j of the row
+          *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(a, b, c2, d);
+        };
+        if (f32) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 s = s4[j];
-              put(j, __float_as_uint(__uint_as_float(r0[4 * j]) * sa * s.x),
-                  __float_as_uint(__uint_as_float(r0[4 * j + 1]) * sa * s.y),
-                  __float_as_uint(__uint_as_float(r0[4 * j + 2]) * sa * s.z),
-                  __float_as_uint(__uint_as_float(r0[4 * j + 3]) * sa * s.w));
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t *r = j < 4 ? r0 + 8 * j : r1 + 8 * (j - 4);
-              const float4 s = s4[2 * j], q4 = s4[2 * j + 1];
-              put(j, pack2(p.tc, __uint_as_float(r[0]) * sa * s.x, __uint_as_float(r[1]) * sa * s.y),
-                  pack2(p.tc, __uint_as_float(r[2]) * sa * s.z, __uint_as_float(r[3]) * sa * s.w),
-                  pack2(p.tc, __uint_as_float(r[4]) * sa * q4.x, __uint_as_float(r[5]) * sa * q4.y),
-                  pack2(p.tc, __uint_as_float(r[6]) * sa * q4.z, __uint_as_float(r[7]) * sa * q4.w));
-            }
+          for (int j = 0; j < 8; ++j) {
+            const float4 s = s4[j];
+            put(j, __float_as_uint(__uint_as_float(r0[4 * j]) * sa * s.x),
+                __float_as_uint(__uint_as_float(r0[4 * j + 1]) * sa * s.y),
+                __float_as_uint(__uint_as_float(r0[4 * j + 2]) * sa * s.z),
+                __float_as_uint(__uint_as_float(r0[4 * j + 3]) * sa * s.w));
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t *r = j < 4 ? r0 + 8 * j : r1 + 8 * (j - 4);
+            const float4 s = s4[2 * j], q4 = s4[2 * j + 1];
+            put(j, pack2(p.tc, __uint_as_float(r[0]) * sa * s.x, __uint_as_float(r[1]) * sa * s.y),
+                pack2(p.tc, __uint_as_float(r[2]) * sa * s.z, __uint_as_float(r[3]) * sa * s.w),
+                pack2(p.tc, __uint_as_float(r[4]) * sa * q4.x, __uint_as_float(r[5]) * sa * q4.y),
+                pack2(p.tc, __uint_as_float(r[6]) * sa * q4.z, __uint_as_float(r[7]) * sa * q4.w));
+          }
+        }
+        if (p.vec) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tma_store_2d(&tmC, smem_u32(box), n0 + c, row0);
-          side ^= 1;
+        } else {
+          __syncwarp();
+          const int left = min(step, p.N - n0 - c), rows = min(32, p.M - row0);  // (the box holds 32)
+          if (f32) store_box<4>(box, p.out, (int64_t)row0 * p.ldc + n0 + c, p.ldc, rows, left);
+          else store_box<2>(box, p.out, (int64_t)row0 * p.ldc + n0 + c, p.ldc, rows, left);
         }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < w && n0 + c < p.N; c += 32) {
-          uint32_t r[32];
-          tmem_ld_32cols(tbase + (uint32_t)c, r);
-          tmem_ld_wait();
-          const int col = n0 + c;
-          if (row < p.M)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (col + i < p.N)
-                store_value(p.out, p.tc, (int64_t)row * p.ldc + col + i,
-                            __uint_as_float(r[i]) * sa * (p.sb ? __ldg(p.sb + col + i) : 1.f));
-        }
+        side ^= 1;
       }
       fence_before();
       __syncwarp();
@@ -475,8 +505,11 @@ mm_status run_pair(const Q8Args &a, Q8Params p, int clusters, LaunchCtx &ctx) {
   if ((st = rows_map(&mb, a.B, a.N, a.K, a.ldb, 128)) != MM_OK) return st;
   if ((st = rows_map(&mbh, a.B, a.N, a.K, a.ldb, 64)) != MM_OK) return st;
   mc = ma;
+  // TMA clips a row's end to 16 bytes, not to an element (at N = 2046 of 16 bits
+  // in rows of 2048 it wrote the two elements behind the row).
+  const int es = dtype_bytes(p.tc);
+  p.vec = p.vec && (int64_t)p.N * es % 16 == 0;
   if (p.vec) {
-    const int es = dtype_bytes(p.tc);
     st = encode_map_2d(&mc,
                        p.tc == MM_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                        : p.tc == MM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16

@@ -657,6 +657,18 @@ def test_q8_many_rows_of_weights(M, N, K):
     check_q8(a, b, sa, sb, F, run_q8(a, b, sa, sb, F))
 
 
+@pytest.mark.parametrize("N", [2041, 2046, 2048, 2049, 2051, 2175])
+@pytest.mark.parametrize("tc", [BF, H, F])
+def test_q8_many_rows_that_end_anywhere(N, tc):
+    """Rows of the output that start on any element, many tiles of them."""
+    g = generator(N)
+    M, K = 2311, 208
+    a, b = q8_rows(g, M, K), q8_rows(g, N, K)
+    sa, sb = q8_scales(g, M), q8_scales(g, N)
+    for pad in (0, 1, 2):
+        check_q8(a, b, sa, sb, tc, run_q8(a, b, sa, sb, tc, pad))
+
+
 @pytest.mark.parametrize("M", [1, 12, 70, 300])
 @pytest.mark.parametrize("K", [1, 3, 16, 31, 32, 33, 127, 129, 257])
 def test_q8_short_k(M, K):
