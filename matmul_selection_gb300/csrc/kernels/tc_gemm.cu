@@ -2055,9 +2055,11 @@ mm_status launch_tc_impl(const Problem &p, LaunchCtx &ctx, int cfg, bool c_trans
                    : run_splitk<4>(p, tp, cfg, ma, mb, sms, tp.c_trans, ctx.stream);
   }
   const int grid = (int)std::min<int64_t>(units, sms);
-  // C by bulk-tensor stores where TMA can describe it, else the per-thread path
+  // C by bulk-tensor stores where TMA can describe it, else the per-thread path.
+  // TMA clips a row's end to 16 bytes, not to an element: rows that end inside a
+  // piece would have what follows them in it overwritten.
   CUtensorMap mc = ma;
-  if (!c_trans && (uintptr_t)p.C % 16 == 0 && (p.ldc * ec) % 16 == 0 &&
+  if (!c_trans && (uintptr_t)p.C % 16 == 0 && (p.ldc * ec) % 16 == 0 && ((int64_t)p.N * ec) % 16 == 0 &&
              (p.batch <= 1 || (p.sC * ec) % 16 == 0) && p.ldc * ec < (1LL << 40) &&
              p.sC * ec < (1LL << 40)) {
     st = encode_map(&mc, p.tc, p.C, p.N, p.M, p.batch, p.ldc * ec, p.sC * ec, 128 / ec, 32);
