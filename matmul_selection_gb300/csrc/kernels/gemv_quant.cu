@@ -14,7 +14,13 @@
 //   e4m3   m16n8k32 on the bytes as they are.
 // The warps' parts (and those of a cluster's CTAs, which split K where there
 // are few rows of weights) meet in the owner's shared memory and are added in
-// order: one launch, the same bits every time.
+// order: one launch, the same bits every time.  Where K is not split a CTA stays
+// and takes tiles in turn, its ring running on over them.
+// Measured: e4m3 1 x 16384 x 8192 (in this form) 23.5 us, 5.7 TB/s, HBM-bound;
+// 4-bit, groups of 128, 1 x 19456 x 16384 40 us (4.1 TB/s), 1 x 16384 x 8192 21, 16
+// x 16384 x 8192 f16 with zero points 32.3 (2.3 TB/s): the instructions that make
+// weights of codes, at about half of the issue rate with the 16 computing warps an
+// SM that registers allow.  1 x 4096 x 4096: 4.6 (e4m3 5.2), a launch's chain.
 #include <algorithm>
 #include <mutex>
 
