@@ -358,7 +358,9 @@ __global__ void __launch_bounds__(T == 32 ? 256 : T) rmsnorm_rows_kernel(const N
     row_sum_max<T>(ss, big, sh);
     const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
     const float scale = row_scale(__uint_as_float(big) * rstd);
-    const float inv = rstd * (1.f / scale);
+    // Two factors in turn, y first: their product is 448 / max|h w|, which is
+    // beyond fp32 for rows below 1.3e-36.
+    const float inv = 1.f / scale;
     if (t == 0) {
       a.scale[r] = scale;
       if (a.rstd) a.rstd[r] = rstd;
@@ -368,11 +370,11 @@ __global__ void __launch_bounds__(T == 32 ? 256 : T) rmsnorm_rows_kernel(const N
       const int j = j0 + v * T * E;
       if (j < end) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[v][e] *= inv;
+        for (int e = 0; e < E; ++e) h[v][e] = h[v][e] * rstd * inv;
         store_piece(a.y, MM_E4M3, r * a.ldy + j, h[v]);
       }
     }
-    if (EDGES && edge >= 0) static_cast<uint8_t *>(a.y)[r * a.ldy + edge] = to_e4m3(eh * inv);
+    if (EDGES && edge >= 0) static_cast<uint8_t *>(a.y)[r * a.ldy + edge] = to_e4m3(eh * rstd * inv);
   } else {
     ss = row_sum<T>(ss, sh);
     const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
