@@ -432,7 +432,10 @@ mm_status mm_rmsnorm_backward(const void *dy, const void *dh, const void *h, con
  *   group     32, 64 or 128 codes; the last group of a row may be short.
  * For M <= 16 the differences code - zero enter the product as they are and
  * the scales are applied to fp32 sums of a group; for larger M each weight is
- * rounded once to A's type.
+ * rounded once to A's type.  With f16 A and bf16 or f32 scales that is done
+ * after a row's scales are divided by a power of two (its column of the output
+ * takes it back), so they may be of any size, a row's largest and its others
+ * up to 2^25 apart.  With f16 scales a weight beyond 65504 becomes infinite.
  * M or N of 0 is a no-op; K = 0 writes zeros.  M, N, K < 2^30.
  */
 mm_status mm_gemm_w4(const void *A, const void *codes, const void *scales, const void *zeros,

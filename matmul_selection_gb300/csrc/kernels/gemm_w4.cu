@@ -9,7 +9,9 @@
 // type) and write them into TMEM, from where the MMA takes its A operand.
 // Through shared memory the writes would have to be fenced to the async proxy
 // stage by stage, which took longer than the MMA of the stage.  Codes and
-// rows of A come by TMA through a ring each; a stage holds 64 of K.  CTAs are
+// rows of A come by TMA through a ring each; a stage holds 64 of K.  With f16 A and
+// scales of a wider type a small kernel ahead finds a power of two for each row of
+// weights that keeps them in f16's range.  CTAs are
 // persistent; where there are few tiles K is split over the CTAs of a cluster,
 // whose fp32 tiles meet in distributed shared memory and are added in rank
 // order.
@@ -74,8 +76,31 @@ struct TileParams {
   int *err;
   W4Scales w;
   int split_scale;  // the scales' type is not A's
+  // f16 A and wider scales, else null: for each row of weights a power of two that
+  // its scales are divided by and its column of the output is multiplied with
+  const float *row_factor;
   bool vec;         // out's rows are 16-byte aligned
 };
+
+// The largest finite scale of a row of weights is brought to [2^11, 2^12): 15 times
+// that is still an f16, and the two parts of a scale (see group_scale) keep f16's
+// whole precision down to 2^-14 of it, one rounding's to 2^-25.  A warp a row; 2.5 us
+// of a call (100 x 4096 x 4096 14.1, with f16 scales 11.0).
+__global__ void __launch_bounds__(256) w4_row_factor_kernel(const W4Scales w, float *factor) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (n >= w.N) return;
+  uint32_t big = 0;
+  for (int g = lane; g < w.groups; g += 32) {
+    const uint32_t s = __float_as_uint(load_value(w.s, w.ts, (int64_t)n * w.lds + g)) & 0x7fffffffu;
+    if (s < 0x7f800000u) big = max(big, s);
+  }
+  big = __reduce_max_sync(0xffffffffu, big);
+  // 2^(e - 11) for big in [2^e, 2^(e + 1)), no smaller than 2^-126
+  const int e = (int)(big >> 23) - 11;
+  if (lane == 0) factor[n] = big == 0 ? 1.f : __uint_as_float((uint32_t)max(e, 1) << 23);
+}
 
 // The scale and zero point of 32 codes of a row.  A scale of another type than
 // A's is taken as a sum of two of A's type, hi + lo, so that a weight is still
@@ -85,15 +110,17 @@ struct GroupScale {
   typename Pair16<TA>::T hi, lo, zero;
 };
 template <int TA>
-__device__ __forceinline__ GroupScale<TA> group_scale(const TileParams &p, const RawScale &r) {
+__device__ __forceinline__ GroupScale<TA> group_scale(const TileParams &p, const RawScale &r, float per_factor) {
   using T = typename Pair16<TA>::T;
   GroupScale<TA> g;
   if (!p.split_scale) {
     g.hi = g.lo = bits_as<T>(r.s * 0x00010001u);
   } else {
-    const float s = raw_scale_value(p.w, r);
+    float s = raw_scale_value(p.w, r);
+    if (TA == MM_F16) s *= per_factor;  // (exact)
     g.hi = Pair16<TA>::both(s);
-    g.lo = Pair16<TA>::both(s - __low2float(g.hi));
+    const float rest = s - __low2float(g.hi);
+    g.lo = Pair16<TA>::both(isfinite(rest) ? rest : 0.f);
   }
   // the bias that the codes are read with, and the zero point
   g.zero = bits_as<T>((TA == MM_BF16 ? 0x43004300u : 0x64006400u) + (r.z & 15u) * 0x00010001u);
@@ -147,6 +174,8 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
   const int j = (int)(((uint32_t)r.group - r.fills) % kGroups), part = j % PER;
   const uint32_t dst0 = r.weights + ((uint32_t)((warp & 3) * 32) << 16);
   const ScaleRow srow = scale_row(p.w, n0 + row);
+  float per_factor = 1.f;
+  if (TA == MM_F16 && p.row_factor && n0 + row < p.N) per_factor = 1.f / p.row_factor[n0 + row];
   const bool two = p.w.group_shift == 5;  // a block of 64 spans two groups
   const uint8_t *crow = r.codes + row * 128;
   const int ns = nk / B;
@@ -182,10 +211,10 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
     fence_after();
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      GroupScale<TA> g = group_scale<TA>(p, cur[b][0]);
+      GroupScale<TA> g = group_scale<TA>(p, cur[b][0], per_factor);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (h && two) g = group_scale<TA>(p, cur[b][1]);
+        if (h && two) g = group_scale<TA>(p, cur[b][1], per_factor);
         const uint4 w = q[2 * b + h];
         uint32_t v[16];
         if (p.split_scale) {
@@ -369,6 +398,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tphase ^= 1;
         fence_after();
         const int m0 = u / p.tiles_n * BN, n = u % p.tiles_n * 128 + q * 32 + lane;
+        const float factor = TA == MM_F16 && p.row_factor && n < p.N ? p.row_factor[n] : 1.f;
 #pragma unroll 1
         for (int c = half * 32; c < BN && m0 + c < p.M; c += 64) {
           uint32_t r[32];
@@ -378,7 +408,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (m0 + c + i < p.M)
-                store_value(p.out, p.tc, (int64_t)(m0 + c + i) * p.ldc + n, __uint_as_float(r[i]));
+                store_value(p.out, p.tc, (int64_t)(m0 + c + i) * p.ldc + n,
+                            TA == MM_F16 ? __uint_as_float(r[i]) * factor : __uint_as_float(r[i]));
           }
         }
         fence_before();
@@ -399,7 +430,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     auto store = [&](auto step) {
       constexpr int STEP = decltype(step)::value;
       const int n = first % p.tiles_n * 128 + (STEP == 1 ? 4 * lane : lane);
+      float f[4] = {1.f, 1.f, 1.f, 1.f};
+      if (TA == MM_F16 && p.row_factor)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i * STEP < p.N) f[i] = p.row_factor[n + i * STEP];
       sum_tile<STEP == 1>(tile, rank, ranks, per, rows, warp, kTileThreads / 32, [&](int m, float4 v) {
+        if (TA == MM_F16) v = make_float4(v.x * f[0], v.y * f[1], v.z * f[2], v.w * f[3]);
         store_four<STEP>(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n, v, p.N - n);
       });
     };
@@ -474,6 +511,15 @@ mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
   p.err = ctx.dev->d_err + kOperatorErrorWord;
   p.w = w4_scales(a);
   p.split_scale = a.ts != a.ta;
+  if (p.split_scale && a.ta == MM_F16) {
+    void *f = nullptr;
+    if ((st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_WORKSPACE, (size_t)a.N * sizeof(float), &f)) != MM_OK) return st;
+    cudaError_t e = launch_pdl(w4_row_factor_kernel, dim3((unsigned)((a.N + 7) / 8)), dim3(256), 0, ctx.stream, dim3(1),
+                               p.w, static_cast<float *>(f));
+    if (e != cudaSuccess) return cuda_error(e, "gemm_w4 launch (row factors)");
+    count_operator_launch();
+    p.row_factor = static_cast<const float *>(f);
+  }
   p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0;
   st = a.ta == MM_BF16 ? launch_tiles<MM_BF16>(a, ra, rw, p, ctx) : launch_tiles<MM_F16>(a, ra, rw, p, ctx);
   if (st == MM_OK) count_operator_launch();
