@@ -157,6 +157,28 @@ struct DequantRing {
   uint32_t fills = 0;        // stages filled before this tile
 };
 
+// The weights past K of the stage that reaches past it, `left` of whose are below:
+// zeros.  A code there is arbitrary, and the weight that it makes may be infinite,
+// which A's zeros would make a NaN.  The stage has been written: what is 32 weights
+// from `c` on is read back, masked and written again (rare, so out of the way).
+template <int BLOCKS>
+__device__ __noinline__ void clear_past_k(uint32_t dst, int left) {
+  tmem_st_wait();
+#pragma unroll 1
+  for (int c = 0; c < BLOCKS * 64; c += 32) {
+    if (c + 32 <= left) continue;
+    uint32_t v[16];
+    tmem_ld_16cols(dst + (uint32_t)(c / 2), v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int n = left - (c + 2 * i);
+      v[i] &= n >= 2 ? 0xffffffffu : n == 1 ? 0x0000ffffu : 0u;
+    }
+    tmem_st_16cols(dst + (uint32_t)(c / 2), v);
+  }
+}
+
 // The weights of 128 rows from row n0, blocks [kb0, kb0 + nk) (whole stages of
 // codes), into TMEM: each thread a row (its lane) of the stages whose place in
 // the ring is its group's modulo 4.
@@ -231,6 +253,8 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
         tmem_st_16cols(dst0 + (uint32_t)((stage * B + b) * 32 + h * 16), v);
       }
     }
+    const int left = p.w.K - (kb0 + i * B) * 64;
+    if (left < B * 64) clear_past_k<B>(dst0 + (uint32_t)(stage * B * 32), left);
     tmem_st_wait();
     fence_before();
     __syncwarp();

@@ -110,8 +110,8 @@ __device__ __forceinline__ void mma_16x8_first(float (&d)[4], uint32_t a0, uint3
 // Where a lane's scales and zero points are: of its two rows, for the 64 codes
 // of a panel from 64 t on (lane t of four), entry h those from 64 t + 32 h
 // (TWO: groups of 32; else both entries are one).  A row past N stands for the
-// last, and a group past the last one for that: their results are not used or
-// multiply zeros.
+// last, and a group past the last one for that: their results are not used, or
+// see scales_below_k.
 struct ScaleCursor {
   const char *s[2];
   const uint8_t *z[2];
@@ -152,6 +152,14 @@ __device__ __forceinline__ void load_panel_scales(const W4Scales &w, ScaleCursor
     }
   }
   c.g += c.step;
+}
+// Of K's last panel: where an entry's codes (from k on) all lie past K its scale is
+// 0, so that an infinite scale of the last group stays with that group's codes.
+template <bool TWO>
+__device__ __forceinline__ void scales_below_k(PanelScales &s, int k, int K) {
+#pragma unroll
+  for (int h = 0; h < (TWO ? 2 : 1); ++h)
+    if (k + 32 * h >= K) s.s[0][h] = s.s[1][h] = 0u;
 }
 // A byte b under a byte of zeros is b 2^-133 as a bf16 (and b 2^-24 as an f16):
 // the denormals and the first binade lie on one line.  So a pair of codes that
@@ -379,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
       for (int i = 0; i < steps && ok; ++i, ++n) {
         const int st = n % kStages;
-        const PanelScales cur = next;
+        PanelScales cur = next;
         if constexpr (W4) {
           if (i + 1 == steps) cursor = scale_cursor(p.w, (tile + hop) * R + row0, k0, WK * 256);
           load_panel_scales<TWO>(p.w, cursor, next);
@@ -389,6 +397,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (i * WK + wk < np) {
           const uint32_t off = after_wait((uint32_t)st * kStageB);
           if constexpr (W4) {
+            const int panel = p0 + i * WK + wk;
+            if (panel == p.panels - 1) scales_below_k<TWO>(cur, panel * 256 + 64 * t, p.w.K);
             if (p.w.z) panel_w4<F, MT, XBLOCK, TWO, true>(p, wrow + off, xrow + off, cur, acc);
             else panel_w4<F, MT, XBLOCK, TWO, false>(p, wrow + off, xrow + off, cur, acc);
           } else {

@@ -10,10 +10,10 @@ struct W4Scales {
   const void *s;
   const uint8_t *z;  // null: 8
   int64_t lds;
-  int N, ts, group_shift, groups;
+  int N, K, ts, group_shift, groups;
 };
 inline W4Scales w4_scales(const W4Args &a) {
-  return W4Scales{a.scales, a.zeros, a.lds, a.N, a.ts, a.group == 32 ? 5 : a.group == 64 ? 6 : 7,
+  return W4Scales{a.scales, a.zeros, a.lds, a.N, a.K, a.ts, a.group == 32 ? 5 : a.group == 64 ? 6 : 7,
                   (a.K + a.group - 1) / a.group};
 }
 
