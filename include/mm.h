@@ -364,6 +364,12 @@ mm_status mm_splitk_gemm_noalloc_status(void *stream);
  * call needs is allocated on the first call of its size on a stream; while
  * the stream is being captured into a graph such a call returns
  * MM_ERR_UNSUPPORTED, so make one call of that size before the capture.
+ * Scratch that a captured call was given stays where it is until
+ * mm_shutdown(), so a graph may be replayed after larger calls; it is still
+ * that stream's scratch, so replays of the graph, whatever stream they run on,
+ * have to be ordered with calls on the captured stream and with replays of
+ * other graphs captured there.  (The same holds for the scratch of captured
+ * products above.)
  * Sums and statistics are held in fp32.  Errors of every one of them:
  * MM_ERR_INVALID_ARG (negative size, leading dimension smaller than a row,
  * null or misaligned pointer, type out of place), MM_ERR_UNSUPPORTED (not an

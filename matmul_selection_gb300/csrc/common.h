@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "../../include/mm.h"
+#include "scratch.h"
 
 #include <utility>
 
@@ -242,7 +243,7 @@ struct DeviceState {
   std::mutex scratch_mu;
   // per-(stream, slot) scratch: slot SCRATCH_TICKETS holds zero-initialised
   // counters that kernels leave at zero; SCRATCH_WORKSPACE holds partial sums
-  std::map<std::pair<cudaStream_t, int>, DevBuf> scratch;
+  std::map<std::pair<cudaStream_t, int>, ScratchBuffer> scratch;
   DevBuf flush_buf;
   DevBuf stage_a, stage_b, stage_c;        // host-buffer entry point staging
   std::mutex stage_mu;
@@ -269,7 +270,8 @@ void noalloc_forget_devices();
 void for_each_device(void (*fn)(DeviceState &));
 
 // Scratch of at least `bytes` private to (device, stream, slot).  A new or
-// grown buffer is zero-filled (stream-ordered).
+// grown buffer is zero-filled (stream-ordered).  One that was handed out while the
+// stream was being captured stays allocated until the state is dropped.
 enum ScratchSlot { SCRATCH_TICKETS = 0, SCRATCH_WORKSPACE = 1, SCRATCH_REPACK = 2 };
 mm_status get_scratch(DeviceState &ds, cudaStream_t s, int slot, size_t bytes, void **out);
 

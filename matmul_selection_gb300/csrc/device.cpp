@@ -19,6 +19,18 @@ std::string uuid_string(const cudaUUID_t &u) {
            b[2], b[3], b[4], b[5], b[6], b[7], b[8], b[9], b[10], b[11], b[12], b[13], b[14], b[15]);
   return s;
 }
+// ScratchBuffer's memory: a stream's device memory.
+struct StreamMemory {
+  cudaStream_t s;
+  cudaError_t err = cudaSuccess;
+  bool allocate(void **p, size_t n) {
+    err = cudaMalloc(p, n);
+    if (err != cudaSuccess) cudaGetLastError();  // (not the next launch's)
+    return err == cudaSuccess;
+  }
+  void release(void *p) { cudaFree(p); }
+  bool wait() { return (err = cudaStreamSynchronize(s)) == cudaSuccess; }
+};
 }  // namespace
 
 mm_status DevBuf::ensure(size_t need) {
@@ -85,7 +97,7 @@ void release_all_devices() {
     DeviceState &ds = *kv.second;
     cudaSetDevice(ds.info.ordinal);
     cudaDeviceSynchronize();
-    for (auto &s : ds.scratch) s.second.release();
+    for (auto &s : ds.scratch) scratch_release(s.second, StreamMemory{s.first.first});
     ds.flush_buf.release();
     ds.stage_a.release();
     ds.stage_b.release();
@@ -100,28 +112,27 @@ void release_all_devices() {
 
 mm_status get_scratch(DeviceState &ds, cudaStream_t s, int slot, size_t bytes, void **out) {
   std::lock_guard<std::mutex> lk(ds.scratch_mu);
-  DevBuf &b = ds.scratch[std::make_pair(s, slot)];
-  if (!b.ptr || b.bytes < bytes) {
-    // Nothing can be allocated while the stream is being captured into a
-    // graph (the allocation would end the capture): the candidate declines
-    // and the caller moves on to one that needs no new scratch.
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone)
-      return set_error(MM_ERR_UNSUPPORTED,
-                       "scratch of %zu bytes not allocated on this stream before the capture",
-                       bytes);
-    // The old buffer may still be read by queued work on this stream.
-    if (b.ptr) {
-      cudaError_t e = cudaStreamSynchronize(s);
-      if (e != cudaSuccess) return cuda_error(e, "cudaStreamSynchronize (scratch growth)");
-    }
-    mm_status st = b.ensure(bytes);
-    if (st != MM_OK) return st;
-    // counters used by single-pass reductions must start at zero
-    cudaError_t e = cudaMemsetAsync(b.ptr, 0, b.bytes, s);
-    if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync (scratch)");
+  ScratchBuffer &b = ds.scratch[std::make_pair(s, slot)];
+  // Nothing can be allocated while the stream is being captured into a
+  // graph (the allocation would end the capture): the candidate declines
+  // and the caller moves on to one that needs no new scratch.
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {  // the legacy stream beside a capture
+    cudaGetLastError();
+    cap = cudaStreamCaptureStatusNone;
   }
-  *out = b.ptr;
+  StreamMemory mem{s};
+  switch (scratch_request(b, bytes, cap != cudaStreamCaptureStatusNone, mem, out)) {
+  case Scratch::READY: return MM_OK;
+  case Scratch::IN_CAPTURE:
+    return set_error(MM_ERR_UNSUPPORTED,
+                     "scratch of %zu bytes not allocated on this stream before the capture", bytes);
+  case Scratch::FAILED: return cuda_error(mem.err, "library scratch");
+  case Scratch::GROWN: break;
+  }
+  // counters used by single-pass reductions must start at zero
+  cudaError_t e = cudaMemsetAsync(b.ptr, 0, b.bytes, s);
+  if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync (scratch)");
   return MM_OK;
 }
 
