@@ -360,7 +360,8 @@ mm_status mm_splitk_gemm_noalloc_status(void *stream);
  * aligned to their element size, asynchronous on `stream`, nothing retained)
  * and take no part in tuning: no key, no table, no candidate.  Each call
  * launches on `stream` only; calls on one stream are ordered, and calls on
- * different streams may overlap (scratch is private to a stream).  Scratch a
+ * different streams may overlap (scratch is private to a stream; each thread's
+ * per-thread default stream counts as one of its own).  Scratch a
  * call needs is allocated on the first call of its size on a stream; while
  * the stream is being captured into a graph such a call returns
  * MM_ERR_UNSUPPORTED, so make one call of that size before the capture.

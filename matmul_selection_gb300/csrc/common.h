@@ -221,6 +221,10 @@ struct DevBuf {
   void release();
 };
 
+// A stream as scratch tells streams apart: its handle, and for the per-thread
+// default stream, whose one handle means another stream in every thread, its id.
+using StreamKey = std::pair<cudaStream_t, unsigned long long>;
+
 struct TableEntry {
   int winner = 0;               // candidate index
   std::vector<int> ranking;     // valid candidates, fastest first
@@ -243,7 +247,7 @@ struct DeviceState {
   std::mutex scratch_mu;
   // per-(stream, slot) scratch: slot SCRATCH_TICKETS holds zero-initialised
   // counters that kernels leave at zero; SCRATCH_WORKSPACE holds partial sums
-  std::map<std::pair<cudaStream_t, int>, ScratchBuffer> scratch;
+  std::map<std::pair<StreamKey, int>, ScratchBuffer> scratch;
   DevBuf flush_buf;
   DevBuf stage_a, stage_b, stage_c;        // host-buffer entry point staging
   std::mutex stage_mu;

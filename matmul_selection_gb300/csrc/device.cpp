@@ -97,7 +97,7 @@ void release_all_devices() {
     DeviceState &ds = *kv.second;
     cudaSetDevice(ds.info.ordinal);
     cudaDeviceSynchronize();
-    for (auto &s : ds.scratch) scratch_release(s.second, StreamMemory{s.first.first});
+    for (auto &s : ds.scratch) scratch_release(s.second, StreamMemory{nullptr});
     ds.flush_buf.release();
     ds.stage_a.release();
     ds.stage_b.release();
@@ -110,9 +110,18 @@ void release_all_devices() {
   if (cur >= 0) cudaSetDevice(cur);
 }
 
+static mm_status stream_key(cudaStream_t s, StreamKey *key) {
+  *key = StreamKey(s == cudaStreamLegacy ? nullptr : s, 0ull);
+  if (s == cudaStreamPerThread) MM_CUDA_TRY(cudaStreamGetId(s, &key->second));
+  return MM_OK;
+}
+
 mm_status get_scratch(DeviceState &ds, cudaStream_t s, int slot, size_t bytes, void **out) {
+  StreamKey key;
+  mm_status st = stream_key(s, &key);
+  if (st != MM_OK) return st;
   std::lock_guard<std::mutex> lk(ds.scratch_mu);
-  ScratchBuffer &b = ds.scratch[std::make_pair(s, slot)];
+  ScratchBuffer &b = ds.scratch[std::make_pair(key, slot)];
   // Nothing can be allocated while the stream is being captured into a
   // graph (the allocation would end the capture): the candidate declines
   // and the caller moves on to one that needs no new scratch.

@@ -65,3 +65,46 @@ def test_graphs_keep_their_scratch():
         for o, w in zip(outs, want):
             assert all(torch.equal(x, y) for x, y in zip(bits(o), w))
     assert all(bool((o == 7).all()) for o in other)
+
+
+PER_THREAD = 2  # the handle of the calling thread's own default stream
+
+
+def test_per_thread_streams_have_their_own_scratch():
+    """Threads that call at one time, each on its per-thread default stream."""
+    import threading
+    torch = T()
+    g = generator(33)
+    todo = [[backward(g, 200 + 50 * i, 4096), product(g, 30 + i, 2000, 3001), split(g, 128, 256, 4096 + 512 * i)]
+            for i in range(4)]
+    torch.cuda.synchronize()
+    want = []
+    for calls in todo:
+        for call, _ in calls:
+            mm.check(call(None))
+        torch.cuda.synchronize()
+        want.append([bits(outs) for _, outs in calls])
+    for calls in todo:
+        for _, outs in calls:
+            for o in outs:
+                o.view(torch.uint8).fill_(0xEE)
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(len(todo)), []
+
+    def work(calls):
+        start.wait()
+        for _ in range(40):
+            for call, _ in calls:
+                if call(PER_THREAD) != mm.MM_OK:
+                    failed.append(mm.mm_last_error())
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in todo]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed[:3]
+    for calls, w in zip(todo, want):
+        for (_, outs), x in zip(calls, w):
+            assert all(torch.equal(a, b) for a, b in zip(bits(outs), x))
