@@ -225,6 +225,18 @@ struct DevBuf {
 // default stream, whose one handle means another stream in every thread, its id.
 using StreamKey = std::pair<cudaStream_t, unsigned long long>;
 
+// A stream's scratch: slot SCRATCH_TICKETS holds zero-initialised counters that
+// kernels leave at zero; SCRATCH_WORKSPACE holds partial sums; SCRATCH_REPACK
+// copies of operands.  `mu` is held from the first request of a call to its last
+// launch (LaunchCtx::scratch_lock): the launches of one call, which hand results
+// to one another through scratch, then stand together on the stream, whatever
+// threads call on it, and no buffer is given back under a call that has it.
+enum ScratchSlot { SCRATCH_TICKETS = 0, SCRATCH_WORKSPACE = 1, SCRATCH_REPACK = 2, SCRATCH_SLOTS = 3 };
+struct StreamScratch {
+  std::mutex mu;
+  ScratchBuffer slot[SCRATCH_SLOTS];
+};
+
 struct TableEntry {
   int winner = 0;               // candidate index
   std::vector<int> ranking;     // valid candidates, fastest first
@@ -244,10 +256,8 @@ struct DeviceState {
   int *d_err = nullptr;                  // kernel error word (bounded-wait timeouts)
   cudaStream_t tune_stream = nullptr;
   cudaEvent_t ev_order = nullptr;
-  std::mutex scratch_mu;
-  // per-(stream, slot) scratch: slot SCRATCH_TICKETS holds zero-initialised
-  // counters that kernels leave at zero; SCRATCH_WORKSPACE holds partial sums
-  std::map<std::pair<StreamKey, int>, ScratchBuffer> scratch;
+  std::mutex scratch_mu;  // of the map, not of what its entries hold
+  std::map<StreamKey, std::unique_ptr<StreamScratch>> scratch;
   DevBuf flush_buf;
   DevBuf stage_a, stage_b, stage_c;        // host-buffer entry point staging
   std::mutex stage_mu;
@@ -273,12 +283,6 @@ void release_all_devices();
 void noalloc_forget_devices();
 void for_each_device(void (*fn)(DeviceState &));
 
-// Scratch of at least `bytes` private to (device, stream, slot).  A new or
-// grown buffer is zero-filled (stream-ordered).  One that was handed out while the
-// stream was being captured stays allocated until the state is dropped.
-enum ScratchSlot { SCRATCH_TICKETS = 0, SCRATCH_WORKSPACE = 1, SCRATCH_REPACK = 2 };
-mm_status get_scratch(DeviceState &ds, cudaStream_t s, int slot, size_t bytes, void **out);
-
 // ---------------------------------------------------------------- candidates
 enum Group { GROUP_GEMV = 0, GROUP_TENSOR = 1, GROUP_NAIVE = 2, GROUP_COUNT = 3 };
 constexpr int PRIORITY_MAX = 3, PRIORITY_HIGH = 2, PRIORITY_MEDIUM = 1, PRIORITY_MIN = 0,
@@ -288,7 +292,18 @@ struct LaunchCtx {
   cudaStream_t stream;
   DeviceState *dev;
   bool tuning;  // benchmark launch (counted separately)
+  std::unique_lock<std::mutex> scratch_lock{};  // see StreamScratch
+
+  void launched() {  // the call's last launch is on the stream
+    if (scratch_lock.owns_lock()) scratch_lock.unlock();
+  }
 };
+
+// Scratch of at least `bytes` private to (device, stream, slot), for the launches
+// of this call.  A new or grown buffer is zero-filled (stream-ordered).  One that
+// was handed out while the stream was being captured stays allocated until the
+// state is dropped.
+mm_status get_scratch(LaunchCtx &ctx, int slot, size_t bytes, void **out);
 
 struct Candidate {
   std::string name;

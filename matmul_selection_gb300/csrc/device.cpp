@@ -97,7 +97,8 @@ void release_all_devices() {
     DeviceState &ds = *kv.second;
     cudaSetDevice(ds.info.ordinal);
     cudaDeviceSynchronize();
-    for (auto &s : ds.scratch) scratch_release(s.second, StreamMemory{nullptr});
+    for (auto &s : ds.scratch)
+      for (ScratchBuffer &b : s.second->slot) scratch_release(b, StreamMemory{nullptr});
     ds.flush_buf.release();
     ds.stage_a.release();
     ds.stage_b.release();
@@ -116,12 +117,20 @@ static mm_status stream_key(cudaStream_t s, StreamKey *key) {
   return MM_OK;
 }
 
-mm_status get_scratch(DeviceState &ds, cudaStream_t s, int slot, size_t bytes, void **out) {
+mm_status get_scratch(LaunchCtx &ctx, int slot, size_t bytes, void **out) {
+  const cudaStream_t s = ctx.stream;
   StreamKey key;
   mm_status st = stream_key(s, &key);
   if (st != MM_OK) return st;
-  std::lock_guard<std::mutex> lk(ds.scratch_mu);
-  ScratchBuffer &b = ds.scratch[std::make_pair(key, slot)];
+  StreamScratch *all;
+  {
+    std::lock_guard<std::mutex> lk(ctx.dev->scratch_mu);
+    std::unique_ptr<StreamScratch> &e = ctx.dev->scratch[key];
+    if (!e) e = std::make_unique<StreamScratch>();
+    all = e.get();
+  }
+  if (!ctx.scratch_lock.owns_lock()) ctx.scratch_lock = std::unique_lock<std::mutex>(all->mu);
+  ScratchBuffer &b = all->slot[slot];
   // Nothing can be allocated while the stream is being captured into a
   // graph (the allocation would end the capture): the candidate declines
   // and the caller moves on to one that needs no new scratch.

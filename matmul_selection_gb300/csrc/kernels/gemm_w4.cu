@@ -537,7 +537,7 @@ mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
   p.split_scale = a.ts != a.ta;
   if (p.split_scale && a.ta == MM_F16) {
     void *f = nullptr;
-    if ((st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_WORKSPACE, (size_t)a.N * sizeof(float), &f)) != MM_OK) return st;
+    if ((st = get_scratch(ctx, SCRATCH_WORKSPACE, (size_t)a.N * sizeof(float), &f)) != MM_OK) return st;
     cudaError_t e = launch_pdl(w4_row_factor_kernel, dim3((unsigned)((a.N + 7) / 8)), dim3(256), 0, ctx.stream, dim3(1),
                                p.w, static_cast<float *>(f));
     if (e != cudaSuccess) return cuda_error(e, "gemm_w4 launch (row factors)");

@@ -437,9 +437,9 @@ mm_status launch_gemv(const Problem &p, LaunchCtx &ctx, int cfg) {
     size_t tickets_bytes = (size_t)tiles * p.batch * sizeof(unsigned);
     size_t ws_bytes = (size_t)g.S * p.batch * p.M * p.N * sizeof(float);
     void *t = nullptr, *w = nullptr;
-    mm_status st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_TICKETS, tickets_bytes, &t);
+    mm_status st = get_scratch(ctx, SCRATCH_TICKETS, tickets_bytes, &t);
     if (st != MM_OK) return st;
-    st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_WORKSPACE, ws_bytes, &w);
+    st = get_scratch(ctx, SCRATCH_WORKSPACE, ws_bytes, &w);
     if (st != MM_OK) return st;
     g.tickets = static_cast<unsigned *>(t);
     g.ws = static_cast<float *>(w);

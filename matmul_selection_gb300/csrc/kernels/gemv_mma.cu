@@ -558,9 +558,9 @@ mm_status launch_gemv_mma(const Problem &p, LaunchCtx &ctx, int cfg) {
     const size_t ws_bytes = (size_t)p.batch * g.G * g.S * 16 * kMmaCW * sizeof(float);
     const size_t tickets_bytes = (size_t)p.batch * g.G * sizeof(unsigned);
     void *w = nullptr, *t = nullptr;
-    mm_status st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_WORKSPACE, ws_bytes, &w);
+    mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, ws_bytes, &w);
     if (st != MM_OK) return st;
-    st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_TICKETS, tickets_bytes, &t);
+    st = get_scratch(ctx, SCRATCH_TICKETS, tickets_bytes, &t);
     if (st != MM_OK) return st;
     g.ws = static_cast<float *>(w);
     g.tickets = static_cast<unsigned *>(t);

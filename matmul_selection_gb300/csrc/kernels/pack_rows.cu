@@ -59,7 +59,7 @@ mm_status align_rows(TmaRows &a, TmaRows &b, LaunchCtx &ctx) {
   }
   if (!need) return MM_OK;
   void *w = nullptr;
-  mm_status st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_REPACK, need, &w);
+  mm_status st = get_scratch(ctx, SCRATCH_REPACK, need, &w);
   if (st != MM_OK) return st;
   for (int i = 0; i < 2; ++i)
     if (!addressable(*op[i]) &&

@@ -183,7 +183,7 @@ mm_status launch_repack(const Problem &p, LaunchCtx &ctx, int cfg) {
   Plan pl = make_plan_for(p);
   const int es = dtype_bytes(p.ta);
   void *scr = nullptr;
-  mm_status st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_REPACK, pl.bytes_a + pl.bytes_b + 512, &scr);
+  mm_status st = get_scratch(ctx, SCRATCH_REPACK, pl.bytes_a + pl.bytes_b + 512, &scr);
   if (st != MM_OK) return st;
   char *base = reinterpret_cast<char *>(((uintptr_t)scr + 255) & ~(uintptr_t)255);
   Problem q = pl.q;

@@ -1062,7 +1062,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float *part
 mm_status partial_space(const NormBwdArgs &a, int64_t parts, size_t more, LaunchCtx &ctx, float **out) {
   void *w = nullptr;
   const size_t bytes = (size_t)parts * (size_t)((a.cols + 3) / 4 * 4) * sizeof(float) + more;
-  mm_status st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_WORKSPACE, bytes, &w);
+  mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, bytes, &w);
   *out = static_cast<float *>(w);
   return st;
 }

@@ -2048,7 +2048,7 @@ mm_status launch_tc_impl(const Problem &p, LaunchCtx &ctx, int cfg, bool c_trans
   if (c.splitk) {
     void *w = nullptr;
     size_t ws_bytes = (size_t)tp.splits * tp.batch * (size_t)p.M * p.N * sizeof(float);
-    st = get_scratch(*ctx.dev, ctx.stream, SCRATCH_WORKSPACE, ws_bytes, &w);
+    st = get_scratch(ctx, SCRATCH_WORKSPACE, ws_bytes, &w);
     if (st != MM_OK) return st;
     tp.ws = static_cast<float *>(w);
     return es == 2 ? run_splitk<2>(p, tp, cfg, ma, mb, sms, tp.c_trans, ctx.stream)

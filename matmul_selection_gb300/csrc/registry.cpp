@@ -258,6 +258,7 @@ mm_status launch_candidate(int index, const Problem &p, LaunchCtx &ctx) {
   if (!o.fault.empty() && fault_error(o.fault, c.name))
     return set_error(MM_ERR_CUDA, "%s: injected launch error", c.name.c_str());
   mm_status st = c.launch(p, ctx, c.cfg);
+  ctx.launched();
   if (st == MM_OK) count_launch(index, ctx.tuning);
   return st;
 }

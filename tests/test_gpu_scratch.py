@@ -70,13 +70,11 @@ def test_graphs_keep_their_scratch():
 PER_THREAD = 2  # the handle of the calling thread's own default stream
 
 
-def test_per_thread_streams_have_their_own_scratch():
-    """Threads that call at one time, each on its per-thread default stream."""
+def threads_at_one_time(todo, stream):
+    """Each thread's calls over and over, all threads at one time: every one's
+    results are those of its calls alone."""
     import threading
     torch = T()
-    g = generator(33)
-    todo = [[backward(g, 200 + 50 * i, 4096), product(g, 30 + i, 2000, 3001), split(g, 128, 256, 4096 + 512 * i)]
-            for i in range(4)]
     torch.cuda.synchronize()
     want = []
     for calls in todo:
@@ -95,7 +93,7 @@ def test_per_thread_streams_have_their_own_scratch():
         start.wait()
         for _ in range(40):
             for call, _ in calls:
-                if call(PER_THREAD) != mm.MM_OK:
+                if call(stream) != mm.MM_OK:
                     failed.append(mm.mm_last_error())
 
     threads = [threading.Thread(target=work, args=(c,)) for c in todo]
@@ -108,3 +106,18 @@ def test_per_thread_streams_have_their_own_scratch():
     for calls, w in zip(todo, want):
         for (_, outs), x in zip(calls, w):
             assert all(torch.equal(a, b) for a, b in zip(bits(outs), x))
+
+
+def test_per_thread_streams_have_their_own_scratch():
+    g = generator(33)
+    threads_at_one_time([[backward(g, 200 + 50 * i, 4096), product(g, 30 + i, 2000, 3001),
+                          split(g, 128, 256, 4096 + 512 * i)] for i in range(4)], PER_THREAD)
+
+
+def test_threads_on_one_stream():
+    """Calls of several launches, with scratch between them that other threads'
+    calls of other sizes use and outgrow."""
+    g = generator(34)
+    s = T().cuda.Stream()
+    threads_at_one_time([[backward(g, 60 * 3 ** i, 4096), product(g, 40, 700 * 3 ** i, 3001),
+                          split(g, 64 * 3 ** i, 256, 4096)] for i in range(4)], s)
