@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "../../include/mm.h"
+#include "per_device.h"
 #include "scratch.h"
 
 #include <utility>
@@ -126,6 +127,11 @@ mm_status make_problem(Problem *p, const void *lhs, const void *rhs, void *out, 
 // ---------------------------------------------------------------- errors
 mm_status set_error(mm_status s, const char *fmt, ...);
 mm_status cuda_error(cudaError_t e, const char *what);
+// The ordinal that PerDevice goes by; -1 (nothing kept) where it cannot be told.
+inline int current_ordinal() {
+  int d = -1;
+  return cudaGetDevice(&d) == cudaSuccess ? d : -1;
+}
 #define MM_CUDA_TRY(expr)                                     \
   do {                                                        \
     cudaError_t e__ = (expr);                                 \

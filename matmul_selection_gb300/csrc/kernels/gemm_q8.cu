@@ -21,7 +21,6 @@
 // Every mbarrier wait is bounded (see tcgen05.cuh); a wait that gives up
 // records a code in the operators' error word.
 #include <algorithm>
-#include <mutex>
 
 #include "../operators.h"
 #include "tcgen05.cuh"
@@ -476,13 +475,11 @@ mm_status rows_map(CUtensorMap *map, const uint8_t *p, int rows, int K, int64_t 
                        kRowB, (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-mm_status pair_capacity(int *clusters) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  static int n = 0;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(q8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
-    if (err != cudaSuccess) return;
+mm_status pair_capacity(int device, int *clusters) {
+  static PerDevice<int> fits;
+  const cudaError_t err = fits.get(device, clusters, [](int *n) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(q8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = 2;
@@ -493,11 +490,10 @@ mm_status pair_capacity(int *clusters) {
     lc.dynamicSmemBytes = kPairSmem;
     lc.attrs = &at;
     lc.numAttrs = 1;
-    err = cudaOccupancyMaxActiveClusters(&n, q8_pair_kernel, &lc);
+    return cudaOccupancyMaxActiveClusters(n, q8_pair_kernel, &lc);
   });
   if (err != cudaSuccess) return cuda_error(err, "gemm_q8 set-up");
-  if (n < 1) return set_error(MM_ERR_UNSUPPORTED, "no pair of CTAs fits on this device");
-  *clusters = n;
+  if (*clusters < 1) return set_error(MM_ERR_UNSUPPORTED, "no pair of CTAs fits on this device");
   return MM_OK;
 }
 
@@ -538,11 +534,11 @@ mm_status run_pair(const Q8Args &a, Q8Params p, int clusters, LaunchCtx &ctx) {
 
 template <int BN>
 mm_status run_swap(const Q8Args &a, Q8Params p, int ranks, LaunchCtx &ctx) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(q8_swap_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)Swap<BN>::kSmem);
+  static PerDevice<int> set_up;
+  int done;
+  const cudaError_t err = set_up.get(ctx.dev->info.ordinal, &done, [](int *) {
+    return cudaFuncSetAttribute(q8_swap_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)Swap<BN>::kSmem);
   });
   if (err != cudaSuccess) return cuda_error(err, "gemm_q8 set-up");
   CUtensorMap ma, mb;
@@ -588,7 +584,7 @@ mm_status launch_gemm_q8(const Q8Args &in, LaunchCtx &ctx) {
   p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0 && a.ldc < (1LL << 37);
   p.err = ctx.dev->d_err + kOperatorErrorWord;
   int clusters = 0;
-  if ((st = pair_capacity(&clusters)) != MM_OK) return st;
+  if ((st = pair_capacity(ctx.dev->info.ordinal, &clusters)) != MM_OK) return st;
   // swap: a tile of as few rows as hold A, and K over as many CTAs as fill the SMs
   const int sms = ctx.dev->info.sms, bn = a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
   const int64_t tiles = ((int64_t)a.N + 127) / 128 * ((a.M + bn - 1) / bn);

@@ -20,7 +20,6 @@
 // 16384 70 us and 32 x 19456 x 16384 64 (2.5 TB/s), bound by the weight-making
 // warps.
 #include <algorithm>
-#include <mutex>
 
 #include "../operators.h"
 #include "tcgen05.cuh"
@@ -475,11 +474,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 template <int TA, int BN>
 mm_status run_tiles(const W4Args &a, const TmaRows &ra, const TmaRows &rw, TileParams p, LaunchCtx &ctx) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
+  static PerDevice<int> set_up;
   auto kern = w4_tile_kernel<TA, BN>;
-  std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile<BN>::kSmem);
+  int done;
+  const cudaError_t err = set_up.get(ctx.dev->info.ordinal, &done, [&](int *) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile<BN>::kSmem);
   });
   if (err != cudaSuccess) return cuda_error(err, "gemm_w4 set-up");
   CUtensorMap mw, ma;

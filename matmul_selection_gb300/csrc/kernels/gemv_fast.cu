@@ -738,10 +738,11 @@ int rows_per_rank(int64_t K) {
 template <typename F>
 cudaError_t smem_attr(F kern, size_t smem) {
   static std::mutex mu;
-  static std::map<const void *, size_t> have;
+  static std::map<std::pair<int, const void *>, size_t> have;  // on each device
+  if (smem <= 48 * 1024) return cudaSuccess;
   std::lock_guard<std::mutex> lk(mu);
-  size_t &h = have[reinterpret_cast<const void *>(kern)];
-  if (smem <= h || smem <= 48 * 1024) return cudaSuccess;
+  size_t &h = have[std::make_pair(current_ordinal(), reinterpret_cast<const void *>(kern))];
+  if (smem <= h) return cudaSuccess;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) h = smem;
   return e;

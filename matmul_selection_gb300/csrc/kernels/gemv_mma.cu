@@ -463,11 +463,11 @@ int mma_steps(const MmaArgs &g, bool bt) {
 template <bool BT, int TT, int XP, int STEPS, bool EVEN = false>
 mm_status launch_mma(const MmaArgs &g, const CUtensorMap &tm, cudaStream_t s) {
   auto kern = gemv_mma_kernel<TT, XP, STEPS, EVEN, BT>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
+  static PerDevice<int> set_up;
   constexpr size_t smem = BT ? kMmaSmemT : kMmaSmem;
-  std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  int done;
+  const cudaError_t attr = set_up.get(current_ordinal(), &done, [&](int *) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (attr != cudaSuccess) return cuda_error(attr, "gemv_mma shared memory attribute");
   cudaError_t e = launch_pdl(kern, dim3((unsigned)(g.G * g.S), (unsigned)g.batch),

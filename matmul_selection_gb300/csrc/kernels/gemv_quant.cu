@@ -22,7 +22,6 @@
 // weights of codes, at about half of the issue rate with the 16 computing warps an
 // SM that registers allow.  1 x 4096 x 4096: 4.6 (e4m3 5.2), a launch's chain.
 #include <algorithm>
-#include <mutex>
 
 #include "../operators.h"
 #include "tcgen05.cuh"
@@ -446,10 +445,10 @@ template <int F, int WR, bool TWO>
 mm_status run(const TmaRows &rx, const TmaRows &rw, int K, GemvParams p, LaunchCtx &ctx) {
   constexpr int WK = kWarps / WR, R = 16 * WR;
   auto kern = gemv_quant_kernel<F, WR, TWO>;
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  static PerDevice<int> set_up;
+  int done;
+  const cudaError_t err = set_up.get(ctx.dev->info.ordinal, &done, [&](int *) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   });
   if (err != cudaSuccess) return cuda_error(err, "quantised GEMV set-up");
   CUtensorMap mw, mx;

@@ -13,7 +13,6 @@
 // registers hold, and rows that do not start on 16 bytes, have forms of their own
 // below.
 #include <algorithm>
-#include <mutex>
 
 #include "../operators.h"
 #include "tcgen05.cuh"
@@ -1090,11 +1089,12 @@ template <int TX, int E, int V>
 mm_status bwd_warps_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   // as many blocks as are resident at once: one more would be a second, nearly
   // empty round over its share of the rows (65536 x 512 bf16: 2 an SM 50 us, 3 60)
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  static int per_sm = 0;
+  static PerDevice<int> fits;
   auto kern = rmsnorm_bwd_warps_kernel<TX, E, V>;
-  std::call_once(once, [&] { err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 256, 0); });
+  int per_sm = 0;
+  const cudaError_t err = fits.get(ctx.dev->info.ordinal, &per_sm, [&](int *n) {
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, 256, 0);
+  });
   if (err != cudaSuccess) return cuda_error(err, "rmsnorm_backward set-up");
   const int64_t blocks = std::min<int64_t>((a.rows + 7) / 8, (int64_t)std::max(1, per_sm) * ctx.dev->info.sms);
   return bwd_blocks(a, kern, blocks, 256, 0, ctx);
@@ -1104,11 +1104,11 @@ constexpr size_t kRingBytes = 208 << 10;  // of an SM's shared memory
 
 template <int TX, int T, int V, int PER_SM, bool EDGES>
 mm_status bwd_ring_form(const NormBwdArgs &a, LaunchCtx &ctx) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
+  static PerDevice<int> set_up;
   auto kern = rmsnorm_bwd_ring_kernel<TX, T, V, PER_SM, EDGES>;
-  std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+  int done;
+  const cudaError_t err = set_up.get(ctx.dev->info.ordinal, &done, [&](int *) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
   });
   if (err != cudaSuccess) return cuda_error(err, "rmsnorm_backward set-up");
   const size_t stage = (size_t)(a.dh ? 3 : 2) * ring_row<EDGES>((uint32_t)a.cols * bytes_of(TX));
@@ -1122,13 +1122,12 @@ mm_status bwd_ring_form(const NormBwdArgs &a, LaunchCtx &ctx) {
 
 template <int TX, int T, int V>
 mm_status bwd_cluster_form(const NormBwdArgs &a, LaunchCtx &ctx) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  static int resident = 0;  // clusters
+  static PerDevice<int> fits;
   auto kern = rmsnorm_bwd_cluster_kernel<TX, T, V>;
-  std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
-    if (err != cudaSuccess) return;
+  int resident = 0;  // clusters
+  const cudaError_t err = fits.get(ctx.dev->info.ordinal, &resident, [&](int *n) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute cluster = {};
     cluster.id = cudaLaunchAttributeClusterDimension;
     cluster.val.clusterDim.x = kCluster;
@@ -1139,7 +1138,7 @@ mm_status bwd_cluster_form(const NormBwdArgs &a, LaunchCtx &ctx) {
     config.dynamicSmemBytes = kRingBytes;
     config.attrs = &cluster;
     config.numAttrs = 1;
-    err = cudaOccupancyMaxActiveClusters(&resident, kern, &config);
+    return cudaOccupancyMaxActiveClusters(n, kern, &config);
   });
   if (err != cudaSuccess) return cuda_error(err, "rmsnorm_backward set-up");
   constexpr int E = 16 / bytes_of(TX);

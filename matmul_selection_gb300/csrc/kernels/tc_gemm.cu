@@ -1555,12 +1555,12 @@ uint64_t smem_desc_bits(uint32_t lbo_bytes, uint32_t sbo_bytes) {
 template <int BN, int STAGES, int ES, bool SK>
 mm_status launch_kernel(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc,
                         const TcParams &tp, int grid, cudaStream_t s) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
+  static PerDevice<int> set_up;
   const size_t smem = smem_bytes(BN, STAGES, SK);
   auto kern = tc_gemm_kernel<BN, STAGES, ES, SK>;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  int done;
+  const cudaError_t attr_err = set_up.get(current_ordinal(), &done, [&](int *) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (attr_err != cudaSuccess) return cuda_error(attr_err, "cudaFuncSetAttribute (tc smem)");
   cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kTcThreads), smem, s, dim3(1), ma, mb, mc, tp);
@@ -1588,24 +1588,20 @@ struct PairKernel {
     const TcCfg shape{"", BN, STAGES, false, true, AL};
     return smem_bytes_cfg(shape);
   }
-  // Set-up once: shared-memory attribute and how many pairs fit at once.
+  // Set-up once a device: shared-memory attribute and how many pairs fit at once.
   static mm_status capacity(int *max_clusters) {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static int clusters = 0;
-    std::call_once(once, [] {
+    static PerDevice<int> fits;
+    const cudaError_t err = fits.get(current_ordinal(), max_clusters, [](int *n) -> cudaError_t {
       auto kern = tc2_gemm_kernel<BN, STAGES, ES, AL>;
-      err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem());
-      if (err == cudaSuccess) {
-        cudaLaunchAttribute attr[1];
-        cudaLaunchConfig_t q = config(smem(), nullptr, attr);
-        q.gridDim = dim3(2);
-        err = cudaOccupancyMaxActiveClusters(&clusters, kern, &q);
-      }
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem());
+      if (e != cudaSuccess) return e;
+      cudaLaunchAttribute attr[1];
+      cudaLaunchConfig_t q = config(smem(), nullptr, attr);
+      q.gridDim = dim3(2);
+      return cudaOccupancyMaxActiveClusters(n, kern, &q);
     });
     if (err != cudaSuccess) return cuda_error(err, "tc2 kernel set-up");
-    if (clusters < 1) return set_error(MM_ERR_UNSUPPORTED, "no cluster of CTA pairs fits on this device");
-    *max_clusters = clusters;
+    if (*max_clusters < 1) return set_error(MM_ERR_UNSUPPORTED, "no cluster of CTA pairs fits on this device");
     return MM_OK;
   }
   static mm_status launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mbh,

@@ -22,3 +22,7 @@ def run(name, tmp_path):
 
 def test_scratch_outlives_the_graphs_that_hold_it(tmp_path):
     run("scratch_test", tmp_path)
+
+
+def test_set_up_is_kept_for_each_device(tmp_path):
+    run("per_device_test", tmp_path)
