@@ -23,6 +23,7 @@
 #include <algorithm>
 
 #include "../operators.h"
+#include "../q8_choice.h"
 #include "tcgen05.cuh"
 #include "values.cuh"
 
@@ -546,8 +547,7 @@ mm_status run_swap(const Q8Args &a, Q8Params p, int ranks, LaunchCtx &ctx) {
   if ((st = rows_map(&mb, a.B, a.N, a.K, a.ldb, 128)) != MM_OK) return st;
   if ((st = rows_map(&ma, a.A, a.M, a.K, a.lda, BN)) != MM_OK) return st;
   p.kb_per_rank = (p.num_kb + ranks - 1) / ranks;
-  const int gx = (a.N + 127) / 128, gz = (a.M + BN - 1) / BN;
-  if (gz > 65535) return set_error(MM_ERR_UNSUPPORTED, "too many rows of A");
+  const int gx = (a.N + 127) / 128, gz = (a.M + BN - 1) / BN;  // at most kQ8SwapRowTiles
   cudaError_t e = launch_pdl(q8_swap_kernel<BN>, dim3((unsigned)gx, (unsigned)ranks, (unsigned)gz),
                              dim3(kSwapThreads), Swap<BN>::kSmem, ctx.stream, dim3(1, (unsigned)ranks), mb, ma, p);
   return e == cudaSuccess ? MM_OK : cuda_error(e, "gemm_q8 launch (swap)");
@@ -559,12 +559,10 @@ mm_status launch_gemm_q8(const Q8Args &in, LaunchCtx &ctx) {
   Q8Args a = in;
   mm_status st;
   if (a.K == 0) return write_zeros(a.out, a.ldc, a.M, a.N, a.tc, ctx);
-  // At most 8 rows of A and too few rows of weights to fill the SMs with tiles
-  // of 128: the GEMV form, whose tiles are of 16 to 64.  us, GEMV / swap: 1 x
-  // 4096 x 4096 5.4 / 6.5, 1 x 2048 x 16384 9.2 / 13.9, 4 x 6144 x 6144 10.6 /
-  // 10.4, 1 x 8192 x 8192 16.1 / 14.2, 1 x 16384 x 8192 29.0 / 23.5; 16 rows:
-  // 16 x 4096 x 4096 7.6 / 6.7.
-  if (a.M <= 8 && a.N <= 6144) return launch_gemv_q8(a, ctx);
+  int clusters = 0;
+  if ((st = pair_capacity(ctx.dev->info.ordinal, &clusters)) != MM_OK) return st;
+  const Q8Choice form = choose_q8(a.M, a.N, ((int64_t)a.K + kRowB - 1) / kRowB, ctx.dev->info.sms, clusters);
+  if (form.form == Q8_GEMV) return launch_gemv_q8(a, ctx);
   TmaRows ra{a.A, a.lda, a.M, a.K}, rb{a.B, a.ldb, a.N, a.K};
   if ((st = align_rows(ra, rb, ctx)) != MM_OK) return st;
   a.A = static_cast<const uint8_t *>(ra.p);
@@ -583,25 +581,10 @@ mm_status launch_gemm_q8(const Q8Args &in, LaunchCtx &ctx) {
   p.num_kb = (int)(((int64_t)a.K + kRowB - 1) / kRowB);
   p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0 && a.ldc < (1LL << 37);
   p.err = ctx.dev->d_err + kOperatorErrorWord;
-  int clusters = 0;
-  if ((st = pair_capacity(ctx.dev->info.ordinal, &clusters)) != MM_OK) return st;
-  // swap: a tile of as few rows as hold A, and K over as many CTAs as fill the SMs
-  const int sms = ctx.dev->info.sms, bn = a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
-  const int64_t tiles = ((int64_t)a.N + 127) / 128 * ((a.M + bn - 1) / bn);
-  int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= sms && p.num_kb >= 4 * ranks) ranks *= 2;
-  // Above 128 rows of A, pair or swap, whichever its waves say takes less: a
-  // wave costs its stages (0.29 us of a pair's, 0.18 of a swap's, the measured
-  // slopes) and what surrounds them.  us, pair / swap: 300 x 4096 x 4096 17.5 /
-  // 13.4, 512 x 4096 x 4096 18.4 / 14.3.
-  const int64_t pairs = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + 255) / 256);
-  const double pair_us = (double)((pairs + clusters - 1) / clusters) * p.num_kb * 0.29 + 8.0;
-  const double swap_us =
-      (double)((tiles * ranks + sms - 1) / sms) * (((p.num_kb + ranks - 1) / ranks) * 0.183 + 2.5) + 5.0;
-  st = a.M > 128 && pair_us < swap_us ? run_pair(a, p, clusters, ctx)
-       : bn == 32                     ? run_swap<32>(a, p, ranks, ctx)
-       : bn == 64                     ? run_swap<64>(a, p, ranks, ctx)
-                                      : run_swap<128>(a, p, ranks, ctx);
+  st = form.form == Q8_PAIR ? run_pair(a, p, clusters, ctx)
+       : form.bn == 32      ? run_swap<32>(a, p, form.ranks, ctx)
+       : form.bn == 64      ? run_swap<64>(a, p, form.ranks, ctx)
+                            : run_swap<128>(a, p, form.ranks, ctx);
   if (st != MM_OK) return st;
   count_operator_launch();
   return MM_OK;

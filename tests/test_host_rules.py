@@ -26,3 +26,7 @@ def test_scratch_outlives_the_graphs_that_hold_it(tmp_path):
 
 def test_set_up_is_kept_for_each_device(tmp_path):
     run("per_device_test", tmp_path)
+
+
+def test_e4m3_product_chooses_a_form_that_takes_the_size(tmp_path):
+    run("q8_choice_test", tmp_path)
