@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // address are read back from the box and stored by the warp, a row at a
       // time: 330 us at 8000 x 16001 x 64.  (Stored by the lanes, a row each, 1298 us.)
       for (int i = (int)threadIdx.x - 64; i < 256; i += 128)
-        col_scale[i] = p.sb && n0 + i < p.N ? __ldg(p.sb + n0 + i) : 1.f;
+        col_scale[i] = p.sb && n0 + i < p.N ? p.sb[n0 + i] : 1.f;
       asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll 1
       for (int c = 0; c < w && n0 + c < p.N && row0 < p.M; c += step) {
@@ -457,9 +457,9 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     const int n = n0 + (STEP == 1 ? 4 * lane : lane), left = p.N - n;
     float sb[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sb[i] = p.sb && i * STEP < left ? __ldg(p.sb + n + i * STEP) : 1.f;
+    for (int i = 0; i < 4; ++i) sb[i] = p.sb && i * STEP < left ? p.sb[n + i * STEP] : 1.f;
     sum_tile<STEP == 1>(tile, rank, ranks, per, rows, warp, kSwapThreads / 32, [&](int m, float4 v) {
-      const float sa = p.sa ? __ldg(p.sa + m0 + m) : 1.f;
+      const float sa = p.sa ? p.sa[m0 + m] : 1.f;
       store_four<STEP>(p.out, p.tc, (int64_t)(m0 + m) * p.ldc + n,
                        make_float4(v.x * sa * sb[0], v.y * sa * sb[1], v.z * sa * sb[2], v.w * sa * sb[3]), left);
     });

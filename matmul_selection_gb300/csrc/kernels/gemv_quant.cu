@@ -140,14 +140,14 @@ __device__ __forceinline__ void load_panel_scales(const W4Scales &w, ScaleCursor
     const int g = min(c.g + h, c.last);
     if (w.ts == MM_F32) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) s.s[r][h] = __ldg(reinterpret_cast<const uint32_t *>(c.s[r]) + g);
+      for (int r = 0; r < 2; ++r) s.s[r][h] = reinterpret_cast<const uint32_t *>(c.s[r])[g];
     } else {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) s.s[r][h] = __ldg(reinterpret_cast<const uint16_t *>(c.s[r]) + g);
+      for (int r = 0; r < 2; ++r) s.s[r][h] = reinterpret_cast<const uint16_t *>(c.s[r])[g];
     }
     if (w.z) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) s.z[r][h] = __ldg(c.z[r] + g);
+      for (int r = 0; r < 2; ++r) s.z[r][h] = c.z[r][g];
     }
   }
   c.g += c.step;
@@ -290,7 +290,7 @@ __device__ __forceinline__ void store_sum(const GemvParams &p, const float *buf,
 #pragma unroll
   for (int q = 0; q < (PARTS ? PARTS : parts); ++q) v += buf[q * p.M * cols + o];
   if constexpr (F != FMT_E4M3) v *= Unpack<F>::kBack;
-  else v = v * (p.sa ? __ldg(p.sa + m) : 1.f) * (p.sb ? __ldg(p.sb + n) : 1.f);
+  else v = v * (p.sa ? p.sa[m] : 1.f) * (p.sb ? p.sb[n] : 1.f);
   store_value(p.out, p.tc, (int64_t)m * p.ldc + n, v);
 }
 

@@ -58,9 +58,9 @@ __device__ __forceinline__ RawScale load_raw_scale(const W4Scales &p, const Scal
   RawScale r{0u, 8u};
   const int g = k >> p.group_shift;
   if (g < row.groups) {
-    r.s = p.ts == MM_F32 ? __ldg(reinterpret_cast<const uint32_t *>(row.s) + g)
-                         : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row.s) + g);
-    if (row.z) r.z = __ldg(row.z + g);
+    r.s = p.ts == MM_F32 ? reinterpret_cast<const uint32_t *>(row.s)[g]
+                         : (uint32_t)reinterpret_cast<const uint16_t *>(row.s)[g];
+    if (row.z) r.z = row.z[g];
   }
   return r;
 }

@@ -6,6 +6,12 @@
 
 namespace mm {
 
+// These kernels start while the one before them on the stream still runs (see
+// launch_pdl), and that one may write what they read: one's output is the next
+// one's operand or scale.  So they read global memory after pdl_wait(), by plain
+// loads and TMA; __ldg and ld.global.nc want memory that nothing writes while the
+// kernel runs.
+
 struct NormArgs {
   const void *x, *residual, *weight;
   void *h, *y;
