@@ -8,15 +8,17 @@ handle, a ``torch.cuda.Stream`` or None (legacy default stream).
 
 Importing the package loads the library and fails loudly when it has not
 been built (``python matmul_selection_gb300/build.py``).  The operators that a
-model calls once a layer and token go through a small extension module instead
-of ctypes (``csrc/binding/fastcall.cpp``): the same C functions, the arguments
-converted in C.
+model calls once a layer and token go through a small extension module
+(``csrc/binding/fastcall.cpp``): the same C functions, the arguments converted
+in C.  Where it was not built for this Python they go through ctypes as well,
+which costs 2-3 us more a call.
 """
 from __future__ import annotations
 
 import ctypes
 import importlib.machinery
 import importlib.util
+import operator
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -72,15 +74,15 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 
 def _load_fastcall():
-    path = os.path.join(_HERE, "_build", "mm_fastcall.so")
+    path = os.path.join(_HERE, "_build", "mm_fastcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
+    if not os.path.exists(path):
+        return None
     loader = importlib.machinery.ExtensionFileLoader("mm_fastcall", path)
     module = importlib.util.module_from_spec(
         importlib.util.spec_from_file_location("mm_fastcall", path, loader=loader))
     loader.exec_module(module)
     return module
 
-
-_fast = _load_fastcall()
 
 _i64, _i32, _vp, _cp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_char_p
 _P32 = ctypes.POINTER(ctypes.c_int32)
@@ -347,6 +349,52 @@ def mm_splitk_gemm_noalloc_status(stream=None):
     """Synchronise `stream` and report (and clear) a bounded wait that gave up
     in a no-allocation call since the previous query."""
     return _lib.mm_splitk_gemm_noalloc_status(_stream(stream))
+
+
+def _int64(v):
+    v = operator.index(v)
+    if not -1 << 63 <= v < 1 << 63:
+        raise OverflowError("int too large for a 64-bit argument")
+    return v
+
+
+def _real(v):
+    if isinstance(v, (str, bytes)):
+        raise TypeError("a number expected")
+    return float(v)
+
+
+class _Ctypes:
+    """The extension module's functions through ctypes."""
+
+    @staticmethod
+    def rmsnorm(*args):
+        return _Ctypes._call(_lib.mm_rmsnorm, 7, 6, args)
+
+    @staticmethod
+    def rmsnorm_backward(*args):
+        return _Ctypes._call(_lib.mm_rmsnorm_backward, 7, 6, args)
+
+    @staticmethod
+    def gemm_w4(*args):
+        if not -1 << 31 <= _int64(args[12]) < 1 << 31:
+            args = (*args[:12], 0, *args[13:])  # no group: refused by the call
+        return _Ctypes._call(_lib.mm_gemm_w4, 5, 8, args)
+
+    @staticmethod
+    def gemm_q8(*args):
+        return _Ctypes._call(_lib.mm_gemm_q8, 5, 6, args)
+
+    @staticmethod
+    def _call(f, pointers, integers, args):
+        dt, *eps = args[pointers + integers:-1]
+        if len(dt) != 3:
+            raise TypeError("types: a tuple of three")
+        return f(*map(_ptr, args[:pointers]), *map(_int64, args[pointers:pointers + integers]),
+                 _dt(tuple(map(_int64, dt))), *map(_real, eps), _stream(args[-1]))
+
+
+_fast = _load_fastcall() or _Ctypes
 
 
 def _types(dt):

@@ -1,13 +1,15 @@
 """Build the library in-tree: nvcc for sm_103a, objects compiled in parallel.
 
 Produces ``matmul_selection_gb300/_build/libmm_gb300.so`` and, linked to it,
-the Python module of the operators' calls, ``_build/mm_fastcall.so``.  Usable
-as ``python matmul_selection_gb300/build.py``.
+the Python module of the operators' calls, ``_build/mm_fastcall.*.so``, for the
+Python that runs this.  That one needs g++ and Python's headers; without them
+the package calls through ctypes.  Usable as ``python matmul_selection_gb300/build.py``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import hashlib
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -19,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmm_gb300.so")
-FASTCALL = os.path.join(BUILD, "mm_fastcall.so")
+FASTCALL = os.path.join(BUILD, "mm_fastcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
 FASTCALL_SRC = os.path.join(CSRC, "binding", "fastcall.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -76,9 +78,14 @@ def _compile_fastcall() -> None:
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared",
            "-I", sysconfig.get_paths()["include"], FASTCALL_SRC, "-o", tmp,
            "-L", BUILD, "-l:libmm_gb300.so", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        print(f"mm_fastcall not built, calls go through ctypes: {e}", file=sys.stderr)
+        return
     if r.returncode != 0:
-        raise RuntimeError(f"compile failed: {FASTCALL_SRC}\n{r.stdout}\n{r.stderr}")
+        print(f"mm_fastcall not built, calls go through ctypes:\n{r.stdout}\n{r.stderr}", file=sys.stderr)
+        return
     os.replace(tmp, FASTCALL)
 
 
@@ -86,9 +93,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     bid = build_id()
     stamp = os.path.join(BUILD, "build_id")
-    if not force and os.path.exists(LIB) and os.path.exists(FASTCALL) and os.path.exists(stamp):
+    if not force and os.path.exists(LIB) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == bid:
+                if not os.path.exists(FASTCALL):  # (built with another Python)
+                    _compile_fastcall()
                 return LIB
     srcs = sources()
     objs = [os.path.join(BUILD, os.path.basename(s) + ".o") for s in srcs]
@@ -103,6 +112,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    for f in os.listdir(BUILD):
+        if f.startswith("mm_fastcall"):  # (of another build of the library)
+            os.remove(os.path.join(BUILD, f))
     _compile_fastcall()
     with open(stamp, "w") as f:
         f.write(bid)
