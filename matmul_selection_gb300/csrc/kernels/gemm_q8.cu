@@ -49,7 +49,7 @@ struct Q8Params {
   int total_units;
   int kb_per_rank;  // swap
   int vec;          // out's rows are 16-byte aligned (pair: and whole pieces of 16 bytes)
-  int *err;
+  Waits wait;
 };
 
 __device__ __forceinline__ uint32_t pack2(int tc, float lo, float hi) {
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nh = w / 2, m0 = tm * 256 + (int)pos * 128;
       const uint32_t bytes = 2 * (128 + nh) * kRowB;  // of both CTAs
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.err, kErrCopy)) {
+        if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.wait, kErrCopy)) {
           ok = false;
           break;
         }
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (leader)  // both CTAs' copies have landed
       for (int s = 0; s < kPairStages; ++s) {
         const int st = (stage + s) % kPairStages;
-        wait_drain(full0 + 8 * st, st < stage ? phase : phase ^ 1, p.err, kErrCopy);
+        wait_drain(full0 + 8 * st, st < stage ? phase : phase ^ 1, p.wait, kErrCopy);
       }
     __syncwarp();
   } else if (warp == 1) {
@@ -229,11 +229,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tm, n0, w;
         pair_unit(p, u, tm, n0, w);
         const uint32_t idesc = instr_desc(0, 256, (uint32_t)w);
-        if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.err, kErrMma)) break;
+        if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.wait, kErrMma)) break;
         fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc * 256);
         for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.err, kErrMma)) {
+          if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.wait, kErrMma)) {
             ok = false;
             break;
           }
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit<2>(drain);
-      wait_drain(drain, 0, p.err, kErrDrain);
+      wait_drain(drain, 0, p.wait, kErrDrain);
     }
     __syncwarp();
   } else {
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pair_unit(p, u, tm, n0, w);
       // the four warps go on or give up together (and are all done with the last
       // tile's column scales)
-      if (!all_of_128(warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.err, kErrStore))) break;
+      if (!all_of_128(warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore))) break;
       fence_after();
       const int row0 = tm * 256 + (int)pos * 128 + q * 32, row = row0 + lane;
       const float sa = p.sa && row < p.M ? p.sa[row] : 1.f;
@@ -415,18 +415,18 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     int i = 0;
     for (; i < nk; ++i) {
       const int st = i % S::kStages;
-      if (!warp_wait(empty0 + 8 * st, ((uint32_t)(i / S::kStages) & 1u) ^ 1u, abort_flag, p.err, kErrCopy)) break;
+      if (!warp_wait(empty0 + 8 * st, ((uint32_t)(i / S::kStages) & 1u) ^ 1u, abort_flag, p.wait, kErrCopy)) break;
       mbar_expect_tx(full0 + 8 * st, bytes);
       tma_load_2d(smem_u32(smem + st * S::kStageB + offset), map, full0 + 8 * st, (kb0 + i) * (int)kRowB, y);
     }
     for (int f = max(0, i - S::kStages); f < i; ++f)
-      wait_drain(full0 + 8 * (f % S::kStages), (uint32_t)(f / S::kStages) & 1u, p.err, kErrCopy);
+      wait_drain(full0 + 8 * (f % S::kStages), (uint32_t)(f / S::kStages) & 1u, p.wait, kErrCopy);
     __syncwarp();
   } else if (warp == 1) {
     constexpr uint32_t idesc = instr_desc(0, 128, BN);
     for (int i = 0; i < nk; ++i) {
       const int st = i % S::kStages;
-      if (!warp_wait(full0 + 8 * st, (uint32_t)(i / S::kStages) & 1u, abort_flag, p.err, kErrMma)) break;
+      if (!warp_wait(full0 + 8 * st, (uint32_t)(i / S::kStages) & 1u, abort_flag, p.wait, kErrMma)) break;
       fence_after();
       const uint32_t sb = smem_u32(smem + st * S::kStageB);
       const uint64_t bd = desc_at(sb), ad = desc_at(sb + 128 * kRowB);
@@ -436,12 +436,12 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
       mma_commit<1>(empty0 + 8 * st);
     }
     mma_commit<1>(done);
-    wait_drain(done, 0, p.err, kErrDrain);
+    wait_drain(done, 0, p.wait, kErrDrain);
     __syncwarp();
   }
   const int rows = min(BN, p.M - m0), per = BN / ranks;
   if (warp >= kSwapStore) {
-    warp_wait(done, 0, abort_flag, p.err, kErrStore);
+    warp_wait(done, 0, abort_flag, p.wait, kErrStore);
     fence_after();
     const int q = warp & 3;
     push_tile(tmem + ((uint32_t)(q * 32) << 16), smem_u32(tile), rank, ranks, per, rows,
@@ -580,7 +580,7 @@ mm_status launch_gemm_q8(const Q8Args &in, LaunchCtx &ctx) {
   p.N = a.N;
   p.num_kb = (int)(((int64_t)a.K + kRowB - 1) / kRowB);
   p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0 && a.ldc < (1LL << 37);
-  p.err = ctx.dev->d_err + kOperatorErrorWord;
+  p.wait = operator_waits(ctx);
   st = form.form == Q8_PAIR ? run_pair(a, p, clusters, ctx)
        : form.bn == 32      ? run_swap<32>(a, p, form.ranks, ctx)
        : form.bn == 64      ? run_swap<64>(a, p, form.ranks, ctx)

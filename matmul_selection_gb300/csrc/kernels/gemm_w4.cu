@@ -72,7 +72,7 @@ struct TileParams {
   int M, N;
   int num_kb, kb_per_rank;  // blocks of 64 of K, multiples of 4
   int tiles_n, tiles;
-  int *err;
+  Waits wait;
   W4Scales w;
   int split_scale;  // the scales' type is not A's
   // f16 A and wider scales, else null: for each row of weights a power of two that
@@ -217,13 +217,13 @@ __device__ __forceinline__ bool dequant_blocks(const TileParams &p, DequantRing 
     for (int b = 0; b < B; ++b) cur[b][0] = next[b][0], cur[b][1] = next[b][1];
     load_scales(i + kGroups);
     const int stage = r.stage;
-    if (!warp_wait(r.empty0 + 8 * stage, r.phase ^ 1, abort_flag, p.err, kErrDequant)) return false;
+    if (!warp_wait(r.empty0 + 8 * stage, r.phase ^ 1, abort_flag, p.wait, kErrDequant)) return false;
     if ((r.stage += kGroups) >= S::kStages) {
       r.stage -= S::kStages;
       r.phase ^= 1;
     }
     const uint32_t cs = c % S::kCodeStages;
-    if (!warp_wait(r.cfull0 + 8 * cs, (c / S::kCodeStages) & 1u, abort_flag, p.err, kErrDequant)) return false;
+    if (!warp_wait(r.cfull0 + 8 * cs, (c / S::kCodeStages) & 1u, abort_flag, p.wait, kErrDequant)) return false;
     uint4 q[2 * B];
 #pragma unroll
     for (int h = 0; h < 2 * B; ++h)
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     for (int u = first; u < p.tiles && ok; u += step)
       for (int i = 0; i < nk; i += B) {
-        if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.err, kErrCopy)) {
+        if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.wait, kErrCopy)) {
           ok = false;
           break;
         }
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     for (int s = 0; s < STAGES; ++s) {
       const int st = (stage + s) % STAGES;
-      wait_drain(full0 + 8 * st, st < stage ? phase : phase ^ 1, p.err, kErrCopy);
+      wait_drain(full0 + 8 * st, st < stage ? phase : phase ^ 1, p.wait, kErrCopy);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -353,9 +353,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint32_t phase = 0, tphase = 0;
     bool ok = true;
     for (int u = first; u < p.tiles && ok; u += step) {
-      if (!warp_wait(tempty, tphase ^ 1, abort_flag, p.err, kErrMma)) break;
+      if (!warp_wait(tempty, tphase ^ 1, abort_flag, p.wait, kErrMma)) break;
       for (int i = 0; i < nk; i += B) {
-        if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.err, kErrMma)) {
+        if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.wait, kErrMma)) {
           ok = false;
           break;
         }
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tphase ^= 1;
     }
     mma_commit<1>(drain);
-    wait_drain(drain, 0, p.err, kErrDrain);
+    wait_drain(drain, 0, p.wait, kErrDrain);
     __syncwarp();
   } else if (warp == 2) {
     int cs = 0;
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     for (int u = first; u < p.tiles && ok; u += step)
       for (int i = 0; i < nk; i += 4) {
-        if (!warp_wait(cempty0 + 8 * cs, phase ^ 1, abort_flag, p.err, kErrCodes)) {
+        if (!warp_wait(cempty0 + 8 * cs, phase ^ 1, abort_flag, p.wait, kErrCodes)) {
           ok = false;
           break;
         }
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     for (int s = 0; s < CSTAGES; ++s) {
       const int st = (cs + s) % CSTAGES;
-      wait_drain(cfull0 + 8 * st, st < cs ? phase : phase ^ 1, p.err, kErrCodes);
+      wait_drain(cfull0 + 8 * st, st < cs ? phase : phase ^ 1, p.wait, kErrCodes);
     }
     __syncwarp();
   } else if (warp >= kDequantWarp) {
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (stores) {
       uint32_t tphase = 0;
       for (int u = first; u < p.tiles; u += step) {
-        if (!warp_wait(tfull, tphase, abort_flag, p.err, kErrStore)) break;
+        if (!warp_wait(tfull, tphase, abort_flag, p.wait, kErrStore)) break;
         tphase ^= 1;
         fence_after();
         const int m0 = u / p.tiles_n * BN, n = u % p.tiles_n * 128 + q * 32 + lane;
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else {  // one tile a cluster
     const int m0 = first / p.tiles_n * BN, rows = min(BN, p.M - m0), per = BN / ranks;
     if (stores) {
-      warp_wait(tfull, 0, abort_flag, p.err, kErrStore);
+      warp_wait(tfull, 0, abort_flag, p.wait, kErrStore);
       fence_after();
     }
     if (S::kOver) cluster_sync_all();  // every CTA's rings are idle
@@ -531,7 +531,7 @@ mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
   p.N = a.N;
   // blocks of 64 of K, up to whole stages of codes (what is past K multiplies zeros)
   p.num_kb = (int)(((int64_t)a.K + 255) / 256 * 4);
-  p.err = ctx.dev->d_err + kOperatorErrorWord;
+  p.wait = operator_waits(ctx);
   p.w = w4_scales(a);
   p.split_scale = a.ts != a.ta;
   if (p.split_scale && a.ta == MM_F16) {

@@ -53,7 +53,7 @@ struct GemvParams {
   int panels, panels_per_rank;
   const float *sa, *sb;
   W4Scales w;
-  int *err;
+  Waits wait;
 };
 
 // The loads and MMAs of a panel are left for the compiler to order (they are
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int tile = tile0; tile < tiles && ok; tile += hop)
       for (int i = 0; i < steps; ++i, ++n) {
         const int st = n % kStages;
-        ok = warp_wait(empty0 + 8 * st, ((uint32_t)(n / kStages) & 1u) ^ 1u, abort_flag, p.err, kErrCopy);
+        ok = warp_wait(empty0 + 8 * st, ((uint32_t)(n / kStages) & 1u) ^ 1u, abort_flag, p.wait, kErrCopy);
         if (!ok) break;
         const int nv = min(WK, np - i * WK);
         mbar_expect_tx(full0 + 8 * st, (uint32_t)nv * bytes);
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     __syncwarp();
     for (int f = max(0, n - kStages); f < n; ++f)
-      wait_drain(full0 + 8 * (f % kStages), (uint32_t)(f / kStages) & 1u, p.err, kErrCopy);
+      wait_drain(full0 + 8 * (f % kStages), (uint32_t)(f / kStages) & 1u, p.wait, kErrCopy);
     __syncwarp();
   } else {
     const int wr = warp % WR, wk = warp / WR, t = lane & 3;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (i + 1 == steps) cursor = scale_cursor(p.w, (tile + hop) * R + row0, k0, WK * 256);
           load_panel_scales<TWO>(p.w, cursor, next);
         }
-        ok = warp_wait(full0 + 8 * st, (uint32_t)(n / kStages) & 1u, abort_flag, p.err, kErrMma);
+        ok = warp_wait(full0 + 8 * st, (uint32_t)(n / kStages) & 1u, abort_flag, p.wait, kErrMma);
         if (!ok) break;
         if (i * WK + wk < np) {
           const uint32_t off = after_wait((uint32_t)st * kStageB);
@@ -493,7 +493,7 @@ GemvParams gemv_params(void *out, int64_t ldc, int tc, int M, int N, LaunchCtx &
   p.tc = tc;
   p.M = M;
   p.N = N;
-  p.err = ctx.dev->d_err + kOperatorErrorWord;
+  p.wait = operator_waits(ctx);
   return p;
 }
 

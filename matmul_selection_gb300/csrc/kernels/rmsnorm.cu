@@ -669,6 +669,12 @@ __device__ __forceinline__ void ring_fill(const NormBwdArgs &a, int64_t r, uint3
       if (size[k]) tc::bulk_load(dst + k * row + (skip[k] ? 16u : 0u), p[k] + skip[k], size[k], bar);
   }
 }
+// After a wait that gave up, by the thread that fills the ring: no copy is in flight
+// any more (waited for with a limit).  A stage's barrier is in a phase of either
+// parity, and waiting for the other one returns at once.
+static __device__ __noinline__ void ring_drain(const uint64_t *full, int stages, int *err) {
+  for (int s = 0; s < 2 * stages; ++s) tc::wait_drain_slow(tc::smem_u32(full + s / 2), s & 1, err, kErrRing);
+}
 // Where the columns of a block's rows lie: the pieces' [head, end); how far into
 // whole pieces the inputs' are; where the inputs' pieces start in the ring's row.
 struct RingPlace {
@@ -712,17 +718,17 @@ __device__ __forceinline__ Piece<TX, 16 / bytes_of(TX)> ring_piece(const uint8_t
 
 template <int TX, int T, int V, int PER_SM, bool EDGES>
 __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormBwdArgs a, float *partial, int stages,
-                                                              int *err) {
+                                                              Waits wait) {
   constexpr int E = 16 / bytes_of(TX);
   using P = Piece<TX, E>;
   pdl_launch_dependents();
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float sh[2][2 * (T / 32)];
-  __shared__ __align__(8) uint64_t full[kMaxRing];
+  __shared__ __align__(8) uint64_t full[kMaxRing + 1];  // a stage each; the test hook's
   const int t = threadIdx.x;
   const uint32_t stage_bytes = (a.dh ? 3 : 2) * ring_row<EDGES>((uint32_t)a.cols * bytes_of(TX));
   if (t == 0) {
-    for (int s = 0; s < stages; ++s) tc::mbar_init(tc::smem_u32(full + s), 1);
+    for (int s = 0; s <= kMaxRing; ++s) tc::mbar_init(tc::smem_u32(full + s), 1);
     tc::mbar_init_fence();
   }
   __syncthreads();
@@ -750,7 +756,9 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
   const float per_col = 1.f / (float)a.cols;
   int s = 0, side = 0;
   uint32_t phase = 0;
-  bool gave_up = false;  // (a wait ran into its limit: no further one is waited for)
+  // A wait ran into its limit: no further one is waited for, and the ring is not
+  // filled again (a barrier would be armed twice).
+  bool gave_up = wait.stall && !tc::thread_wait(tc::smem_u32(full + kMaxRing), 0, wait, kErrRing);
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const float given = a.rstd ? a.rstd[r] : 0.f;
     const uint8_t *stage = ring + (size_t)s * stage_bytes;
@@ -759,7 +767,7 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
     const float edy = next_dy, eh = next_h, edh = next_dh;
     load_edge(r + gridDim.x);
     float dot = edy * ew * eh, ss = eh * eh;
-    if (!gave_up && !tc::thread_wait(tc::smem_u32(full + s), phase, err, kErrRing)) gave_up = true;
+    if (!gave_up && !tc::thread_wait(tc::smem_u32(full + s), phase, wait, kErrRing)) gave_up = true;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = v * T + t;
@@ -772,7 +780,7 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
     side ^= 1;
     // every thread is done with the row before: its stage takes the row `stages` after it
     const int64_t r_next = r + (int64_t)(stages - 1) * gridDim.x;
-    if (t == 0 && r != blockIdx.x && r_next < a.rows) fill(r_next, s == 0 ? stages - 1 : s - 1);
+    if (t == 0 && !gave_up && r != blockIdx.x && r_next < a.rows) fill(r_next, s == 0 ? stages - 1 : s - 1);
     const float c = dot * per_col * rs * rs;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -810,6 +818,7 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
     }
     if (EDGES && edge >= 0) out[edge] = edw;
   }
+  if (gave_up && t == 0) ring_drain(full, stages, wait.err);
 }
 
 // Longer rows: a cluster a row, each CTA a quarter of the columns, as above in
@@ -821,7 +830,7 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
 constexpr int kCluster = 4;
 template <int TX, int T, int V>
 __global__ void __launch_bounds__(T, 1) rmsnorm_bwd_cluster_kernel(const NormBwdArgs whole, float *partial,
-                                                                   int stages, int *err) {
+                                                                   int stages, Waits wait) {
   constexpr int E = 16 / bytes_of(TX), WARPS = T / 32;
   static_assert(WARPS >= kMaxRing, "a warp a row of the ring");
   using P = Piece<TX, E>;
@@ -830,7 +839,7 @@ __global__ void __launch_bounds__(T, 1) rmsnorm_bwd_cluster_kernel(const NormBwd
   __shared__ float2 warp_sums[kMaxRing][WARPS];
   __shared__ float2 sums[2][kMaxRing][kCluster];
   __shared__ float edges[kMaxRing][3][32];  // dy, h, dh outside the pieces; [0][31]: the given rstd
-  __shared__ __align__(8) uint64_t full[kMaxRing];
+  __shared__ __align__(8) uint64_t full[kMaxRing + 1];  // a stage each; the test hook's
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int rank = (int)blockIdx.x % kCluster;
   const int64_t first = blockIdx.x / kCluster, hop = gridDim.x / kCluster;
@@ -845,7 +854,7 @@ __global__ void __launch_bounds__(T, 1) rmsnorm_bwd_cluster_kernel(const NormBwd
   // the slices differ by a column or so: the largest one's ring in every CTA
   const uint32_t stage_bytes = (a.dh ? 3 : 2) * ring_row<true>((uint32_t)slice * bytes_of(TX));
   if (t == 0) {
-    for (int s = 0; s < stages; ++s) tc::mbar_init(tc::smem_u32(full + s), 1);
+    for (int s = 0; s <= kMaxRing; ++s) tc::mbar_init(tc::smem_u32(full + s), 1);
     tc::mbar_init_fence();
   }
   tc::cluster_sync_all();  // the others run: their memory may be written
@@ -878,7 +887,7 @@ __global__ void __launch_bounds__(T, 1) rmsnorm_bwd_cluster_kernel(const NormBwd
   float edw = 0.f;
   const float per_col = 1.f / (float)whole.cols;
   int side = 0;
-  bool gave_up = false;  // (a wait ran into its limit: no further one is waited for)
+  bool gave_up = wait.stall && !tc::thread_wait(tc::smem_u32(full + kMaxRing), 0, wait, kErrRing);  // as in the ring
   for (int64_t k0 = 0; k0 < count; k0 += stages, side ^= 1) {
     const int nb = (int)min((int64_t)stages, count - k0);
     if (warp < stages) edges[warp][0][lane] = e_dy, edges[warp][1][lane] = e_h, edges[warp][2][lane] = e_dh;
@@ -891,7 +900,7 @@ __global__ void __launch_bounds__(T, 1) rmsnorm_bwd_cluster_kernel(const NormBwd
         dot = edges[s][0][lane] * ew * eh;
         ss = eh * eh;
       }
-      if (!gave_up && !tc::thread_wait(tc::smem_u32(full + s), (uint32_t)side, err, kErrRing)) gave_up = true;
+      if (!gave_up && !tc::thread_wait(tc::smem_u32(full + s), (uint32_t)side, wait, kErrRing)) gave_up = true;
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (v < n)
@@ -942,7 +951,7 @@ __global__ void __launch_bounds__(T, 1) rmsnorm_bwd_cluster_kernel(const NormBwd
         edw += g * x * rs;
       }
       __syncthreads();  // the stage, and in the end the edges, have been read
-      if (t == 0 && k0 + stages + s < count) fill(k0 + stages + s, s);
+      if (t == 0 && !gave_up && k0 + stages + s < count) fill(k0 + stages + s, s);
     }
   }
   if (partial) {
@@ -954,6 +963,7 @@ __global__ void __launch_bounds__(T, 1) rmsnorm_bwd_cluster_kernel(const NormBwd
         for (int e = 0; e < E; ++e) out[head + (v * T + t) * E + e] = dw[v][e];
     if (warp == 0 && edge >= 0) out[edge] = edw;
   }
+  if (gave_up && t == 0) ring_drain(full, stages, wait.err);
 }
 
 // Longer rows still, and dy of another type than h: 1 / rms and the mean of g h of each row (two
@@ -1117,7 +1127,7 @@ mm_status bwd_ring_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   constexpr int E = 16 / bytes_of(TX);
   const int64_t most = (int64_t)PER_SM * ctx.dev->info.sms;
   const int64_t blocks = std::min<int64_t>(a.rows, EDGES ? std::max<int64_t>(E, most / E * E) : most);
-  return bwd_blocks(a, kern, blocks, T, stages * stage, ctx, stages, ctx.dev->d_err + kOperatorErrorWord);
+  return bwd_blocks(a, kern, blocks, T, stages * stage, ctx, stages, operator_waits(ctx));
 }
 
 template <int TX, int T, int V>
@@ -1152,7 +1162,7 @@ mm_status bwd_cluster_form(const NormBwdArgs &a, LaunchCtx &ctx) {
   mm_status st;
   if (a.dweight && (st = partial_space(a, clusters, 0, ctx, &partial)) != MM_OK) return st;
   cudaError_t e = launch_pdl(kern, dim3((unsigned)(clusters * kCluster)), dim3(T), stages * stage, ctx.stream,
-                             dim3(kCluster), a, partial, stages, ctx.dev->d_err + kOperatorErrorWord);
+                             dim3(kCluster), a, partial, stages, operator_waits(ctx));
   if (e != cudaSuccess) return cuda_error(e, "rmsnorm_backward launch (clusters)");
   count_operator_launch();
   return a.dweight ? add_parts(a, partial, (int)clusters, ctx) : MM_OK;

@@ -12,12 +12,11 @@
 
 #include <cstdint>
 
-#include "../common.h"
+#include "../operators.h"
 
 namespace mm {
 namespace tc {
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // a main-loop wait
 constexpr uint64_t kDrainLimitNs = 20000000ull;   // waits for what is in flight after an abort
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
@@ -80,10 +79,10 @@ __device__ __forceinline__ uint64_t global_ns() {
 }
 
 // Wait for the phase of `parity`, by a whole warp.  Gives up (false, in every
-// lane) when the CTA's abort flag is up, or after the limit: then it raises
+// lane) when the CTA's abort flag is up, or after the limit (Waits): then it raises
 // the flag and records `code` in the error word.
 static __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                            int *err, int code) {
+                                            int *err, uint64_t limit_ns, int code) {
   const uint64_t t0 = global_ns();
   while (true) {
 #pragma unroll 1
@@ -93,7 +92,7 @@ static __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity
     if ((threadIdx.x & 31) == 0) {
       if (*abort_flag) {
         stop = 1;
-      } else if (global_ns() - t0 > kWaitLimitNs) {
+      } else if (global_ns() - t0 > limit_ns) {
         *abort_flag = 1;
         atomicCAS(err, 0, code);
         stop = 1;
@@ -103,12 +102,12 @@ static __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity
   }
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                          int *err, int code) {
+                                          const Waits &w, int code) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return warp_wait_slow(bar, parity, abort_flag, err, code);
+  return warp_wait_slow(bar, parity, abort_flag, w.err, w.limit_ns, code);
 }
 // A bounded wait that ignores the abort flag, for copies and MMAs in flight.
-static __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, int *err, int code) {
+static __device__ __noinline__ void wait_drain_slow(uint32_t bar, uint32_t parity, int *err, int code) {
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
     if (global_ns() - t0 > kDrainLimitNs) {
@@ -116,14 +115,17 @@ static __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, in
       return;
     }
 }
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const Waits &w, int code) {
+  if (!mbar_try_wait(bar, parity)) wait_drain_slow(bar, parity, w.err, code);
+}
 
 // Wait by one thread on its own; false after the limit (recorded).
-__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, int *err, int code) {
+__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, const Waits &w, int code) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait_for(bar, parity, 20000u))
-    if (global_ns() - t0 > kWaitLimitNs) {
-      atomicCAS(err, 0, code);
+    if (global_ns() - t0 > w.limit_ns) {
+      atomicCAS(w.err, 0, code);
       return false;
     }
   return true;

@@ -80,6 +80,19 @@ mm_status align_rows(TmaRows &a, TmaRows &b, LaunchCtx &ctx);
 // there; mm_operator_status reports and clears it.
 constexpr int kOperatorErrorWord = 8;
 
+// A kernel's bounded waits: the error word, the limit of a main-loop wait (option
+// wait_limit_us), and the test hook (option wait_stall) that makes a kernel first
+// wait on a barrier that nothing arrives on.
+struct Waits {
+  int *err;
+  uint64_t limit_ns;
+  int stall;
+};
+inline Waits operator_waits(const LaunchCtx &ctx) {
+  const Options &o = get_options();
+  return Waits{ctx.dev->d_err + kOperatorErrorWord, (uint64_t)(o.wait_limit_us * 1000.0), o.wait_stall};
+}
+
 // A kernel launch of the library outside the candidates, for the counters.
 inline void count_operator_launch() { stats().launches.fetch_add(1, std::memory_order_relaxed); }
 

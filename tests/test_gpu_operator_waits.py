@@ -1,0 +1,45 @@
+"""Waits that run out: the test hook makes a kernel first wait, 1 ms, on a
+barrier that nothing arrives on.  The kernel records that, lets its copies land
+and returns; mm_operator_status reports it once; the next calls are right."""
+import pytest
+
+import matmul_selection_gb300 as mm
+from test_gpu_operators import BF, F, H, T, check_bwd, generator, rows_of, run_bwd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def stalled():
+    """Switches the hook on and off."""
+    def switch(on):
+        mm.check(mm.mm_set_option("wait_limit_us", "1000" if on else "2000000"))
+        mm.check(mm.mm_set_option("wait_stall", "1" if on else "0"))
+    yield switch
+    switch(False)
+    mm.mm_operator_status()
+
+
+def gives_up_and_recovers(call, check, switch):
+    assert mm.mm_operator_status() == mm.MM_OK
+    switch(True)
+    call()
+    assert mm.mm_operator_status() == mm.MM_ERR_TIMEOUT and "gave up" in mm.mm_last_error()
+    assert mm.mm_operator_status() == mm.MM_OK
+    switch(False)
+    for _ in range(2):
+        check(call())
+    assert mm.mm_operator_status() == mm.MM_OK
+
+
+@pytest.mark.parametrize("rows,cols,t,pad", [
+    (5000, 2048, (BF, BF, BF), 0), (3000, 4096, (BF, F, BF), 0), (2000, 8192, (F, F, F), 0),
+    (2000, 16384, (H, H, H), 0), (4001, 1003, (BF, BF, BF), 0), (1500, 4097, (F, BF, F), 3), (700, 16383, (BF, BF, BF), 0),
+    (400, 16388, (F, F, F), 0), (300, 40001, (BF, BF, BF), 5)])
+def test_backward_whose_ring_gives_up(rows, cols, t, pad, stalled):
+    """More rows than the rings hold at once, in each of the forms with a ring."""
+    g = generator(cols)
+    dy, dh, h = (rows_of(g, rows, cols, t[0], pad) for _ in range(3))
+    w = rows_of(g, 1, cols, t[1])[0]
+    gives_up_and_recovers(lambda: run_bwd(dy, dh, h, w, t, pad=pad),
+                          lambda got: check_bwd(dy, dh, h, w, t, got), stalled)
