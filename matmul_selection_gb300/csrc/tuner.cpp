@@ -251,7 +251,7 @@ CandResult bench_candidate(int idx, BenchEnv &env, double best_ms) {
   }
   LaunchCtx ctx{ds.tune_stream, &ds, true};
   const int R = (int)env.rot->sets.size();
-  cudaMemsetAsync(ds.d_err, 0, 64, ds.tune_stream);
+  cudaMemsetAsync(ds.d_err, 0, sizeof(int), ds.tune_stream);  // (the candidates' word alone)
   // warm-up
   mm_status st = launch_candidate(idx, env.rot->sets[0], ctx);
   cudaError_t ce = cudaStreamSynchronize(ds.tune_stream);
@@ -332,7 +332,7 @@ CandResult bench_candidate(int idx, BenchEnv &env, double best_ms) {
     char b[96];
     snprintf(b, sizeof b, "kernel wait gave up (code 0x%x)", err_word);
     r.err = b;
-    cudaMemset(ds.d_err, 0, 64);
+    cudaMemset(ds.d_err, 0, sizeof(int));
     return r;
   }
   if (r.state != "slow") r.state = "ok";

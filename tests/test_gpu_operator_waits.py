@@ -43,3 +43,21 @@ def test_backward_whose_ring_gives_up(rows, cols, t, pad, stalled):
     w = rows_of(g, 1, cols, t[1])[0]
     gives_up_and_recovers(lambda: run_bwd(dy, dh, h, w, t, pad=pad),
                           lambda got: check_bwd(dy, dh, h, w, t, got), stalled)
+
+
+def test_the_record_outlives_a_tuning_run(stalled):
+    """Candidates are measured between an operator's call and the query."""
+    from gpu_util import Case
+    g = generator(1)
+    dy, h = (rows_of(g, 1000, 4096, BF) for _ in range(2))
+    w = rows_of(g, 1, 4096, BF)[0]
+    stalled(True)
+    run_bwd(dy, None, h, w, (BF, BF, BF))
+    stalled(False)
+    tunes = mm.mm_get_stats()["tunes"]
+    c = Case(224, 96, 352, dist="int4", seed=77).device()
+    mm.check(mm.mm_autotune_execute(*c.args()))
+    c.check(exact=True)
+    assert mm.mm_get_stats()["tunes"] == tunes + 1
+    assert mm.mm_operator_status() == mm.MM_ERR_TIMEOUT
+    assert mm.mm_operator_status() == mm.MM_OK
