@@ -292,9 +292,10 @@ double mm_roofline_limit_ns(double ops, double peak_ops_per_s, double bytes,
  *   last before the kernel gives up, records MM_ERR_TIMEOUT's cause in its
  *   error word and returns; its drain waits keep 2 s; likewise the waits of
  *   the operators around a quantised linear layer, see mm_operator_status),
- *   wait_stall (0; test hook: 1 makes the MMA warp of those kernels first wait
- *   on a barrier that nothing arrives on, so that the wait limit runs out and
- *   the kernel's abort path runs; it never faults or hangs the device).
+ *   wait_stall (0; test hook: 1 makes the warps of those kernels that compute
+ *   first wait on a barrier that nothing arrives on, so that the wait limit
+ *   runs out and the kernel's abort path runs; it never faults or hangs the
+ *   device).
  * An environment variable, when set, takes precedence over the API (the
  * environment is read once, at first use).  Errors: MM_ERR_NOT_FOUND for an
  * unknown name, MM_ERR_INVALID_ARG for a bad value.

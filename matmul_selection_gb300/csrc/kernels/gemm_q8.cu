@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float *col_scale = reinterpret_cast<float *>(boxes + kPairBoxesB);  // of the tile being stored
   uint64_t *bars = reinterpret_cast<uint64_t *>(boxes + kPairBoxesB + 1024);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kPairStages;
-  const uint32_t tfull0 = empty0 + 8 * kPairStages, tempty0 = tfull0 + 16, drain = tempty0 + 16;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kPairStages + 5);
+  const uint32_t tfull0 = empty0 + 8 * kPairStages, tempty0 = tfull0 + 16, drain = tempty0 + 16, stall = drain + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kPairStages + 6);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t pos = cluster_ctarank();
@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty0 + 8 * a, 8);  // four storing warps of both CTAs
     }
     mbar_init(drain, 1);
+    mbar_init(stall, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -224,7 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (leader) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
+      // (test hook: a wait that only its limit ends; in the other kernels likewise)
+      bool ok = !p.wait.stall || warp_wait(stall, 0, abort_flag, p.wait, kErrMma);
       for (int u = cid; u < p.total_units && ok; u += ncl) {
         int tm, n0, w;
         pair_unit(p, u, tm, n0, w);
@@ -378,8 +380,8 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
   float *tile = reinterpret_cast<float *>(smem + S::kStages * S::kStageB);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kStages * S::kStageB + S::kTileB);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages;
-  const uint32_t done = empty0 + 8 * S::kStages;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S::kStages + 1);
+  const uint32_t done = empty0 + 8 * S::kStages, stall = done + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S::kStages + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = (int)gridDim.y, rank = (int)blockIdx.y;  // a cluster along y splits K
@@ -392,6 +394,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
       mbar_init(empty0 + 8 * s, 1);
     }
     mbar_init(done, 1);
+    mbar_init(stall, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -424,7 +427,8 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     constexpr uint32_t idesc = instr_desc(0, 128, BN);
-    for (int i = 0; i < nk; ++i) {
+    const bool ok = !p.wait.stall || warp_wait(stall, 0, abort_flag, p.wait, kErrMma);
+    for (int i = 0; i < nk && ok; ++i) {
       const int st = i % S::kStages;
       if (!warp_wait(full0 + 8 * st, (uint32_t)(i / S::kStages) & 1u, abort_flag, p.wait, kErrMma)) break;
       fence_after();

@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(codes + CSTAGES * kCodeStageB + S::kTileB);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
   const uint32_t cfull0 = empty0 + 8 * STAGES, cempty0 = cfull0 + 8 * CSTAGES;
-  const uint32_t tfull = cempty0 + 8 * CSTAGES, tempty = tfull + 8, drain = tempty + 8;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 2 * CSTAGES + 3);
+  const uint32_t tfull = cempty0 + 8 * CSTAGES, tempty = tfull + 8, drain = tempty + 8, stall = drain + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 2 * CSTAGES + 4);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster along x splits K
@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     mbar_init(tfull, 1);
     mbar_init(tempty, kStoreWarps);
     mbar_init(drain, 1);
+    mbar_init(stall, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr uint32_t idesc = instr_desc(TA == MM_BF16 ? 1 : 0, 128, BN);
     int stage = 0;
     uint32_t phase = 0, tphase = 0;
-    bool ok = true;
+    bool ok = !p.wait.stall || warp_wait(stall, 0, abort_flag, p.wait, kErrMma);
     for (int u = first; u < p.tiles && ok; u += step) {
       if (!warp_wait(tempty, tphase ^ 1, abort_flag, p.wait, kErrMma)) break;
       for (int i = 0; i < nk; i += B) {

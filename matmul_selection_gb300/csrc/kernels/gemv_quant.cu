@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   float *parts = reinterpret_cast<float *>(smem + kStages * kStageB + kSlackB);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kStageB + kSlackB + kPartsB);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 2 * kStages);
+  const uint32_t stall = empty0 + 8 * kStages;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 2 * kStages + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = (int)gridDim.y, rank = (int)blockIdx.y;  // a cluster along y splits K
   const int tile0 = (int)blockIdx.x, tiles = (p.N + R - 1) / R, hop = (int)gridDim.x;
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(full0 + 8 * s, 2);  // both copying warps arm their bytes
       mbar_init(empty0 + 8 * s, kWarps);
     }
+    mbar_init(stall, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -377,7 +379,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       load_panel_scales<TWO>(p.w, cursor, next);
     }
     int n = 0, buffer = 0;
-    bool ok = true;  // (after a wait that gave up the barriers below are still met)
+    // (after a wait that gave up the barriers below are still met)
+    bool ok = !p.wait.stall || warp_wait(stall, 0, abort_flag, p.wait, kErrMma);
     for (int tile = tile0; tile < tiles; tile += hop, buffer ^= 1) {
       float acc[MT][4];
 #pragma unroll

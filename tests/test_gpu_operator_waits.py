@@ -4,7 +4,8 @@ and returns; mm_operator_status reports it once; the next calls are right."""
 import pytest
 
 import matmul_selection_gb300 as mm
-from test_gpu_operators import BF, F, H, T, check_bwd, generator, rows_of, run_bwd
+from test_gpu_operators import (BF, F, H, check_bwd, check_q8, check_w4, generator, q8_rows, q8_scales, rows_of,
+                                run_bwd, run_q8, run_w4, w4_weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,26 @@ def test_the_record_outlives_a_tuning_run(stalled):
     assert mm.mm_get_stats()["tunes"] == tunes + 1
     assert mm.mm_operator_status() == mm.MM_ERR_TIMEOUT
     assert mm.mm_operator_status() == mm.MM_OK
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (1, 512, 4096), (3, 6000, 1000), (8, 6144, 2000),     # GEMV form, K split and not
+    (1, 6400, 4096), (30, 512, 4096), (64, 300, 8192), (100, 4096, 1000), (300, 4096, 4096),  # swap
+    (2000, 4096, 1000), (3000, 8192, 300)])               # pair
+def test_8_bit_product_that_gives_up(M, N, K, stalled):
+    g = generator(M)
+    a, b = q8_rows(g, M, K, -K % 16), q8_rows(g, N, K, -K % 16)
+    sa, sb = q8_scales(g, M), q8_scales(g, N)
+    gives_up_and_recovers(lambda: run_q8(a, b, sa, sb, BF), lambda out: check_q8(a, b, sa, sb, BF, out), stalled)
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (1, 512, 4096), (2, 20000, 1000), (4, 20000, 1000), (8, 20000, 1000), (16, 512, 4096), (16, 40000, 512),  # GEMV
+    (20, 512, 4096), (50, 512, 4096), (100, 512, 4096), (250, 512, 4096),      # tiles, K split
+    (32, 20000, 2048), (64, 20000, 2048), (128, 20000, 2048), (1000, 8192, 2048)])  # and not
+def test_4_bit_product_that_gives_up(M, N, K, stalled):
+    g = generator(M)
+    t = (BF, BF, F)
+    a = rows_of(g, M, K, BF)
+    codes, ldw, s, z, w = w4_weights(g, N, K, 64, BF, True)
+    gives_up_and_recovers(lambda: run_w4(a, codes, ldw, s, z, N, K, 64, t), lambda out: check_w4(a, w, t, out), stalled)
