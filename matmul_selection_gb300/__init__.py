@@ -138,14 +138,12 @@ EXPORTED = tuple(_sig)
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    try:  # torch tensors first: the common case, and the one that is called most
+    if x is None or isinstance(x, int):
+        return x
+    try:  # a torch tensor, the common case
         return x.data_ptr()
     except AttributeError:
         pass
-    if isinstance(x, int):
-        return x
     if hasattr(x, "ctypes"):  # numpy array (host entry point)
         return x.ctypes.data
     raise TypeError(f"cannot take the address of {type(x)}")
