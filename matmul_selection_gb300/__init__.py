@@ -166,7 +166,8 @@ def _dt(dt):
     dt = tuple(dt)
     got = _dtypes_of.get(dt)
     if got is None:
-        a, b, c = dt
+        # a number past 32 bits is no type: refused by the call
+        a, b, c = (t if -1 << 31 <= t < 1 << 31 else -1 for t in dt)
         got = _dtypes_of[dt] = mm_dtypes(a, b, c)
     return got
 

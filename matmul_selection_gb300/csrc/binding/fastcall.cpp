@@ -40,8 +40,10 @@ bool types(PyObject *o, mm_dtypes *out) {
     return false;
   }
   int64_t v[3];
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < 3; ++i) {
     if (!integer(PyTuple_GET_ITEM(o, i), &v[i])) return false;
+    if (v[i] < INT32_MIN || v[i] > INT32_MAX) v[i] = -1;  // no type: refused by the call
+  }
   out->a = (int32_t)v[0];
   out->b = (int32_t)v[1];
   out->c = (int32_t)v[2];
