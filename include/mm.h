@@ -373,7 +373,10 @@ mm_status mm_splitk_gemm_noalloc_status(void *stream);
  * have to be ordered with calls on the captured stream and with replays of
  * other graphs captured there.  (The same holds for the scratch of captured
  * products above.)
- * Sums and statistics are held in fp32.  Errors of every one of them:
+ * Sums and statistics are held in fp32.  The products read operands whose
+ * base and row distance are multiples of 16 bytes in place; others are copied
+ * into scratch of their size on every call, weights too, so lay weights out
+ * on 16 bytes.  Errors of every one of them:
  * MM_ERR_INVALID_ARG (negative size, leading dimension smaller than a row,
  * null or misaligned pointer, type out of place), MM_ERR_UNSUPPORTED (not an
  * sm_10x device, or a size beyond the limits given), MM_ERR_CUDA.
@@ -392,7 +395,8 @@ mm_status mm_splitk_gemm_noalloc_status(void *stream);
  *             otherwise: scale = max|y| / 448 (1 for a row of zeros, at least
  *             2^-126 for any other), and the 8-bit values are e4m3(y / scale),
  *             nearest even, so that y ~ scale * value.  A row that holds a
- *             NaN gets a NaN scale.
+ *             NaN gets a NaN scale.  (h * weight is formed before rstd is
+ *             known and has to lie within fp32's range.)
  *   rstd      one fp32 a row (what mm_rmsnorm_backward takes); NULL: not
  *             written.
  *   dt        a: type of x, residual and h; b: of weight; c: of y

@@ -15,7 +15,7 @@
 //          their fp32 tiles meet in distributed shared memory and are added
 //          in rank order, which is one launch, no workspace and the same bits
 //          every time.
-// Measured: 8192^3 286 us in short runs (3.84 PFLOP/s), 334 in long ones (power);
+// Measured: 8192^3 334-349 us under the power cap (279-288 in short runs, 3.9 PFLOP/s);
 // 1000 x 4096 x 4096 17.5 us, 300 x 4096 x 4096 13.4, 32 x 19456 x 16384 49 us (6.5
 // TB/s, HBM-bound), 127 x 4097 x 4100 10.3 (prologue, split and meeting).
 // Every mbarrier wait is bounded (see tcgen05.cuh); a wait that gives up

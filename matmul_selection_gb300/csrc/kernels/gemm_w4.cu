@@ -15,10 +15,10 @@
 // persistent; where there are few tiles K is split over the CTAs of a cluster,
 // whose fp32 tiles meet in distributed shared memory and are added in rank
 // order.
-// Measured (bf16, groups of 128): 4096^3 103 us (1.33 PFLOP/s), 1000 x 4096 x
+// Measured (bf16, groups of 128): 4096^3 100 us (1.37 PFLOP/s), 1000 x 4096 x
 // 4096 27.3, bound by the tensor cores and the ends of the waves; 128 x 19456 x
-// 16384 70 us and 32 x 19456 x 16384 64 (2.5 TB/s), bound by the weight-making
-// warps.
+// 16384 68 us and 32 x 19456 x 16384 65 (2.5 TB/s), bound by the weight-making
+// warps (58 % of the integer pipe, 61 % of the issue slots).
 #include <algorithm>
 
 #include "../operators.h"
@@ -503,8 +503,8 @@ mm_status run_tiles(const W4Args &a, const TmaRows &ra, const TmaRows &rw, TileP
 }
 
 // The narrowest tile that holds A's rows: the codes are unpacked once, and the
-// narrower the tile, the deeper its rings (19456 x 16384, 32 rows 64 us, 128 rows
-// 70).
+// narrower the tile, the deeper its rings (19456 x 16384, 32 rows 65 us, 128 rows
+// 68).
 template <int TA>
 mm_status launch_tiles(const W4Args &a, const TmaRows &ra, const TmaRows &rw, const TileParams &p, LaunchCtx &ctx) {
   return a.M <= 32    ? run_tiles<TA, 32>(a, ra, rw, p, ctx)
@@ -517,8 +517,8 @@ mm_status launch_tiles(const W4Args &a, const TmaRows &ra, const TmaRows &rw, co
 
 mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
   if (a.K == 0) return write_zeros(a.out, a.ldc, a.M, a.N, a.tc, ctx);
-  // Up to 16 rows the GEMV form, exact in the codes (16 x 19456 x 16384 53 us; the
-  // narrowest tiles, of 32 rows, 64).
+  // Up to 16 rows the GEMV form, exact in the codes (16 x 19456 x 16384 55 us; the
+  // narrowest tiles, of 32 rows, 65).
   if (a.M <= 16) return launch_gemv_w4(a, ctx);
   mm_status st;
   TmaRows ra{a.A, a.lda * 2, a.M, (int64_t)a.K * 2}, rw{a.codes, a.ldw / 2, a.N, ((int64_t)a.K + 1) / 2};

@@ -17,10 +17,11 @@
 // order: one launch, the same bits every time.  Where K is not split a CTA stays
 // and takes tiles in turn, its ring running on over them.
 // Measured: e4m3 1 x 16384 x 8192 (in this form) 23.5 us, 5.7 TB/s, HBM-bound;
-// 4-bit, groups of 128, 1 x 19456 x 16384 40 us (4.1 TB/s), 1 x 16384 x 8192 21, 16
-// x 16384 x 8192 f16 with zero points 32.3 (2.3 TB/s): the instructions that make
-// weights of codes, at about half of the issue rate with the 16 computing warps an
-// SM that registers allow.  1 x 4096 x 4096: 4.6 (e4m3 5.2), a launch's chain.
+// 4-bit, groups of 128, 1 x 19456 x 16384 41 us (4.0 TB/s), 1 x 16384 x 8192 22, 16
+// x 16384 x 8192 f16 with zero points 32.2 (2.3 TB/s): the instructions that make
+// weights of codes, in 64 % (one row) and 45 % (16 rows) of the issue slots with the
+// 16 computing warps an SM that registers allow.  1 x 4096 x 4096: 4.6 (e4m3 5.2), a
+// launch's chain.
 #include <algorithm>
 
 #include "../operators.h"

@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(T, PER_SM) rmsnorm_bwd_ring_kernel(const NormB
 // Longer rows: a cluster a row, each CTA a quarter of the columns, as above in
 // rows that start anywhere.  The rows of a whole ring are summed before the
 // CTAs' sums are exchanged, so that the cluster meets once for up to eight rows.
-// 2048 x 16384 f32 108 us (5.0 TB/s; in two passes over memory 127), 127 x 16385
+// 2048 x 16384 f32 104 us (5.1 TB/s; in two passes over memory 127), 127 x 16385
 // 16 (19), 1000 x 32768 bf16 72 (109).  Clusters of eight with a full ring an SM
 // find room for fewer than half as many rows at a time: 234, 25, 144.
 constexpr int kCluster = 4;
@@ -1198,8 +1198,8 @@ mm_status bwd_form(const NormBwdArgs &a, LaunchCtx &ctx) {
     } else {
       // Rows that start anywhere: up to 512 elements a warp and an element an
       // access (50000 x 333 bf16: 49 us; the ring with 64 threads 84), above that
-      // the ring (33000 x 1001 76 us, an element an access 91; 8192 x 4097 73 and
-      // 130; 2000 x 16383 82 and 201).
+      // the ring (33000 x 1001 74 us, an element an access 91; 8192 x 4097 70 and
+      // 130; 2000 x 16383 84 and 201).
       if (a.cols <= 128) return bwd_warps_form<TX, 1, 4>(a, ctx);
       if (a.cols <= 256) return bwd_warps_form<TX, 1, 8>(a, ctx);
       if (a.cols <= 512) return bwd_warps_form<TX, 1, 16>(a, ctx);
