@@ -521,6 +521,11 @@ mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
   // narrowest tiles, of 32 rows, 65).
   if (a.M <= 16) return launch_gemv_w4(a, ctx);
   mm_status st;
+  // (all scratch before the first launch: a call that is refused has launched nothing)
+  void *factor = nullptr;
+  if (a.ta == MM_F16 && a.ts != a.ta &&
+      (st = get_scratch(ctx, SCRATCH_WORKSPACE, (size_t)a.N * sizeof(float), &factor)) != MM_OK)
+    return st;
   TmaRows ra{a.A, a.lda * 2, a.M, (int64_t)a.K * 2}, rw{a.codes, a.ldw / 2, a.N, ((int64_t)a.K + 1) / 2};
   if ((st = align_rows(ra, rw, ctx)) != MM_OK) return st;
   TileParams p;
@@ -535,14 +540,12 @@ mm_status launch_gemm_w4(const W4Args &a, LaunchCtx &ctx) {
   p.wait = operator_waits(ctx);
   p.w = w4_scales(a);
   p.split_scale = a.ts != a.ta;
-  if (p.split_scale && a.ta == MM_F16) {
-    void *f = nullptr;
-    if ((st = get_scratch(ctx, SCRATCH_WORKSPACE, (size_t)a.N * sizeof(float), &f)) != MM_OK) return st;
+  if (factor) {
     cudaError_t e = launch_pdl(w4_row_factor_kernel, dim3((unsigned)((a.N + 7) / 8)), dim3(256), 0, ctx.stream, dim3(1),
-                               p.w, static_cast<float *>(f));
+                               p.w, static_cast<float *>(factor));
     if (e != cudaSuccess) return cuda_error(e, "gemm_w4 launch (row factors)");
     count_operator_launch();
-    p.row_factor = static_cast<const float *>(f);
+    p.row_factor = static_cast<const float *>(factor);
   }
   p.vec = (uintptr_t)a.out % 16 == 0 && (a.ldc * dtype_bytes(a.tc)) % 16 == 0;
   st = a.ta == MM_BF16 ? launch_tiles<MM_BF16>(a, ra, rw, p, ctx) : launch_tiles<MM_F16>(a, ra, rw, p, ctx);

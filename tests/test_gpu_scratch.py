@@ -2,7 +2,7 @@
 import pytest
 
 import matmul_selection_gb300 as mm
-from test_gpu_operators import BF, EPS, F, T, bits, generator, q8_rows, rows_of, ttype
+from test_gpu_operators import BF, EPS, F, H, T, bits, generator, q8_rows, rows_of, ttype
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,35 @@ def test_threads_on_one_stream():
     s = T().cuda.Stream()
     threads_at_one_time([[backward(g, 60 * 3 ** i, 4096), product(g, 40, 700 * 3 ** i, 3001),
                           split(g, 64 * 3 ** i, 256, 4096)] for i in range(4)], s)
+
+
+def test_a_call_refused_in_a_capture_launches_nothing():
+    """4-bit weights with row factors and operands off 16 bytes: one kind of
+    scratch is there from an earlier call, the other is not."""
+    torch = T()
+    g = generator(35)
+    M, N, K = 40, 300, 512
+    scales = {BF: rows_of(g, N, K // 64, BF, scale=0.01), F: rows_of(g, N, K // 64, F, scale=0.01)}
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    a = {t: rows_of(g, M, K, t, 3, offset=1) for t in (BF, H)}
+    out = torch.empty(M, N, device="cuda")
+    s = torch.cuda.Stream()
+
+    def call(ta, ts, stream):
+        return mm.mm_gemm_w4(a[ta], codes, scales[ts], None, out, M, N, K, K + 3, K, K // 64, N, 64, (ta, ts, F), stream)
+
+    torch.cuda.synchronize()
+    mm.check(call(BF, BF, s))
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        before = mm.mm_get_stats()["launches"]
+        refused = call(H, F, s), mm.mm_get_stats()["launches"] - before
+        mm.check(call(BF, BF, s))
+    assert refused == (mm.MM_ERR_UNSUPPORTED, 0)
+    want = bits([out])[0]
+    out.fill_(0)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits([out])[0], want)
