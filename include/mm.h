@@ -69,6 +69,9 @@ typedef enum { MM_BF16 = 0, MM_F16 = 1, MM_F32 = 2 } mm_dtype;
 /* 8-bit floating point (4 exponent, 3 mantissa bits, largest value 448, no
  * infinities), taken only by the operators that name it. */
 #define MM_E4M3 3
+/* Integers, for token numbers, taken only by the operators that name them. */
+#define MM_I32 4
+#define MM_I64 5
 
 /* Element types of A, B and C (mm_dtype values). */
 typedef struct {
@@ -468,6 +471,85 @@ mm_status mm_gemm_w4(const void *A, const void *codes, const void *scales, const
 mm_status mm_gemm_q8(const void *A, const void *B, const float *scale_a, const float *scale_b,
                      void *out, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
                      int64_t ldc, mm_dtypes dt, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The two ends of a language model: the lookup of its tokens' rows and the loss
+ * over its vocabulary, each with its gradient.  Both work on a matrix that has a
+ * row of `cols` values for each of `vocab` tokens (one matrix where the weights
+ * are tied).  The conventions are those of the operators above.  A token number
+ * outside 0 .. vocab - 1 stands for no token (padding, a position that is not
+ * trained on): its row of the outputs is zero and it adds nothing to a gradient,
+ * whatever its row of the inputs holds.  Outputs overlap no input except where
+ * said.
+ * --------------------------------------------------------------------- */
+
+/*
+ * mm_embedding -- out[t] = scale * weight[tokens[t]], formed in fp32 and rounded
+ * once.
+ *   weight    vocab x cols, type dt.a: bf16, f16 or f32.
+ *   tokens    `rows` numbers, type dt.b: MM_I32 or MM_I64.
+ *   out       rows x cols, type dt.c: bf16, f16 or f32.
+ * rows or cols of 0 is a no-op.  rows and vocab < 2^30, cols < 2^23.
+ */
+mm_status mm_embedding(const void *weight, const void *tokens, void *out, int64_t rows, int64_t cols,
+                       int64_t vocab, int64_t ldw, int64_t ldo, mm_dtypes dt, float scale, void *stream);
+
+/*
+ * mm_embedding_backward -- the gradient of mm_embedding to its matrix:
+ *   dweight[v] = base[v] + scale * sum over {t : tokens[t] = v} of dout[t]
+ * The sum is held in fp32 and rounded once, with the base; its order follows t
+ * and depends on the sizes and the tokens only, so equal calls give equal bits.
+ *   dout      rows x cols, type dt.c; tokens: type dt.b.
+ *   base      the gradient that reaches the matrix from elsewhere (the loss of
+ *             tied weights, an earlier batch), vocab x cols of type dt.a; NULL:
+ *             none.  It may be dweight in place (the same address and leading
+ *             dimension): then only the rows of tokens that occur are touched.
+ *   dweight   vocab x cols, type dt.a; every row is written otherwise.
+ * cols or vocab of 0 is a no-op.  rows and vocab < 2^30, cols < 2^23.
+ */
+mm_status mm_embedding_backward(const void *dout, const void *tokens, const void *base, void *dweight,
+                                int64_t rows, int64_t cols, int64_t vocab, int64_t lddo, int64_t ldb,
+                                int64_t lddw, mm_dtypes dt, float scale, void *stream);
+
+/*
+ * mm_cross_entropy -- the softmax cross entropy of x projected on a vocabulary,
+ * without keeping the logits:
+ *   l[t, v] = sum_c x[t, c] * weight[v, c];  lse[t] = log sum_v exp l[t, v]
+ *   loss[t] = lse[t] - l[t, targets[t]]
+ *   x         rows x cols; weight: vocab x cols; both of type dt.a: bf16 or f16.
+ *   targets   `rows` numbers, type dt.b: MM_I32 or MM_I64.
+ *   loss      `rows` fp32 (dt.c = MM_F32); 0 for a position without a target.
+ *   lse       `rows` fp32, what mm_cross_entropy_backward takes; 0 for a position
+ *             without a target; NULL: not written.
+ * The products are summed in fp32 and enter the exponentials unrounded.  Positions
+ * without a target are left out of the products, so they cost next to nothing.
+ * rows of 0 is a no-op; cols of 0 makes every logit 0.  rows, cols, vocab < 2^30.
+ */
+mm_status mm_cross_entropy(const void *x, const void *weight, const void *targets, float *loss, float *lse,
+                           int64_t rows, int64_t cols, int64_t vocab, int64_t ldx, int64_t ldw, mm_dtypes dt,
+                           void *stream);
+
+/*
+ * mm_cross_entropy_backward -- the gradients of mm_cross_entropy, the logits
+ * formed again a piece of the vocabulary at a time:
+ *   g[t, v] = dloss[t] * (exp(l[t, v] - lse[t]) - [v = targets[t]])
+ *   dx = g . weight,  dweight = g^T . x
+ *   lse       as the forward pass wrote it.
+ *   dloss     `rows` fp32: the gradient of each loss; NULL: 1.
+ *   dx        rows x cols; NULL: not computed.  It may be x in place (the same
+ *             address and leading dimension).
+ *   dweight   vocab x cols, overwritten; NULL: not computed.
+ *             Both are of type dt.c, which is dt.a.
+ * g, divided by the largest |dloss|, is rounded to dt.a (f16: after 2^14 is
+ * taken in) before the two products, whose sums are fp32; equal calls give equal
+ * bits.  In f16 positions whose dloss is below 2^-20 of the largest lose bits of
+ * their dx.  cols of 0 is a no-op; rows of 0 writes zeros to dweight.
+ * rows, cols, vocab < 2^30.
+ */
+mm_status mm_cross_entropy_backward(const void *x, const void *weight, const void *targets, const float *lse,
+                                    const float *dloss, void *dx, void *dweight, int64_t rows, int64_t cols,
+                                    int64_t vocab, int64_t ldx, int64_t ldw, int64_t lddx, int64_t lddw,
+                                    mm_dtypes dt, void *stream);
 
 /*
  * mm_operator_status -- synchronises `stream` and reports whether a kernel of

@@ -37,6 +37,7 @@ MM_ERR_NOT_FOUND = 8
 
 MM_BF16, MM_F16, MM_F32 = 0, 1, 2
 MM_E4M3 = 3  # only where an operator names it
+MM_I32, MM_I64 = 4, 5  # likewise
 MM_NN, MM_NT, MM_TN, MM_TT = 0, 1, 2, 3
 LAYOUTS = {"NN": MM_NN, "NT": MM_NT, "TN": MM_TN, "TT": MM_TT}
 
@@ -127,6 +128,10 @@ _sig = {
     "mm_rmsnorm_backward": (_i32, [_vp] * 7 + [_i64] * 6 + [mm_dtypes, ctypes.c_float, _vp]),
     "mm_gemm_w4": (_i32, [_vp] * 5 + [_i64] * 7 + [_i32, mm_dtypes, _vp]),
     "mm_gemm_q8": (_i32, [_vp] * 5 + [_i64] * 6 + [mm_dtypes, _vp]),
+    "mm_embedding": (_i32, [_vp] * 3 + [_i64] * 5 + [mm_dtypes, ctypes.c_float, _vp]),
+    "mm_embedding_backward": (_i32, [_vp] * 4 + [_i64] * 6 + [mm_dtypes, ctypes.c_float, _vp]),
+    "mm_cross_entropy": (_i32, [_vp] * 5 + [_i64] * 5 + [mm_dtypes, _vp]),
+    "mm_cross_entropy_backward": (_i32, [_vp] * 7 + [_i64] * 7 + [mm_dtypes, _vp]),
     "mm_operator_status": (_i32, [_vp]),
 }
 for _name, (_res, _args) in _sig.items():
@@ -385,12 +390,28 @@ class _Ctypes:
         return _Ctypes._call(_lib.mm_gemm_q8, 5, 6, args)
 
     @staticmethod
+    def embedding(*args):
+        return _Ctypes._call(_lib.mm_embedding, 3, 5, args)
+
+    @staticmethod
+    def embedding_backward(*args):
+        return _Ctypes._call(_lib.mm_embedding_backward, 4, 6, args)
+
+    @staticmethod
+    def cross_entropy(*args):
+        return _Ctypes._call(_lib.mm_cross_entropy, 5, 5, args)
+
+    @staticmethod
+    def cross_entropy_backward(*args):
+        return _Ctypes._call(_lib.mm_cross_entropy_backward, 7, 7, args)
+
+    @staticmethod
     def _call(f, pointers, integers, args):
-        dt, *eps = args[pointers + integers:-1]
+        dt, *reals = args[pointers + integers:-1]
         if len(dt) != 3:
             raise TypeError("types: a tuple of three")
         return f(*map(_ptr, args[:pointers]), *map(_int64, args[pointers:pointers + integers]),
-                 _dt(tuple(map(_int64, dt))), *map(_real, eps), _stream(args[-1]))
+                 _dt(tuple(map(_int64, dt))), *map(_real, reals), _stream(args[-1]))
 
 
 _fast = _load_fastcall() or _Ctypes
@@ -432,6 +453,38 @@ def mm_gemm_q8(A, B, scale_a, scale_b, out, M, N, K, lda, ldb, ldc, dtypes, stre
     if type(dtypes) is not tuple:
         dtypes = _types(dtypes)
     return _fast.gemm_q8(A, B, scale_a, scale_b, out, M, N, K, lda, ldb, ldc, dtypes, stream)
+
+
+def mm_embedding(weight, tokens, out, rows, cols, vocab, ldw, ldo, dtypes, scale=1.0, stream=None):
+    """out[t] = scale * weight[tokens[t]]; zeros where there is no such token."""
+    if type(dtypes) is not tuple:
+        dtypes = _types(dtypes)
+    return _fast.embedding(weight, tokens, out, rows, cols, vocab, ldw, ldo, dtypes, scale, stream)
+
+
+def mm_embedding_backward(dout, tokens, base, dweight, rows, cols, vocab, lddo, ldb, lddw, dtypes,
+                          scale=1.0, stream=None):
+    """dweight[v] = base[v] + scale * the sum of dout over the places of token v."""
+    if type(dtypes) is not tuple:
+        dtypes = _types(dtypes)
+    return _fast.embedding_backward(dout, tokens, base, dweight, rows, cols, vocab, lddo, ldb, lddw,
+                                    dtypes, scale, stream)
+
+
+def mm_cross_entropy(x, weight, targets, loss, lse, rows, cols, vocab, ldx, ldw, dtypes, stream=None):
+    """Softmax cross entropy of x . weight^T; the logits are not kept."""
+    if type(dtypes) is not tuple:
+        dtypes = _types(dtypes)
+    return _fast.cross_entropy(x, weight, targets, loss, lse, rows, cols, vocab, ldx, ldw, dtypes, stream)
+
+
+def mm_cross_entropy_backward(x, weight, targets, lse, dloss, dx, dweight, rows, cols, vocab, ldx, ldw,
+                              lddx, lddw, dtypes, stream=None):
+    """The gradients of mm_cross_entropy to x and to its matrix."""
+    if type(dtypes) is not tuple:
+        dtypes = _types(dtypes)
+    return _fast.cross_entropy_backward(x, weight, targets, lse, dloss, dx, dweight, rows, cols, vocab,
+                                        ldx, ldw, lddx, lddw, dtypes, stream)
 
 
 def mm_operator_status(stream=None):

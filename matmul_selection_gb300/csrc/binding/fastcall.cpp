@@ -127,8 +127,65 @@ PyObject *gemm_q8(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return PyLong_FromLong(st);
 }
 
+PyObject *embedding(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  void *p[3], *s;
+  int64_t i[5];
+  mm_dtypes t;
+  if (!convert("mm_embedding", args, n, 3, p, i) || !types(args[8], &t)) return nullptr;
+  const double scale = PyFloat_AsDouble(args[9]);
+  if ((scale == -1.0 && PyErr_Occurred()) || !stream_of(args[10], &s)) return nullptr;
+  mm_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = mm_embedding(p[0], p[1], p[2], i[0], i[1], i[2], i[3], i[4], t, (float)scale, s);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
+PyObject *embedding_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  void *p[4], *s;
+  int64_t i[6];
+  mm_dtypes t;
+  if (!convert("mm_embedding_backward", args, n, 3, p, i) || !types(args[10], &t)) return nullptr;
+  const double scale = PyFloat_AsDouble(args[11]);
+  if ((scale == -1.0 && PyErr_Occurred()) || !stream_of(args[12], &s)) return nullptr;
+  mm_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = mm_embedding_backward(p[0], p[1], p[2], p[3], i[0], i[1], i[2], i[3], i[4], i[5], t, (float)scale, s);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
+PyObject *cross_entropy(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  void *p[5], *s;
+  int64_t i[5];
+  mm_dtypes t;
+  if (!convert("mm_cross_entropy", args, n, 2, p, i) || !types(args[10], &t) || !stream_of(args[11], &s))
+    return nullptr;
+  mm_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = mm_cross_entropy(p[0], p[1], p[2], (float *)p[3], (float *)p[4], i[0], i[1], i[2], i[3], i[4], t, s);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
+PyObject *cross_entropy_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  void *p[7], *s;
+  int64_t i[7];
+  mm_dtypes t;
+  if (!convert("mm_cross_entropy_backward", args, n, 2, p, i) || !types(args[14], &t) || !stream_of(args[15], &s))
+    return nullptr;
+  mm_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = mm_cross_entropy_backward(p[0], p[1], p[2], (const float *)p[3], (const float *)p[4], p[5], p[6], i[0], i[1],
+                                 i[2], i[3], i[4], i[5], i[6], t, s);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
 #define MM_FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {MM_FAST(rmsnorm), MM_FAST(rmsnorm_backward), MM_FAST(gemm_w4), MM_FAST(gemm_q8),
+                           MM_FAST(embedding), MM_FAST(embedding_backward), MM_FAST(cross_entropy),
+                           MM_FAST(cross_entropy_backward),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "mm_fastcall", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

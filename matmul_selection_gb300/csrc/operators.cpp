@@ -1,6 +1,7 @@
-// extern "C" entry points of the operators around a quantised linear layer:
-// argument checks, then one launch function each (kernels/rmsnorm.cu,
-// kernels/gemm_w4.cu, kernels/gemm_q8.cu).
+// extern "C" entry points of the operators around a quantised linear layer and at
+// the ends of a language model: argument checks, then one launch function each
+// (kernels/rmsnorm.cu, kernels/gemm_w4.cu, kernels/gemm_q8.cu,
+// kernels/embedding.cu, kernels/cross_entropy.cu).
 #include "operators.h"
 
 #include <cmath>
@@ -11,9 +12,11 @@ using namespace mm;
 namespace {
 
 constexpr int64_t kMaxDim = 1LL << 30;
+constexpr int64_t kMaxEmbeddingCols = 1LL << 23;  // (slabs of 256 columns are a grid's y)
 
 bool is_float_type(int t) { return t == MM_BF16 || t == MM_F16 || t == MM_F32; }
-int type_bytes(int t) { return t == MM_E4M3 ? 1 : dtype_bytes(t); }
+bool is_index_type(int t) { return t == MM_I32 || t == MM_I64; }
+int type_bytes(int t) { return t == MM_E4M3 ? 1 : t == MM_I32 ? 4 : t == MM_I64 ? 8 : dtype_bytes(t); }
 
 // A rows x cols operand with leading dimension ld: ld covers a row, the
 // pointer is there and on a multiple of the element size.
@@ -38,6 +41,20 @@ mm_status check_vector(const char *name, const void *p, int t) {
 
 mm_status check_eps(float eps) {
   if (!(eps >= 0.f) || std::isinf(eps)) return set_error(MM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  return MM_OK;
+}
+
+mm_status check_embedding_types(mm_dtypes dt) {
+  if (!is_float_type(dt.a) || !is_float_type(dt.c))
+    return set_error(MM_ERR_INVALID_ARG, "types of the matrix and the rows (%d, %d): bf16, f16 or f32", dt.a, dt.c);
+  if (!is_index_type(dt.b)) return set_error(MM_ERR_INVALID_ARG, "type of tokens %d: i32 or i64", dt.b);
+  return MM_OK;
+}
+
+mm_status check_loss_types(mm_dtypes dt) {
+  if (dt.a != MM_BF16 && dt.a != MM_F16)
+    return set_error(MM_ERR_INVALID_ARG, "type of x and weight %d: bf16 or f16", dt.a);
+  if (!is_index_type(dt.b)) return set_error(MM_ERR_INVALID_ARG, "type of targets %d: i32 or i64", dt.b);
   return MM_OK;
 }
 
@@ -184,6 +201,100 @@ mm_status mm_gemm_q8(const void *A, const void *B, const float *scale_a, const f
     Q8Args a{static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(B), scale_a, scale_b, out,
              (int)M, (int)N, (int)K, lda, ldb, ldc, dt.c};
     return launch_gemm_q8(a, ctx);
+  });
+}
+
+mm_status mm_embedding(const void *weight, const void *tokens, void *out, int64_t rows, int64_t cols,
+                       int64_t vocab, int64_t ldw, int64_t ldo, mm_dtypes dt, float scale, void *stream) {
+  return guarded([&]() -> mm_status {
+    if (rows < 0 || cols < 0 || vocab < 0) return set_error(MM_ERR_INVALID_ARG, "negative size");
+    MM_TRY(check_embedding_types(dt));
+    if (rows == 0 || cols == 0) return MM_OK;
+    if (rows >= kMaxDim || cols >= kMaxEmbeddingCols || vocab >= kMaxDim) return set_error(MM_ERR_UNSUPPORTED, "size too large");
+    if (vocab > 0) MM_TRY(check_rows("weight", weight, vocab, cols, ldw, dt.a));
+    MM_TRY(check_vector("tokens", tokens, dt.b));
+    MM_TRY(check_rows("out", out, rows, cols, ldo, dt.c));
+    LaunchCtx ctx;
+    MM_TRY(operator_context(stream, &ctx));
+    EmbedArgs a{weight, tokens, out, rows, (int)cols, vocab, ldw, ldo, dt.a, dt.b, dt.c, scale};
+    return launch_embedding(a, ctx);
+  });
+}
+
+mm_status mm_embedding_backward(const void *dout, const void *tokens, const void *base, void *dweight,
+                                int64_t rows, int64_t cols, int64_t vocab, int64_t lddo, int64_t ldb,
+                                int64_t lddw, mm_dtypes dt, float scale, void *stream) {
+  return guarded([&]() -> mm_status {
+    if (rows < 0 || cols < 0 || vocab < 0) return set_error(MM_ERR_INVALID_ARG, "negative size");
+    MM_TRY(check_embedding_types(dt));
+    if (cols == 0 || vocab == 0) return MM_OK;
+    if (rows >= kMaxDim || cols >= kMaxEmbeddingCols || vocab >= kMaxDim) return set_error(MM_ERR_UNSUPPORTED, "size too large");
+    if (rows > 0) {
+      MM_TRY(check_rows("dout", dout, rows, cols, lddo, dt.c));
+      MM_TRY(check_vector("tokens", tokens, dt.b));
+    }
+    if (base) MM_TRY(check_rows("base", base, vocab, cols, ldb, dt.a));
+    MM_TRY(check_rows("dweight", dweight, vocab, cols, lddw, dt.a));
+    if (base == dweight && ldb != lddw && vocab > 1)
+      return set_error(MM_ERR_INVALID_ARG, "base in place of dweight with another leading dimension");
+    LaunchCtx ctx;
+    MM_TRY(operator_context(stream, &ctx));
+    EmbedBwdArgs a{dout, tokens, base, dweight, rows, (int)cols, vocab, lddo, ldb, lddw, dt.a, dt.b, dt.c, scale};
+    return launch_embedding_backward(a, ctx);
+  });
+}
+
+mm_status mm_cross_entropy(const void *x, const void *weight, const void *targets, float *loss, float *lse,
+                           int64_t rows, int64_t cols, int64_t vocab, int64_t ldx, int64_t ldw, mm_dtypes dt,
+                           void *stream) {
+  return guarded([&]() -> mm_status {
+    if (rows < 0 || cols < 0 || vocab < 0) return set_error(MM_ERR_INVALID_ARG, "negative size");
+    MM_TRY(check_loss_types(dt));
+    if (dt.c != MM_F32) return set_error(MM_ERR_INVALID_ARG, "type of loss and lse %d: f32", dt.c);
+    if (rows == 0) return MM_OK;
+    if (rows >= kMaxDim || cols >= kMaxDim || vocab >= kMaxDim) return set_error(MM_ERR_UNSUPPORTED, "size too large");
+    if (cols > 0 && vocab > 0) {
+      MM_TRY(check_rows("x", x, rows, cols, ldx, dt.a));
+      MM_TRY(check_rows("weight", weight, vocab, cols, ldw, dt.a));
+    }
+    MM_TRY(check_vector("targets", targets, dt.b));
+    MM_TRY(check_vector("loss", loss, MM_F32));
+    if (lse) MM_TRY(check_vector("lse", lse, MM_F32));
+    LaunchCtx ctx;
+    MM_TRY(operator_context(stream, &ctx));
+    LossArgs a{x, weight, targets, loss, lse, (int)rows, (int)cols, (int)vocab, ldx, ldw, dt.a, dt.b,
+               nullptr, nullptr, nullptr, 0, 0};
+    return launch_cross_entropy(a, ctx);
+  });
+}
+
+mm_status mm_cross_entropy_backward(const void *x, const void *weight, const void *targets, const float *lse,
+                                    const float *dloss, void *dx, void *dweight, int64_t rows, int64_t cols,
+                                    int64_t vocab, int64_t ldx, int64_t ldw, int64_t lddx, int64_t lddw,
+                                    mm_dtypes dt, void *stream) {
+  return guarded([&]() -> mm_status {
+    if (rows < 0 || cols < 0 || vocab < 0) return set_error(MM_ERR_INVALID_ARG, "negative size");
+    MM_TRY(check_loss_types(dt));
+    if (dt.c != dt.a) return set_error(MM_ERR_INVALID_ARG, "type of dx and dweight %d: that of x (%d)", dt.c, dt.a);
+    if (cols == 0 || (!dx && !dweight)) return MM_OK;
+    if (rows >= kMaxDim || cols >= kMaxDim || vocab >= kMaxDim) return set_error(MM_ERR_UNSUPPORTED, "size too large");
+    if (dx && rows > 0) MM_TRY(check_rows("dx", dx, rows, cols, lddx, dt.a));
+    if (dweight && vocab > 0) MM_TRY(check_rows("dweight", dweight, vocab, cols, lddw, dt.a));
+    if (rows > 0 && vocab > 0) {
+      MM_TRY(check_rows("x", x, rows, cols, ldx, dt.a));
+      MM_TRY(check_rows("weight", weight, vocab, cols, ldw, dt.a));
+      MM_TRY(check_vector("targets", targets, dt.b));
+      MM_TRY(check_vector("lse", lse, MM_F32));
+      if (dloss) MM_TRY(check_vector("dloss", dloss, MM_F32));
+      if (dweight == weight) return set_error(MM_ERR_INVALID_ARG, "dweight may not be weight in place");
+    } else if (rows == 0 ? !dweight || vocab == 0 : !dx) {
+      return MM_OK;  // nothing to write
+    }
+    LaunchCtx ctx;
+    MM_TRY(operator_context(stream, &ctx));
+    LossArgs a{x, weight, targets, nullptr, const_cast<float *>(lse), (int)rows, (int)cols, (int)vocab, ldx, ldw,
+               dt.a, dt.b, dloss, dx, dweight, lddx, lddw};
+    return launch_cross_entropy_backward(a, ctx);
   });
 }
 

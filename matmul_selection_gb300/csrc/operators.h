@@ -1,5 +1,6 @@
-// Internal declarations of the operators around a quantised linear layer:
-// what operators.cpp has checked and the kernels take.
+// Internal declarations of the operators (those around a quantised linear layer
+// and those at the ends of a language model): what operators.cpp has checked and
+// the kernels take.
 #pragma once
 
 #include "common.h"
@@ -62,6 +63,43 @@ mm_status launch_gemm_q8(const Q8Args &a, LaunchCtx &ctx);
 // Their forms for at most 16 and at most 8 rows of A (K > 0).
 mm_status launch_gemv_w4(const W4Args &a, LaunchCtx &ctx);
 mm_status launch_gemv_q8(const Q8Args &a, LaunchCtx &ctx);
+
+struct EmbedArgs {
+  const void *weight, *tokens;
+  void *out;
+  int64_t rows;
+  int cols;
+  int64_t vocab, ldw, ldo;
+  int tw, ti, to;  // ti: MM_I32 or MM_I64
+  float scale;
+};
+mm_status launch_embedding(const EmbedArgs &a, LaunchCtx &ctx);
+
+struct EmbedBwdArgs {
+  const void *dout, *tokens, *base;  // base null: none
+  void *dweight;
+  int64_t rows;
+  int cols;
+  int64_t vocab, lddo, ldb, lddw;
+  int tw, ti, to;  // dweight and base; tokens; dout
+  float scale;
+};
+mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx);
+
+// The loss over a vocabulary and its gradients (those: dloss or null for 1, dx
+// and dweight, either null).
+struct LossArgs {
+  const void *x, *weight, *targets;
+  float *loss, *lse;
+  int rows, cols, vocab;
+  int64_t ldx, ldw;
+  int tx, ti;
+  const float *dloss;
+  void *dx, *dweight;
+  int64_t lddx, lddw;
+};
+mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx);
+mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx);
 
 // The product over no k.
 mm_status write_zeros(void *out, int64_t ldc, int M, int N, int tc, LaunchCtx &ctx);
