@@ -16,13 +16,17 @@
 #include <algorithm>
 
 #include "../operators.h"
+#include "../per_device.h"
 #include "indices.cuh"
 #include "tcgen05.cuh"
+#include "tile_out.cuh"
 #include "values.cuh"
 
 namespace mm {
 
 namespace {
+
+using namespace tc;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRowTile = 256;
@@ -43,6 +47,7 @@ struct Rows {
   int *count;       // [0] the rows that count
   float *gain;      // largest |dloss|
   int *slot;        // [rows] i of a row, or -1
+  int *row;         // [rows] the row of an i
   int *target;      // [rows_pad], -1 past the count
   float *ratio;     // [rows_pad] dloss / gain (f16: times kF16Gain), 0 past the count
   float *lse2;      // [rows_pad] lse log2(e)
@@ -111,6 +116,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
     if (i < r1) p.r.slot[i] = target >= 0 ? before + at : -1;
     if (target >= 0) {
       at_row[at] = i;
+      p.r.row[before + at] = i;
       p.r.target[before + at] = target;
       if (p.backward) {
         const float d = a.dloss ? a.dloss[i] : 1.f;
@@ -155,126 +161,428 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
 }
 
 // ---------------------------------------------------------------- the products
+// Products on tcgen05 (kind::f16), one after another:
+//   LSE, G   x W^T, both K-major: the sums of a tile's rows, or g in 16 bits
+//   DX       g W, W MN-major as it lies, K the piece of the vocabulary; added to
+//            fp32 sums over the pieces
+//   DW       g^T x, both MN-major as they lie, K the rows
+// 256 x 256 tiles on pairs of SMs, or 128 x 256 on single ones where there are few
+// rows; persistent, two accumulators in TMEM, so that a tile's epilogue runs under
+// the next tile's main loop.  Neither the rows that count nor the tiles are known
+// to the host: each kernel reads the count and lays out its own tiles.
 enum Mode { MODE_LSE, MODE_G, MODE_DX, MODE_DW };
+
+constexpr int kThreads = 192;  // warp 0 copies, warp 1 issues MMAs, warps 2-5 take tiles out
+constexpr int kErrCopy = 0xa01, kErrMma = 0xa02, kErrStore = 0xa03, kErrDrain = 0xa04;
+constexpr int kGroupRows = 8;  // row tiles walked together, so that their operands stay in L2
+
+// How the tiles of a product are walked: grouped by row tiles; those of a last wave
+// that fills at most half the places (all, where there are so few) as two halves.
+struct Tiles {
+  int tiles_m, tiles_n, full, total;
+};
+__device__ __forceinline__ Tiles tiles_of(int M, int tile_m, int tiles_n, int splits, int bn, int places) {
+  Tiles s;
+  s.tiles_m = (M + tile_m - 1) / tile_m;
+  s.tiles_n = tiles_n;
+  const int tiles = s.tiles_m * tiles_n * splits, rem = tiles % places;
+  const bool halve = bn == 256 && rem > 0 && 2 * rem <= places;
+  s.full = halve ? tiles - rem : tiles;
+  s.total = halve ? tiles + rem : tiles;
+  return s;
+}
+struct Unit {
+  int tm, n0, w, split;
+};
+__device__ __forceinline__ Unit unit_at(const Tiles &s, int bn, int u) {
+  int t = u, half = -1;
+  if (u >= s.full) t = s.full + ((u - s.full) >> 1), half = (u - s.full) & 1;
+  Unit x;
+  const int area = s.tiles_m * s.tiles_n;
+  x.split = t / area;
+  t -= x.split * area;
+  const int per = kGroupRows * s.tiles_n, g = t / per, rows = min(kGroupRows, s.tiles_m - g * kGroupRows);
+  const int r = t - g * per;
+  x.tm = g * kGroupRows + r % rows;
+  x.n0 = (r / rows) * bn + (half > 0 ? bn / 2 : 0);
+  x.w = half < 0 ? bn : bn / 2;
+  return x;
+}
+// Whether tile (tm, tn) of split 0 is walked as halves.
+__device__ __forceinline__ bool halved(const Tiles &s, int tm, int tn) {
+  const int g = tm / kGroupRows, rows = min(kGroupRows, s.tiles_m - g * kGroupRows);
+  return g * kGroupRows * s.tiles_n + tn * rows + tm - g * kGroupRows >= s.full;
+}
 
 struct TileParams {
   Rows r;
-  const uint16_t *W;
-  int64_t ldw;
   int cols, vocab;
   int v0, width;     // the piece of the vocabulary: its first token, how many (G: padded to 64)
   int tx;
-  float2 *part;      // LSE: [tile of the vocabulary][rows_pad] (r, s)
+  int bn, tiles_n, splits, places;
+  int num_kb;        // 64-element blocks of K (DW: of the rows that count)
+  int kb_per_split;  // DX
+  float2 *part;      // LSE: [128 of the vocabulary][rows_pad] (r, s)
   float *hit;        // LSE: [rows_pad] the target's logit
-  uint16_t *g;       // [rows_pad][ldg]
-  int64_t ldg;
-  float *acc;        // DX: [rows_pad][ldacc]
-  int64_t ldacc;
+  float *acc;        // DX: [split][32 rows][32 columns][4 columns][row]
+  int acc_cols;      // DX: blocks of 32 columns
   int first;         // DX: the first piece
   uint16_t *dw;
   int64_t lddw;
+  int vec;           // DW: its rows are whole 16-byte pieces
+  Waits wait;
 };
 
-__device__ __forceinline__ float value16(const uint16_t *p, int t, int64_t i) {
-  return t == MM_BF16 ? __bfloat162float(__ushort_as_bfloat16(p[i])) : __half2float(__ushort_as_half(p[i]));
-}
-__device__ __forceinline__ uint16_t bits16(int t, float v) {
-  return t == MM_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+template <int CG>
+struct Ring {
+  static constexpr int kStages = CG == 2 ? 6 : 4;
+  static constexpr uint32_t kA = 128 * 128, kStageB = kA + (CG == 2 ? 128 : 256) * 128;
+  static constexpr uint32_t kBoxes = 4 * 2 * kBoxB;  // two for each warp that takes tiles out
+  static constexpr size_t kSmem = kStages * kStageB + kBoxes + 1024 + 256;
+};
+
+template <int CG>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
+  if constexpr (CG == 2) tma_load_2d_pair(dst, map, bar, x, y);
+  else tma_load_2d(dst, map, bar, x, y);
 }
 
-// 64 x 64 of a product, 4 x 4 a thread.
-template <int MODE>
-__global__ void __launch_bounds__(256) tile_kernel(const TileParams p) {
+// What a tile leaves (by one warp: 32 rows of TMEM from `tmem` on).
+// A row's sum of 2^(l log2e - r) and r over w columns.
+__device__ __forceinline__ void take_lse(const TileParams &p, uint32_t tmem, const Unit &u, int row) {
+  if (u.n0 >= p.vocab) return;  // (a half tile past the end)
+  const int target = p.r.target[row];
+  float r = -3e38f, s = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < u.w && u.n0 + c < p.vocab; c += 32) {
+    uint32_t v[32];
+    tmem_ld_32cols(tmem + (uint32_t)c, v);
+    tmem_ld_wait();
+    const int left = p.vocab - u.n0 - c;
+    if (left < 32) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i >= left) v[i] = 0xff800000u;  // -infinity
+    }
+    float top[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      top[k] = __uint_as_float(v[k]);
+#pragma unroll
+      for (int i = k + 4; i < 32; i += 4) top[k] = fmaxf(top[k], __uint_as_float(v[i]));
+    }
+    const float next = fmaxf(r, ceilf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e));
+    float sum[4] = {s * exp2_fast(r - next), 0.f, 0.f, 0.f};
+    r = next;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum[i & 3] += exp2_fast(fmaf(__uint_as_float(v[i]), kLog2e, -r));
+    s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    const int at = target - u.n0 - c;
+    if (__any_sync(0xffffffffu, (unsigned)at < 32u)) {
+      float h = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) h = at == i ? __uint_as_float(v[i]) : h;
+      if ((unsigned)at < 32u) p.hit[row] = h;
+    }
+  }
+  p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row] = make_float2(r, s);
+}
+
+// 64 columns of 32 rows in 16 bits to a box.
+template <typename F>
+__device__ __forceinline__ void fill_box(uint8_t *box, int tx, F &&value) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_uint4(pack2(tx, value(8 * j), value(8 * j + 1)), pack2(tx, value(8 * j + 2), value(8 * j + 3)),
+                   pack2(tx, value(8 * j + 4), value(8 * j + 5)), pack2(tx, value(8 * j + 6), value(8 * j + 7)));
+}
+
+__device__ __forceinline__ void take_g(const TileParams &p, const CUtensorMap *map, uint32_t tmem, const Unit &u,
+                                       int row0, uint8_t *boxes, int &side) {
+  const int lane = threadIdx.x & 31, row = row0 + lane;
+  const int target = p.r.target[row];
+  const float ratio = p.r.ratio[row], lse2 = p.r.lse2[row];
+  const bool live = ratio != 0.f;  // (a weight of 0 takes its row out, whatever its logits)
+#pragma unroll 1
+  for (int c = 0; c < u.w && u.n0 + c < p.width; c += 64) {
+    uint32_t v[2][32];
+    tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
+    tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+      float &x = reinterpret_cast<float &>(v[i >> 5][i & 31]);
+      x = exp2_fast(fmaf(x, kLog2e, -lse2)) * ratio;
+    }
+    const int at = target - p.v0 - u.n0 - c;
+    if (__any_sync(0xffffffffu, (unsigned)at < 64u)) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        float &x = reinterpret_cast<float &>(v[i >> 5][i & 31]);
+        x = at == i ? x - ratio : x;
+      }
+    }
+    const int left = p.vocab - p.v0 - u.n0 - c;
+    if (left < 64 || __any_sync(0xffffffffu, !live)) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] = live && i < left ? v[i >> 5][i & 31] : 0u;
+    }
+    if (lane == 0) tma_store_wait_read<1>();  // this box's previous store has read it
+    __syncwarp();
+    uint8_t *box = boxes + side * kBoxB;
+    fill_box(box, p.tx, [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); });
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tma_store_2d(map, smem_u32(box), u.n0 + c, row0);
+    side ^= 1;
+  }
+}
+
+__device__ __forceinline__ void take_dw(const TileParams &p, const CUtensorMap *map, uint32_t tmem, const Unit &u,
+                                        int row0, uint8_t *boxes, int &side, float gain) {
+  const int lane = threadIdx.x & 31, v0 = p.v0 + row0;
+  if (v0 >= p.vocab) return;
+#pragma unroll 1
+  for (int c = 0; c < u.w && u.n0 + c < p.cols; c += 64) {
+    uint32_t v[2][32];
+    tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
+    tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
+    tmem_ld_wait();
+    if (lane == 0) tma_store_wait_read<1>();
+    __syncwarp();
+    uint8_t *box = boxes + side * kBoxB;
+    fill_box(box, p.tx, [&](int i) { return __uint_as_float(v[i >> 5][i & 31]) * gain; });
+    if (p.vec) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tma_store_2d(map, smem_u32(box), u.n0 + c, v0);
+    } else {  // rows that TMA cannot address, or would clip behind their end
+      __syncwarp();
+      store_box<2>(box, p.dw, (int64_t)v0 * p.lddw + u.n0 + c, p.lddw, min(32, p.vocab - v0),
+                   min(64, p.cols - u.n0 - c));
+      __syncwarp();
+    }
+    side ^= 1;
+  }
+}
+
+// Added to the pieces before; the layout has a lane's 16 bytes beside the next one's.
+__device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, const Unit &u, int row0, bool empty) {
+  const int lane = threadIdx.x & 31;
+  if (empty && !p.first) return;
+#pragma unroll 1
+  for (int c = 0; c < u.w; c += 32) {
+    const int cb = (u.n0 + c) >> 5;
+    if (cb >= p.acc_cols) break;
+    float4 *to = reinterpret_cast<float4 *>(
+                     p.acc + (((int64_t)u.split * (p.r.rows_pad >> 5) + (row0 >> 5)) * p.acc_cols + cb) * 1024) + lane;
+    float4 sum[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] = p.first ? make_float4(0.f, 0.f, 0.f, 0.f) : to[k * 32];
+    uint32_t v[32];
+    tmem_ld_32cols(tmem + (uint32_t)c, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (!empty) {
+        sum[k].x += __uint_as_float(v[4 * k]), sum[k].y += __uint_as_float(v[4 * k + 1]);
+        sum[k].z += __uint_as_float(v[4 * k + 2]), sum[k].w += __uint_as_float(v[4 * k + 3]);
+      }
+      to[k * 32] = sum[k];
+    }
+  }
+}
+
+template <int MODE, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmO,
+                const TileParams p) {
+  using R = Ring<CG>;
+  constexpr int S = R::kStages;
+  constexpr bool kMnA = MODE == MODE_DW, kMnB = MODE == MODE_DX || MODE == MODE_DW;
   pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *boxes = smem + S * R::kStageB;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(boxes + R::kBoxes);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S;
+  const uint32_t tfull0 = empty0 + 8 * S, tempty0 = tfull0 + 16, drain = tempty0 + 16, stall = drain + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 6);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pos = CG == 2 ? (int)cluster_ctarank() : 0;
+  const bool leader = pos == 0;
+  const int cid = (int)blockIdx.x / CG, ncl = (int)gridDim.x / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, 4 * CG);
+    }
+    mbar_init(drain, 1);
+    mbar_init(stall, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmBh);
+    if (MODE == MODE_G || (MODE == MODE_DW && p.vec)) prefetch_tmap(&tmO);
+  }
+  if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), 512);
+  fence_before();
+  if (CG == 2) cluster_sync_all();
+  else __syncthreads();
+  fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t leader_full0 = CG == 2 ? map_to_rank(full0, 0) : full0;
+  const uint32_t leader_tempty0 = CG == 2 ? map_to_rank(tempty0, 0) : tempty0;
   pdl_wait();
-  __shared__ float sa[16][65], sb[16][65];
-  const int count = *p.r.count, rows = max(1, (count + 63) / 64) * 64;
-  const int m0 = (int)blockIdx.y * 64, n0 = (int)blockIdx.x * 64, t = threadIdx.x;
-  const int tm = t >> 4, tn = t & 15;
-  constexpr bool kLogits = MODE == MODE_LSE || MODE == MODE_G;
-  const int M = MODE == MODE_DW ? p.width : rows;
-  const int K = kLogits ? p.cols : MODE == MODE_DX ? p.width : rows;
-  if (m0 >= M) return;
-  const auto A = [&](int m, int k) -> float {
-    if (m >= M || k >= K) return 0.f;
-    if (kLogits) return value16(p.r.x, p.tx, (int64_t)m * p.r.ldx + k);
-    if (MODE == MODE_DX) return value16(p.g, p.tx, (int64_t)m * p.ldg + k);
-    return value16(p.g, p.tx, (int64_t)k * p.ldg + m);
+  const int rows = max(1, *p.r.count);
+  const Tiles tiles = tiles_of(MODE == MODE_DW ? p.width : rows, 128 * CG, p.tiles_n, p.splits, p.bn, p.places);
+  const int num_kb = MODE == MODE_DW ? (rows + 63) / 64 : p.num_kb;
+  // the blocks of K of a unit
+  const auto k_of = [&](const Unit &u, int &kb0) {
+    kb0 = u.split * p.kb_per_split;
+    return MODE == MODE_DX ? max(0, min(p.kb_per_split, num_kb - kb0)) : num_kb;
   };
-  const auto B = [&](int n, int k) -> float {
-    if (k >= K) return 0.f;
-    if (kLogits) return p.v0 + n < p.vocab ? value16(p.W, p.tx, (int64_t)(p.v0 + n) * p.ldw + k) : 0.f;
-    if (n >= p.cols) return 0.f;
-    if (MODE == MODE_DX) return p.v0 + k < p.vocab ? value16(p.W, p.tx, (int64_t)(p.v0 + k) * p.ldw + n) : 0.f;
-    return value16(p.r.x, p.tx, (int64_t)k * p.r.ldx + n);
-  };
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    for (int i = t; i < 1024; i += 256) {
-      // neighbouring threads along what is contiguous in memory
-      const int am = MODE == MODE_DW ? i & 63 : i >> 4, ak = MODE == MODE_DW ? i >> 6 : i & 15;
-      sa[ak][am] = A(m0 + am, k0 + ak);
-      const int bn = kLogits ? i >> 4 : i & 63, bk = kLogits ? i & 15 : i >> 6;
-      sb[bk][bn] = B(n0 + bn, k0 + bk);
+
+  if (warp == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int i = cid; i < tiles.total && ok; i += ncl) {
+      const Unit u = unit_at(tiles, p.bn, i);
+      int kb0;
+      const int nk = k_of(u, kb0), nh = u.w / CG, m0 = u.tm * 128 * CG + pos * 128, n0 = u.n0 + pos * nh;
+      for (int kb = kb0; kb < kb0 + nk; ++kb) {
+        if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.wait, kErrCopy)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = smem_u32(smem + stage * R::kStageB), sb = sa + R::kA, bar = leader_full0 + 8 * stage;
+        if (leader) mbar_expect_tx(full0 + 8 * stage, (uint32_t)(CG * (128 + nh)) * 128);
+        if (!kMnA) load_box<CG>(sa, &tmA, bar, kb * 64, m0);
+        else
+          for (int j = 0; j < 2; ++j) load_box<CG>(sa + j * 8192, &tmA, bar, m0 + j * 64, kb * 64);
+        if (!kMnB) load_box<CG>(sb, u.w == p.bn ? &tmB : &tmBh, bar, kb * 64, n0);
+        else
+          for (int j = 0; j < nh / 64; ++j) load_box<CG>(sb + j * 8192, &tmB, bar, n0 + j * 64, kb * 64);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
     }
-    __syncthreads();
+    if (leader)  // the copies (of both CTAs) have landed
+      for (int s = 0; s < S; ++s) {
+        const int st = (stage + s) % S;
+        wait_drain(full0 + 8 * st, st < stage ? phase : phase ^ 1, p.wait, kErrCopy);
+      }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (leader) {
+      constexpr uint64_t kDescA = kMnA ? kDescMnMajor128 : kDescKMajor128;
+      constexpr uint64_t kDescB = kMnB ? kDescMnMajor128 : kDescKMajor128;
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = !p.wait.stall || warp_wait(stall, 0, abort_flag, p.wait, kErrMma);  // (test hook)
+      for (int i = cid; i < tiles.total && ok; i += ncl) {
+        const Unit u = unit_at(tiles, p.bn, i);
+        int kb0;
+        const int nk = k_of(u, kb0);
+        const uint32_t idesc = instr_desc(p.tx == MM_BF16, 128 * CG, (uint32_t)u.w) | (kMnA ? kMnMajorA : 0u) |
+                               (kMnB ? kMnMajorB : 0u);
+        if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.wait, kErrMma)) break;
+        fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * 256);
+        for (int k = 0; k < nk; ++k) {
+          if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.wait, kErrMma)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint32_t sa = smem_u32(smem + stage * R::kStageB);
+          const uint64_t ad = kDescA | (uint64_t)((sa >> 4) & 0x3FFFu);
+          const uint64_t bd = kDescB | (uint64_t)(((sa + R::kA) >> 4) & 0x3FFFu);
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][tm * 4 + i] * sb[k][tn * 4 + j];
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + tm * 4 + i;
-    if constexpr (kLogits) {
-      const int target = p.r.target[m];
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16<CG>(d, ad + (kMnA ? 128 : 2) * kk, bd + (kMnB ? 128 : 2) * kk, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+          if (CG == 2) mma_commit_pair(empty0 + 8 * stage);
+          else mma_commit<1>(empty0 + 8 * stage);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (CG == 2) mma_commit_pair(tfull0 + 8 * acc);
+        else mma_commit<1>(tfull0 + 8 * acc);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      mma_commit<CG>(drain);
+      wait_drain(drain, 0, p.wait, kErrDrain);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;  // the TMEM lanes this warp may read
+    uint8_t *mine = boxes + (warp - 2) * 2 * kBoxB;
+    const float gain = MODE == MODE_DW ? *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f) : 0.f;
+    int acc = 0, side = 0;
+    uint32_t acc_phase = 0;
+    for (int i = cid; i < tiles.total; i += ncl) {
+      const Unit u = unit_at(tiles, p.bn, i);
+      if (!warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)) break;
+      fence_after();
+      const int row0 = u.tm * 128 * CG + pos * 128 + q * 32;
+      const uint32_t tmem = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
+      int kb0;
       if constexpr (MODE == MODE_LSE) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n0 + tn * 4 + j < p.vocab) top = fmaxf(top, acc[i][j]);
-        for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float r = top == -INFINITY ? 0.f : ceilf(top * kLog2e);
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = n0 + tn * 4 + j;
-          if (n < p.vocab) s += exp2_fast(fmaf(acc[i][j], kLog2e, -r));
-          if (n == target) p.hit[m] = acc[i][j];
-        }
-        for (int o = 1; o < 16; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (tn == 0) p.part[(int64_t)blockIdx.x * p.r.rows_pad + m] = make_float2(r, s);
+        if (row0 < rows) take_lse(p, tmem, u, row0 + lane);
+      } else if constexpr (MODE == MODE_G) {
+        take_g(p, &tmO, tmem, u, row0, mine, side);
+      } else if constexpr (MODE == MODE_DX) {
+        if (row0 < rows) take_dx(p, tmem, u, row0, k_of(u, kb0) == 0);
       } else {
-        const float ratio = p.r.ratio[m], lse2 = p.r.lse2[m];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = n0 + tn * 4 + j;
-          if (n >= p.width) continue;
-          float g = 0.f;
-          if (target >= 0 && p.v0 + n < p.vocab)
-            g = ratio * (exp2_fast(fmaf(acc[i][j], kLog2e, -lse2)) - (p.v0 + n == target ? 1.f : 0.f));
-          p.g[(int64_t)m * p.ldg + n] = bits16(p.tx, g);
-        }
+        take_dw(p, &tmO, tmem, u, row0, mine, side, gain);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tn * 4 + j;
-        if (n >= p.cols) continue;
-        if constexpr (MODE == MODE_DX) {
-          float *to = p.acc + (int64_t)m * p.ldacc + n;
-          *to = p.first ? acc[i][j] : *to + acc[i][j];
-        } else {
-          if (p.v0 + m >= p.vocab || m >= M) continue;
-          const float gain = *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
-          p.dw[(int64_t)(p.v0 + m) * p.lddw + n] = bits16(p.tx, acc[i][j] * gain);
-        }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2) mbar_arrive_cluster(leader_tempty0 + 8 * acc);
+        else mbar_arrive(tempty0 + 8 * acc);
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
       }
     }
+    if (lane == 0) tma_store_wait_all();
+    __syncwarp();
   }
+  fence_before();
+  __syncthreads();
+  if (CG == 2) {
+    if (*abort_flag) {  // the other CTA's copies into this one may still be landing
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 100000ull) __nanosleep(1000);
+    }
+    cluster_sync_all();  // the leader's MMAs read both CTAs' memory
+  }
+  fence_after();
+  if (warp == 1) tmem_dealloc<CG>(tmem_base, 512);
 }
 
 // ---------------------------------------------------------------- loss and dx by row
@@ -283,7 +591,7 @@ struct LossParams {
   Rows r;
   const float2 *part;
   const float *hit;
-  int tiles;
+  int tile_m, bn, tiles_n, places;  // of the product
 };
 
 // 32 rows a block, 8 threads a row over the tiles of the vocabulary; the last
@@ -296,8 +604,11 @@ __global__ void __launch_bounds__(256) loss_kernel(const LossParams p) {
   const int64_t row = (int64_t)blockIdx.x * 32 + x;
   const int slot = row < p.a.rows ? p.r.slot[row] : -1;
   float r = -INFINITY, s = 0.f;
+  const Tiles tiles = tiles_of(max(1, *p.r.count), p.tile_m, p.tiles_n, 1, p.bn, p.places);
   if (slot >= 0)
-    for (int i = y; i < p.tiles; i += 8) {
+    for (int i = y; i * 128 < p.a.vocab; i += 8) {
+      // a whole tile of 256 has left its sums with its first half
+      if ((i & 1) && p.bn == 256 && !halved(tiles, slot / p.tile_m, i >> 1)) continue;
       const float2 v = p.part[(int64_t)i * p.r.rows_pad + slot];
       const float top = fmaxf(r, v.x);
       s = s * exp2_fast(r - top) + v.y * exp2_fast(v.x - top);
@@ -322,18 +633,54 @@ struct DxParams {
   LossArgs a;
   Rows r;
   const float *acc;
-  int64_t ldacc;
+  int acc_cols, splits;
+  int vec;  // dx's rows start on 16 bytes
 };
+// A warp 32 rows by 32 columns, a row a lane: the splits added in order, scaled and
+// rounded.  Then the rows that do not count.
 __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   pdl_launch_dependents();
   pdl_wait();
+  const int lane = threadIdx.x & 31, count = *p.r.count;
   const float gain = *p.r.gain * (p.a.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
-  for (int64_t row = blockIdx.x; row < p.a.rows; row += gridDim.x) {
-    const int slot = p.r.slot[row];
-    for (int c = threadIdx.x; c < p.a.cols; c += 256)
-      static_cast<uint16_t *>(p.a.dx)[row * p.a.lddx + c] =
-          slot < 0 ? (uint16_t)0 : bits16(p.a.tx, p.acc[(int64_t)slot * p.ldacc + c] * gain);
+  const int64_t warps = (int64_t)gridDim.x * 8, warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  uint16_t *dx = static_cast<uint16_t *>(p.a.dx);
+  const int64_t split_at = (int64_t)p.r.rows_pad * p.acc_cols * 8;  // float4 a split
+  for (int64_t b = warp; b < (int64_t)((count + 31) / 32) * p.acc_cols; b += warps) {
+    const int rb = (int)(b / p.acc_cols), cb = (int)(b - (int64_t)rb * p.acc_cols);
+    const float4 *from = reinterpret_cast<const float4 *>(p.acc) + b * 256 + lane;
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = from[k * 32];
+    for (int s = 1; s < p.splits; ++s)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 w = from[s * split_at + k * 32];
+        v[k].x += w.x, v[k].y += w.y, v[k].z += w.z, v[k].w += w.w;
+      }
+    const int i = rb * 32 + lane;
+    if (i >= count) continue;
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      w[2 * k] = pack2(p.a.tx, v[k].x * gain, v[k].y * gain);
+      w[2 * k + 1] = pack2(p.a.tx, v[k].z * gain, v[k].w * gain);
+    }
+    uint16_t *to = dx + (int64_t)p.r.row[i] * p.a.lddx + cb * 32;
+    const int left = p.a.cols - cb * 32;
+    if (p.vec && left >= 32) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        reinterpret_cast<uint4 *>(to)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (e < left) to[e] = (uint16_t)(w[e >> 1] >> (e & 1) * 16);
+    }
   }
+  for (int64_t row = warp; row < p.a.rows; row += warps)
+    if (p.r.slot[row] < 0)
+      for (int c = lane; c < p.a.cols; c += 32) dx[row * p.a.lddx + c] = 0;
 }
 
 // A call's scratch, cut up.
@@ -356,6 +703,7 @@ Rows cut_rows(Cut &cut, const LossArgs &a, bool backward) {
   r.count = cut.take<int>(1);
   r.gain = cut.take<float>(1);
   r.slot = cut.take<int>(a.rows);
+  r.row = cut.take<int>(a.rows);
   r.target = cut.take<int>(r.rows_pad);
   if (backward) {
     r.ratio = cut.take<float>(r.rows_pad);
@@ -374,27 +722,136 @@ mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, LaunchC
   return MM_OK;
 }
 
-template <int MODE>
-mm_status launch_tiles(const TileParams &p, int M, int N, LaunchCtx &ctx) {
-  cudaError_t e = launch_pdl(tile_kernel<MODE>, dim3((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64)), dim3(256), 0,
-                             ctx.stream, dim3(1), p);
+// The maps of a product's operands: rows of 16-bit elements, in boxes of 64 elements
+// (128 bytes, swizzled) by `box_rows`.
+mm_status rows_map(CUtensorMap *map, int tx, const void *p, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+  return encode_map_2d(map, tx == MM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p,
+                       (uint64_t)cols, (uint64_t)rows, (uint64_t)ld * 2, 64, (uint32_t)box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int MODE, int CG>
+cudaLaunchConfig_t tile_config(int grid, cudaStream_t s, cudaLaunchAttribute *at) {
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = CG;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = Ring<CG>::kSmem;
+  lc.stream = s;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return lc;
+}
+// Set-up once a device, and how many pairs (or CTAs) run at once.
+template <int MODE, int CG>
+mm_status tile_places(LaunchCtx &ctx, int *places) {
+  static PerDevice<int> fits;
+  const cudaError_t err = fits.get(ctx.dev->info.ordinal, places, [](int *n) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(tile_kernel<MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Ring<CG>::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t lc = tile_config<MODE, CG>(CG, nullptr, &at);
+    return cudaOccupancyMaxActiveClusters(n, tile_kernel<MODE, CG>, &lc);
+  });
+  if (err != cudaSuccess) return cuda_error(err, "cross_entropy set-up");
+  if (*places < 1) return set_error(MM_ERR_UNSUPPORTED, "no tile of cross_entropy fits on this device");
+  return MM_OK;
+}
+
+// A form of the products: few rows on single SMs.
+struct Form {
+  int cg;  // 1 or 2
+  int tile_m() const { return 128 * cg; }
+};
+Form form_of(int rows) { return Form{rows <= 128 ? 1 : 2}; }
+
+struct Maps {
+  CUtensorMap a, b, bh, o;
+};
+
+// M, N: the product's (M as if every row counted).
+template <int MODE, int CG>
+mm_status launch_tiles(TileParams &p, const Maps &m, int64_t M, LaunchCtx &ctx) {
+  mm_status st = tile_places<MODE, CG>(ctx, &p.places);
+  if (st != MM_OK) return st;
+  const int64_t tiles = (M + 128 * CG - 1) / (128 * CG) * p.tiles_n * p.splits;
+  if (tiles >= 1 << 30) return set_error(MM_ERR_UNSUPPORTED, "too many tiles");
+  const int grid = CG * (int)std::min<int64_t>(p.bn == 256 ? 2 * tiles : tiles, p.places);
+  cudaError_t e = launch_pdl(tile_kernel<MODE, CG>, dim3((unsigned)grid), dim3(kThreads), Ring<CG>::kSmem, ctx.stream,
+                             dim3(CG), m.a, m.b, m.bh, m.o, p);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch");
   count_operator_launch();
   return MM_OK;
+}
+template <int MODE>
+mm_status launch_tiles(Form f, TileParams &p, const Maps &m, int64_t M, LaunchCtx &ctx) {
+  return f.cg == 1 ? launch_tiles<MODE, 1>(p, m, M, ctx) : launch_tiles<MODE, 2>(p, m, M, ctx);
+}
+
+// Width of a product's tiles along N.
+int tile_width(int64_t N) { return N <= 128 ? 128 : 256; }
+
+// x W^T over `width` tokens from v0 on, LSE or G.
+mm_status logits_maps(Maps *m, TileParams &p, Form f, const TmaRows &w) {
+  p.bn = tile_width(p.width);
+  p.tiles_n = (p.width + p.bn - 1) / p.bn;
+  p.splits = 1;
+  p.num_kb = p.kb_per_split = (p.cols + 63) / 64;
+  const char *base = static_cast<const char *>(w.p) + (int64_t)p.v0 * w.ld;
+  const int64_t tokens = std::min(p.width, p.vocab - p.v0);
+  mm_status st;
+  if ((st = rows_map(&m->a, p.tx, p.r.x, p.cols, p.r.rows_pad, p.r.ldx, 128)) != MM_OK) return st;
+  if ((st = rows_map(&m->b, p.tx, base, p.cols, tokens, w.ld / 2, p.bn / f.cg)) != MM_OK) return st;
+  return rows_map(&m->bh, p.tx, base, p.cols, tokens, w.ld / 2, p.bn / f.cg / 2);
+}
+
+// W where TMA can read it: in place, or copied.
+mm_status align_weight(const LossArgs &a, TmaRows *w, LaunchCtx &ctx) {
+  *w = TmaRows{a.weight, a.ldw * 2, a.vocab, (int64_t)a.cols * 2};
+  TmaRows none{nullptr, 16, 1, 16};
+  return align_rows(*w, none, ctx);
+}
+
+TileParams tile_params(const LossArgs &a, LaunchCtx &ctx) {
+  TileParams p;
+  std::memset(&p, 0, sizeof p);
+  p.cols = a.cols;
+  p.vocab = a.vocab;
+  p.tx = a.tx;
+  p.wait = operator_waits(ctx);
+  return p;
+}
+
+// No columns: every logit is 0.
+__global__ void __launch_bounds__(256) flat_loss_kernel(const LossArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.rows) return;
+  const float v = valid_target(a, i) >= 0 ? logf((float)a.vocab) : 0.f;
+  a.loss[i] = v;
+  if (a.lse) a.lse[i] = v;
 }
 
 }  // namespace
 
 mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
-  TileParams p;
-  std::memset(&p, 0, sizeof p);
-  const int tiles = (a.vocab + 63) / 64;
+  if (a.cols == 0 || a.vocab == 0) {
+    cudaError_t e = launch_pdl(flat_loss_kernel, dim3((unsigned)((a.rows + 255) / 256)), dim3(256), 0, ctx.stream, dim3(1), a);
+    if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch (no products)");
+    count_operator_launch();
+    return MM_OK;
+  }
+  TileParams p = tile_params(a, ctx);
   Cut cut;
   for (int pass = 0; pass < 2; ++pass) {
     cut.used = 0;
     p.r = cut_rows(cut, a, false);
     p.hit = cut.take<float>(p.r.rows_pad);
-    p.part = cut.take<float2>((int64_t)tiles * p.r.rows_pad);
+    p.part = cut.take<float2>(((int64_t)a.vocab + 127) / 128 * p.r.rows_pad);
     if (pass == 0) {
       void *w = nullptr;
       mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, cut.used, &w);
@@ -402,15 +859,17 @@ mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
       cut.base = static_cast<char *>(w);
     }
   }
-  p.W = static_cast<const uint16_t *>(a.weight);
-  p.ldw = a.ldw;
-  p.cols = a.cols;
-  p.vocab = p.width = a.vocab;
-  p.tx = a.tx;
-  mm_status st = launch_gather(a, p.r, false, ctx);
-  if (st != MM_OK) return st;
-  if (tiles > 0 && (st = launch_tiles<MODE_LSE>(p, a.rows, a.vocab, ctx)) != MM_OK) return st;
-  LossParams l{a, p.r, p.part, p.hit, tiles};
+  mm_status st;
+  TmaRows w;
+  if ((st = align_weight(a, &w, ctx)) != MM_OK) return st;
+  if ((st = launch_gather(a, p.r, false, ctx)) != MM_OK) return st;
+  const Form f = form_of(a.rows);
+  p.width = a.vocab;
+  Maps m;
+  if ((st = logits_maps(&m, p, f, w)) != MM_OK) return st;
+  m.o = m.a;  // (none)
+  if ((st = launch_tiles<MODE_LSE>(f, p, m, a.rows, ctx)) != MM_OK) return st;
+  LossParams l{a, p.r, p.part, p.hit, f.tile_m(), p.bn, p.tiles_n, p.places};
   cudaError_t e = launch_pdl(loss_kernel, dim3((unsigned)((a.rows + 31) / 32)), dim3(256), 0, ctx.stream, dim3(1), l);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch (loss)");
   count_operator_launch();
@@ -420,17 +879,28 @@ mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
 mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   if (a.rows == 0) return write_zeros(a.dweight, a.lddw, a.vocab, a.cols, a.tx, ctx);
   if (a.vocab == 0) return write_zeros(a.dx, a.lddx, a.rows, a.cols, a.tx, ctx);
-  TileParams p;
-  std::memset(&p, 0, sizeof p);
-  const int piece = std::min((a.vocab + 63) / 64 * 64, 4096);
+  TileParams p = tile_params(a, ctx);
+  const Form f = form_of(a.rows);
+  const int64_t rows_pad = ((int64_t)a.rows + kRowTile - 1) / kRowTile * kRowTile;
+  // Pieces of the vocabulary of equal size, whole tiles, whose g takes kPieceBytes
+  // at most (and at least one tile).
+  constexpr int64_t kPieceBytes = 512ll << 20;
+  const int64_t most = std::max<int64_t>(256, kPieceBytes / (rows_pad * 2) / 256 * 256);
+  const int64_t pieces = (a.vocab + most - 1) / most;
+  const int piece = (int)std::min(((a.vocab + pieces - 1) / pieces + 255) / 256 * 256, ((int64_t)a.vocab + 63) / 64 * 64);
+  // dx: K is split where the tiles are fewer than the places
+  const int bn_cols = tile_width(a.cols), tiles_cols = (a.cols + bn_cols - 1) / bn_cols;
+  const int64_t dx_tiles = ((int64_t)a.rows + f.tile_m() - 1) / f.tile_m() * tiles_cols;
+  const int places = ctx.dev->info.sms / f.cg;
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(places / dx_tiles, piece / 64 / 8));
+  p.acc_cols = (a.cols + 31) / 32;
   Cut cut;
+  uint16_t *g = nullptr;
   for (int pass = 0; pass < 2; ++pass) {
     cut.used = 0;
     p.r = cut_rows(cut, a, true);
-    p.ldg = piece;
-    p.g = cut.take<uint16_t>((int64_t)p.r.rows_pad * piece);
-    p.ldacc = ((int64_t)a.cols + 63) / 64 * 64;
-    if (a.dx) p.acc = cut.take<float>((int64_t)p.r.rows_pad * p.ldacc);
+    g = cut.take<uint16_t>(rows_pad * piece);
+    if (a.dx) p.acc = cut.take<float>(splits * rows_pad * p.acc_cols * 32);
     if (pass == 0) {
       void *w = nullptr;
       mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, cut.used, &w);
@@ -438,26 +908,46 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
       cut.base = static_cast<char *>(w);
     }
   }
-  p.W = static_cast<const uint16_t *>(a.weight);
-  p.ldw = a.ldw;
-  p.cols = a.cols;
-  p.vocab = a.vocab;
-  p.tx = a.tx;
+  mm_status st;
+  TmaRows w;
+  if ((st = align_weight(a, &w, ctx)) != MM_OK) return st;
   p.dw = static_cast<uint16_t *>(a.dweight);
   p.lddw = a.lddw;
-  mm_status st = launch_gather(a, p.r, true, ctx);
-  if (st != MM_OK) return st;
+  p.vec = (uintptr_t)a.dweight % 16 == 0 && a.lddw % 8 == 0 && a.cols % 8 == 0 && a.lddw < (1LL << 37);
+  if ((st = launch_gather(a, p.r, true, ctx)) != MM_OK) return st;
   for (p.v0 = 0; p.v0 < a.vocab; p.v0 += piece) {
+    Maps m;
     p.first = p.v0 == 0;
     p.width = std::min(piece, (a.vocab - p.v0 + 63) / 64 * 64);
-    if ((st = launch_tiles<MODE_G>(p, a.rows, p.width, ctx)) != MM_OK) return st;
-    if (a.dx && (st = launch_tiles<MODE_DX>(p, a.rows, a.cols, ctx)) != MM_OK) return st;
-    if (a.dweight && (st = launch_tiles<MODE_DW>(p, p.width, a.cols, ctx)) != MM_OK) return st;
+    if ((st = logits_maps(&m, p, f, w)) != MM_OK) return st;
+    if ((st = rows_map(&m.o, p.tx, g, p.width, rows_pad, piece, 32)) != MM_OK) return st;
+    if ((st = launch_tiles<MODE_G>(f, p, m, a.rows, ctx)) != MM_OK) return st;
+    p.bn = bn_cols;
+    p.tiles_n = tiles_cols;
+    if (a.dx) {
+      p.num_kb = p.width / 64;
+      p.splits = splits;
+      p.kb_per_split = (p.num_kb + splits - 1) / splits;
+      if ((st = rows_map(&m.a, p.tx, g, p.width, rows_pad, piece, 128)) != MM_OK) return st;
+      if ((st = rows_map(&m.b, p.tx, static_cast<const char *>(w.p) + (int64_t)p.v0 * w.ld, a.cols,
+                         std::min(p.width, a.vocab - p.v0), w.ld / 2, 64)) != MM_OK)
+        return st;
+      m.bh = m.o = m.b;  // (boxes of 64: the same for half tiles)
+      if ((st = launch_tiles<MODE_DX>(f, p, m, a.rows, ctx)) != MM_OK) return st;
+    }
+    if (a.dweight) {
+      p.splits = 1;
+      if ((st = rows_map(&m.a, p.tx, g, p.width, rows_pad, piece, 64)) != MM_OK) return st;
+      if ((st = rows_map(&m.b, p.tx, p.r.x, a.cols, rows_pad, p.r.ldx, 64)) != MM_OK) return st;
+      m.bh = m.o = m.b;
+      if (p.vec && (st = rows_map(&m.o, p.tx, a.dweight, a.cols, a.vocab, a.vocab == 1 ? p.r.ldx : a.lddw, 32)) != MM_OK)
+        return st;
+      if ((st = launch_tiles<MODE_DW, 2>(p, m, p.width, ctx)) != MM_OK) return st;
+    }
   }
   if (!a.dx) return MM_OK;
-  DxParams d{a, p.r, p.acc, p.ldacc};
-  cudaError_t e = launch_pdl(dx_kernel, dim3((unsigned)std::min(a.rows, 8 * ctx.dev->info.sms)), dim3(256), 0,
-                             ctx.stream, dim3(1), d);
+  DxParams d{a, p.r, p.acc, p.acc_cols, splits, (uintptr_t)a.dx % 16 == 0 && (a.lddx % 8 == 0 || a.rows == 1)};
+  cudaError_t e = launch_pdl(dx_kernel, dim3((unsigned)(4 * ctx.dev->info.sms)), dim3(256), 0, ctx.stream, dim3(1), d);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy_backward launch (dx)");
   count_operator_launch();
   return MM_OK;

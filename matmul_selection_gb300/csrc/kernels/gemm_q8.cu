@@ -25,6 +25,7 @@
 #include "../operators.h"
 #include "../q8_choice.h"
 #include "tcgen05.cuh"
+#include "tile_out.cuh"
 #include "values.cuh"
 
 namespace mm {
@@ -52,15 +53,6 @@ struct Q8Params {
   Waits wait;
 };
 
-__device__ __forceinline__ uint32_t pack2(int tc, float lo, float hi) {
-  if (tc == MM_BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-  }
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-
 // Whether `ok` holds in all of the 128 threads of the storing warps (barrier 1).
 __device__ __forceinline__ bool all_of_128(bool ok) {
   uint32_t all;
@@ -76,7 +68,6 @@ __device__ __forceinline__ bool all_of_128(bool ok) {
 // ---------------------------------------------------------------- pair
 constexpr int kPairStages = 6;
 constexpr uint32_t kPairStageB = 2 * 128 * kRowB;
-constexpr uint32_t kBoxB = 32 * 128;                 // an output box: 32 rows of 128 bytes
 constexpr uint32_t kPairBoxesB = 4 * 2 * kBoxB;      // two for each storing warp
 constexpr size_t kPairSmem = kPairStages * kPairStageB + kPairBoxesB + 1024 /* column scales */ + 1024 + 256;
 constexpr int kGroupRows = 8;  // row tiles walked together, so their A and B stay in L2
@@ -95,43 +86,6 @@ __device__ __forceinline__ void pair_unit(const Q8Params &p, int u, int &tm, int
   tm = g * kGroupRows + r % rows;
   n0 = (r / rows) * 256 + (half > 0 ? 128 : 0);
   w = half < 0 ? 256 : 128;
-}
-
-// A box of rows of 128 swizzled bytes to a matrix of ES-byte elements, from
-// element i on, `left` columns: a row an access of up to 128 bytes, which for
-// 2-byte elements is two a lane; where the row starts between two, its first
-// element goes alone.
-template <int ES>
-__device__ __forceinline__ void store_box(const uint8_t *box, void *out, int64_t i, int64_t ldc, int rows, int left) {
-  const int lane = threadIdx.x & 31;
-  constexpr int U = 8;  // rows read before the first of them is stored
-#pragma unroll 1
-  for (int r0 = 0; r0 < rows; r0 += U) {
-    uint32_t v[U], next[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const auto word = [&](int k) {
-        return *reinterpret_cast<const uint32_t *>(box + (r0 + u) * 128 + (((k >> 2) ^ u) << 4) + (k & 3) * 4);
-      };
-      v[u] = word(lane);
-      if (ES == 2) next[u] = word((lane + 1) & 31);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (r0 + u >= rows) break;
-      char *to = static_cast<char *>(out) + (i + (r0 + u) * ldc) * ES;
-      if constexpr (ES == 4) {
-        if (lane < left) reinterpret_cast<uint32_t *>(to)[lane] = v[u];
-      } else {
-        uint16_t *const row = reinterpret_cast<uint16_t *>(to);
-        const int odd = (int)((uintptr_t)to >> 1) & 1, j = 2 * lane + odd;
-        if (odd && lane == 0) row[0] = (uint16_t)v[u];
-        const uint32_t x = __funnelshift_r(v[u], next[u], odd * 16);
-        if (j + 1 < left) *reinterpret_cast<uint32_t *>(row + j) = x;
-        else if (j < left) row[j] = (uint16_t)x;
-      }
-    }
-  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)

@@ -276,6 +276,15 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
   else
     MM_MMA_ASM("2", "f8f6f4");
 }
+// The same of 16-bit operands (kind::f16), 16 of K.
+template <int CG>
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if constexpr (CG == 1)
+    MM_MMA_ASM("1", "f16");
+  else
+    MM_MMA_ASM("2", "f16");
+}
 #undef MM_MMA_ASM
 // The same with A in TMEM (16-bit types, two of K a column), one CTA.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -425,6 +434,12 @@ constexpr uint64_t kDescKMajor128 = ((uint64_t)(16 >> 4) << 16) | ((uint64_t)(10
 __device__ __forceinline__ uint64_t desc_at(uint32_t smem_addr) {
   return kDescKMajor128 | (uint64_t)((smem_addr >> 4) & 0x3FFFu);
 }
+// The same of an MN-major operand of 16 bits, 64 of K a stage: boxes of 64 of M or N
+// (a swizzled row) by 64 of K, 8192 bytes apart; 16 of K are 2048 bytes.
+constexpr uint64_t kDescMnMajor128 = ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+                                     ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Bits of the instruction descriptor for an MN-major A and B.
+constexpr uint32_t kMnMajorA = 1u << 15, kMnMajorB = 1u << 16;
 
 // A 2-D tiled map: `inner` elements a row, `outer` rows ld_bytes apart, boxes
 // of box_inner x box_outer.
