@@ -18,6 +18,7 @@
 #include "../operators.h"
 #include "../per_device.h"
 #include "indices.cuh"
+#include "row_copy.cuh"
 #include "tcgen05.cuh"
 #include "tile_out.cuh"
 #include "values.cuh"
@@ -67,15 +68,16 @@ __device__ __forceinline__ int valid_target(const LossArgs &a, int64_t t) {
   return v < a.vocab ? (int)v : -1;
 }
 
-// Each block has an equal share of the rows and counts the rows that count
-// before its own.
-constexpr int kGatherThreads = 256;
+// Each block has an equal share of the rows and counts the rows that count before its
+// own (and, backward, finds the largest |dloss| of all) for itself: a few KB from L2
+// instead of another kernel.  Rows move in 16-byte pieces, wherever they start.
+constexpr int kGatherThreads = 512, kGatherWarps = kGatherThreads / 32;
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ int warp_count[kGatherThreads / 32];
-  __shared__ float warp_max[kGatherThreads / 32];
-  __shared__ int at_row[kGatherThreads];  // the source row of slot first + k
+  __shared__ int warp_count[kGatherWarps];
+  __shared__ float warp_max[kGatherWarps];
+  __shared__ int at_row[kGatherThreads];  // the source row of the k-th that counts
   const LossArgs &a = p.a;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int r0 = (int)((int64_t)a.rows * blockIdx.x / gridDim.x);
@@ -83,33 +85,31 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
   int before = 0;
   float top = 0.f;  // of the finite ones
   const int look = p.backward ? a.rows : r0;
-  for (int i = t; i < look; i += kGatherThreads)
-    if (valid_target(a, i) >= 0) {
-      before += i < r0;
-      if (p.backward) {
-        const float d = a.dloss ? fabsf(a.dloss[i]) : 1.f;
-        if (d <= 3.402823466e38f) top = fmaxf(top, d);
-      }
-    }
+#pragma unroll 4
+  for (int i = t; i < look; i += kGatherThreads) {
+    const int target = valid_target(a, i);
+    const float d = p.backward && a.dloss ? fabsf(a.dloss[i]) : 1.f;
+    before += target >= 0 && i < r0;
+    if (target >= 0 && d <= 3.402823466e38f) top = fmaxf(top, d);
+  }
   before = __reduce_add_sync(0xffffffffu, before);
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) warp_count[warp] = before, warp_max[warp] = top;
   __syncthreads();
   before = 0;
-  for (int w = 0; w < kGatherThreads / 32; ++w) before += warp_count[w], top = fmaxf(top, warp_max[w]);
+  for (int w = 0; w < kGatherWarps; ++w) before += warp_count[w], top = fmaxf(top, warp_max[w]);
   if (top == 0.f) top = 1.f;
   __syncthreads();
 
   const int pieces = (int)(p.r.ldx / 8);
-  const uint16_t *x = static_cast<const uint16_t *>(a.x);
-  const bool whole = (uintptr_t)x % 16 == 0 && a.ldx % 8 == 0;
+  const uint8_t *x = static_cast<const uint8_t *>(a.x);
   for (int g0 = r0; g0 < r1; g0 += kGatherThreads) {
     const int i = g0 + t, target = i < r1 ? valid_target(a, i) : -1;
     const uint32_t mask = __ballot_sync(0xffffffffu, target >= 0);
     if (lane == 0) warp_count[warp] = __popc(mask);
     __syncthreads();
     int at = __popc(mask & ((1u << lane) - 1)), total = 0;
-    for (int w = 0; w < kGatherThreads / 32; ++w) {
+    for (int w = 0; w < kGatherWarps; ++w) {
       if (w < warp) at += warp_count[w];
       total += warp_count[w];
     }
@@ -125,24 +125,23 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
       }
     }
     __syncthreads();
-    for (int k = warp; k < total; k += kGatherThreads / 32) {
-      const uint16_t *from = x + (int64_t)at_row[k] * a.ldx;
-      uint16_t *to = p.r.x + (int64_t)(before + k) * p.r.ldx;
-      for (int c = lane; c < pieces; c += 32) {
-        uint4 v;
-        if (whole && c * 8 + 8 <= a.cols) {
-          v = reinterpret_cast<const uint4 *>(from)[c];
-        } else {
-          uint32_t w[4];
+    constexpr int U = 4;  // pieces read before the first is stored
+    const int64_t all = (int64_t)total * pieces;
+    for (int64_t j0 = t; j0 < all; j0 += kGatherThreads * U) {
+      uint4 v[U];
+      uint16_t *to[U];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = c * 8 + 2 * e;
-            w[e] = (j < a.cols ? from[j] : 0u) | (j + 1 < a.cols ? (uint32_t)from[j + 1] << 16 : 0u);
-          }
-          v = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int u = 0; u < U; ++u) {
+        const int64_t j = j0 + u * kGatherThreads;
+        if (j < all) {
+          const int k = (int)(j / pieces), c = (int)(j - (int64_t)k * pieces);
+          v[u] = row_piece<2>(x + (int64_t)at_row[k] * a.ldx * 2, (int64_t)a.cols * 2, (int64_t)c * 16);
+          to[u] = p.r.x + (int64_t)(before + k) * p.r.ldx + c * 8;
         }
-        reinterpret_cast<uint4 *>(to)[c] = v;
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j0 + u * kGatherThreads < all) *reinterpret_cast<uint4 *>(to[u]) = v[u];
     }
     before += total;
     __syncthreads();
@@ -172,7 +171,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
 // to the host: each kernel reads the count and lays out its own tiles.
 enum Mode { MODE_LSE, MODE_G, MODE_DX, MODE_DW };
 
-constexpr int kThreads = 192;  // warp 0 copies, warp 1 issues MMAs, warps 2-5 take tiles out
+constexpr int kThreads = 320;  // warp 0 copies, warp 1 issues MMAs, warps 2-9 take tiles out
 constexpr int kErrCopy = 0xa01, kErrMma = 0xa02, kErrStore = 0xa03, kErrDrain = 0xa04;
 constexpr int kGroupRows = 8;  // row tiles walked together, so that their operands stay in L2
 
@@ -233,11 +232,15 @@ struct TileParams {
   Waits wait;
 };
 
-template <int CG>
+// Stages of 64 of K: 128 rows of A, and of B 128 (its half of a pair's tile) or 256.
+// Where tiles leave through boxes in shared memory, two for each warp that takes them
+// out; one for the few rows of CG = 1, whose products wait for W.
+template <int MODE, int CG>
 struct Ring {
-  static constexpr int kStages = CG == 2 ? 6 : 4;
   static constexpr uint32_t kA = 128 * 128, kStageB = kA + (CG == 2 ? 128 : 256) * 128;
-  static constexpr uint32_t kBoxes = 4 * 2 * kBoxB;  // two for each warp that takes tiles out
+  static constexpr int kBoxesAWarp = (MODE == MODE_G || MODE == MODE_DW) && CG == 2 ? 2 : 1;
+  static constexpr int kStages = CG == 1 ? 4 : kBoxesAWarp == 2 ? 5 : 6;
+  static constexpr uint32_t kBoxes = 8 * kBoxesAWarp * kBoxB;  // (LSE: sums)
   static constexpr size_t kSmem = kStages * kStageB + kBoxes + 1024 + 256;
 };
 
@@ -247,48 +250,89 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, u
   else tma_load_2d(dst, map, bar, x, y);
 }
 
-// What a tile leaves (by one warp: 32 rows of TMEM from `tmem` on).
-// A row's sum of 2^(l log2e - r) and r over w columns.
-__device__ __forceinline__ void take_lse(const TileParams &p, uint32_t tmem, const Unit &u, int row) {
-  if (u.n0 >= p.vocab) return;  // (a half tile past the end)
-  const int target = p.r.target[row];
+// Whether `ok` holds in all of the warps that take tiles out (barrier 1).
+__device__ __forceinline__ bool all_take(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
+// What a tile leaves, by eight warps: two for each quarter of the 128 rows, a half of
+// the columns each.
+
+// LSE: the logits are fp32 sums over K that the tensor core truncates at each step of
+// 16, towards zero, so that their error grows with K and the sum itself.  A sum over
+// kChunkKb blocks at a time, added up here in registers, rounded, keeps it at that of
+// an fp32 loop (8192 x 4096 x 131072: 2.9e-6 of the loss in one chain).
+constexpr int kChunkKb = 16;
+
+// A chunk of w columns, added to a thread's sums.
+__device__ __forceinline__ void add_chunk(float (&sum)[128], uint32_t tmem, int w, bool first) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (b * 32 < w) {
+      uint32_t v[32];
+      tmem_ld_32cols(tmem + (uint32_t)(b * 32), v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[b * 32 + i] = first ? __uint_as_float(v[i]) : sum[b * 32 + i] + __uint_as_float(v[i]);
+    }
+}
+// A row's sum of 2^(l log2e - r) and r over w logits, the first of which is token n0.
+__device__ __forceinline__ float2 sum_exp(const TileParams &p, float (&l)[128], int n0, int w, int target, float *hit) {
   float r = -3e38f, s = 0.f;
-#pragma unroll 1
-  for (int c = 0; c < u.w && u.n0 + c < p.vocab; c += 32) {
-    uint32_t v[32];
-    tmem_ld_32cols(tmem + (uint32_t)c, v);
-    tmem_ld_wait();
-    const int left = p.vocab - u.n0 - c;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int left = p.vocab - n0 - b * 32, at = target - n0 - b * 32;
+    if (b * 32 >= w || left <= 0) break;
+    if (__any_sync(0xffffffffu, (unsigned)at < 32u)) {
+      float h = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) h = at == i ? l[b * 32 + i] : h;
+      if ((unsigned)at < 32u) *hit = h;
+    }
     if (left < 32) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (i >= left) v[i] = 0xff800000u;  // -infinity
+        if (i >= left) l[b * 32 + i] = -INFINITY;
     }
     float top[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      top[k] = __uint_as_float(v[k]);
+      top[k] = l[b * 32 + k];
 #pragma unroll
-      for (int i = k + 4; i < 32; i += 4) top[k] = fmaxf(top[k], __uint_as_float(v[i]));
+      for (int i = k + 4; i < 32; i += 4) top[k] = fmaxf(top[k], l[b * 32 + i]);
     }
     const float next = fmaxf(r, ceilf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e));
     float sum[4] = {s * exp2_fast(r - next), 0.f, 0.f, 0.f};
     r = next;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum[i & 3] += exp2_fast(fmaf(__uint_as_float(v[i]), kLog2e, -r));
+    for (int i = 0; i < 32; ++i) sum[i & 3] += exp2_fast(fmaf(l[b * 32 + i], kLog2e, -r));
     s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    const int at = target - u.n0 - c;
-    if (__any_sync(0xffffffffu, (unsigned)at < 32u)) {
-      float h = 0.f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) h = at == i ? __uint_as_float(v[i]) : h;
-      if ((unsigned)at < 32u) p.hit[row] = h;
-    }
   }
-  p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row] = make_float2(r, s);
+  return make_float2(r, s);
+}
+// Two such sums as one.
+__device__ __forceinline__ float2 join_sums(float2 a, float2 b) {
+  const float r = fmaxf(a.x, b.x);
+  return make_float2(r, a.y * exp2_fast(a.x - r) + b.y * exp2_fast(b.x - r));
 }
 
 // 64 columns of 32 rows in 16 bits to a box.
+// A warp's next box of N, free: its store has read it.
+template <int N>
+__device__ __forceinline__ uint8_t *next_box(uint8_t *boxes, int &side) {
+  if ((threadIdx.x & 31) == 0) tma_store_wait_read<N - 1>();
+  __syncwarp();
+  uint8_t *box = boxes + side * kBoxB;
+  side = side + 1 == N ? 0 : side + 1;
+  return box;
+}
 template <typename F>
 __device__ __forceinline__ void fill_box(uint8_t *box, int tx, F &&value) {
   const int lane = threadIdx.x & 31;
@@ -299,14 +343,15 @@ __device__ __forceinline__ void fill_box(uint8_t *box, int tx, F &&value) {
                    pack2(tx, value(8 * j + 4), value(8 * j + 5)), pack2(tx, value(8 * j + 6), value(8 * j + 7)));
 }
 
+template <int BOXES>
 __device__ __forceinline__ void take_g(const TileParams &p, const CUtensorMap *map, uint32_t tmem, const Unit &u,
-                                       int row0, uint8_t *boxes, int &side) {
+                                       int row0, int c0, int c1, uint8_t *boxes, int &side) {
   const int lane = threadIdx.x & 31, row = row0 + lane;
   const int target = p.r.target[row];
   const float ratio = p.r.ratio[row], lse2 = p.r.lse2[row];
   const bool live = ratio != 0.f;  // (a weight of 0 takes its row out, whatever its logits)
 #pragma unroll 1
-  for (int c = 0; c < u.w && u.n0 + c < p.width; c += 64) {
+  for (int c = c0; c < c1 && u.n0 + c < p.width; c += 64) {
     uint32_t v[2][32];
     tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
     tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
@@ -329,30 +374,26 @@ __device__ __forceinline__ void take_g(const TileParams &p, const CUtensorMap *m
 #pragma unroll
       for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] = live && i < left ? v[i >> 5][i & 31] : 0u;
     }
-    if (lane == 0) tma_store_wait_read<1>();  // this box's previous store has read it
-    __syncwarp();
-    uint8_t *box = boxes + side * kBoxB;
+    uint8_t *box = next_box<BOXES>(boxes, side);
     fill_box(box, p.tx, [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); });
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) tma_store_2d(map, smem_u32(box), u.n0 + c, row0);
-    side ^= 1;
   }
 }
 
+template <int BOXES>
 __device__ __forceinline__ void take_dw(const TileParams &p, const CUtensorMap *map, uint32_t tmem, const Unit &u,
-                                        int row0, uint8_t *boxes, int &side, float gain) {
+                                        int row0, int c0, int c1, uint8_t *boxes, int &side, float gain) {
   const int lane = threadIdx.x & 31, v0 = p.v0 + row0;
   if (v0 >= p.vocab) return;
 #pragma unroll 1
-  for (int c = 0; c < u.w && u.n0 + c < p.cols; c += 64) {
+  for (int c = c0; c < c1 && u.n0 + c < p.cols; c += 64) {
     uint32_t v[2][32];
     tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
     tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
     tmem_ld_wait();
-    if (lane == 0) tma_store_wait_read<1>();
-    __syncwarp();
-    uint8_t *box = boxes + side * kBoxB;
+    uint8_t *box = next_box<BOXES>(boxes, side);
     fill_box(box, p.tx, [&](int i) { return __uint_as_float(v[i >> 5][i & 31]) * gain; });
     if (p.vec) {
       fence_proxy_async_smem();
@@ -364,16 +405,16 @@ __device__ __forceinline__ void take_dw(const TileParams &p, const CUtensorMap *
                    min(64, p.cols - u.n0 - c));
       __syncwarp();
     }
-    side ^= 1;
   }
 }
 
 // Added to the pieces before; the layout has a lane's 16 bytes beside the next one's.
-__device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, const Unit &u, int row0, bool empty) {
+__device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, const Unit &u, int row0, int c0, int c1,
+                                        bool empty) {
   const int lane = threadIdx.x & 31;
   if (empty && !p.first) return;
 #pragma unroll 1
-  for (int c = 0; c < u.w; c += 32) {
+  for (int c = c0; c < c1; c += 32) {
     const int cb = (u.n0 + c) >> 5;
     if (cb >= p.acc_cols) break;
     float4 *to = reinterpret_cast<float4 *>(
@@ -400,9 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmO,
                 const TileParams p) {
-  using R = Ring<CG>;
+  using R = Ring<MODE, CG>;
   constexpr int S = R::kStages;
   constexpr bool kMnA = MODE == MODE_DW, kMnB = MODE == MODE_DX || MODE == MODE_DW;
+  constexpr bool kChunk = MODE == MODE_LSE;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -425,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
-      mbar_init(tempty0 + 8 * a, 4 * CG);
+      mbar_init(tempty0 + 8 * a, 8 * CG);
     }
     mbar_init(drain, 1);
     mbar_init(stall, 1);
@@ -437,6 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmB);
     prefetch_tmap(&tmBh);
     if (MODE == MODE_G || (MODE == MODE_DW && p.vec)) prefetch_tmap(&tmO);
+  }
+  if (CG == 1 && !kMnB && warp == 0 && lane == 0) {
+    // few rows: the first blocks of W into L2 while the rows are gathered (one row tile,
+    // so the first unit does not depend on their count)
+    const Tiles tiles = tiles_of(1, 128, p.tiles_n, 1, p.bn, p.places);
+    if (cid < tiles.total) {
+      const Unit u = unit_at(tiles, p.bn, cid);
+      for (int kb = 0; kb < min(p.num_kb, 8); ++kb) tma_prefetch_2d(u.w == p.bn ? &tmB : &tmBh, kb * 64, u.n0);
+    }
   }
   if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), 512);
   fence_before();
@@ -496,16 +547,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = !p.wait.stall || warp_wait(stall, 0, abort_flag, p.wait, kErrMma);  // (test hook)
+      const auto finish = [&] {  // the accumulator is handed on when the MMAs so far are done
+        if (CG == 2) mma_commit_pair(tfull0 + 8 * acc);
+        else mma_commit<1>(tfull0 + 8 * acc);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      };
       for (int i = cid; i < tiles.total && ok; i += ncl) {
         const Unit u = unit_at(tiles, p.bn, i);
         int kb0;
         const int nk = k_of(u, kb0);
         const uint32_t idesc = instr_desc(p.tx == MM_BF16, 128 * CG, (uint32_t)u.w) | (kMnA ? kMnMajorA : 0u) |
                                (kMnB ? kMnMajorB : 0u);
-        if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.wait, kErrMma)) break;
-        fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * 256);
-        for (int k = 0; k < nk; ++k) {
+        uint32_t d = 0;
+        for (int k = 0; k < max(nk, 1); ++k) {
+          // an accumulator for the tile, or (LSE) for each chunk of K
+          const bool start = k == 0 || (kChunk && k % kChunkKb == 0);
+          if (start) {
+            if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.wait, kErrMma)) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            d = tmem_base + (uint32_t)(acc * 256);
+          }
+          if (nk == 0) {
+            finish();
+            break;
+          }
           if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.wait, kErrMma)) {
             ok = false;
             break;
@@ -516,20 +587,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t bd = kDescB | (uint64_t)(((sa + R::kA) >> 4) & 0x3FFFu);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f16<CG>(d, ad + (kMnA ? 128 : 2) * kk, bd + (kMnB ? 128 : 2) * kk, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+            mma_f16<CG>(d, ad + (kMnA ? 128 : 2) * kk, bd + (kMnB ? 128 : 2) * kk, idesc, (!start || kk > 0) ? 1u : 0u);
           if (CG == 2) mma_commit_pair(empty0 + 8 * stage);
           else mma_commit<1>(empty0 + 8 * stage);
           if (++stage == S) {
             stage = 0;
             phase ^= 1;
           }
-        }
-        if (!ok) break;
-        if (CG == 2) mma_commit_pair(tfull0 + 8 * acc);
-        else mma_commit<1>(tfull0 + 8 * acc);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1;
+          if (k + 1 == nk || (kChunk && (k + 1) % kChunkKb == 0)) finish();
         }
       }
       mma_commit<CG>(drain);
@@ -537,27 +602,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;  // the TMEM lanes this warp may read
-    uint8_t *mine = boxes + (warp - 2) * 2 * kBoxB;
+    const int q = warp & 3, half = (warp - 2) >> 2;  // q: the TMEM lanes this warp may read
+    uint8_t *mine = boxes + (warp - 2) * R::kBoxesAWarp * kBoxB;
+    int side = 0;
     const float gain = MODE == MODE_DW ? *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f) : 0.f;
-    int acc = 0, side = 0;
+    int acc = 0;
     uint32_t acc_phase = 0;
-    for (int i = cid; i < tiles.total; i += ncl) {
-      const Unit u = unit_at(tiles, p.bn, i);
-      if (!warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)) break;
-      fence_after();
-      const int row0 = u.tm * 128 * CG + pos * 128 + q * 32;
-      const uint32_t tmem = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
-      int kb0;
-      if constexpr (MODE == MODE_LSE) {
-        if (row0 < rows) take_lse(p, tmem, u, row0 + lane);
-      } else if constexpr (MODE == MODE_G) {
-        take_g(p, &tmO, tmem, u, row0, mine, side);
-      } else if constexpr (MODE == MODE_DX) {
-        if (row0 < rows) take_dx(p, tmem, u, row0, k_of(u, kb0) == 0);
-      } else {
-        take_dw(p, &tmO, tmem, u, row0, mine, side, gain);
-      }
+    const auto release = [&] {  // the accumulator has been read
       fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -567,6 +618,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
+      }
+    };
+    bool ok = true;
+    int turn = 0;
+    for (int i = cid; i < tiles.total && ok; i += ncl, turn ^= 1) {
+      const Unit u = unit_at(tiles, p.bn, i);
+      const int row0 = u.tm * 128 * CG + pos * 128 + q * 32, c0 = half * (u.w / 2), c1 = c0 + u.w / 2;
+      const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
+      if constexpr (MODE == MODE_LSE) {
+        const bool live = row0 < rows && u.n0 < p.vocab;  // (else a half tile past the end)
+        float l[128];
+        for (int k = 0; k < num_kb; k += kChunkKb) {
+          // the eight warps go on or give up together
+          if (!(ok = all_take(warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)))) break;
+          fence_after();
+          if (live) add_chunk(l, lanes + (uint32_t)(acc * 256 + c0), u.w / 2, k == 0);
+          release();
+        }
+        if (!ok) break;
+        // the upper half's sums to the lower half's warps; a buffer for each of two turns
+        float2 *upper = reinterpret_cast<float2 *>(boxes) + turn * 128 + q * 32 + lane;
+        float2 sum = make_float2(-3e38f, 0.f);
+        if (live) {
+          const int row = row0 + lane;
+          sum = sum_exp(p, l, u.n0 + c0, u.w / 2, p.r.target[row], p.hit + row);
+          if (half) *upper = sum;
+        }
+        all_take(true);
+        if (live && !half) p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row0 + lane] = join_sums(sum, *upper);
+      } else {
+        if (!warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)) break;
+        fence_after();
+        const uint32_t tmem = lanes + (uint32_t)(acc * 256);
+        int kb0;
+        if constexpr (MODE == MODE_G) {
+          take_g<R::kBoxesAWarp>(p, &tmO, tmem, u, row0, c0, c1, mine, side);
+        } else if constexpr (MODE == MODE_DX) {
+          if (row0 < rows) take_dx(p, tmem, u, row0, c0, c1, k_of(u, kb0) == 0);
+        } else {
+          take_dw<R::kBoxesAWarp>(p, &tmO, tmem, u, row0, c0, c1, mine, side, gain);
+        }
+        release();
       }
     }
     if (lane == 0) tma_store_wait_all();
@@ -594,39 +687,53 @@ struct LossParams {
   int tile_m, bn, tiles_n, places;  // of the product
 };
 
-// 32 rows a block, 8 threads a row over the tiles of the vocabulary; the last
-// steps in fp64, so that a loss is no less exact than its sums.
-__global__ void __launch_bounds__(256) loss_kernel(const LossParams p) {
+// 32 rows a block, 32 threads a row over the tiles of the vocabulary; the last steps
+// in fp64, so that a loss is no less exact than its sums.
+constexpr int kLossThreads = 1024;
+__global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float2 sh[8][32];
+  constexpr int Y = kLossThreads / 32, U = 4;
+  __shared__ float2 sh[Y][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * 32 + x;
   const int slot = row < p.a.rows ? p.r.slot[row] : -1;
-  float r = -INFINITY, s = 0.f;
   const Tiles tiles = tiles_of(max(1, *p.r.count), p.tile_m, p.tiles_n, 1, p.bn, p.places);
-  if (slot >= 0)
-    for (int i = y; i * 128 < p.a.vocab; i += 8) {
-      // a whole tile of 256 has left its sums with its first half
-      if ((i & 1) && p.bn == 256 && !halved(tiles, slot / p.tile_m, i >> 1)) continue;
-      const float2 v = p.part[(int64_t)i * p.r.rows_pad + slot];
-      const float top = fmaxf(r, v.x);
-      s = s * exp2_fast(r - top) + v.y * exp2_fast(v.x - top);
-      r = top;
+  const float2 none = make_float2(-3e38f, 0.f);
+  float2 sum = none;
+  if (slot >= 0) {
+    // a slot for each 128 of the vocabulary; a whole tile of 256 has left its sums
+    // in the first of its two
+    const int per = p.bn / 128;
+    for (int i0 = y; i0 < p.tiles_n; i0 += Y * U) {
+      float2 v[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * Y;
+        const float2 *part = p.part + (int64_t)i * per * p.r.rows_pad + slot;
+        v[u][0] = i < p.tiles_n ? part[0] : none;
+        v[u][1] = i < p.tiles_n && per == 2 && i * 256 + 128 < p.a.vocab && halved(tiles, slot / p.tile_m, i)
+                      ? part[p.r.rows_pad]
+                      : none;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) sum = join_sums(join_sums(sum, v[u][0]), v[u][1]);
     }
-  sh[y][x] = make_float2(r, s);
-  __syncthreads();
-  if (y > 0 || row >= p.a.rows) return;
-  for (int k = 1; k < 8; ++k) {
-    const float2 v = sh[k][x];
-    const float top = fmaxf(r, v.x);
-    if (v.x == -INFINITY) continue;  // (no tile)
-    s = s * exp2_fast(r - top) + v.y * exp2_fast(v.x - top);
-    r = top;
   }
-  const double lse = slot < 0 ? 0.0 : (double)r * 0.693147180559945309 + log((double)s);
-  p.a.loss[row] = slot < 0 ? 0.f : (float)(lse - (double)p.hit[slot]);
-  if (p.a.lse) p.a.lse[row] = (float)lse;
+  sh[y][x] = sum;
+  __syncthreads();
+  // the 32 sums of a row by a warp
+  const float2 mine = sh[x][y];
+  float r = mine.x;
+  for (int o = 16; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+  float s = mine.y * exp2_fast(mine.x - r);
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int64_t to = (int64_t)blockIdx.x * 32 + y;
+  if (x != 0 || to >= p.a.rows) return;
+  const int at = p.r.slot[to];
+  const double lse = at < 0 ? 0.0 : (double)r * 0.693147180559945309 + log((double)s);
+  p.a.loss[to] = at < 0 ? 0.f : (float)(lse - (double)p.hit[at]);
+  if (p.a.lse) p.a.lse[to] = (float)lse;
 }
 
 struct DxParams {
@@ -636,45 +743,57 @@ struct DxParams {
   int acc_cols, splits;
   int vec;  // dx's rows start on 16 bytes
 };
-// A warp 32 rows by 32 columns, a row a lane: the splits added in order, scaled and
-// rounded.  Then the rows that do not count.
+// A warp 32 rows by 4 Q columns, a row a lane: the splits added in order, scaled and
+// rounded.  Then the rows that do not count.  Q: 8 (64 bytes of a row), or 2 where
+// there are splits, and few rows: more warps (16 rows of 4096 in 9 splits: 12.7 us
+// with 8).
+template <int Q>
 __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   pdl_launch_dependents();
   pdl_wait();
+  constexpr int U = Q == 8 ? 1 : 4;  // splits read at once
   const int lane = threadIdx.x & 31, count = *p.r.count;
   const float gain = *p.r.gain * (p.a.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
   const int64_t warps = (int64_t)gridDim.x * 8, warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   uint16_t *dx = static_cast<uint16_t *>(p.a.dx);
   const int64_t split_at = (int64_t)p.r.rows_pad * p.acc_cols * 8;  // float4 a split
-  for (int64_t b = warp; b < (int64_t)((count + 31) / 32) * p.acc_cols; b += warps) {
-    const int rb = (int)(b / p.acc_cols), cb = (int)(b - (int64_t)rb * p.acc_cols);
-    const float4 *from = reinterpret_cast<const float4 *>(p.acc) + b * 256 + lane;
-    float4 v[8];
+  const int across = p.acc_cols * (8 / Q);
+  for (int64_t b = warp; b < (int64_t)((count + 31) / 32) * across; b += warps) {
+    const int rb = (int)(b / across), col = (int)(b - (int64_t)rb * across) * 4 * Q;
+    const float4 *from = reinterpret_cast<const float4 *>(p.acc) + b * 32 * Q + lane;
+    float4 v[Q];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = from[k * 32];
-    for (int s = 1; s < p.splits; ++s)
+    for (int k = 0; k < Q; ++k) v[k] = from[k * 32];
+    for (int s = 1; s < p.splits; s += U) {
+      float4 w[U][Q];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 w = from[s * split_at + k * 32];
-        v[k].x += w.x, v[k].y += w.y, v[k].z += w.z, v[k].w += w.w;
-      }
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < Q; ++k)
+          w[u][k] = s + u < p.splits ? from[(s + u) * split_at + k * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < Q; ++k)
+          v[k].x += w[u][k].x, v[k].y += w[u][k].y, v[k].z += w[u][k].z, v[k].w += w[u][k].w;
+    }
     const int i = rb * 32 + lane;
     if (i >= count) continue;
-    uint32_t w[16];
+    uint32_t w[2 * Q];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < Q; ++k) {
       w[2 * k] = pack2(p.a.tx, v[k].x * gain, v[k].y * gain);
       w[2 * k + 1] = pack2(p.a.tx, v[k].z * gain, v[k].w * gain);
     }
-    uint16_t *to = dx + (int64_t)p.r.row[i] * p.a.lddx + cb * 32;
-    const int left = p.a.cols - cb * 32;
-    if (p.vec && left >= 32) {
+    uint16_t *to = dx + (int64_t)p.r.row[i] * p.a.lddx + col;
+    const int left = p.a.cols - col;
+    if (p.vec && left >= 4 * Q) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < Q / 2; ++k)
         reinterpret_cast<uint4 *>(to)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
+      for (int e = 0; e < 4 * Q; ++e)
         if (e < left) to[e] = (uint16_t)(w[e >> 1] >> (e & 1) * 16);
     }
   }
@@ -738,7 +857,7 @@ cudaLaunchConfig_t tile_config(int grid, cudaStream_t s, cudaLaunchAttribute *at
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)grid);
   lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = Ring<CG>::kSmem;
+  lc.dynamicSmemBytes = Ring<MODE, CG>::kSmem;
   lc.stream = s;
   lc.attrs = at;
   lc.numAttrs = 1;
@@ -750,7 +869,7 @@ mm_status tile_places(LaunchCtx &ctx, int *places) {
   static PerDevice<int> fits;
   const cudaError_t err = fits.get(ctx.dev->info.ordinal, places, [](int *n) -> cudaError_t {
     cudaError_t e = cudaFuncSetAttribute(tile_kernel<MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Ring<CG>::kSmem);
+                                         (int)Ring<MODE, CG>::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t lc = tile_config<MODE, CG>(CG, nullptr, &at);
@@ -780,7 +899,7 @@ mm_status launch_tiles(TileParams &p, const Maps &m, int64_t M, LaunchCtx &ctx) 
   const int64_t tiles = (M + 128 * CG - 1) / (128 * CG) * p.tiles_n * p.splits;
   if (tiles >= 1 << 30) return set_error(MM_ERR_UNSUPPORTED, "too many tiles");
   const int grid = CG * (int)std::min<int64_t>(p.bn == 256 ? 2 * tiles : tiles, p.places);
-  cudaError_t e = launch_pdl(tile_kernel<MODE, CG>, dim3((unsigned)grid), dim3(kThreads), Ring<CG>::kSmem, ctx.stream,
+  cudaError_t e = launch_pdl(tile_kernel<MODE, CG>, dim3((unsigned)grid), dim3(kThreads), Ring<MODE, CG>::kSmem, ctx.stream,
                              dim3(CG), m.a, m.b, m.bh, m.o, p);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch");
   count_operator_launch();
@@ -870,7 +989,7 @@ mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
   m.o = m.a;  // (none)
   if ((st = launch_tiles<MODE_LSE>(f, p, m, a.rows, ctx)) != MM_OK) return st;
   LossParams l{a, p.r, p.part, p.hit, f.tile_m(), p.bn, p.tiles_n, p.places};
-  cudaError_t e = launch_pdl(loss_kernel, dim3((unsigned)((a.rows + 31) / 32)), dim3(256), 0, ctx.stream, dim3(1), l);
+  cudaError_t e = launch_pdl(loss_kernel, dim3((unsigned)((a.rows + 31) / 32)), dim3(kLossThreads), 0, ctx.stream, dim3(1), l);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch (loss)");
   count_operator_launch();
   return MM_OK;
@@ -947,7 +1066,8 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   }
   if (!a.dx) return MM_OK;
   DxParams d{a, p.r, p.acc, p.acc_cols, splits, (uintptr_t)a.dx % 16 == 0 && (a.lddx % 8 == 0 || a.rows == 1)};
-  cudaError_t e = launch_pdl(dx_kernel, dim3((unsigned)(4 * ctx.dev->info.sms)), dim3(256), 0, ctx.stream, dim3(1), d);
+  cudaError_t e = launch_pdl(splits > 1 ? dx_kernel<2> : dx_kernel<8>, dim3((unsigned)(4 * ctx.dev->info.sms)), dim3(256),
+                             0, ctx.stream, dim3(1), d);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy_backward launch (dx)");
   count_operator_launch();
   return MM_OK;

@@ -14,8 +14,11 @@
 #include <algorithm>
 
 #include "../operators.h"
+#include "../per_device.h"
 #include "indices.cuh"
 #include "pieces.cuh"
+#include "row_copy.cuh"
+#include "tcgen05.cuh"
 
 namespace mm {
 
@@ -63,70 +66,160 @@ cudaError_t embed_launch(const EmbedArgs &a, LaunchCtx &ctx) {
                : launch_pdl(embed_kernel<TW, TO, true>, grid, dim3(256), 0, ctx.stream, dim3(1), a, log_threads);
 }
 
-// ---------------------------------------------------------------- sort
-// Least significant digit first, 8 bits a pass, by one block: tiles of a key a
-// thread; a key's rank among the equal digits of its tile is its warp's, by
-// matching, behind those of the warps before.
-constexpr int kSortThreads = 1024, kBins = 256;
+// ---------------------------------------------------------------- sort, and the rows of the others
+// Least significant digit first, 9 bits a pass (a vocabulary below 2^18 takes two), by
+// one cluster of eight CTAs.  Each warp has a run of consecutive places: it counts its
+// digits, the counts of all become places, and it goes over its run again; equal
+// digits keep their order because a warp takes 32 at a time, ranked by matching.
+// The places lie in global memory (L2) between passes, so any number of them sorts.
+//
+// dW's rows of zeros, or the base's, are written meanwhile by the other clusters of
+// the same launch: more time than the sort takes, where a whole matrix is written.
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCtas = 8;
+constexpr int kDigit = 9, kBins = 1 << kDigit;
+constexpr size_t kSortSmem = (kSortWarps * kBins + kBins + 32) * sizeof(uint32_t);
 
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const void *tokens, int ti, int64_t vocab, int rows,
-                                                            uint2 *to, uint2 *other, int passes) {
+struct SortParams {
+  const void *tokens;
+  int ti;
+  int64_t vocab;
+  int rows, passes;
+  uint2 *to, *other;   // (token, place)
+  uint32_t *spanning;  // set to 0: how many tokens the sums will have left in parts
+  // the rows
+  const uint8_t *base;  // null: zeros
+  uint8_t *dweight;
+  int64_t bytes, ldb, ldw, fill_rows;  // of a row and between rows, in bytes
+  int log_threads;      // threads a row
+};
+
+__device__ __forceinline__ uint32_t cluster_u32(uint32_t addr, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(tc::map_to_rank(addr, (uint32_t)rank)) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem) {
+  uint32_t(*off)[kBins] = reinterpret_cast<uint32_t(*)[kBins]>(smem);
+  uint32_t *count = smem + kSortWarps * kBins, *warp_sum = count + kBins;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rank = (int)tc::cluster_ctarank();
+  const int lo = (int)((int64_t)p.rows * rank / kSortCtas), n = (int)((int64_t)p.rows * (rank + 1) / kSortCtas) - lo;
+  const int w0 = lo + (int)((int64_t)n * warp / kSortWarps), w1 = lo + (int)((int64_t)n * (warp + 1) / kSortWarps);
+  const uint32_t below = (1u << lane) - 1;
+  uint2 *src = nullptr, *dst = p.passes & 1 ? p.to : p.other;  // the last pass ends in `to`
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * kDigit;
+    const auto pair_at = [&](int i) {  // (written by other SMs: past L1)
+      return pass ? __ldcg(src + i) : make_uint2((uint32_t)load_token(p.tokens, p.ti, i, p.vocab), (uint32_t)i);
+    };
+    for (int b = lane; b < kBins; b += 32) off[warp][b] = 0;
+    __syncwarp();
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+      const uint32_t d = i < w1 ? (pair_at(i).x >> shift) & (kBins - 1) : kBins;
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      if (d < kBins && !(same & below)) off[warp][d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    if (t < kBins) {
+      uint32_t sum = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = off[w][t];
+        off[w][t] = sum;
+        sum += c;
+      }
+      count[t] = sum;
+    }
+    tc::cluster_sync_all();
+    if (t < kBins) {
+      const uint32_t addr = tc::smem_u32(count + t);
+      uint32_t c[kSortCtas], before = 0, total = 0;
+#pragma unroll
+      for (int r = 0; r < kSortCtas; ++r) c[r] = cluster_u32(addr, r);
+#pragma unroll
+      for (int r = 0; r < kSortCtas; ++r) before += r < rank ? c[r] : 0, total += c[r];
+      uint32_t sum = total;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+      }
+      if (lane == 31) warp_sum[warp] = sum;
+      asm volatile("bar.sync 1, 512;" ::: "memory");
+      uint32_t at = before + sum - total;
+      for (int w = 0; w < warp; ++w) at += warp_sum[w];
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) off[w][t] += at;
+    }
+    __syncthreads();
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+      const uint2 v = i < w1 ? pair_at(i) : make_uint2(0, 0);
+      const uint32_t d = i < w1 ? (v.x >> shift) & (kBins - 1) : kBins;
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      if (d < kBins) dst[off[warp][d] + __popc(same & below)] = v;
+      __syncwarp();
+      if (d < kBins && !(same & below)) off[warp][d] += __popc(same);
+      __syncwarp();
+    }
+    tc::cluster_sync_all();  // (releases and acquires the places, too)
+    src = dst;
+    dst = dst == p.to ? p.other : p.to;
+  }
+}
+static_assert(kBins == 512, "the barrier of the threads that have a digit");
+
+// This thread's pieces of the rows, `threads` threads to a row: 16 bytes as dW has them.
+template <bool BASE>
+__device__ __forceinline__ void fill_rows(const SortParams &p, int64_t thread, int64_t threads) {
+  constexpr int U = 4;  // pieces read before the first is stored
+  const int64_t row_threads = p.fill_rows == 1 ? threads : 1ll << p.log_threads;
+  for (int64_t v = thread / row_threads; v < p.fill_rows; v += threads / row_threads) {
+    uint8_t *to = p.dweight + v * p.ldw;
+    const uint8_t *from = BASE ? p.base + v * p.ldb : nullptr;
+    const int64_t first = -(int64_t)(reinterpret_cast<uintptr_t>(to) & 15);
+    for (int64_t b0 = first + (thread % row_threads) * 16; b0 < p.bytes; b0 += row_threads * 16 * U) {
+      uint4 x[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int64_t b = b0 + k * row_threads * 16;
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (BASE && b >= 0 && b + 16 <= p.bytes) x[k] = row_piece<2>(from, p.bytes, b);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int64_t b = b0 + k * row_threads * 16;
+        if (b >= 0 && b + 16 <= p.bytes) {
+          *reinterpret_cast<uint4 *>(to + b) = x[k];
+        } else {  // a row's ends
+          for (int64_t e = max(b, (int64_t)0); e < min(b + 16, p.bytes); e += 2)
+            *reinterpret_cast<uint16_t *>(to + e) = BASE ? *reinterpret_cast<const uint16_t *>(from + e) : (uint16_t)0;
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ uint32_t base[kBins];
-  __shared__ uint16_t count[kSortThreads / 32][kBins];
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  uint2 *src = nullptr, *dst = passes & 1 ? to : other;  // the last pass ends in `to`
-  for (int pass = 0; pass < passes; ++pass) {
-    const auto pair_at = [&](int i) {
-      return pass ? src[i] : make_uint2((uint32_t)load_token(tokens, ti, i, vocab), (uint32_t)i);
-    };
-    const int shift = pass * 8;
-    if (t < kBins) base[t] = 0;
-    __syncthreads();
-    for (int i = t; i < rows; i += kSortThreads) atomicAdd(&base[(pair_at(i).x >> shift) & 255], 1u);
-    __syncthreads();
-    if (warp == 0) {
-      uint32_t before = 0;
-      for (int b = lane; b < kBins; b += 32) {
-        const uint32_t n = base[b];
-        uint32_t sum = n;
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += u;
-        }
-        base[b] = before + sum - n;
-        before += __shfl_sync(0xffffffffu, sum, 31);
-      }
-    }
-    for (int i0 = 0; i0 < rows; i0 += kSortThreads) {
-      for (int b = lane; b < kBins; b += 32) count[warp][b] = 0;
-      __syncthreads();
-      const bool have = i0 + t < rows;
-      const uint2 p = have ? pair_at(i0 + t) : make_uint2(0, 0);
-      const uint32_t d = have ? (p.x >> shift) & 255 : kBins;
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      const int rank = __popc(same & ((1u << lane) - 1));
-      if (have && rank == 0) count[warp][d] = (uint16_t)__popc(same);
-      __syncthreads();
-      if (t < kBins) {
-        uint32_t at = 0;
-        for (int w = 0; w < kSortThreads / 32; ++w) {
-          const uint32_t n = count[w][t];
-          count[w][t] = (uint16_t)at;
-          at += n;
-        }
-      }
-      __syncthreads();
-      if (have) dst[base[d] + count[warp][d] + rank] = p;
-      __syncthreads();
-      if (have) atomicAdd(&base[d], 1u);
-      __syncthreads();
-    }
-    src = dst;
-    dst = dst == to ? other : to;
-    __syncthreads();
+  extern __shared__ uint32_t sort_smem[];
+  if (blockIdx.x < kSortCtas) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.spanning = 0;
+    sort_places(p, sort_smem);
+    return;
   }
+  const int64_t thread = (int64_t)(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x;
+  const int64_t threads = (int64_t)(gridDim.x - kSortCtas) * kSortThreads;
+  if (p.base) fill_rows<true>(p, thread, threads);
+  else fill_rows<false>(p, thread, threads);
+}
+// The rows alone, where there are no places.
+__global__ void __launch_bounds__(kSortThreads) embed_fill_kernel(const SortParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t thread = (int64_t)blockIdx.x * kSortThreads + threadIdx.x, threads = (int64_t)gridDim.x * kSortThreads;
+  if (p.base) fill_rows<true>(p, thread, threads);
+  else fill_rows<false>(p, thread, threads);
 }
 
 // ---------------------------------------------------------------- sums
@@ -134,12 +227,15 @@ struct SumParams {
   EmbedBwdArgs a;
   const uint2 *sorted;  // (token, place)
   float *parts;         // [chunk][2][cols]: a token from the chunk before; one that goes on
+  uint32_t *spanning;   // [0] how many tokens go past the end of the chunk where they begin,
+                        // [1 ...] those chunks, in any order
   int chunk, chunks;
   int log_threads;
 };
+constexpr int kMinLogThreads = 3, kMaxChunk = 32;
 
-template <int TW, int TO, int E>
-__device__ __forceinline__ void write_sum(const EmbedBwdArgs &a, int64_t token, int j, float (&sum)[E]) {
+template <int TW, int E>
+__device__ __forceinline__ void write_sum(const EmbedBwdArgs &a, int64_t token, int j, const float (&sum)[E]) {
   float b[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) b[e] = 0.f;
@@ -149,70 +245,111 @@ __device__ __forceinline__ void write_sum(const EmbedBwdArgs &a, int64_t token, 
   store_piece<TW>(a.dweight, token * a.lddw + j, b);
 }
 
+// A chunk of places to a power of two of threads, a piece of the columns each.
 template <int TW, int TO, int E>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p) {
+  constexpr int U = TO == MM_F32 ? 4 : 8;  // rows read before the first is added
+  __shared__ uint2 places[(256 >> kMinLogThreads) * (kMaxChunk + 2)];
   pdl_launch_dependents();
   pdl_wait();
   const EmbedBwdArgs &a = p.a;
-  const int threads = 1 << p.log_threads, t = threadIdx.x & (threads - 1);
-  const int chunk = (int)blockIdx.x * (256 >> p.log_threads) + (threadIdx.x >> p.log_threads);
+  const int threads = 1 << p.log_threads, t = threadIdx.x & (threads - 1), group = threadIdx.x >> p.log_threads;
+  const int chunk = (int)blockIdx.x * (256 >> p.log_threads) + group;
   const int j = ((int)blockIdx.y * threads + t) * E;
-  if (chunk >= p.chunks || j >= a.cols) return;
-  const int rows = (int)a.rows, i0 = chunk * p.chunk, i1 = min(rows, i0 + p.chunk);
+  const int rows = (int)a.rows, i0 = min(rows, chunk * p.chunk), n = min(rows - i0, p.chunk);
   const uint32_t none = (uint32_t)a.vocab;
+  // the places of the chunk, and its neighbours' tokens (or none)
+  uint2 *mine = places + group * (kMaxChunk + 2) + 1;
+  for (int i = t - 1; i <= n; i += threads)
+    mine[i] = i0 + i >= 0 && i0 + i < rows ? p.sorted[i0 + i] : make_uint2(none, 0);
+  __syncthreads();
+  if (n <= 0 || j >= a.cols) return;
+  uint32_t token = mine[0].x;
+  bool from_before = mine[-1].x == token;
   float sum[E];
-  uint32_t token = p.sorted[i0].x;
-  bool from_before = i0 > 0 && p.sorted[i0 - 1].x == token;
-  for (int i = i0; i < i1;) {
-    if (token == none) return;
-    int n = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] = 0.f;
-    uint32_t next = token;
-    for (; i < i1; ++i, ++n) {
-      const uint2 s = p.sorted[i];
-      next = s.x;
-      if (next != token) break;
-      float v[E];
-      load_piece<TO>(a.dout, (int64_t)s.y * a.lddo + j, v);
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum[e] += v[e];
-    }
-    const bool goes_on = i == i1 && i1 < rows && p.sorted[i1].x == token;
+  for (int e = 0; e < E; ++e) sum[e] = 0.f;
+  const auto leave = [&](bool goes_on) {
     if (from_before || goes_on) {
-      float *part = p.parts + ((int64_t)chunk * 2 + (from_before ? 0 : 1)) * a.cols + j;
-#pragma unroll
-      for (int e = 0; e < E; ++e) part[e] = sum[e];
+      store_piece<MM_F32>(p.parts, ((int64_t)chunk * 2 + (from_before ? 0 : 1)) * a.cols + j, sum);
+      if (!from_before && j == 0) p.spanning[1 + atomicAdd(p.spanning, 1u)] = (uint32_t)chunk;
     } else {
-      write_sum<TW, TO, E>(a, token, j, sum);
+      write_sum<TW, E>(a, token, j, sum);
     }
-    from_before = false;
-    token = next;
+  };
+  for (int i = 0; i < n; i += U) {
+    Piece<TO, E> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u < n && mine[i + u].x != none)
+        v[u] = Piece<TO, E>::load(at<TO>(a.dout, (int64_t)mine[i + u].y * a.lddo + j));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u >= n) break;
+      const uint32_t next = mine[i + u].x;
+      if (next != token) {
+        leave(false);
+        token = next;
+        from_before = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] = 0.f;
+      }
+      if (token == none) return;
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[e] += v[u].get(e);
+    }
   }
+  leave(mine[n].x == token);
 }
 
-// Tokens whose places go past a chunk's end: the chunk where one begins adds the
-// parts of the chunks after it, a column a thread.
-template <int TW, int TO>
+// Tokens whose places go past a chunk's end: their parts, 64 threads of V columns each a
+// block, the chunks in four runs that are added in order.
+template <int TW, int V>
 __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p) {
+  __shared__ float runs[4][64][V + 1];
   pdl_launch_dependents();
   pdl_wait();
   const EmbedBwdArgs &a = p.a;
-  const int j = (int)blockIdx.y * 256 + threadIdx.x;
-  if (j >= a.cols) return;
-  const int rows = (int)a.rows;
-  for (int c = (int)blockIdx.x; c + 1 < p.chunks; c += (int)gridDim.x) {
-    const int i0 = c * p.chunk, i1 = i0 + p.chunk;
-    const uint32_t token = p.sorted[i1].x;
-    if (token == (uint32_t)a.vocab) return;
-    if (p.sorted[i1 - 1].x != token) continue;                             // none goes past this end
-    if (p.sorted[i0].x == token && i0 > 0 && p.sorted[i0 - 1].x == token) continue;  // it began before
-    float sum[1] = {p.parts[((int64_t)c * 2 + 1) * a.cols + j]};
-    for (int k = c + 1; k < p.chunks && p.sorted[k * p.chunk].x == token; ++k) {
-      sum[0] += p.parts[(int64_t)k * 2 * a.cols + j];
-      if (p.sorted[min(rows, (k + 1) * p.chunk) - 1].x != token) break;
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  const int j = ((int)blockIdx.y * 64 + x) * V, total = (int)p.spanning[0];
+  for (int s = (int)blockIdx.x; s < total; s += (int)gridDim.x) {
+    const int c = (int)p.spanning[1 + s];
+    const uint32_t token = p.sorted[(int64_t)(c + 1) * p.chunk].x;
+    int more = 0;  // the chunks after c that begin with the token
+    for (int k = c + 1;; k += 256) {
+      const int at = k + (int)threadIdx.x;
+      const int here = __syncthreads_count(at < p.chunks && p.sorted[(int64_t)at * p.chunk].x == token);
+      more += here;
+      if (here < 256) break;
     }
-    write_sum<TW, TO, 1>(a, token, j, sum);
+    const int k0 = (int)((int64_t)more * y / 4), k1 = (int)((int64_t)more * (y + 1) / 4);
+    float sum[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = 0.f;
+    if (j < a.cols) {
+      const int64_t part = (int64_t)(c + 1) * 2 * a.cols + j;
+      if (y == 0) load_piece<MM_F32>(p.parts, part - a.cols, sum);  // the second of chunk c
+      for (int k = k0; k < k1; k += 8) {
+        float v[8][V];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (k + u < k1) load_piece<MM_F32>(p.parts, part + (int64_t)(k + u) * 2 * a.cols, v[u]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (k + u < k1)
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] += v[u][e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) runs[y][x][e] = sum[e];
+    __syncthreads();
+    if (y == 0 && j < a.cols) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum[e] = ((sum[e] + runs[1][x][e]) + runs[2][x][e]) + runs[3][x][e];
+      write_sum<TW, V>(a, token, j, sum);
+    }
+    __syncthreads();
   }
 }
 
@@ -223,7 +360,7 @@ mm_status embed_sums(const EmbedBwdArgs &a, SumParams p, LaunchCtx &ctx) {
                      (uintptr_t)a.base % 16 == 0 && (a.lddo * bo % 16 == 0 || a.rows == 1) &&
                      (a.vocab == 1 || (a.lddw * bw % 16 == 0 && a.ldb * bw % 16 == 0));
   const int64_t pieces = whole ? a.cols / kE : a.cols;
-  p.log_threads = 0;
+  p.log_threads = kMinLogThreads;
   while (p.log_threads < 8 && (1ll << p.log_threads) < pieces) ++p.log_threads;
   const int64_t groups = 256 >> p.log_threads;
   const dim3 grid((unsigned)((p.chunks + groups - 1) / groups),
@@ -233,8 +370,9 @@ mm_status embed_sums(const EmbedBwdArgs &a, SumParams p, LaunchCtx &ctx) {
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch");
   count_operator_launch();
   if (p.chunks == 1) return MM_OK;
-  const dim3 join((unsigned)std::min(p.chunks, 64), (unsigned)((a.cols + 255) / 256));
-  e = launch_pdl(embed_join_kernel<TW, TO>, join, dim3(256), 0, ctx.stream, dim3(1), p);
+  const int64_t columns = whole ? 256 : 64, slabs = (a.cols + columns - 1) / columns;
+  const int64_t across = std::max<int64_t>(1, std::min<int64_t>(p.chunks - 1, 8 * ctx.dev->info.sms / slabs));
+  e = launch_pdl(whole ? embed_join_kernel<TW, 4> : embed_join_kernel<TW, 1>, dim3((unsigned)across, (unsigned)slabs), dim3(256), 0, ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (join)");
   count_operator_launch();
   return MM_OK;
@@ -260,33 +398,72 @@ mm_status launch_embedding(const EmbedArgs &a, LaunchCtx &ctx) {
 }
 
 mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
-  const size_t es = (size_t)dtype_bytes(a.tw);
+  const int64_t es = dtype_bytes(a.tw);
   SumParams p;
   std::memset(&p, 0, sizeof p);
   p.a = a;
-  p.chunk = a.rows >= 4096 ? 32 : 8;
+  p.chunk = a.rows >= 4096 ? kMaxChunk : 8;
   p.chunks = (int)((a.rows + p.chunk - 1) / p.chunk);
-  const size_t pairs = ((size_t)a.rows * sizeof(uint2) + 255) / 256 * 256;
-  char *w = nullptr;
-  if (a.rows > 0) {
-    void *s = nullptr;
-    mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, 2 * pairs + (size_t)p.chunks * 2 * a.cols * sizeof(float), &s);
-    if (st != MM_OK) return st;
-    w = static_cast<char *>(s);
+  SortParams f;
+  std::memset(&f, 0, sizeof f);
+  f.base = static_cast<const uint8_t *>(a.base);
+  f.dweight = static_cast<uint8_t *>(a.dweight);
+  f.bytes = a.cols * es;
+  f.ldb = a.ldb * es;
+  f.ldw = a.lddw * es;
+  f.fill_rows = a.base == a.dweight ? 0 : a.vocab;
+  if (a.lddw == a.cols && (!a.base || a.ldb == a.cols) && f.fill_rows) {  // one long row
+    f.bytes *= a.vocab;
+    f.fill_rows = 1;
   }
-  if (!a.base)
-    MM_CUDA_TRY(cudaMemset2DAsync(a.dweight, (size_t)a.lddw * es, 0, (size_t)a.cols * es, (size_t)a.vocab, ctx.stream));
-  else if (a.base != a.dweight)
-    MM_CUDA_TRY(cudaMemcpy2DAsync(a.dweight, (size_t)a.lddw * es, a.base, (size_t)a.ldb * es, (size_t)a.cols * es,
-                                  (size_t)a.vocab, cudaMemcpyDeviceToDevice, ctx.stream));
-  if (a.rows == 0) return MM_OK;
-  uint2 *sorted = reinterpret_cast<uint2 *>(w), *other = reinterpret_cast<uint2 *>(w + pairs);
-  p.sorted = sorted;
-  p.parts = reinterpret_cast<float *>(w + 2 * pairs);
-  int passes = 1;
-  while (passes < 4 && a.vocab >> (8 * passes)) ++passes;
-  cudaError_t e = launch_pdl(sort_kernel, dim3(1), dim3(kSortThreads), 0, ctx.stream, dim3(1), a.tokens, a.ti, a.vocab,
-                             (int)a.rows, sorted, other, passes);
+  while (f.log_threads < 10 && (64ll << f.log_threads) < f.bytes) ++f.log_threads;
+  if (a.rows == 0) {
+    if (!f.fill_rows) return MM_OK;
+    cudaError_t e = launch_pdl(embed_fill_kernel, dim3((unsigned)ctx.dev->info.sms), dim3(kSortThreads), 0, ctx.stream, dim3(1), f);
+    if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (rows)");
+    count_operator_launch();
+    return MM_OK;
+  }
+  const auto whole = [](int64_t bytes) { return ((size_t)bytes + 255) / 256 * 256; };
+  const size_t pairs = whole(a.rows * (int64_t)sizeof(uint2)), list = whole((p.chunks + 1) * (int64_t)sizeof(uint32_t));
+  // as many clusters as run at once: one sorts, the others write rows
+  static PerDevice<int> fits;
+  int clusters;
+  const cudaError_t err = fits.get(ctx.dev->info.ordinal, &clusters, [](int *n) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = kSortCtas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(kSortCtas);
+    lc.blockDim = dim3(kSortThreads);
+    lc.dynamicSmemBytes = kSortSmem;
+    lc.attrs = &at;
+    lc.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, embed_sort_kernel, &lc);
+  });
+  if (err != cudaSuccess) return cuda_error(err, "embedding_backward set-up");
+  if (clusters < 1) return set_error(MM_ERR_UNSUPPORTED, "no cluster of CTAs fits on this device");
+  const int fill_ctas = f.fill_rows ? std::max(1, clusters - 1) * kSortCtas : 0;
+  void *scratch = nullptr;
+  mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, 2 * pairs + list + (size_t)p.chunks * 2 * a.cols * sizeof(float), &scratch);
+  if (st != MM_OK) return st;
+  char *w = static_cast<char *>(scratch);
+  f.to = reinterpret_cast<uint2 *>(w);
+  f.other = reinterpret_cast<uint2 *>(w + pairs);
+  f.spanning = p.spanning = reinterpret_cast<uint32_t *>(w + 2 * pairs);
+  p.parts = reinterpret_cast<float *>(w + 2 * pairs + list);
+  p.sorted = f.to;
+  f.tokens = a.tokens;
+  f.ti = a.ti;
+  f.vocab = a.vocab;
+  f.rows = (int)a.rows;
+  f.passes = 1;
+  while (a.vocab >> (kDigit * f.passes)) ++f.passes;
+  cudaError_t e = launch_pdl(embed_sort_kernel, dim3((unsigned)(kSortCtas + fill_ctas)), dim3(kSortThreads), kSortSmem,
+                             ctx.stream, dim3(kSortCtas), f);
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (sort)");
   count_operator_launch();
   return with_type(a.tw, [&](auto tw) {

@@ -3,37 +3,42 @@
 #include <algorithm>
 
 #include "../operators.h"
+#include "row_copy.cuh"
 
 namespace mm {
 
 namespace {
 
-// A thread 16 bytes of the copy; a source on any address, read byte by byte
-// (neighbouring threads share its sectors).
+// A power of two of threads to a row, 16 bytes of the copy each, up to four pieces read
+// before the first is stored.
 __global__ void __launch_bounds__(256) pack_rows_kernel(const uint8_t *src, int64_t ld, int64_t rows,
-                                                        int64_t bytes, uint8_t *dst, int64_t ld16) {
+                                                        int64_t bytes, uint8_t *dst, int64_t ld16, int log_threads) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t per = ld16 / 16, total = per * rows;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per, c = (i - r * per) * 16;
-    const uint8_t *s = src + r * ld + c;
-    uint32_t w[4];
+  constexpr int U = 4;
+  const int threads = 1 << log_threads, t = threadIdx.x & (threads - 1);
+  const int64_t groups = (int64_t)gridDim.x << (8 - log_threads);
+  for (int64_t r = ((int64_t)blockIdx.x << (8 - log_threads)) + (threadIdx.x >> log_threads); r < rows; r += groups) {
+    const uint8_t *from = src + r * ld;
+    for (int64_t b0 = t * 16; b0 < ld16; b0 += threads * 16 * U) {
+      uint4 v[U];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      w[k] = 0;
+      for (int k = 0; k < U; ++k)
+        if (b0 + k * threads * 16 < ld16) v[k] = row_piece<1>(from, bytes, b0 + k * threads * 16);
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (c + 4 * k + b < bytes) w[k] |= (uint32_t)s[4 * k + b] << (8 * b);
+      for (int k = 0; k < U; ++k)
+        if (b0 + k * threads * 16 < ld16) *reinterpret_cast<uint4 *>(dst + r * ld16 + b0 + k * threads * 16) = v[k];
     }
-    *reinterpret_cast<uint4 *>(dst + r * ld16 + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
 mm_status pack(TmaRows &r, uint8_t *dst, int64_t ld16, LaunchCtx &ctx) {
-  const int64_t blocks = std::min<int64_t>((ld16 / 16 * r.rows + 255) / 256, 16 * ctx.dev->info.sms);
+  int log_threads = 0;
+  while (log_threads < 8 && (64ll << log_threads) < ld16) ++log_threads;
+  const int64_t per = 256 >> log_threads;
+  const int64_t blocks = std::min<int64_t>((r.rows + per - 1) / per, 16 * ctx.dev->info.sms);
   cudaError_t e = launch_pdl(pack_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, ctx.stream, dim3(1),
-                             static_cast<const uint8_t *>(r.p), r.ld, r.rows, r.bytes, dst, ld16);
+                             static_cast<const uint8_t *>(r.p), r.ld, r.rows, r.bytes, dst, ld16, log_threads);
   if (e != cudaSuccess) return cuda_error(e, "row copy launch");
   count_operator_launch();
   r.p = dst;
