@@ -61,6 +61,7 @@ struct GatherParams {
   LossArgs a;
   Rows r;
   int backward;
+  int log_threads;  // threads a row
 };
 
 __device__ __forceinline__ int valid_target(const LossArgs &a, int64_t t) {
@@ -72,7 +73,7 @@ __device__ __forceinline__ int valid_target(const LossArgs &a, int64_t t) {
 // own (and, backward, finds the largest |dloss| of all) for itself: a few KB from L2
 // instead of another kernel.  Rows move in 16-byte pieces, wherever they start.
 constexpr int kGatherThreads = 512, kGatherWarps = kGatherThreads / 32;
-__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
+__global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherParams p) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ int warp_count[kGatherWarps];
@@ -126,22 +127,20 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
     }
     __syncthreads();
     constexpr int U = 4;  // pieces read before the first is stored
-    const int64_t all = (int64_t)total * pieces;
-    for (int64_t j0 = t; j0 < all; j0 += kGatherThreads * U) {
-      uint4 v[U];
-      uint16_t *to[U];
+    const int threads = 1 << p.log_threads, t0 = t & (threads - 1);
+    for (int k = t >> p.log_threads; k < total; k += kGatherThreads >> p.log_threads) {
+      const uint8_t *from = x + (int64_t)at_row[k] * a.ldx * 2;
+      uint4 *to = reinterpret_cast<uint4 *>(p.r.x + (int64_t)(before + k) * p.r.ldx);
+      for (int c = t0; c < pieces; c += threads * U) {
+        RowPiece<2> v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t j = j0 + u * kGatherThreads;
-        if (j < all) {
-          const int k = (int)(j / pieces), c = (int)(j - (int64_t)k * pieces);
-          v[u] = row_piece<2>(x + (int64_t)at_row[k] * a.ldx * 2, (int64_t)a.cols * 2, (int64_t)c * 16);
-          to[u] = p.r.x + (int64_t)(before + k) * p.r.ldx + c * 8;
-        }
+        for (int u = 0; u < U; ++u)
+          if (c + u * threads < pieces) v[u].load(from, (int64_t)a.cols * 2, (int64_t)(c + u * threads) * 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c + u * threads < pieces)
+            to[c + u * threads] = v[u].value(from, (int64_t)a.cols * 2, (int64_t)(c + u * threads) * 16);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j0 + u * kGatherThreads < all) *reinterpret_cast<uint4 *>(to[u]) = v[u];
     }
     before += total;
     __syncthreads();
@@ -171,7 +170,11 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
 // to the host: each kernel reads the count and lays out its own tiles.
 enum Mode { MODE_LSE, MODE_G, MODE_DX, MODE_DW };
 
-constexpr int kThreads = 320;  // warp 0 copies, warp 1 issues MMAs, warps 2-9 take tiles out
+// Warp 0 copies, warp 1 issues MMAs, the others take tiles out: 16 where a tile leaves in
+// 16 bits (a product over few rows of K is all epilogue: 16 x 4096 x 32000, dW, 62 us
+// with 8), 8 where its rows' sums stay in registers or it is added to fp32 sums.
+constexpr int out_warps(int mode) { return mode == MODE_G || mode == MODE_DW ? 16 : 8; }
+constexpr int tile_threads(int mode) { return 64 + 32 * out_warps(mode); }
 constexpr int kErrCopy = 0xa01, kErrMma = 0xa02, kErrStore = 0xa03, kErrDrain = 0xa04;
 constexpr int kGroupRows = 8;  // row tiles walked together, so that their operands stay in L2
 
@@ -215,6 +218,8 @@ __device__ __forceinline__ bool halved(const Tiles &s, int tm, int tn) {
 
 struct TileParams {
   Rows r;
+  const void *targets;  // LSE of few rows: x as it lies (r.count null), `rows` of it
+  int ti, rows;
   int cols, vocab;
   int v0, width;     // the piece of the vocabulary: its first token, how many (G: padded to 64)
   int tx;
@@ -233,16 +238,23 @@ struct TileParams {
 };
 
 // Stages of 64 of K: 128 rows of A, and of B 128 (its half of a pair's tile) or 256.
-// Where tiles leave through boxes in shared memory, two for each warp that takes them
-// out; one for the few rows of CG = 1, whose products wait for W.
+// Tiles in 16 bits leave through boxes in shared memory, one for each warp that takes
+// them out.
 template <int MODE, int CG>
 struct Ring {
   static constexpr uint32_t kA = 128 * 128, kStageB = kA + (CG == 2 ? 128 : 256) * 128;
-  static constexpr int kBoxesAWarp = (MODE == MODE_G || MODE == MODE_DW) && CG == 2 ? 2 : 1;
-  static constexpr int kStages = CG == 1 ? 4 : kBoxesAWarp == 2 ? 5 : 6;
-  static constexpr uint32_t kBoxes = 8 * kBoxesAWarp * kBoxB;  // (LSE: sums)
+  static constexpr int kOut = out_warps(MODE);
+  static constexpr int kStages = CG == 2 ? (kOut == 16 ? 5 : 6) : kOut == 16 ? 3 : 4;
+  static constexpr uint32_t kBoxes = kOut * kBoxB;  // (LSE: sums)
   static constexpr size_t kSmem = kStages * kStageB + kBoxes + 1024 + 256;
 };
+
+__device__ __forceinline__ int row_count(const Rows &r, int rows) { return r.count ? max(1, *r.count) : rows; }
+__device__ __forceinline__ int target_of(const TileParams &p, int row) {
+  if (p.r.count) return p.r.target[row];
+  const int64_t v = row < p.rows ? load_token(p.targets, p.ti, row, p.vocab) : p.vocab;
+  return v < p.vocab ? (int)v : -1;
+}
 
 template <int CG>
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
@@ -323,88 +335,77 @@ __device__ __forceinline__ float2 join_sums(float2 a, float2 b) {
   return make_float2(r, a.y * exp2_fast(a.x - r) + b.y * exp2_fast(b.x - r));
 }
 
-// 64 columns of 32 rows in 16 bits to a box.
-// A warp's next box of N, free: its store has read it.
-template <int N>
-__device__ __forceinline__ uint8_t *next_box(uint8_t *boxes, int &side) {
-  if ((threadIdx.x & 31) == 0) tma_store_wait_read<N - 1>();
+// A box, free: its store has read it.
+__device__ __forceinline__ void wait_box() {
+  if ((threadIdx.x & 31) == 0) tma_store_wait_read<0>();
   __syncwarp();
-  uint8_t *box = boxes + side * kBoxB;
-  side = side + 1 == N ? 0 : side + 1;
-  return box;
 }
-template <typename F>
-__device__ __forceinline__ void fill_box(uint8_t *box, int tx, F &&value) {
+// Columns 32 h .. of 32 rows in 16 bits to half a box.
+__device__ __forceinline__ void fill_box(uint8_t *box, int tx, int h, const uint32_t (&v)[32]) {
   const int lane = threadIdx.x & 31;
+  const auto f = [&](int i) { return __uint_as_float(v[i]); };
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-        make_uint4(pack2(tx, value(8 * j), value(8 * j + 1)), pack2(tx, value(8 * j + 2), value(8 * j + 3)),
-                   pack2(tx, value(8 * j + 4), value(8 * j + 5)), pack2(tx, value(8 * j + 6), value(8 * j + 7)));
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4 *>(box + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4)) =
+        make_uint4(pack2(tx, f(8 * j), f(8 * j + 1)), pack2(tx, f(8 * j + 2), f(8 * j + 3)),
+                   pack2(tx, f(8 * j + 4), f(8 * j + 5)), pack2(tx, f(8 * j + 6), f(8 * j + 7)));
+}
+// 64 columns of a tile in registers; then the accumulator is given back.
+template <typename F>
+__device__ __forceinline__ void take_columns(uint32_t tmem, uint32_t (&v)[2][32], F &&release) {
+  tmem_ld_32cols(tmem, v[0]);
+  tmem_ld_32cols(tmem + 32, v[1]);
+  tmem_ld_wait();
+  release();
+}
+__device__ __forceinline__ void store_box_tma(const CUtensorMap *map, uint8_t *box, int x, int y) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tma_store_2d(map, smem_u32(box), x, y);
 }
 
-template <int BOXES>
-__device__ __forceinline__ void take_g(const TileParams &p, const CUtensorMap *map, uint32_t tmem, const Unit &u,
-                                       int row0, int c0, int c1, uint8_t *boxes, int &side) {
-  const int lane = threadIdx.x & 31, row = row0 + lane;
+// G, DW: columns n .. n + 63 of the product's rows row0 .. row0 + 31.
+__device__ __forceinline__ void leave_g(const TileParams &p, const CUtensorMap *map, uint32_t (&v)[2][32], int n, int row0,
+                                        uint8_t *box) {
+  const int row = row0 + (threadIdx.x & 31);
   const int target = p.r.target[row];
   const float ratio = p.r.ratio[row], lse2 = p.r.lse2[row];
   const bool live = ratio != 0.f;  // (a weight of 0 takes its row out, whatever its logits)
-#pragma unroll 1
-  for (int c = c0; c < c1 && u.n0 + c < p.width; c += 64) {
-    uint32_t v[2][32];
-    tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
-    tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
-    tmem_ld_wait();
+  wait_box();
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      float &x = reinterpret_cast<float &>(v[i >> 5][i & 31]);
-      x = exp2_fast(fmaf(x, kLog2e, -lse2)) * ratio;
-    }
-    const int at = target - p.v0 - u.n0 - c;
-    if (__any_sync(0xffffffffu, (unsigned)at < 64u)) {
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        float &x = reinterpret_cast<float &>(v[i >> 5][i & 31]);
-        x = at == i ? x - ratio : x;
-      }
-    }
-    const int left = p.vocab - p.v0 - u.n0 - c;
-    if (left < 64 || __any_sync(0xffffffffu, !live)) {
+    for (int i = 0; i < 32; ++i)
+      v[h][i] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[h][i]), kLog2e, -lse2)) * ratio);
+    const int first = p.v0 + n + 32 * h, at = target - first, left = p.vocab - first;
+    if (__any_sync(0xffffffffu, (unsigned)at < 32u)) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] = live && i < left ? v[i >> 5][i & 31] : 0u;
+      for (int i = 0; i < 32; ++i) v[h][i] = at == i ? __float_as_uint(__uint_as_float(v[h][i]) - ratio) : v[h][i];
     }
-    uint8_t *box = next_box<BOXES>(boxes, side);
-    fill_box(box, p.tx, [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); });
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) tma_store_2d(map, smem_u32(box), u.n0 + c, row0);
+    if (left < 32 || __any_sync(0xffffffffu, !live)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[h][i] = live && i < left ? v[h][i] : 0u;
+    }
+    fill_box(box, p.tx, h, v[h]);
   }
+  store_box_tma(map, box, n, row0);
 }
 
-template <int BOXES>
-__device__ __forceinline__ void take_dw(const TileParams &p, const CUtensorMap *map, uint32_t tmem, const Unit &u,
-                                        int row0, int c0, int c1, uint8_t *boxes, int &side, float gain) {
-  const int lane = threadIdx.x & 31, v0 = p.v0 + row0;
-  if (v0 >= p.vocab) return;
-#pragma unroll 1
-  for (int c = c0; c < c1 && u.n0 + c < p.cols; c += 64) {
-    uint32_t v[2][32];
-    tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
-    tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
-    tmem_ld_wait();
-    uint8_t *box = next_box<BOXES>(boxes, side);
-    fill_box(box, p.tx, [&](int i) { return __uint_as_float(v[i >> 5][i & 31]) * gain; });
-    if (p.vec) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tma_store_2d(map, smem_u32(box), u.n0 + c, v0);
-    } else {  // rows that TMA cannot address, or would clip behind their end
-      __syncwarp();
-      store_box<2>(box, p.dw, (int64_t)v0 * p.lddw + u.n0 + c, p.lddw, min(32, p.vocab - v0),
-                   min(64, p.cols - u.n0 - c));
-      __syncwarp();
-    }
+__device__ __forceinline__ void leave_dw(const TileParams &p, const CUtensorMap *map, uint32_t (&v)[2][32], int n, int v0,
+                                         uint8_t *box, float gain) {
+  wait_box();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[h][i] = __float_as_uint(__uint_as_float(v[h][i]) * gain);
+    fill_box(box, p.tx, h, v[h]);
+  }
+  if (p.vec) {
+    store_box_tma(map, box, n, v0);
+  } else {  // rows that TMA cannot address, or would clip behind their end
+    __syncwarp();
+    store_box<2>(box, p.dw, (int64_t)v0 * p.lddw + n, p.lddw, min(32, p.vocab - v0), min(64, p.cols - n));
+    __syncwarp();
   }
 }
 
@@ -437,7 +438,7 @@ __device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, cons
 }
 
 template <int MODE, int CG>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(tile_threads(MODE), 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmO,
                 const TileParams p) {
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
-      mbar_init(tempty0 + 8 * a, 8 * CG);
+      mbar_init(tempty0 + 8 * a, R::kOut * CG);
     }
     mbar_init(drain, 1);
     mbar_init(stall, 1);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t leader_full0 = CG == 2 ? map_to_rank(full0, 0) : full0;
   const uint32_t leader_tempty0 = CG == 2 ? map_to_rank(tempty0, 0) : tempty0;
   pdl_wait();
-  const int rows = max(1, *p.r.count);
+  const int rows = row_count(p.r, p.rows);
   const Tiles tiles = tiles_of(MODE == MODE_DW ? p.width : rows, 128 * CG, p.tiles_n, p.splits, p.bn, p.places);
   const int num_kb = MODE == MODE_DW ? (rows + 63) / 64 : p.num_kb;
   // the blocks of K of a unit
@@ -602,9 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;  // q: the TMEM lanes this warp may read
-    uint8_t *mine = boxes + (warp - 2) * R::kBoxesAWarp * kBoxB;
-    int side = 0;
+    const int q = warp & 3, group = (warp - 2) >> 2;  // q: the TMEM lanes this warp may read
+    uint8_t *box = boxes + (warp - 2) * kBoxB;
     const float gain = MODE == MODE_DW ? *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f) : 0.f;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -624,7 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int turn = 0;
     for (int i = cid; i < tiles.total && ok; i += ncl, turn ^= 1) {
       const Unit u = unit_at(tiles, p.bn, i);
-      const int row0 = u.tm * 128 * CG + pos * 128 + q * 32, c0 = half * (u.w / 2), c1 = c0 + u.w / 2;
+      const int row0 = u.tm * 128 * CG + pos * 128 + q * 32;
+      // this warp's columns: half of the tile's, or 64 (a half tile has none for some)
+      const int wide = R::kOut == 8 ? u.w / 2 : 64, c0 = group * wide, n = u.n0 + c0;
       const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
       if constexpr (MODE == MODE_LSE) {
         const bool live = row0 < rows && u.n0 < p.vocab;  // (else a half tile past the end)
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the eight warps go on or give up together
           if (!(ok = all_take(warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)))) break;
           fence_after();
-          if (live) add_chunk(l, lanes + (uint32_t)(acc * 256 + c0), u.w / 2, k == 0);
+          if (live) add_chunk(l, lanes + (uint32_t)(acc * 256 + c0), wide, k == 0);
           release();
         }
         if (!ok) break;
@@ -642,24 +644,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 sum = make_float2(-3e38f, 0.f);
         if (live) {
           const int row = row0 + lane;
-          sum = sum_exp(p, l, u.n0 + c0, u.w / 2, p.r.target[row], p.hit + row);
-          if (half) *upper = sum;
+          sum = sum_exp(p, l, n, wide, target_of(p, row), p.hit + row);
+          if (group) *upper = sum;
         }
         all_take(true);
-        if (live && !half) p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row0 + lane] = join_sums(sum, *upper);
+        if (live && !group) p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row0 + lane] = join_sums(sum, *upper);
       } else {
         if (!warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)) break;
         fence_after();
         const uint32_t tmem = lanes + (uint32_t)(acc * 256);
         int kb0;
-        if constexpr (MODE == MODE_G) {
-          take_g<R::kBoxesAWarp>(p, &tmO, tmem, u, row0, c0, c1, mine, side);
-        } else if constexpr (MODE == MODE_DX) {
-          if (row0 < rows) take_dx(p, tmem, u, row0, c0, c1, k_of(u, kb0) == 0);
+        if constexpr (MODE == MODE_DX) {
+          if (row0 < rows) take_dx(p, tmem, u, row0, c0, c0 + wide, k_of(u, kb0) == 0);
+          release();
+        } else if (c0 < u.w && n < (MODE == MODE_G ? p.width : p.cols) && (MODE == MODE_G || p.v0 + row0 < p.vocab)) {
+          uint32_t v[2][32];
+          take_columns(tmem + (uint32_t)c0, v, release);
+          if constexpr (MODE == MODE_G) leave_g(p, &tmO, v, n, row0, box);
+          else leave_dw(p, &tmO, v, n, p.v0 + row0, box, gain);
         } else {
-          take_dw<R::kBoxesAWarp>(p, &tmO, tmem, u, row0, c0, c1, mine, side, gain);
+          release();
         }
-        release();
       }
     }
     if (lane == 0) tma_store_wait_all();
@@ -687,8 +692,9 @@ struct LossParams {
   int tile_m, bn, tiles_n, places;  // of the product
 };
 
-// 32 rows a block, 32 threads a row over the tiles of the vocabulary; the last steps
-// in fp64, so that a loss is no less exact than its sums.
+// 32 rows a block, 32 threads a row over the tiles of the vocabulary.  r log 2 is kept
+// as a product and its error, so that a loss is no less exact than its sums.  (In fp64
+// the logarithm of 32 rows took 10 us.)
 constexpr int kLossThreads = 1024;
 __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) {
   pdl_launch_dependents();
@@ -697,8 +703,13 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) 
   __shared__ float2 sh[Y][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * 32 + x;
-  const int slot = row < p.a.rows ? p.r.slot[row] : -1;
-  const Tiles tiles = tiles_of(max(1, *p.r.count), p.tile_m, p.tiles_n, 1, p.bn, p.places);
+  // where a row's sums are, or -1
+  const auto slot_of = [&](int64_t i) {
+    if (p.r.count) return p.r.slot[i];
+    return valid_target(p.a, i) < 0 ? -1 : (int)i;
+  };
+  const int slot = row < p.a.rows ? slot_of(row) : -1;
+  const Tiles tiles = tiles_of(row_count(p.r, p.a.rows), p.tile_m, p.tiles_n, 1, p.bn, p.places);
   const float2 none = make_float2(-3e38f, 0.f);
   float2 sum = none;
   if (slot >= 0) {
@@ -730,10 +741,11 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) 
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   const int64_t to = (int64_t)blockIdx.x * 32 + y;
   if (x != 0 || to >= p.a.rows) return;
-  const int at = p.r.slot[to];
-  const double lse = at < 0 ? 0.0 : (double)r * 0.693147180559945309 + log((double)s);
-  p.a.loss[to] = at < 0 ? 0.f : (float)(lse - (double)p.hit[at]);
-  if (p.a.lse) p.a.lse[to] = (float)lse;
+  const int at = slot_of(to);
+  constexpr float kLn2 = 0.693147180559945309f, kLn2Rest = (float)(0.693147180559945309 - (double)kLn2);
+  const float whole = r * kLn2, rest = fmaf(r, kLn2, -whole) + r * kLn2Rest + logf(s);
+  p.a.loss[to] = at < 0 ? 0.f : (whole - p.hit[at]) + rest;
+  if (p.a.lse) p.a.lse[to] = at < 0 ? 0.f : whole + rest;
 }
 
 struct DxParams {
@@ -833,7 +845,8 @@ Rows cut_rows(Cut &cut, const LossArgs &a, bool backward) {
 }
 
 mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, LaunchCtx &ctx) {
-  GatherParams p{a, r, backward};
+  GatherParams p{a, r, backward, 0};
+  while (p.log_threads < 9 && (32ll << p.log_threads) < r.ldx) ++p.log_threads;  // (up to four pieces each)
   const int blocks = std::min(a.rows, 2 * ctx.dev->info.sms);
   cudaError_t e = launch_pdl(gather_kernel, dim3((unsigned)blocks), dim3(kGatherThreads), 0, ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch (gather)");
@@ -856,7 +869,7 @@ cudaLaunchConfig_t tile_config(int grid, cudaStream_t s, cudaLaunchAttribute *at
   at->val.clusterDim.y = at->val.clusterDim.z = 1;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)grid);
-  lc.blockDim = dim3(kThreads);
+  lc.blockDim = dim3(tile_threads(MODE));
   lc.dynamicSmemBytes = Ring<MODE, CG>::kSmem;
   lc.stream = s;
   lc.attrs = at;
@@ -899,7 +912,7 @@ mm_status launch_tiles(TileParams &p, const Maps &m, int64_t M, LaunchCtx &ctx) 
   const int64_t tiles = (M + 128 * CG - 1) / (128 * CG) * p.tiles_n * p.splits;
   if (tiles >= 1 << 30) return set_error(MM_ERR_UNSUPPORTED, "too many tiles");
   const int grid = CG * (int)std::min<int64_t>(p.bn == 256 ? 2 * tiles : tiles, p.places);
-  cudaError_t e = launch_pdl(tile_kernel<MODE, CG>, dim3((unsigned)grid), dim3(kThreads), Ring<MODE, CG>::kSmem, ctx.stream,
+  cudaError_t e = launch_pdl(tile_kernel<MODE, CG>, dim3((unsigned)grid), dim3(tile_threads(MODE)), Ring<MODE, CG>::kSmem, ctx.stream,
                              dim3(CG), m.a, m.b, m.bh, m.o, p);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch");
   count_operator_launch();
@@ -922,7 +935,7 @@ mm_status logits_maps(Maps *m, TileParams &p, Form f, const TmaRows &w) {
   const char *base = static_cast<const char *>(w.p) + (int64_t)p.v0 * w.ld;
   const int64_t tokens = std::min(p.width, p.vocab - p.v0);
   mm_status st;
-  if ((st = rows_map(&m->a, p.tx, p.r.x, p.cols, p.r.rows_pad, p.r.ldx, 128)) != MM_OK) return st;
+  if (p.r.x && (st = rows_map(&m->a, p.tx, p.r.x, p.cols, p.r.rows_pad, p.r.ldx, 128)) != MM_OK) return st;
   if ((st = rows_map(&m->b, p.tx, base, p.cols, tokens, w.ld / 2, p.bn / f.cg)) != MM_OK) return st;
   return rows_map(&m->bh, p.tx, base, p.cols, tokens, w.ld / 2, p.bn / f.cg / 2);
 }
@@ -965,10 +978,15 @@ mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
     return MM_OK;
   }
   TileParams p = tile_params(a, ctx);
+  const Form f = form_of(a.rows);
+  // Few rows are one row tile whether or not all of them count, so they are not
+  // gathered where TMA reads x as it lies.
+  const bool direct = f.cg == 1 && (uintptr_t)a.x % 16 == 0 && (a.ldx % 8 == 0 || a.rows == 1) && a.ldx < (1LL << 37);
   Cut cut;
   for (int pass = 0; pass < 2; ++pass) {
     cut.used = 0;
-    p.r = cut_rows(cut, a, false);
+    if (direct) std::memset(&p.r, 0, sizeof p.r), p.r.rows_pad = kRowTile;
+    else p.r = cut_rows(cut, a, false);
     p.hit = cut.take<float>(p.r.rows_pad);
     p.part = cut.take<float2>(((int64_t)a.vocab + 127) / 128 * p.r.rows_pad);
     if (pass == 0) {
@@ -981,11 +999,17 @@ mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
   mm_status st;
   TmaRows w;
   if ((st = align_weight(a, &w, ctx)) != MM_OK) return st;
-  if ((st = launch_gather(a, p.r, false, ctx)) != MM_OK) return st;
-  const Form f = form_of(a.rows);
+  if (!direct && (st = launch_gather(a, p.r, false, ctx)) != MM_OK) return st;
   p.width = a.vocab;
   Maps m;
   if ((st = logits_maps(&m, p, f, w)) != MM_OK) return st;
+  if (direct) {
+    p.targets = a.targets;
+    p.ti = a.ti;
+    p.rows = a.rows;
+    st = rows_map(&m.a, p.tx, a.x, p.cols, a.rows, a.rows == 1 ? ((int64_t)a.cols + 7) / 8 * 8 : a.ldx, 128);
+    if (st != MM_OK) return st;
+  }
   m.o = m.a;  // (none)
   if ((st = launch_tiles<MODE_LSE>(f, p, m, a.rows, ctx)) != MM_OK) return st;
   LossParams l{a, p.r, p.part, p.hit, f.tile_m(), p.bn, p.tiles_n, p.places};

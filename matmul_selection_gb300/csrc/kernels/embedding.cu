@@ -73,8 +73,10 @@ cudaError_t embed_launch(const EmbedArgs &a, LaunchCtx &ctx) {
 // digits keep their order because a warp takes 32 at a time, ranked by matching.
 // The places lie in global memory (L2) between passes, so any number of them sorts.
 //
-// dW's rows of zeros, or the base's, are written meanwhile by the other clusters of
-// the same launch: more time than the sort takes, where a whole matrix is written.
+// dW's rows are written meanwhile, as zeros or the base's, by the other clusters of the
+// launch, those that the sums will write again among them.  (Untouched rows written
+// beside the sums instead: 76 -> 88 us at 8192 x 4096 into 32000, 150 -> 191 at 65536 x
+// 1024 into 131072.)
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCtas = 8;
 constexpr int kDigit = 9, kBins = 1 << kDigit;
 constexpr size_t kSortSmem = (kSortWarps * kBins + kBins + 32) * sizeof(uint32_t);
@@ -89,8 +91,8 @@ struct SortParams {
   // the rows
   const uint8_t *base;  // null: zeros
   uint8_t *dweight;
-  int64_t bytes, ldb, ldw, fill_rows;  // of a row and between rows, in bytes
-  int log_threads;      // threads a row
+  int64_t bytes, ldb, ldw;  // of a row and between rows, in bytes
+  int64_t fill_rows;        // rows that follow one another without a gap count as one
 };
 
 __device__ __forceinline__ uint32_t cluster_u32(uint32_t addr, int rank) {
@@ -106,19 +108,35 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
   const int lo = (int)((int64_t)p.rows * rank / kSortCtas), n = (int)((int64_t)p.rows * (rank + 1) / kSortCtas) - lo;
   const int w0 = lo + (int)((int64_t)n * warp / kSortWarps), w1 = lo + (int)((int64_t)n * (warp + 1) / kSortWarps);
   const uint32_t below = (1u << lane) - 1;
+  constexpr int K = 8;
   uint2 *src = nullptr, *dst = p.passes & 1 ? p.to : p.other;  // the last pass ends in `to`
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * kDigit;
     const auto pair_at = [&](int i) {  // (written by other SMs: past L1)
       return pass ? __ldcg(src + i) : make_uint2((uint32_t)load_token(p.tokens, p.ti, i, p.vocab), (uint32_t)i);
     };
+    // the run, 32 K places at a time; a run of one batch stays in registers
+    uint2 v[K];
+    const auto load = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int i = i0 + k * 32 + lane;
+        v[k] = i < w1 ? pair_at(i) : make_uint2(~0u, 0);
+      }
+    };
+    const auto digit = [&](int i, uint2 x) { return i < w1 ? (x.x >> shift) & (kBins - 1) : (uint32_t)kBins; };
     for (int b = lane; b < kBins; b += 32) off[warp][b] = 0;
     __syncwarp();
-    for (int i = w0 + lane; i - lane < w1; i += 32) {
-      const uint32_t d = i < w1 ? (pair_at(i).x >> shift) & (kBins - 1) : kBins;
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      if (d < kBins && !(same & below)) off[warp][d] += __popc(same);
-      __syncwarp();
+    for (int i0 = w0; i0 < w1; i0 += 32 * K) {
+      load(i0);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (i0 + k * 32 >= w1) break;
+        const uint32_t d = digit(i0 + k * 32 + lane, v[k]);
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        if (d < kBins && !(same & below)) off[warp][d] += __popc(same);
+        __syncwarp();
+      }
     }
     __syncthreads();
     if (t < kBins) {
@@ -152,14 +170,18 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
       for (int w = 0; w < kSortWarps; ++w) off[w][t] += at;
     }
     __syncthreads();
-    for (int i = w0 + lane; i - lane < w1; i += 32) {
-      const uint2 v = i < w1 ? pair_at(i) : make_uint2(0, 0);
-      const uint32_t d = i < w1 ? (v.x >> shift) & (kBins - 1) : kBins;
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      if (d < kBins) dst[off[warp][d] + __popc(same & below)] = v;
-      __syncwarp();
-      if (d < kBins && !(same & below)) off[warp][d] += __popc(same);
-      __syncwarp();
+    for (int i0 = w0; i0 < w1; i0 += 32 * K) {
+      if (w1 - w0 > 32 * K) load(i0);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (i0 + k * 32 >= w1) break;
+        const uint32_t d = digit(i0 + k * 32 + lane, v[k]);
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        if (d < kBins) dst[off[warp][d] + __popc(same & below)] = v[k];
+        __syncwarp();
+        if (d < kBins && !(same & below)) off[warp][d] += __popc(same);
+        __syncwarp();
+      }
     }
     tc::cluster_sync_all();  // (releases and acquires the places, too)
     src = dst;
@@ -168,34 +190,51 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
 }
 static_assert(kBins == 512, "the barrier of the threads that have a digit");
 
-// This thread's pieces of the rows, `threads` threads to a row: 16 bytes as dW has them.
+// Row v of dW as zeros or the base's, by `threads` threads (this is the t-th): pieces of 16
+// bytes as dW has them.
 template <bool BASE>
-__device__ __forceinline__ void fill_rows(const SortParams &p, int64_t thread, int64_t threads) {
+__device__ __forceinline__ void write_row(const SortParams &p, int64_t v, int t, int threads) {
   constexpr int U = 4;  // pieces read before the first is stored
-  const int64_t row_threads = p.fill_rows == 1 ? threads : 1ll << p.log_threads;
-  for (int64_t v = thread / row_threads; v < p.fill_rows; v += threads / row_threads) {
-    uint8_t *to = p.dweight + v * p.ldw;
-    const uint8_t *from = BASE ? p.base + v * p.ldb : nullptr;
-    const int64_t first = -(int64_t)(reinterpret_cast<uintptr_t>(to) & 15);
-    for (int64_t b0 = first + (thread % row_threads) * 16; b0 < p.bytes; b0 += row_threads * 16 * U) {
-      uint4 x[U];
+  uint8_t *to = p.dweight + v * p.ldw;
+  const uint8_t *from = BASE ? p.base + v * p.ldb : nullptr;
+  const int64_t first = -(int64_t)(reinterpret_cast<uintptr_t>(to) & 15);
+  for (int64_t b0 = first + t * 16; b0 < p.bytes; b0 += threads * 16 * U) {
+    RowPiece<2> x[U];
+    const auto whole = [&](int64_t b) { return b >= 0 && b + 16 <= p.bytes; };
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int64_t b = b0 + k * row_threads * 16;
-        x[k] = make_uint4(0, 0, 0, 0);
-        if (BASE && b >= 0 && b + 16 <= p.bytes) x[k] = row_piece<2>(from, p.bytes, b);
-      }
+    for (int k = 0; k < U; ++k) {
+      const int64_t b = b0 + k * threads * 16;
+      if (BASE && whole(b)) x[k].load(from, p.bytes, b);
+    }
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int64_t b = b0 + k * row_threads * 16;
-        if (b >= 0 && b + 16 <= p.bytes) {
-          *reinterpret_cast<uint4 *>(to + b) = x[k];
-        } else {  // a row's ends
-          for (int64_t e = max(b, (int64_t)0); e < min(b + 16, p.bytes); e += 2)
-            *reinterpret_cast<uint16_t *>(to + e) = BASE ? *reinterpret_cast<const uint16_t *>(from + e) : (uint16_t)0;
-        }
+    for (int k = 0; k < U; ++k) {
+      const int64_t b = b0 + k * threads * 16;
+      if (whole(b)) {
+        *reinterpret_cast<uint4 *>(to + b) = BASE ? x[k].value(from, p.bytes, b) : make_uint4(0, 0, 0, 0);
+      } else {  // a row's ends
+        for (int64_t e = max(b, (int64_t)0); e < min(b + 16, p.bytes); e += 2)
+          *reinterpret_cast<uint16_t *>(to + e) = BASE ? *reinterpret_cast<const uint16_t *>(from + e) : (uint16_t)0;
       }
     }
+  }
+}
+// Threads to a row: a power of two, up to 256, with up to four pieces each.
+__device__ __forceinline__ int log_row_threads(int64_t bytes) {
+  int n = 0;
+  while (n < 8 && (64ll << n) < bytes + 15) ++n;
+  return n;
+}
+// All rows, by `threads` threads, of which this is one.
+__device__ __forceinline__ void write_rows(const SortParams &p, int64_t thread, int64_t threads) {
+  if (p.fill_rows == 1) {
+    if (p.base) write_row<true>(p, 0, (int)thread, (int)threads);
+    else write_row<false>(p, 0, (int)thread, (int)threads);
+    return;
+  }
+  const int log_threads = log_row_threads(p.bytes), t = (int)thread & ((1 << log_threads) - 1);
+  for (int64_t v = thread >> log_threads; v < p.fill_rows; v += threads >> log_threads) {
+    if (p.base) write_row<true>(p, v, t, 1 << log_threads);
+    else write_row<false>(p, v, t, 1 << log_threads);
   }
 }
 
@@ -208,18 +247,14 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortPara
     sort_places(p, sort_smem);
     return;
   }
-  const int64_t thread = (int64_t)(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x;
-  const int64_t threads = (int64_t)(gridDim.x - kSortCtas) * kSortThreads;
-  if (p.base) fill_rows<true>(p, thread, threads);
-  else fill_rows<false>(p, thread, threads);
+  write_rows(p, (int64_t)(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x,
+             (int64_t)(gridDim.x - kSortCtas) * kSortThreads);
 }
 // The rows alone, where there are no places.
-__global__ void __launch_bounds__(kSortThreads) embed_fill_kernel(const SortParams p) {
+__global__ void __launch_bounds__(256) embed_rows_kernel(const SortParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t thread = (int64_t)blockIdx.x * kSortThreads + threadIdx.x, threads = (int64_t)gridDim.x * kSortThreads;
-  if (p.base) fill_rows<true>(p, thread, threads);
-  else fill_rows<false>(p, thread, threads);
+  write_rows(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 // ---------------------------------------------------------------- sums
@@ -231,8 +266,9 @@ struct SumParams {
                         // [1 ...] those chunks, in any order
   int chunk, chunks;
   int log_threads;
+  int across;           // blocks for all chunks of a slab of columns
 };
-constexpr int kMinLogThreads = 3, kMaxChunk = 32;
+constexpr int kMinLogThreads = 3, kMaxChunk = 32, kGroupPlaces = kMaxChunk + 2;
 
 template <int TW, int E>
 __device__ __forceinline__ void write_sum(const EmbedBwdArgs &a, int64_t token, int j, const float (&sum)[E]) {
@@ -247,25 +283,32 @@ __device__ __forceinline__ void write_sum(const EmbedBwdArgs &a, int64_t token, 
 
 // A chunk of places to a power of two of threads, a piece of the columns each.
 template <int TW, int TO, int E>
-__global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p) {
+__global__ void __launch_bounds__(256, 4) embed_sum_kernel(const SumParams p) {
   constexpr int U = TO == MM_F32 ? 4 : 8;  // rows read before the first is added
-  __shared__ uint2 places[(256 >> kMinLogThreads) * (kMaxChunk + 2)];
+  constexpr int kPlaces = (256 >> kMinLogThreads) * kGroupPlaces;
+  __shared__ uint32_t tokens[kPlaces];
+  __shared__ int64_t starts[kPlaces];  // of a place's row of dout
   pdl_launch_dependents();
   pdl_wait();
   const EmbedBwdArgs &a = p.a;
   const int threads = 1 << p.log_threads, t = threadIdx.x & (threads - 1), group = threadIdx.x >> p.log_threads;
-  const int chunk = (int)blockIdx.x * (256 >> p.log_threads) + group;
-  const int j = ((int)blockIdx.y * threads + t) * E;
-  const int rows = (int)a.rows, i0 = min(rows, chunk * p.chunk), n = min(rows - i0, p.chunk);
+  const int slab = (int)blockIdx.x / p.across;
+  const int chunk = ((int)blockIdx.x - slab * p.across) * (256 >> p.log_threads) + group;
+  const int j = (slab * threads + t) * E;
+  const int rows = (int)a.rows, i0 = (int)min((int64_t)rows, (int64_t)chunk * p.chunk), n = min(rows - i0, p.chunk);
   const uint32_t none = (uint32_t)a.vocab;
   // the places of the chunk, and its neighbours' tokens (or none)
-  uint2 *mine = places + group * (kMaxChunk + 2) + 1;
-  for (int i = t - 1; i <= n; i += threads)
-    mine[i] = i0 + i >= 0 && i0 + i < rows ? p.sorted[i0 + i] : make_uint2(none, 0);
+  uint32_t *mine = tokens + group * kGroupPlaces + 1;
+  int64_t *start = starts + group * kGroupPlaces + 1;
+  for (int i = t - 1; i <= n; i += threads) {
+    const uint2 s = i0 + i >= 0 && i0 + i < rows ? p.sorted[i0 + i] : make_uint2(none, 0);
+    mine[i] = s.x;
+    start[i] = (int64_t)s.y * a.lddo;
+  }
   __syncthreads();
   if (n <= 0 || j >= a.cols) return;
-  uint32_t token = mine[0].x;
-  bool from_before = mine[-1].x == token;
+  uint32_t token = mine[0];
+  bool from_before = mine[-1] == token;
   float sum[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = 0.f;
@@ -281,12 +324,11 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p) {
     Piece<TO, E> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i + u < n && mine[i + u].x != none)
-        v[u] = Piece<TO, E>::load(at<TO>(a.dout, (int64_t)mine[i + u].y * a.lddo + j));
+      if (i + u < n && mine[i + u] != none) v[u] = Piece<TO, E>::load(at<TO>(a.dout, start[i + u] + j));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i + u >= n) break;
-      const uint32_t next = mine[i + u].x;
+      const uint32_t next = mine[i + u];
       if (next != token) {
         leave(false);
         token = next;
@@ -299,7 +341,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p) {
       for (int e = 0; e < E; ++e) sum[e] += v[u].get(e);
     }
   }
-  leave(mine[n].x == token);
+  leave(mine[n] == token);
 }
 
 // Tokens whose places go past a chunk's end: their parts, 64 threads of V columns each a
@@ -362,17 +404,18 @@ mm_status embed_sums(const EmbedBwdArgs &a, SumParams p, LaunchCtx &ctx) {
   const int64_t pieces = whole ? a.cols / kE : a.cols;
   p.log_threads = kMinLogThreads;
   while (p.log_threads < 8 && (1ll << p.log_threads) < pieces) ++p.log_threads;
-  const int64_t groups = 256 >> p.log_threads;
-  const dim3 grid((unsigned)((p.chunks + groups - 1) / groups),
-                  (unsigned)((pieces + (1 << p.log_threads) - 1) >> p.log_threads));
+  const int64_t groups = 256 >> p.log_threads, slabs = (pieces + (1 << p.log_threads) - 1) >> p.log_threads;
+  p.across = (int)((p.chunks + groups - 1) / groups);
+  if (p.across * slabs >= 1 << 30) return set_error(MM_ERR_UNSUPPORTED, "too many blocks");
+  const dim3 grid((unsigned)(p.across * slabs));
   cudaError_t e = whole ? launch_pdl(embed_sum_kernel<TW, TO, kE>, grid, dim3(256), 0, ctx.stream, dim3(1), p)
                         : launch_pdl(embed_sum_kernel<TW, TO, 1>, grid, dim3(256), 0, ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch");
   count_operator_launch();
   if (p.chunks == 1) return MM_OK;
-  const int64_t columns = whole ? 256 : 64, slabs = (a.cols + columns - 1) / columns;
-  const int64_t across = std::max<int64_t>(1, std::min<int64_t>(p.chunks - 1, 8 * ctx.dev->info.sms / slabs));
-  e = launch_pdl(whole ? embed_join_kernel<TW, 4> : embed_join_kernel<TW, 1>, dim3((unsigned)across, (unsigned)slabs), dim3(256), 0, ctx.stream, dim3(1), p);
+  const int64_t columns = whole ? 256 : 64, join_slabs = (a.cols + columns - 1) / columns;
+  const int64_t across = std::max<int64_t>(1, std::min<int64_t>(p.chunks - 1, 8 * ctx.dev->info.sms / join_slabs));
+  e = launch_pdl(whole ? embed_join_kernel<TW, 4> : embed_join_kernel<TW, 1>, dim3((unsigned)across, (unsigned)join_slabs), dim3(256), 0, ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (join)");
   count_operator_launch();
   return MM_OK;
@@ -411,15 +454,15 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   f.bytes = a.cols * es;
   f.ldb = a.ldb * es;
   f.ldw = a.lddw * es;
-  f.fill_rows = a.base == a.dweight ? 0 : a.vocab;
-  if (a.lddw == a.cols && (!a.base || a.ldb == a.cols) && f.fill_rows) {  // one long row
+  f.vocab = f.fill_rows = a.vocab;
+  if (a.lddw == a.cols && (!a.base || a.ldb == a.cols)) {
     f.bytes *= a.vocab;
     f.fill_rows = 1;
   }
-  while (f.log_threads < 10 && (64ll << f.log_threads) < f.bytes) ++f.log_threads;
+  const bool fills = a.base != a.dweight;  // else only the touched rows
   if (a.rows == 0) {
-    if (!f.fill_rows) return MM_OK;
-    cudaError_t e = launch_pdl(embed_fill_kernel, dim3((unsigned)ctx.dev->info.sms), dim3(kSortThreads), 0, ctx.stream, dim3(1), f);
+    if (!fills) return MM_OK;
+    cudaError_t e = launch_pdl(embed_rows_kernel, dim3((unsigned)(8 * ctx.dev->info.sms)), dim3(256), 0, ctx.stream, dim3(1), f);
     if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (rows)");
     count_operator_launch();
     return MM_OK;
@@ -446,7 +489,7 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   });
   if (err != cudaSuccess) return cuda_error(err, "embedding_backward set-up");
   if (clusters < 1) return set_error(MM_ERR_UNSUPPORTED, "no cluster of CTAs fits on this device");
-  const int fill_ctas = f.fill_rows ? std::max(1, clusters - 1) * kSortCtas : 0;
+  const int row_ctas = fills ? std::max(1, clusters - 1) * kSortCtas : 0;
   void *scratch = nullptr;
   mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, 2 * pairs + list + (size_t)p.chunks * 2 * a.cols * sizeof(float), &scratch);
   if (st != MM_OK) return st;
@@ -458,11 +501,10 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   p.sorted = f.to;
   f.tokens = a.tokens;
   f.ti = a.ti;
-  f.vocab = a.vocab;
   f.rows = (int)a.rows;
   f.passes = 1;
   while (a.vocab >> (kDigit * f.passes)) ++f.passes;
-  cudaError_t e = launch_pdl(embed_sort_kernel, dim3((unsigned)(kSortCtas + fill_ctas)), dim3(kSortThreads), kSortSmem,
+  cudaError_t e = launch_pdl(embed_sort_kernel, dim3((unsigned)(kSortCtas + row_ctas)), dim3(kSortThreads), kSortSmem,
                              ctx.stream, dim3(kSortCtas), f);
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (sort)");
   count_operator_launch();

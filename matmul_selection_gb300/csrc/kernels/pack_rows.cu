@@ -21,13 +21,13 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const uint8_t *src, int6
   for (int64_t r = ((int64_t)blockIdx.x << (8 - log_threads)) + (threadIdx.x >> log_threads); r < rows; r += groups) {
     const uint8_t *from = src + r * ld;
     for (int64_t b0 = t * 16; b0 < ld16; b0 += threads * 16 * U) {
-      uint4 v[U];
+      RowPiece<1> v[U];
 #pragma unroll
       for (int k = 0; k < U; ++k)
-        if (b0 + k * threads * 16 < ld16) v[k] = row_piece<1>(from, bytes, b0 + k * threads * 16);
+        if (b0 + k * threads * 16 < ld16) v[k].load(from, bytes, b0 + k * threads * 16);
 #pragma unroll
       for (int k = 0; k < U; ++k)
-        if (b0 + k * threads * 16 < ld16) *reinterpret_cast<uint4 *>(dst + r * ld16 + b0 + k * threads * 16) = v[k];
+        if (b0 + k * threads * 16 < ld16) *reinterpret_cast<uint4 *>(dst + r * ld16 + b0 + k * threads * 16) = v[k].value(from, bytes, b0 + k * threads * 16);
     }
   }
 }

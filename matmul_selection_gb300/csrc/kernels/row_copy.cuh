@@ -19,25 +19,40 @@ __device__ __forceinline__ uint4 shifted_bytes(uint4 first, uint4 second, int sh
 }
 
 // Bytes b .. b + 15 of a row of `bytes`, zeros past its end.  Whole 16-byte words are
-// read where the two that hold a piece lie inside the row; else single elements of
-// ES bytes.
+// read where those that hold the piece lie inside the row; else single elements of ES
+// bytes.  load() reads the words and value() makes the piece, so that the reads of
+// several pieces can be issued before the first is waited for.
 template <int ES>
-__device__ __forceinline__ uint4 row_piece(const uint8_t *row, int64_t bytes, int64_t b) {
-  const int shift = (int)(reinterpret_cast<uintptr_t>(row + b) & 15);
-  if (shift == 0 && b + 16 <= bytes) return *reinterpret_cast<const uint4 *>(row + b);
-  if (b >= shift && b - shift + 32 <= bytes) {
-    const uint4 *at = reinterpret_cast<const uint4 *>(row + b - shift);
-    return shifted_bytes(at[0], at[1], shift);
+struct RowPiece {
+  uint4 first, second;
+  static __device__ __forceinline__ int shift_of(const uint8_t *row, int64_t b) {
+    return (int)(reinterpret_cast<uintptr_t>(row + b) & 15);
   }
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < 16; e += ES)
-    if (b + e < bytes) {
-      const uint32_t v = ES == 1 ? row[b + e] : *reinterpret_cast<const uint16_t *>(row + b + e);
-      w[e >> 2] |= v << (8 * (e & 3));
+  static __device__ __forceinline__ bool in_words(const uint8_t *row, int64_t bytes, int64_t b) {
+    const int shift = shift_of(row, b);
+    return b >= shift && b - shift + (shift ? 32 : 16) <= bytes;
+  }
+  __device__ __forceinline__ void load(const uint8_t *row, int64_t bytes, int64_t b) {
+    const int shift = shift_of(row, b);
+    const uint4 *at = reinterpret_cast<const uint4 *>(row + b - shift);
+    first = second = make_uint4(0, 0, 0, 0);
+    if (in_words(row, bytes, b)) {
+      first = at[0];
+      if (shift) second = at[1];
     }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+  }
+  __device__ __forceinline__ uint4 value(const uint8_t *row, int64_t bytes, int64_t b) const {
+    if (in_words(row, bytes, b)) return shifted_bytes(first, second, shift_of(row, b));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; e += ES)
+      if (b + e < bytes) {
+        const uint32_t v = ES == 1 ? row[b + e] : *reinterpret_cast<const uint16_t *>(row + b + e);
+        w[e >> 2] |= v << (8 * (e & 3));
+      }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
 
 }  // namespace
 }  // namespace mm
