@@ -170,9 +170,10 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
 // to the host: each kernel reads the count and lays out its own tiles.
 enum Mode { MODE_LSE, MODE_G, MODE_DX, MODE_DW };
 
-// Warp 0 copies, warp 1 issues MMAs, the others take tiles out: 16 where a tile leaves in
-// 16 bits (a product over few rows of K is all epilogue: 16 x 4096 x 32000, dW, 62 us
-// with 8), 8 where its rows' sums stay in registers or it is added to fp32 sums.
+// Warp 0 copies, warp 1 issues MMAs, the others take tiles out, eight a tile.  Where a
+// tile leaves in 16 bits there are 16, eight for each accumulator: products over few
+// rows of K are all epilogue, and what writes to memory in one half overlaps with what
+// is converted in the other (all 16 on one tile: converted, then written).
 constexpr int out_warps(int mode) { return mode == MODE_G || mode == MODE_DW ? 16 : 8; }
 constexpr int tile_threads(int mode) { return 64 + 32 * out_warps(mode); }
 constexpr int kErrCopy = 0xa01, kErrMma = 0xa02, kErrStore = 0xa03, kErrDrain = 0xa04;
@@ -350,14 +351,6 @@ __device__ __forceinline__ void fill_box(uint8_t *box, int tx, int h, const uint
         make_uint4(pack2(tx, f(8 * j), f(8 * j + 1)), pack2(tx, f(8 * j + 2), f(8 * j + 3)),
                    pack2(tx, f(8 * j + 4), f(8 * j + 5)), pack2(tx, f(8 * j + 6), f(8 * j + 7)));
 }
-// 64 columns of a tile in registers; then the accumulator is given back.
-template <typename F>
-__device__ __forceinline__ void take_columns(uint32_t tmem, uint32_t (&v)[2][32], F &&release) {
-  tmem_ld_32cols(tmem, v[0]);
-  tmem_ld_32cols(tmem + 32, v[1]);
-  tmem_ld_wait();
-  release();
-}
 __device__ __forceinline__ void store_box_tma(const CUtensorMap *map, uint8_t *box, int x, int y) {
   fence_proxy_async_smem();
   __syncwarp();
@@ -410,16 +403,16 @@ __device__ __forceinline__ void leave_dw(const TileParams &p, const CUtensorMap 
 }
 
 // Added to the pieces before; the layout has a lane's 16 bytes beside the next one's.
-__device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, const Unit &u, int row0, int c0, int c1,
+__device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, int n, int w, int split, int row0,
                                         bool empty) {
   const int lane = threadIdx.x & 31;
   if (empty && !p.first) return;
 #pragma unroll 1
-  for (int c = c0; c < c1; c += 32) {
-    const int cb = (u.n0 + c) >> 5;
+  for (int c = 0; c < w; c += 32) {
+    const int cb = (n + c) >> 5;
     if (cb >= p.acc_cols) break;
     float4 *to = reinterpret_cast<float4 *>(
-                     p.acc + (((int64_t)u.split * (p.r.rows_pad >> 5) + (row0 >> 5)) * p.acc_cols + cb) * 1024) + lane;
+                     p.acc + (((int64_t)split * (p.r.rows_pad >> 5) + (row0 >> 5)) * p.acc_cols + cb) * 1024) + lane;
     float4 sum[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum[k] = p.first ? make_float4(0.f, 0.f, 0.f, 0.f) : to[k * 32];
@@ -468,7 +461,7 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
-      mbar_init(tempty0 + 8 * a, R::kOut * CG);
+      mbar_init(tempty0 + 8 * a, 8 * CG);
     }
     mbar_init(drain, 1);
     mbar_init(stall, 1);
@@ -603,10 +596,13 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3, group = (warp - 2) >> 2;  // q: the TMEM lanes this warp may read
+    // q: the TMEM lanes this warp may read; half: its half of a tile's columns; team: of the
+    // two that take turns, each with an accumulator of its own
+    const int q = warp & 3, half = (warp - 2) >> 2 & 1, team = (warp - 2) >> 3;
+    constexpr int kTeams = R::kOut / 8;
     uint8_t *box = boxes + (warp - 2) * kBoxB;
     const float gain = MODE == MODE_DW ? *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f) : 0.f;
-    int acc = 0;
+    int acc = team;
     uint32_t acc_phase = 0;
     const auto release = [&] {  // the accumulator has been read
       fence_before();
@@ -615,18 +611,16 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
         if (CG == 2) mbar_arrive_cluster(leader_tempty0 + 8 * acc);
         else mbar_arrive(tempty0 + 8 * acc);
       }
-      if (++acc == 2) {
-        acc = 0;
+      if (kTeams == 2 || ++acc == 2) {
+        acc = team;
         acc_phase ^= 1;
       }
     };
     bool ok = true;
     int turn = 0;
-    for (int i = cid; i < tiles.total && ok; i += ncl, turn ^= 1) {
+    for (int i = cid + team * ncl; i < tiles.total && ok; i += kTeams * ncl, turn ^= 1) {
       const Unit u = unit_at(tiles, p.bn, i);
-      const int row0 = u.tm * 128 * CG + pos * 128 + q * 32;
-      // this warp's columns: half of the tile's, or 64 (a half tile has none for some)
-      const int wide = R::kOut == 8 ? u.w / 2 : 64, c0 = group * wide, n = u.n0 + c0;
+      const int row0 = u.tm * 128 * CG + pos * 128 + q * 32, wide = u.w / 2, c0 = half * wide, n = u.n0 + c0;
       const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
       if constexpr (MODE == MODE_LSE) {
         const bool live = row0 < rows && u.n0 < p.vocab;  // (else a half tile past the end)
@@ -645,25 +639,31 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
         if (live) {
           const int row = row0 + lane;
           sum = sum_exp(p, l, n, wide, target_of(p, row), p.hit + row);
-          if (group) *upper = sum;
+          if (half) *upper = sum;
         }
         all_take(true);
-        if (live && !group) p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row0 + lane] = join_sums(sum, *upper);
+        if (live && !half) p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row0 + lane] = join_sums(sum, *upper);
       } else {
         if (!warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)) break;
         fence_after();
-        const uint32_t tmem = lanes + (uint32_t)(acc * 256);
+        const uint32_t tmem = lanes + (uint32_t)(acc * 256 + c0);
         int kb0;
         if constexpr (MODE == MODE_DX) {
-          if (row0 < rows) take_dx(p, tmem, u, row0, c0, c0 + wide, k_of(u, kb0) == 0);
+          if (row0 < rows) take_dx(p, tmem, n, wide, u.split, row0, k_of(u, kb0) == 0);
           release();
-        } else if (c0 < u.w && n < (MODE == MODE_G ? p.width : p.cols) && (MODE == MODE_G || p.v0 + row0 < p.vocab)) {
-          uint32_t v[2][32];
-          take_columns(tmem + (uint32_t)c0, v, release);
-          if constexpr (MODE == MODE_G) leave_g(p, &tmO, v, n, row0, box);
-          else leave_dw(p, &tmO, v, n, p.v0 + row0, box, gain);
         } else {
-          release();
+          const int end = MODE == MODE_G ? p.width : p.v0 + row0 < p.vocab ? p.cols : 0;
+          const int left = min(wide, end - n);
+          if (left <= 0) release();
+          for (int c = 0; c < left; c += 64) {
+            uint32_t v[2][32];
+            tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
+            tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
+            tmem_ld_wait();
+            if (c + 64 >= left) release();
+            if constexpr (MODE == MODE_G) leave_g(p, &tmO, v, n + c, row0, box);
+            else leave_dw(p, &tmO, v, n + c, p.v0 + row0, box, gain);
+          }
         }
       }
     }
