@@ -44,8 +44,10 @@ __device__ __forceinline__ float exp2_fast(float v) {
 // ---------------------------------------------------------------- the rows that count
 // Where each call's scratch holds what; i: a row among those that count, of
 // `rows_pad`, a multiple of 256.
+// Few rows that TMA reads as they lie are not gathered (they are one row tile whether or
+// not all count): count is null then, i is the row itself, and there are only gain and x.
 struct Rows {
-  int *count;       // [0] the rows that count
+  int *count;       // [0] the rows that count, or null
   float *gain;      // largest |dloss|
   int *slot;        // [rows] i of a row, or -1
   int *row;         // [rows] the row of an i
@@ -57,11 +59,20 @@ struct Rows {
   int rows_pad;
 };
 
+__device__ __forceinline__ float abs_weight(const float *dloss, int64_t i) { return dloss ? fabsf(dloss[i]) : 1.f; }
+constexpr float kLargestFinite = 3.402823466e38f;
+// What g's rows are multiplied by.
+__device__ __forceinline__ float ratio_of(const float *dloss, int64_t i, float gain, int tx) {
+  return (dloss ? dloss[i] : 1.f) / gain * (tx == MM_F16 ? kF16Gain : 1.f);
+}
+
 struct GatherParams {
   LossArgs a;
   Rows r;
   int backward;
   int log_threads;  // threads a row
+  int blocks;       // that gather; those after them copy
+  PackRows pack;    // W, where TMA cannot read it as it lies
 };
 
 __device__ __forceinline__ int valid_target(const LossArgs &a, int64_t t) {
@@ -71,7 +82,8 @@ __device__ __forceinline__ int valid_target(const LossArgs &a, int64_t t) {
 
 // Each block has an equal share of the rows and counts the rows that count before its
 // own (and, backward, finds the largest |dloss| of all) for itself: a few KB from L2
-// instead of another kernel.  Rows move in 16-byte pieces, wherever they start.
+// instead of another kernel.  Rows move in 16-byte pieces, wherever they start.  W is
+// copied by the same launch where it has to be.
 constexpr int kGatherThreads = 512, kGatherWarps = kGatherThreads / 32;
 __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherParams p) {
   pdl_launch_dependents();
@@ -81,17 +93,21 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
   __shared__ int at_row[kGatherThreads];  // the source row of the k-th that counts
   const LossArgs &a = p.a;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int r0 = (int)((int64_t)a.rows * blockIdx.x / gridDim.x);
-  const int r1 = (int)((int64_t)a.rows * (blockIdx.x + 1) / gridDim.x);
+  if ((int)blockIdx.x >= p.blocks) {
+    pack_rows(p.pack, ((int64_t)blockIdx.x - p.blocks) * kGatherThreads + t, ((int64_t)gridDim.x - p.blocks) * kGatherThreads);
+    return;
+  }
+  const int r0 = (int)((int64_t)a.rows * blockIdx.x / p.blocks);
+  const int r1 = (int)((int64_t)a.rows * (blockIdx.x + 1) / p.blocks);
   int before = 0;
   float top = 0.f;  // of the finite ones
   const int look = p.backward ? a.rows : r0;
 #pragma unroll 4
   for (int i = t; i < look; i += kGatherThreads) {
     const int target = valid_target(a, i);
-    const float d = p.backward && a.dloss ? fabsf(a.dloss[i]) : 1.f;
+    const float d = abs_weight(p.backward ? a.dloss : nullptr, i);
     before += target >= 0 && i < r0;
-    if (target >= 0 && d <= 3.402823466e38f) top = fmaxf(top, d);
+    if (target >= 0 && d <= kLargestFinite) top = fmaxf(top, d);
   }
   before = __reduce_add_sync(0xffffffffu, before);
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -120,8 +136,7 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
       p.r.row[before + at] = i;
       p.r.target[before + at] = target;
       if (p.backward) {
-        const float d = a.dloss ? a.dloss[i] : 1.f;
-        p.r.ratio[before + at] = d / top * (a.tx == MM_F16 ? kF16Gain : 1.f);
+        p.r.ratio[before + at] = ratio_of(a.dloss, i, top, a.tx);
         p.r.lse2[before + at] = a.lse[i] * kLog2e;
       }
     }
@@ -145,7 +160,7 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
     before += total;
     __syncthreads();
   }
-  if (blockIdx.x == gridDim.x - 1) {
+  if ((int)blockIdx.x == p.blocks - 1) {
     if (t == 0) *p.r.count = before, *p.r.gain = top;
     const int end = max(1, (before + kRowTile - 1) / kRowTile) * kRowTile;
     for (int i = before + t; i < end; i += kGatherThreads) {
@@ -174,63 +189,73 @@ enum Mode { MODE_LSE, MODE_G, MODE_DX, MODE_DW };
 // tile leaves in 16 bits there are 16, eight for each accumulator: products over few
 // rows of K are all epilogue, and what writes to memory in one half overlaps with what
 // is converted in the other (all 16 on one tile: converted, then written).
-constexpr int out_warps(int mode) { return mode == MODE_G || mode == MODE_DW ? 16 : 8; }
-constexpr int tile_threads(int mode) { return 64 + 32 * out_warps(mode); }
+constexpr int out_warps(int mode, int cg) { return cg == 2 && (mode == MODE_G || mode == MODE_DW) ? 16 : 8; }
+constexpr int tile_threads(int mode, int cg) { return 64 + 32 * out_warps(mode, cg); }
 constexpr int kErrCopy = 0xa01, kErrMma = 0xa02, kErrStore = 0xa03, kErrDrain = 0xa04;
 constexpr int kGroupRows = 8;  // row tiles walked together, so that their operands stay in L2
 
-// How the tiles of a product are walked: grouped by row tiles; those of a last wave
-// that fills at most half the places (all, where there are so few) as two halves.
+// How the tiles of a product are walked: grouped by row tiles.  Those of a last wave that
+// does not fill the places are cut: in two halves where they fill at most half of them
+// (or there are no more), or, in DX, whose K is long, in as many parts of K as fit.
 struct Tiles {
-  int tiles_m, tiles_n, full, total;
+  int tiles_m, tiles_n, full, parts, total;
+  bool cut_k;
 };
-__device__ __forceinline__ Tiles tiles_of(int M, int tile_m, int tiles_n, int splits, int bn, int places) {
+__device__ __forceinline__ Tiles tiles_of(int M, int tile_m, int tiles_n, int bn, int places, int max_parts = 0) {
   Tiles s;
   s.tiles_m = (M + tile_m - 1) / tile_m;
   s.tiles_n = tiles_n;
-  const int tiles = s.tiles_m * tiles_n * splits, rem = tiles % places;
-  const bool halve = bn == 256 && rem > 0 && 2 * rem <= places;
-  s.full = halve ? tiles - rem : tiles;
-  s.total = halve ? tiles + rem : tiles;
+  s.cut_k = max_parts > 0;
+  const int tiles = s.tiles_m * tiles_n, rem = tiles % places;
+  s.parts = rem == 0 ? 1 : s.cut_k ? max(1, min(places / rem, max_parts)) : bn == 256 && 2 * rem <= places ? 2 : 1;
+  s.full = s.parts > 1 ? tiles - rem : tiles;
+  s.total = s.full + (tiles - s.full) * s.parts;
   return s;
 }
 struct Unit {
-  int tm, n0, w, split;
+  int tm, n0, w, part;
 };
 __device__ __forceinline__ Unit unit_at(const Tiles &s, int bn, int u) {
-  int t = u, half = -1;
-  if (u >= s.full) t = s.full + ((u - s.full) >> 1), half = (u - s.full) & 1;
   Unit x;
-  const int area = s.tiles_m * s.tiles_n;
-  x.split = t / area;
-  t -= x.split * area;
+  int t = u;
+  x.part = 0;
+  const bool cut = u >= s.full;
+  if (cut) t = s.full + (u - s.full) / s.parts, x.part = (u - s.full) % s.parts;
   const int per = kGroupRows * s.tiles_n, g = t / per, rows = min(kGroupRows, s.tiles_m - g * kGroupRows);
   const int r = t - g * per;
   x.tm = g * kGroupRows + r % rows;
-  x.n0 = (r / rows) * bn + (half > 0 ? bn / 2 : 0);
-  x.w = half < 0 ? bn : bn / 2;
+  x.n0 = (r / rows) * bn;
+  x.w = bn;
+  if (cut && !s.cut_k) x.w = bn / 2, x.n0 += x.part * x.w;
   return x;
 }
-// Whether tile (tm, tn) of split 0 is walked as halves.
-__device__ __forceinline__ bool halved(const Tiles &s, int tm, int tn) {
+// The place of tile (tm, tn) in the walk.
+__device__ __forceinline__ int tile_at(const Tiles &s, int tm, int tn) {
   const int g = tm / kGroupRows, rows = min(kGroupRows, s.tiles_m - g * kGroupRows);
-  return g * kGroupRows * s.tiles_n + tn * rows + tm - g * kGroupRows >= s.full;
+  return g * kGroupRows * s.tiles_n + tn * rows + tm - g * kGroupRows;
 }
+// DX: parts of at least eight blocks of K.
+__device__ __forceinline__ int max_parts_of(int piece_kb) { return max(1, piece_kb / 8); }
 
 struct TileParams {
   Rows r;
-  const void *targets;  // LSE of few rows: x as it lies (r.count null), `rows` of it
+  const void *x, *targets;  // where r.count is null: x as it lies, `rows` of it ...
+  const float *lse, *dloss;
+  int64_t ldx;
   int ti, rows;
   int cols, vocab;
   int v0, width;     // the piece of the vocabulary: its first token, how many (G: padded to 64)
   int tx;
-  int bn, tiles_n, splits, places;
+  int bn, tiles_n, places;
   int num_kb;        // 64-element blocks of K (DW: of the rows that count)
-  int kb_per_split;  // DX
+  int piece_kb;      // DX: those of a whole piece
   float2 *part;      // LSE: [128 of the vocabulary][rows_pad] (r, s)
   float *hit;        // LSE: [rows_pad] the target's logit
-  float *acc;        // DX: [split][32 rows][32 columns][4 columns][row]
-  int acc_cols;      // DX: blocks of 32 columns
+  // DX: blocks of 32 rows by 32 columns, each [4 columns][row][column]: the whole tiles'
+  // [row block][acc_cols], then, from acc_cut on, [unit][row block][column block] of those
+  // that are cut in parts
+  float *acc, *acc_cut;
+  int acc_cols;
   int first;         // DX: the first piece
   uint16_t *dw;
   int64_t lddw;
@@ -244,8 +269,8 @@ struct TileParams {
 template <int MODE, int CG>
 struct Ring {
   static constexpr uint32_t kA = 128 * 128, kStageB = kA + (CG == 2 ? 128 : 256) * 128;
-  static constexpr int kOut = out_warps(MODE);
-  static constexpr int kStages = CG == 2 ? (kOut == 16 ? 5 : 6) : kOut == 16 ? 3 : 4;
+  static constexpr int kOut = out_warps(MODE, CG);
+  static constexpr int kStages = CG == 1 ? 4 : kOut == 16 ? 5 : 6;
   static constexpr uint32_t kBoxes = kOut * kBoxB;  // (LSE: sums)
   static constexpr size_t kSmem = kStages * kStageB + kBoxes + 1024 + 256;
 };
@@ -359,10 +384,15 @@ __device__ __forceinline__ void store_box_tma(const CUtensorMap *map, uint8_t *b
 
 // G, DW: columns n .. n + 63 of the product's rows row0 .. row0 + 31.
 __device__ __forceinline__ void leave_g(const TileParams &p, const CUtensorMap *map, uint32_t (&v)[2][32], int n, int row0,
-                                        uint8_t *box) {
+                                        uint8_t *box, float gain) {
   const int row = row0 + (threadIdx.x & 31);
-  const int target = p.r.target[row];
-  const float ratio = p.r.ratio[row], lse2 = p.r.lse2[row];
+  const int target = target_of(p, row);
+  float ratio = 0.f, lse2 = 0.f;
+  if (p.r.count) {
+    ratio = p.r.ratio[row], lse2 = p.r.lse2[row];
+  } else if (target >= 0) {
+    ratio = ratio_of(p.dloss, row, gain, p.tx), lse2 = p.lse[row] * kLog2e;
+  }
   const bool live = ratio != 0.f;  // (a weight of 0 takes its row out, whatever its logits)
   wait_box();
 #pragma unroll
@@ -402,17 +432,14 @@ __device__ __forceinline__ void leave_dw(const TileParams &p, const CUtensorMap 
   }
 }
 
-// Added to the pieces before; the layout has a lane's 16 bytes beside the next one's.
-__device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, int n, int w, int split, int row0,
-                                        bool empty) {
+// Added to the pieces before: w columns of 32 rows, blocks of 32 x 32 from `acc` on, laid
+// out so that a lane's 16 bytes lie beside the next one's.
+__device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, float *acc, int w, bool empty) {
   const int lane = threadIdx.x & 31;
   if (empty && !p.first) return;
 #pragma unroll 1
   for (int c = 0; c < w; c += 32) {
-    const int cb = (n + c) >> 5;
-    if (cb >= p.acc_cols) break;
-    float4 *to = reinterpret_cast<float4 *>(
-                     p.acc + (((int64_t)split * (p.r.rows_pad >> 5) + (row0 >> 5)) * p.acc_cols + cb) * 1024) + lane;
+    float4 *to = reinterpret_cast<float4 *>(acc + c * 32) + lane;
     float4 sum[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum[k] = p.first ? make_float4(0.f, 0.f, 0.f, 0.f) : to[k * 32];
@@ -430,8 +457,35 @@ __device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, int 
   }
 }
 
+// What the gather does, for few rows that stay where they lie, by the warps that take
+// tiles out while they wait for the first one: the largest |dloss| (for each CTA by
+// itself), and this CTA's share of x with zeros for the rows that do not count, which dW's
+// product adds up times g's zeros (they may hold anything).
+__device__ __forceinline__ float prepare_few(const TileParams &p, int cta, int ctas, int t) {
+  const int lane = t & 31;
+  float top = 0.f;
+  for (int i = lane; i < p.rows; i += 32)
+    if (target_of(p, i) >= 0) {
+      const float d = abs_weight(p.dloss, i);
+      if (d <= kLargestFinite) top = fmaxf(top, d);
+    }
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (top == 0.f) top = 1.f;
+  if (cta == 0 && t == 0) *p.r.gain = top;
+  const int pieces = (int)(p.r.ldx / 8), rows = (p.rows + 63) / 64 * 64;
+  for (int i = cta * 256 + t; i < rows * pieces; i += ctas * 256) {
+    const int row = i / pieces, c = i - row * pieces;
+    RowPiece<2> v;
+    const uint8_t *from = static_cast<const uint8_t *>(p.x) + (int64_t)row * p.ldx * 2;
+    const bool live = target_of(p, row) >= 0;
+    if (live) v.load(from, (int64_t)p.cols * 2, (int64_t)c * 16);
+    reinterpret_cast<uint4 *>(p.r.x)[i] = live ? v.value(from, (int64_t)p.cols * 2, (int64_t)c * 16) : make_uint4(0, 0, 0, 0);
+  }
+  return top;
+}
+
 template <int MODE, int CG>
-__global__ void __launch_bounds__(tile_threads(MODE), 1)
+__global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmO,
                 const TileParams p) {
@@ -477,7 +531,7 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
   if (CG == 1 && !kMnB && warp == 0 && lane == 0) {
     // few rows: the first blocks of W into L2 while the rows are gathered (one row tile,
     // so the first unit does not depend on their count)
-    const Tiles tiles = tiles_of(1, 128, p.tiles_n, 1, p.bn, p.places);
+    const Tiles tiles = tiles_of(1, 128, p.tiles_n, p.bn, p.places);
     if (cid < tiles.total) {
       const Unit u = unit_at(tiles, p.bn, cid);
       for (int kb = 0; kb < min(p.num_kb, 8); ++kb) tma_prefetch_2d(u.w == p.bn ? &tmB : &tmBh, kb * 64, u.n0);
@@ -493,12 +547,16 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
   const uint32_t leader_tempty0 = CG == 2 ? map_to_rank(tempty0, 0) : tempty0;
   pdl_wait();
   const int rows = row_count(p.r, p.rows);
-  const Tiles tiles = tiles_of(MODE == MODE_DW ? p.width : rows, 128 * CG, p.tiles_n, p.splits, p.bn, p.places);
+  const Tiles tiles = tiles_of(MODE == MODE_DW ? p.width : rows, 128 * CG, p.tiles_n, p.bn, p.places,
+                               MODE == MODE_DX ? max_parts_of(p.piece_kb) : 0);
   const int num_kb = MODE == MODE_DW ? (rows + 63) / 64 : p.num_kb;
   // the blocks of K of a unit
-  const auto k_of = [&](const Unit &u, int &kb0) {
-    kb0 = u.split * p.kb_per_split;
-    return MODE == MODE_DX ? max(0, min(p.kb_per_split, num_kb - kb0)) : num_kb;
+  const auto k_of = [&](const Unit &u, int i, int &kb0) {
+    kb0 = 0;
+    if (MODE != MODE_DX || i < tiles.full) return num_kb;
+    const int per = (num_kb + tiles.parts - 1) / tiles.parts;
+    kb0 = u.part * per;
+    return max(0, min(per, num_kb - kb0));
   };
 
   if (warp == 0) {
@@ -508,7 +566,7 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
     for (int i = cid; i < tiles.total && ok; i += ncl) {
       const Unit u = unit_at(tiles, p.bn, i);
       int kb0;
-      const int nk = k_of(u, kb0), nh = u.w / CG, m0 = u.tm * 128 * CG + pos * 128, n0 = u.n0 + pos * nh;
+      const int nk = k_of(u, i, kb0), nh = u.w / CG, m0 = u.tm * 128 * CG + pos * 128, n0 = u.n0 + pos * nh;
       for (int kb = kb0; kb < kb0 + nk; ++kb) {
         if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.wait, kErrCopy)) {
           ok = false;
@@ -552,7 +610,7 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
       for (int i = cid; i < tiles.total && ok; i += ncl) {
         const Unit u = unit_at(tiles, p.bn, i);
         int kb0;
-        const int nk = k_of(u, kb0);
+        const int nk = k_of(u, i, kb0);
         const uint32_t idesc = instr_desc(p.tx == MM_BF16, 128 * CG, (uint32_t)u.w) | (kMnA ? kMnMajorA : 0u) |
                                (kMnB ? kMnMajorB : 0u);
         uint32_t d = 0;
@@ -601,7 +659,9 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
     const int q = warp & 3, half = (warp - 2) >> 2 & 1, team = (warp - 2) >> 3;
     constexpr int kTeams = R::kOut / 8;
     uint8_t *box = boxes + (warp - 2) * kBoxB;
-    const float gain = MODE == MODE_DW ? *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f) : 0.f;
+    float gain = 0.f;
+    if (MODE == MODE_DW) gain = *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
+    if (MODE == MODE_G && CG == 1 && !p.r.count) gain = prepare_few(p, cid, ncl, (int)threadIdx.x - 64);
     int acc = team;
     uint32_t acc_phase = 0;
     const auto release = [&] {  // the accumulator has been read
@@ -649,7 +709,13 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
         const uint32_t tmem = lanes + (uint32_t)(acc * 256 + c0);
         int kb0;
         if constexpr (MODE == MODE_DX) {
-          if (row0 < rows) take_dx(p, tmem, n, wide, u.split, row0, k_of(u, kb0) == 0);
+          // (columns past cols stay unwritten: nothing reads them)
+          const int w = min(wide, (p.cols - n + 31) / 32 * 32);
+          float *acc_at =
+              i < tiles.full ? p.acc + ((int64_t)(row0 >> 5) * p.acc_cols + (n >> 5)) * 1024
+                             : p.acc_cut + (int64_t)(i - tiles.full) * (128 * CG * p.bn) +
+                                   ((pos * 4 + q) * (p.bn / 32) + c0 / 32) * 1024;
+          if (row0 < rows && w > 0) take_dx(p, tmem, acc_at, w, k_of(u, i, kb0) == 0);
           release();
         } else {
           const int end = MODE == MODE_G ? p.width : p.v0 + row0 < p.vocab ? p.cols : 0;
@@ -661,7 +727,7 @@ __global__ void __launch_bounds__(tile_threads(MODE), 1)
             tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
             tmem_ld_wait();
             if (c + 64 >= left) release();
-            if constexpr (MODE == MODE_G) leave_g(p, &tmO, v, n + c, row0, box);
+            if constexpr (MODE == MODE_G) leave_g(p, &tmO, v, n + c, row0, box, gain);
             else leave_dw(p, &tmO, v, n + c, p.v0 + row0, box, gain);
           }
         }
@@ -709,7 +775,7 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) 
     return valid_target(p.a, i) < 0 ? -1 : (int)i;
   };
   const int slot = row < p.a.rows ? slot_of(row) : -1;
-  const Tiles tiles = tiles_of(row_count(p.r, p.a.rows), p.tile_m, p.tiles_n, 1, p.bn, p.places);
+  const Tiles tiles = tiles_of(row_count(p.r, p.a.rows), p.tile_m, p.tiles_n, p.bn, p.places);
   const float2 none = make_float2(-3e38f, 0.f);
   float2 sum = none;
   if (slot >= 0) {
@@ -723,7 +789,7 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) 
         const int i = i0 + u * Y;
         const float2 *part = p.part + (int64_t)i * per * p.r.rows_pad + slot;
         v[u][0] = i < p.tiles_n ? part[0] : none;
-        v[u][1] = i < p.tiles_n && per == 2 && i * 256 + 128 < p.a.vocab && halved(tiles, slot / p.tile_m, i)
+        v[u][1] = i < p.tiles_n && per == 2 && i * 256 + 128 < p.a.vocab && tile_at(tiles, slot / p.tile_m, i) >= tiles.full
                       ? part[p.r.rows_pad]
                       : none;
       }
@@ -751,38 +817,48 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) 
 struct DxParams {
   LossArgs a;
   Rows r;
-  const float *acc;
-  int acc_cols, splits;
+  const float *acc, *acc_cut;
+  int tile_m, bn, tiles_n, places, piece_kb, acc_cols;  // of the product
   int vec;  // dx's rows start on 16 bytes
 };
-// A warp 32 rows by 4 Q columns, a row a lane: the splits added in order, scaled and
-// rounded.  Then the rows that do not count.  Q: 8 (64 bytes of a row), or 2 where
-// there are splits, and few rows: more warps (16 rows of 4096 in 9 splits: 12.7 us
-// with 8).
+// A warp 32 rows by 4 Q columns, a row a lane: a tile's parts added in order, scaled and
+// rounded.  Then the rows that do not count.  Q: 8 (64 bytes of a row), or 2 where the
+// tiles are few, and cut in many parts: more warps (16 rows of 4096 in 9 parts: 12.7 us
+// with 8, 5.2 with 2).  Neighbouring warps take neighbouring blocks of the sums, and the
+// whole tiles' lie row block by row block: 36 us at 6144 x 4096 (tile by tile 55; a
+// tile's columns a warp, accesses 32 KB apart, 200).
 template <int Q>
-__global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
+__global__ void __launch_bounds__(256, Q == 8 ? 3 : 4) dx_kernel(const DxParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int U = Q == 8 ? 1 : 4;  // splits read at once
-  const int lane = threadIdx.x & 31, count = *p.r.count;
+  constexpr int U = Q == 8 ? 1 : 4;  // parts read at once
+  const int lane = threadIdx.x & 31, count = row_count(p.r, p.a.rows);
   const float gain = *p.r.gain * (p.a.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
-  const int64_t warps = (int64_t)gridDim.x * 8, warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t warps = gridDim.x * 8, warp = blockIdx.x * 8 + (threadIdx.x >> 5);
   uint16_t *dx = static_cast<uint16_t *>(p.a.dx);
-  const int64_t split_at = (int64_t)p.r.rows_pad * p.acc_cols * 8;  // float4 a split
-  const int across = p.acc_cols * (8 / Q);
-  for (int64_t b = warp; b < (int64_t)((count + 31) / 32) * across; b += warps) {
-    const int rb = (int)(b / across), col = (int)(b - (int64_t)rb * across) * 4 * Q;
-    const float4 *from = reinterpret_cast<const float4 *>(p.acc) + b * 32 * Q + lane;
+  const Tiles tiles = tiles_of(count, p.tile_m, p.tiles_n, p.bn, p.places, max_parts_of(p.piece_kb));
+  const int log_rows = p.tile_m == 256 ? 3 : 2, log_cols = p.bn == 256 ? 3 : 2;  // blocks of 32 a tile
+  const uint32_t across = (uint32_t)(p.a.cols + 4 * Q - 1) / (4 * Q);
+  const int64_t part_at = (int64_t)p.tile_m * p.bn / 4;  // float4 a unit
+  // (as many blocks as there are 4 KB or 1 KB of sums: they count in 32 bits)
+  for (uint32_t b = warp; b < (uint32_t)((count + 31) / 32) * across; b += warps) {
+    const int rb = (int)(b / across), col = (int)(b - (uint32_t)rb * across) * 4 * Q, cb = col / 32;
+    const int t = tile_at(tiles, rb >> log_rows, cb >> log_cols);
+    const int parts = t < tiles.full ? 1 : tiles.parts;
+    const int block = ((rb & ((1 << log_rows) - 1)) << log_cols) + (cb & ((1 << log_cols) - 1));
+    const float *at = t < tiles.full ? p.acc + ((int64_t)rb * p.acc_cols + cb) * 1024
+                                     : p.acc_cut + (int64_t)(t - tiles.full) * parts * p.tile_m * p.bn + block * 1024;
+    const float4 *from = reinterpret_cast<const float4 *>(at) + col % 32 * 8 + lane;
     float4 v[Q];
 #pragma unroll
     for (int k = 0; k < Q; ++k) v[k] = from[k * 32];
-    for (int s = 1; s < p.splits; s += U) {
+    for (int s = 1; s < parts; s += U) {
       float4 w[U][Q];
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < Q; ++k)
-          w[u][k] = s + u < p.splits ? from[(s + u) * split_at + k * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
+          w[u][k] = s + u < parts ? from[(s + u) * part_at + k * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -790,14 +866,14 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
           v[k].x += w[u][k].x, v[k].y += w[u][k].y, v[k].z += w[u][k].z, v[k].w += w[u][k].w;
     }
     const int i = rb * 32 + lane;
-    if (i >= count) continue;
+    if (i >= count || (!p.r.count && valid_target(p.a, i) < 0)) continue;
     uint32_t w[2 * Q];
 #pragma unroll
     for (int k = 0; k < Q; ++k) {
       w[2 * k] = pack2(p.a.tx, v[k].x * gain, v[k].y * gain);
       w[2 * k + 1] = pack2(p.a.tx, v[k].z * gain, v[k].w * gain);
     }
-    uint16_t *to = dx + (int64_t)p.r.row[i] * p.a.lddx + col;
+    uint16_t *to = dx + (int64_t)(p.r.count ? p.r.row[i] : i) * p.a.lddx + col;
     const int left = p.a.cols - col;
     if (p.vec && left >= 4 * Q) {
 #pragma unroll
@@ -810,7 +886,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
     }
   }
   for (int64_t row = warp; row < p.a.rows; row += warps)
-    if (p.r.slot[row] < 0)
+    if (p.r.count ? p.r.slot[row] < 0 : valid_target(p.a, row) < 0)
       for (int c = lane; c < p.a.cols; c += 32) dx[row * p.a.lddx + c] = 0;
 }
 
@@ -826,13 +902,17 @@ struct Cut {
   }
 };
 
-Rows cut_rows(Cut &cut, const LossArgs &a, bool backward) {
+Rows cut_rows(Cut &cut, const LossArgs &a, bool backward, bool direct) {
   Rows r;
   std::memset(&r, 0, sizeof r);
   r.rows_pad = (a.rows + kRowTile - 1) / kRowTile * kRowTile;
   r.ldx = ((int64_t)a.cols + 7) / 8 * 8;
-  r.count = cut.take<int>(1);
   r.gain = cut.take<float>(1);
+  if (direct) {
+    if (backward) r.x = cut.take<uint16_t>(128 * r.ldx);
+    return r;
+  }
+  r.count = cut.take<int>(1);
   r.slot = cut.take<int>(a.rows);
   r.row = cut.take<int>(a.rows);
   r.target = cut.take<int>(r.rows_pad);
@@ -844,11 +924,12 @@ Rows cut_rows(Cut &cut, const LossArgs &a, bool backward) {
   return r;
 }
 
-mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, LaunchCtx &ctx) {
-  GatherParams p{a, r, backward, 0};
+mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, const PackRows &pack, LaunchCtx &ctx) {
+  const int sms = ctx.dev->info.sms;
+  GatherParams p{a, r, backward, 0, std::min(a.rows, 2 * sms), pack};
   while (p.log_threads < 9 && (32ll << p.log_threads) < r.ldx) ++p.log_threads;  // (up to four pieces each)
-  const int blocks = std::min(a.rows, 2 * ctx.dev->info.sms);
-  cudaError_t e = launch_pdl(gather_kernel, dim3((unsigned)blocks), dim3(kGatherThreads), 0, ctx.stream, dim3(1), p);
+  const int64_t copy = std::min<int64_t>(((pack.rows << pack.log_threads) + kGatherThreads - 1) / kGatherThreads, 8 * sms);
+  cudaError_t e = launch_pdl(gather_kernel, dim3((unsigned)(p.blocks + copy)), dim3(kGatherThreads), 0, ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch (gather)");
   count_operator_launch();
   return MM_OK;
@@ -869,7 +950,7 @@ cudaLaunchConfig_t tile_config(int grid, cudaStream_t s, cudaLaunchAttribute *at
   at->val.clusterDim.y = at->val.clusterDim.z = 1;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)grid);
-  lc.blockDim = dim3(tile_threads(MODE));
+  lc.blockDim = dim3(tile_threads(MODE, CG));
   lc.dynamicSmemBytes = Ring<MODE, CG>::kSmem;
   lc.stream = s;
   lc.attrs = at;
@@ -909,10 +990,10 @@ template <int MODE, int CG>
 mm_status launch_tiles(TileParams &p, const Maps &m, int64_t M, LaunchCtx &ctx) {
   mm_status st = tile_places<MODE, CG>(ctx, &p.places);
   if (st != MM_OK) return st;
-  const int64_t tiles = (M + 128 * CG - 1) / (128 * CG) * p.tiles_n * p.splits;
+  const int64_t tiles = (M + 128 * CG - 1) / (128 * CG) * p.tiles_n;
   if (tiles >= 1 << 30) return set_error(MM_ERR_UNSUPPORTED, "too many tiles");
-  const int grid = CG * (int)std::min<int64_t>(p.bn == 256 ? 2 * tiles : tiles, p.places);
-  cudaError_t e = launch_pdl(tile_kernel<MODE, CG>, dim3((unsigned)grid), dim3(tile_threads(MODE)), Ring<MODE, CG>::kSmem, ctx.stream,
+  const int grid = CG * (int)std::min<int64_t>(MODE == MODE_DX ? p.places : p.bn == 256 ? 2 * tiles : tiles, p.places);
+  cudaError_t e = launch_pdl(tile_kernel<MODE, CG>, dim3((unsigned)grid), dim3(tile_threads(MODE, CG)), Ring<MODE, CG>::kSmem, ctx.stream,
                              dim3(CG), m.a, m.b, m.bh, m.o, p);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch");
   count_operator_launch();
@@ -930,21 +1011,38 @@ int tile_width(int64_t N) { return N <= 128 ? 128 : 256; }
 mm_status logits_maps(Maps *m, TileParams &p, Form f, const TmaRows &w) {
   p.bn = tile_width(p.width);
   p.tiles_n = (p.width + p.bn - 1) / p.bn;
-  p.splits = 1;
-  p.num_kb = p.kb_per_split = (p.cols + 63) / 64;
+  p.num_kb = (p.cols + 63) / 64;
   const char *base = static_cast<const char *>(w.p) + (int64_t)p.v0 * w.ld;
   const int64_t tokens = std::min(p.width, p.vocab - p.v0);
   mm_status st;
-  if (p.r.x && (st = rows_map(&m->a, p.tx, p.r.x, p.cols, p.r.rows_pad, p.r.ldx, 128)) != MM_OK) return st;
+  if (p.r.count && (st = rows_map(&m->a, p.tx, p.r.x, p.cols, p.r.rows_pad, p.r.ldx, 128)) != MM_OK) return st;
   if ((st = rows_map(&m->b, p.tx, base, p.cols, tokens, w.ld / 2, p.bn / f.cg)) != MM_OK) return st;
   return rows_map(&m->bh, p.tx, base, p.cols, tokens, w.ld / 2, p.bn / f.cg / 2);
 }
 
-// W where TMA can read it: in place, or copied.
-mm_status align_weight(const LossArgs &a, TmaRows *w, LaunchCtx &ctx) {
+// W where TMA can read it: in place, or to be copied (by pack).
+mm_status place_weight(const LossArgs &a, TmaRows *w, PackRows *pack, LaunchCtx &ctx) {
+  std::memset(pack, 0, sizeof *pack);
   *w = TmaRows{a.weight, a.ldw * 2, a.vocab, (int64_t)a.cols * 2};
-  TmaRows none{nullptr, 16, 1, 16};
-  return align_rows(*w, none, ctx);
+  const int64_t ld16 = (w->bytes + 15) / 16 * 16;
+  if (addressable(*w)) {
+    if (a.vocab == 1) w->ld = ld16;  // (a distance that is never used, as maps want it)
+    return MM_OK;
+  }
+  void *to = nullptr;
+  mm_status st = get_scratch(ctx, SCRATCH_REPACK, (size_t)(ld16 * a.vocab), &to);
+  if (st != MM_OK) return st;
+  *pack = pack_job(w->p, w->ld, w->rows, w->bytes, to, ld16);
+  w->p = to;
+  w->ld = ld16;
+  return MM_OK;
+}
+// Few rows that TMA reads as they lie, and W too: see Rows.
+bool is_direct(const LossArgs &a, Form f) {
+  return f.cg == 1 && addressable(TmaRows{a.x, a.ldx * 2, a.rows, 0}) && addressable(TmaRows{a.weight, a.ldw * 2, a.vocab, 0});
+}
+mm_status direct_map(CUtensorMap *map, const LossArgs &a) {
+  return rows_map(map, a.tx, a.x, a.cols, a.rows, a.rows == 1 ? ((int64_t)a.cols + 7) / 8 * 8 : a.ldx, 128);
 }
 
 TileParams tile_params(const LossArgs &a, LaunchCtx &ctx) {
@@ -953,6 +1051,13 @@ TileParams tile_params(const LossArgs &a, LaunchCtx &ctx) {
   p.cols = a.cols;
   p.vocab = a.vocab;
   p.tx = a.tx;
+  p.x = a.x;
+  p.targets = a.targets;
+  p.lse = a.lse;
+  p.dloss = a.dloss;
+  p.ldx = a.ldx;
+  p.ti = a.ti;
+  p.rows = a.rows;
   p.wait = operator_waits(ctx);
   return p;
 }
@@ -979,14 +1084,11 @@ mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
   }
   TileParams p = tile_params(a, ctx);
   const Form f = form_of(a.rows);
-  // Few rows are one row tile whether or not all of them count, so they are not
-  // gathered where TMA reads x as it lies.
-  const bool direct = f.cg == 1 && (uintptr_t)a.x % 16 == 0 && (a.ldx % 8 == 0 || a.rows == 1) && a.ldx < (1LL << 37);
+  const bool direct = is_direct(a, f);
   Cut cut;
   for (int pass = 0; pass < 2; ++pass) {
     cut.used = 0;
-    if (direct) std::memset(&p.r, 0, sizeof p.r), p.r.rows_pad = kRowTile;
-    else p.r = cut_rows(cut, a, false);
+    p.r = cut_rows(cut, a, false, direct);
     p.hit = cut.take<float>(p.r.rows_pad);
     p.part = cut.take<float2>(((int64_t)a.vocab + 127) / 128 * p.r.rows_pad);
     if (pass == 0) {
@@ -998,18 +1100,13 @@ mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
   }
   mm_status st;
   TmaRows w;
-  if ((st = align_weight(a, &w, ctx)) != MM_OK) return st;
-  if (!direct && (st = launch_gather(a, p.r, false, ctx)) != MM_OK) return st;
-  p.width = a.vocab;
+  PackRows pack;
   Maps m;
+  if ((st = place_weight(a, &w, &pack, ctx)) != MM_OK) return st;
+  if (!direct && (st = launch_gather(a, p.r, false, pack, ctx)) != MM_OK) return st;
+  p.width = a.vocab;
   if ((st = logits_maps(&m, p, f, w)) != MM_OK) return st;
-  if (direct) {
-    p.targets = a.targets;
-    p.ti = a.ti;
-    p.rows = a.rows;
-    st = rows_map(&m.a, p.tx, a.x, p.cols, a.rows, a.rows == 1 ? ((int64_t)a.cols + 7) / 8 * 8 : a.ldx, 128);
-    if (st != MM_OK) return st;
-  }
+  if (direct && (st = direct_map(&m.a, a)) != MM_OK) return st;
   m.o = m.a;  // (none)
   if ((st = launch_tiles<MODE_LSE>(f, p, m, a.rows, ctx)) != MM_OK) return st;
   LossParams l{a, p.r, p.part, p.hit, f.tile_m(), p.bn, p.tiles_n, p.places};
@@ -1031,46 +1128,50 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   const int64_t most = std::max<int64_t>(256, kPieceBytes / (rows_pad * 2) / 256 * 256);
   const int64_t pieces = (a.vocab + most - 1) / most;
   const int piece = (int)std::min(((a.vocab + pieces - 1) / pieces + 255) / 256 * 256, ((int64_t)a.vocab + 63) / 64 * 64);
-  // dx: K is split where the tiles are fewer than the places
+  // dx: sums of all tiles, and of the parts of cut ones, at most one a place
+  p.acc_cols = (a.cols + 31) / 32;
   const int bn_cols = tile_width(a.cols), tiles_cols = (a.cols + bn_cols - 1) / bn_cols;
   const int64_t dx_tiles = ((int64_t)a.rows + f.tile_m() - 1) / f.tile_m() * tiles_cols;
-  const int places = ctx.dev->info.sms / f.cg;
-  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(places / dx_tiles, piece / 64 / 8));
-  p.acc_cols = (a.cols + 31) / 32;
+  int dx_places = 0;
+  mm_status st = f.cg == 1 ? tile_places<MODE_DX, 1>(ctx, &dx_places) : tile_places<MODE_DX, 2>(ctx, &dx_places);
+  if (st != MM_OK) return st;
+  const bool direct = is_direct(a, f);
   Cut cut;
   uint16_t *g = nullptr;
   for (int pass = 0; pass < 2; ++pass) {
     cut.used = 0;
-    p.r = cut_rows(cut, a, true);
+    p.r = cut_rows(cut, a, true, direct);
     g = cut.take<uint16_t>(rows_pad * piece);
-    if (a.dx) p.acc = cut.take<float>(splits * rows_pad * p.acc_cols * 32);
+    if (a.dx) {
+      p.acc = cut.take<float>(rows_pad * p.acc_cols * 32);
+      p.acc_cut = cut.take<float>((int64_t)dx_places * f.tile_m() * bn_cols);
+    }
     if (pass == 0) {
       void *w = nullptr;
-      mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, cut.used, &w);
-      if (st != MM_OK) return st;
+      if ((st = get_scratch(ctx, SCRATCH_WORKSPACE, cut.used, &w)) != MM_OK) return st;
       cut.base = static_cast<char *>(w);
     }
   }
-  mm_status st;
   TmaRows w;
-  if ((st = align_weight(a, &w, ctx)) != MM_OK) return st;
+  PackRows pack;
+  if ((st = place_weight(a, &w, &pack, ctx)) != MM_OK) return st;
   p.dw = static_cast<uint16_t *>(a.dweight);
   p.lddw = a.lddw;
   p.vec = (uintptr_t)a.dweight % 16 == 0 && a.lddw % 8 == 0 && a.cols % 8 == 0 && a.lddw < (1LL << 37);
-  if ((st = launch_gather(a, p.r, true, ctx)) != MM_OK) return st;
+  if (!direct && (st = launch_gather(a, p.r, true, pack, ctx)) != MM_OK) return st;
+  p.piece_kb = piece / 64;
   for (p.v0 = 0; p.v0 < a.vocab; p.v0 += piece) {
     Maps m;
     p.first = p.v0 == 0;
     p.width = std::min(piece, (a.vocab - p.v0 + 63) / 64 * 64);
     if ((st = logits_maps(&m, p, f, w)) != MM_OK) return st;
+    if (direct && (st = direct_map(&m.a, a)) != MM_OK) return st;
     if ((st = rows_map(&m.o, p.tx, g, p.width, rows_pad, piece, 32)) != MM_OK) return st;
     if ((st = launch_tiles<MODE_G>(f, p, m, a.rows, ctx)) != MM_OK) return st;
     p.bn = bn_cols;
     p.tiles_n = tiles_cols;
     if (a.dx) {
       p.num_kb = p.width / 64;
-      p.splits = splits;
-      p.kb_per_split = (p.num_kb + splits - 1) / splits;
       if ((st = rows_map(&m.a, p.tx, g, p.width, rows_pad, piece, 128)) != MM_OK) return st;
       if ((st = rows_map(&m.b, p.tx, static_cast<const char *>(w.p) + (int64_t)p.v0 * w.ld, a.cols,
                          std::min(p.width, a.vocab - p.v0), w.ld / 2, 64)) != MM_OK)
@@ -1079,9 +1180,8 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
       if ((st = launch_tiles<MODE_DX>(f, p, m, a.rows, ctx)) != MM_OK) return st;
     }
     if (a.dweight) {
-      p.splits = 1;
       if ((st = rows_map(&m.a, p.tx, g, p.width, rows_pad, piece, 64)) != MM_OK) return st;
-      if ((st = rows_map(&m.b, p.tx, p.r.x, a.cols, rows_pad, p.r.ldx, 64)) != MM_OK) return st;
+      if ((st = rows_map(&m.b, p.tx, p.r.x, a.cols, direct ? 128 : rows_pad, p.r.ldx, 64)) != MM_OK) return st;
       m.bh = m.o = m.b;
       if (p.vec && (st = rows_map(&m.o, p.tx, a.dweight, a.cols, a.vocab, a.vocab == 1 ? p.r.ldx : a.lddw, 32)) != MM_OK)
         return st;
@@ -1089,9 +1189,10 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
     }
   }
   if (!a.dx) return MM_OK;
-  DxParams d{a, p.r, p.acc, p.acc_cols, splits, (uintptr_t)a.dx % 16 == 0 && (a.lddx % 8 == 0 || a.rows == 1)};
-  cudaError_t e = launch_pdl(splits > 1 ? dx_kernel<2> : dx_kernel<8>, dim3((unsigned)(4 * ctx.dev->info.sms)), dim3(256),
-                             0, ctx.stream, dim3(1), d);
+  DxParams d{a, p.r, p.acc, p.acc_cut, f.tile_m(), bn_cols, tiles_cols, dx_places, p.piece_kb, p.acc_cols,
+             (uintptr_t)a.dx % 16 == 0 && (a.lddx % 8 == 0 || a.rows == 1)};
+  cudaError_t e = launch_pdl(dx_tiles < dx_places ? dx_kernel<2> : dx_kernel<8>, dim3((unsigned)(4 * ctx.dev->info.sms)),
+                             dim3(256), 0, ctx.stream, dim3(1), d);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy_backward launch (dx)");
   count_operator_launch();
   return MM_OK;

@@ -3,8 +3,8 @@
 //   out[t] = scale W[token[t]]
 //   dW[v]  = base[v] + scale sum over {t : token[t] = v} of dout[t]
 //
-// Forward: memory traffic, the rows read and written once.  A power of two of
-// threads has a row, each thread up to four 16-byte pieces in flight.
+// Forward: memory traffic, the rows read and written once, a power of two of threads to
+// a row.
 //
 // Backward: the places t are sorted by token (stable), so that the rows of one
 // token stand together and are added in the order of t, in registers, without
@@ -27,9 +27,13 @@ namespace {
 constexpr int kE = 8;  // elements of a piece: 16 bytes of the 16-bit types
 
 // ---------------------------------------------------------------- forward
+// Pieces (16 bytes, or single elements of rows that start anywhere) a thread has in
+// flight.
+template <bool EDGES>
+constexpr int kEmbedPieces = EDGES ? 16 : 4;
 template <int TW, int TO, bool EDGES>
 __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int log_threads) {
-  constexpr int E = EDGES ? 1 : kE;
+  constexpr int E = EDGES ? 1 : kE, N = kEmbedPieces<EDGES>;
   pdl_launch_dependents();
   pdl_wait();
   const int threads = 1 << log_threads, t = threadIdx.x & (threads - 1);
@@ -38,12 +42,12 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int log_t
   const int64_t token = load_token(a.tokens, a.ti, r, a.vocab);
   const float scale = token < a.vocab ? a.scale : 0.f;  // (zeros, whatever the scale)
   const int step = threads * E;
-  for (int j0 = t * E; j0 < a.cols; j0 += 4 * step) {
-    float v[4][E];
-    const int n = token < a.vocab ? pieces_below<4>(j0, step, a.cols) : 0;
+  for (int j0 = t * E; j0 < a.cols; j0 += N * step) {
+    float v[N][E];
+    const int n = token < a.vocab ? pieces_below<N>(j0, step, a.cols) : 0;
     load_pieces<TW>(a.weight, token * a.ldw + j0, step, n, v);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < N; ++k) {
       if (j0 + k * step >= a.cols) break;
 #pragma unroll
       for (int e = 0; e < E; ++e) v[k][e] *= scale;
@@ -59,7 +63,8 @@ cudaError_t embed_launch(const EmbedArgs &a, LaunchCtx &ctx) {
                      (a.ldw * bw % 16 == 0 || a.vocab <= 1) && (a.ldo * bo % 16 == 0 || a.rows == 1);
   const int64_t pieces = whole ? a.cols / kE : a.cols;
   int log_threads = 0;
-  while (log_threads < 8 && (4ll << log_threads) < pieces) ++log_threads;
+  const int64_t each = whole ? kEmbedPieces<false> : kEmbedPieces<true>;
+  while (log_threads < 8 && each << log_threads < pieces) ++log_threads;
   const int64_t rows = 256 >> log_threads;
   const dim3 grid((unsigned)((a.rows + rows - 1) / rows));
   return whole ? launch_pdl(embed_kernel<TW, TO, false>, grid, dim3(256), 0, ctx.stream, dim3(1), a, log_threads)
@@ -68,16 +73,17 @@ cudaError_t embed_launch(const EmbedArgs &a, LaunchCtx &ctx) {
 
 // ---------------------------------------------------------------- sort, and the rows of the others
 // Least significant digit first, 9 bits a pass (a vocabulary below 2^18 takes two), by
-// one cluster of eight CTAs.  Each warp has a run of consecutive places: it counts its
+// one CTA or one cluster of eight.  Each warp has a run of consecutive places: it counts its
 // digits, the counts of all become places, and it goes over its run again; equal
 // digits keep their order because a warp takes 32 at a time, ranked by matching.
 // The places lie in global memory (L2) between passes, so any number of them sorts.
 //
-// dW's rows are written meanwhile, as zeros or the base's, by the other clusters of the
+// dW's rows are written meanwhile, as zeros or the base's, by the other CTAs of the
 // launch, those that the sums will write again among them.  (Untouched rows written
 // beside the sums instead: 76 -> 88 us at 8192 x 4096 into 32000, 150 -> 191 at 65536 x
-// 1024 into 131072.)
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCtas = 8;
+// 1024 into 131072.)  One CTA sorts where that takes no longer than the rows: clusters
+// of eight find room on 120 of the 152 SMs only.
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kMaxSortCtas = 8;
 constexpr int kDigit = 9, kBins = 1 << kDigit;
 constexpr size_t kSortSmem = (kSortWarps * kBins + kBins + 32) * sizeof(uint32_t);
 
@@ -85,7 +91,7 @@ struct SortParams {
   const void *tokens;
   int ti;
   int64_t vocab;
-  int rows, passes;
+  int rows, passes, ctas;  // ctas: 1 or kMaxSortCtas
   uint2 *to, *other;   // (token, place)
   uint32_t *spanning;  // set to 0: how many tokens the sums will have left in parts
   // the rows
@@ -104,10 +110,14 @@ __device__ __forceinline__ uint32_t cluster_u32(uint32_t addr, int rank) {
 __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem) {
   uint32_t(*off)[kBins] = reinterpret_cast<uint32_t(*)[kBins]>(smem);
   uint32_t *count = smem + kSortWarps * kBins, *warp_sum = count + kBins;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rank = (int)tc::cluster_ctarank();
-  const int lo = (int)((int64_t)p.rows * rank / kSortCtas), n = (int)((int64_t)p.rows * (rank + 1) / kSortCtas) - lo;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rank = (int)blockIdx.x;
+  const int lo = (int)((int64_t)p.rows * rank / p.ctas), n = (int)((int64_t)p.rows * (rank + 1) / p.ctas) - lo;
   const int w0 = lo + (int)((int64_t)n * warp / kSortWarps), w1 = lo + (int)((int64_t)n * (warp + 1) / kSortWarps);
   const uint32_t below = (1u << lane) - 1;
+  const auto sync = [&] {  // of all CTAs that sort
+    if (p.ctas > 1) tc::cluster_sync_all();
+    else __syncthreads();
+  };
   constexpr int K = 8;
   uint2 *src = nullptr, *dst = p.passes & 1 ? p.to : p.other;  // the last pass ends in `to`
   for (int pass = 0; pass < p.passes; ++pass) {
@@ -149,14 +159,14 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
       }
       count[t] = sum;
     }
-    tc::cluster_sync_all();
+    sync();
     if (t < kBins) {
       const uint32_t addr = tc::smem_u32(count + t);
-      uint32_t c[kSortCtas], before = 0, total = 0;
+      uint32_t c[kMaxSortCtas], before = 0, total = 0;
 #pragma unroll
-      for (int r = 0; r < kSortCtas; ++r) c[r] = cluster_u32(addr, r);
+      for (int r = 0; r < kMaxSortCtas; ++r) c[r] = r >= p.ctas ? 0 : p.ctas > 1 ? cluster_u32(addr, r) : count[t];
 #pragma unroll
-      for (int r = 0; r < kSortCtas; ++r) before += r < rank ? c[r] : 0, total += c[r];
+      for (int r = 0; r < kMaxSortCtas; ++r) before += r < rank ? c[r] : 0, total += c[r];
       uint32_t sum = total;
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
@@ -183,7 +193,7 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
         __syncwarp();
       }
     }
-    tc::cluster_sync_all();  // (releases and acquires the places, too)
+    sync();  // (releases and acquires the places, too)
     src = dst;
     dst = dst == p.to ? p.other : p.to;
   }
@@ -242,13 +252,13 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortPara
   pdl_launch_dependents();
   pdl_wait();
   extern __shared__ uint32_t sort_smem[];
-  if (blockIdx.x < kSortCtas) {
+  if ((int)blockIdx.x < p.ctas) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.spanning = 0;
     sort_places(p, sort_smem);
     return;
   }
-  write_rows(p, (int64_t)(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x,
-             (int64_t)(gridDim.x - kSortCtas) * kSortThreads);
+  write_rows(p, ((int64_t)blockIdx.x - p.ctas) * kSortThreads + threadIdx.x,
+             ((int64_t)gridDim.x - p.ctas) * kSortThreads);
 }
 // The rows alone, where there are no places.
 __global__ void __launch_bounds__(256) embed_rows_kernel(const SortParams p) {
@@ -270,21 +280,27 @@ struct SumParams {
 };
 constexpr int kMinLogThreads = 3, kMaxChunk = 32, kGroupPlaces = kMaxChunk + 2;
 
+// The base's piece of a token's row.
 template <int TW, int E>
-__device__ __forceinline__ void write_sum(const EmbedBwdArgs &a, int64_t token, int j, const float (&sum)[E]) {
-  float b[E];
+__device__ __forceinline__ Piece<TW, E> base_piece(const EmbedBwdArgs &a, int64_t token, int j) {
+  return Piece<TW, E>::load(at<TW>(a.base, token * a.ldb + j));
+}
+template <int TW, int E>
+__device__ __forceinline__ void write_sum(const EmbedBwdArgs &a, int64_t token, int j, const float (&sum)[E],
+                                          const Piece<TW, E> &base) {
+  float v[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) b[e] = 0.f;
-  if (a.base) load_piece<TW>(a.base, token * a.ldb + j, b);
-#pragma unroll
-  for (int e = 0; e < E; ++e) b[e] = fmaf(a.scale, sum[e], b[e]);
-  store_piece<TW>(a.dweight, token * a.lddw + j, b);
+  for (int e = 0; e < E; ++e) v[e] = fmaf(a.scale, sum[e], a.base ? base.get(e) : 0.f);
+  store_piece<TW>(a.dweight, token * a.lddw + j, v);
 }
 
 // A chunk of places to a power of two of threads, a piece of the columns each.
-template <int TW, int TO, int E>
+// BASE: there is one; its row is read with the token's first, ahead of the sum (read when
+// the sum was written it held up every token: 5000 x 1001 23 us).
+template <int TW, int TO, int E, bool BASE>
 __global__ void __launch_bounds__(256, 4) embed_sum_kernel(const SumParams p) {
-  constexpr int U = TO == MM_F32 ? 4 : 8;  // rows read before the first is added
+  // rows read before the first is added (as the registers hold)
+  constexpr int U = E == 1 ? 16 : BASE ? (TW == MM_F32 || TO == MM_F32 ? 2 : 4) : TO == MM_F32 ? 4 : 8;
   constexpr int kPlaces = (256 >> kMinLogThreads) * kGroupPlaces;
   __shared__ uint32_t tokens[kPlaces];
   __shared__ int64_t starts[kPlaces];  // of a place's row of dout
@@ -309,6 +325,7 @@ __global__ void __launch_bounds__(256, 4) embed_sum_kernel(const SumParams p) {
   if (n <= 0 || j >= a.cols) return;
   uint32_t token = mine[0];
   bool from_before = mine[-1] == token;
+  Piece<TW, E> base;
   float sum[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = 0.f;
@@ -317,11 +334,18 @@ __global__ void __launch_bounds__(256, 4) embed_sum_kernel(const SumParams p) {
       store_piece<MM_F32>(p.parts, ((int64_t)chunk * 2 + (from_before ? 0 : 1)) * a.cols + j, sum);
       if (!from_before && j == 0) p.spanning[1 + atomicAdd(p.spanning, 1u)] = (uint32_t)chunk;
     } else {
-      write_sum<TW, E>(a, token, j, sum);
+      write_sum<TW, E>(a, token, j, sum, base);
     }
   };
   for (int i = 0; i < n; i += U) {
     Piece<TO, E> v[U];
+    Piece<TW, E> b[BASE ? U : 1];
+    if constexpr (BASE) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u < n && mine[i + u] != none && (i + u == 0 || mine[i + u] != mine[i + u - 1]))
+          b[u] = base_piece<TW, E>(a, mine[i + u], j);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i + u < n && mine[i + u] != none) v[u] = Piece<TO, E>::load(at<TO>(a.dout, start[i + u] + j));
@@ -333,10 +357,14 @@ __global__ void __launch_bounds__(256, 4) embed_sum_kernel(const SumParams p) {
         leave(false);
         token = next;
         from_before = false;
+        if constexpr (BASE) base = b[u];
 #pragma unroll
         for (int e = 0; e < E; ++e) sum[e] = 0.f;
       }
       if (token == none) return;
+      if constexpr (BASE) {
+        if (i + u == 0) base = b[0];
+      }
 #pragma unroll
       for (int e = 0; e < E; ++e) sum[e] += v[u].get(e);
     }
@@ -389,7 +417,9 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p) {
     if (y == 0 && j < a.cols) {
 #pragma unroll
       for (int e = 0; e < V; ++e) sum[e] = ((sum[e] + runs[1][x][e]) + runs[2][x][e]) + runs[3][x][e];
-      write_sum<TW, V>(a, token, j, sum);
+      Piece<TW, V> base;
+      if (a.base) base = base_piece<TW, V>(a, token, j);
+      write_sum<TW, V>(a, token, j, sum, base);
     }
     __syncthreads();
   }
@@ -408,8 +438,9 @@ mm_status embed_sums(const EmbedBwdArgs &a, SumParams p, LaunchCtx &ctx) {
   p.across = (int)((p.chunks + groups - 1) / groups);
   if (p.across * slabs >= 1 << 30) return set_error(MM_ERR_UNSUPPORTED, "too many blocks");
   const dim3 grid((unsigned)(p.across * slabs));
-  cudaError_t e = whole ? launch_pdl(embed_sum_kernel<TW, TO, kE>, grid, dim3(256), 0, ctx.stream, dim3(1), p)
-                        : launch_pdl(embed_sum_kernel<TW, TO, 1>, grid, dim3(256), 0, ctx.stream, dim3(1), p);
+  const auto kernel = whole ? (a.base ? embed_sum_kernel<TW, TO, kE, true> : embed_sum_kernel<TW, TO, kE, false>)
+                            : (a.base ? embed_sum_kernel<TW, TO, 1, true> : embed_sum_kernel<TW, TO, 1, false>);
+  cudaError_t e = launch_pdl(kernel, grid, dim3(256), 0, ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch");
   count_operator_launch();
   if (p.chunks == 1) return MM_OK;
@@ -469,7 +500,7 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   }
   const auto whole = [](int64_t bytes) { return ((size_t)bytes + 255) / 256 * 256; };
   const size_t pairs = whole(a.rows * (int64_t)sizeof(uint2)), list = whole((p.chunks + 1) * (int64_t)sizeof(uint32_t));
-  // as many clusters as run at once: one sorts, the others write rows
+  // as many CTAs as run at once: the first sort, the others write rows
   static PerDevice<int> fits;
   int clusters;
   const cudaError_t err = fits.get(ctx.dev->info.ordinal, &clusters, [](int *n) -> cudaError_t {
@@ -477,10 +508,10 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = kSortCtas;
+    at.val.clusterDim.x = kMaxSortCtas;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(kSortCtas);
+    lc.gridDim = dim3(kMaxSortCtas);
     lc.blockDim = dim3(kSortThreads);
     lc.dynamicSmemBytes = kSortSmem;
     lc.attrs = &at;
@@ -489,7 +520,11 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   });
   if (err != cudaSuccess) return cuda_error(err, "embedding_backward set-up");
   if (clusters < 1) return set_error(MM_ERR_UNSUPPORTED, "no cluster of CTAs fits on this device");
-  const int row_ctas = fills ? std::max(1, clusters - 1) * kSortCtas : 0;
+  // One CTA sorts within 10 us and 3.7 ns a place (65536: 243 us; eight 42), and rows are
+  // written at 5 TB/s or more.
+  const int64_t written = fills ? f.bytes * f.fill_rows : 0;
+  f.ctas = a.rows <= 2048 || (50 << 20) + a.rows * 18500 <= written ? 1 : kMaxSortCtas;
+  const int row_ctas = !fills ? 0 : f.ctas == 1 ? ctx.dev->info.sms - 1 : std::max(1, clusters - 1) * kMaxSortCtas;
   void *scratch = nullptr;
   mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, 2 * pairs + list + (size_t)p.chunks * 2 * a.cols * sizeof(float), &scratch);
   if (st != MM_OK) return st;
@@ -504,8 +539,8 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   f.rows = (int)a.rows;
   f.passes = 1;
   while (a.vocab >> (kDigit * f.passes)) ++f.passes;
-  cudaError_t e = launch_pdl(embed_sort_kernel, dim3((unsigned)(kSortCtas + row_ctas)), dim3(kSortThreads), kSortSmem,
-                             ctx.stream, dim3(kSortCtas), f);
+  cudaError_t e = launch_pdl(embed_sort_kernel, dim3((unsigned)(f.ctas + row_ctas)), dim3(kSortThreads), kSortSmem,
+                             ctx.stream, dim3((unsigned)f.ctas), f);
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (sort)");
   count_operator_launch();
   return with_type(a.tw, [&](auto tw) {

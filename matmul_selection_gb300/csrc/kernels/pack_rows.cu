@@ -9,36 +9,16 @@ namespace mm {
 
 namespace {
 
-// A power of two of threads to a row, 16 bytes of the copy each, up to four pieces read
-// before the first is stored.
-__global__ void __launch_bounds__(256) pack_rows_kernel(const uint8_t *src, int64_t ld, int64_t rows,
-                                                        int64_t bytes, uint8_t *dst, int64_t ld16, int log_threads) {
+__global__ void __launch_bounds__(256) pack_rows_kernel(const PackRows p) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int U = 4;
-  const int threads = 1 << log_threads, t = threadIdx.x & (threads - 1);
-  const int64_t groups = (int64_t)gridDim.x << (8 - log_threads);
-  for (int64_t r = ((int64_t)blockIdx.x << (8 - log_threads)) + (threadIdx.x >> log_threads); r < rows; r += groups) {
-    const uint8_t *from = src + r * ld;
-    for (int64_t b0 = t * 16; b0 < ld16; b0 += threads * 16 * U) {
-      RowPiece<1> v[U];
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (b0 + k * threads * 16 < ld16) v[k].load(from, bytes, b0 + k * threads * 16);
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (b0 + k * threads * 16 < ld16) *reinterpret_cast<uint4 *>(dst + r * ld16 + b0 + k * threads * 16) = v[k].value(from, bytes, b0 + k * threads * 16);
-    }
-  }
+  pack_rows(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 mm_status pack(TmaRows &r, uint8_t *dst, int64_t ld16, LaunchCtx &ctx) {
-  int log_threads = 0;
-  while (log_threads < 8 && (64ll << log_threads) < ld16) ++log_threads;
-  const int64_t per = 256 >> log_threads;
-  const int64_t blocks = std::min<int64_t>((r.rows + per - 1) / per, 16 * ctx.dev->info.sms);
-  cudaError_t e = launch_pdl(pack_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, ctx.stream, dim3(1),
-                             static_cast<const uint8_t *>(r.p), r.ld, r.rows, r.bytes, dst, ld16, log_threads);
+  const PackRows p = pack_job(r.p, r.ld, r.rows, r.bytes, dst, ld16);
+  const int64_t blocks = std::min<int64_t>(((r.rows << p.log_threads) + 255) / 256, 16 * ctx.dev->info.sms);
+  cudaError_t e = launch_pdl(pack_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "row copy launch");
   count_operator_launch();
   r.p = dst;
@@ -46,11 +26,11 @@ mm_status pack(TmaRows &r, uint8_t *dst, int64_t ld16, LaunchCtx &ctx) {
   return MM_OK;
 }
 
+}  // namespace
+
 bool addressable(const TmaRows &r) {
   return (uintptr_t)r.p % 16 == 0 && (r.rows == 1 || (r.ld % 16 == 0 && r.ld < (1LL << 40)));
 }
-
-}  // namespace
 
 mm_status align_rows(TmaRows &a, TmaRows &b, LaunchCtx &ctx) {
   TmaRows *op[2] = {&a, &b};

@@ -109,6 +109,8 @@ struct TmaRows {
   const void *p;
   int64_t ld, rows, bytes;
 };
+// Whether TMA reads them as they lie.
+bool addressable(const TmaRows &r);
 // Operands whose base or distance between rows is not a multiple of 16 bytes
 // are copied into the stream's scratch and pointed there.
 mm_status align_rows(TmaRows &a, TmaRows &b, LaunchCtx &ctx);
