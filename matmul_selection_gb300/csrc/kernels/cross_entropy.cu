@@ -247,6 +247,8 @@ struct TileParams {
   int v0, width;     // the piece of the vocabulary: its first token, how many (G: padded to 64)
   int tx;
   int bn, tiles_n, places;
+  int a_rows;        // CG = 1: the rows of A that are loaded
+  int boxes;         // DW: boxes a warp
   int num_kb;        // 64-element blocks of K (DW: of the rows that count)
   int piece_kb;      // DX: those of a whole piece
   float2 *part;      // LSE: [128 of the vocabulary][rows_pad] (r, s)
@@ -257,6 +259,8 @@ struct TileParams {
   float *acc, *acc_cut;
   int acc_cols;
   int first;         // DX: the first piece
+  uint16_t *g;       // G of few rows: its rows, ldg apart
+  int64_t ldg;
   uint16_t *dw;
   int64_t lddw;
   int vec;           // DW: its rows are whole 16-byte pieces
@@ -264,16 +268,33 @@ struct TileParams {
 };
 
 // Stages of 64 of K: 128 rows of A, and of B 128 (its half of a pair's tile) or 256.
-// Tiles in 16 bits leave through boxes in shared memory, one for each warp that takes
-// them out.
+// Few rows (CG = 1) wait for W, so their A has room for no more rows than there are (a
+// multiple of 16): the MMA's other rows read what lies behind, and nobody reads theirs.
+// That leaves more of the ring to W in flight.  A pair's tiles in 16 bits leave through
+// boxes in shared memory, one for each warp that takes them out, or two where K is a
+// stage or two and the ring need not be long (see boxes_of).
+constexpr uint32_t kSmemBytes = 227 * 1024, kBarBytes = 1024;
 template <int MODE, int CG>
 struct Ring {
-  static constexpr uint32_t kA = 128 * 128, kStageB = kA + (CG == 2 ? 128 : 256) * 128;
   static constexpr int kOut = out_warps(MODE, CG);
-  static constexpr int kStages = CG == 1 ? 4 : kOut == 16 ? 5 : 6;
-  static constexpr uint32_t kBoxes = kOut * kBoxB;  // (LSE: sums)
-  static constexpr size_t kSmem = kStages * kStageB + kBoxes + 1024 + 256;
+  static constexpr bool kHasBoxes = kOut == 16;
+  static constexpr uint32_t kB = (CG == 2 ? 128 : 256) * 128;
+  static constexpr int kMaxStages = 6;
+  static constexpr size_t kSmem = kSmemBytes;
+  // bytes before the ring's: boxes, or (LSE) sums
+  static __host__ __device__ constexpr uint32_t front(int boxes) { return kHasBoxes ? kOut * boxes * kBoxB : 2 * 128 * 8; }
+  static __host__ __device__ constexpr int stages(int a_rows, int boxes) {
+    const int n = (int)((kSmemBytes - 1024 /* alignment */ - kBarBytes - front(boxes)) / (a_rows * 128 + kB));
+    return n < kMaxStages ? n : kMaxStages;
+  }
 };
+static_assert(Ring<MODE_G, 2>::stages(128, 1) == 5 && Ring<MODE_DW, 2>::stages(128, 2) == 3 &&
+                  Ring<MODE_LSE, 2>::stages(128, 1) == 6 && Ring<MODE_LSE, 1>::stages(128, 1) == 4 &&
+                  Ring<MODE_G, 1>::stages(16, 1) == 6,
+              "what the measurements were taken with");
+// Boxes a warp for dW: a product over at most two blocks of K is bound by its stores, and a
+// warp fills one box while the other is read (16 x 4096 x 32000: 51 us with one).
+inline int boxes_of(int rows) { return rows <= 128 ? 2 : 1; }
 
 __device__ __forceinline__ int row_count(const Rows &r, int rows) { return r.count ? max(1, *r.count) : rows; }
 __device__ __forceinline__ int target_of(const TileParams &p, int row) {
@@ -361,11 +382,22 @@ __device__ __forceinline__ float2 join_sums(float2 a, float2 b) {
   return make_float2(r, a.y * exp2_fast(a.x - r) + b.y * exp2_fast(b.x - r));
 }
 
-// A box, free: its store has read it.
-__device__ __forceinline__ void wait_box() {
-  if ((threadIdx.x & 31) == 0) tma_store_wait_read<0>();
-  __syncwarp();
-}
+// A warp's boxes, filled in turn.
+struct Boxes {
+  uint8_t *first;
+  int n, turn;
+  // the next one, free: its store has read it
+  __device__ __forceinline__ uint8_t *next() {
+    if ((threadIdx.x & 31) == 0) {
+      if (n == 2) tma_store_wait_read<1>();
+      else tma_store_wait_read<0>();
+    }
+    __syncwarp();
+    uint8_t *box = first + turn * kBoxB;
+    if (++turn == n) turn = 0;
+    return box;
+  }
+};
 // Columns 32 h .. of 32 rows in 16 bits to half a box.
 __device__ __forceinline__ void fill_box(uint8_t *box, int tx, int h, const uint32_t (&v)[32]) {
   const int lane = threadIdx.x & 31;
@@ -382,41 +414,58 @@ __device__ __forceinline__ void store_box_tma(const CUtensorMap *map, uint8_t *b
   if ((threadIdx.x & 31) == 0) tma_store_2d(map, smem_u32(box), x, y);
 }
 
+// g of 32 columns, token `first` the first of them, in place of the logits: a thread's row.
+struct GRow {
+  int target;
+  float ratio, lse2;
+};
+__device__ __forceinline__ GRow g_row(const TileParams &p, int row, float gain) {
+  GRow r{target_of(p, row), 0.f, 0.f};
+  if (p.r.count) r.ratio = p.r.ratio[row], r.lse2 = p.r.lse2[row];
+  else if (r.target >= 0) r.ratio = ratio_of(p.dloss, row, gain, p.tx), r.lse2 = p.lse[row] * kLog2e;
+  return r;
+}
+__device__ __forceinline__ void make_g(const TileParams &p, const GRow &r, uint32_t (&v)[32], int first) {
+  const bool live = r.ratio != 0.f;  // (a weight of 0 takes its row out, whatever its logits)
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    v[i] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[i]), kLog2e, -r.lse2)) * r.ratio);
+  const int at = r.target - first, left = p.vocab - first;
+  if (__any_sync(0xffffffffu, (unsigned)at < 32u)) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = at == i ? __float_as_uint(__uint_as_float(v[i]) - r.ratio) : v[i];
+  }
+  if (left < 32 || __any_sync(0xffffffffu, !live)) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = live && i < left ? v[i] : 0u;
+  }
+}
 // G, DW: columns n .. n + 63 of the product's rows row0 .. row0 + 31.
 __device__ __forceinline__ void leave_g(const TileParams &p, const CUtensorMap *map, uint32_t (&v)[2][32], int n, int row0,
-                                        uint8_t *box, float gain) {
-  const int row = row0 + (threadIdx.x & 31);
-  const int target = target_of(p, row);
-  float ratio = 0.f, lse2 = 0.f;
-  if (p.r.count) {
-    ratio = p.r.ratio[row], lse2 = p.r.lse2[row];
-  } else if (target >= 0) {
-    ratio = ratio_of(p.dloss, row, gain, p.tx), lse2 = p.lse[row] * kLog2e;
-  }
-  const bool live = ratio != 0.f;  // (a weight of 0 takes its row out, whatever its logits)
-  wait_box();
+                                        Boxes &boxes) {
+  const GRow r = g_row(p, row0 + (threadIdx.x & 31), 0.f);
+  uint8_t *box = boxes.next();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      v[h][i] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[h][i]), kLog2e, -lse2)) * ratio);
-    const int first = p.v0 + n + 32 * h, at = target - first, left = p.vocab - first;
-    if (__any_sync(0xffffffffu, (unsigned)at < 32u)) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[h][i] = at == i ? __float_as_uint(__uint_as_float(v[h][i]) - ratio) : v[h][i];
-    }
-    if (left < 32 || __any_sync(0xffffffffu, !live)) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[h][i] = live && i < left ? v[h][i] : 0u;
-    }
+    make_g(p, r, v[h], p.v0 + n + 32 * h);
     fill_box(box, p.tx, h, v[h]);
   }
   store_box_tma(map, box, n, row0);
 }
+// Few rows: 32 columns from registers, 64 bytes a lane.
+__device__ __forceinline__ void leave_g_few(const TileParams &p, const GRow &r, uint32_t (&v)[32], int n, int row) {
+  make_g(p, r, v, p.v0 + n);
+  uint4 *to = reinterpret_cast<uint4 *>(p.g + (int64_t)row * p.ldg + n);
+  const auto f = [&](int i) { return __uint_as_float(v[i]); };
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    to[j] = make_uint4(pack2(p.tx, f(8 * j), f(8 * j + 1)), pack2(p.tx, f(8 * j + 2), f(8 * j + 3)),
+                       pack2(p.tx, f(8 * j + 4), f(8 * j + 5)), pack2(p.tx, f(8 * j + 6), f(8 * j + 7)));
+}
 
 __device__ __forceinline__ void leave_dw(const TileParams &p, const CUtensorMap *map, uint32_t (&v)[2][32], int n, int v0,
-                                         uint8_t *box, float gain) {
-  wait_box();
+                                         Boxes &boxes, float gain) {
+  uint8_t *box = boxes.next();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -490,18 +539,20 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
                 const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmO,
                 const TileParams p) {
   using R = Ring<MODE, CG>;
-  constexpr int S = R::kStages;
+  const int a_rows = CG == 1 ? p.a_rows : 128;
+  const uint32_t a_bytes = (uint32_t)a_rows * 128, stage_bytes = a_bytes + R::kB;
+  const int S = CG == 1 ? R::stages(a_rows, 1) : MODE == MODE_DW ? R::stages(128, p.boxes) : R::stages(128, 1);
   constexpr bool kMnA = MODE == MODE_DW, kMnB = MODE == MODE_DX || MODE == MODE_DW;
   constexpr bool kChunk = MODE == MODE_LSE;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint8_t *boxes = smem + S * R::kStageB;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(boxes + R::kBoxes);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S;
-  const uint32_t tfull0 = empty0 + 8 * S, tempty0 = tfull0 + 16, drain = tempty0 + 16, stall = drain + 8;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 6);
+  uint8_t *boxes = smem + kBarBytes, *ring = boxes + R::front(MODE == MODE_DW ? p.boxes : 1);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * R::kMaxStages;
+  const uint32_t tfull0 = empty0 + 8 * R::kMaxStages, tempty0 = tfull0 + 16, drain = tempty0 + 16, stall = drain + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * R::kMaxStages + 6);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pos = CG == 2 ? (int)cluster_ctarank() : 0;
@@ -526,7 +577,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
     prefetch_tmap(&tmBh);
-    if (MODE == MODE_G || (MODE == MODE_DW && p.vec)) prefetch_tmap(&tmO);
+    if (R::kHasBoxes && (MODE == MODE_G || p.vec)) prefetch_tmap(&tmO);
   }
   if (CG == 1 && !kMnB && warp == 0 && lane == 0) {
     // few rows: the first blocks of W into L2 while the rows are gathered (one row tile,
@@ -572,8 +623,8 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
           ok = false;
           break;
         }
-        const uint32_t sa = smem_u32(smem + stage * R::kStageB), sb = sa + R::kA, bar = leader_full0 + 8 * stage;
-        if (leader) mbar_expect_tx(full0 + 8 * stage, (uint32_t)(CG * (128 + nh)) * 128);
+        const uint32_t sa = smem_u32(ring + stage * stage_bytes), sb = sa + a_bytes, bar = leader_full0 + 8 * stage;
+        if (leader) mbar_expect_tx(full0 + 8 * stage, (uint32_t)(CG * (a_rows + nh)) * 128);
         if (!kMnA) load_box<CG>(sa, &tmA, bar, kb * 64, m0);
         else
           for (int j = 0; j < 2; ++j) load_box<CG>(sa + j * 8192, &tmA, bar, m0 + j * 64, kb * 64);
@@ -634,9 +685,9 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
             break;
           }
           fence_after();
-          const uint32_t sa = smem_u32(smem + stage * R::kStageB);
+          const uint32_t sa = smem_u32(ring + stage * stage_bytes);
           const uint64_t ad = kDescA | (uint64_t)((sa >> 4) & 0x3FFFu);
-          const uint64_t bd = kDescB | (uint64_t)(((sa + R::kA) >> 4) & 0x3FFFu);
+          const uint64_t bd = kDescB | (uint64_t)(((sa + a_bytes) >> 4) & 0x3FFFu);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f16<CG>(d, ad + (kMnA ? 128 : 2) * kk, bd + (kMnB ? 128 : 2) * kk, idesc, (!start || kk > 0) ? 1u : 0u);
@@ -658,7 +709,8 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
     // two that take turns, each with an accumulator of its own
     const int q = warp & 3, half = (warp - 2) >> 2 & 1, team = (warp - 2) >> 3;
     constexpr int kTeams = R::kOut / 8;
-    uint8_t *box = boxes + (warp - 2) * kBoxB;
+    const int box_count = MODE == MODE_DW ? p.boxes : 1;
+    Boxes mine{boxes + (warp - 2) * box_count * (int)kBoxB, box_count, 0};
     float gain = 0.f;
     if (MODE == MODE_DW) gain = *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
     if (MODE == MODE_G && CG == 1 && !p.r.count) gain = prepare_few(p, cid, ncl, (int)threadIdx.x - 64);
@@ -680,7 +732,8 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
     int turn = 0;
     for (int i = cid + team * ncl; i < tiles.total && ok; i += kTeams * ncl, turn ^= 1) {
       const Unit u = unit_at(tiles, p.bn, i);
-      const int row0 = u.tm * 128 * CG + pos * 128 + q * 32, wide = u.w / 2, c0 = half * wide, n = u.n0 + c0;
+      const int row0 = u.tm * 128 * CG + pos * 128 + q * 32;
+      const int lower = u.w > 128 ? 128 : u.w / 2, c0 = half ? lower : 0, wide = half ? u.w - lower : lower, n = u.n0 + c0;
       const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
       if constexpr (MODE == MODE_LSE) {
         const bool live = row0 < rows && u.n0 < p.vocab;  // (else a half tile past the end)
@@ -720,15 +773,26 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
         } else {
           const int end = MODE == MODE_G ? p.width : p.v0 + row0 < p.vocab ? p.cols : 0;
           const int left = min(wide, end - n);
-          if (left <= 0) release();
-          for (int c = 0; c < left; c += 64) {
-            uint32_t v[2][32];
-            tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
-            tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
-            tmem_ld_wait();
-            if (c + 64 >= left) release();
-            if constexpr (MODE == MODE_G) leave_g(p, &tmO, v, n + c, row0, box, gain);
-            else leave_dw(p, &tmO, v, n + c, p.v0 + row0, box, gain);
+          if constexpr (!R::kHasBoxes) {  // (G of few rows)
+            const GRow r = g_row(p, row0 + lane, gain);
+            for (int c = 0; c < left; c += 32) {
+              uint32_t v[32];
+              tmem_ld_32cols(tmem + (uint32_t)c, v);
+              tmem_ld_wait();
+              leave_g_few(p, r, v, n + c, row0 + lane);
+            }
+            release();
+          } else {
+            if (left <= 0) release();
+            for (int c = 0; c < left; c += 64) {
+              uint32_t v[2][32];
+              tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
+              tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
+              tmem_ld_wait();
+              if (c + 64 >= left) release();
+              if constexpr (MODE == MODE_G) leave_g(p, &tmO, v, n + c, row0, mine);
+              else leave_dw(p, &tmO, v, n + c, p.v0 + row0, mine, gain);
+            }
           }
         }
       }
@@ -779,17 +843,16 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) 
   const float2 none = make_float2(-3e38f, 0.f);
   float2 sum = none;
   if (slot >= 0) {
-    // a slot for each 128 of the vocabulary; a whole tile of 256 has left its sums
-    // in the first of its two
-    const int per = p.bn / 128;
+    // a slot for each 128 of the vocabulary; a tile has left its sums in the first of
+    // its slots, the second half of a cut one in its own
     for (int i0 = y; i0 < p.tiles_n; i0 += Y * U) {
       float2 v[U][2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * Y;
-        const float2 *part = p.part + (int64_t)i * per * p.r.rows_pad + slot;
+        const float2 *part = p.part + ((int64_t)i * p.bn >> 7) * p.r.rows_pad + slot;
         v[u][0] = i < p.tiles_n ? part[0] : none;
-        v[u][1] = i < p.tiles_n && per == 2 && i * 256 + 128 < p.a.vocab && tile_at(tiles, slot / p.tile_m, i) >= tiles.full
+        v[u][1] = i < p.tiles_n && p.bn == 256 && i * 256 + 128 < p.a.vocab && tile_at(tiles, slot / p.tile_m, i) >= tiles.full
                       ? part[p.r.rows_pad]
                       : none;
       }
@@ -976,10 +1039,13 @@ mm_status tile_places(LaunchCtx &ctx, int *places) {
 
 // A form of the products: few rows on single SMs.
 struct Form {
-  int cg;  // 1 or 2
+  int cg;      // 1 or 2
+  int a_rows;  // of A that a CTA loads
   int tile_m() const { return 128 * cg; }
 };
-Form form_of(int rows) { return Form{rows <= 128 ? 1 : 2}; }
+Form form_of(int rows) {
+  return rows > 128 ? Form{2, 128} : Form{1, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128};
+}
 
 struct Maps {
   CUtensorMap a, b, bh, o;
@@ -1007,15 +1073,30 @@ mm_status launch_tiles(Form f, TileParams &p, const Maps &m, int64_t M, LaunchCt
 // Width of a product's tiles along N.
 int tile_width(int64_t N) { return N <= 128 ? 128 : 256; }
 
+// The same for few rows, whose products read W once: the SMs' shares as equal as tiles
+// of a multiple of 32 make them (32000 tokens: 143 tiles of 224 on 152 SMs, 125 of 256).
+int tile_width_few(int64_t N, int places) {
+  int best = 256;
+  int64_t least = INT64_MAX;
+  for (int w = 256; w >= 128; w -= 32) {
+    const int64_t tiles = (N + w - 1) / w, rem = tiles % places;
+    // (the last wave's tiles are halved where that fits: w 256 only)
+    const int64_t span = tiles / places * w + (rem == 0 ? 0 : w == 256 && 2 * rem <= places ? w / 2 : w);
+    if (span < least) least = span, best = w;
+  }
+  return best;
+}
+
 // x W^T over `width` tokens from v0 on, LSE or G.
-mm_status logits_maps(Maps *m, TileParams &p, Form f, const TmaRows &w) {
-  p.bn = tile_width(p.width);
+mm_status logits_maps(Maps *m, TileParams &p, Form f, const TmaRows &w, int places) {
+  p.a_rows = f.a_rows;
+  p.bn = f.cg == 1 ? tile_width_few(p.width, places) : tile_width(p.width);
   p.tiles_n = (p.width + p.bn - 1) / p.bn;
   p.num_kb = (p.cols + 63) / 64;
   const char *base = static_cast<const char *>(w.p) + (int64_t)p.v0 * w.ld;
   const int64_t tokens = std::min(p.width, p.vocab - p.v0);
   mm_status st;
-  if (p.r.count && (st = rows_map(&m->a, p.tx, p.r.x, p.cols, p.r.rows_pad, p.r.ldx, 128)) != MM_OK) return st;
+  if (p.r.count && (st = rows_map(&m->a, p.tx, p.r.x, p.cols, p.r.rows_pad, p.r.ldx, f.a_rows)) != MM_OK) return st;
   if ((st = rows_map(&m->b, p.tx, base, p.cols, tokens, w.ld / 2, p.bn / f.cg)) != MM_OK) return st;
   return rows_map(&m->bh, p.tx, base, p.cols, tokens, w.ld / 2, p.bn / f.cg / 2);
 }
@@ -1041,8 +1122,8 @@ mm_status place_weight(const LossArgs &a, TmaRows *w, PackRows *pack, LaunchCtx 
 bool is_direct(const LossArgs &a, Form f) {
   return f.cg == 1 && addressable(TmaRows{a.x, a.ldx * 2, a.rows, 0}) && addressable(TmaRows{a.weight, a.ldw * 2, a.vocab, 0});
 }
-mm_status direct_map(CUtensorMap *map, const LossArgs &a) {
-  return rows_map(map, a.tx, a.x, a.cols, a.rows, a.rows == 1 ? ((int64_t)a.cols + 7) / 8 * 8 : a.ldx, 128);
+mm_status direct_map(CUtensorMap *map, const LossArgs &a, Form f) {
+  return rows_map(map, a.tx, a.x, a.cols, a.rows, a.rows == 1 ? ((int64_t)a.cols + 7) / 8 * 8 : a.ldx, f.a_rows);
 }
 
 TileParams tile_params(const LossArgs &a, LaunchCtx &ctx) {
@@ -1105,8 +1186,8 @@ mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
   if ((st = place_weight(a, &w, &pack, ctx)) != MM_OK) return st;
   if (!direct && (st = launch_gather(a, p.r, false, pack, ctx)) != MM_OK) return st;
   p.width = a.vocab;
-  if ((st = logits_maps(&m, p, f, w)) != MM_OK) return st;
-  if (direct && (st = direct_map(&m.a, a)) != MM_OK) return st;
+  if ((st = logits_maps(&m, p, f, w, ctx.dev->info.sms)) != MM_OK) return st;
+  if (direct && (st = direct_map(&m.a, a, f)) != MM_OK) return st;
   m.o = m.a;  // (none)
   if ((st = launch_tiles<MODE_LSE>(f, p, m, a.rows, ctx)) != MM_OK) return st;
   LossParams l{a, p.r, p.part, p.hit, f.tile_m(), p.bn, p.tiles_n, p.places};
@@ -1160,19 +1241,22 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   p.vec = (uintptr_t)a.dweight % 16 == 0 && a.lddw % 8 == 0 && a.cols % 8 == 0 && a.lddw < (1LL << 37);
   if (!direct && (st = launch_gather(a, p.r, true, pack, ctx)) != MM_OK) return st;
   p.piece_kb = piece / 64;
+  p.boxes = boxes_of(a.rows);
+  p.g = g;
+  p.ldg = piece;
   for (p.v0 = 0; p.v0 < a.vocab; p.v0 += piece) {
     Maps m;
     p.first = p.v0 == 0;
     p.width = std::min(piece, (a.vocab - p.v0 + 63) / 64 * 64);
-    if ((st = logits_maps(&m, p, f, w)) != MM_OK) return st;
-    if (direct && (st = direct_map(&m.a, a)) != MM_OK) return st;
+    if ((st = logits_maps(&m, p, f, w, ctx.dev->info.sms)) != MM_OK) return st;
+    if (direct && (st = direct_map(&m.a, a, f)) != MM_OK) return st;
     if ((st = rows_map(&m.o, p.tx, g, p.width, rows_pad, piece, 32)) != MM_OK) return st;
     if ((st = launch_tiles<MODE_G>(f, p, m, a.rows, ctx)) != MM_OK) return st;
     p.bn = bn_cols;
     p.tiles_n = tiles_cols;
     if (a.dx) {
       p.num_kb = p.width / 64;
-      if ((st = rows_map(&m.a, p.tx, g, p.width, rows_pad, piece, 128)) != MM_OK) return st;
+      if ((st = rows_map(&m.a, p.tx, g, p.width, rows_pad, piece, f.a_rows)) != MM_OK) return st;
       if ((st = rows_map(&m.b, p.tx, static_cast<const char *>(w.p) + (int64_t)p.v0 * w.ld, a.cols,
                          std::min(p.width, a.vocab - p.v0), w.ld / 2, 64)) != MM_OK)
         return st;
