@@ -541,9 +541,9 @@ mm_status mm_cross_entropy(const void *x, const void *weight, const void *target
  *   dweight   vocab x cols, overwritten; NULL: not computed.
  *             Both are of type dt.c, which is dt.a.
  * g, divided by the largest |dloss|, is rounded to dt.a (f16: after 2^14 is
- * taken in) before the two products, whose sums are fp32; equal calls give equal
- * bits.  In f16 positions whose dloss is below 2^-20 of the largest lose bits of
- * their dx.  cols of 0 is a no-op; rows of 0 writes zeros to dweight.
+ * taken in; up to 128 rows: to the sum of two such values) before the two
+ * products, whose sums are fp32; equal calls give equal bits.  In f16 positions
+ * whose dloss is below 2^-20 of the largest lose bits of their dx.  cols of 0 is a no-op; rows of 0 writes zeros to dweight.
  * rows, cols, vocab < 2^30.
  */
 mm_status mm_cross_entropy_backward(const void *x, const void *weight, const void *targets, const float *lse,

@@ -249,6 +249,7 @@ struct TileParams {
   int bn, tiles_n, places;
   int a_rows;        // CG = 1: the rows of A that are loaded
   int boxes;         // DW: boxes a warp
+  int two;           // DW: g is two values (few rows)
   int num_kb;        // 64-element blocks of K (DW: of the rows that count)
   int piece_kb;      // DX: those of a whole piece
   float2 *part;      // LSE: [128 of the vocabulary][rows_pad] (r, s)
@@ -271,8 +272,8 @@ struct TileParams {
 // Few rows (CG = 1) wait for W, so their A has room for no more rows than there are (a
 // multiple of 16): the MMA's other rows read what lies behind, and nobody reads theirs.
 // That leaves more of the ring to W in flight.  A pair's tiles in 16 bits leave through
-// boxes in shared memory, one for each warp that takes them out, or two where K is a
-// stage or two and the ring need not be long (see boxes_of).
+// boxes in shared memory, one for each warp that takes them out, or two where K is a few
+// stages and the ring need not be long.
 constexpr uint32_t kSmemBytes = 227 * 1024, kBarBytes = 1024;
 template <int MODE, int CG>
 struct Ring {
@@ -292,9 +293,6 @@ static_assert(Ring<MODE_G, 2>::stages(128, 1) == 5 && Ring<MODE_DW, 2>::stages(1
                   Ring<MODE_LSE, 2>::stages(128, 1) == 6 && Ring<MODE_LSE, 1>::stages(128, 1) == 4 &&
                   Ring<MODE_G, 1>::stages(16, 1) == 6,
               "what the measurements were taken with");
-// Boxes a warp for dW: a product over at most two blocks of K is bound by its stores, and a
-// warp fills one box while the other is read (16 x 4096 x 32000: 51 us with one).
-inline int boxes_of(int rows) { return rows <= 128 ? 2 : 1; }
 
 __device__ __forceinline__ int row_count(const Rows &r, int rows) { return r.count ? max(1, *r.count) : rows; }
 __device__ __forceinline__ int target_of(const TileParams &p, int row) {
@@ -327,8 +325,9 @@ __device__ __forceinline__ bool all_take(bool ok) {
 // LSE: the logits are fp32 sums over K that the tensor core truncates at each step of
 // 16, towards zero, so that their error grows with K and the sum itself.  A sum over
 // kChunkKb blocks at a time, added up here in registers, rounded, keeps it at that of
-// an fp32 loop (8192 x 4096 x 131072: 2.9e-6 of the loss in one chain).
-constexpr int kChunkKb = 16;
+// an fp32 loop (8192 x 4096 x 131072: the loss off by 2.9e-6 of itself in one chain, by
+// 7e-7 in chunks of 1024 of K, by 3e-7 of 512, for 2 % of the time).
+constexpr int kChunkKb = 8;
 
 // A chunk of w columns, added to a thread's sums.
 __device__ __forceinline__ void add_chunk(float (&sum)[128], uint32_t tmem, int w, bool first) {
@@ -452,15 +451,32 @@ __device__ __forceinline__ void leave_g(const TileParams &p, const CUtensorMap *
   }
   store_box_tma(map, box, n, row0);
 }
-// Few rows: 32 columns from registers, 64 bytes a lane.
+// Few rows: 32 columns from registers, 64 bytes a lane, as two 16-bit values whose sum is
+// g to twice the bits, the second 128 rows behind the first.  Their products wait for
+// memory, so the second costs no time, and a dx or dW of few terms does not show the
+// rounding of one g (off by up to half a step, as its own rounding).
+constexpr int kLowRows = 128;
+__device__ __forceinline__ float unpack(int tx, uint32_t w, int odd) {
+  if (tx == MM_BF16) return __uint_as_float(odd ? w & 0xffff0000u : w << 16);
+  const __half2 v = *reinterpret_cast<const __half2 *>(&w);
+  return odd ? __high2float(v) : __low2float(v);
+}
 __device__ __forceinline__ void leave_g_few(const TileParams &p, const GRow &r, uint32_t (&v)[32], int n, int row) {
   make_g(p, r, v, p.v0 + n);
-  uint4 *to = reinterpret_cast<uint4 *>(p.g + (int64_t)row * p.ldg + n);
-  const auto f = [&](int i) { return __uint_as_float(v[i]); };
+  uint4 *high = reinterpret_cast<uint4 *>(p.g + (int64_t)row * p.ldg + n);
+  uint4 *low = reinterpret_cast<uint4 *>(p.g + (int64_t)(row + kLowRows) * p.ldg + n);
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    to[j] = make_uint4(pack2(p.tx, f(8 * j), f(8 * j + 1)), pack2(p.tx, f(8 * j + 2), f(8 * j + 3)),
-                       pack2(p.tx, f(8 * j + 4), f(8 * j + 5)), pack2(p.tx, f(8 * j + 6), f(8 * j + 7)));
+  for (int j = 0; j < 4; ++j) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = __uint_as_float(v[8 * j + 2 * k]), b = __uint_as_float(v[8 * j + 2 * k + 1]);
+      h[k] = pack2(p.tx, a, b);
+      l[k] = pack2(p.tx, a - unpack(p.tx, h[k], 0), b - unpack(p.tx, h[k], 1));
+    }
+    high[j] = make_uint4(h[0], h[1], h[2], h[3]);
+    low[j] = make_uint4(l[0], l[1], l[2], l[3]);
+  }
 }
 
 __device__ __forceinline__ void leave_dw(const TileParams &p, const CUtensorMap *map, uint32_t (&v)[2][32], int n, int v0,
@@ -539,9 +555,11 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
                 const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmO,
                 const TileParams p) {
   using R = Ring<MODE, CG>;
+  // (DX of few rows: both of g's values)
+  constexpr int kAParts = MODE == MODE_DX && CG == 1 ? 2 : 1;
   const int a_rows = CG == 1 ? p.a_rows : 128;
-  const uint32_t a_bytes = (uint32_t)a_rows * 128, stage_bytes = a_bytes + R::kB;
-  const int S = CG == 1 ? R::stages(a_rows, 1) : MODE == MODE_DW ? R::stages(128, p.boxes) : R::stages(128, 1);
+  const uint32_t a_bytes = (uint32_t)(kAParts * a_rows) * 128, stage_bytes = a_bytes + R::kB;
+  const int S = CG == 1 ? R::stages(kAParts * a_rows, 1) : MODE == MODE_DW ? R::stages(128, p.boxes) : R::stages(128, 1);
   constexpr bool kMnA = MODE == MODE_DW, kMnB = MODE == MODE_DX || MODE == MODE_DW;
   constexpr bool kChunk = MODE == MODE_LSE;
   pdl_launch_dependents();
@@ -600,7 +618,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
   const int rows = row_count(p.r, p.rows);
   const Tiles tiles = tiles_of(MODE == MODE_DW ? p.width : rows, 128 * CG, p.tiles_n, p.bn, p.places,
                                MODE == MODE_DX ? max_parts_of(p.piece_kb) : 0);
-  const int num_kb = MODE == MODE_DW ? (rows + 63) / 64 : p.num_kb;
+  const int num_kb = MODE == MODE_DW ? (rows + 63) / 64 * (p.two ? 2 : 1) : p.num_kb;
   // the blocks of K of a unit
   const auto k_of = [&](const Unit &u, int i, int &kb0) {
     kb0 = 0;
@@ -624,13 +642,19 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
           break;
         }
         const uint32_t sa = smem_u32(ring + stage * stage_bytes), sb = sa + a_bytes, bar = leader_full0 + 8 * stage;
-        if (leader) mbar_expect_tx(full0 + 8 * stage, (uint32_t)(CG * (a_rows + nh)) * 128);
-        if (!kMnA) load_box<CG>(sa, &tmA, bar, kb * 64, m0);
-        else
-          for (int j = 0; j < 2; ++j) load_box<CG>(sa + j * 8192, &tmA, bar, m0 + j * 64, kb * 64);
+        if (leader) mbar_expect_tx(full0 + 8 * stage, (uint32_t)(CG * (kAParts * a_rows + nh)) * 128);
+        // (dW of few rows: both of g's values, one after the other along K)
+        const bool low = MODE == MODE_DW && p.two && 2 * kb >= num_kb;
+        const int xb = low ? kb - num_kb / 2 : kb;
+        if (kMnA) {
+          for (int j = 0; j < 2; ++j) load_box<CG>(sa + j * 8192, &tmA, bar, m0 + j * 64, (low ? kLowRows : 0) + xb * 64);
+        } else {
+          load_box<CG>(sa, &tmA, bar, kb * 64, m0);
+          if (kAParts == 2) load_box<CG>(sa + a_rows * 128, &tmA, bar, kb * 64, kLowRows);
+        }
         if (!kMnB) load_box<CG>(sb, u.w == p.bn ? &tmB : &tmBh, bar, kb * 64, n0);
         else
-          for (int j = 0; j < nh / 64; ++j) load_box<CG>(sb + j * 8192, &tmB, bar, n0 + j * 64, kb * 64);
+          for (int j = 0; j < nh / 64; ++j) load_box<CG>(sb + j * 8192, &tmB, bar, n0 + j * 64, xb * 64);
         if (++stage == S) {
           stage = 0;
           phase ^= 1;
@@ -691,6 +715,11 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f16<CG>(d, ad + (kMnA ? 128 : 2) * kk, bd + (kMnB ? 128 : 2) * kk, idesc, (!start || kk > 0) ? 1u : 0u);
+          if constexpr (kAParts == 2) {
+            const uint64_t al = ad + (uint64_t)(a_rows * 128 >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_f16<CG>(d, al + 2 * kk, bd + 128 * kk, idesc, 1u);
+          }
           if (CG == 2) mma_commit_pair(empty0 + 8 * stage);
           else mma_commit<1>(empty0 + 8 * stage);
           if (++stage == S) {
@@ -1241,7 +1270,8 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   p.vec = (uintptr_t)a.dweight % 16 == 0 && a.lddw % 8 == 0 && a.cols % 8 == 0 && a.lddw < (1LL << 37);
   if (!direct && (st = launch_gather(a, p.r, true, pack, ctx)) != MM_OK) return st;
   p.piece_kb = piece / 64;
-  p.boxes = boxes_of(a.rows);
+  p.two = f.cg == 1;
+  p.boxes = p.two ? 2 : 1;
   p.g = g;
   p.ldg = piece;
   for (p.v0 = 0; p.v0 < a.vocab; p.v0 += piece) {

@@ -9,8 +9,9 @@ truncate), u the unit roundoff of the 16-bit type, C columns, V tokens:
              and its own rounding to fp32, e |lse|
   p          relative 2 L + e (8 + 4 max|l|): the exponential of a logit less lse,
              lse taken as given
-  g          that on p, and u |g| of its rounding (f16: and half the least value
-             over 2^14, times the largest |dloss|)
+  g          that on p, and u |g| of its rounding (up to 128 rows, where it is held in
+             two values, u^2 |g|: the second is at most u |g| and off by u of itself;
+             f16: and half the least value over 2^14, times the largest |dloss|)
   dx, dW     the errors of g against |W|, |x|; e (n + 16) sum|g W| of the sums;
              u of the result's rounding
 """
@@ -99,7 +100,7 @@ class Problem:
         at = torch.where(ok, self.targets.long()[:, None], 0)
         g.scatter_(1, at, g.gather(1, at) - 1)
         g = g * d
-        off = rel * p * d.abs() * (1 + u) + (u + 4 * E) * g.abs()
+        off = rel * p * d.abs() * (1 + u) + ((u if self.rows > 128 else u * u) + 4 * E) * g.abs()
         if self.t == H:
             off = torch.where(ok, off + LEAST[H] / 2 / 2 ** 14 * d.abs().max(), 0.0)
         for got, want, size, miss, n in ((dx, g @ w, g.abs() @ w.abs(), off @ w.abs(), self.vocab),
