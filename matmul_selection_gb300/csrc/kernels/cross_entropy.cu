@@ -249,7 +249,7 @@ struct TileParams {
   int bn, tiles_n, places;
   int a_rows;        // CG = 1: the rows of A that are loaded
   int boxes;         // DW: boxes a warp
-  int two;           // DW: g is two values (few rows)
+  int low;           // few rows: g is two values, the second in the rows from here on (else 0)
   int num_kb;        // 64-element blocks of K (DW: of the rows that count)
   int piece_kb;      // DX: those of a whole piece
   float2 *part;      // LSE: [128 of the vocabulary][rows_pad] (r, s)
@@ -329,7 +329,7 @@ __device__ __forceinline__ bool all_take(bool ok) {
 // 7e-7 in chunks of 1024 of K, by 3e-7 of 512, for 2 % of the time).
 constexpr int kChunkKb = 8;
 
-// A chunk of w columns, added to a thread's sums.
+// A chunk of w columns, added to a thread's sums (the first: the sums themselves).
 __device__ __forceinline__ void add_chunk(float (&sum)[128], uint32_t tmem, int w, bool first) {
 #pragma unroll
   for (int b = 0; b < 4; ++b)
@@ -452,10 +452,11 @@ __device__ __forceinline__ void leave_g(const TileParams &p, const CUtensorMap *
   store_box_tma(map, box, n, row0);
 }
 // Few rows: 32 columns from registers, 64 bytes a lane, as two 16-bit values whose sum is
-// g to twice the bits, the second 128 rows behind the first.  Their products wait for
+// g to twice the bits, the second some rows behind the first (p.low).  Their products wait for
 // memory, so the second costs no time, and a dx or dW of few terms does not show the
 // rounding of one g (off by up to half a step, as its own rounding).
-constexpr int kLowRows = 128;
+// Up to 32 rows the two fill the 64 rows of one block of dW's K, with x twice.
+constexpr int kFewestRows = 32;
 __device__ __forceinline__ float unpack(int tx, uint32_t w, int odd) {
   if (tx == MM_BF16) return __uint_as_float(odd ? w & 0xffff0000u : w << 16);
   const __half2 v = *reinterpret_cast<const __half2 *>(&w);
@@ -464,7 +465,7 @@ __device__ __forceinline__ float unpack(int tx, uint32_t w, int odd) {
 __device__ __forceinline__ void leave_g_few(const TileParams &p, const GRow &r, uint32_t (&v)[32], int n, int row) {
   make_g(p, r, v, p.v0 + n);
   uint4 *high = reinterpret_cast<uint4 *>(p.g + (int64_t)row * p.ldg + n);
-  uint4 *low = reinterpret_cast<uint4 *>(p.g + (int64_t)(row + kLowRows) * p.ldg + n);
+  uint4 *low = reinterpret_cast<uint4 *>(p.g + (int64_t)(row + p.low) * p.ldg + n);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t h[4], l[4];
@@ -539,7 +540,7 @@ __device__ __forceinline__ float prepare_few(const TileParams &p, int cta, int c
   if (cta == 0 && t == 0) *p.r.gain = top;
   const int pieces = (int)(p.r.ldx / 8), rows = (p.rows + 63) / 64 * 64;
   for (int i = cta * 256 + t; i < rows * pieces; i += ctas * 256) {
-    const int row = i / pieces, c = i - row * pieces;
+    const int c = i % pieces, row = i / pieces & (p.low - 1);  // (twice, where p.low is 32)
     RowPiece<2> v;
     const uint8_t *from = static_cast<const uint8_t *>(p.x) + (int64_t)row * p.ldx * 2;
     const bool live = target_of(p, row) >= 0;
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
   const int rows = row_count(p.r, p.rows);
   const Tiles tiles = tiles_of(MODE == MODE_DW ? p.width : rows, 128 * CG, p.tiles_n, p.bn, p.places,
                                MODE == MODE_DX ? max_parts_of(p.piece_kb) : 0);
-  const int num_kb = MODE == MODE_DW ? (rows + 63) / 64 * (p.two ? 2 : 1) : p.num_kb;
+  const int num_kb = MODE == MODE_DW ? (rows + 63) / 64 * (p.low > 64 ? 2 : 1) : p.num_kb;
   // the blocks of K of a unit
   const auto k_of = [&](const Unit &u, int i, int &kb0) {
     kb0 = 0;
@@ -644,13 +645,13 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
         const uint32_t sa = smem_u32(ring + stage * stage_bytes), sb = sa + a_bytes, bar = leader_full0 + 8 * stage;
         if (leader) mbar_expect_tx(full0 + 8 * stage, (uint32_t)(CG * (kAParts * a_rows + nh)) * 128);
         // (dW of few rows: both of g's values, one after the other along K)
-        const bool low = MODE == MODE_DW && p.two && 2 * kb >= num_kb;
+        const bool low = MODE == MODE_DW && p.low > 64 && 2 * kb >= num_kb;
         const int xb = low ? kb - num_kb / 2 : kb;
         if (kMnA) {
-          for (int j = 0; j < 2; ++j) load_box<CG>(sa + j * 8192, &tmA, bar, m0 + j * 64, (low ? kLowRows : 0) + xb * 64);
+          for (int j = 0; j < 2; ++j) load_box<CG>(sa + j * 8192, &tmA, bar, m0 + j * 64, (low ? p.low : 0) + xb * 64);
         } else {
           load_box<CG>(sa, &tmA, bar, kb * 64, m0);
-          if (kAParts == 2) load_box<CG>(sa + a_rows * 128, &tmA, bar, kb * 64, kLowRows);
+          if (kAParts == 2) load_box<CG>(sa + a_rows * 128, &tmA, bar, kb * 64, p.low);
         }
         if (!kMnB) load_box<CG>(sb, u.w == p.bn ? &tmB : &tmBh, bar, kb * 64, n0);
         else
@@ -767,23 +768,22 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
       if constexpr (MODE == MODE_LSE) {
         const bool live = row0 < rows && u.n0 < p.vocab;  // (else a half tile past the end)
         float l[128];
+        bool good = true;
         for (int k = 0; k < num_kb; k += kChunkKb) {
-          // the eight warps go on or give up together
-          if (!(ok = all_take(warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)))) break;
+          if (!(good = warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore))) break;
           fence_after();
           if (live) add_chunk(l, lanes + (uint32_t)(acc * 256 + c0), wide, k == 0);
           release();
         }
-        if (!ok) break;
         // the upper half's sums to the lower half's warps; a buffer for each of two turns
         float2 *upper = reinterpret_cast<float2 *>(boxes) + turn * 128 + q * 32 + lane;
         float2 sum = make_float2(-3e38f, 0.f);
-        if (live) {
+        if (live && good) {
           const int row = row0 + lane;
           sum = sum_exp(p, l, n, wide, target_of(p, row), p.hit + row);
           if (half) *upper = sum;
         }
-        all_take(true);
+        if (!(ok = all_take(good))) break;  // the eight warps go on or give up together
         if (live && !half) p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row0 + lane] = join_sums(sum, *upper);
       } else {
         if (!warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)) break;
@@ -804,7 +804,8 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
           const int left = min(wide, end - n);
           if constexpr (!R::kHasBoxes) {  // (G of few rows)
             const GRow r = g_row(p, row0 + lane, gain);
-            for (int c = 0; c < left; c += 32) {
+            // (rows from p.low on are the second values')
+            for (int c = 0; c < left && row0 < p.low; c += 32) {
               uint32_t v[32];
               tmem_ld_32cols(tmem + (uint32_t)c, v);
               tmem_ld_wait();
@@ -1270,8 +1271,8 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   p.vec = (uintptr_t)a.dweight % 16 == 0 && a.lddw % 8 == 0 && a.cols % 8 == 0 && a.lddw < (1LL << 37);
   if (!direct && (st = launch_gather(a, p.r, true, pack, ctx)) != MM_OK) return st;
   p.piece_kb = piece / 64;
-  p.two = f.cg == 1;
-  p.boxes = p.two ? 2 : 1;
+  p.low = f.cg == 2 ? 0 : direct && a.rows <= kFewestRows ? kFewestRows : 128;
+  p.boxes = p.low ? 2 : 1;
   p.g = g;
   p.ldg = piece;
   for (p.v0 = 0; p.v0 < a.vocab; p.v0 += piece) {
