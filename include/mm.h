@@ -294,7 +294,7 @@ double mm_roofline_limit_ns(double ops, double peak_ops_per_s, double bytes,
  *   (2000000: how long a wait of a 1-SM tensor-core kernel's main loop may
  *   last before the kernel gives up, records MM_ERR_TIMEOUT's cause in its
  *   error word and returns; its drain waits keep 2 s; likewise the waits of
- *   the operators around a quantised linear layer, see mm_operator_status),
+ *   the operators, see mm_operator_status),
  *   wait_stall (0; test hook: 1 makes the warps of those kernels that compute
  *   first wait on a barrier that nothing arrives on, so that the wait limit
  *   runs out and the kernel's abort path runs; it never faults or hangs the
