@@ -497,8 +497,9 @@ mm_status mm_embedding(const void *weight, const void *tokens, void *out, int64_
 /*
  * mm_embedding_backward -- the gradient of mm_embedding to its matrix:
  *   dweight[v] = base[v] + scale * sum over {t : tokens[t] = v} of dout[t]
- * The sum is held in fp32 and rounded once, with the base; its order follows t
- * and depends on the sizes and the tokens only, so equal calls give equal bits.
+ * The sum is held in fp32 and rounded once, with the base; its order follows t,
+ * in runs that depend on the sizes, the alignment, the tokens and the device only,
+ * so equal calls give equal bits.
  *   dout      rows x cols, type dt.c; tokens: type dt.b.
  *   base      the gradient that reaches the matrix from elsewhere (the loss of
  *             tied weights, an earlier batch), vocab x cols of type dt.a; NULL:

@@ -538,14 +538,16 @@ __device__ __forceinline__ float prepare_few(const TileParams &p, int cta, int c
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (top == 0.f) top = 1.f;
   if (cta == 0 && t == 0) *p.r.gain = top;
-  const int pieces = (int)(p.r.ldx / 8), rows = (p.rows + 63) / 64 * 64;
-  for (int i = cta * 256 + t; i < rows * pieces; i += ctas * 256) {
-    const int c = i % pieces, row = i / pieces & (p.low - 1);  // (twice, where p.low is 32)
+  const int64_t pieces = p.r.ldx / 8, all = (p.rows + 63) / 64 * 64 * pieces;
+  for (int64_t i = cta * 256 + t; i < all; i += ctas * 256) {
+    const int row = (int)(i / pieces);
+    const int64_t c = i - row * pieces;
     RowPiece<2> v;
-    const uint8_t *from = static_cast<const uint8_t *>(p.x) + (int64_t)row * p.ldx * 2;
-    const bool live = target_of(p, row) >= 0;
-    if (live) v.load(from, (int64_t)p.cols * 2, (int64_t)c * 16);
-    reinterpret_cast<uint4 *>(p.r.x)[i] = live ? v.value(from, (int64_t)p.cols * 2, (int64_t)c * 16) : make_uint4(0, 0, 0, 0);
+    const int source = row & (p.low - 1);  // (where p.low is 32 the rows stand twice)
+    const uint8_t *from = static_cast<const uint8_t *>(p.x) + (int64_t)source * p.ldx * 2;
+    const bool live = target_of(p, source) >= 0;
+    if (live) v.load(from, (int64_t)p.cols * 2, c * 16);
+    reinterpret_cast<uint4 *>(p.r.x)[i] = live ? v.value(from, (int64_t)p.cols * 2, c * 16) : make_uint4(0, 0, 0, 0);
   }
   return top;
 }
@@ -914,70 +916,81 @@ struct DxParams {
   int tile_m, bn, tiles_n, places, piece_kb, acc_cols;  // of the product
   int vec;  // dx's rows start on 16 bytes
 };
-// A warp 32 rows by 4 Q columns, a row a lane: a tile's parts added in order, scaled and
-// rounded.  Then the rows that do not count.  Q: 8 (64 bytes of a row), or 2 where the
-// tiles are few, and cut in many parts: more warps (16 rows of 4096 in 9 parts: 12.7 us
-// with 8, 5.2 with 2).  Neighbouring warps take neighbouring blocks of the sums, and the
-// whole tiles' lie row block by row block: 36 us at 6144 x 4096 (tile by tile 55; a
-// tile's columns a warp, accesses 32 KB apart, 200).
-template <int Q>
-__global__ void __launch_bounds__(256, Q == 8 ? 3 : 4) dx_kernel(const DxParams p) {
+// 32 rows, a row a lane, by 4 Q columns from `col` on: the parts (part_at apart) added in
+// order, U of them read at once, scaled and rounded.
+template <int Q, int U>
+__device__ __forceinline__ void round_dx(const DxParams &p, const float4 *from, int parts, int64_t part_at, int rb, int col,
+                                         int count, float gain) {
+  float4 v[Q];
+#pragma unroll
+  for (int k = 0; k < Q; ++k) v[k] = from[k * 32];
+  for (int s = 1; s < parts; s += U) {
+    float4 w[U][Q];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < Q; ++k)
+        w[u][k] = s + u < parts ? from[(s + u) * part_at + k * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < Q; ++k)
+        v[k].x += w[u][k].x, v[k].y += w[u][k].y, v[k].z += w[u][k].z, v[k].w += w[u][k].w;
+  }
+  const int i = rb * 32 + (threadIdx.x & 31);
+  if (i >= count || (!p.r.count && valid_target(p.a, i) < 0)) return;
+  uint32_t w[2 * Q];
+#pragma unroll
+  for (int k = 0; k < Q; ++k) {
+    w[2 * k] = pack2(p.a.tx, v[k].x * gain, v[k].y * gain);
+    w[2 * k + 1] = pack2(p.a.tx, v[k].z * gain, v[k].w * gain);
+  }
+  uint16_t *to = static_cast<uint16_t *>(p.a.dx) + (int64_t)(p.r.count ? p.r.row[i] : i) * p.a.lddx + col;
+  const int left = p.a.cols - col;
+  if (p.vec && left >= 4 * Q) {
+#pragma unroll
+    for (int k = 0; k < Q / 2; ++k)
+      reinterpret_cast<uint4 *>(to)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4 * Q; ++e)
+      if (e < left) to[e] = (uint16_t)(w[e >> 1] >> (e & 1) * 16);
+  }
+}
+// A warp 32 x 32 of the whole tiles' sums (64 bytes of a row), neighbouring warps
+// neighbouring blocks, row block by row block; then 32 x 8 of the cut tiles', whose many
+// parts want more warps; then the rows that do not count.  (6144 x 4096: 33 us; the
+// sums tile by tile 55; a tile's columns a warp, accesses 32 KB apart, 200.)
+__global__ void __launch_bounds__(256, 4) dx_kernel(const DxParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int U = Q == 8 ? 1 : 4;  // parts read at once
   const int lane = threadIdx.x & 31, count = row_count(p.r, p.a.rows);
   const float gain = *p.r.gain * (p.a.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
   const uint32_t warps = gridDim.x * 8, warp = blockIdx.x * 8 + (threadIdx.x >> 5);
-  uint16_t *dx = static_cast<uint16_t *>(p.a.dx);
   const Tiles tiles = tiles_of(count, p.tile_m, p.tiles_n, p.bn, p.places, max_parts_of(p.piece_kb));
   const int log_rows = p.tile_m == 256 ? 3 : 2, log_cols = p.bn == 256 ? 3 : 2;  // blocks of 32 a tile
-  const uint32_t across = (uint32_t)(p.a.cols + 4 * Q - 1) / (4 * Q);
-  const int64_t part_at = (int64_t)p.tile_m * p.bn / 4;  // float4 a unit
-  // (as many blocks as there are 4 KB or 1 KB of sums: they count in 32 bits)
-  for (uint32_t b = warp; b < (uint32_t)((count + 31) / 32) * across; b += warps) {
-    const int rb = (int)(b / across), col = (int)(b - (uint32_t)rb * across) * 4 * Q, cb = col / 32;
-    const int t = tile_at(tiles, rb >> log_rows, cb >> log_cols);
-    const int parts = t < tiles.full ? 1 : tiles.parts;
-    const int block = ((rb & ((1 << log_rows) - 1)) << log_cols) + (cb & ((1 << log_cols) - 1));
-    const float *at = t < tiles.full ? p.acc + ((int64_t)rb * p.acc_cols + cb) * 1024
-                                     : p.acc_cut + (int64_t)(t - tiles.full) * parts * p.tile_m * p.bn + block * 1024;
-    const float4 *from = reinterpret_cast<const float4 *>(at) + col % 32 * 8 + lane;
-    float4 v[Q];
-#pragma unroll
-    for (int k = 0; k < Q; ++k) v[k] = from[k * 32];
-    for (int s = 1; s < parts; s += U) {
-      float4 w[U][Q];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int k = 0; k < Q; ++k)
-          w[u][k] = s + u < parts ? from[(s + u) * part_at + k * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int k = 0; k < Q; ++k)
-          v[k].x += w[u][k].x, v[k].y += w[u][k].y, v[k].z += w[u][k].z, v[k].w += w[u][k].w;
-    }
-    const int i = rb * 32 + lane;
-    if (i >= count || (!p.r.count && valid_target(p.a, i) < 0)) continue;
-    uint32_t w[2 * Q];
-#pragma unroll
-    for (int k = 0; k < Q; ++k) {
-      w[2 * k] = pack2(p.a.tx, v[k].x * gain, v[k].y * gain);
-      w[2 * k + 1] = pack2(p.a.tx, v[k].z * gain, v[k].w * gain);
-    }
-    uint16_t *to = dx + (int64_t)(p.r.count ? p.r.row[i] : i) * p.a.lddx + col;
-    const int left = p.a.cols - col;
-    if (p.vec && left >= 4 * Q) {
-#pragma unroll
-      for (int k = 0; k < Q / 2; ++k)
-        reinterpret_cast<uint4 *>(to)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4 * Q; ++e)
-        if (e < left) to[e] = (uint16_t)(w[e >> 1] >> (e & 1) * 16);
+  if (tiles.full > 0) {
+    // (as many blocks as there are 4 KB of sums: they count in 32 bits)
+    const uint32_t blocks = (uint32_t)((count + 31) / 32) * (uint32_t)p.acc_cols;
+    for (uint32_t b = warp; b < blocks; b += warps) {
+      const int rb = (int)(b / (uint32_t)p.acc_cols), cb = (int)(b - (uint32_t)rb * (uint32_t)p.acc_cols);
+      if (tile_at(tiles, rb >> log_rows, cb >> log_cols) < tiles.full)
+        round_dx<8, 1>(p, reinterpret_cast<const float4 *>(p.acc) + (int64_t)b * 256 + lane, 1, 0, rb, cb * 32, count, gain);
     }
   }
+  const int log_strips = log_cols + 2, log_units = log_rows + log_strips;
+  const uint32_t cut = (uint32_t)(tiles.tiles_m * tiles.tiles_n - tiles.full) << log_units;
+  for (uint32_t b = warp; b < cut; b += warps) {
+    const int t = (int)(b >> log_units), r = (int)(b >> log_strips) & ((1 << log_rows) - 1);
+    const int strip = (int)b & ((1 << log_strips) - 1);
+    const Unit u = unit_at(tiles, p.bn, tiles.full + t * tiles.parts);
+    const int rb = (u.tm << log_rows) + r, col = u.n0 + strip * 8;
+    if (rb * 32 >= count || col >= p.a.cols) continue;
+    const float4 *from = reinterpret_cast<const float4 *>(p.acc_cut) + (int64_t)t * tiles.parts * p.tile_m * p.bn / 4 +
+                         ((r << log_cols) + (strip >> 2)) * 256 + (strip & 3) * 64 + lane;
+    round_dx<2, 4>(p, from, tiles.parts, (int64_t)p.tile_m * p.bn / 4, rb, col, count, gain);
+  }
+  uint16_t *dx = static_cast<uint16_t *>(p.a.dx);
   for (int64_t row = warp; row < p.a.rows; row += warps)
     if (p.r.count ? p.r.slot[row] < 0 : valid_target(p.a, row) < 0)
       for (int c = lane; c < p.a.cols; c += 32) dx[row * p.a.lddx + c] = 0;
@@ -1242,7 +1255,6 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   // dx: sums of all tiles, and of the parts of cut ones, at most one a place
   p.acc_cols = (a.cols + 31) / 32;
   const int bn_cols = tile_width(a.cols), tiles_cols = (a.cols + bn_cols - 1) / bn_cols;
-  const int64_t dx_tiles = ((int64_t)a.rows + f.tile_m() - 1) / f.tile_m() * tiles_cols;
   int dx_places = 0;
   mm_status st = f.cg == 1 ? tile_places<MODE_DX, 1>(ctx, &dx_places) : tile_places<MODE_DX, 2>(ctx, &dx_places);
   if (st != MM_OK) return st;
@@ -1306,7 +1318,7 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   if (!a.dx) return MM_OK;
   DxParams d{a, p.r, p.acc, p.acc_cut, f.tile_m(), bn_cols, tiles_cols, dx_places, p.piece_kb, p.acc_cols,
              (uintptr_t)a.dx % 16 == 0 && (a.lddx % 8 == 0 || a.rows == 1)};
-  cudaError_t e = launch_pdl(dx_tiles < dx_places ? dx_kernel<2> : dx_kernel<8>, dim3((unsigned)(4 * ctx.dev->info.sms)),
+  cudaError_t e = launch_pdl(dx_kernel, dim3((unsigned)(4 * ctx.dev->info.sms)),
                              dim3(256), 0, ctx.stream, dim3(1), d);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy_backward launch (dx)");
   count_operator_launch();

@@ -136,11 +136,27 @@ def test_gradients(rows, cols, vocab, t, ti):
 @pytest.mark.parametrize("rows,cols,vocab", [(2000, 520, 3001), (1025, 1536, 9000), (5000, 136, 600), (40, 264, 70001)])
 @pytest.mark.parametrize("t", [BF, H])
 def test_larger(rows, cols, vocab, t):
-    """Several tiles each way, and a vocabulary of several pieces."""
+    """Several tiles each way."""
     p = Problem(rows, cols, vocab, t, size=4.0)
     loss, lse = p.forward()
     p.check_forward(loss, lse)
     p.check_backward(*p.backward(lse=lse))
+
+
+@pytest.mark.parametrize("rows,cols,vocab", [(20, 8, 1_100_000), (100, 24, 1_050_001), (5000, 64, 60_001), (9000, 32, 70_000)])
+def test_several_pieces_of_the_vocabulary(rows, cols, vocab):
+    """More g than is held at once, so dx is added up over pieces."""
+    p = Problem(rows, cols, vocab)
+    p.check_forward(*p.forward())
+    p.check_backward(*p.backward())
+
+
+@pytest.mark.parametrize("rows,cols,vocab", [(5000, 1096, 3000), (2500, 2100, 1500), (130, 20_000, 700), (30, 40_000, 1500)])
+def test_whole_and_cut_tiles(rows, cols, vocab):
+    """More tiles of dx than places: a last wave cut along K; few rows, and rows of
+    many tiles."""
+    p = Problem(rows, cols, vocab)
+    p.check_backward(*p.backward())
 
 
 @pytest.mark.parametrize("want", [(True, False), (False, True)])
