@@ -8,9 +8,9 @@
 //
 // Backward: the places t are sorted by token (stable), so that the rows of one
 // token stand together and are added in the order of t, in registers, without
-// atomics.  Threads take equal chunks of the sorted places, however often a token
-// occurs; a token whose places go past a chunk's end leaves fp32 parts, which a
-// second kernel adds in order.
+// atomics.  Threads take nearly equal chunks of the sorted places, however often a token
+// occurs; a token of many places leaves fp32 parts, a chunk each, which a second kernel
+// adds in order.
 #include <algorithm>
 
 #include "../operators.h"
@@ -278,7 +278,11 @@ struct SumParams {
   int log_threads;
   int across;           // blocks for all chunks of a slab of columns
 };
-constexpr int kMinLogThreads = 3, kMinChunk = 8, kMaxChunk = 64, kGroupPlaces = kMaxChunk + 2;
+// A border between two chunks moves up to kSnap places on, to where a token ends; inside a
+// longer run it stays.  (8192 x 4096 66 -> 63 us, 65536 x 1024 151 -> 147: fewer parts to
+// join; 32 places make the chunks too unequal.)
+constexpr int kSnap = 8;
+constexpr int kMinLogThreads = 3, kMinChunk = 8, kMaxChunk = 64, kGroupPlaces = kMaxChunk + kSnap + 2;
 constexpr int kSumBlocks = 4;  // an SM, at once
 
 // The base's piece of a token's row.
@@ -301,10 +305,11 @@ __device__ __forceinline__ void write_sum(const EmbedBwdArgs &a, int64_t token, 
 template <int TW, int TO, int E, bool BASE>
 __global__ void __launch_bounds__(256, kSumBlocks) embed_sum_kernel(const SumParams p) {
   // rows read before the first is added (as the registers hold)
-  constexpr int U = E == 1 ? 16 : BASE ? (TW == MM_F32 || TO == MM_F32 ? 2 : 4) : TO == MM_F32 ? 4 : 8;
+  constexpr int U = E == 1 ? (BASE ? 8 : 16) : BASE ? (TW == MM_F32 || TO == MM_F32 ? 2 : 4) : TO == MM_F32 ? 4 : 8;
   constexpr int kPlaces = (256 >> kMinLogThreads) * kGroupPlaces;
   __shared__ uint32_t tokens[kPlaces];
   __shared__ int64_t starts[kPlaces];  // of a place's row of dout
+  __shared__ int borders[256 >> kMinLogThreads][2];
   pdl_launch_dependents();
   pdl_wait();
   const EmbedBwdArgs &a = p.a;
@@ -312,20 +317,28 @@ __global__ void __launch_bounds__(256, kSumBlocks) embed_sum_kernel(const SumPar
   const int slab = (int)blockIdx.x / p.across;
   const int chunk = ((int)blockIdx.x - slab * p.across) * (256 >> p.log_threads) + group;
   const int j = (slab * threads + t) * E;
-  const int rows = (int)a.rows, i0 = (int)min((int64_t)rows, (int64_t)chunk * p.chunk), n = min(rows - i0, p.chunk);
+  const int64_t i0 = (int64_t)chunk * p.chunk;
+  const int left = (int)max((int64_t)0, min(a.rows - i0, (int64_t)p.chunk + kSnap + 1));
   const uint32_t none = (uint32_t)a.vocab;
-  // the places of the chunk, and its neighbours' tokens (or none)
+  // the places of the chunk and those that may be taken over, and the one before
   uint32_t *mine = tokens + group * kGroupPlaces + 1;
   int64_t *start = starts + group * kGroupPlaces + 1;
-  for (int i = t - 1; i <= n; i += threads) {
-    const uint2 s = i0 + i >= 0 && i0 + i < rows ? p.sorted[i0 + i] : make_uint2(none, 0);
+  for (int i = t - 1; i <= p.chunk + kSnap; i += threads) {
+    const uint2 s = i0 + i >= 0 && i < left ? p.sorted[i0 + i] : make_uint2(none, 0);
     mine[i] = s.x;
     start[i] = (int64_t)s.y * a.lddo;
   }
+  if (t < 2) borders[group][t] = kSnap + 1;
   __syncthreads();
-  if (n <= 0 || j >= a.cols) return;
-  uint32_t token = mine[0];
-  bool from_before = mine[-1] == token;
+  for (int k = 0; k < 2; ++k)
+    for (int i = t; i <= kSnap; i += threads)
+      if (mine[k * p.chunk + i - 1] != mine[k * p.chunk + i]) atomicMin(&borders[group][k], i);
+  __syncthreads();
+  const int from = chunk == 0 || borders[group][0] > kSnap ? 0 : borders[group][0];
+  const int n = min(left, p.chunk + (borders[group][1] > kSnap ? 0 : borders[group][1]));
+  if (from >= n || j >= a.cols) return;
+  uint32_t token = mine[from];
+  bool from_before = mine[from - 1] == token;
   Piece<TW, E> base;
   float sum[E];
 #pragma unroll
@@ -338,13 +351,13 @@ __global__ void __launch_bounds__(256, kSumBlocks) embed_sum_kernel(const SumPar
       write_sum<TW, E>(a, token, j, sum, base);
     }
   };
-  for (int i = 0; i < n; i += U) {
+  for (int i = from; i < n; i += U) {
     Piece<TO, E> v[U];
     Piece<TW, E> b[BASE ? U : 1];
     if constexpr (BASE) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i + u < n && mine[i + u] != none && (i + u == 0 || mine[i + u] != mine[i + u - 1]))
+        if (i + u < n && mine[i + u] != none && (i + u == from || mine[i + u] != mine[i + u - 1]))
           b[u] = base_piece<TW, E>(a, mine[i + u], j);
     }
 #pragma unroll
@@ -364,7 +377,7 @@ __global__ void __launch_bounds__(256, kSumBlocks) embed_sum_kernel(const SumPar
       }
       if (token == none) return;
       if constexpr (BASE) {
-        if (i + u == 0) base = b[0];
+        if (i + u == from) base = b[0];
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) sum[e] += v[u].get(e);
@@ -386,10 +399,11 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p) {
   for (int s = (int)blockIdx.x; s < total; s += (int)gridDim.x) {
     const int c = (int)p.spanning[1 + s];
     const uint32_t token = p.sorted[(int64_t)(c + 1) * p.chunk].x;
-    int more = 0;  // the chunks after c that begin with the token
+    int more = 0;  // the chunks after c that begin inside the token's run
     for (int k = c + 1;; k += 256) {
       const int at = k + (int)threadIdx.x;
-      const int here = __syncthreads_count(at < p.chunks && p.sorted[(int64_t)at * p.chunk].x == token);
+      const int64_t inside = (int64_t)at * p.chunk + kSnap;  // (the border stayed in the token's run)
+      const int here = __syncthreads_count(at < p.chunks && inside < a.rows && p.sorted[inside].x == token);
       more += here;
       if (here < 256) break;
     }

@@ -149,7 +149,7 @@ def test_embedding_backward(rows, cols, vocab, pads, t, base):
 
 
 @pytest.mark.parametrize("rows", [1, 8, 9, 31, 4096, 4128, 9000, 70000])
-@pytest.mark.parametrize("kind", ["one", "two", "ends", "none", "all different"])
+@pytest.mark.parametrize("kind", ["one", "two", "ends", "lengths", "none", "all different"])
 def test_embedding_backward_runs(rows, kind):
     """Tokens that fill many chunks, begin and end on a chunk's border, never occur."""
     torch = T()
@@ -157,7 +157,9 @@ def test_embedding_backward_runs(rows, kind):
     vocab = 131000
     i = torch.arange(rows, device="cuda")
     tokens = {"one": torch.full_like(i, 70001), "two": torch.where(i % 3 == 0, 5, 130999),
-              "ends": i // 32 * 11, "none": torch.full_like(i, vocab), "all different": (i * 7919) % vocab}[kind]
+              "ends": i // 32 * 11,
+              "lengths": torch.repeat_interleave(i, torch.randint(1, 90, (rows,), generator=g, device="cuda"))[:rows],
+              "none": torch.full_like(i, vocab), "all different": (i * 7919) % vocab}[kind]
     t = (F, I64, BF)
     dout = rows_of(g, rows, 40, BF)
     check_bwd(dout, tokens, None, vocab, t, 1.0, run_bwd(dout, tokens, None, vocab, t))
