@@ -72,7 +72,7 @@ cudaError_t embed_launch(const EmbedArgs &a, LaunchCtx &ctx) {
 }
 
 // ---------------------------------------------------------------- sort, and the rows of the others
-// Least significant digit first, 9 bits a pass (a vocabulary below 2^18 takes two), by
+// Least significant digit first, up to 9 bits a pass (a vocabulary below 2^18 takes two), by
 // one CTA or one cluster of eight.  Each warp has a run of consecutive places: it counts its
 // digits, the counts of all become places, and it goes over its run again; equal
 // digits keep their order because a warp takes 32 at a time, ranked by matching.
@@ -81,8 +81,8 @@ cudaError_t embed_launch(const EmbedArgs &a, LaunchCtx &ctx) {
 // dW's rows are written meanwhile, as zeros or the base's, by the other CTAs of the
 // launch, those that the sums will write again among them.  (Untouched rows written
 // beside the sums instead: 76 -> 88 us at 8192 x 4096 into 32000, 150 -> 191 at 65536 x
-// 1024 into 131072.)  One CTA sorts where that takes no longer than the rows: clusters
-// of eight find room on 120 of the 152 SMs only.
+// 1024 into 131072.)  One CTA sorts where that takes no longer than the rows, since clusters
+// of eight find room on 120 of the 152 SMs only: 8192 x 4096 63 us, by eight 68.
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kMaxSortCtas = 8;
 constexpr int kDigit = 9, kBins = 1 << kDigit;
 constexpr size_t kSortSmem = (kSortWarps * kBins + kBins + 32) * sizeof(uint32_t);
@@ -91,7 +91,7 @@ struct SortParams {
   const void *tokens;
   int ti;
   int64_t vocab;
-  int rows, passes, ctas;  // ctas: 1 or kMaxSortCtas
+  int rows, passes, digit, ctas;  // bits a pass; ctas: 1 or kMaxSortCtas
   uint2 *to, *other;   // (token, place)
   uint32_t *spanning;  // set to 0: how many tokens the sums will have left in parts
   // the rows
@@ -114,6 +114,7 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
   const int lo = (int)((int64_t)p.rows * rank / p.ctas), n = (int)((int64_t)p.rows * (rank + 1) / p.ctas) - lo;
   const int w0 = lo + (int)((int64_t)n * warp / kSortWarps), w1 = lo + (int)((int64_t)n * (warp + 1) / kSortWarps);
   const uint32_t below = (1u << lane) - 1;
+  const int bins = 1 << p.digit;
   const auto sync = [&] {  // of all CTAs that sort
     if (p.ctas > 1) tc::cluster_sync_all();
     else __syncthreads();
@@ -121,37 +122,43 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
   constexpr int K = 8;
   uint2 *src = nullptr, *dst = p.passes & 1 ? p.to : p.other;  // the last pass ends in `to`
   for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = pass * kDigit;
+    const int shift = pass * p.digit;
     const auto pair_at = [&](int i) {  // (written by other SMs: past L1)
       return pass ? __ldcg(src + i) : make_uint2((uint32_t)load_token(p.tokens, p.ti, i, p.vocab), (uint32_t)i);
     };
-    // the run, 32 K places at a time; a run of one batch stays in registers
-    uint2 v[K];
+    // the run, 32 K places at a time, and which lanes have equal digits; a run of one batch
+    // stays in registers
+    uint2 v[K] = {};
+    uint32_t same[K];
+    const auto digit = [&](int k, int i0) {
+      return i0 + k * 32 + lane < w1 ? (v[k].x >> shift) & (bins - 1) : (uint32_t)kBins;
+    };
     const auto load = [&](int i0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int i = i0 + k * 32 + lane;
-        v[k] = i < w1 ? pair_at(i) : make_uint2(~0u, 0);
+        v[k] = i < w1 ? pair_at(i) : make_uint2(0, 0);
       }
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (i0 + k * 32 < w1) same[k] = __match_any_sync(0xffffffffu, digit(k, i0));
     };
-    const auto digit = [&](int i, uint2 x) { return i < w1 ? (x.x >> shift) & (kBins - 1) : (uint32_t)kBins; };
-    for (int b = lane; b < kBins; b += 32) off[warp][b] = 0;
+    for (int b = lane; b < bins; b += 32) off[warp][b] = 0;
     __syncwarp();
     for (int i0 = w0; i0 < w1; i0 += 32 * K) {
       load(i0);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (i0 + k * 32 >= w1) break;
-        const uint32_t d = digit(i0 + k * 32 + lane, v[k]);
-        const uint32_t same = __match_any_sync(0xffffffffu, d);
-        if (d < kBins && !(same & below)) off[warp][d] += __popc(same);
+        const uint32_t d = digit(k, i0);
+        if (d < kBins && !(same[k] & below)) off[warp][d] += __popc(same[k]);
         __syncwarp();
       }
     }
     __syncthreads();
-    if (t < kBins) {
+    if (t < bins) {
       uint32_t sum = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t c = off[w][t];
         off[w][t] = sum;
@@ -160,23 +167,26 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
       count[t] = sum;
     }
     sync();
-    if (t < kBins) {
+    uint32_t before = 0, total = 0, sum = 0;
+    if (t < bins) {
       const uint32_t addr = tc::smem_u32(count + t);
-      uint32_t c[kMaxSortCtas], before = 0, total = 0;
+      uint32_t c[kMaxSortCtas];
 #pragma unroll
       for (int r = 0; r < kMaxSortCtas; ++r) c[r] = r >= p.ctas ? 0 : p.ctas > 1 ? cluster_u32(addr, r) : count[t];
 #pragma unroll
       for (int r = 0; r < kMaxSortCtas; ++r) before += r < rank ? c[r] : 0, total += c[r];
-      uint32_t sum = total;
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += u;
-      }
-      if (lane == 31) warp_sum[warp] = sum;
-      asm volatile("bar.sync 1, 512;" ::: "memory");
+      sum = total;
+    }
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    if (t < bins) {
       uint32_t at = before + sum - total;
       for (int w = 0; w < warp; ++w) at += warp_sum[w];
-#pragma unroll 8
+#pragma unroll 16
       for (int w = 0; w < kSortWarps; ++w) off[w][t] += at;
     }
     __syncthreads();
@@ -185,11 +195,10 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (i0 + k * 32 >= w1) break;
-        const uint32_t d = digit(i0 + k * 32 + lane, v[k]);
-        const uint32_t same = __match_any_sync(0xffffffffu, d);
-        if (d < kBins) dst[off[warp][d] + __popc(same & below)] = v[k];
+        const uint32_t d = digit(k, i0);
+        if (d < kBins) dst[off[warp][d] + __popc(same[k] & below)] = v[k];
         __syncwarp();
-        if (d < kBins && !(same & below)) off[warp][d] += __popc(same);
+        if (d < kBins && !(same[k] & below)) off[warp][d] += __popc(same[k]);
         __syncwarp();
       }
     }
@@ -198,7 +207,6 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
     dst = dst == p.to ? p.other : p.to;
   }
 }
-static_assert(kBins == 512, "the barrier of the threads that have a digit");
 
 // Row v of dW as zeros or the base's, by `threads` threads (this is the t-th): pieces of 16
 // bytes as dW has them.
@@ -571,8 +579,10 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   f.tokens = a.tokens;
   f.ti = a.ti;
   f.rows = (int)a.rows;
-  f.passes = 1;
-  while (a.vocab >> (kDigit * f.passes)) ++f.passes;
+  int bits = 1;  // of the numbers up to vocab, which stands for none
+  while (a.vocab >> bits) ++bits;
+  f.passes = (bits + kDigit - 1) / kDigit;
+  f.digit = (bits + f.passes - 1) / f.passes;
   cudaError_t e = launch_pdl(embed_sort_kernel, dim3((unsigned)(f.ctas + row_ctas)), dim3(kSortThreads), kSortSmem,
                              ctx.stream, dim3((unsigned)f.ctas), f);
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (sort)");
