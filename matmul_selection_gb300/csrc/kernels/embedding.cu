@@ -4,13 +4,14 @@
 //   dW[v]  = base[v] + scale sum over {t : token[t] = v} of dout[t]
 //
 // Forward: memory traffic, the rows read and written once, a power of two of threads to
-// a row.
+// a row.  8192 x 4096 bf16 19 us (7 TB/s, the frequent rows from L2), one row 3.
 //
 // Backward: the places t are sorted by token (stable), so that the rows of one
 // token stand together and are added in the order of t, in registers, without
 // atomics.  Threads take nearly equal chunks of the sorted places, however often a token
 // occurs; a token of many places leaves fp32 parts, a chunk each, which a second kernel
-// adds in order.
+// adds in order.  8192 x 4096 bf16 into 32000 rows 63 us: the rows 39 (6.8 TB/s), the sums
+// 17, the parts 5; 65536 x 1024 into 131072 of fp32 147.
 #include <algorithm>
 
 #include "../operators.h"
