@@ -159,6 +159,12 @@ def test_whole_and_cut_tiles(rows, cols, vocab):
     p.check_backward(*p.backward())
 
 
+def test_many_rows():
+    p = Problem(70_000, 16, 300, none=0.5)
+    p.check_forward(*p.forward())
+    p.check_backward(*p.backward())
+
+
 @pytest.mark.parametrize("want", [(True, False), (False, True)])
 @pytest.mark.parametrize("rows", [50, 600])
 def test_one_gradient_alone(rows, want):

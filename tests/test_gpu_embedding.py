@@ -165,6 +165,20 @@ def test_embedding_backward_runs(rows, kind):
     check_bwd(dout, tokens, None, vocab, t, 1.0, run_bwd(dout, tokens, None, vocab, t))
 
 
+@pytest.mark.parametrize("rows,cols,vocab", [(5000, 8, 1_000_000), (3000, 12, 270_000), (600, 100_000, 3), (40, 30_001, 9),
+                                             (300_000, 8, 511), (300_000, 5, 512)])
+def test_embedding_backward_extents(rows, cols, vocab):
+    """Three passes of the sort, rows of many slabs, many places; a vocabulary that ends
+    at a power of two."""
+    g = generator(rows + vocab)
+    dout = rows_of(g, rows, cols, BF)
+    tokens = tokens_of(g, rows, vocab, I32, 0.1)
+    t = (F, I32, BF)
+    check_bwd(dout, tokens, None, vocab, t, 1.0, run_bwd(dout, tokens, None, vocab, t))
+    base = rows_of(g, vocab, cols, F)
+    check_bwd(dout, tokens, base, vocab, t, 1.0, run_bwd(dout, tokens, base, vocab, t, in_place=True))
+
+
 @pytest.mark.parametrize("offsets", [(1, 0), (0, 1), (2, 3), (8, 4)])
 def test_embedding_backward_alignments(offsets):
     g = generator(6)

@@ -36,6 +36,39 @@ def test_training_step_with_tied_weights(tokens, hidden, vocab):
         assert rel[name] < 6 * 2.0 ** -8, rel
 
 
+@pytest.mark.parametrize("rows", [5, 40, 128, 400])
+def test_operands_written_a_moment_ago(rows):
+    """x, W, targets and dloss come from the kernels just before, in buffers that the
+    calls before read with other contents (some of it is asked for ahead of time)."""
+    torch = T()
+    s = torch.cuda.Stream()
+    t = (BF, I64, BF)
+    problems = [Problem(rows, 520, 4000, seed=k) for k in range(6)]
+    vocab = [torch.randperm(4000, generator=problems[0].g, device="cuda") for _ in problems]
+    x, w = torch.zeros(rows, 520, device="cuda").bfloat16(), torch.zeros(4000, 520, device="cuda").bfloat16()
+    targets, dloss = torch.zeros(rows, dtype=torch.int64, device="cuda"), torch.zeros(rows, device="cuda")
+    loss, lse = (torch.zeros(len(problems), rows + 8, device="cuda") for _ in range(2))
+    loss.fill_(77), lse.fill_(77)
+    dx, dw = (torch.zeros(len(problems), n, 520, device="cuda").bfloat16() for n in (rows, 4000))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for k, p in enumerate(problems):
+            targets.copy_(p.targets)
+            dloss.copy_(p.dloss)
+            x.copy_(p.x)
+            # the library's own kernels write W: its rows as their own gradient
+            mm.check(mm.mm_embedding_backward(p.w[vocab[k]].contiguous(), vocab[k], None, w, 4000, 520, 4000, 520, 0, 520,
+                                              t, 1.0, s))
+            mm.check(mm.mm_cross_entropy(x, w, targets, loss[k], lse[k], rows, 520, 4000, 520, 520, (BF, I64, F), s))
+            mm.check(mm.mm_cross_entropy_backward(x, w, targets, lse[k], dloss, dx[k], dw[k], rows, 520, 4000, 520, 520,
+                                                  520, 520, t, s))
+    torch.cuda.synchronize()
+    for k, p in enumerate(problems):
+        p.lse = lse[k][:rows]
+        p.check_forward(loss[k], lse[k])
+        p.check_backward((dx[k], lambda: None), (dw[k], lambda: None))
+
+
 def test_streams_beside_one_another():
     """Calls of every operator on three streams at once."""
     torch = T()
