@@ -299,7 +299,10 @@ static_assert(Ring<MODE_G, 2>::stages(128, 1) == 5 && Ring<MODE_DW, 2>::stages(1
                   Ring<MODE_G, 1>::stages(16, 1) == 6,
               "what the measurements were taken with");
 
-__device__ __forceinline__ int row_count(const Rows &r, int rows) { return r.count ? max(1, *r.count) : rows; }
+// The rows that count, and how many a product has: one at least (a tile of zeros where
+// none counts, so that dW is written), which then has no row of x behind it.
+__device__ __forceinline__ int live_rows(const Rows &r, int rows) { return r.count ? *r.count : rows; }
+__device__ __forceinline__ int row_count(const Rows &r, int rows) { return max(1, live_rows(r, rows)); }
 __device__ __forceinline__ int target_of(const TileParams &p, int row) {
   if (p.r.count) return p.r.target[row];
   const int64_t v = row < p.rows ? load_token(p.targets, p.ti, row, p.vocab) : p.vocab;
@@ -975,10 +978,10 @@ __device__ __forceinline__ void round_dx(const DxParams &p, const float4 *from, 
 __global__ void __launch_bounds__(256, 4) dx_kernel(const DxParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, count = row_count(p.r, p.a.rows);
+  const int lane = threadIdx.x & 31, count = live_rows(p.r, p.a.rows);  // (0: r.row holds nothing)
   const float gain = *p.r.gain * (p.a.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
   const uint32_t warps = gridDim.x * 8, warp = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const Tiles tiles = tiles_of(count, p.tile_m, p.tiles_n, p.bn, p.places, max_parts_of(p.piece_kb));
+  const Tiles tiles = tiles_of(max(1, count), p.tile_m, p.tiles_n, p.bn, p.places, max_parts_of(p.piece_kb));
   const int log_rows = p.tile_m == 256 ? 3 : 2, log_cols = p.bn == 256 ? 3 : 2;  // blocks of 32 a tile
   if (tiles.full > 0) {
     // (as many blocks as there are 4 KB of sums: they count in 32 bits)
