@@ -14,6 +14,7 @@
 // 17, the parts 5; 65536 x 1024 into 131072 of fp32 147.
 #include <algorithm>
 
+#include "../embed_chunks.h"
 #include "../operators.h"
 #include "../per_device.h"
 #include "indices.cuh"
@@ -287,11 +288,7 @@ struct SumParams {
   int log_threads;
   int across;           // blocks for all chunks of a slab of columns
 };
-// A border between two chunks moves up to kSnap places on, to where a token ends; inside a
-// longer run it stays.  (8192 x 4096 66 -> 63 us, 65536 x 1024 151 -> 147: fewer parts to
-// join; 32 places make the chunks too unequal.)
-constexpr int kSnap = 8;
-constexpr int kMinLogThreads = 3, kMinChunk = 8, kMaxChunk = 64, kGroupPlaces = kMaxChunk + kSnap + 2;
+constexpr int kMinLogThreads = 3, kGroupPlaces = kMaxChunk + kSnap + 2;
 constexpr int kSumBlocks = 4;  // an SM, at once
 
 // The base's piece of a token's row.
@@ -327,13 +324,13 @@ __global__ void __launch_bounds__(256, kSumBlocks) embed_sum_kernel(const SumPar
   const int chunk = ((int)blockIdx.x - slab * p.across) * (256 >> p.log_threads) + group;
   const int j = (slab * threads + t) * E;
   const int64_t i0 = (int64_t)chunk * p.chunk;
-  const int left = (int)max((int64_t)0, min(a.rows - i0, (int64_t)p.chunk + kSnap + 1));
+  const int left = places_left(a.rows, i0, p.chunk);
   const uint32_t none = (uint32_t)a.vocab;
   // the places of the chunk and those that may be taken over, and the one before
   uint32_t *mine = tokens + group * kGroupPlaces + 1;
   int64_t *start = starts + group * kGroupPlaces + 1;
   for (int i = t - 1; i <= p.chunk + kSnap; i += threads) {
-    const uint2 s = i0 + i >= 0 && i < left ? p.sorted[i0 + i] : make_uint2(none, 0);
+    const uint2 s = reads_place(i0, i, left) ? p.sorted[i0 + i] : make_uint2(none, 0);
     mine[i] = s.x;
     start[i] = (int64_t)s.y * a.lddo;
   }

@@ -1,0 +1,6 @@
+"""Host-side rules of the operators at the ends of a language model."""
+from test_host_rules import run
+
+
+def test_chunks_read_the_places_that_there_are(tmp_path):
+    run("embed_chunks_test", tmp_path)
