@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p) {
   pdl_wait();
   const EmbedBwdArgs &a = p.a;
   const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  const int j = ((int)blockIdx.y * 64 + x) * V, total = (int)p.spanning[0];
-  for (int s = (int)blockIdx.x; s < total; s += (int)gridDim.x) {
+  const int j = ((int)blockIdx.x * 64 + x) * V, total = (int)p.spanning[0];
+  for (int s = (int)blockIdx.y; s < total; s += (int)gridDim.y) {
     const int c = (int)p.spanning[1 + s];
     const uint32_t token = p.sorted[(int64_t)(c + 1) * p.chunk].x;
     int more = 0;  // the chunks after c that begin inside the token's run
@@ -482,9 +482,11 @@ mm_status embed_sums(const EmbedBwdArgs &a, SumParams p, const SumShape &shape, 
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch");
   count_operator_launch();
   if (p.chunks == 1) return MM_OK;
+  // (slabs of columns along x: there may be more than the 65535 that y takes)
   const int64_t columns = whole ? 256 : 64, join_slabs = (a.cols + columns - 1) / columns;
   const int64_t across = std::max<int64_t>(1, std::min<int64_t>(p.chunks - 1, 8 * ctx.dev->info.sms / join_slabs));
-  e = launch_pdl(whole ? embed_join_kernel<TW, 4> : embed_join_kernel<TW, 1>, dim3((unsigned)across, (unsigned)join_slabs), dim3(256), 0, ctx.stream, dim3(1), p);
+  e = launch_pdl(whole ? embed_join_kernel<TW, 4> : embed_join_kernel<TW, 1>, dim3((unsigned)join_slabs, (unsigned)across), dim3(256), 0,
+                 ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (join)");
   count_operator_launch();
   return MM_OK;

@@ -12,7 +12,7 @@ using namespace mm;
 namespace {
 
 constexpr int64_t kMaxDim = 1LL << 30;
-constexpr int64_t kMaxEmbeddingCols = 1LL << 23;  // (slabs of 256 columns are a grid's y)
+constexpr int64_t kMaxEmbeddingCols = 1LL << 23;  // (a thread's columns count in 32 bits)
 
 bool is_float_type(int t) { return t == MM_BF16 || t == MM_F16 || t == MM_F32; }
 bool is_index_type(int t) { return t == MM_I32 || t == MM_I64; }
