@@ -288,8 +288,7 @@ struct SumParams {
   int log_threads;
   int across;           // blocks for all chunks of a slab of columns
 };
-constexpr int kMinLogThreads = 3, kGroupPlaces = kMaxChunk + kSnap + 2;
-constexpr int kSumBlocks = 4;  // an SM, at once
+constexpr int kGroupPlaces = kMaxChunk + kSnap + 2;
 
 // The base's piece of a token's row.
 template <int TW, int E>
@@ -446,36 +445,18 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p) {
   }
 }
 
-// How the sums are laid out over threads: pieces or single elements, and chunks that fill
-// the device once (65536 x 1024 in chunks of 54 40 us; of 32, 1.7 times, 48).
-struct SumShape {
-  bool whole;
-  int log_threads, chunk, chunks;
-  int64_t slabs;
-};
-SumShape sum_shape(const EmbedBwdArgs &a, int sms) {
+// Whether rows move in whole pieces, else in single elements.
+bool whole_pieces(const EmbedBwdArgs &a) {
   const int bw = dtype_bytes(a.tw), bo = dtype_bytes(a.to);
-  SumShape s;
-  s.whole = a.cols % kE == 0 && (uintptr_t)a.dout % 16 == 0 && (uintptr_t)a.dweight % 16 == 0 &&
-            (uintptr_t)a.base % 16 == 0 && (a.lddo * bo % 16 == 0 || a.rows == 1) &&
-            (a.vocab == 1 || (a.lddw * bw % 16 == 0 && a.ldb * bw % 16 == 0));
-  const int64_t pieces = s.whole ? a.cols / kE : a.cols;
-  s.log_threads = kMinLogThreads;
-  while (s.log_threads < 8 && (1ll << s.log_threads) < pieces) ++s.log_threads;
-  s.slabs = (pieces + (1 << s.log_threads) - 1) >> s.log_threads;
-  const int64_t groups = std::max<int64_t>(1, kSumBlocks * sms / s.slabs) * (256 >> s.log_threads);
-  s.chunk = (int)std::max<int64_t>(kMinChunk, std::min<int64_t>(kMaxChunk, (a.rows + groups - 1) / groups));
-  s.chunks = (int)((a.rows + s.chunk - 1) / s.chunk);
-  return s;
+  return a.cols % kE == 0 && (uintptr_t)a.dout % 16 == 0 && (uintptr_t)a.dweight % 16 == 0 &&
+         (uintptr_t)a.base % 16 == 0 && (a.lddo * bo % 16 == 0 || a.rows == 1) &&
+         (a.vocab == 1 || (a.lddw * bw % 16 == 0 && a.ldb * bw % 16 == 0));
 }
 
 template <int TW, int TO>
-mm_status embed_sums(const EmbedBwdArgs &a, SumParams p, const SumShape &shape, LaunchCtx &ctx) {
-  const bool whole = shape.whole;
-  const int64_t groups = 256 >> p.log_threads, slabs = shape.slabs;
-  p.across = (int)((p.chunks + groups - 1) / groups);
-  if (p.across * slabs >= 1 << 30) return set_error(MM_ERR_UNSUPPORTED, "too many blocks");
-  const dim3 grid((unsigned)(p.across * slabs));
+mm_status embed_sums(const EmbedBwdArgs &a, const SumParams &p, const SumShape &shape, LaunchCtx &ctx) {
+  const bool whole = whole_pieces(a);
+  const dim3 grid((unsigned)(shape.across * shape.slabs));
   const auto kernel = whole ? (a.base ? embed_sum_kernel<TW, TO, kE, true> : embed_sum_kernel<TW, TO, kE, false>)
                             : (a.base ? embed_sum_kernel<TW, TO, 1, true> : embed_sum_kernel<TW, TO, 1, false>);
   cudaError_t e = launch_pdl(kernel, grid, dim3(256), 0, ctx.stream, dim3(1), p);
@@ -516,10 +497,12 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   SumParams p;
   std::memset(&p, 0, sizeof p);
   p.a = a;
-  const SumShape shape = sum_shape(a, ctx.dev->info.sms);
+  const SumShape shape = sum_shape(a.rows, whole_pieces(a) ? a.cols / kE : a.cols, ctx.dev->info.sms);
+  if (!shape.fits) return set_error(MM_ERR_UNSUPPORTED, "too many blocks");
   p.chunk = shape.chunk;
   p.chunks = shape.chunks;
   p.log_threads = shape.log_threads;
+  p.across = (int)shape.across;
   SortParams f;
   std::memset(&f, 0, sizeof f);
   f.base = static_cast<const uint8_t *>(a.base);

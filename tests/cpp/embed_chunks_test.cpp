@@ -1,5 +1,6 @@
-// Places that the chunks of the embedding's gradient read: every one that they need, none
-// that is not there.
+// The chunks of the embedding's gradient: the places that they read are every one that
+// they need and none that is not there, and their grid is one that a launch takes.
+#include <algorithm>
 #include <cstdio>
 
 #include "embed_chunks.h"
@@ -32,5 +33,24 @@ int main() {
     std::printf("far places\n");
     return 1;
   }
+  // the grid of the sums: one that a launch takes, or refused as such (before any launch)
+  const int64_t most = (1LL << 30) - 1, most_cols = (1LL << 23) - 1;
+  for (int sms : {1, 132, 152})
+    for (int64_t r = 1;; r = std::min(most, r < 100 ? r + 1 : r * 5 / 4)) {
+      for (int64_t pieces = 1;; pieces = std::min(most_cols, pieces < 100 ? pieces + 1 : pieces * 5 / 4)) {
+        const SumShape s = sum_shape(r, pieces, sms);
+        const int64_t per_block = kSumThreads >> s.log_threads;
+        const bool good = s.chunk >= kMinChunk && s.chunk <= kMaxChunk && (int64_t)s.chunk * s.chunks >= r &&
+                          (int64_t)s.chunk * (s.chunks - 1) < r && s.across * per_block >= s.chunks &&
+                          (s.slabs << s.log_threads) >= pieces && s.fits == (s.across * s.slabs < (1LL << 30)) &&
+                          (s.fits || r * pieces >= 1LL << 40);  // (as many elements never lie in memory)
+        if (!good) {
+          std::printf("%lld rows of %lld pieces\n", (long long)r, (long long)pieces);
+          return 1;
+        }
+        if (pieces == most_cols) break;
+      }
+      if (r == most) break;
+    }
   std::printf("ok\n");
 }
