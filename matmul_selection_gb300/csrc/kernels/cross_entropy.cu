@@ -5,9 +5,9 @@
 //   g[t, v] = dloss[t] (exp(l[t, v] - lse[t]) - [v = y[t]]);  dx = g W, dW = g^T x
 //
 // Forward: a product whose tiles never leave the SM: a tile's rows leave their
-// maximum and sum of exponentials, and the target's logit.  The sums are kept as
-// s 2^r, r a whole number not below the logits times log2(e): the powers of two
-// that bring two sums together are exact.
+// maximum m and s = sum exp(l - m), and the target's logit; loss = (m - l[y]) + log s.
+// The maximum is subtracted before the factor log2(e): the difference is exact where the
+// share is not small, whatever the logits' size, and the largest one's share is exactly 1.
 // Backward: the vocabulary in pieces, each the product again with g as the
 // epilogue's output in 16 bits, then its two products.
 // Rows without a target are left out: the others' x is gathered first, so the
@@ -44,6 +44,12 @@ __device__ __forceinline__ float exp2_fast(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// exp of a difference of two logits, the smaller first.  (2^(l log2(e) - r) in one FMA, r a
+// rounded multiple, is off by half a step of r: it passed 2^x's range from logits of 3e9 on,
+// and log2(e)'s rounding put a loss off by 1.5e-8 of its largest logit.)
+__device__ __forceinline__ float exp_fast(float d) { return exp2_fast(d * kLog2e); }
+// Below every logit but -infinity, and what a sum of none has for its maximum.
+constexpr float kLeast = -3.402823466e38f;
 
 // ---------------------------------------------------------------- the rows that count
 // Where each call's scratch holds what; i: a row among those that count, of
@@ -257,7 +263,7 @@ struct TileParams {
   int low;           // few rows: g is two values, the second in the rows from here on (else 0)
   int num_kb;        // 64-element blocks of K (DW: of the rows that count)
   int piece_kb;      // DX: those of a whole piece
-  float2 *part;      // LSE: [128 of the vocabulary][rows_pad] (r, s)
+  float2 *part;      // LSE: [128 of the vocabulary][rows_pad] (m, s)
   float *hit;        // LSE: [rows_pad] the target's logit
   // DX: blocks of 32 rows by 32 columns, each [4 columns][row][column]: the whole tiles'
   // [row block][acc_cols], then, from acc_cut on, [unit][row block][column block] of those
@@ -349,9 +355,9 @@ __device__ __forceinline__ void add_chunk(float (&sum)[128], uint32_t tmem, int 
       for (int i = 0; i < 32; ++i) sum[b * 32 + i] = first ? __uint_as_float(v[i]) : sum[b * 32 + i] + __uint_as_float(v[i]);
     }
 }
-// A row's sum of 2^(l log2e - r) and r over w logits, the first of which is token n0.
+// A row's maximum m and sum of exp(l - m) over w logits, the first of which is token n0.
 __device__ __forceinline__ float2 sum_exp(const TileParams &p, float (&l)[128], int n0, int w, int target, float *hit) {
-  float r = -3e38f, s = 0.f;
+  float m = kLeast, s = 0.f;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const int left = p.vocab - n0 - b * 32, at = target - n0 - b * 32;
@@ -374,19 +380,19 @@ __device__ __forceinline__ float2 sum_exp(const TileParams &p, float (&l)[128], 
 #pragma unroll
       for (int i = k + 4; i < 32; i += 4) top[k] = fmaxf(top[k], l[b * 32 + i]);
     }
-    const float next = fmaxf(r, ceilf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e));
-    float sum[4] = {s * exp2_fast(r - next), 0.f, 0.f, 0.f};
-    r = next;
+    const float next = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+    float sum[4] = {s * exp_fast(m - next), 0.f, 0.f, 0.f};
+    m = next;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum[i & 3] += exp2_fast(fmaf(l[b * 32 + i], kLog2e, -r));
+    for (int i = 0; i < 32; ++i) sum[i & 3] += exp_fast(l[b * 32 + i] - m);
     s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
-  return make_float2(r, s);
+  return make_float2(m, s);
 }
 // Two such sums as one.
 __device__ __forceinline__ float2 join_sums(float2 a, float2 b) {
-  const float r = fmaxf(a.x, b.x);
-  return make_float2(r, a.y * exp2_fast(a.x - r) + b.y * exp2_fast(b.x - r));
+  const float m = fmaxf(a.x, b.x);
+  return make_float2(m, a.y * exp_fast(a.x - m) + b.y * exp_fast(b.x - m));
 }
 
 // A warp's boxes, filled in turn.
@@ -793,7 +799,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
         }
         // the upper half's sums to the lower half's warps; a buffer for each of two turns
         float2 *upper = reinterpret_cast<float2 *>(boxes) + turn * 128 + q * 32 + lane;
-        float2 sum = make_float2(-3e38f, 0.f);
+        float2 sum = make_float2(kLeast, 0.f);
         if (live && good) {
           const int row = row0 + lane;
           sum = sum_exp(p, l, n, wide, target_of(p, row), p.hit + row);
@@ -868,9 +874,8 @@ struct LossParams {
   int tile_m, bn, tiles_n, places;  // of the product
 };
 
-// 32 rows a block, 32 threads a row over the tiles of the vocabulary.  r log 2 is kept
-// as a product and its error, so that a loss is no less exact than its sums.  (In fp64
-// the logarithm of 32 rows took 10 us; 8192 rows of 512 tiles now 17.)
+// 32 rows a block, 32 threads a row over the tiles of the vocabulary.  (In fp64 the
+// logarithm of 32 rows took 10 us; 8192 rows of 512 tiles now 17.)
 constexpr int kLossThreads = 1024;
 __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) {
   pdl_launch_dependents();
@@ -886,7 +891,7 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) 
   };
   const int slot = row < p.a.rows ? slot_of(row) : -1;
   const Tiles tiles = tiles_of(row_count(p.r, p.a.rows), p.tile_m, p.tiles_n, p.bn, p.places);
-  const float2 none = make_float2(-3e38f, 0.f);
+  const float2 none = make_float2(kLeast, 0.f);
   float2 sum = none;
   if (slot >= 0) {
     // a slot for each 128 of the vocabulary; a tile has left its sums in the first of
@@ -910,17 +915,16 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(const LossParams p) 
   __syncthreads();
   // the 32 sums of a row by a warp
   const float2 mine = sh[x][y];
-  float r = mine.x;
-  for (int o = 16; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
-  float s = mine.y * exp2_fast(mine.x - r);
+  float m = mine.x;
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = mine.y * exp_fast(mine.x - m);
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   const int64_t to = (int64_t)blockIdx.x * 32 + y;
   if (x != 0 || to >= p.a.rows) return;
   const int at = slot_of(to);
-  constexpr float kLn2 = 0.693147180559945309f, kLn2Rest = (float)(0.693147180559945309 - (double)kLn2);
-  const float whole = r * kLn2, rest = fmaf(r, kLn2, -whole) + r * kLn2Rest + logf(s);
-  p.a.loss[to] = at < 0 ? 0.f : (whole - p.hit[at]) + rest;
-  if (p.a.lse) p.a.lse[to] = at < 0 ? 0.f : whole + rest;
+  const float rest = logf(s);
+  p.a.loss[to] = at < 0 ? 0.f : (m - p.hit[at]) + rest;
+  if (p.a.lse) p.a.lse[to] = at < 0 ? 0.f : m + rest;
 }
 
 struct DxParams {
