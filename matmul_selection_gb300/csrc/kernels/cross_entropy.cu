@@ -44,7 +44,7 @@ __device__ __forceinline__ float exp2_fast(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// exp of a difference of two logits, the smaller first.  (2^(l log2(e) - r) in one FMA, r a
+// exp of a logit less another, or less the logarithm of a row's sum, not above it.  (2^(l log2(e) - r) in one FMA, r a
 // rounded multiple, is off by half a step of r: it passed 2^x's range from logits of 3e9 on,
 // and log2(e)'s rounding put a loss off by 1.5e-8 of its largest logit.)
 __device__ __forceinline__ float exp_fast(float d) { return exp2_fast(d * kLog2e); }
@@ -63,7 +63,7 @@ struct Rows {
   int *row;         // [rows] the row of an i
   int *target;      // [rows_pad], -1 past the count
   float *ratio;     // [rows_pad] dloss / gain (f16: times kF16Gain), 0 past the count
-  float *lse2;      // [rows_pad] lse log2(e)
+  float *lse;       // [rows_pad]
   uint16_t *x;      // [rows_pad][ldx], zeros from cols to ldx and for rows up to a multiple of 64
   int64_t ldx;
   int rows_pad;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
       p.r.target[before + at] = target;
       if (p.backward) {
         p.r.ratio[before + at] = ratio_of(a.dloss, i, top, a.tx);
-        p.r.lse2[before + at] = a.lse[i] * kLog2e;
+        p.r.lse[before + at] = a.lse[i];
       }
     }
     __syncthreads();
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
     const int end = max(1, (before + kRowTile - 1) / kRowTile) * kRowTile;
     for (int i = before + t; i < end; i += kGatherThreads) {
       p.r.target[i] = -1;
-      if (p.backward) p.r.ratio[i] = p.r.lse2[i] = 0.f;
+      if (p.backward) p.r.ratio[i] = p.r.lse[i] = 0.f;
     }
     const int64_t z0 = (int64_t)before * pieces, z1 = (int64_t)max(1, (before + 63) / 64) * 64 * pieces;
     for (int64_t i = z0 + t; i < z1; i += kGatherThreads)
@@ -430,19 +430,19 @@ __device__ __forceinline__ void store_box_tma(const CUtensorMap *map, uint8_t *b
 // g of 32 columns, token `first` the first of them, in place of the logits: a thread's row.
 struct GRow {
   int target;
-  float ratio, lse2;
+  float ratio, lse;
 };
 __device__ __forceinline__ GRow g_row(const TileParams &p, int row, float gain) {
   GRow r{target_of(p, row), 0.f, 0.f};
-  if (p.r.count) r.ratio = p.r.ratio[row], r.lse2 = p.r.lse2[row];
-  else if (r.target >= 0) r.ratio = ratio_of(p.dloss, row, gain, p.tx), r.lse2 = p.lse[row] * kLog2e;
+  if (p.r.count) r.ratio = p.r.ratio[row], r.lse = p.r.lse[row];
+  else if (r.target >= 0) r.ratio = ratio_of(p.dloss, row, gain, p.tx), r.lse = p.lse[row];
   return r;
 }
 __device__ __forceinline__ void make_g(const TileParams &p, const GRow &r, uint32_t (&v)[32], int first) {
   const bool live = r.ratio != 0.f;  // (a weight of 0 takes its row out, whatever its logits)
 #pragma unroll
   for (int i = 0; i < 32; ++i)
-    v[i] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[i]), kLog2e, -r.lse2)) * r.ratio);
+    v[i] = __float_as_uint(exp_fast(__uint_as_float(v[i]) - r.lse) * r.ratio);
   const int at = r.target - first, left = p.vocab - first;
   if (__any_sync(0xffffffffu, (unsigned)at < 32u)) {
 #pragma unroll
@@ -1042,7 +1042,7 @@ Rows cut_rows(Cut &cut, const LossArgs &a, bool backward, bool direct) {
   r.target = cut.take<int>(r.rows_pad);
   if (backward) {
     r.ratio = cut.take<float>(r.rows_pad);
-    r.lse2 = cut.take<float>(r.rows_pad);
+    r.lse = cut.take<float>(r.rows_pad);
   }
   r.x = cut.take<uint16_t>((int64_t)r.rows_pad * r.ldx);
   return r;
