@@ -16,7 +16,7 @@
 // What bounds it: above a few hundred rows the tensor cores, under the power cap
 // (8192 x 4096 x 131072 5.1-5.3 ms, 1.65-1.72 PFLOP/s, 1.94 in a short burst; backward
 // 8192 x 4096 x 32000, a quarter without a target, 2.9-3.0 ms); below, W's bytes (16 x
-// 4096 x 32000 46 us, 5.7 TB/s over the whole call; backward, W twice and dW, 158 us).
+// 4096 x 32000 47 us, 5.6 TB/s over the whole call; backward, W twice and dW, 164 us).
 #include <algorithm>
 
 #include "../operators.h"
@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
 // ---------------------------------------------------------------- the products
 // Products on tcgen05 (kind::f16), one after another:
 //   LSE, G   x W^T, both K-major: the sums of a tile's rows, or g in 16 bits
+//   G_ONE    G over no more of K than one chunk (see kChunkKb), on pairs
 //   DX       g W, W MN-major as it lies, K the piece of the vocabulary; added to
 //            fp32 sums over the pieces
 //   DW       g^T x, both MN-major as they lie, K the rows
@@ -194,13 +195,15 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
 // rows; persistent, two accumulators in TMEM, so that a tile's epilogue runs under
 // the next tile's main loop.  Neither the rows that count nor the tiles are known
 // to the host: each kernel reads the count and lays out its own tiles.
-enum Mode { MODE_LSE, MODE_G, MODE_DX, MODE_DW };
+enum Mode { MODE_LSE, MODE_G, MODE_G_ONE, MODE_DX, MODE_DW };
 
 // Warp 0 copies, warp 1 issues MMAs, the others take tiles out, eight a tile.  Where a
-// tile leaves in 16 bits there are 16, eight for each accumulator: products over few
-// rows of K are all epilogue, and what writes to memory in one half overlaps with what
-// is converted in the other (all 16 on one tile: converted, then written).
-constexpr int out_warps(int mode, int cg) { return cg == 2 && (mode == MODE_G || mode == MODE_DW) ? 16 : 8; }
+// tile leaves in 16 bits from one sum over K there are 16, eight for each accumulator:
+// products over few of K are all epilogue, and what writes to memory in one half overlaps with
+// what is converted in the other (all 16 on one tile: converted, then written).  G holds its
+// sums over chunks of K in registers, so it has eight (16 with half of the columns each:
+// gradients of 2048 x 4096 x 32000 1025 -> 1098 us).
+constexpr int out_warps(int mode, int cg) { return cg == 2 && (mode == MODE_G_ONE || mode == MODE_DW) ? 16 : 8; }
 constexpr int tile_threads(int mode, int cg) { return 64 + 32 * out_warps(mode, cg); }
 constexpr int kErrCopy = 0xa01, kErrMma = 0xa02, kErrStore = 0xa03, kErrDrain = 0xa04;
 constexpr int kGroupRows = 8;  // row tiles walked together, so that their operands stay in L2
@@ -288,8 +291,8 @@ struct TileParams {
 constexpr uint32_t kSmemBytes = 227 * 1024, kBarBytes = 1024;
 template <int MODE, int CG>
 struct Ring {
-  static constexpr int kOut = out_warps(MODE, CG);
-  static constexpr bool kHasBoxes = kOut == 16;
+  static constexpr int kOut = out_warps(MODE, CG), kTeams = kOut / 8;
+  static constexpr bool kHasBoxes = CG == 2 && (MODE == MODE_G || MODE == MODE_G_ONE || MODE == MODE_DW);
   static constexpr uint32_t kB = (CG == 2 ? 128 : 256) * 128;
   static constexpr int kMaxStages = 6;
   static constexpr size_t kSmem = kSmemBytes;
@@ -300,7 +303,7 @@ struct Ring {
     return n < kMaxStages ? n : kMaxStages;
   }
 };
-static_assert(Ring<MODE_G, 2>::stages(128, 1) == 5 && Ring<MODE_DW, 2>::stages(128, 2) == 3 &&
+static_assert(Ring<MODE_G, 2>::stages(128, 1) == 6 && Ring<MODE_G_ONE, 2>::stages(128, 1) == 5 && Ring<MODE_DW, 2>::stages(128, 2) == 3 &&
                   Ring<MODE_LSE, 2>::stages(128, 1) == 6 && Ring<MODE_LSE, 1>::stages(128, 1) == 4 &&
                   Ring<MODE_G, 1>::stages(16, 1) == 6,
               "what the measurements were taken with");
@@ -336,11 +339,15 @@ __device__ __forceinline__ bool all_take(bool ok) {
 // What a tile leaves, by eight warps: two for each quarter of the 128 rows, a half of
 // the columns each.
 
-// LSE: the logits are fp32 sums over K that the tensor core truncates at each step of
+// LSE, G: the logits are fp32 sums over K that the tensor core truncates at each step of
 // 16, towards zero, so that their error grows with K and the sum itself.  A sum over
 // kChunkKb blocks at a time, added up here in registers, rounded, keeps it at that of
 // an fp32 loop (8192 x 4096 x 131072: the loss off by 2.9e-6 of itself in one chain, by
-// 7e-7 in chunks of 1024 of K, by 3e-7 of 512, for 2 % of the time).
+// 7e-7 in chunks of 1024 of K, by 3e-7 of 512, for 2 % of the time).  Backward, the same sums
+// in the same order give the same logits, bit for bit, so that a share is the exponential of
+// what lse was made from.  (In one chain the share of a token that holds a row's whole mass
+// was off by -2.4e-4 at K = 4096 and a logit of 30, by -0.8 % at 1000, by -6 % at K = 16384 and
+// 1000, which is a gradient where there is none.  The chunks take 2-4 % of the gradients' time.)
 constexpr int kChunkKb = 8;
 
 // A chunk of w columns, added to a thread's sums (the first: the sums themselves).
@@ -453,10 +460,9 @@ __device__ __forceinline__ void make_g(const TileParams &p, const GRow &r, uint3
     for (int i = 0; i < 32; ++i) v[i] = live && i < left ? v[i] : 0u;
   }
 }
-// G, DW: columns n .. n + 63 of the product's rows row0 .. row0 + 31.
-__device__ __forceinline__ void leave_g(const TileParams &p, const CUtensorMap *map, uint32_t (&v)[2][32], int n, int row0,
-                                        Boxes &boxes) {
-  const GRow r = g_row(p, row0 + (threadIdx.x & 31), 0.f);
+// G: columns n .. n + 63 of the product's rows row0 .. row0 + 31.
+__device__ __forceinline__ void leave_g(const TileParams &p, const CUtensorMap *map, const GRow &r, uint32_t (&v)[2][32], int n,
+                                        int row0, Boxes &boxes) {
   uint8_t *box = boxes.next();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -538,20 +544,20 @@ __device__ __forceinline__ void take_dx(const TileParams &p, uint32_t tmem, floa
 }
 
 // What the gather does, for few rows that stay where they lie, by the warps that take
-// tiles out while they wait for the first one: the largest |dloss| (for each CTA by
-// itself), and this CTA's share of x with zeros for the rows that do not count, which dW's
-// product adds up times g's zeros (they may hold anything).
-__device__ __forceinline__ float prepare_few(const TileParams &p, int cta, int ctas, int t) {
-  const int lane = t & 31;
+// tiles out: the largest |dloss| (for each warp by itself), and this CTA's share of x with zeros
+// for the rows that do not count, which dW's product adds up times g's zeros (they may hold
+// anything).
+__device__ __forceinline__ float gain_of_few(const TileParams &p) {
   float top = 0.f;
-  for (int i = lane; i < p.rows; i += 32)
+  for (int i = threadIdx.x & 31; i < p.rows; i += 32)
     if (target_of(p, i) >= 0) {
       const float d = abs_weight(p.dloss, i);
       if (d <= kLargestFinite) top = fmaxf(top, d);
     }
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (top == 0.f) top = 1.f;
-  if (cta == 0 && t == 0) *p.r.gain = top;
+  return top == 0.f ? 1.f : top;
+}
+__device__ __forceinline__ void copy_few(const TileParams &p, int cta, int ctas, int t) {
   const int64_t pieces = p.r.ldx / 8, all = (p.rows + 63) / 64 * 64 * pieces;
   for (int64_t i = cta * 256 + t; i < all; i += ctas * 256) {
     const int row = (int)(i / pieces);
@@ -563,7 +569,6 @@ __device__ __forceinline__ float prepare_few(const TileParams &p, int cta, int c
     if (live) v.load(from, (int64_t)p.cols * 2, c * 16);
     reinterpret_cast<uint4 *>(p.r.x)[i] = live ? v.value(from, (int64_t)p.cols * 2, c * 16) : make_uint4(0, 0, 0, 0);
   }
-  return top;
 }
 
 template <int MODE, int CG>
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
   const uint32_t a_bytes = (uint32_t)(kAParts * a_rows) * 128, stage_bytes = a_bytes + R::kB;
   const int S = CG == 1 ? R::stages(kAParts * a_rows, 1) : MODE == MODE_DW ? R::stages(128, p.boxes) : R::stages(128, 1);
   constexpr bool kMnA = MODE == MODE_DW, kMnB = MODE == MODE_DX || MODE == MODE_DW;
-  constexpr bool kChunk = MODE == MODE_LSE;
+  constexpr bool kChunk = MODE == MODE_LSE || MODE == MODE_G;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
     prefetch_tmap(&tmBh);
-    if (R::kHasBoxes && (MODE == MODE_G || p.vec)) prefetch_tmap(&tmO);
+    if (R::kHasBoxes && (MODE != MODE_DW || p.vec)) prefetch_tmap(&tmO);
   }
   // the blocks of K of a unit
   const auto k_of = [&](const Tiles &tiles, int num_kb, const Unit &u, int i, int &kb0) {
@@ -713,7 +718,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
                                (kMnB ? kMnMajorB : 0u);
         uint32_t d = 0;
         for (int k = 0; k < max(nk, 1); ++k) {
-          // an accumulator for the tile, or (LSE) for each chunk of K
+          // an accumulator for the tile, or (LSE, G) for each chunk of K
           const bool start = k == 0 || (kChunk && k % kChunkKb == 0);
           if (start) {
             if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.wait, kErrMma)) {
@@ -759,13 +764,17 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
   } else {
     // q: the TMEM lanes this warp may read; half: its half of a tile's columns; team: of the
     // two that take turns, each with an accumulator of its own
+    constexpr int kTeams = R::kTeams;
     const int q = warp & 3, half = (warp - 2) >> 2 & 1, team = (warp - 2) >> 3;
-    constexpr int kTeams = R::kOut / 8;
     const int box_count = MODE == MODE_DW ? p.boxes : 1;
     Boxes mine{boxes + (warp - 2) * box_count * (int)kBoxB, box_count, 0};
     float gain = 0.f;
     if (MODE == MODE_DW) gain = *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
-    if (MODE == MODE_G && CG == 1 && !p.r.count) gain = prepare_few(p, cid, ncl, (int)threadIdx.x - 64);
+    bool copy = MODE == MODE_G && CG == 1 && !p.r.count;
+    if (copy) {
+      gain = gain_of_few(p);
+      if (cid == 0 && threadIdx.x == 64) *p.r.gain = gain;
+    }
     int acc = team;
     uint32_t acc_phase = 0;
     const auto release = [&] {  // the accumulator has been read
@@ -787,26 +796,52 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
       const int row0 = u.tm * 128 * CG + pos * 128 + q * 32;
       const int lower = u.w > 128 ? 128 : u.w / 2, c0 = half ? lower : 0, wide = half ? u.w - lower : lower, n = u.n0 + c0;
       const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
-      if constexpr (MODE == MODE_LSE) {
-        const bool live = row0 < rows && u.n0 < p.vocab;  // (else a half tile past the end)
+      if constexpr (kChunk) {
+        const int left = min(wide, p.width - n);  // (G)
+        const bool live = MODE == MODE_LSE ? row0 < rows && u.n0 < p.vocab  // (else a half tile past the end)
+                                           : left > 0 && (CG == 2 || row0 < p.low);
         float l[128];
+        GRow r{};
+        if (MODE == MODE_G) r = g_row(p, row0 + lane, gain);  // (read while the tile is waited for)
         bool good = true;
         for (int k = 0; k < num_kb; k += kChunkKb) {
           if (!(good = warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore))) break;
           fence_after();
           if (live) add_chunk(l, lanes + (uint32_t)(acc * 256 + c0), wide, k == 0);
           release();
+          if (copy && (k > 0 || num_kb <= kChunkKb)) {  // (the first two chunks come from L2)
+            copy_few(p, cid, ncl, (int)threadIdx.x - 64);
+            copy = false;
+          }
         }
-        // the upper half's sums to the lower half's warps; a buffer for each of two turns
-        float2 *upper = reinterpret_cast<float2 *>(boxes) + turn * 128 + q * 32 + lane;
-        float2 sum = make_float2(kLeast, 0.f);
-        if (live && good) {
-          const int row = row0 + lane;
-          sum = sum_exp(p, l, n, wide, target_of(p, row), p.hit + row);
-          if (half) *upper = sum;
+        if constexpr (MODE == MODE_G) {
+          if (!good) break;
+          if (!live) continue;
+          // the sums move down as columns are taken, so that the code for those is there once
+          // (800 x 1000 x 50264 118 -> 100 us of this kernel)
+          constexpr int W = CG == 1 ? 32 : 64;
+#pragma unroll 1
+          for (int c = 0; c < left; c += W) {
+            uint32_t v[W / 32][32];
+#pragma unroll
+            for (int k = 0; k < W; ++k) v[k / 32][k % 32] = __float_as_uint(l[k]);
+            if constexpr (CG == 1) leave_g_few(p, r, v[0], n + c, row0 + lane);  // (rows from p.low on are the second values')
+            else leave_g(p, &tmO, r, v, n + c, row0, mine);
+#pragma unroll
+            for (int k = 0; k + W < 128; ++k) l[k] = l[k + W];
+          }
+        } else {
+          // the upper half's sums to the lower half's warps; a buffer for each of two turns
+          float2 *upper = reinterpret_cast<float2 *>(boxes) + turn * 128 + q * 32 + lane;
+          float2 sum = make_float2(kLeast, 0.f);
+          if (live && good) {
+            const int row = row0 + lane;
+            sum = sum_exp(p, l, n, wide, target_of(p, row), p.hit + row);
+            if (half) *upper = sum;
+          }
+          if (!(ok = all_take(good))) break;  // the eight warps go on or give up together
+          if (live && !half) p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row0 + lane] = join_sums(sum, *upper);
         }
-        if (!(ok = all_take(good))) break;  // the eight warps go on or give up together
-        if (live && !half) p.part[(int64_t)(u.n0 >> 7) * p.r.rows_pad + row0 + lane] = join_sums(sum, *upper);
       } else {
         if (!warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore)) break;
         fence_after();
@@ -822,33 +857,22 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
           if (row0 < rows && w > 0) take_dx(p, tmem, acc_at, w, k_of(tiles, num_kb, u, i, kb0) == 0);
           release();
         } else {
-          const int end = MODE == MODE_G ? p.width : p.v0 + row0 < p.vocab ? p.cols : 0;
+          const int end = MODE == MODE_G_ONE ? p.width : p.v0 + row0 < p.vocab ? p.cols : 0;
           const int left = min(wide, end - n);
-          if constexpr (!R::kHasBoxes) {  // (G of few rows)
-            const GRow r = g_row(p, row0 + lane, gain);
-            // (rows from p.low on are the second values')
-            for (int c = 0; c < left && row0 < p.low; c += 32) {
-              uint32_t v[32];
-              tmem_ld_32cols(tmem + (uint32_t)c, v);
-              tmem_ld_wait();
-              leave_g_few(p, r, v, n + c, row0 + lane);
-            }
-            release();
-          } else {
-            if (left <= 0) release();
-            for (int c = 0; c < left; c += 64) {
-              uint32_t v[2][32];
-              tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
-              tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
-              tmem_ld_wait();
-              if (c + 64 >= left) release();
-              if constexpr (MODE == MODE_G) leave_g(p, &tmO, v, n + c, row0, mine);
-              else leave_dw(p, &tmO, v, n + c, p.v0 + row0, mine, gain);
-            }
+          if (left <= 0) release();
+          for (int c = 0; c < left; c += 64) {
+            uint32_t v[2][32];
+            tmem_ld_32cols(tmem + (uint32_t)c, v[0]);
+            tmem_ld_32cols(tmem + (uint32_t)(c + 32), v[1]);
+            tmem_ld_wait();
+            if (c + 64 >= left) release();
+            if constexpr (MODE == MODE_G_ONE) leave_g(p, &tmO, g_row(p, row0 + lane, 0.f), v, n + c, row0, mine);
+            else leave_dw(p, &tmO, v, n + c, p.v0 + row0, mine, gain);
           }
         }
       }
     }
+    if (copy) copy_few(p, cid, ncl, (int)threadIdx.x - 64);  // (a CTA without a tile)
     if (lane == 0) tma_store_wait_all();
     __syncwarp();
   }
@@ -1312,7 +1336,9 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
     if ((st = logits_maps(&m, p, f, w, ctx.dev->info.sms)) != MM_OK) return st;
     if (direct && (st = direct_map(&m.a, a, f)) != MM_OK) return st;
     if ((st = rows_map(&m.o, p.tx, g, p.width, rows_pad, piece, 32)) != MM_OK) return st;
-    if ((st = launch_tiles<MODE_G>(f, p, m, a.rows, ctx)) != MM_OK) return st;
+    if ((st = f.cg == 2 && p.num_kb <= kChunkKb ? launch_tiles<MODE_G_ONE, 2>(p, m, a.rows, ctx)
+                                                : launch_tiles<MODE_G>(f, p, m, a.rows, ctx)) != MM_OK)
+      return st;
     p.bn = bn_cols;
     p.tiles_n = tiles_cols;
     if (a.dx) {
