@@ -191,11 +191,13 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
 //   DX       g W, W MN-major as it lies, K the piece of the vocabulary; added to
 //            fp32 sums over the pieces
 //   DW       g^T x, both MN-major as they lie, K the rows
+//   DW_LONG  DW over more rows than kLongRows, in chunks of kLongChunkKb
 // 256 x 256 tiles on pairs of SMs, or 128 x 256 on single ones where there are few
 // rows; persistent, two accumulators in TMEM, so that a tile's epilogue runs under
 // the next tile's main loop.  Neither the rows that count nor the tiles are known
 // to the host: each kernel reads the count and lays out its own tiles.
-enum Mode { MODE_LSE, MODE_G, MODE_G_ONE, MODE_DX, MODE_DW };
+enum Mode { MODE_LSE, MODE_G, MODE_G_ONE, MODE_DX, MODE_DW, MODE_DW_LONG };
+constexpr __host__ __device__ bool is_dw(int mode) { return mode == MODE_DW || mode == MODE_DW_LONG; }
 
 // Warp 0 copies, warp 1 issues MMAs, the others take tiles out, eight a tile.  Where a
 // tile leaves in 16 bits from one sum over K there are 16, eight for each accumulator:
@@ -292,7 +294,7 @@ constexpr uint32_t kSmemBytes = 227 * 1024, kBarBytes = 1024;
 template <int MODE, int CG>
 struct Ring {
   static constexpr int kOut = out_warps(MODE, CG), kTeams = kOut / 8;
-  static constexpr bool kHasBoxes = CG == 2 && (MODE == MODE_G || MODE == MODE_G_ONE || MODE == MODE_DW);
+  static constexpr bool kHasBoxes = CG == 2 && (MODE == MODE_G || MODE == MODE_G_ONE || is_dw(MODE));
   static constexpr uint32_t kB = (CG == 2 ? 128 : 256) * 128;
   static constexpr int kMaxStages = 6;
   static constexpr size_t kSmem = kSmemBytes;
@@ -349,6 +351,14 @@ __device__ __forceinline__ bool all_take(bool ok) {
 // was off by -2.4e-4 at K = 4096 and a logit of 30, by -0.8 % at 1000, by -6 % at K = 16384 and
 // 1000, which is a gradient where there is none.  The chunks take 2-4 % of the gradients' time.)
 constexpr int kChunkKb = 8;
+// DW: a sum over the rows falls short by up to 2^-24 of itself a step of 16 rows, in one chain
+// by 6e-5 at 65536 rows, a third of an f16 rounding, 3e-4 at 262144 and 1.1e-3 at 1048576 (an
+// error of 1.2e-3 where rounding alone leaves 2e-4).  Sums over 8192 rows at a time leave 1e-5.
+// They take a longer ring and half of the warps, which is faster besides, from about 1000 rows
+// on: us of this product, two teams / one with chunks: 800 x 1000 x 50264 67 / 67, 2048 x 4096 x
+// 32000 305 / 292, 8192 x 256 x 32000 104 / 97, 8192 x 4096 x 16000 607 / 588; chunks of 1024 rows
+// 597; 16 x 4096 x 32000, all epilogue, two teams 51, one 64.
+constexpr int kLongChunkKb = 128, kLongRows = 1024;
 
 // A chunk of w columns, added to a thread's sums (the first: the sums themselves).
 __device__ __forceinline__ void add_chunk(float (&sum)[128], uint32_t tmem, int w, bool first) {
@@ -582,8 +592,9 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
   const int a_rows = CG == 1 ? p.a_rows : 128;
   const uint32_t a_bytes = (uint32_t)(kAParts * a_rows) * 128, stage_bytes = a_bytes + R::kB;
   const int S = CG == 1 ? R::stages(kAParts * a_rows, 1) : MODE == MODE_DW ? R::stages(128, p.boxes) : R::stages(128, 1);
-  constexpr bool kMnA = MODE == MODE_DW, kMnB = MODE == MODE_DX || MODE == MODE_DW;
-  constexpr bool kChunk = MODE == MODE_LSE || MODE == MODE_G;
+  constexpr bool kMnA = is_dw(MODE), kMnB = MODE == MODE_DX || is_dw(MODE);
+  // blocks of K that an accumulator holds (0: all)
+  constexpr int kChunk = MODE == MODE_LSE || MODE == MODE_G ? kChunkKb : MODE == MODE_DW_LONG ? kLongChunkKb : 0;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -617,7 +628,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
     prefetch_tmap(&tmBh);
-    if (R::kHasBoxes && (MODE != MODE_DW || p.vec)) prefetch_tmap(&tmO);
+    if (R::kHasBoxes && (!is_dw(MODE) || p.vec)) prefetch_tmap(&tmO);
   }
   // the blocks of K of a unit
   const auto k_of = [&](const Tiles &tiles, int num_kb, const Unit &u, int i, int &kb0) {
@@ -653,9 +664,9 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
   const uint32_t leader_tempty0 = CG == 2 ? map_to_rank(tempty0, 0) : tempty0;
   pdl_wait();
   const int rows = row_count(p.r, p.rows);
-  const Tiles tiles = tiles_of(MODE == MODE_DW ? p.width : rows, 128 * CG, p.tiles_n, p.bn, p.places,
+  const Tiles tiles = tiles_of(is_dw(MODE) ? p.width : rows, 128 * CG, p.tiles_n, p.bn, p.places,
                                MODE == MODE_DX ? max_parts_of(p.piece_kb) : 0);
-  const int num_kb = MODE == MODE_DW ? (rows + 63) / 64 * (p.low > 64 ? 2 : 1) : p.num_kb;
+  const int num_kb = is_dw(MODE) ? (rows + 63) / 64 * (p.low > 64 ? 2 : 1) : p.num_kb;
   if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0;
@@ -718,8 +729,8 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
                                (kMnB ? kMnMajorB : 0u);
         uint32_t d = 0;
         for (int k = 0; k < max(nk, 1); ++k) {
-          // an accumulator for the tile, or (LSE, G) for each chunk of K
-          const bool start = k == 0 || (kChunk && k % kChunkKb == 0);
+          // an accumulator for the tile, or for each chunk of K
+          const bool start = k == 0 || (kChunk && k % max(kChunk, 1) == 0);
           if (start) {
             if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.wait, kErrMma)) {
               ok = false;
@@ -754,7 +765,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
             stage = 0;
             phase ^= 1;
           }
-          if (k + 1 == nk || (kChunk && (k + 1) % kChunkKb == 0)) finish();
+          if (k + 1 == nk || (kChunk && (k + 1) % max(kChunk, 1) == 0)) finish();
         }
       }
       mma_commit<CG>(drain);
@@ -769,7 +780,7 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
     const int box_count = MODE == MODE_DW ? p.boxes : 1;
     Boxes mine{boxes + (warp - 2) * box_count * (int)kBoxB, box_count, 0};
     float gain = 0.f;
-    if (MODE == MODE_DW) gain = *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
+    if (is_dw(MODE)) gain = *p.r.gain * (p.tx == MM_F16 ? 1.f / kF16Gain : 1.f);
     bool copy = MODE == MODE_G && CG == 1 && !p.r.count;
     if (copy) {
       gain = gain_of_few(p);
@@ -796,25 +807,25 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
       const int row0 = u.tm * 128 * CG + pos * 128 + q * 32;
       const int lower = u.w > 128 ? 128 : u.w / 2, c0 = half ? lower : 0, wide = half ? u.w - lower : lower, n = u.n0 + c0;
       const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
-      if constexpr (kChunk) {
-        const int left = min(wide, p.width - n);  // (G)
+      if constexpr (kChunk > 0) {
+        const int left = min(wide, (MODE == MODE_G ? p.width : p.v0 + row0 < p.vocab ? p.cols : 0) - n);  // (G, DW)
         const bool live = MODE == MODE_LSE ? row0 < rows && u.n0 < p.vocab  // (else a half tile past the end)
                                            : left > 0 && (CG == 2 || row0 < p.low);
         float l[128];
         GRow r{};
         if (MODE == MODE_G) r = g_row(p, row0 + lane, gain);  // (read while the tile is waited for)
         bool good = true;
-        for (int k = 0; k < num_kb; k += kChunkKb) {
+        for (int k = 0; k < num_kb; k += kChunk) {
           if (!(good = warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore))) break;
           fence_after();
           if (live) add_chunk(l, lanes + (uint32_t)(acc * 256 + c0), wide, k == 0);
           release();
-          if (copy && (k > 0 || num_kb <= kChunkKb)) {  // (the first two chunks come from L2)
+          if (copy && (k > 0 || num_kb <= kChunk)) {  // (the first two chunks come from L2)
             copy_few(p, cid, ncl, (int)threadIdx.x - 64);
             copy = false;
           }
         }
-        if constexpr (MODE == MODE_G) {
+        if constexpr (MODE != MODE_LSE) {
           if (!good) break;
           if (!live) continue;
           // the sums move down as columns are taken, so that the code for those is there once
@@ -825,7 +836,8 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
             uint32_t v[W / 32][32];
 #pragma unroll
             for (int k = 0; k < W; ++k) v[k / 32][k % 32] = __float_as_uint(l[k]);
-            if constexpr (CG == 1) leave_g_few(p, r, v[0], n + c, row0 + lane);  // (rows from p.low on are the second values')
+            if constexpr (MODE == MODE_DW_LONG) leave_dw(p, &tmO, v, n + c, p.v0 + row0, mine, gain);
+            else if constexpr (CG == 1) leave_g_few(p, r, v[0], n + c, row0 + lane);  // (rows from p.low on are the second values')
             else leave_g(p, &tmO, r, v, n + c, row0, mine);
 #pragma unroll
             for (int k = 0; k + W < 128; ++k) l[k] = l[k + W];
@@ -1356,7 +1368,8 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
       m.bh = m.o = m.b;
       if (p.vec && (st = rows_map(&m.o, p.tx, a.dweight, a.cols, a.vocab, a.vocab == 1 ? p.r.ldx : a.lddw, 32)) != MM_OK)
         return st;
-      if ((st = launch_tiles<MODE_DW, 2>(p, m, p.width, ctx)) != MM_OK) return st;
+      st = a.rows > kLongRows ? launch_tiles<MODE_DW_LONG, 2>(p, m, p.width, ctx) : launch_tiles<MODE_DW, 2>(p, m, p.width, ctx);
+      if (st != MM_OK) return st;
     }
   }
   if (!a.dx) return MM_OK;
