@@ -1088,8 +1088,9 @@ mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, const P
   const int sms = ctx.dev->info.sms;
   GatherParams p{a, r, backward, 0, std::min(a.rows, 2 * sms), pack};
   while (p.log_threads < 9 && (32ll << p.log_threads) < r.ldx) ++p.log_threads;  // (up to four pieces each)
-  const int64_t copy = std::min<int64_t>(((pack.rows << pack.log_threads) + kGatherThreads - 1) / kGatherThreads, 8 * sms);
-  cudaError_t e = launch_pdl(gather_kernel, dim3((unsigned)(p.blocks + copy)), dim3(kGatherThreads), 0, ctx.stream, dim3(1), p);
+  const PackShape copy = pack_shape(pack.rows, pack.ld16, kGatherThreads, 8 * sms);
+  p.pack.log_threads = copy.log_threads;
+  cudaError_t e = launch_pdl(gather_kernel, dim3((unsigned)(p.blocks + copy.blocks)), dim3(kGatherThreads), 0, ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch (gather)");
   count_operator_launch();
   return MM_OK;
@@ -1210,7 +1211,7 @@ mm_status place_weight(const LossArgs &a, TmaRows *w, PackRows *pack, LaunchCtx 
   void *to = nullptr;
   mm_status st = get_scratch(ctx, SCRATCH_REPACK, (size_t)(ld16 * a.vocab), &to);
   if (st != MM_OK) return st;
-  *pack = pack_job(w->p, w->ld, w->rows, w->bytes, to, ld16);
+  *pack = pack_job(w->p, w->ld, w->rows, w->bytes, to, ld16, 0);  // (shared out where it is launched)
   w->p = to;
   w->ld = ld16;
   return MM_OK;

@@ -16,9 +16,9 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackRows p) {
 }
 
 mm_status pack(TmaRows &r, uint8_t *dst, int64_t ld16, LaunchCtx &ctx) {
-  const PackRows p = pack_job(r.p, r.ld, r.rows, r.bytes, dst, ld16);
-  const int64_t blocks = std::min<int64_t>(((r.rows << p.log_threads) + 255) / 256, 16 * ctx.dev->info.sms);
-  cudaError_t e = launch_pdl(pack_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, ctx.stream, dim3(1), p);
+  const PackShape shape = pack_shape(r.rows, ld16, 256, 16 * ctx.dev->info.sms);
+  const PackRows p = pack_job(r.p, r.ld, r.rows, r.bytes, dst, ld16, shape.log_threads);
+  cudaError_t e = launch_pdl(pack_rows_kernel, dim3((unsigned)shape.blocks), dim3(256), 0, ctx.stream, dim3(1), p);
   if (e != cudaSuccess) return cuda_error(e, "row copy launch");
   count_operator_launch();
   r.p = dst;

@@ -3,6 +3,8 @@
 
 #include <cstdint>
 
+#include "../pack_shape.h"
+
 namespace mm {
 namespace {
 
@@ -56,7 +58,7 @@ struct RowPiece {
 
 // `rows` rows of `bytes` bytes, ld apart, to rows of ld16 bytes that start on 16, the last
 // piece of each filled up with zeros.  `threads`: those that take part, of which this is
-// number `thread`; a power of two of them to a row.
+// number `thread`; a power of two of them to a row, no more than there are.
 struct PackRows {
   const uint8_t *from;
   int64_t ld, rows, bytes;
@@ -64,14 +66,13 @@ struct PackRows {
   int64_t ld16;
   int log_threads;
 };
-inline PackRows pack_job(const void *from, int64_t ld, int64_t rows, int64_t bytes, void *to, int64_t ld16) {
-  PackRows p{static_cast<const uint8_t *>(from), ld, rows, bytes, static_cast<uint8_t *>(to), ld16, 0};
-  while (p.log_threads < 8 && (64ll << p.log_threads) < ld16) ++p.log_threads;  // (up to four pieces each)
-  return p;
+inline PackRows pack_job(const void *from, int64_t ld, int64_t rows, int64_t bytes, void *to, int64_t ld16, int log_threads) {
+  return {static_cast<const uint8_t *>(from), ld, rows, bytes, static_cast<uint8_t *>(to), ld16, log_threads};
 }
 __device__ __forceinline__ void pack_rows(const PackRows &p, int64_t thread, int64_t threads) {
   constexpr int U = 4;  // pieces read before the first is stored
   const int row_threads = 1 << p.log_threads, t = (int)thread & (row_threads - 1);
+  // (a last, incomplete group of threads writes what others write too)
   for (int64_t r = thread >> p.log_threads; r < p.rows; r += threads >> p.log_threads) {
     const uint8_t *from = p.from + r * p.ld;
     uint8_t *to = p.to + r * p.ld16;
