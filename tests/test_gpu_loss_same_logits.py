@@ -40,3 +40,24 @@ def test_one_token_holds_all(rows, cols, vocab, offset, t):
     mm.check(mm.mm_cross_entropy_backward(x, w, targets, lse, None, dx, dw, rows, cols, vocab, x.stride(0), w.stride(0),
                                           dx.stride(0), dw.stride(0), (t, I64, t)))
     assert not bool(dx.any()) and not bool(dw.any())
+
+
+@pytest.mark.parametrize("cols", [520, 4096])
+@pytest.mark.parametrize("t", [BF, H])
+def test_backward_in_slices(cols, t):
+    """lse of one call over all positions, gradients by calls over some of them, whose products
+    have other tiles: the same logits still."""
+    torch = T()
+    g = generator(cols)
+    rows, vocab = 700, 900
+    x, w = rows_of(g, rows, cols, t), rows_of(g, vocab, cols, t)
+    x.copy_((x.abs() + 0.5) * 4)
+    w.copy_((w.abs() + 0.5) * 4)
+    w[1:] *= 0.25
+    targets = torch.zeros(rows, dtype=torch.int64, device="cuda")
+    _, lse = forward(x, w, targets)
+    for n in (1, 16, 100, 128, 129, 300):
+        dx, dw = torch.ones_like(x), torch.ones_like(w)
+        mm.check(mm.mm_cross_entropy_backward(x, w, targets, lse, None, dx, dw, n, cols, vocab, x.stride(0), w.stride(0),
+                                              dx.stride(0), dw.stride(0), (t, I64, t)))
+        assert not bool(dx[:n].any()) and not bool(dw.any()) and bool((dx[n:] == 1).all())
