@@ -638,20 +638,16 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
     kb0 = u.part * per;
     return max(0, min(per, num_kb - kb0));
   };
-  if (CG == 1 && warp == 0 && lane == 0) {
+  if (MODE == MODE_LSE && CG == 1 && warp == 0 && lane == 0) {
     // few rows: the first blocks of W into L2 while the kernel before still runs (one row
     // tile, so the first unit does not depend on the rows that count).  16 x 4096 x 32000:
-    // none 47.5 us, 8 blocks 46.4, 16 45.8.
-    const Tiles tiles = tiles_of(1, 128, p.tiles_n, p.bn, p.places, MODE == MODE_DX ? max_parts_of(p.piece_kb) : 0);
+    // none 48.5 us, 8 blocks 47.4, 16 46.7.  Backward, where products of W follow one another,
+    // it gains nothing there (164.4 us without, 164.6 with) and loses where W stays in L2: 64 x
+    // 1024 x 32000 82.4 and 88.5.
+    const Tiles tiles = tiles_of(1, 128, p.tiles_n, p.bn, p.places);
     if (cid < tiles.total) {
       const Unit u = unit_at(tiles, p.bn, cid);
-      int kb0;
-      const int nk = min(k_of(tiles, p.num_kb, u, cid, kb0), 16);
-      for (int kb = kb0; kb < kb0 + nk; ++kb) {
-        if (!kMnB) tma_prefetch_2d(u.w == p.bn ? &tmB : &tmBh, kb * 64, u.n0);
-        else
-          for (int j = 0; j < u.w / 64; ++j) tma_prefetch_2d(&tmB, u.n0 + j * 64, kb * 64);
-      }
+      for (int kb = 0; kb < min(p.num_kb, 16); ++kb) tma_prefetch_2d(u.w == p.bn ? &tmB : &tmBh, kb * 64, u.n0);
     }
   }
   if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), 512);
