@@ -522,8 +522,11 @@ mm_status mm_embedding_backward(const void *dout, const void *tokens, const void
  *   loss      `rows` fp32 (dt.c = MM_F32); 0 for a position without a target.
  *   lse       `rows` fp32, what mm_cross_entropy_backward takes; 0 for a position
  *             without a target; NULL: not written.
- * The products are summed in fp32 and enter the exponentials unrounded.  Positions
- * without a target are left out of the products, so they cost next to nothing.
+ * The products are summed in fp32 and enter the exponentials unrounded, less the
+ * largest of their row, so that logits of any finite size have their loss; one of
+ * +infinity or NaN makes its row's loss and lse NaN, one of -infinity has no share.
+ * Positions without a target are left out of the products, so they cost next to
+ * nothing.
  * rows of 0 is a no-op; cols of 0 makes every logit 0.  rows, cols, vocab < 2^30.
  */
 mm_status mm_cross_entropy(const void *x, const void *weight, const void *targets, float *loss, float *lse,
@@ -541,11 +544,14 @@ mm_status mm_cross_entropy(const void *x, const void *weight, const void *target
  *             address and leading dimension).
  *   dweight   vocab x cols, overwritten; NULL: not computed.
  *             Both are of type dt.c, which is dt.a.
- * g, divided by the largest |dloss|, is rounded to dt.a (f16: after 2^14 is
- * taken in; up to 128 rows: to the sum of two such values) before the two
- * products, whose sums are fp32; equal calls give equal bits.  In f16 positions
- * whose dloss is below 2^-20 of the largest lose bits of their dx.  cols of 0 is a no-op; rows of 0 writes zeros to dweight.
- * rows, cols, vocab < 2^30.
+ * The logits are the forward pass's, bit for bit, for some of its positions as for
+ * all of them, so that a token that holds a position's whole mass has a share of 1
+ * and no gradient.  g, divided by the largest |dloss|, is rounded to dt.a (f16:
+ * after 2^14 is taken in; up to 128 rows: to the sum of two such values) before the
+ * two products, whose sums are fp32; equal calls give equal bits.  In f16 positions
+ * whose dloss is below 2^-20 of the largest lose bits of their dx.
+ * cols of 0 is a no-op; rows of 0 writes zeros to dweight; vocab of 0 writes zeros
+ * to dx.  rows, cols, vocab < 2^30.
  */
 mm_status mm_cross_entropy_backward(const void *x, const void *weight, const void *targets, const float *lse,
                                     const float *dloss, void *dx, void *dweight, int64_t rows, int64_t cols,

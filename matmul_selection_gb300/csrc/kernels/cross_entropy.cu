@@ -14,9 +14,9 @@
 // products run over whole tiles of rows that count, and what a padded row holds
 // is never read.
 // What bounds it: above a few hundred rows the tensor cores, under the power cap
-// (8192 x 4096 x 131072 5.1-5.3 ms, 1.65-1.72 PFLOP/s, 1.94 in a short burst; backward
-// 8192 x 4096 x 32000, a quarter without a target, 2.9-3.0 ms); below, W's bytes (16 x
-// 4096 x 32000 47 us, 5.6 TB/s over the whole call; backward, W twice and dW, 164 us).
+// (8192 x 4096 x 131072 5.2-5.3 ms, 1.66-1.70 PFLOP/s; backward 8192 x 4096 x 32000, a
+// quarter without a target, 3.0 ms); below, W's bytes (16 x 4096 x 32000 46-47 us, 5.6 TB/s
+// over the whole call; backward, W twice and dW, 163 us).
 #include <algorithm>
 
 #include "../operators.h"

@@ -138,3 +138,32 @@ def test_one_token_holds_the_mass(rows, vocab):
         off = torch.minimum(1.01 * R, R * 2.0 ** -17 + chain(vocab) * U32 * (1 + R)) + 4 * U32 * want
         close(loss, want, off)
         close(lse, 64 + want, off + 65 * U32)
+
+
+@pytest.mark.parametrize("rows,vocab", [(20, 1000), (300, 700)])
+@pytest.mark.parametrize("t", [BF, H])
+def test_infinite_logits(rows, vocab, t):
+    """-infinity has no share (as a target, an infinite loss), +infinity leaves its rows NaN."""
+    torch = T()
+    x, w = one_column(rows, 16, vocab, t, (1.0, 3.0))
+    c, inf = 8, float("inf")
+    w[5, c] = w[400:, c] = -inf
+    targets = torch.full((rows,), 7, device="cuda")
+    targets[1] = 5
+    loss, lse = forward(x, w, targets)
+    want = torch.full((rows,), 399.0, dtype=torch.float64, device="cuda").log()
+    off = chain(vocab) * U32 + 4 * U32 * want
+    close(lse, 3 + want, off + 9 * U32)
+    want[1] = inf
+    close(loss, want, off)
+    x[2] = 0
+    x[2, c] = -1.0  # (so that -infinity becomes +infinity)
+    x[3] *= -0.0
+    w[:, c] = torch.where(torch.isinf(w[:, c]), 1.0, w[:, c].float()).to(w.dtype)
+    w[650, c] = -inf
+    targets[1] = 7
+    loss, lse = forward(x, w, targets)
+    assert bool(torch.isnan(loss[2:4]).all()) and bool(torch.isnan(lse[2:4]).all())  # (0 times infinity: NaN)
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[2:4] = False
+    assert bool(torch.isfinite(loss[rest]).all()) and bool(torch.isfinite(lse[rest]).all())
