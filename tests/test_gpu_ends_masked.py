@@ -17,7 +17,7 @@ def no_wait_gave_up():
     assert mm.mm_operator_status() == mm.MM_OK, mm.mm_last_error()
 
 
-def masked_call(rows, cols, vocab, t, offset, dw, stream):
+def masked_call(rows, cols, vocab, t, offset, dw):
     torch = T()
     p = Problem(8, cols, vocab, t)
     x = rows_of(p.g, rows, cols, t, offset=offset)
@@ -28,10 +28,8 @@ def masked_call(rows, cols, vocab, t, offset, dw, stream):
     at = AROUND * cols
     dx = flat[at:at + rows * cols].view(rows, cols)
     dweight = torch.full((vocab, cols), 77.0, device="cuda").to(x.dtype) if dw else None
-    torch.cuda.synchronize()
     mm.check(mm.mm_cross_entropy_backward(x, p.w, targets, lse, dloss, dx, dweight, rows, cols, vocab, cols,
-                                          p.w.stride(0), cols, cols, (t, p.ti, t), stream))
-    torch.cuda.synchronize()
+                                          p.w.stride(0), cols, cols, (t, p.ti, t)))
     assert not bool(dx.any())
     assert bool((flat[:at] == 77).all()) and bool((flat[at + rows * cols:] == 77).all())
     assert dweight is None or not bool(dweight.any())
@@ -43,15 +41,11 @@ def masked_call(rows, cols, vocab, t, offset, dw, stream):
 def test_no_position_counts_after_a_larger_call(rows, cols, offset, dw, t):
     """The scratch starts at the same address for each call: the larger call's rows, whose
     first ones do not count and leave -1, lie where the masked call's row numbers would."""
-    torch = T()
-    stream = torch.cuda.Stream()
-    with torch.cuda.stream(stream):
-        before = Problem(2000, cols, 500, t)
-        before.targets[256:512] = -100
-        before.ok[256:512] = False
-        before.x[~before.ok] = float("nan")
-        before.work()
-        torch.cuda.synchronize()
-        before.check_backward(*before.backward(stream=stream.cuda_stream))
-        masked_call(rows, cols, 500, t, offset, dw, stream.cuda_stream)
-        before.check_backward(*before.backward(stream=stream.cuda_stream))
+    before = Problem(2000, cols, 500, t)
+    before.targets[256:512] = -100
+    before.ok[256:512] = False
+    before.x[~before.ok] = float("nan")
+    before.work()
+    before.check_backward(*before.backward())
+    masked_call(rows, cols, 500, t, offset, dw)
+    before.check_backward(*before.backward())
