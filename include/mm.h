@@ -547,9 +547,10 @@ mm_status mm_cross_entropy(const void *x, const void *weight, const void *target
  * The logits are the forward pass's, bit for bit, for some of its positions as for
  * all of them, so that a token that holds a position's whole mass has a share of 1
  * and no gradient.  g, divided by the largest |dloss|, is rounded to dt.a (f16:
- * after 2^14 is taken in; up to 128 rows: to the sum of two such values) before the
- * two products, whose sums are fp32; equal calls give equal bits.  In f16 positions
- * whose dloss is below 2^-20 of the largest lose bits of their dx.
+ * after 2^14 is taken in; at the targets, and up to 128 rows everywhere, to the sum
+ * of two such values) before the two products, whose sums are fp32; equal calls give
+ * equal bits.  In f16 positions whose dloss is below 2^-20 of the largest lose bits of
+ * their dx.
  * cols of 0 is a no-op; rows of 0 writes zeros to dweight; vocab of 0 writes zeros
  * to dx.  rows, cols, vocab < 2^30.
  */

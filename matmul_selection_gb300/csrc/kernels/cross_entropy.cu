@@ -9,14 +9,15 @@
 // The maximum is subtracted before the factor log2(e): the difference is exact where the
 // share is not small, whatever the logits' size, and the largest one's share is exactly 1.
 // Backward: the vocabulary in pieces, each the product again with g as the
-// epilogue's output in 16 bits, then its two products.
+// epilogue's output in 16 bits, then its two products; what g's rounding loses at the
+// targets, whose terms are the large ones, is kept and added.
 // Rows without a target are left out: the others' x is gathered first, so the
 // products run over whole tiles of rows that count, and what a padded row holds
 // is never read.
 // What bounds it: above a few hundred rows the tensor cores, under the power cap
 // (8192 x 4096 x 131072 5.2-5.3 ms, 1.66-1.70 PFLOP/s; backward 8192 x 4096 x 32000, a
 // quarter without a target, 3.0 ms); below, W's bytes (16 x 4096 x 32000 46-47 us, 5.6 TB/s
-// over the whole call; backward, W twice and dW, 163 us).
+// over the whole call; backward, W twice and dW, 164 us).
 #include <algorithm>
 
 #include "../operators.h"
@@ -65,6 +66,11 @@ struct Rows {
   float *ratio;     // [rows_pad] dloss / gain (f16: times kF16Gain), 0 past the count
   float *lse;       // [rows_pad]
   uint16_t *x;      // [rows_pad][ldx], zeros from cols to ldx and for rows up to a multiple of 64
+  // Backward of many rows: the rows in the order of their targets' tiles of 256 tokens, and
+  // what the rounding of g leaves at the targets (see leave_rest).
+  float *rest;      // [rows_pad] as g is scaled; 0 where nothing was left
+  int *first;       // [tiles + 1] the first i of a tile's targets
+  uint16_t *cells;  // [cell][64 rows][256 tokens]
   int64_t ldx;
   int rows_pad;
 };
@@ -181,6 +187,89 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
     const int64_t z0 = (int64_t)before * pieces, z1 = (int64_t)max(1, (before + 63) / 64) * 64 * pieces;
     for (int64_t i = z0 + t; i < z1; i += kGatherThreads)
       reinterpret_cast<uint4 *>(p.r.x)[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// The same for the backward pass of many rows, in the order in which the targets were sorted.
+constexpr int kTileTokens = 256, kLogTileTokens = 8, kCellRows = 64;
+struct SortedParams {
+  GatherParams g;
+  const uint2 *sorted;  // (tile of the target, row)
+  int tiles;            // the key of a row without a target
+  int64_t cell_pieces;  // all cells', of 16 bytes
+};
+__global__ void __launch_bounds__(kGatherThreads, 2) gather_sorted_kernel(const SortedParams q) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ float warp_max[kGatherWarps];
+  __shared__ int at_row[kGatherThreads];  // the source row of a place, -1: zeros, -2: left as it is
+  const GatherParams &p = q.g;
+  const LossArgs &a = p.a;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if ((int)blockIdx.x >= p.blocks) {
+    pack_rows(p.pack, ((int64_t)blockIdx.x - p.blocks) * kGatherThreads + t, ((int64_t)gridDim.x - p.blocks) * kGatherThreads);
+    return;
+  }
+  for (int64_t i = (int64_t)blockIdx.x * kGatherThreads + t; i < q.cell_pieces; i += (int64_t)p.blocks * kGatherThreads)
+    reinterpret_cast<uint4 *>(p.r.cells)[i] = make_uint4(0, 0, 0, 0);
+  float top = 0.f;  // of the finite ones
+#pragma unroll 4
+  for (int i = t; i < a.rows; i += kGatherThreads) {
+    const float d = abs_weight(a.dloss, i);
+    if (valid_target(a, i) >= 0 && d <= kLargestFinite) top = fmaxf(top, d);
+  }
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) warp_max[warp] = top;
+  __syncthreads();
+  for (int w = 0; w < kGatherWarps; ++w) top = fmaxf(top, warp_max[w]);
+  if (top == 0.f) top = 1.f;
+  if (blockIdx.x == 0 && t == 0) *p.r.gain = top;
+
+  const int none = q.tiles, pieces = (int)(p.r.ldx / 8);
+  const auto key_at = [&](int i) { return i < 0 ? -1 : i < a.rows ? (int)q.sorted[i].x : none; };
+  const int r0 = (int)((int64_t)p.r.rows_pad * blockIdx.x / p.blocks);
+  const int r1 = (int)((int64_t)p.r.rows_pad * (blockIdx.x + 1) / p.blocks);
+  const uint8_t *x = static_cast<const uint8_t *>(a.x);
+  for (int g0 = r0; g0 < r1; g0 += kGatherThreads) {
+    const int i = g0 + t;
+    if (i < r1) {
+      const int key = key_at(i), row = i < a.rows ? (int)q.sorted[i].y : -1;
+      const bool live = key < none;
+      at_row[t] = live ? row : i < kCellRows || key_at(i & ~(kCellRows - 1)) < none ? -1 : -2;
+      if (row >= 0) p.r.slot[row] = live ? i : -1;
+      if (live) p.r.row[i] = row;
+      p.r.target[i] = live ? valid_target(a, row) : -1;
+      p.r.ratio[i] = live ? ratio_of(a.dloss, row, top, a.tx) : 0.f;
+      p.r.lse[i] = live ? a.lse[row] : 0.f;
+      p.r.rest[i] = 0.f;
+      // (rows_pad is past the rows or the last of them is the last place: both ends are seen)
+      for (int k = key_at(i - 1) + 1; k <= key; ++k) p.r.first[k] = i;
+      if (i + 1 == p.r.rows_pad && live)
+        for (int k = key + 1; k <= none; ++k) p.r.first[k] = i + 1;
+      if (live && key_at(i + 1) >= none) *p.r.count = i + 1;
+      if (i == 0 && !live) *p.r.count = 0;
+    }
+    __syncthreads();
+    constexpr int U = 4;  // pieces read before the first is stored
+    const int threads = 1 << p.log_threads, t0 = t & (threads - 1), total = min(kGatherThreads, r1 - g0);
+    for (int k = t >> p.log_threads; k < total; k += kGatherThreads >> p.log_threads) {
+      const int source = at_row[k];
+      if (source == -2) continue;
+      const uint8_t *from = x + (int64_t)source * a.ldx * 2;
+      uint4 *to = reinterpret_cast<uint4 *>(p.r.x + (int64_t)(g0 + k) * p.r.ldx);
+      for (int c = t0; c < pieces; c += threads * U) {
+        RowPiece<2> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (source >= 0 && c + u * threads < pieces) v[u].load(from, (int64_t)a.cols * 2, (int64_t)(c + u * threads) * 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c + u * threads < pieces)
+            to[c + u * threads] = source >= 0 ? v[u].value(from, (int64_t)a.cols * 2, (int64_t)(c + u * threads) * 16)
+                                              : make_uint4(0, 0, 0, 0);
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -455,15 +544,42 @@ __device__ __forceinline__ GRow g_row(const TileParams &p, int row, float gain) 
   else if (r.target >= 0) r.ratio = ratio_of(p.dloss, row, gain, p.tx), r.lse = p.lse[row];
   return r;
 }
-__device__ __forceinline__ void make_g(const TileParams &p, const GRow &r, uint32_t (&v)[32], int first) {
+__device__ __forceinline__ float unpack(int tx, uint32_t w, int odd) {
+  if (tx == MM_BF16) return __uint_as_float(odd ? w & 0xffff0000u : w << 16);
+  const __half2 v = *reinterpret_cast<const __half2 *>(&w);
+  return odd ? __high2float(v) : __low2float(v);
+}
+// g of many rows is one 16-bit value.  Where a result has few large terms, which are those of the
+// targets, their rounding would be in it as its own is: errors 1.2 to 1.5 times those of the
+// results' rounding alone.  So what a target's g has lost is kept: dx adds it in fp32, times W's
+// row (dx_kernel), and dW as 64 more of K for each 64 rows and tile of 256 tokens in which
+// there are targets, which are few, since the rows are sorted by those tiles: cell b + j holds
+// rows 64 b .. and tile j, along a path on which one of the two grows at a time.  That takes
+// 3 % of the gradients' time above 800 rows, 5 % there, 10 % at 300 x 1024 x 32000 (the sort's 6
+// us, 4 % more of dW's K, W's rows in the last step); a second value of all g took twice dx's
+// and dW's products.
+__device__ __noinline__ void leave_rest(float *rests, uint16_t *cells, int tx, int row, int target, float g) {
+  const float rest = g - unpack(tx, pack2(tx, g, 0.f), 0);
+  rests[row] = rest;
+  const int64_t cell = (row >> 6) + (target >> kLogTileTokens);
+  cells[(cell * kCellRows + (row & (kCellRows - 1))) * kTileTokens + (target & (kTileTokens - 1))] =
+      (uint16_t)pack2(tx, rest, 0.f);
+}
+// (row: of many, where what g's rounding leaves is kept; else -1)
+__device__ __forceinline__ void make_g(const TileParams &p, const GRow &r, uint32_t (&v)[32], int first, int row) {
   const bool live = r.ratio != 0.f;  // (a weight of 0 takes its row out, whatever its logits)
 #pragma unroll
   for (int i = 0; i < 32; ++i)
     v[i] = __float_as_uint(exp_fast(__uint_as_float(v[i]) - r.lse) * r.ratio);
   const int at = r.target - first, left = p.vocab - first;
   if (__any_sync(0xffffffffu, (unsigned)at < 32u)) {
+    float g = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = at == i ? __float_as_uint(__uint_as_float(v[i]) - r.ratio) : v[i];
+    for (int i = 0; i < 32; ++i) {
+      g = at == i ? __uint_as_float(v[i]) - r.ratio : g;
+      v[i] = at == i ? __float_as_uint(g) : v[i];
+    }
+    if (row >= 0 && live && (unsigned)at < 32u) leave_rest(p.r.rest, p.r.cells, p.tx, row, r.target, g);
   }
   if (left < 32 || __any_sync(0xffffffffu, !live)) {
 #pragma unroll
@@ -476,7 +592,7 @@ __device__ __forceinline__ void leave_g(const TileParams &p, const CUtensorMap *
   uint8_t *box = boxes.next();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    make_g(p, r, v[h], p.v0 + n + 32 * h);
+    make_g(p, r, v[h], p.v0 + n + 32 * h, row0 + (int)(threadIdx.x & 31));
     fill_box(box, p.tx, h, v[h]);
   }
   store_box_tma(map, box, n, row0);
@@ -487,13 +603,8 @@ __device__ __forceinline__ void leave_g(const TileParams &p, const CUtensorMap *
 // rounding of one g (off by up to half a step, as its own rounding).
 // Up to 32 rows the two fill the 64 rows of one block of dW's K, with x twice.
 constexpr int kFewestRows = 32;
-__device__ __forceinline__ float unpack(int tx, uint32_t w, int odd) {
-  if (tx == MM_BF16) return __uint_as_float(odd ? w & 0xffff0000u : w << 16);
-  const __half2 v = *reinterpret_cast<const __half2 *>(&w);
-  return odd ? __high2float(v) : __low2float(v);
-}
 __device__ __forceinline__ void leave_g_few(const TileParams &p, const GRow &r, uint32_t (&v)[32], int n, int row) {
-  make_g(p, r, v, p.v0 + n);
+  make_g(p, r, v, p.v0 + n, -1);
   uint4 *high = reinterpret_cast<uint4 *>(p.g + (int64_t)row * p.ldg + n);
   uint4 *low = reinterpret_cast<uint4 *>(p.g + (int64_t)(row + p.low) * p.ldg + n);
 #pragma unroll
@@ -663,15 +774,27 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
   const Tiles tiles = tiles_of(is_dw(MODE) ? p.width : rows, 128 * CG, p.tiles_n, p.bn, p.places,
                                MODE == MODE_DX ? max_parts_of(p.piece_kb) : 0);
   const int num_kb = is_dw(MODE) ? (rows + 63) / 64 * (p.low > 64 ? 2 : 1) : p.num_kb;
+  // DW of many rows: where the targets of a unit's tile of tokens are, whose cells are more
+  // blocks of K (see leave_rest); read a unit ahead
+  const auto targets_of = [&](int i) {
+    if (!is_dw(MODE) || !p.r.first || i >= tiles.total) return make_int2(0, 0);
+    const int *first = p.r.first + (p.v0 >> kLogTileTokens) + unit_at(tiles, p.bn, i).tm;
+    return make_int2(first[0], first[1]);
+  };
+  const auto cells_of = [](int2 at) { return at.y > at.x ? ((at.y - 1) >> 6) - (at.x >> 6) + 1 : 0; };
   if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
+    int2 next = targets_of(cid);
     for (int i = cid; i < tiles.total && ok; i += ncl) {
       const Unit u = unit_at(tiles, p.bn, i);
+      const int2 at = next;
+      next = targets_of(i + ncl);
       int kb0;
       const int nk = k_of(tiles, num_kb, u, i, kb0), nh = u.w / CG, m0 = u.tm * 128 * CG + pos * 128, n0 = u.n0 + pos * nh;
-      for (int kb = kb0; kb < kb0 + nk; ++kb) {
+      const int end = kb0 + nk + cells_of(at), to_cells = (at.x >> 6) - nk, tile = (p.v0 >> kLogTileTokens) + u.tm;
+      for (int kb = kb0; kb < end; ++kb) {
         if (!warp_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.wait, kErrCopy)) {
           ok = false;
           break;
@@ -680,9 +803,12 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
         if (leader) mbar_expect_tx(full0 + 8 * stage, (uint32_t)(CG * (kAParts * a_rows + nh)) * 128);
         // (dW of few rows: both of g's values, one after the other along K)
         const bool low = MODE == MODE_DW && p.low > 64 && 2 * kb >= num_kb;
-        const int xb = low ? kb - num_kb / 2 : kb;
+        const bool rest = is_dw(MODE) && kb >= nk;  // (of a cell)
+        const int xb = low ? kb - num_kb / 2 : rest ? kb + to_cells : kb;
         if (kMnA) {
-          for (int j = 0; j < 2; ++j) load_box<CG>(sa + j * 8192, &tmA, bar, m0 + j * 64, (low ? p.low : 0) + xb * 64);
+          const CUtensorMap *ma = rest ? &tmBh : &tmA;
+          const int xa = rest ? pos * 128 : m0, ya = (low ? p.low : 0) + (rest ? xb + tile : xb) * 64;
+          for (int j = 0; j < 2; ++j) load_box<CG>(sa + j * 8192, ma, bar, xa + j * 64, ya);
         } else {
           load_box<CG>(sa, &tmA, bar, kb * 64, m0);
           if (kAParts == 2) load_box<CG>(sa + a_rows * 128, &tmA, bar, kb * 64, p.low);
@@ -717,10 +843,13 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
           acc_phase ^= 1;
         }
       };
+      int2 next = targets_of(cid);
       for (int i = cid; i < tiles.total && ok; i += ncl) {
         const Unit u = unit_at(tiles, p.bn, i);
+        const int2 at = next;
+        next = targets_of(i + ncl);
         int kb0;
-        const int nk = k_of(tiles, num_kb, u, i, kb0);
+        const int nk = k_of(tiles, num_kb, u, i, kb0) + cells_of(at);
         const uint32_t idesc = instr_desc(p.tx == MM_BF16, 128 * CG, (uint32_t)u.w) | (kMnA ? kMnMajorA : 0u) |
                                (kMnB ? kMnMajorB : 0u);
         uint32_t d = 0;
@@ -811,12 +940,14 @@ __global__ void __launch_bounds__(tile_threads(MODE, CG), 1)
         GRow r{};
         if (MODE == MODE_G) r = g_row(p, row0 + lane, gain);  // (read while the tile is waited for)
         bool good = true;
-        for (int k = 0; k < num_kb; k += kChunk) {
+        int nk = num_kb;
+        if (MODE == MODE_DW_LONG) nk += cells_of(targets_of(i));
+        for (int k = 0; k < nk; k += kChunk) {
           if (!(good = warp_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.wait, kErrStore))) break;
           fence_after();
           if (live) add_chunk(l, lanes + (uint32_t)(acc * 256 + c0), wide, k == 0);
           release();
-          if (copy && (k > 0 || num_kb <= kChunk)) {  // (the first two chunks come from L2)
+          if (copy && (k > 0 || nk <= kChunk)) {  // (the first two chunks come from L2)
             copy_few(p, cid, ncl, (int)threadIdx.x - 64);
             copy = false;
           }
@@ -963,6 +1094,8 @@ struct DxParams {
   LossArgs a;
   Rows r;
   const float *acc, *acc_cut;
+  const uint8_t *w;  // W, rows on 16 bytes ...
+  int64_t ldw;       // ... this far apart
   int tile_m, bn, tiles_n, places, piece_kb, acc_cols;  // of the product
   int vec;  // dx's rows start on 16 bytes
 };
@@ -971,9 +1104,29 @@ struct DxParams {
 template <int Q, int U>
 __device__ __forceinline__ void round_dx(const DxParams &p, const float4 *from, int parts, int64_t part_at, int rb, int col,
                                          int count, float gain) {
+  const int i = rb * 32 + (threadIdx.x & 31), left = p.a.cols - col;
+  const float rest = p.r.rest && i < count ? p.r.rest[i] : 0.f;  // (see leave_rest)
+  const int token = rest != 0.f ? p.r.target[i] : 0;
   float4 v[Q];
 #pragma unroll
   for (int k = 0; k < Q; ++k) v[k] = from[k * 32];
+  uint32_t row[2 * Q];
+  if (rest != 0.f) {
+    const uint16_t *from_w = reinterpret_cast<const uint16_t *>(p.w + (int64_t)token * p.ldw) + col;
+#pragma unroll
+    for (int k = 0; k < Q / 2; ++k) {
+      if (8 * k + 8 <= left) {
+        const uint4 u = reinterpret_cast<const uint4 *>(from_w)[k];
+        row[4 * k] = u.x, row[4 * k + 1] = u.y, row[4 * k + 2] = u.z, row[4 * k + 3] = u.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = 8 * k + 2 * e;
+          row[4 * k + e] = (c < left ? from_w[c] : 0u) | (c + 1 < left ? (uint32_t)from_w[c + 1] << 16 : 0u);
+        }
+      }
+    }
+  }
   for (int s = 1; s < parts; s += U) {
     float4 w[U][Q];
 #pragma unroll
@@ -987,8 +1140,14 @@ __device__ __forceinline__ void round_dx(const DxParams &p, const float4 *from, 
       for (int k = 0; k < Q; ++k)
         v[k].x += w[u][k].x, v[k].y += w[u][k].y, v[k].z += w[u][k].z, v[k].w += w[u][k].w;
   }
-  const int i = rb * 32 + (threadIdx.x & 31);
   if (i >= count || (!p.r.count && valid_target(p.a, i) < 0)) return;
+  if (rest != 0.f) {
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      v[k].x = fmaf(rest, unpack(p.a.tx, row[2 * k], 0), v[k].x), v[k].y = fmaf(rest, unpack(p.a.tx, row[2 * k], 1), v[k].y);
+      v[k].z = fmaf(rest, unpack(p.a.tx, row[2 * k + 1], 0), v[k].z), v[k].w = fmaf(rest, unpack(p.a.tx, row[2 * k + 1], 1), v[k].w);
+    }
+  }
   uint32_t w[2 * Q];
 #pragma unroll
   for (int k = 0; k < Q; ++k) {
@@ -996,7 +1155,6 @@ __device__ __forceinline__ void round_dx(const DxParams &p, const float4 *from, 
     w[2 * k + 1] = pack2(p.a.tx, v[k].z * gain, v[k].w * gain);
   }
   uint16_t *to = static_cast<uint16_t *>(p.a.dx) + (int64_t)(p.r.count ? p.r.row[i] : i) * p.a.lddx + col;
-  const int left = p.a.cols - col;
   if (p.vec && left >= 4 * Q) {
 #pragma unroll
     for (int k = 0; k < Q / 2; ++k)
@@ -1058,6 +1216,8 @@ struct Cut {
   }
 };
 
+int token_tiles(int vocab) { return (int)keys_of(vocab, kLogTileTokens); }
+int64_t cell_count(const Rows &r, int vocab) { return r.rows_pad / kCellRows + token_tiles(vocab); }
 Rows cut_rows(Cut &cut, const LossArgs &a, bool backward, bool direct) {
   Rows r;
   std::memset(&r, 0, sizeof r);
@@ -1080,13 +1240,23 @@ Rows cut_rows(Cut &cut, const LossArgs &a, bool backward, bool direct) {
   return r;
 }
 
-mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, const PackRows &pack, LaunchCtx &ctx) {
+// (sorted: room for twice as many (tile, row) as there are rows, or null)
+mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, const PackRows &pack, uint2 *sorted, LaunchCtx &ctx) {
   const int sms = ctx.dev->info.sms;
   GatherParams p{a, r, backward, 0, std::min(a.rows, 2 * sms), pack};
   while (p.log_threads < 9 && (32ll << p.log_threads) < r.ldx) ++p.log_threads;  // (up to four pieces each)
   const PackShape copy = pack_shape(pack.rows, pack.ld16, kGatherThreads, 8 * sms);
   p.pack.log_threads = copy.log_threads;
-  cudaError_t e = launch_pdl(gather_kernel, dim3((unsigned)(p.blocks + copy.blocks)), dim3(kGatherThreads), 0, ctx.stream, dim3(1), p);
+  const dim3 grid((unsigned)(p.blocks + copy.blocks));
+  cudaError_t e;
+  if (sorted) {
+    mm_status st = sort_tokens({a.targets, a.ti, a.vocab, a.rows, kLogTileTokens, sorted, sorted + a.rows}, ctx);
+    if (st != MM_OK) return st;
+    const SortedParams q{p, sorted, token_tiles(a.vocab), cell_count(r, a.vocab) * kCellRows * kTileTokens / 8};
+    e = launch_pdl(gather_sorted_kernel, grid, dim3(kGatherThreads), 0, ctx.stream, dim3(1), q);
+  } else {
+    e = launch_pdl(gather_kernel, grid, dim3(kGatherThreads), 0, ctx.stream, dim3(1), p);
+  }
   if (e != cudaSuccess) return cuda_error(e, "cross_entropy launch (gather)");
   count_operator_launch();
   return MM_OK;
@@ -1278,7 +1448,7 @@ mm_status launch_cross_entropy(const LossArgs &a, LaunchCtx &ctx) {
   PackRows pack;
   Maps m;
   if ((st = place_weight(a, &w, &pack, ctx)) != MM_OK) return st;
-  if (!direct && (st = launch_gather(a, p.r, false, pack, ctx)) != MM_OK) return st;
+  if (!direct && (st = launch_gather(a, p.r, false, pack, nullptr, ctx)) != MM_OK) return st;
   p.width = a.vocab;
   if ((st = logits_maps(&m, p, f, w, ctx.dev->info.sms)) != MM_OK) return st;
   if (direct && (st = direct_map(&m.a, a, f)) != MM_OK) return st;
@@ -1309,9 +1479,11 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   int dx_places = 0;
   mm_status st = f.cg == 1 ? tile_places<MODE_DX, 1>(ctx, &dx_places) : tile_places<MODE_DX, 2>(ctx, &dx_places);
   if (st != MM_OK) return st;
-  const bool direct = is_direct(a, f);
+  const bool direct = is_direct(a, f), many = f.cg == 2;
+  if (many && (st = sort_ready(ctx)) != MM_OK) return st;
   Cut cut;
   uint16_t *g = nullptr;
+  uint2 *sorted = nullptr;
   for (int pass = 0; pass < 2; ++pass) {
     cut.used = 0;
     p.r = cut_rows(cut, a, true, direct);
@@ -1319,6 +1491,12 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
     if (a.dx) {
       p.acc = cut.take<float>(rows_pad * p.acc_cols * 32);
       p.acc_cut = cut.take<float>((int64_t)dx_places * f.tile_m() * bn_cols);
+    }
+    if (many) {
+      p.r.rest = cut.take<float>(p.r.rows_pad);
+      p.r.first = cut.take<int>(token_tiles(a.vocab) + 1);
+      p.r.cells = cut.take<uint16_t>(cell_count(p.r, a.vocab) * kCellRows * kTileTokens);
+      sorted = cut.take<uint2>(2 * (int64_t)a.rows);
     }
     if (pass == 0) {
       void *w = nullptr;
@@ -1332,7 +1510,7 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   p.dw = static_cast<uint16_t *>(a.dweight);
   p.lddw = a.lddw;
   p.vec = (uintptr_t)a.dweight % 16 == 0 && a.lddw % 8 == 0 && a.cols % 8 == 0 && a.lddw < (1LL << 37);
-  if (!direct && (st = launch_gather(a, p.r, true, pack, ctx)) != MM_OK) return st;
+  if (!direct && (st = launch_gather(a, p.r, true, pack, sorted, ctx)) != MM_OK) return st;
   p.piece_kb = piece / 64;
   p.low = f.cg == 2 ? 0 : direct && a.rows <= kFewestRows ? kFewestRows : 128;
   p.boxes = p.low ? 2 : 1;
@@ -1363,6 +1541,8 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
       if ((st = rows_map(&m.a, p.tx, g, p.width, rows_pad, piece, 64)) != MM_OK) return st;
       if ((st = rows_map(&m.b, p.tx, p.r.x, a.cols, direct ? 128 : rows_pad, p.r.ldx, 64)) != MM_OK) return st;
       m.bh = m.o = m.b;
+      if (many && (st = rows_map(&m.bh, p.tx, p.r.cells, kTileTokens, cell_count(p.r, a.vocab) * kCellRows, kTileTokens, kCellRows)) != MM_OK)
+        return st;
       if (p.vec && (st = rows_map(&m.o, p.tx, a.dweight, a.cols, a.vocab, a.vocab == 1 ? p.r.ldx : a.lddw, 32)) != MM_OK)
         return st;
       st = a.rows > kLongRows ? launch_tiles<MODE_DW_LONG, 2>(p, m, p.width, ctx) : launch_tiles<MODE_DW, 2>(p, m, p.width, ctx);
@@ -1370,7 +1550,7 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
     }
   }
   if (!a.dx) return MM_OK;
-  DxParams d{a, p.r, p.acc, p.acc_cut, f.tile_m(), bn_cols, tiles_cols, dx_places, p.piece_kb, p.acc_cols,
+  DxParams d{a, p.r, p.acc, p.acc_cut, static_cast<const uint8_t *>(w.p), w.ld, f.tile_m(), bn_cols, tiles_cols, dx_places, p.piece_kb, p.acc_cols,
              (uintptr_t)a.dx % 16 == 0 && (a.lddx % 8 == 0 || a.rows == 1)};
   cudaError_t e = launch_pdl(dx_kernel, dim3((unsigned)(4 * ctx.dev->info.sms)),
                              dim3(256), 0, ctx.stream, dim3(1), d);

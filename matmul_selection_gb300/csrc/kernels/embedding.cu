@@ -93,9 +93,10 @@ struct SortParams {
   const void *tokens;
   int ti;
   int64_t vocab;
+  int drop;            // tokens that differ in this many low bits only are one key
   int rows, passes, digit, ctas;  // bits a pass; ctas: 1 or kMaxSortCtas
-  uint2 *to, *other;   // (token, place)
-  uint32_t *spanning;  // set to 0: how many tokens the sums will have left in parts
+  uint2 *to, *other;   // (key, place)
+  uint32_t *spanning;  // set to 0: how many tokens the sums will have left in parts (or null)
   // the rows
   const uint8_t *base;  // null: zeros
   uint8_t *dweight;
@@ -126,7 +127,9 @@ __device__ __forceinline__ void sort_places(const SortParams &p, uint32_t *smem)
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.digit;
     const auto pair_at = [&](int i) {  // (written by other SMs: past L1)
-      return pass ? __ldcg(src + i) : make_uint2((uint32_t)load_token(p.tokens, p.ti, i, p.vocab), (uint32_t)i);
+      if (pass) return __ldcg(src + i);
+      const int64_t v = load_token(p.tokens, p.ti, i, p.vocab);
+      return make_uint2((uint32_t)(v < p.vocab ? v >> p.drop : keys_of(p.vocab, p.drop)), (uint32_t)i);
     };
     // the run, 32 K places at a time, and which lanes have equal digits; a run of one batch
     // stays in registers
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortPara
   pdl_wait();
   extern __shared__ uint32_t sort_smem[];
   if ((int)blockIdx.x < p.ctas) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.spanning = 0;
+    if (p.spanning && blockIdx.x == 0 && threadIdx.x == 0) *p.spanning = 0;
     sort_places(p, sort_smem);
     return;
   }
@@ -473,6 +476,43 @@ mm_status embed_sums(const EmbedBwdArgs &a, const SumParams &p, const SumShape &
   return MM_OK;
 }
 
+// Set-up once a device, and how many clusters sort at once.
+mm_status sort_places_at_once(LaunchCtx &ctx, int *clusters) {
+  static PerDevice<int> fits;
+  const cudaError_t err = fits.get(ctx.dev->info.ordinal, clusters, [](int *n) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = kMaxSortCtas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(kMaxSortCtas);
+    lc.blockDim = dim3(kSortThreads);
+    lc.dynamicSmemBytes = kSortSmem;
+    lc.attrs = &at;
+    lc.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, embed_sort_kernel, &lc);
+  });
+  if (err != cudaSuccess) return cuda_error(err, "sort set-up");
+  if (*clusters < 1) return set_error(MM_ERR_UNSUPPORTED, "no cluster of CTAs fits on this device");
+  return MM_OK;
+}
+// f's passes over the keys' bits, and its launch beside `row_ctas` that write rows.
+mm_status launch_sort(SortParams &f, int row_ctas, LaunchCtx &ctx) {
+  int bits = 1;  // of the keys up to that of none
+  while (keys_of(f.vocab, f.drop) >> bits) ++bits;
+  f.passes = (bits + kDigit - 1) / kDigit;
+  f.digit = (bits + f.passes - 1) / f.passes;
+  cudaError_t e = launch_pdl(embed_sort_kernel, dim3((unsigned)(f.ctas + row_ctas)), dim3(kSortThreads), kSortSmem,
+                             ctx.stream, dim3((unsigned)f.ctas), f);
+  if (e != cudaSuccess) return cuda_error(e, "sort launch");
+  count_operator_launch();
+  return MM_OK;
+}
+// Places that one CTA sorts where nothing else runs beside it.
+constexpr int64_t kAlonePlaces = 2048;
+
 // f(type of one, type of the other) as constants.
 template <typename F>
 auto with_type(int t, F &&f) {
@@ -482,6 +522,25 @@ auto with_type(int t, F &&f) {
 }
 
 }  // namespace
+
+mm_status sort_ready(LaunchCtx &ctx) {
+  int clusters;
+  return sort_places_at_once(ctx, &clusters);
+}
+
+mm_status sort_tokens(const SortArgs &a, LaunchCtx &ctx) {
+  SortParams f;
+  std::memset(&f, 0, sizeof f);
+  f.tokens = a.tokens;
+  f.ti = a.ti;
+  f.vocab = a.vocab;
+  f.drop = a.drop;
+  f.rows = a.rows;
+  f.ctas = a.rows <= kAlonePlaces ? 1 : kMaxSortCtas;
+  f.to = static_cast<uint2 *>(a.to);
+  f.other = static_cast<uint2 *>(a.other);
+  return launch_sort(f, 0, ctx);
+}
 
 mm_status launch_embedding(const EmbedArgs &a, LaunchCtx &ctx) {
   const cudaError_t e = with_type(a.tw, [&](auto tw) {
@@ -526,32 +585,16 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   const auto whole = [](int64_t bytes) { return ((size_t)bytes + 255) / 256 * 256; };
   const size_t pairs = whole(a.rows * (int64_t)sizeof(uint2)), list = whole((p.chunks + 1) * (int64_t)sizeof(uint32_t));
   // as many CTAs as run at once: the first sort, the others write rows
-  static PerDevice<int> fits;
   int clusters;
-  const cudaError_t err = fits.get(ctx.dev->info.ordinal, &clusters, [](int *n) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = kMaxSortCtas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(kMaxSortCtas);
-    lc.blockDim = dim3(kSortThreads);
-    lc.dynamicSmemBytes = kSortSmem;
-    lc.attrs = &at;
-    lc.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(n, embed_sort_kernel, &lc);
-  });
-  if (err != cudaSuccess) return cuda_error(err, "embedding_backward set-up");
-  if (clusters < 1) return set_error(MM_ERR_UNSUPPORTED, "no cluster of CTAs fits on this device");
+  mm_status st = sort_places_at_once(ctx, &clusters);
+  if (st != MM_OK) return st;
   // One CTA sorts within 10 us and 3.7 ns a place (65536: 243 us; eight 42), and rows are
   // written at 5 TB/s or more.
   const int64_t written = fills ? f.bytes * f.fill_rows : 0;
-  f.ctas = a.rows <= 2048 || (50 << 20) + a.rows * 18500 <= written ? 1 : kMaxSortCtas;
+  f.ctas = a.rows <= kAlonePlaces || (50 << 20) + a.rows * 18500 <= written ? 1 : kMaxSortCtas;
   const int row_ctas = !fills ? 0 : f.ctas == 1 ? ctx.dev->info.sms - 1 : std::max(1, clusters - 1) * kMaxSortCtas;
   void *scratch = nullptr;
-  mm_status st = get_scratch(ctx, SCRATCH_WORKSPACE, 2 * pairs + list + (size_t)p.chunks * 2 * a.cols * sizeof(float), &scratch);
+  st = get_scratch(ctx, SCRATCH_WORKSPACE, 2 * pairs + list + (size_t)p.chunks * 2 * a.cols * sizeof(float), &scratch);
   if (st != MM_OK) return st;
   char *w = static_cast<char *>(scratch);
   f.to = reinterpret_cast<uint2 *>(w);
@@ -562,14 +605,7 @@ mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx) {
   f.tokens = a.tokens;
   f.ti = a.ti;
   f.rows = (int)a.rows;
-  int bits = 1;  // of the numbers up to vocab, which stands for none
-  while (a.vocab >> bits) ++bits;
-  f.passes = (bits + kDigit - 1) / kDigit;
-  f.digit = (bits + f.passes - 1) / f.passes;
-  cudaError_t e = launch_pdl(embed_sort_kernel, dim3((unsigned)(f.ctas + row_ctas)), dim3(kSortThreads), kSortSmem,
-                             ctx.stream, dim3((unsigned)f.ctas), f);
-  if (e != cudaSuccess) return cuda_error(e, "embedding_backward launch (sort)");
-  count_operator_launch();
+  if ((st = launch_sort(f, row_ctas, ctx)) != MM_OK) return st;
   return with_type(a.tw, [&](auto tw) {
     return with_type(a.to, [&](auto to) { return embed_sums<decltype(tw)::value, decltype(to)::value>(a, p, shape, ctx); });
   });

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.h"
+#include "embed_chunks.h"
 
 namespace mm {
 
@@ -85,6 +86,20 @@ struct EmbedBwdArgs {
   float scale;
 };
 mm_status launch_embedding_backward(const EmbedBwdArgs &a, LaunchCtx &ctx);
+
+// The places 0 .. rows - 1 of tokens in the order of their keys, equal ones in their own:
+// (key, place) as two 32-bit numbers each to `to`; `other`: room for as many.  A key is a
+// token without its `drop` low bits; no token has the key keys_of(vocab, drop).
+MM_HOST_DEVICE int64_t keys_of(int64_t vocab, int drop) { return (vocab + (1 << drop) - 1) >> drop; }
+struct SortArgs {
+  const void *tokens;
+  int ti;
+  int64_t vocab;
+  int rows, drop;
+  void *to, *other;
+};
+mm_status sort_ready(LaunchCtx &ctx);  // what a launch needs set up, which may fail
+mm_status sort_tokens(const SortArgs &a, LaunchCtx &ctx);
 
 // The loss over a vocabulary and its gradients (those: dloss or null for 1, dx
 // and dweight, either null).
