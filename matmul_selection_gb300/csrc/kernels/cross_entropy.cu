@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const GatherP
 constexpr int kTileTokens = 256, kLogTileTokens = 8, kCellRows = 64;
 struct SortedParams {
   GatherParams g;
-  const uint2 *sorted;  // (tile of the target, row)
+  const uint2 *sorted;  // (tile of the target, row), or null: to be counted
   int tiles;            // the key of a row without a target
   int64_t cell_pieces;  // all cells', of 16 bytes
 };
@@ -270,6 +270,91 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_sorted_kernel(const 
       }
     }
     __syncthreads();
+  }
+}
+
+// The same of fewer rows, by counting: a row's place is how many come before it, one by a
+// smaller key or by the same and a smaller number, counted by a warp over all keys in shared
+// memory.  (A sort and its launch are 5-8 us: gradients of 129 x 256 x 512 36 -> 32 us, 300 x 1024
+// x 32000 114 -> 108; 4096 x 1024 x 32000 sorted 572, counted 575.)
+constexpr int kCountedRows = 2048;
+__global__ void __launch_bounds__(kGatherThreads, 2) gather_counted_kernel(const SortedParams q) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ float warp_max[kGatherWarps];
+  __shared__ int keys[kCountedRows], at_place[kGatherThreads];
+  const GatherParams &p = q.g;
+  const LossArgs &a = p.a;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, none = q.tiles;
+  if ((int)blockIdx.x >= p.blocks) {
+    pack_rows(p.pack, ((int64_t)blockIdx.x - p.blocks) * kGatherThreads + t, ((int64_t)gridDim.x - p.blocks) * kGatherThreads);
+    return;
+  }
+  const int64_t thread = (int64_t)blockIdx.x * kGatherThreads + t, threads = (int64_t)p.blocks * kGatherThreads;
+  for (int64_t i = thread; i < q.cell_pieces; i += threads) reinterpret_cast<uint4 *>(p.r.cells)[i] = make_uint4(0, 0, 0, 0);
+  float top = 0.f;  // of the finite ones
+  for (int i = t; i < a.rows; i += kGatherThreads) {
+    const int target = valid_target(a, i);
+    const float d = abs_weight(a.dloss, i);
+    keys[i] = target >= 0 ? target >> kLogTileTokens : none;
+    if (target >= 0 && d <= kLargestFinite) top = fmaxf(top, d);
+  }
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) warp_max[warp] = top;
+  __syncthreads();
+  for (int w = 0; w < kGatherWarps; ++w) top = fmaxf(top, warp_max[w]);
+  if (top == 0.f) top = 1.f;
+  // how many rows have a smaller key, or this one and a number below `row`
+  const auto before = [&](int key, int row) {
+    int n = 0;
+    for (int j = lane; j < a.rows; j += 32) n += keys[j] < key || (keys[j] == key && j < row);
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  const int count = before(none, 0);
+  if (thread == 0) *p.r.gain = top, *p.r.count = count;
+  for (int64_t k = (int64_t)blockIdx.x * kGatherWarps + warp; k <= none; k += (int64_t)p.blocks * kGatherWarps) {
+    const int n = before((int)k, 0);
+    if (lane == 0) p.r.first[k] = n;
+  }
+  const int pieces = (int)(p.r.ldx / 8);
+  for (int64_t i = count + thread; i < p.r.rows_pad; i += threads) {
+    p.r.target[i] = -1;
+    p.r.ratio[i] = p.r.lse[i] = p.r.rest[i] = 0.f;
+  }
+  const int64_t z1 = (int64_t)max(1, (count + 63) / 64) * 64 * pieces;
+  for (int64_t i = (int64_t)count * pieces + thread; i < z1; i += threads) reinterpret_cast<uint4 *>(p.r.x)[i] = make_uint4(0, 0, 0, 0);
+
+  const int r0 = (int)((int64_t)a.rows * blockIdx.x / p.blocks), n = (int)((int64_t)a.rows * (blockIdx.x + 1) / p.blocks) - r0;
+  for (int k = warp; k < n; k += kGatherWarps) {
+    const int row = r0 + k, key = keys[row], place = before(key, row);
+    if (lane != 0) continue;
+    at_place[k] = key < none ? place : -1;
+    p.r.slot[row] = at_place[k];
+    if (key < none) {
+      p.r.row[place] = row;
+      p.r.target[place] = valid_target(a, row);
+      p.r.ratio[place] = ratio_of(a.dloss, row, top, a.tx);
+      p.r.lse[place] = a.lse[row];
+      p.r.rest[place] = 0.f;
+    }
+  }
+  __syncthreads();
+  constexpr int U = 4;  // pieces read before the first is stored
+  const int row_threads = 1 << p.log_threads, t0 = t & (row_threads - 1);
+  for (int k = t >> p.log_threads; k < n; k += kGatherThreads >> p.log_threads) {
+    if (at_place[k] < 0) continue;
+    const uint8_t *from = static_cast<const uint8_t *>(a.x) + (int64_t)(r0 + k) * a.ldx * 2;
+    uint4 *to = reinterpret_cast<uint4 *>(p.r.x + (int64_t)at_place[k] * p.r.ldx);
+    for (int c = t0; c < pieces; c += row_threads * U) {
+      RowPiece<2> v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c + u * row_threads < pieces) v[u].load(from, (int64_t)a.cols * 2, (int64_t)(c + u * row_threads) * 16);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c + u * row_threads < pieces)
+          to[c + u * row_threads] = v[u].value(from, (int64_t)a.cols * 2, (int64_t)(c + u * row_threads) * 16);
+    }
   }
 }
 
@@ -555,9 +640,9 @@ __device__ __forceinline__ float unpack(int tx, uint32_t w, int odd) {
 // row (dx_kernel), and dW as 64 more of K for each 64 rows and tile of 256 tokens in which
 // there are targets, which are few, since the rows are sorted by those tiles: cell b + j holds
 // rows 64 b .. and tile j, along a path on which one of the two grows at a time.  That takes
-// 3 % of the gradients' time above 800 rows, 5 % there, 10 % at 300 x 1024 x 32000 (the sort's 6
-// us, 4 % more of dW's K, W's rows in the last step); a second value of all g took twice dx's
-// and dW's products.
+// 1-4 % of the gradients' time over 4096 columns, 6 % at 300 x 1024 x 32000 (their order, 4 %
+// more of dW's K, W's rows in the last step), more where a few tiles are all the tokens (dW's K
+// grows by half over 512); a second value of all g would double dx's and dW's products.
 __device__ __noinline__ void leave_rest(float *rests, uint16_t *cells, int tx, int row, int target, float g) {
   const float rest = g - unpack(tx, pack2(tx, g, 0.f), 0);
   rests[row] = rest;
@@ -1106,7 +1191,7 @@ __device__ __forceinline__ void round_dx(const DxParams &p, const float4 *from, 
                                          int count, float gain) {
   const int i = rb * 32 + (threadIdx.x & 31), left = p.a.cols - col;
   const float rest = p.r.rest && i < count ? p.r.rest[i] : 0.f;  // (see leave_rest)
-  const int token = rest != 0.f ? p.r.target[i] : 0;
+  const int token = p.r.rest && i < count ? p.r.target[i] : 0;
   float4 v[Q];
 #pragma unroll
   for (int k = 0; k < Q; ++k) v[k] = from[k * 32];
@@ -1240,7 +1325,8 @@ Rows cut_rows(Cut &cut, const LossArgs &a, bool backward, bool direct) {
   return r;
 }
 
-// (sorted: room for twice as many (tile, row) as there are rows, or null)
+// (sorted, of many rows: room for twice as many (tile, row) as there are rows, where they are
+// not counted)
 mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, const PackRows &pack, uint2 *sorted, LaunchCtx &ctx) {
   const int sms = ctx.dev->info.sms;
   GatherParams p{a, r, backward, 0, std::min(a.rows, 2 * sms), pack};
@@ -1249,11 +1335,15 @@ mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, const P
   p.pack.log_threads = copy.log_threads;
   const dim3 grid((unsigned)(p.blocks + copy.blocks));
   cudaError_t e;
-  if (sorted) {
-    mm_status st = sort_tokens({a.targets, a.ti, a.vocab, a.rows, kLogTileTokens, sorted, sorted + a.rows}, ctx);
-    if (st != MM_OK) return st;
+  if (r.cells) {
     const SortedParams q{p, sorted, token_tiles(a.vocab), cell_count(r, a.vocab) * kCellRows * kTileTokens / 8};
-    e = launch_pdl(gather_sorted_kernel, grid, dim3(kGatherThreads), 0, ctx.stream, dim3(1), q);
+    if (sorted) {
+      mm_status st = sort_tokens({a.targets, a.ti, a.vocab, a.rows, kLogTileTokens, sorted, sorted + a.rows}, ctx);
+      if (st != MM_OK) return st;
+      e = launch_pdl(gather_sorted_kernel, grid, dim3(kGatherThreads), 0, ctx.stream, dim3(1), q);
+    } else {
+      e = launch_pdl(gather_counted_kernel, grid, dim3(kGatherThreads), 0, ctx.stream, dim3(1), q);
+    }
   } else {
     e = launch_pdl(gather_kernel, grid, dim3(kGatherThreads), 0, ctx.stream, dim3(1), p);
   }
@@ -1480,7 +1570,8 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
   mm_status st = f.cg == 1 ? tile_places<MODE_DX, 1>(ctx, &dx_places) : tile_places<MODE_DX, 2>(ctx, &dx_places);
   if (st != MM_OK) return st;
   const bool direct = is_direct(a, f), many = f.cg == 2;
-  if (many && (st = sort_ready(ctx)) != MM_OK) return st;
+  const bool sorts = many && a.rows > kCountedRows;
+  if (sorts && (st = sort_ready(ctx)) != MM_OK) return st;
   Cut cut;
   uint16_t *g = nullptr;
   uint2 *sorted = nullptr;
@@ -1496,7 +1587,7 @@ mm_status launch_cross_entropy_backward(const LossArgs &a, LaunchCtx &ctx) {
       p.r.rest = cut.take<float>(p.r.rows_pad);
       p.r.first = cut.take<int>(token_tiles(a.vocab) + 1);
       p.r.cells = cut.take<uint16_t>(cell_count(p.r, a.vocab) * kCellRows * kTileTokens);
-      sorted = cut.take<uint2>(2 * (int64_t)a.rows);
+      if (sorts) sorted = cut.take<uint2>(2 * (int64_t)a.rows);
     }
     if (pass == 0) {
       void *w = nullptr;
