@@ -1329,13 +1329,13 @@ Rows cut_rows(Cut &cut, const LossArgs &a, bool backward, bool direct) {
 // not counted)
 mm_status launch_gather(const LossArgs &a, const Rows &r, bool backward, const PackRows &pack, uint2 *sorted, LaunchCtx &ctx) {
   const int sms = ctx.dev->info.sms;
-  GatherParams p{a, r, backward, 0, std::min(a.rows, 2 * sms), pack};
+  GatherParams p{a, r, backward, 0, std::min(a.rows, std::max(2 * sms, kCountedRows / kGatherThreads)), pack};
   while (p.log_threads < 9 && (32ll << p.log_threads) < r.ldx) ++p.log_threads;  // (up to four pieces each)
   const PackShape copy = pack_shape(pack.rows, pack.ld16, kGatherThreads, 8 * sms);
   p.pack.log_threads = copy.log_threads;
   const dim3 grid((unsigned)(p.blocks + copy.blocks));
   cudaError_t e;
-  if (r.cells) {
+  if (r.cells) {  // (a block's rows: no more than its threads)
     const SortedParams q{p, sorted, token_tiles(a.vocab), cell_count(r, a.vocab) * kCellRows * kTileTokens / 8};
     if (sorted) {
       mm_status st = sort_tokens({a.targets, a.ti, a.vocab, a.rows, kLogTileTokens, sorted, sorted + a.rows}, ctx);
